@@ -443,6 +443,159 @@ idx_status sparse_decode_step(const void* q, idx_dtype q_dtype, const float* w, 
 int32_t sparse_decode_step_fused(int64_t n_rows, int32_t n_q_per_seq, int32_t max_n_kv, int32_t top_k,
                                  int64_t idx_row_stride);
 
+/*
+ * dense_attn -- softmax attention of each query row over EVERY key it sees: a
+ * chunk of new tokens per sequence (n_q_per_seq rows; 1 is a decode step) over
+ * a contiguous or paged cache.  It serves the layers without an indexer that
+ * stand beside the sparse ones ("openpangu: DSA lightning indexer + SWA
+ * schedule", ik_llama_opt commit log) and contexts too short to select from.
+ * Row r = b*T + t of sequence b, head h, kv head g(h) = h / (Hq / Hkv), position
+ * p = q_pos[r], key position j:
+ *     x[h, j] = scale * q[r, h, :] . K[j, g(h), :]
+ *     x[h, j] = softcap * tanh(x[h, j] / softcap)            when softcap > 0
+ *     x[h, j] = x[h, j] - slopes[h] * |p - j|                when slopes is given
+ *     out[r, h, :] = sum_j softmax_j(x)[h, j] * V[j, g(h), :]
+ *     lse[r, h] = log(sum_j exp(x[h, j]))                    (natural logarithm)
+ * over the keys lo(r) <= j < hi(r):
+ *     hi(r) = n_kv[b]                                        without q_pos
+ *           = 0                                              p < 0 (a padding row)
+ *           = min(n_kv[b], max(p + 1, prefix_len[b]))        else (prefix_len NULL: 0)
+ *     lo(r) = max(0, doc_start[r], p - window + 1)           (each where given)
+ * Chunks of unequal length are padded to n_q_per_seq rows with q_pos = -1.  A row
+ * that sees no key, or whose every score is -inf, gets zeros and lse = -inf.
+ * Keys outside a row's interval never reach its result, whatever bytes they hold
+ * (rows of a page past the sequence's end, other documents, later tokens): NaN
+ * and infinities there included.
+ *   q, k, v, dtype, strides, kv_rows   as sparse_attn_decode (v NULL: the MLA
+ *              latent form), K and V rows addressed by batch.
+ *   mods       HOST pointer to the options below, or NULL for none of them.
+ *   out        [B*T, Hq, dv] contiguous, of q's dtype.
+ *   lse        f32 [B*T, Hq] or NULL.
+ *   workspace  dense_attn_workspace_size(...) bytes, 16-byte aligned: the partial
+ *              results of key splits.  With less (or NULL) the keys are split
+ *              less or not at all, with the same results up to rounding.  Calls
+ *              whose work overlaps on the GPU need workspaces of their own.
+ * Sums, maxima and outputs are accumulated in f32.  A key row outside the cache
+ * (a page number out of range) is skipped and flagged (IDX_ERR_DEVICE_BOUNDS).
+ * Errors: those of sparse_attn_decode's arguments; softcap or window negative,
+ * softcap not finite, window, slopes or prefix_len without q_pos: INVALID_ARG.
+ */
+typedef struct idx_attn_mods {
+    float softcap;             /* 0: scores are not capped */
+    const float* slopes;       /* device f32 [n_q_heads] or NULL: distance bias of each head */
+    int32_t window;            /* 0: none; else a row sees at most this many positions up to its own */
+    const int32_t* prefix_len; /* device int32 [n_seq] or NULL: positions every row of the sequence sees */
+    const int32_t* doc_start;  /* device int32 [n_seq*n_q_per_seq] or NULL: first position of the row's document */
+} idx_attn_mods;
+
+idx_status dense_attn(const void* q, idx_dtype dtype, int32_t n_q_heads, int32_t n_kv_heads, int32_t dk, int32_t dv,
+                      const void* k, const void* v, int64_t kv_row_stride, int64_t v_row_stride, int64_t kv_rows,
+                      idx_batch batch, const idx_attn_mods* mods, float scale, void* out, float* lse,
+                      void* workspace, size_t workspace_bytes, idx_stream_t stream);
+
+/* Bytes of device workspace with which dense_attn splits keys as it would like to (0 when it needs
+   none); host arithmetic, 0 for nonsense sizes.  Arguments as the call's. */
+size_t dense_attn_workspace_size(idx_dtype dtype, int32_t n_seq, int32_t n_q_per_seq, int32_t max_n_kv,
+                                 int32_t n_q_heads, int32_t n_kv_heads, int32_t dk, int32_t dv);
+
+/*
+ * The pages of paged caches (idx_batch.page_table): several caches (indexer keys,
+ * latent or K and V, coded keys) share one table, page p of a cache being its rows
+ * p*page_size .. p*page_size + page_size - 1.  A page belongs to whoever's table
+ * row names it: there is no other state (no reference counts, no free list), so a
+ * page that no row names and that is not `held` is free.
+ *
+ * idx_page_cache: one cache, described on the HOST.  data: device; row i at
+ * data + i*row_stride_bytes, row_bytes of it are payload (only those are moved).
+ */
+typedef struct idx_page_cache {
+    void* data;
+    int64_t row_stride_bytes;
+    int64_t row_bytes;
+} idx_page_cache;
+
+#define IDX_MAX_PAGE_CACHES 8
+
+/*
+ * idx_page_copy -- page dst[i] of every cache := page src[i], for i < n.
+ *   caches     HOST array of n_caches (1 .. IDX_MAX_PAGE_CACHES) descriptions.
+ *   n_pages    pages in each cache.
+ *   src, dst   device int32 [n].  An entry with src[i] == dst[i] or either one
+ *              negative is skipped; one outside [0, n_pages) is skipped and flagged
+ *              (IDX_ERR_DEVICE_BOUNDS).  The pages of dst must differ from one
+ *              another and from those of src (the entries are copied in no
+ *              particular order).
+ */
+idx_status idx_page_copy(const idx_page_cache* caches, int32_t n_caches, int32_t page_size, int32_t n_pages,
+                         const int32_t* src, const int32_t* dst, int32_t n, idx_stream_t stream);
+
+/*
+ * idx_page_update -- one step's changes of a batch's sequences: free, truncate,
+ * fork and grow, in one call.  Row b of the new table becomes the first n_keep[b]
+ * positions of row parent[b] of the old one, with pages for n_new[b] positions:
+ *   - pages that the kept positions fill are shared with whoever else names them;
+ *   - the page that they fill only in part stays with the row if it is the first
+ *     one (the lowest b) that wants it so, no row keeps it whole and it is not
+ *     held; otherwise its kept rows are copied to a new page, in every cache;
+ *   - further pages up to ceil(n_new[b] / page_size) are new, the rest is -1.
+ * New pages are the lowest-numbered ones that no new row names and that are not
+ * held, handed out by row, then by entry.  (parent b = b, n_keep = n_len,
+ * n_new = n_len + 1 lets row b grow; parent -1 with n_keep 0 starts a row from
+ * nothing, n_new 0 leaves it empty.)  Pages of rows that are not taken over are
+ * thereby free.  A copied page is complete when the call's work is: append to it
+ * after the call, on the same stream.
+ *   page_table  old table, device int32 [n_seq_old] rows of table_cols entries,
+ *               table_stride apart.
+ *   parent, n_keep, n_new   device int32 [n_seq].
+ *   held        device uint8 [n_pages] or NULL: pages marked nonzero belong to
+ *               someone outside the tables (a kept prefix): never handed out,
+ *               never written.
+ *   new_table   device int32 [n_seq] rows of new_cols entries, new_stride apart;
+ *               must not overlap page_table.
+ *   n_free      device int32 [1]: pages left free.  If there are too few, minus
+ *               the number missing, and nothing else is written.  If a request is
+ *               impossible (parent outside [-1, n_seq_old), n_keep or n_new
+ *               negative, n_keep > n_new, n_keep > 0 without a parent, either
+ *               beyond its table's columns, a kept page outside [0, n_pages)),
+ *               INT32_MIN, nothing else is written, and IDX_ERR_DEVICE_BOUNDS is
+ *               recorded.
+ *   caches      HOST array, n_caches may be 0 (tables only).
+ *   workspace   idx_page_workspace_size(n_seq, n_pages) bytes, 16-byte aligned; not
+ *               shared with calls whose work overlaps this one's.
+ */
+idx_status idx_page_update(const int32_t* page_table, int64_t table_stride, int32_t table_cols, int32_t n_seq_old,
+                           const int32_t* parent, const int32_t* n_keep, const int32_t* n_new, int32_t n_seq,
+                           int32_t page_size, int32_t n_pages, const uint8_t* held, int32_t* new_table,
+                           int64_t new_stride, int32_t new_cols, int32_t* n_free, const idx_page_cache* caches,
+                           int32_t n_caches, void* workspace, size_t workspace_bytes, idx_stream_t stream);
+
+/*
+ * idx_page_compact -- move the used pages to the lowest numbers.  With U the pages
+ * that the live entries (the first ceil(n_len[b] / page_size) of row b) name, and
+ * the held ones: the pages of U numbered |U| or higher that are not held move, in
+ * ascending order, to the numbers below |U| that are not in U, in ascending order,
+ * in every cache; held pages stay.  Without held pages the used pages end up as
+ * 0 .. |U| - 1.
+ *   n_len       device int32 [n_seq]: positions that each row holds or has room
+ *               for.  A live entry outside [0, n_pages) becomes -1 and is flagged,
+ *               a length outside [0, table_cols*page_size] is clamped and flagged
+ *               (IDX_ERR_DEVICE_BOUNDS).
+ *   new_table   as page_table with the new numbers, -1 past the live entries; may be
+ *               page_table itself (then new_stride == table_stride).
+ *   n_used      device int32 [1]: |U|.
+ *   remap       device int32 [n_pages] or NULL: the new number of each page (its own
+ *               where it does not move).
+ * Other arguments as idx_page_update.
+ */
+idx_status idx_page_compact(const int32_t* page_table, int64_t table_stride, int32_t table_cols, int32_t n_seq,
+                            const int32_t* n_len, int32_t page_size, int32_t n_pages, const uint8_t* held,
+                            int32_t* new_table, int64_t new_stride, int32_t* n_used, int32_t* remap,
+                            const idx_page_cache* caches, int32_t n_caches, void* workspace, size_t workspace_bytes,
+                            idx_stream_t stream);
+
+/* Bytes of device workspace of idx_page_update and idx_page_compact; host arithmetic, 0 for nonsense sizes. */
+size_t idx_page_workspace_size(int32_t n_seq, int32_t n_pages);
+
 /* Operation selectors for idx_workspace_size. */
 enum {
     IDX_OP_SCORE = 0,

@@ -11,6 +11,7 @@ Build with ``lightning_indexer_top_gb300.build()`` (nvcc, sm_103a).
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -26,6 +27,8 @@ __all__ = [
     "idx_quantize_rows", "idx_score_q8", "inline_scales",
     "idx_topk", "sparse_attn_decode", "sparse_attn_prefill", "idx_workspace_size",
     "idx_device_status", "topk_capacity", "sparse_attn_decode_noalloc", "idx_score_topk", "idx_block_score_topk", "sparse_decode_step", "sparse_decode_step_fused",
+    "dense_attn", "dense_attn_workspace_size", "idx_page_copy", "idx_page_update", "idx_page_compact",
+    "idx_page_workspace_size",
 ]
 
 IDX_OK, IDX_ERR_INVALID_ARG, IDX_ERR_UNSUPPORTED, IDX_ERR_CUDA, IDX_ERR_TIMEOUT, IDX_ERR_DEVICE_BOUNDS, IDX_ERR_INEXACT = range(7)
@@ -56,6 +59,26 @@ class _Batch(ctypes.Structure):
         ("page_size", ctypes.c_int32),
     ]
 
+
+class _Mods(ctypes.Structure):
+    _fields_ = [
+        ("softcap", ctypes.c_float),
+        ("slopes", ctypes.c_void_p),
+        ("window", ctypes.c_int32),
+        ("prefix_len", ctypes.c_void_p),
+        ("doc_start", ctypes.c_void_p),
+    ]
+
+
+class _PageCache(ctypes.Structure):
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("row_stride_bytes", ctypes.c_int64),
+        ("row_bytes", ctypes.c_int64),
+    ]
+
+
+IDX_MAX_PAGE_CACHES = 8
 
 _lib = None
 
@@ -90,6 +113,14 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
                                P, I32, I32, I32, I32, I32, P, P, I64, I64, I64, F, P, I32, P, SZ, P],
         "idx_workspace_size": [I32, I64, I32, I32, I32, I32],
         "sparse_decode_step_fused": [I64, I32, I32, I32, I64],
+        "dense_attn": [P, I32, I32, I32, I32, I32, P, P, I64, I64, I64, _Batch, ctypes.POINTER(_Mods), F, P, P, P, SZ,
+                       P],
+        "dense_attn_workspace_size": [I32, I32, I32, I32, I32, I32, I32, I32],
+        "idx_page_copy": [ctypes.POINTER(_PageCache), I32, I32, I32, P, P, I32, P],
+        "idx_page_update": [P, I64, I32, I32, P, P, P, I32, I32, I32, P, P, I64, I32, P, ctypes.POINTER(_PageCache), I32,
+                            P, SZ, P],
+        "idx_page_compact": [P, I64, I32, I32, P, I32, I32, P, P, I64, P, P, ctypes.POINTER(_PageCache), I32, P, SZ, P],
+        "idx_page_workspace_size": [I32, I32],
         "idx_last_error": [],
         "idx_device_status": [I32],
     }
@@ -97,7 +128,8 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = ctypes.c_int
-    lib.idx_workspace_size.restype = ctypes.c_size_t
+    for name in ("idx_workspace_size", "dense_attn_workspace_size", "idx_page_workspace_size"):
+        getattr(lib, name).restype = ctypes.c_size_t
     lib.idx_last_error.restype = ctypes.c_char_p
     _lib = lib
     return lib
@@ -477,6 +509,233 @@ def sparse_attn_decode_noalloc(q, latent, batch, idx, n_sel, scale, *, out=None,
                                              latent.shape[0], batch.c(), _ptr(idx), idx.stride(0), _ptr(n_sel),
                                              float(scale), _ptr(out), _dtype(out), _stream(q.device)))
     return out
+
+
+def _on(device):
+    """Makes `device` current for a call (nothing to do where it is)."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _same_device(device, *ts):
+    for t in ts:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors on {device} and {t.device}: lidx works on one device per call")
+
+
+def _i32(name: str, t: Optional[torch.Tensor], n: int):
+    if t is not None and (t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < n):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of at least {n} entries")
+
+
+def dense_attn_workspace_size(dtype: torch.dtype, n_seq: int, n_q_per_seq: int, max_n_kv: int, n_q_heads: int,
+                              n_kv_heads: int, dk: int, dv: int) -> int:
+    """Bytes of workspace with which dense_attn splits the keys as it would like to."""
+    return int(load().dense_attn_workspace_size(_DTYPES[dtype], n_seq, n_q_per_seq, max_n_kv, n_q_heads, n_kv_heads,
+                                                dk, dv))
+
+
+def dense_attn(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tensor], batch: Batch, scale: float, *,
+               softcap: float = 0.0, slopes: Optional[torch.Tensor] = None, window: int = 0,
+               prefix_len: Optional[torch.Tensor] = None, doc_start: Optional[torch.Tensor] = None,
+               out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None, dv: Optional[int] = None) -> torch.Tensor:
+    """Attention of a chunk of new tokens (batch.n_q_per_seq rows per sequence, 1 = decode) over every key
+    its rows see in a contiguous or paged cache.  q [B*T, Hq, dk]; k [rows, Hkv, dk] and v [rows, Hkv, dv],
+    or the MLA latent [rows, dk] with v=None (dv columns of it, 512 unless given).  Returns out
+    [B*T, Hq, dv] of q's dtype; lse, if given (f32 [B*T, Hq]), gets the log of the rows' softmax sums.
+
+    Row r sees positions up to batch.q_pos[r] (none if that is negative: a padding row, whose out is
+    zero), or up to prefix_len[b] where that is further; not before doc_start[r]; with window, at most
+    that many positions up to its own.  softcap c > 0: scores x become c * tanh(x / c); slopes (f32 [Hq]):
+    minus slopes[h] * |q_pos[r] - j| for key j."""
+    _need_cuda(q, k, v, slopes, prefix_len, doc_start, out, lse, workspace)
+    _same_device(q.device, k, v, slopes, prefix_len, doc_start, out, lse, workspace, batch.n_kv)
+    if q.dim() != 3 or not q.is_contiguous() or q.shape[0] != batch.n_rows:
+        raise ValueError("q must be a contiguous [n_seq * n_q_per_seq, heads, dk] tensor")
+    rows, Hq, dk = q.shape
+    if v is None:
+        if k.dim() == 3 and k.shape[1] == 1:
+            k = k[:, 0]
+        if k.dim() != 2 or k.shape[1] < dk or k.stride(1) != 1:
+            raise ValueError("the latent cache must be [rows, dk] with contiguous rows")
+        hkv, dv, v_row_stride = 1, (512 if dv is None else dv), 0
+    else:
+        if k.dim() != 3 or v.dim() != 3 or k.shape[:2] != v.shape[:2] or k.shape[2] != dk:
+            raise ValueError("k and v must be [rows, kv heads, dk] and [rows, kv heads, dv]")
+        if dv is not None and dv != v.shape[2]:
+            raise ValueError("dv differs from v's last dimension")
+        hkv, dv = k.shape[1], v.shape[2]
+        for t in (k, v):
+            if t.stride(2) != 1 or (hkv > 1 and t.stride(1) != t.shape[2]):
+                raise ValueError("the heads of a cache row must be contiguous")
+        v_row_stride = v.stride(0)
+    if k.dtype != q.dtype or (v is not None and v.dtype != q.dtype):
+        raise ValueError("q, k and v must have the same dtype")
+    if slopes is not None and (slopes.dtype != torch.float32 or not slopes.is_contiguous() or slopes.numel() != Hq):
+        raise ValueError("slopes must be a contiguous float32 tensor with one entry per query head")
+    _i32("prefix_len", prefix_len, batch.n_seq)
+    _i32("doc_start", doc_start, rows)
+    if out is None:
+        out = torch.empty(rows, Hq, dv, device=q.device, dtype=q.dtype)
+    elif out.shape != (rows, Hq, dv) or out.dtype != q.dtype or not out.is_contiguous():
+        raise ValueError("out must be a contiguous [rows, heads, dv] tensor of q's dtype")
+    if lse is not None and (lse.shape != (rows, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 [rows, heads] tensor")
+    lib = load()
+    mods = None
+    if softcap or slopes is not None or window or prefix_len is not None or doc_start is not None:
+        mods = ctypes.byref(_Mods(softcap, _ptr(slopes), window, _ptr(prefix_len), _ptr(doc_start)))
+    with _on(q.device):
+        dt = _dtype(q)
+        if workspace is None:
+            need = lib.dense_attn_workspace_size(dt, batch.n_seq, batch.n_q_per_seq, batch.max_n_kv, Hq, hkv, dk, dv)
+            if need:
+                workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        # an empty cache has no address; v's tells the latent form apart and is not read
+        v_ptr = None if v is None else v.data_ptr() or q.data_ptr()
+        _check(lib.dense_attn(q.data_ptr(), dt, Hq, hkv, dk, dv, k.data_ptr(), v_ptr, k.stride(0), v_row_stride, k.shape[0],
+                              batch.c(), mods, scale, out.data_ptr(), _ptr(lse), _ptr(workspace), ws_bytes,
+                              _stream(q.device)))
+    return out
+
+
+def _page_caches(caches, page_size: int):
+    """(ctypes array of cache descriptions, pages in each) of caches sharing page numbers."""
+    if not 1 <= len(caches) <= IDX_MAX_PAGE_CACHES:
+        raise ValueError(f"1 to {IDX_MAX_PAGE_CACHES} caches share a page table")
+    if page_size < 1:
+        raise ValueError("page_size < 1")
+    arr = (_PageCache * len(caches))()
+    n_pages = caches[0].shape[0] // page_size
+    for i, c in enumerate(caches):
+        if c.dim() < 1 or c.shape[0] // page_size != n_pages:
+            raise ValueError("the caches must hold the same number of pages")
+        inner = 1
+        for d in range(c.dim() - 1, 0, -1):
+            if c.shape[d] != 1 and c.stride(d) != inner:
+                raise ValueError("the elements of a cache row must be contiguous")
+            inner *= c.shape[d]
+        if c.shape[0] > 1 and c.stride(0) < inner:
+            raise ValueError("the rows of a cache must not overlap")
+        size = c.element_size()
+        arr[i] = _PageCache(c.data_ptr(), max(c.stride(0), inner) * size, inner * size)
+    return arr, n_pages
+
+
+def idx_page_workspace_size(n_seq: int, n_pages: int) -> int:
+    return int(load().idx_page_workspace_size(n_seq, n_pages))
+
+
+def idx_page_copy(caches, page_size: int, src: torch.Tensor, dst: torch.Tensor) -> None:
+    """Copies page src[i] to page dst[i] in every cache (tensors whose dim 0 is the cache row), in place.
+    The pages of dst must differ from one another and from those of src; entries below 0 are skipped."""
+    _need_cuda(src, dst, *caches)
+    _same_device(src.device, dst, *caches)
+    arr, n_pages = _page_caches(caches, page_size)
+    _i32("src", src, 0)
+    _i32("dst", dst, 0)
+    if src.numel() != dst.numel():
+        raise ValueError("src and dst must have the same length")
+    with _on(src.device):
+        _check(load().idx_page_copy(arr, len(caches), page_size, n_pages, src.data_ptr(), dst.data_ptr(), src.numel(),
+                                    _stream(src.device)))
+
+
+def _table(name: str, t: torch.Tensor):
+    if t.dim() != 2 or t.dtype != torch.int32 or (t.shape[1] > 1 and t.stride(1) != 1) or \
+            (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{name} must be an int32 [sequences, pages] tensor with contiguous rows")
+    return max(t.stride(0), t.shape[1])
+
+
+def _held(held, n_pages):
+    if held is not None and (held.dtype not in (torch.uint8, torch.bool) or not held.is_contiguous() or
+                             held.numel() != n_pages):
+        raise ValueError("held must be a contiguous uint8 or bool tensor with one entry per page")
+
+
+def idx_page_update(page_table: torch.Tensor, parent: torch.Tensor, n_keep: torch.Tensor, n_new: torch.Tensor,
+                    page_size: int, caches, *, held: Optional[torch.Tensor] = None,
+                    new_table: Optional[torch.Tensor] = None, n_free: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None):
+    """One step's frees, truncations, forks and growth of the sequences over a page table: row b of the
+    new table is the first n_keep[b] positions of row parent[b] of the old one (-1: nothing), with pages
+    for n_new[b] positions.  Whole pages are shared, a shared last page is copied in every cache, new pages
+    are the lowest free ones (neither named by a new row nor held).  Returns (new_table, n_free): n_free
+    (int32 [1], on the device) is the number of pages left, minus the number missing if there were too few
+    (new_table is then not written), or -2**31 if a request was impossible."""
+    _need_cuda(page_table, parent, n_keep, n_new, held, new_table, n_free, workspace, *caches)
+    _same_device(page_table.device, parent, n_keep, n_new, held, new_table, n_free, workspace, *caches)
+    arr, n_pages = _page_caches(caches, page_size)
+    stride = _table("page_table", page_table)
+    n = parent.numel()
+    for name, t in (("parent", parent), ("n_keep", n_keep), ("n_new", n_new)):
+        _i32(name, t, n)
+    if n_keep.numel() != n or n_new.numel() != n:
+        raise ValueError("parent, n_keep and n_new must have the same length")
+    _held(held, n_pages)
+    if new_table is None:
+        new_table = torch.empty(n, page_table.shape[1], device=page_table.device, dtype=torch.int32)
+    elif new_table.shape[0] != n:
+        raise ValueError("new_table must have one row per entry of parent")
+    new_stride = _table("new_table", new_table)
+    _i32("n_free", n_free, 1)
+    if n_free is None:
+        n_free = torch.empty(1, device=page_table.device, dtype=torch.int32)
+    lib = load()
+    with _on(page_table.device):
+        if workspace is None:
+            workspace = torch.empty(max(lib.idx_page_workspace_size(n, n_pages), 16), device=page_table.device,
+                                    dtype=torch.uint8)
+        _check(lib.idx_page_update(page_table.data_ptr(), stride, page_table.shape[1], page_table.shape[0],
+                                   parent.data_ptr(), n_keep.data_ptr(), n_new.data_ptr(), n, page_size, n_pages,
+                                   _ptr(held), new_table.data_ptr(), new_stride, new_table.shape[1], n_free.data_ptr(),
+                                   arr, len(caches), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                   _stream(page_table.device)))
+    return new_table, n_free
+
+
+def idx_page_compact(page_table: torch.Tensor, n_len: torch.Tensor, page_size: int, caches, *,
+                     held: Optional[torch.Tensor] = None, new_table: Optional[torch.Tensor] = None,
+                     n_used: Optional[torch.Tensor] = None, remap: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None):
+    """Moves the used pages (those of the first n_len[b] positions of each row; held ones stay where they
+    are) to the lowest numbers, in every cache.  Returns (new_table, n_used, remap): n_used (int32 [1], on
+    the device) counts the used and held pages, remap[p] is the new number of page p.  new_table may be
+    page_table itself."""
+    _need_cuda(page_table, n_len, held, new_table, n_used, remap, workspace, *caches)
+    _same_device(page_table.device, n_len, held, new_table, n_used, remap, workspace, *caches)
+    arr, n_pages = _page_caches(caches, page_size)
+    stride = _table("page_table", page_table)
+    n = page_table.shape[0]
+    _i32("n_len", n_len, n)
+    if n_len.numel() != n:
+        raise ValueError("n_len must have one entry per row of page_table")
+    _held(held, n_pages)
+    dev = page_table.device
+    if new_table is None:
+        new_table = torch.empty(n, page_table.shape[1], device=dev, dtype=torch.int32)
+    elif new_table.shape != page_table.shape:
+        raise ValueError("new_table must have page_table's shape")
+    new_stride = _table("new_table", new_table)
+    _i32("n_used", n_used, 1)
+    _i32("remap", remap, n_pages)
+    if n_used is None:
+        n_used = torch.empty(1, device=dev, dtype=torch.int32)
+    if remap is None:
+        remap = torch.empty(n_pages, device=dev, dtype=torch.int32)
+    lib = load()
+    with _on(dev):
+        if workspace is None:
+            workspace = torch.empty(max(lib.idx_page_workspace_size(n, n_pages), 16), device=dev, dtype=torch.uint8)
+        _check(lib.idx_page_compact(page_table.data_ptr(), stride, page_table.shape[1], n, n_len.data_ptr(), page_size,
+                                    n_pages, _ptr(held), new_table.data_ptr(), new_stride, n_used.data_ptr(),
+                                    remap.data_ptr(), arr, len(caches), workspace.data_ptr(),
+                                    workspace.numel() * workspace.element_size(), _stream(dev)))
+    return new_table, n_used, remap
 
 
 def idx_device_status(reset: bool = True) -> int:

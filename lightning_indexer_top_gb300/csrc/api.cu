@@ -148,8 +148,16 @@ idx_status attn_common(const char* what, const void* q, idx_dtype dtype, int32_t
 // for entry points defined in other files: record the calling thread's message
 idx_status record_error(idx_status s, const char* msg) { return fail(s, "%s", msg); }
 
+// for entry points defined in other files: the checks of a batch
+idx_status validate_batch(const idx_batch& b, const char* what) { return check_batch(b, what); }
+
+// for entry points defined in other files: the status of a launch
+idx_status cuda_status(cudaError_t e, const char* what) { return from_cuda(e, what); }
+
 // for entry points defined in other files: the kernels' view of a validated batch
 Geom geom_of(const idx_batch& b) { return make_geom(b); }
+
+int* device_status_ptr() { return status_ptr(); }
 
 int sm_count() {
     const int dev = current_device();

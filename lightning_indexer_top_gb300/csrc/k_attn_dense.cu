@@ -1,0 +1,458 @@
+// Dense attention over (paged) caches on the CUDA cores (dense_attn in lidx.h):
+// every type, head layout, width and alignment, and all of f32.
+//
+// The T query rows and the G = Hq / Hkv heads that share kv head g are packed
+// into rows m = t*G + h, so that a tile of R packed rows reads each K and V row
+// once for all of them.  A CTA of 128 threads owns R rows (64 for wide chunks,
+// 16 for few rows or values wider than 128) and one split of the key line, and
+// walks it in tiles of 32 keys held in shared memory as f32:
+//   scores: thread = (row group, key group), a register block of 4 rows x
+//           (R/16) keys fed by 16-byte reads; masked by the rows' intervals;
+//   softmax: running maximum and sum per row (natural logarithm), f32;
+//   values: thread = (row group, 4-column groups), a register block of the
+//           output rescaled by the rows' factors each tile.
+// Bound by the f32 FMAs (and, for few rows, by the latency of a tile's loads).
+// A key that only some rows of a tile see is skipped, not multiplied by zero,
+// for the others, so that NaN or infinity in it cannot reach them.
+#include <float.h>
+
+#include "dense_attn.cuh"
+
+namespace lidx {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kKeys = 32;
+
+__host__ __device__ constexpr int round_up(int x, int m) { return (x + m - 1) / m * m; }
+
+template <int R, int DV>
+struct Shape {
+    static constexpr int kKeyGroups = R == 64 ? 8 : 32;      // threads along the keys (scores)
+    static constexpr int kRowGroups = kThreads / kKeyGroups; // R / 4
+    static constexpr int kKeysPer = kKeys / kKeyGroups;
+    static constexpr int kColGroups = R == 64 ? 16 : 32;     // threads along the columns (values)
+    static constexpr int kRowsPer = R / (kThreads / kColGroups);
+    static constexpr int kCol4 = DV / (4 * kColGroups);      // 4-column groups per thread
+    static_assert(kRowGroups * 4 == R && kRowsPer % 4 == 0 && kCol4 >= 1, "thread layout");
+};
+
+size_t smem_bytes(int R, int DV, int dk, bool latent) {
+    const int kp = round_up(dk, 4) + 4;
+    const int vp = DV + 4;
+    return sizeof(float) * ((size_t)R * kp + (size_t)kKeys * kp + (latent ? 0 : (size_t)kKeys * vp) +
+                            (size_t)kKeys * (R + 4) + 2 * R) +
+           sizeof(int) * 3 * R + sizeof(int64_t) * kKeys;
+}
+
+template <typename T, int R, int DV>
+__global__ void __launch_bounds__(kThreads) dense_generic_kernel(DenseArgs a, Geom g, int tiles, bool vec) {
+    using S = Shape<R, DV>;
+    extern __shared__ __align__(16) unsigned char sm_raw[];
+    const int kp = round_up(a.dk, 4) + 4;       // K and Q pitch: rows 4 banks apart
+    const bool latent = a.v == nullptr;
+    const int vp = latent ? kp : DV + 4;
+    int64_t* rows_s = reinterpret_cast<int64_t*>(sm_raw);
+    float* qs = reinterpret_cast<float*>(rows_s + kKeys);       // [R][kp]
+    float* ks = qs + R * kp;                                    // [kKeys][kp]
+    float* vs = latent ? ks : ks + kKeys * kp;                  // [kKeys][vp]
+    float* ss = (latent ? ks + kKeys * kp : vs + kKeys * vp);   // [kKeys][R + 4] scores, then weights
+    float* alpha_s = ss + kKeys * (R + 4);                      // [R]
+    float* slope_s = alpha_s + R;                               // [R]
+    int* lo_s = reinterpret_cast<int*>(slope_s + R);
+    int* hi_s = lo_s + R;
+    int* pos_s = hi_s + R;
+
+    const int tid = threadIdx.x;
+    const int G = a.Hq / a.Hkv;
+    int64_t u = blockIdx.x;
+    const int split = (int)(u % a.splits);
+    u /= a.splits;
+    const int tile = (int)(u % tiles);
+    u /= tiles;
+    const int gkv = (int)(u % a.Hkv);
+    const int b = (int)(u / a.Hkv);
+    const int64_t m0 = (int64_t)tile * R;        // first packed row
+    const int64_t m_end = (int64_t)g.T * G;
+    pdl_trigger();
+    pdl_wait();
+    const int n_kv = seq_n_kv(g, b);
+
+    // the rows' intervals, and the CTA's: the keys that some row sees
+    if (tid < R) {
+        const int64_t m = m0 + tid;
+        Interval iv = {0, 0, 0};
+        float slope = 0.f;
+        if (m < m_end) {
+            const int t = (int)(m / G), h = gkv * G + (int)(m % G);
+            iv = row_interval(g, a.mods, (int64_t)b * g.T + t, b, n_kv);
+            if (a.mods.slopes) slope = a.mods.slopes[h];
+        }
+        lo_s[tid] = iv.lo;
+        hi_s[tid] = iv.hi;
+        pos_s[tid] = iv.pos;
+        slope_s[tid] = slope;
+    }
+    for (int i = tid; i < R * kp; i += kThreads) {
+        const int rr = i / kp, c = i % kp;
+        const int64_t m = m0 + rr;
+        float x = 0.f;
+        if (m < m_end && c < a.dk)
+            x = to_f32(static_cast<const T*>(a.q)[((int64_t)(b * (int64_t)g.T + m / G) * a.Hq + gkv * G + m % G) * a.dk + c]);
+        qs[i] = x;
+    }
+    // the columns that a tile's rows do not fill
+    for (int i = tid; i < kKeys * (kp - a.dk); i += kThreads) ks[i / (kp - a.dk) * kp + a.dk + i % (kp - a.dk)] = 0.f;
+    if (!latent && a.dv < vp)
+        for (int i = tid; i < kKeys * (vp - a.dv); i += kThreads)
+            vs[i / (vp - a.dv) * vp + a.dv + i % (vp - a.dv)] = 0.f;
+    __syncthreads();
+    int k0 = INT32_MAX, k1 = 0, full0 = 0, full1 = INT32_MAX;
+    for (int i = 0; i < R; ++i) {
+        const int lo = lo_s[i], hi = hi_s[i];
+        if (lo >= hi) continue;          // a row that sees nothing takes what it gets and writes zeros
+        k0 = min(k0, lo);
+        k1 = max(k1, hi);
+        full0 = max(full0, lo);
+        full1 = min(full1, hi);
+    }
+    const int64_t s0 = (int64_t)split * a.kps;
+    if (s0 > k0) k0 = (int)min(s0, (int64_t)INT32_MAX);
+    if (s0 + a.kps < k1) k1 = (int)(s0 + a.kps);
+
+    const int kg = tid % S::kKeyGroups, rg = tid / S::kKeyGroups;     // scores
+    const int cg = tid % S::kColGroups, vg = tid / S::kColGroups;     // values
+    constexpr int kPerRow = kThreads / R;                             // threads of a row's softmax
+    const int srow = tid / kPerRow, sk = tid % kPerRow;
+    float o[S::kRowsPer][4 * S::kCol4];
+#pragma unroll
+    for (int i = 0; i < S::kRowsPer; ++i)
+#pragma unroll
+        for (int c = 0; c < 4 * S::kCol4; ++c) o[i][c] = 0.f;
+    float m_run = -INFINITY, l_run = 0.f;
+    const float cap = a.mods.softcap, inv_cap = cap > 0.f ? 1.f / cap : 0.f;
+
+    for (int t0 = k0; t0 < k1; t0 += kKeys) {
+        __syncthreads();
+        if (tid < kKeys) {
+            int64_t row = -1;
+            if (t0 + tid < k1) {
+                row = key_row(g, b, t0 + tid);
+                if (row < 0 || row >= a.kv_rows) {
+                    flag(g.status, IDX_ERR_DEVICE_BOUNDS);
+                    row = -1;
+                }
+            }
+            rows_s[tid] = row;
+        }
+        const bool bad = __syncthreads_or(tid < kKeys && rows_s[tid < kKeys ? tid : 0] < 0);
+        // K and V rows, widened
+        if (vec) {
+            constexpr int E = 16 / (int)sizeof(T);
+            const int wk = a.dk / E, wv = latent ? 0 : a.dv / E;
+            const int total = kKeys * (wk + wv);
+            constexpr int kBatch = 4;
+            for (int e0 = tid; e0 < total; e0 += kThreads * kBatch) {
+                uint4 x[kBatch];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int e = e0 + i * kThreads;
+                    x[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (e < total) {
+                        const bool isk = e < kKeys * wk;
+                        const int ee = isk ? e : e - kKeys * wk, w = isk ? wk : wv;
+                        const int64_t row = rows_s[ee / w];
+                        if (row >= 0)
+                            x[i] = *reinterpret_cast<const uint4*>(
+                                isk ? static_cast<const T*>(a.k) + row * a.k_stride + (int64_t)gkv * a.dk + ee % w * E
+                                    : static_cast<const T*>(a.v) + row * a.v_stride + (int64_t)gkv * a.dv + ee % w * E);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int e = e0 + i * kThreads;
+                    if (e < total) {
+                        const bool isk = e < kKeys * wk;
+                        const int ee = isk ? e : e - kKeys * wk, w = isk ? wk : wv;
+                        float* d = isk ? ks + ee / w * kp + ee % w * E : vs + ee / w * vp + ee % w * E;
+                        const T* p = reinterpret_cast<const T*>(&x[i]);
+#pragma unroll
+                        for (int j = 0; j < E; ++j) d[j] = to_f32(p[j]);
+                    }
+                }
+            }
+        } else {
+            for (int e = tid; e < kKeys * a.dk; e += kThreads) {
+                const int64_t row = rows_s[e / a.dk];
+                ks[e / a.dk * kp + e % a.dk] =
+                    row >= 0 ? to_f32(static_cast<const T*>(a.k)[row * a.k_stride + (int64_t)gkv * a.dk + e % a.dk]) : 0.f;
+            }
+            if (!latent)
+                for (int e = tid; e < kKeys * a.dv; e += kThreads) {
+                    const int64_t row = rows_s[e / a.dv];
+                    vs[e / a.dv * vp + e % a.dv] =
+                        row >= 0 ? to_f32(static_cast<const T*>(a.v)[row * a.v_stride + (int64_t)gkv * a.dv + e % a.dv])
+                                 : 0.f;
+                }
+        }
+        __syncthreads();
+        // ---- scores
+        const bool whole = !bad && t0 >= full0 && t0 + kKeys <= min(full1, k1);
+        {
+            float acc[4][S::kKeysPer];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < S::kKeysPer; ++j) acc[i][j] = 0.f;
+            const float* qr = qs + rg * kp;
+            const float* kr = ks + kg * kp;
+            for (int c = 0; c < kp - 4; c += 4) {
+                float4 kk[S::kKeysPer], qq[4];
+#pragma unroll
+                for (int j = 0; j < S::kKeysPer; ++j)
+                    kk[j] = *reinterpret_cast<const float4*>(kr + j * S::kKeyGroups * kp + c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) qq[i] = *reinterpret_cast<const float4*>(qr + i * S::kRowGroups * kp + c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < S::kKeysPer; ++j) {
+                        acc[i][j] = fmaf(qq[i].x, kk[j].x, acc[i][j]);
+                        acc[i][j] = fmaf(qq[i].y, kk[j].y, acc[i][j]);
+                        acc[i][j] = fmaf(qq[i].z, kk[j].z, acc[i][j]);
+                        acc[i][j] = fmaf(qq[i].w, kk[j].w, acc[i][j]);
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int rr = rg + i * S::kRowGroups;
+#pragma unroll
+                for (int j = 0; j < S::kKeysPer; ++j) {
+                    float x = acc[i][j] * a.scale;
+                    if (cap > 0.f) x = cap * tanhf(x * inv_cap);
+                    const int kl = kg + j * S::kKeyGroups;
+                    if (a.mods.slopes) x -= slope_s[rr] * fabsf((float)((int64_t)pos_s[rr] - (t0 + kl)));
+                    ss[kl * (R + 4) + rr] = x;
+                }
+            }
+        }
+        __syncthreads();
+        // ---- softmax: kPerRow threads of a warp per row; a masked key's weight is marked by -1
+        {
+            const int lo = lo_s[srow], hi = hi_s[srow];
+            const bool none = lo >= hi;
+            float mt = -INFINITY;
+            uint32_t seen = 0u;
+#pragma unroll
+            for (int j = 0; j < kKeys / kPerRow; ++j) {
+                const int kl = sk + j * kPerRow;
+                const int key = t0 + kl;
+                const bool v = whole ? !none : (key >= lo && key < hi && key < k1 && rows_s[kl] >= 0);
+                if (v) {
+                    seen |= 1u << j;
+                    mt = fmaxf(mt, ss[kl * (R + 4) + srow]);
+                }
+            }
+#pragma unroll
+            for (int off = 1; off < kPerRow; off <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, off));
+            const float m_new = fmaxf(m_run, mt);
+            const float m_ref = m_new == -INFINITY ? 0.f : m_new;
+            const float alpha = m_run == m_new ? 1.f : expf(m_run - m_ref);
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < kKeys / kPerRow; ++j) {
+                float* p = ss + (sk + j * kPerRow) * (R + 4) + srow;
+                if ((seen >> j) & 1u) {
+                    const float w = expf(*p - m_ref);
+                    *p = w;
+                    sum += w;
+                } else {
+                    *p = -1.f;
+                }
+            }
+#pragma unroll
+            for (int off = 1; off < kPerRow; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            l_run = l_run * alpha + sum;
+            m_run = m_new;
+            if (sk == 0) alpha_s[srow] = alpha;
+        }
+        __syncthreads();
+        // ---- values
+        bool scaled = false;
+#pragma unroll
+        for (int i = 0; i < S::kRowsPer; ++i) scaled |= alpha_s[vg * S::kRowsPer + i] != 1.f;
+        if (scaled) {
+#pragma unroll
+            for (int i = 0; i < S::kRowsPer; ++i) {
+                const float al = alpha_s[vg * S::kRowsPer + i];
+#pragma unroll
+                for (int c = 0; c < 4 * S::kCol4; ++c) o[i][c] *= al;
+            }
+        }
+        const int n_keys = min(kKeys, k1 - t0);
+        auto values = [&](auto masked) {
+#pragma unroll 4
+            for (int kl = 0; kl < n_keys; ++kl) {
+                float p[S::kRowsPer];
+#pragma unroll
+                for (int i = 0; i < S::kRowsPer; i += 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(ss + kl * (R + 4) + vg * S::kRowsPer + i);
+                    p[i] = x.x;
+                    p[i + 1] = x.y;
+                    p[i + 2] = x.z;
+                    p[i + 3] = x.w;
+                }
+#pragma unroll
+                for (int c = 0; c < S::kCol4; ++c) {
+                    const int col = 4 * cg + 4 * S::kColGroups * c;
+                    if (col >= a.dv) continue;
+                    const float4 x = *reinterpret_cast<const float4*>(vs + kl * vp + col);
+#pragma unroll
+                    for (int i = 0; i < S::kRowsPer; ++i) {
+                        if (decltype(masked)::value && p[i] < 0.f) continue;
+                        o[i][4 * c] = fmaf(p[i], x.x, o[i][4 * c]);
+                        o[i][4 * c + 1] = fmaf(p[i], x.y, o[i][4 * c + 1]);
+                        o[i][4 * c + 2] = fmaf(p[i], x.z, o[i][4 * c + 2]);
+                        o[i][4 * c + 3] = fmaf(p[i], x.w, o[i][4 * c + 3]);
+                    }
+                }
+            }
+        };
+        if (whole)
+            values(std::false_type{});
+        else
+            values(std::true_type{});
+    }
+
+    // ---- output: l per row through shared memory
+    __syncthreads();
+    if (sk == 0) {
+        const bool none = lo_s[srow] >= hi_s[srow];
+        const float l = none ? 0.f : l_run;
+        alpha_s[srow] = l;
+        const int64_t m = m0 + srow;
+        if (m < m_end) {
+            const int64_t rh = ((int64_t)b * g.T + m / G) * a.Hq + gkv * G + m % G;
+            if (a.splits > 1) {
+                a.part_ml[(rh * a.splits + split) * 2] = m_run;
+                a.part_ml[(rh * a.splits + split) * 2 + 1] = l;
+            } else if (a.lse) {
+                a.lse[rh] = l == 0.f ? -INFINITY : m_run + logf(l);
+            }
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < S::kRowsPer; ++i) {
+        const int rr = vg * S::kRowsPer + i;
+        const int64_t m = m0 + rr;
+        if (m >= m_end) continue;
+        const int64_t rh = ((int64_t)b * g.T + m / G) * a.Hq + gkv * G + m % G;
+        const float l = alpha_s[rr];
+        const float inv = a.splits > 1 ? 1.f : 1.f / l;
+#pragma unroll
+        for (int c = 0; c < S::kCol4; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int col = 4 * cg + 4 * S::kColGroups * c + e;
+                if (col >= a.dv) continue;
+                const float x = l == 0.f ? 0.f : o[i][4 * c + e] * inv;
+                if (a.splits > 1)
+                    a.part_o[(rh * a.splits + split) * a.dv + col] = x;
+                else
+                    static_cast<T*>(a.out)[rh * a.dv + col] = from_f32<T>(x);
+            }
+    }
+}
+
+// one warp per (row, head): out = sum_s e^(m_s - M) o_s / sum_s e^(m_s - M) l_s
+template <typename T>
+__global__ void __launch_bounds__(128) dense_combine_kernel(DenseArgs a, int64_t n) {
+    pdl_trigger();
+    pdl_wait();
+    const int64_t rh = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (rh >= n) return;
+    const float* ml = a.part_ml + rh * a.splits * 2;
+    float M = -INFINITY;
+    for (int s = lane; s < a.splits; s += 32)
+        if (ml[2 * s + 1] != 0.f) M = fmaxf(M, ml[2 * s]);
+#pragma unroll
+    for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    float den = 0.f;
+    for (int s = lane; s < a.splits; s += 32)
+        if (ml[2 * s + 1] != 0.f) den += expf(ml[2 * s] - M) * ml[2 * s + 1];
+#pragma unroll
+    for (int off = 16; off; off >>= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
+    if (a.lse && lane == 0) a.lse[rh] = den == 0.f ? -INFINITY : M + logf(den);
+    const float inv = 1.f / den;
+    for (int c = lane; c < a.dv; c += 32) {
+        float acc = 0.f;
+        for (int s = 0; s < a.splits; ++s)
+            if (ml[2 * s + 1] != 0.f) acc += expf(ml[2 * s] - M) * a.part_o[(rh * a.splits + s) * a.dv + c];
+        static_cast<T*>(a.out)[rh * a.dv + c] = from_f32<T>(den == 0.f ? 0.f : acc * inv);
+    }
+}
+
+// rows of a CTA's tile: 64 when the sequence's packed rows fill more than one tile of 16 and the
+// values are at most 128 wide (the wider output block needs the registers)
+int tile_rows(int64_t packed, int dv) { return dv <= 128 && packed > 16 ? 64 : 16; }
+
+template <typename T>
+cudaError_t run(const DenseArgs& a, const Geom& g, cudaStream_t st) {
+    const int64_t packed = (int64_t)g.T * (a.Hq / a.Hkv);
+    const int R = tile_rows(packed, a.dv);
+    const int64_t tiles = (packed + R - 1) / R;
+    const int64_t grid = (int64_t)g.B * a.Hkv * tiles * a.splits;
+    if (grid > INT32_MAX || tiles > INT32_MAX) return cudaErrorNotSupported;
+    const uint64_t all = reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) |
+                         (uint64_t)a.k_stride * sizeof(T) | (a.v ? (uint64_t)a.v_stride * sizeof(T) : 0) |
+                         (uint64_t)a.dk * sizeof(T) | (a.v ? (uint64_t)a.dv * sizeof(T) : 0);
+    const bool vec = all % 16 == 0;
+    auto go = [&](auto kern, int dvp) {
+        const size_t sm = smem_bytes(R, dvp, a.dk, !a.v);
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+        if (e != cudaSuccess) return e;
+        return launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), sm, st, a, g, (int)tiles, vec);
+    };
+    if (R == 64) return a.dv <= 64 ? go(dense_generic_kernel<T, 64, 64>, 64) : go(dense_generic_kernel<T, 64, 128>, 128);
+    return a.dv <= 128 ? go(dense_generic_kernel<T, 16, 128>, 128) : go(dense_generic_kernel<T, 16, 512>, 512);
+}
+
+}  // namespace
+
+// enough CTAs to cover the SMs four times, at least 128 keys per split
+int dense_generic_splits(int64_t n_seq, int64_t n_q, int64_t max_n_kv, int Hq, int Hkv, int dk, int dv) {
+    (void)dk;
+    const int64_t packed = n_q * (Hq / Hkv);
+    const int R = tile_rows(packed, dv);
+    const int64_t units = n_seq * Hkv * ((packed + R - 1) / R);
+    int sms = sm_count();
+    if (sms < 2) sms = 152;
+    if (units < 1) return 1;
+    int64_t s = 4 * (int64_t)sms / units;
+    const int64_t by_keys = (max_n_kv + 127) / 128;
+    if (s > by_keys) s = by_keys;
+    if (s > 128) s = 128;
+    return s < 1 ? 1 : (int)s;
+}
+
+cudaError_t launch_dense_generic(const DenseArgs& a, int dtype, const Geom& g, cudaStream_t st) {
+    switch (dtype) {
+        case IDX_F16: return run<__half>(a, g, st);
+        case IDX_BF16: return run<__nv_bfloat16>(a, g, st);
+        default: return run<float>(a, g, st);
+    }
+}
+
+cudaError_t launch_dense_combine(const DenseArgs& a, int dtype, int64_t n_rows, cudaStream_t st) {
+    const int64_t n = n_rows * a.Hq;
+    const dim3 grid((unsigned)((n + 3) / 4));
+    switch (dtype) {
+        case IDX_F16: return launch_pdl(dense_combine_kernel<__half>, grid, dim3(128), 0, st, a, n);
+        case IDX_BF16: return launch_pdl(dense_combine_kernel<__nv_bfloat16>, grid, dim3(128), 0, st, a, n);
+        default: return launch_pdl(dense_combine_kernel<float>, grid, dim3(128), 0, st, a, n);
+    }
+}
+
+}  // namespace lidx

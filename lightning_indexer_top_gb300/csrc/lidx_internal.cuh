@@ -271,4 +271,11 @@ idx_status record_error(idx_status s, const char* msg);
 // kernel geometry of a batch (with the device status word of the current device)
 Geom geom_of(const idx_batch& b);
 
+// the checks every entry point makes of its batch, and the status of a launch (both record their message)
+idx_status validate_batch(const idx_batch& b, const char* what);
+idx_status cuda_status(cudaError_t e, const char* what);
+
+// the device status word of the current device (NULL when there is none)
+int* device_status_ptr();
+
 }  // namespace lidx
