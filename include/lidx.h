@@ -478,7 +478,8 @@ int32_t sparse_decode_step_fused(int64_t n_rows, int32_t n_q_per_seq, int32_t ma
  * Sums, maxima and outputs are accumulated in f32.  A key row outside the cache
  * (a page number out of range) is skipped and flagged (IDX_ERR_DEVICE_BOUNDS).
  * Errors: those of sparse_attn_decode's arguments; softcap or window negative,
- * softcap not finite, window, slopes or prefix_len without q_pos: INVALID_ARG.
+ * softcap not finite, window, slopes or prefix_len without q_pos: INVALID_ARG;
+ * max_n_kv > 2^31 - 1025: UNSUPPORTED.
  */
 typedef struct idx_attn_mods {
     float softcap;             /* 0: scores are not capped */

@@ -32,6 +32,12 @@ idx_status bad(idx_status s, const char* fmt, ...) {
     return record_error(s, buf);
 }
 
+// the key splits that a call of these sizes would like (the tensor-core kernel's where its types and widths are)
+int want_splits(int dtype, int64_t n_seq, int64_t n_q, int64_t max_n_kv, int Hq, int Hkv, int dk, int dv, bool tc) {
+    return tc ? dense_tc_splits(n_seq, n_q, max_n_kv, Hq, Hkv)
+              : dense_generic_splits(n_seq, n_q, max_n_kv, Hq, Hkv, dk, dv);
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // bytes of one split's partial results
@@ -64,11 +70,12 @@ extern "C" {
 
 size_t dense_attn_workspace_size(idx_dtype dtype, int32_t n_seq, int32_t n_q_per_seq, int32_t max_n_kv,
                                  int32_t n_q_heads, int32_t n_kv_heads, int32_t dk, int32_t dv) {
-    (void)dtype;
     if (n_seq < 1 || n_q_per_seq < 1 || max_n_kv < 1 || n_kv_heads < 1 || n_q_heads < 1 || n_q_heads % n_kv_heads ||
         dk < 1 || dk > 576 || dv < 1 || dv > 512)
         return 0;
-    const int splits = dense_generic_splits(n_seq, n_q_per_seq, max_n_kv, n_q_heads, n_kv_heads, dk, dv);
+    // (a call whose pages or addresses the tensor-core kernel does not take splits as far as this reaches)
+    const bool tc = dtype != IDX_F32 && dk <= 128 && dv <= 128 && dk % 8 == 0 && dv % 8 == 0;
+    const int splits = want_splits(dtype, n_seq, n_q_per_seq, max_n_kv, n_q_heads, n_kv_heads, dk, dv, tc);
     return splits > 1 ? splits * split_bytes((int64_t)n_seq * n_q_per_seq, n_q_heads, dv) : 0;
 }
 
@@ -101,6 +108,8 @@ idx_status dense_attn(const void* q, idx_dtype dtype, int32_t n_q_heads, int32_t
         return bad(IDX_ERR_INVALID_ARG, "%s: window, slopes and prefix_len need q_pos", what);
     if (workspace && !aligned16(workspace))
         return bad(IDX_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", what);
+    if (batch.max_n_kv > INT32_MAX - 1024)
+        return bad(IDX_ERR_UNSUPPORTED, "%s: max_n_kv must be at most 2^31 - 1025", what);
     const int64_t n_rows = (int64_t)batch.n_seq * batch.n_q_per_seq;
     if (n_rows == 0) return IDX_OK;
     if (!q || !out || (batch.max_n_kv > 0 && !k)) return bad(IDX_ERR_INVALID_ARG, "%s: NULL q/k/out", what);
@@ -121,15 +130,23 @@ idx_status dense_attn(const void* q, idx_dtype dtype, int32_t n_q_heads, int32_t
     const cudaStream_t st = (cudaStream_t)stream;
     const size_t per_split = split_bytes(n_rows, n_q_heads, dv);
     const int64_t fit = workspace ? (int64_t)(workspace_bytes / per_split) : 0;
-    int64_t splits = dense_generic_splits(batch.n_seq, batch.n_q_per_seq, batch.max_n_kv, n_q_heads, n_kv_heads, dk, dv);
+    const bool tc = dense_tc_supported(a, dtype, g);
+    int64_t splits = want_splits(dtype, batch.n_seq, batch.n_q_per_seq, batch.max_n_kv, n_q_heads, n_kv_heads, dk, dv, tc);
     if (splits > fit) splits = fit;
     if (splits < 1) splits = 1;
+    // keys per split: whole tiles; fewer splits where that leaves some without keys
+    const int64_t unit = tc ? kDenseTcKeys : 1;
+    int64_t kps = ((int64_t)batch.max_n_kv + splits - 1) / splits;
+    kps = kps < 1 ? unit : (kps + unit - 1) / unit * unit;
+    splits = ((int64_t)batch.max_n_kv + kps - 1) / kps;
+    if (splits < 1) splits = 1;
+    if (kps > INT32_MAX) kps = INT32_MAX;   // (one split)
     a.splits = (int32_t)splits;
-    const int64_t kps = ((int64_t)batch.max_n_kv + splits - 1) / splits;
-    a.kps = (int32_t)(kps < 1 ? 1 : kps);
+    a.kps = (int32_t)kps;
     a.part_o = splits > 1 ? static_cast<float*>(workspace) : nullptr;
     a.part_ml = splits > 1 ? a.part_o + (size_t)n_rows * n_q_heads * dv * splits : nullptr;
-    cudaError_t e = launch_dense_generic(a, dtype, g, st);
+    cudaError_t e = tc ? launch_dense_tc(a, dtype, g, st) : cudaErrorNotSupported;
+    if (e == cudaErrorNotSupported) e = launch_dense_generic(a, dtype, g, st);
     if (e == cudaSuccess && splits > 1) e = launch_dense_combine(a, dtype, n_rows, st);
     return cuda_status(e, what);
 }

@@ -54,6 +54,12 @@ __device__ __forceinline__ Interval row_interval(const Geom& g, const idx_attn_m
 cudaError_t launch_dense_generic(const DenseArgs& a, int dtype, const Geom& g, cudaStream_t st);
 int dense_generic_splits(int64_t n_seq, int64_t n_q, int64_t max_n_kv, int Hq, int Hkv, int dk, int dv);
 
+// tensor cores: 16-bit K and V of at most 128 columns each, 16-byte aligned, pages of a multiple of 8 rows
+bool dense_tc_supported(const DenseArgs& a, int dtype, const Geom& g);
+cudaError_t launch_dense_tc(const DenseArgs& a, int dtype, const Geom& g, cudaStream_t st);
+int dense_tc_splits(int64_t n_seq, int64_t n_q, int64_t max_n_kv, int Hq, int Hkv);
+constexpr int kDenseTcKeys = 128;   // its splits are whole tiles of this many keys
+
 // merges part_o / part_ml into out and lse
 cudaError_t launch_dense_combine(const DenseArgs& a, int dtype, int64_t n_rows, cudaStream_t st);
 

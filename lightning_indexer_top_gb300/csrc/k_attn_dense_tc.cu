@@ -1,0 +1,696 @@
+// Dense attention over (paged) caches on the 5th-generation tensor cores
+// (dense_attn in lidx.h), for 16-bit K/V of at most 128 columns each.
+//
+// The T query rows and the G = Hq / Hkv heads that share a kv head are packed
+// into rows m = t*G + h, 128 to a tile (the M side of the MMAs), so a K or V
+// tile that is read once serves every head of the group.  A CTA owns kTiles
+// such tiles of one (sequence, kv head) and one split of the key line, and
+// walks it in tiles of 128 keys:
+//     S = Q K^T       [128 x 128] f32 in TMEM     (Q, K from shared memory)
+//     P = 2^(S*c - m) bf16/f16, written over S in TMEM
+//     O = O + P V     [128 x dv] f32 in TMEM      (P from TMEM, V from shared memory)
+// Warps 0-3: TMA producer, MMA issuer, two V checkers; then four softmax warps
+// per row tile (thread = row = TMEM lane), which also write the output.  With
+// two row tiles the tensor core works on one while the other's softmax runs,
+// and a K/V tile is read for 256 rows; with one (few rows: a decode step) the
+// walk is bound by the stream of K and V.
+//
+// A row's maximum follows its scores lazily: O is rescaled (by the softmax
+// warps, in TMEM) only when a score passes it by 2^8, so P stays <= 2^8.
+// f16 weights are kept 2^7 larger still, so that weights down to 2^-31 of the
+// largest are not lost in f16's subnormals.  P is rounded to the inputs' type
+// for the second product (an error of half a step, averaged over the keys); its
+// sum, the maxima and O stay f32.
+//
+// Masks are intervals: a tile that every row of a warp sees whole skips them.
+// A tile that some row sees in part is looked over before its PV product: V rows
+// that nobody sees (a page's unwritten end) are zeroed in shared memory, and a
+// NaN or infinity in any other row of it - 0 times which would reach rows that
+// do not see it - sends the CTA's rows to a scalar loop over their own keys,
+// as does a page number out of range (found before anything is loaded).
+// Every wait is bounded; a timeout records IDX_ERR_TIMEOUT and the CTA winds down.
+#include "dense_attn.cuh"
+#include "sm100_ptx.cuh"
+
+namespace lidx {
+namespace {
+using namespace sm100;
+
+constexpr int kKeys = 128;             // keys per tile
+constexpr int kRows = 128;             // packed query rows per row tile
+constexpr int kColBlock = 128 * 128;   // 64 columns x 128 rows of a tile, in the 128-byte swizzle
+constexpr int kOtherWarps = 4;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int D, int kTiles>
+struct Cfg {
+    static constexpr int kTileBytes = kKeys * D * 2;
+    static constexpr int kQBytes = kTiles * kRows * D * 2;
+    static constexpr int kStagesK = kTiles == 2 ? 2 : 3;
+    static constexpr int kStagesV = 3;
+    static constexpr int kVOff = kQBytes + kStagesK * kTileBytes;
+    static constexpr int kCtlOff = kVOff + kStagesV * kTileBytes;
+    static constexpr int kThreads = 32 * kOtherWarps + kRows * kTiles;
+    static constexpr int kTmemCols = kTiles == 2 ? 512 : 256;
+    static constexpr int kOCol = kTiles * kKeys;      // O of row tile i at kOCol + i*D
+};
+
+struct Ctl {
+    uint64_t kfull[3], kempty[3];
+    uint64_t vfull[3], vempty[3];
+    uint64_t vok[3];              // V looked over (both checker warps)
+    uint64_t sfull[2];            // S of a row tile written (and its earlier PV products complete)
+    uint64_t pready[2];           // P of a row tile written, O rescaled
+    uint64_t odone[2];            // every product of a row tile complete
+    uint64_t done;
+    uint32_t tmem_base;
+    int abort;
+    int dirty;                    // a NaN or infinity in a V row that only some rows see
+    int k0, k1, full0, full1;     // the CTA's keys, and those that each of its rows sees
+};
+
+template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&x);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+    const __half2 x = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&x);
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// the options as the softmax applies them, in log2 units
+struct Score {
+    float c;            // scale * log2(e)
+    float inv_cap;      // scale / softcap (0: no cap)
+    float cap;          // softcap * log2(e)
+    float slope;        // the row's slope * log2(e)
+    bool biased;        // slopes are given
+};
+
+// tanh on [-1/2, 1/2] by its Taylor series up to x^13 (the next term is below 2^-23 of x there)
+__device__ __forceinline__ float tanh_small(float x) {
+    const float y = x * x;
+    float p = 21844.f / 6081075.f;
+    p = fmaf(p, y, -1382.f / 155925.f);
+    p = fmaf(p, y, 62.f / 2835.f);
+    p = fmaf(p, y, -17.f / 315.f);
+    p = fmaf(p, y, 2.f / 15.f);
+    p = fmaf(p, y, -1.f / 3.f);
+    return fmaf(p * y, x, x);
+}
+
+// 1 - 2 / (1 + e^(2x)): for |x| > 1/2, where it does not cancel
+__device__ __forceinline__ float tanh_large(float x) {
+    return fmaf(-2.f, rcp_approx(1.f + ex2_approx(x * (2.f * kLog2e))), 1.f);
+}
+
+// 32 raw products -> scores in log2 units; d0 = the row's position minus the first key's
+__device__ __forceinline__ void modify(float (&s)[32], const Score& sc, float d0) {
+    if (sc.inv_cap != 0.f) {
+        float big = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            s[i] *= sc.inv_cap;
+            big = fmaxf(big, fabsf(s[i]));
+        }
+        if (__any_sync(0xffffffffu, big > 0.5f)) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const float t = fabsf(s[i]) > 0.5f ? tanh_large(s[i]) : tanh_small(s[i]);
+                s[i] = sc.cap * t;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[i] = sc.cap * tanh_small(s[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s[i] *= sc.c;
+    }
+    if (sc.biased) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s[i] = fmaf(-sc.slope, fabsf(d0 - (float)i), s[i]);
+    }
+}
+
+struct TcArgs {
+    DenseArgs a;
+    int tiles;        // groups of kTiles row tiles per (sequence, kv head)
+    int box;          // rows per TMA box: 128, or the largest power of two that divides the page
+};
+
+// The rows' attention key by key, each thread its own row: the rare way, see the top.  q, K and V as
+// stored, f32 sums.  Returns the maximum (log2 units) and the sum; acc gets the weighted values.
+template <typename T>
+__device__ __noinline__ void scalar_row(const TcArgs& p, const Geom& g, int b, int gkv, int64_t qrow, int h, Interval iv,
+                                        int64_t s0, int64_t s1, float* acc, float* m_out, float* l_out) {
+    const DenseArgs& a = p.a;
+    const T* q = static_cast<const T*>(a.q) + (qrow * a.Hq + h) * a.dk;
+    for (int c = 0; c < a.dv; ++c) acc[c] = 0.f;
+    float m = -INFINITY, l = 0.f;
+    const int64_t lo = iv.lo > s0 ? iv.lo : s0, hi = iv.hi < s1 ? iv.hi : s1;
+    for (int64_t j = lo; j < hi; ++j) {
+        const int64_t row = key_row(g, b, j);
+        if (row < 0 || row >= a.kv_rows) {
+            flag(g.status, IDX_ERR_DEVICE_BOUNDS);
+            continue;
+        }
+        const T* k = static_cast<const T*>(a.k) + row * a.k_stride + (int64_t)gkv * a.dk;
+        const T* v = static_cast<const T*>(a.v) + row * a.v_stride + (int64_t)gkv * a.dv;
+        float x = 0.f;
+        for (int c = 0; c < a.dk; ++c) x = fmaf(to_f32(q[c]), to_f32(k[c]), x);
+        x *= a.scale;
+        if (a.mods.softcap > 0.f) x = a.mods.softcap * tanhf(x / a.mods.softcap);
+        if (a.mods.slopes) x -= a.mods.slopes[h] * fabsf((float)(iv.pos - j));
+        x *= kLog2e;
+        const float mn = fmaxf(m, x);
+        const float ref = mn == -INFINITY ? 0.f : mn;
+        const float al = m == mn ? 1.f : exp2f(m - ref);
+        const float w = exp2f(x - ref);
+        m = mn;
+        l = fmaf(l, al, w);
+        for (int c = 0; c < a.dv; ++c) acc[c] = fmaf(w, to_f32(v[c]), al == 1.f ? acc[c] : acc[c] * al);
+    }
+    *m_out = m;
+    *l_out = l;
+}
+
+// columns [c0, c0 + n) of a row's result, n a multiple of 8 and at most 32: normalised to the output, or a
+// split's partial
+template <typename T>
+__device__ __forceinline__ void store_cols(const DenseArgs& a, int64_t rh, int split, int c0, int n, const float (&v)[32],
+                                           float inv) {
+    if (a.splits > 1) {
+        float4* d = reinterpret_cast<float4*>(a.part_o + (rh * a.splits + split) * a.dv + c0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (4 * i < n) d[i] = make_float4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
+    } else {
+        uint4* d = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + rh * a.dv + c0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (8 * i < n)
+                d[i] = make_uint4(pack2<T>(v[8 * i] * inv, v[8 * i + 1] * inv), pack2<T>(v[8 * i + 2] * inv, v[8 * i + 3] * inv),
+                                  pack2<T>(v[8 * i + 4] * inv, v[8 * i + 5] * inv),
+                                  pack2<T>(v[8 * i + 6] * inv, v[8 * i + 7] * inv));
+    }
+}
+
+template <typename T, int D, int kTiles, bool kMods>
+__global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1)
+    dense_tc_kernel(TcArgs p, Geom g, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+    using C = Cfg<D, kTiles>;
+    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    constexpr float kShift = kBf16 ? 0.f : 7.f;     // P is kept this much (log2) larger
+    constexpr float kTop = kShift + 8.f;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* kt = smem + C::kQBytes;
+    uint8_t* vt = smem + C::kVOff;
+    Ctl& c = *reinterpret_cast<Ctl*>(smem + C::kCtlOff);
+    const DenseArgs& a = p.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = a.Hq / a.Hkv;
+    // units: key split fastest, then (sequence, kv head), then the row tiles from the last one on (under
+    // the causal bound they see the most keys)
+    int64_t u = blockIdx.x;
+    const int split = (int)(u % a.splits);
+    u /= a.splits;
+    const int bg = (int)(u % ((int64_t)g.B * a.Hkv));
+    const int tile = p.tiles - 1 - (int)(u / ((int64_t)g.B * a.Hkv));
+    const int gkv = bg % a.Hkv, b = bg / a.Hkv;
+    const int64_t m0 = (int64_t)tile * (kTiles * kRows), m_end = (int64_t)g.T * G;
+
+    pdl_trigger();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(&c.kfull[i], 1);
+            mbar_init(&c.kempty[i], 1);
+            mbar_init(&c.vfull[i], 1);
+            mbar_init(&c.vempty[i], 1);
+            mbar_init(&c.vok[i], 2);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&c.sfull[i], 1);
+            mbar_init(&c.pready[i], 4);
+            mbar_init(&c.odone[i], 1);
+        }
+        mbar_init(&c.done, 1);
+        c.abort = 0;
+        c.dirty = 0;
+        c.k0 = INT32_MAX;
+        c.k1 = 0;
+        c.full0 = 0;
+        c.full1 = INT32_MAX;
+        fence_mbar_init();
+        tma_prefetch_desc(&kmap);
+        tma_prefetch_desc(&vmap);
+    }
+    if (warp == 0) {
+        tmem_alloc(&c.tmem_base, C::kTmemCols);
+        tmem_relinquish();
+    }
+    pdl_wait();
+    __syncthreads();
+
+    // ---- the rows: interval, position, slope; the CTA's keys
+    const int n_kv = seq_n_kv(g, b);
+    const int rt = (warp - kOtherWarps) >> 2;                       // this thread's row tile (softmax warps)
+    const int64_t m = m0 + (int64_t)threadIdx.x - 32 * kOtherWarps; // ... and packed row
+    Interval iv = {0, 0, 0};
+    int64_t qrow = 0;
+    int h = 0, wlo = 0, whi = INT32_MAX;    // keys that every row of the warp sees
+    if (warp >= kOtherWarps) {
+        if (m < m_end) {
+            const int t = (int)(m / G);
+            h = gkv * G + (int)(m - (int64_t)t * G);
+            qrow = (int64_t)b * g.T + t;
+            iv = row_interval(g, a.mods, qrow, b, n_kv);
+        }
+        const bool some = iv.lo < iv.hi;    // rows that see nothing take what they get and write zeros
+        const int w0 = __reduce_min_sync(0xffffffffu, some ? iv.lo : INT32_MAX);
+        const int w1 = __reduce_max_sync(0xffffffffu, some ? iv.hi : 0);
+        wlo = __reduce_max_sync(0xffffffffu, some ? iv.lo : 0);
+        whi = __reduce_min_sync(0xffffffffu, some ? iv.hi : INT32_MAX);
+        if (lane == 0 && w1 > 0) {
+            atomicMin(&c.k0, w0);
+            atomicMax(&c.k1, w1);
+            atomicMax(&c.full0, wlo);
+            atomicMin(&c.full1, whi);
+        }
+    }
+    // Q: 16-byte pieces into the swizzled K-major layout; rows and columns past the end are zero
+    for (int i = threadIdx.x; i < kTiles * kRows * (D / 8); i += C::kThreads) {
+        const int r = i / (D / 8), cc = i % (D / 8);
+        const int64_t mm = m0 + r;
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (mm < m_end && cc * 8 < a.dk) {
+            const int64_t t = mm / G;
+            x = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) +
+                                                (((int64_t)b * g.T + t) * a.Hq + gkv * G + (mm - t * G)) * a.dk + cc * 8);
+        }
+        const int rr = r & (kRows - 1);
+        *reinterpret_cast<uint4*>(smem + (r / kRows) * (kRows * D * 2) + (cc >> 3) * kColBlock + rr * 128 +
+                                  (((cc & 7) ^ (rr & 7)) << 4)) = x;
+    }
+    __syncthreads();
+    // this split's keys, from a whole tile on (tiles are cuts of the position line)
+    const int64_t s0 = (int64_t)split * a.kps, s1 = s0 + a.kps;
+    int k0 = c.k0, k1 = c.k1;
+    if (k0 < s0) k0 = (int)(s0 < INT32_MAX ? s0 : INT32_MAX);
+    if (k1 > s1) k1 = (int)s1;
+    const int t0 = k0 / kKeys;
+    const int n = k1 > k0 ? (k1 + kKeys - 1) / kKeys - t0 : 0;
+    // every cache row of them exists?
+    bool bad = false;
+    if (n > 0) {
+        if (g.page_table) {
+            const int64_t p1 = ((int64_t)k1 - 1) / g.page_size;
+            for (int64_t pg = k0 / g.page_size + threadIdx.x; pg <= p1; pg += C::kThreads) {
+                const int64_t row = (int64_t)g.page_table[(int64_t)b * g.page_table_stride + pg] * g.page_size;
+                const int64_t last = pg == p1 ? (k1 - 1) % g.page_size : g.page_size - 1;
+                bad |= row < 0 || row + last >= a.kv_rows;
+            }
+        } else {
+            const int64_t row = seq_row0(g, b);
+            bad = row + k0 < 0 || row + k1 > a.kv_rows;
+        }
+    }
+    fence_proxy_async_smem();   // Q before the MMAs read it
+    tc_fence_before();
+    bad = __syncthreads_or(bad);
+    tc_fence_after();
+    const uint32_t tmem = c.tmem_base;
+    const int full0 = c.full0, full1 = c.full1;
+
+    if (n > 0 && !bad) {
+        auto aborted = [&] { return *(volatile int*)&c.abort != 0; };
+        auto warp_aborted = [&] { return __any_sync(0xffffffffu, aborted()); };
+        auto give_up = [&] {
+            *(volatile int*)&c.abort = 1;
+            flag(g.status, IDX_ERR_TIMEOUT);
+        };
+        if (warp == 0) {
+            // -------------------------------------------------- producer: a lane per (piece, 64 columns)
+            const int pieces = kKeys / p.box;
+            const int64_t row_base = g.page_table ? 0 : seq_row0(g, b);
+            int sent = 0;     // tiles whose loads were issued (K and V alike)
+            bool sent_v = true;
+            auto load = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* bar, int j) {
+                if (lane == 0) mbar_arrive_expect_tx(bar, C::kTileBytes);
+                __syncwarp();
+                if (lane < pieces * (D / 64)) {
+                    const int pc = lane / (D / 64), cb = lane % (D / 64);
+                    const int64_t key = (int64_t)(t0 + j) * kKeys + pc * p.box;
+                    // a piece that holds none of the keys is filled with zeros (a row past the cache)
+                    int64_t row = a.kv_rows;
+                    if (key < k1 && key + p.box > k0)
+                        row = g.page_table ? key_row(g, b, key) : row_base + key;
+                    tma_load_3d(dst + cb * kColBlock + pc * p.box * 128, map, bar, cb * 64, gkv, (int32_t)row);
+                }
+            };
+            for (int j = 0; j < n; ++j) {
+                const int sk = j % C::kStagesK, sv = j % C::kStagesV;
+                if (warp_aborted() || !warp_wait(&c.kempty[sk], (uint32_t)((j / C::kStagesK) & 1) ^ 1)) {
+                    give_up();
+                    break;
+                }
+                load(&kmap, kt + sk * C::kTileBytes, &c.kfull[sk], j);
+                sent = j + 1;
+                sent_v = false;
+                if (warp_aborted() || !warp_wait(&c.vempty[sv], (uint32_t)((j / C::kStagesV) & 1) ^ 1)) {
+                    give_up();
+                    break;
+                }
+                load(&vmap, vt + sv * C::kTileBytes, &c.vfull[sv], j);
+                sent_v = true;
+            }
+            if (warp_aborted()) {
+                // no load may still be in flight when the CTA ends
+                for (int j = max(0, sent - C::kStagesK); j < sent; ++j)
+                    warp_wait(&c.kfull[j % C::kStagesK], (uint32_t)((j / C::kStagesK) & 1));
+                const int nv = sent_v ? sent : sent - 1;
+                for (int j = max(0, nv - C::kStagesV); j < nv; ++j)
+                    warp_wait(&c.vfull[j % C::kStagesV], (uint32_t)((j / C::kStagesV) & 1));
+            }
+        } else if (warp == 1) {
+            if (lane == 0) {
+                // ---------------------------------------------- MMA issuer
+                const uint32_t id_qk = idesc_f16_f32_major(kRows, kKeys, kBf16 ? 1 : 0, 0, 0);
+                const uint32_t id_pv = idesc_f16_f32_major(kRows, (a.dv + 15) & ~15, kBf16 ? 1 : 0, 0, 1);
+                const int nk = (a.dk + 15) / 16;
+                const uint32_t qb = smem_u32(smem), kb = smem_u32(kt), vb = smem_u32(vt);
+                auto qk = [&](int i, int j) {
+                    const uint32_t qa = qb + i * (kRows * D * 2), ka = kb + (j % C::kStagesK) * C::kTileBytes;
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        if (ks >= nk) break;
+                        const uint32_t o = (ks >> 2) * kColBlock + (ks & 3) * 32;
+                        mma_f16_ss(tmem + i * kKeys, desc_sw128_kmajor(qa + o, 1024), desc_sw128_kmajor(ka + o, 1024), id_qk,
+                                   ks > 0 ? 1u : 0u);
+                    }
+                    mma_commit(&c.sfull[i]);
+                };
+                bool ok = mbar_wait(&c.kfull[0], 0);
+                if (ok) {
+                    tc_fence_after();
+                    for (int i = 0; i < kTiles; ++i) qk(i, 0);
+                    mma_commit(&c.kempty[0]);
+                }
+                for (int j = 0; ok && j < n && !aborted(); ++j) {
+                    const int sv = j % C::kStagesV;
+                    for (int i = 0; ok && i < kTiles; ++i) {
+                        ok = mbar_wait(&c.pready[i], (uint32_t)(j & 1)) &&
+                             (i > 0 || mbar_wait(&c.vok[sv], (uint32_t)((j / C::kStagesV) & 1)));
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t va = vb + sv * C::kTileBytes;
+#pragma unroll
+                        for (int ks = 0; ks < kKeys / 16; ++ks)
+                            mma_f16_ts(tmem + C::kOCol + i * D, tmem + i * kKeys + ks * 8,
+                                       desc_sw128_mnmajor(va + ks * 2048, kColBlock, 1024), id_pv,
+                                       (j > 0 || ks > 0) ? 1u : 0u);
+                        if (j + 1 < n) {
+                            // S of the next tile over P of this one: the products run in order
+                            const int sk = (j + 1) % C::kStagesK;
+                            ok = i > 0 || mbar_wait(&c.kfull[sk], (uint32_t)(((j + 1) / C::kStagesK) & 1));
+                            if (!ok) break;
+                            qk(i, j + 1);
+                        } else {
+                            mma_commit(&c.odone[i]);
+                        }
+                    }
+                    if (ok) {
+                        mma_commit(&c.vempty[sv]);
+                        if (j + 1 < n) mma_commit(&c.kempty[(j + 1) % C::kStagesK]);
+                    }
+                }
+                if (!ok) give_up();
+                mma_commit(&c.done);
+                mbar_wait(&c.done, 0);
+            }
+            __syncwarp();
+        } else if (warp < kOtherWarps) {
+            // -------------------------------------------------- V checkers: tiles that some row sees in part
+            const int w = warp - 2;
+            for (int j = 0; j < n; ++j) {
+                const int sv = j % C::kStagesV;
+                if (warp_aborted() || !warp_wait(&c.vfull[sv], (uint32_t)((j / C::kStagesV) & 1))) {
+                    give_up();
+                    break;
+                }
+                const int key0 = (t0 + j) * kKeys;
+                if (key0 < max(full0, k0) || key0 + kKeys > min(full1, k1)) {
+                    uint8_t* v = vt + sv * C::kTileBytes;
+                    bool found = false;
+                    // four lanes per V row and column block (rows of 128 bytes)
+                    for (int e = w * 32 + lane; e < kKeys * 4 * (D / 64); e += 64) {
+                        const int row = (e >> 2) & (kKeys - 1), cb = e / (kKeys * 4);
+                        uint4* x = reinterpret_cast<uint4*>(v + cb * kColBlock + row * 128 + (e & 3) * 32);
+                        if (key0 + row < k0 || key0 + row >= k1) {
+                            x[0] = x[1] = make_uint4(0u, 0u, 0u, 0u);
+                        } else if (key0 + row < full0 || key0 + row >= full1) {
+                            const uint4 y[2] = {x[0], x[1]};
+                            const uint32_t* z = reinterpret_cast<const uint32_t*>(y);
+                            constexpr uint32_t kExp = kBf16 ? 0x7F80u : 0x7C00u;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                found |= (z[i] & kExp) == kExp || (z[i] & (kExp << 16)) == (kExp << 16);
+                        }
+                    }
+                    if (__any_sync(0xffffffffu, found) && lane == 0) *(volatile int*)&c.dirty = 1;
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c.vok[sv]);
+            }
+        }
+    }
+    // -------------------------------------------------------------- softmax and output (thread = row)
+    if (warp >= kOtherWarps) {
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lane_off + rt * kKeys;
+        const uint32_t to = tmem + lane_off + C::kOCol + rt * D;
+        Score sc;
+        sc.c = a.scale * kLog2e;
+        sc.inv_cap = a.mods.softcap > 0.f ? a.scale / a.mods.softcap : 0.f;
+        sc.cap = a.mods.softcap * kLog2e;
+        sc.slope = a.mods.slopes && m < m_end ? a.mods.slopes[h] * kLog2e : 0.f;
+        sc.biased = a.mods.slopes != nullptr;
+        float m_used = -INFINITY, l_run = 0.f;
+        bool ok = n > 0 && !bad;
+        for (int j = 0; ok && j < n; ++j) {
+            if (__any_sync(0xffffffffu, *(volatile int*)&c.abort != 0) || !warp_wait(&c.sfull[rt], (uint32_t)(j & 1))) {
+                *(volatile int*)&c.abort = 1;
+                flag(g.status, IDX_ERR_TIMEOUT);
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const int key0 = (t0 + j) * kKeys;
+            const bool masked = key0 < wlo || key0 < s0 || key0 + kKeys > whi || key0 + kKeys > s1;
+            // visible columns [a0, a1) of this row
+            const int a0 = max(max(iv.lo, k0) - key0, 0), a1 = min(min(iv.hi, k1) - key0, kKeys);
+            float s[32];
+            auto load = [&](int cb) {
+                tmem_ld_32x32b_x32(ts + cb * 32, s);
+                tmem_ld_wait();
+                if (kMods) modify(s, sc, (float)(iv.pos - key0 - cb * 32));
+                if (masked) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (cb * 32 + i < a0 || cb * 32 + i >= a1) s[i] = -INFINITY;
+                }
+            };
+            // the row's maximum
+            float mt = -INFINITY;
+#pragma unroll
+            for (int cb = 0; cb < kKeys / 32; ++cb) {
+                load(cb);
+                float x0 = s[0], x1 = s[1], x2 = s[2], x3 = s[3];
+#pragma unroll
+                for (int i = 4; i < 32; i += 4) {
+                    x0 = fmaxf(x0, s[i]);
+                    x1 = fmaxf(x1, s[i + 1]);
+                    x2 = fmaxf(x2, s[i + 2]);
+                    x3 = fmaxf(x3, s[i + 3]);
+                }
+                mt = fmaxf(mt, fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)));
+            }
+            if (!kMods) mt *= sc.c;     // c > 0 here: the largest product gives the largest score
+            const bool rise = mt > m_used + kTop || (m_used == -INFINITY && mt > -INFINITY);
+            if (__any_sync(0xffffffffu, rise)) {
+                float al = 1.f;
+                if (rise) {
+                    const float to_m = mt - kShift;
+                    al = m_used == -INFINITY ? 1.f : ex2_approx(m_used - to_m);
+                    m_used = to_m;
+                    l_run *= al;
+                }
+                if (j > 0) {
+#pragma unroll 1
+                    for (int cb = 0; cb < D / 32; ++cb) {
+                        float o[32];
+                        tmem_ld_32x32b_x32(to + cb * 32, o);
+                        tmem_ld_wait();
+                        uint32_t w[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(o[i] * al);
+                        tmem_st_32x32b_x32(to + cb * 32, w);
+                    }
+                }
+            }
+            const float nm = m_used == -INFINITY ? 0.f : -m_used;
+            float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+            for (int cb = 0; cb < kKeys / 32; ++cb) {
+                load(cb);
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float p0 = ex2_approx(kMods ? s[2 * i] + nm : fmaf(s[2 * i], sc.c, nm));
+                    const float p1 = ex2_approx(kMods ? s[2 * i + 1] + nm : fmaf(s[2 * i + 1], sc.c, nm));
+                    l0 += p0;
+                    l1 += p1;
+                    w[i] = pack2<T>(p0, p1);
+                }
+                tmem_st_32x32b_x16(ts + cb * 16, w);
+            }
+            l_run += l0 + l1;
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c.pready[rt]);
+        }
+        if (ok) ok = warp_wait(&c.odone[rt], 0);
+        tc_fence_after();
+        const bool some = iv.lo < iv.hi;
+        const int64_t rh = qrow * a.Hq + h;
+        // the V checkers have seen every tile by now: each PV product waited for them
+        const bool by_key = bad || (n > 0 && *(volatile int*)&c.dirty != 0);
+        float acc[D];
+        if (by_key) {
+            float mm = -INFINITY, ll = 0.f;
+            if (m < m_end && some) scalar_row<T>(p, g, b, gkv, qrow, h, iv, s0, s1, acc, &mm, &ll);
+            m_used = mm;
+            l_run = ll;
+        }
+        const float l = some && n > 0 ? l_run : 0.f;
+        const float inv = l == 0.f ? 0.f : a.splits > 1 ? 1.f : 1.f / l;
+        if (m < m_end) {
+            if (a.splits > 1) {
+                a.part_ml[(rh * a.splits + split) * 2] = m_used * kLn2;
+                a.part_ml[(rh * a.splits + split) * 2 + 1] = l;
+            } else if (a.lse) {
+                a.lse[rh] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * kLn2;
+            }
+        }
+#pragma unroll
+        for (int cb = 0; cb < D / 32; ++cb) {
+            float o[32];
+            if (by_key) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = cb * 32 + i < a.dv ? acc[cb * 32 + i] : 0.f;
+            } else if (ok) {
+                tmem_ld_32x32b_x32(to + cb * 32, o);
+                tmem_ld_wait();
+            }
+            if (l == 0.f || (!ok && !by_key)) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = 0.f;
+            }
+            const int cols = min(32, a.dv - cb * 32);
+            if (m < m_end && cols > 0) store_cols<T>(a, rh, split, cb * 32, cols, o, inv);
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(tmem, C::kTmemCols);
+}
+
+int box_rows(int page_size) {
+    if (!page_size) return kKeys;
+    int b = page_size & -page_size;
+    return b < kKeys ? b : kKeys;
+}
+
+// row tiles per CTA: two when the packed rows do not fit one
+int row_tiles(int64_t packed) { return packed > kRows ? 2 : 1; }
+
+template <typename T, int D, int kTiles, bool kMods>
+cudaError_t go(const TcArgs& p, const Geom& g, const CUtensorMap& km, const CUtensorMap& vm, int64_t grid,
+               cudaStream_t st) {
+    using C = Cfg<D, kTiles>;
+    constexpr size_t sm = 1024 + (size_t)C::kCtlOff + sizeof(Ctl);
+    static_assert(sm <= 232448, "shared memory");
+    auto kern = dense_tc_kernel<T, D, kTiles, kMods>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3((unsigned)grid), dim3(C::kThreads), sm, st, p, g, km, vm);
+}
+
+template <typename T>
+cudaError_t run(const DenseArgs& a, const Geom& g, cudaStream_t st) {
+    const int64_t packed = (int64_t)g.T * (a.Hq / a.Hkv);
+    const int tiles = row_tiles(packed);
+    TcArgs p = {a, (int)((packed + tiles * kRows - 1) / (tiles * kRows)), box_rows(g.page_size)};
+    const int64_t grid = (int64_t)g.B * a.Hkv * p.tiles * a.splits;
+    if (grid > INT32_MAX) return cudaErrorNotSupported;
+    CUtensorMap km, vm;
+    constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
+    if (!make_head_tmap(&km, a.k, bf16, a.dk, a.Hkv, a.k_stride, a.kv_rows, p.box) ||
+        !make_head_tmap(&vm, a.v, bf16, a.dv, a.Hkv, a.v_stride, a.kv_rows, p.box))
+        return cudaErrorNotSupported;
+    const bool small = a.dk <= 64 && a.dv <= 64;
+    const bool mods = a.mods.softcap > 0.f || a.mods.slopes || a.scale <= 0.f;
+    if (small) {
+        if (tiles == 1)
+            return mods ? go<T, 64, 1, true>(p, g, km, vm, grid, st) : go<T, 64, 1, false>(p, g, km, vm, grid, st);
+        return mods ? go<T, 64, 2, true>(p, g, km, vm, grid, st) : go<T, 64, 2, false>(p, g, km, vm, grid, st);
+    }
+    if (tiles == 1)
+        return mods ? go<T, 128, 1, true>(p, g, km, vm, grid, st) : go<T, 128, 1, false>(p, g, km, vm, grid, st);
+    return mods ? go<T, 128, 2, true>(p, g, km, vm, grid, st) : go<T, 128, 2, false>(p, g, km, vm, grid, st);
+}
+
+}  // namespace
+
+bool dense_tc_supported(const DenseArgs& a, int dtype, const Geom& g) {
+    if (dtype == IDX_F32 || !a.v || a.dk > 128 || a.dv > 128 || a.dk % 8 || a.dv % 8) return false;
+    if (a.kv_rows < 1 || a.kv_rows > INT32_MAX - kKeys || a.k_stride % 8 || a.v_stride % 8) return false;
+    // pages are loaded in boxes of whole 8-row swizzle groups
+    if (g.page_table && box_rows(g.page_size) < 8) return false;
+    const uint64_t all = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) |
+                         reinterpret_cast<uintptr_t>(a.v) | reinterpret_cast<uintptr_t>(a.out);
+    return all % 16 == 0;
+}
+
+// one CTA per SM: split the keys until the CTAs cover the SMs twice, at least 512 keys each
+int dense_tc_splits(int64_t n_seq, int64_t n_q, int64_t max_n_kv, int Hq, int Hkv) {
+    const int64_t packed = n_q * (Hq / Hkv);
+    const int64_t rows = row_tiles(packed) * kRows;
+    const int64_t units = n_seq * Hkv * ((packed + rows - 1) / rows);
+    int sms = sm_count();
+    if (sms < 2) sms = 152;
+    if (units < 1) return 1;
+    int64_t s = 2 * (int64_t)sms / units;
+    const int64_t by_keys = (max_n_kv + 511) / 512;
+    if (s > by_keys) s = by_keys;
+    if (s > 128) s = 128;
+    return s < 1 ? 1 : (int)s;
+}
+
+cudaError_t launch_dense_tc(const DenseArgs& a, int dtype, const Geom& g, cudaStream_t st) {
+    return dtype == IDX_BF16 ? run<__nv_bfloat16>(a, g, st) : run<__half>(a, g, st);
+}
+
+}  // namespace lidx

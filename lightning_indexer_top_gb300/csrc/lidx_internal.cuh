@@ -239,6 +239,8 @@ cudaError_t launch_decode_fused(const void* qi, int qi_dtype, const float* w, co
 // TMA tensor maps over 16-bit caches (128-byte swizzle); false if encoding fails
 bool make_key_tmap(CUtensorMap* m, const void* k, bool bf16, int64_t k_row_stride, int64_t k_rows, int box_rows);
 bool make_q3d_tmap(CUtensorMap* m, const void* q, bool bf16, int64_t rows);
+bool make_head_tmap(CUtensorMap* m, const void* x, bool bf16, int d, int heads, int64_t row_stride, int64_t rows,
+                    int box_rows);
 bool make_w_tmap(CUtensorMap* m, const float* w, int64_t rows);
 // [rows, payload] int8 keys (128 codes, or 144 bytes with the scale inline): boxes of
 // payload bytes x box_rows rows, unswizzled or (128-byte rows) in the 128-byte swizzle

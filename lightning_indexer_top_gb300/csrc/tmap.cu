@@ -71,6 +71,21 @@ bool make_key_tmap(CUtensorMap* m, const void* k, bool bf16, int64_t k_row_strid
     return encode_2d(m, k, bf16, 128, (uint64_t)k_rows, (uint64_t)k_row_stride * 2, 64, (uint32_t)box_rows);
 }
 
+// K or V rows of a cache, [rows, heads, d] 16-bit with the heads of a row contiguous: boxes of 64 columns of
+// one head x box_rows rows, 128-byte swizzle; columns past d and rows outside the cache read as zero
+bool make_head_tmap(CUtensorMap* m, const void* x, bool bf16, int d, int heads, int64_t row_stride, int64_t rows,
+                    int box_rows) {
+    EncodeFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
+    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)row_stride * 2};
+    cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(x),
+              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool make_key8_tmap(CUtensorMap* m, const int8_t* k, int64_t row_bytes, int64_t k_rows, int box_rows,
                     int payload, bool swizzle128) {
     EncodeFn fn = encode_fn();
