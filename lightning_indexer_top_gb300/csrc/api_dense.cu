@@ -73,6 +73,8 @@ size_t dense_attn_workspace_size(idx_dtype dtype, int32_t n_seq, int32_t n_q_per
     if (n_seq < 1 || n_q_per_seq < 1 || max_n_kv < 1 || n_kv_heads < 1 || n_q_heads < 1 || n_q_heads % n_kv_heads ||
         dk < 1 || dk > 576 || dv < 1 || dv > 512)
         return 0;
+    if (dtype == IDX_BF16 && n_q_heads == 128 && n_kv_heads == 1 && dk == 576 && dv == 512)
+        return dense_mla_workspace_bytes((int64_t)n_seq * n_q_per_seq, max_n_kv);
     // (a call whose pages or addresses the tensor-core kernel does not take splits as far as this reaches)
     const bool tc = dtype != IDX_F32 && dk <= 128 && dv <= 128 && dk % 8 == 0 && dv % 8 == 0;
     const int splits = want_splits(dtype, n_seq, n_q_per_seq, max_n_kv, n_q_heads, n_kv_heads, dk, dv, tc);
@@ -128,6 +130,10 @@ idx_status dense_attn(const void* q, idx_dtype dtype, int32_t n_q_heads, int32_t
     a.lse = lse;
     const Geom g = geom_of(batch);
     const cudaStream_t st = (cudaStream_t)stream;
+    if (dense_mla_supported(a, dtype, g)) {
+        const cudaError_t e = launch_dense_mla(a, g, workspace, workspace ? workspace_bytes : 0, st);
+        if (e != cudaErrorNotSupported) return cuda_status(e, what);
+    }
     const size_t per_split = split_bytes(n_rows, n_q_heads, dv);
     const int64_t fit = workspace ? (int64_t)(workspace_bytes / per_split) : 0;
     const bool tc = dense_tc_supported(a, dtype, g);

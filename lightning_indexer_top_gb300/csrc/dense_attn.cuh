@@ -3,6 +3,7 @@
 #pragma once
 
 #include "lidx_internal.cuh"
+#include "sm100_ptx.cuh"
 
 namespace lidx {
 
@@ -50,6 +51,80 @@ __device__ __forceinline__ Interval row_interval(const Geom& g, const idx_attn_m
     return v;
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// the options as the softmax applies them, in log2 units
+struct Score {
+    float c;            // scale * log2(e)
+    float inv_cap;      // scale / softcap (0: no cap)
+    float cap;          // softcap * log2(e)
+    float slope;        // the row's slope * log2(e)
+    bool biased;        // slopes are given
+};
+
+// tanh on [-1/2, 1/2] by its Taylor series up to x^13 (the next term is below 2^-23 of x there)
+__device__ __forceinline__ float tanh_small(float x) {
+    const float y = x * x;
+    float p = 21844.f / 6081075.f;
+    p = fmaf(p, y, -1382.f / 155925.f);
+    p = fmaf(p, y, 62.f / 2835.f);
+    p = fmaf(p, y, -17.f / 315.f);
+    p = fmaf(p, y, 2.f / 15.f);
+    p = fmaf(p, y, -1.f / 3.f);
+    return fmaf(p * y, x, x);
+}
+
+// 1 - 2 / (1 + e^(2x)): for |x| > 1/2, where it does not cancel
+__device__ __forceinline__ float tanh_large(float x) {
+    return fmaf(-2.f, rcp_approx(1.f + sm100::ex2_approx(x * (2.f * kLog2e))), 1.f);
+}
+
+// 32 raw products -> scores in log2 units; d0 = the row's position minus the first key's
+__device__ __forceinline__ void modify(float (&s)[32], const Score& sc, float d0) {
+    if (sc.inv_cap != 0.f) {
+        float big = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            s[i] *= sc.inv_cap;
+            big = fmaxf(big, fabsf(s[i]));
+        }
+        if (__any_sync(0xffffffffu, big > 0.5f)) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const float t = fabsf(s[i]) > 0.5f ? tanh_large(s[i]) : tanh_small(s[i]);
+                s[i] = sc.cap * t;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[i] = sc.cap * tanh_small(s[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s[i] *= sc.c;
+    }
+    if (sc.biased) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s[i] = fmaf(-sc.slope, fabsf(d0 - (float)i), s[i]);
+    }
+}
+
+__device__ __forceinline__ Score make_score(const DenseArgs& a, float slope) {
+    Score s;
+    s.c = a.scale * kLog2e;
+    s.inv_cap = a.mods.softcap > 0.f ? a.scale / a.mods.softcap : 0.f;
+    s.cap = a.mods.softcap * kLog2e;
+    s.slope = slope * kLog2e;
+    s.biased = a.mods.slopes != nullptr;
+    return s;
+}
+
 // CUDA cores: every type, width and alignment
 cudaError_t launch_dense_generic(const DenseArgs& a, int dtype, const Geom& g, cudaStream_t st);
 int dense_generic_splits(int64_t n_seq, int64_t n_q, int64_t max_n_kv, int Hq, int Hkv, int dk, int dv);
@@ -59,6 +134,12 @@ bool dense_tc_supported(const DenseArgs& a, int dtype, const Geom& g);
 cudaError_t launch_dense_tc(const DenseArgs& a, int dtype, const Geom& g, cudaStream_t st);
 int dense_tc_splits(int64_t n_seq, int64_t n_q, int64_t max_n_kv, int Hq, int Hkv);
 constexpr int kDenseTcKeys = 128;   // its splits are whole tiles of this many keys
+
+// tensor cores: the bf16 MLA latent of 128 heads (576 / 512 columns), 2-CTA clusters; its own key splits and partials
+bool dense_mla_supported(const DenseArgs& a, int dtype, const Geom& g);
+int dense_mla_splits(int64_t n_rows, int64_t max_n_kv);
+size_t dense_mla_workspace_bytes(int64_t n_rows, int64_t max_n_kv);
+cudaError_t launch_dense_mla(const DenseArgs& a, const Geom& g, void* ws, size_t ws_bytes, cudaStream_t st);
 
 // merges part_o / part_ml into out and lse
 cudaError_t launch_dense_combine(const DenseArgs& a, int dtype, int64_t n_rows, cudaStream_t st);

@@ -40,8 +40,6 @@ constexpr int kKeys = 128;             // keys per tile
 constexpr int kRows = 128;             // packed query rows per row tile
 constexpr int kColBlock = 128 * 128;   // 64 columns x 128 rows of a tile, in the 128-byte swizzle
 constexpr int kOtherWarps = 4;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 template <int D, int kTiles>
 struct Cfg {
@@ -78,67 +76,6 @@ template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, f
 template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
     const __half2 x = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&x);
-}
-
-__device__ __forceinline__ float rcp_approx(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// the options as the softmax applies them, in log2 units
-struct Score {
-    float c;            // scale * log2(e)
-    float inv_cap;      // scale / softcap (0: no cap)
-    float cap;          // softcap * log2(e)
-    float slope;        // the row's slope * log2(e)
-    bool biased;        // slopes are given
-};
-
-// tanh on [-1/2, 1/2] by its Taylor series up to x^13 (the next term is below 2^-23 of x there)
-__device__ __forceinline__ float tanh_small(float x) {
-    const float y = x * x;
-    float p = 21844.f / 6081075.f;
-    p = fmaf(p, y, -1382.f / 155925.f);
-    p = fmaf(p, y, 62.f / 2835.f);
-    p = fmaf(p, y, -17.f / 315.f);
-    p = fmaf(p, y, 2.f / 15.f);
-    p = fmaf(p, y, -1.f / 3.f);
-    return fmaf(p * y, x, x);
-}
-
-// 1 - 2 / (1 + e^(2x)): for |x| > 1/2, where it does not cancel
-__device__ __forceinline__ float tanh_large(float x) {
-    return fmaf(-2.f, rcp_approx(1.f + ex2_approx(x * (2.f * kLog2e))), 1.f);
-}
-
-// 32 raw products -> scores in log2 units; d0 = the row's position minus the first key's
-__device__ __forceinline__ void modify(float (&s)[32], const Score& sc, float d0) {
-    if (sc.inv_cap != 0.f) {
-        float big = 0.f;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            s[i] *= sc.inv_cap;
-            big = fmaxf(big, fabsf(s[i]));
-        }
-        if (__any_sync(0xffffffffu, big > 0.5f)) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const float t = fabsf(s[i]) > 0.5f ? tanh_large(s[i]) : tanh_small(s[i]);
-                s[i] = sc.cap * t;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) s[i] = sc.cap * tanh_small(s[i]);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) s[i] *= sc.c;
-    }
-    if (sc.biased) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) s[i] = fmaf(-sc.slope, fabsf(d0 - (float)i), s[i]);
-    }
 }
 
 struct TcArgs {
@@ -479,12 +416,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1)
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lane_off + rt * kKeys;
         const uint32_t to = tmem + lane_off + C::kOCol + rt * D;
-        Score sc;
-        sc.c = a.scale * kLog2e;
-        sc.inv_cap = a.mods.softcap > 0.f ? a.scale / a.mods.softcap : 0.f;
-        sc.cap = a.mods.softcap * kLog2e;
-        sc.slope = a.mods.slopes && m < m_end ? a.mods.slopes[h] * kLog2e : 0.f;
-        sc.biased = a.mods.slopes != nullptr;
+        const Score sc = make_score(a, a.mods.slopes && m < m_end ? a.mods.slopes[h] : 0.f);
         float m_used = -INFINITY, l_run = 0.f;
         bool ok = n > 0 && !bad;
         for (int j = 0; ok && j < n; ++j) {
