@@ -69,16 +69,42 @@ struct Score {
     bool biased;        // slopes are given
 };
 
-// tanh on [-1/2, 1/2] by its Taylor series up to x^13 (the next term is below 2^-23 of x there)
-__device__ __forceinline__ float tanh_small(float x) {
-    const float y = x * x;
-    float p = 21844.f / 6081075.f;
-    p = fmaf(p, y, -1382.f / 155925.f);
-    p = fmaf(p, y, 62.f / 2835.f);
-    p = fmaf(p, y, -17.f / 315.f);
-    p = fmaf(p, y, 2.f / 15.f);
-    p = fmaf(p, y, -1.f / 3.f);
-    return fmaf(p * y, x, x);
+// two f32 in one 64-bit register, for the packed FMA and add
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// k * tanh of two numbers in [-1/2, 1/2] by its Taylor series up to x^13 (the next term is below 2^-23 of x there)
+__device__ __forceinline__ uint64_t tanh_small2(uint64_t x, uint64_t k) {
+    auto both = [](float c) { return pair(c, c); };
+    const uint64_t y = mul2(x, x);
+    uint64_t p = both(21844.f / 6081075.f);
+    p = fma2(p, y, both(-1382.f / 155925.f));
+    p = fma2(p, y, both(62.f / 2835.f));
+    p = fma2(p, y, both(-17.f / 315.f));
+    p = fma2(p, y, both(2.f / 15.f));
+    p = fma2(p, y, both(-1.f / 3.f));
+    return mul2(fma2(mul2(p, y), x, x), k);
 }
 
 // 1 - 2 / (1 + e^(2x)): for |x| > 1/2, where it does not cancel
@@ -86,32 +112,43 @@ __device__ __forceinline__ float tanh_large(float x) {
     return fmaf(-2.f, rcp_approx(1.f + sm100::ex2_approx(x * (2.f * kLog2e))), 1.f);
 }
 
-// 32 raw products -> scores in log2 units; d0 = the row's position minus the first key's
-__device__ __forceinline__ void modify(float (&s)[32], const Score& sc, float d0) {
+// N raw products of consecutive keys -> scores in log2 units; d0 = the row's position minus the first key's.
+// Every lane of a warp comes here together.
+template <int N>
+__device__ __forceinline__ void modify(float (&s)[N], const Score& sc, float d0) {
     if (sc.inv_cap != 0.f) {
         float big = 0.f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            s[i] *= sc.inv_cap;
-            big = fmaxf(big, fabsf(s[i]));
-        }
-        if (__any_sync(0xffffffffu, big > 0.5f)) {
+        for (int i = 0; i < N; ++i) big = fmaxf(big, fabsf(s[i]));
+        const uint64_t k = pair(sc.cap, sc.cap), ic = pair(sc.inv_cap, sc.inv_cap);
+        // (a NaN is no larger than anything and goes through the series)
+        if (__any_sync(0xffffffffu, big * fabsf(sc.inv_cap) > 0.5f)) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const float t = fabsf(s[i]) > 0.5f ? tanh_large(s[i]) : tanh_small(s[i]);
-                s[i] = sc.cap * t;
+            for (int i = 0; i < N; i += 2) {
+                const float x0 = s[i] * sc.inv_cap, x1 = s[i + 1] * sc.inv_cap;
+                float y0, y1;
+                unpair(tanh_small2(pair(x0, x1), k), y0, y1);
+                s[i] = fabsf(x0) > 0.5f ? sc.cap * tanh_large(x0) : y0;
+                s[i + 1] = fabsf(x1) > 0.5f ? sc.cap * tanh_large(x1) : y1;
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) s[i] = sc.cap * tanh_small(s[i]);
+            for (int i = 0; i < N; i += 2)
+                unpair(tanh_small2(mul2(pair(s[i], s[i + 1]), ic), k), s[i], s[i + 1]);
         }
     } else {
+        const uint64_t c = pair(sc.c, sc.c);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) s[i] *= sc.c;
+        for (int i = 0; i < N; i += 2) unpair(mul2(pair(s[i], s[i + 1]), c), s[i], s[i + 1]);
     }
     if (sc.biased) {
+        const uint64_t sl = pair(-sc.slope, -sc.slope), d = pair(d0, d0);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) s[i] = fmaf(-sc.slope, fabsf(d0 - (float)i), s[i]);
+        for (int i = 0; i < N; i += 2) {
+            float x0, x1;
+            unpair(add2(d, pair(-(float)i, -(float)(i + 1))), x0, x1);
+            unpair(fma2(sl, pair(fabsf(x0), fabsf(x1)), pair(s[i], s[i + 1])), s[i], s[i + 1]);
+        }
     }
 }
 

@@ -5,15 +5,18 @@
 // into rows m = t*G + h, 128 to a tile (the M side of the MMAs), so a K or V
 // tile that is read once serves every head of the group.  A CTA owns kTiles
 // such tiles of one (sequence, kv head) and one split of the key line, and
-// walks it in tiles of 128 keys:
-//     S = Q K^T       [128 x 128] f32 in TMEM     (Q, K from shared memory)
+// walks it in steps of 64 keys (K and V come in tiles of 128):
+//     S = Q K^T       [128 x 64] f32 in TMEM      (Q, K from shared memory)
 //     P = 2^(S*c - m) bf16/f16, written over S in TMEM
 //     O = O + P V     [128 x dv] f32 in TMEM      (P from TMEM, V from shared memory)
+// S has two buffers per row tile, so that the scores of the next step are there
+// when the softmax of one ends: the softmax warps never wait for the tensor core
+// (one 128-key buffer, no lookahead: 1.03 ms on 4096 rows x 16384 keys, the
+// tensor pipe 42 % busy and nothing else above 33 %).
 // Warps 0-3: TMA producer, MMA issuer, two V checkers; then four softmax warps
 // per row tile (thread = row = TMEM lane), which also write the output.  With
-// two row tiles the tensor core works on one while the other's softmax runs,
-// and a K/V tile is read for 256 rows; with one (few rows: a decode step) the
-// walk is bound by the stream of K and V.
+// two row tiles per CTA a K/V tile is read for 256 rows; with one (few rows: a
+// decode step) two CTAs share an SM and the walk is bound by the stream of K and V.
 //
 // A row's maximum follows its scores lazily: O is rescaled (by the softmax
 // warps, in TMEM) only when a score passes it by 2^8, so P stays <= 2^8.
@@ -36,7 +39,8 @@ namespace lidx {
 namespace {
 using namespace sm100;
 
-constexpr int kKeys = 128;             // keys per tile
+constexpr int kKeys = 128;             // keys per K/V tile
+constexpr int kStep = 64;              // keys per softmax step
 constexpr int kRows = 128;             // packed query rows per row tile
 constexpr int kColBlock = 128 * 128;   // 64 columns x 128 rows of a tile, in the 128-byte swizzle
 constexpr int kOtherWarps = 4;
@@ -45,21 +49,23 @@ template <int D, int kTiles>
 struct Cfg {
     static constexpr int kTileBytes = kKeys * D * 2;
     static constexpr int kQBytes = kTiles * kRows * D * 2;
-    static constexpr int kStagesK = kTiles == 2 ? 2 : 3;
-    static constexpr int kStagesV = 3;
+    // one row tile: two CTAs per SM share its shared memory
+    static constexpr int kStagesK = kTiles == 2 ? 2 : D == 64 ? 2 : 1;
+    static constexpr int kStagesV = kTiles == 2 ? 3 : D == 64 ? 2 : 1;
+    static constexpr int kCtas = kTiles == 2 ? 1 : 2;
     static constexpr int kVOff = kQBytes + kStagesK * kTileBytes;
     static constexpr int kCtlOff = kVOff + kStagesV * kTileBytes;
     static constexpr int kThreads = 32 * kOtherWarps + kRows * kTiles;
     static constexpr int kTmemCols = kTiles == 2 ? 512 : 256;
-    static constexpr int kOCol = kTiles * kKeys;      // O of row tile i at kOCol + i*D
+    static constexpr int kOCol = kTiles * 2 * kStep;  // S buffer b of row tile i at (2*i + b)*kStep; O at kOCol + i*D
 };
 
 struct Ctl {
     uint64_t kfull[3], kempty[3];
     uint64_t vfull[3], vempty[3];
     uint64_t vok[3];              // V looked over (both checker warps)
-    uint64_t sfull[2];            // S of a row tile written (and its earlier PV products complete)
-    uint64_t pready[2];           // P of a row tile written, O rescaled
+    uint64_t sfull[2][2];         // S buffer of a row tile written (and the PV products of two steps before complete)
+    uint64_t pready[2][2];        // P written over it, O rescaled
     uint64_t odone[2];            // every product of a row tile complete
     uint64_t done;
     uint32_t tmem_base;
@@ -142,7 +148,7 @@ __device__ __forceinline__ void store_cols(const DenseArgs& a, int64_t rh, int s
 }
 
 template <typename T, int D, int kTiles, bool kMods>
-__global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCtas)
     dense_tc_kernel(TcArgs p, Geom g, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
     using C = Cfg<D, kTiles>;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -176,8 +182,10 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1)
             mbar_init(&c.vok[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&c.sfull[i], 1);
-            mbar_init(&c.pready[i], 4);
+            for (int x = 0; x < 2; ++x) {
+                mbar_init(&c.sfull[i][x], 1);
+                mbar_init(&c.pready[i][x], 4);
+            }
             mbar_init(&c.odone[i], 1);
         }
         mbar_init(&c.done, 1);
@@ -244,7 +252,8 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1)
     int k0 = c.k0, k1 = c.k1;
     if (k0 < s0) k0 = (int)(s0 < INT32_MAX ? s0 : INT32_MAX);
     if (k1 > s1) k1 = (int)s1;
-    const int t0 = k0 / kKeys;
+    const int t0 = k0 / kKeys, st0 = k0 / kStep;
+    const int ns = k1 > k0 ? (k1 + kStep - 1) / kStep - st0 : 0;
     const int n = k1 > k0 ? (k1 + kKeys - 1) / kKeys - t0 : 0;
     // every cache row of them exists?
     bool bad = false;
@@ -321,54 +330,66 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1)
         } else if (warp == 1) {
             if (lane == 0) {
                 // ---------------------------------------------- MMA issuer
-                const uint32_t id_qk = idesc_f16_f32_major(kRows, kKeys, kBf16 ? 1 : 0, 0, 0);
+                const uint32_t id_qk = idesc_f16_f32_major(kRows, kStep, kBf16 ? 1 : 0, 0, 0);
                 const uint32_t id_pv = idesc_f16_f32_major(kRows, (a.dv + 15) & ~15, kBf16 ? 1 : 0, 0, 1);
-                const int nk = (a.dk + 15) / 16;
                 const uint32_t qb = smem_u32(smem), kb = smem_u32(kt), vb = smem_u32(vt);
-                auto qk = [&](int i, int j) {
-                    const uint32_t qa = qb + i * (kRows * D * 2), ka = kb + (j % C::kStagesK) * C::kTileBytes;
+                // step q is half (st0 + q) & 1 of tile (st0 + q) / 2 - t0
+                auto tile_of = [&](int q) { return ((st0 + q) >> 1) - t0; };
+                auto first_of = [&](int q) { return q == 0 || ((st0 + q) & 1) == 0; };
+                auto last_of = [&](int q) { return q == ns - 1 || ((st0 + q) & 1) == 1; };
+                auto qk = [&](int i, int q) {
+                    // descriptors of the first k-step; a later one adds its offset to the start address (16-byte units).
+                    // All D / 16 steps run (columns past dk are zero): stopped at dk by a run-time bound, the unrolled
+                    // chain's last descriptor came out wrong (nvcc 13.0; the basis-vector test shows it)
+                    const uint64_t qd = desc_sw128_kmajor(qb + i * (kRows * D * 2), 1024);
+                    const uint64_t kd = desc_sw128_kmajor(
+                        kb + (tile_of(q) % C::kStagesK) * C::kTileBytes + ((st0 + q) & 1) * (kStep * 128), 1024);
+                    const uint32_t d = tmem + (2 * i + (q & 1)) * kStep;
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks) {
-                        if (ks >= nk) break;
-                        const uint32_t o = (ks >> 2) * kColBlock + (ks & 3) * 32;
-                        mma_f16_ss(tmem + i * kKeys, desc_sw128_kmajor(qa + o, 1024), desc_sw128_kmajor(ka + o, 1024), id_qk,
-                                   ks > 0 ? 1u : 0u);
+                        const uint64_t o = ((ks >> 2) * kColBlock + (ks & 3) * 32) >> 4;
+                        mma_f16_ss(d, qd + o, kd + o, id_qk, ks > 0 ? 1u : 0u);
                     }
-                    mma_commit(&c.sfull[i]);
                 };
-                bool ok = mbar_wait(&c.kfull[0], 0);
-                if (ok) {
+                auto k_ready = [&](int q) {
+                    const int j = tile_of(q);
+                    return !first_of(q) || mbar_wait(&c.kfull[j % C::kStagesK], (uint32_t)((j / C::kStagesK) & 1));
+                };
+                bool ok = true;
+                for (int q = 0; ok && q < 2; ++q) {
+                    if (q < ns && !(ok = k_ready(q))) break;
                     tc_fence_after();
-                    for (int i = 0; i < kTiles; ++i) qk(i, 0);
-                    mma_commit(&c.kempty[0]);
+                    for (int i = 0; i < kTiles; ++i) {
+                        if (q < ns) qk(i, q);
+                        mma_commit(&c.sfull[i][q]);
+                    }
+                    if (q < ns && last_of(q)) mma_commit(&c.kempty[tile_of(q) % C::kStagesK]);
                 }
-                for (int j = 0; ok && j < n && !aborted(); ++j) {
-                    const int sv = j % C::kStagesV;
+                for (int q = 0; ok && q < ns && !aborted(); ++q) {
+                    const int j = tile_of(q), sv = j % C::kStagesV, b2 = q & 1;
                     for (int i = 0; ok && i < kTiles; ++i) {
-                        ok = mbar_wait(&c.pready[i], (uint32_t)(j & 1)) &&
-                             (i > 0 || mbar_wait(&c.vok[sv], (uint32_t)((j / C::kStagesV) & 1)));
+                        ok = mbar_wait(&c.pready[i][b2], (uint32_t)((q >> 1) & 1)) &&
+                             (i > 0 || !first_of(q) || mbar_wait(&c.vok[sv], (uint32_t)((j / C::kStagesV) & 1)));
                         if (!ok) break;
                         tc_fence_after();
-                        const uint32_t va = vb + sv * C::kTileBytes;
+                        const uint64_t vd = desc_sw128_mnmajor(
+                            vb + sv * C::kTileBytes + ((st0 + q) & 1) * (kStep * 128), kColBlock, 1024);
 #pragma unroll
-                        for (int ks = 0; ks < kKeys / 16; ++ks)
-                            mma_f16_ts(tmem + C::kOCol + i * D, tmem + i * kKeys + ks * 8,
-                                       desc_sw128_mnmajor(va + ks * 2048, kColBlock, 1024), id_pv,
-                                       (j > 0 || ks > 0) ? 1u : 0u);
-                        if (j + 1 < n) {
-                            // S of the next tile over P of this one: the products run in order
-                            const int sk = (j + 1) % C::kStagesK;
-                            ok = i > 0 || mbar_wait(&c.kfull[sk], (uint32_t)(((j + 1) / C::kStagesK) & 1));
+                        for (int ks = 0; ks < kStep / 16; ++ks)
+                            mma_f16_ts(tmem + C::kOCol + i * D, tmem + (2 * i + b2) * kStep + ks * 8,
+                                       vd + (uint64_t)(ks * 2048 >> 4), id_pv, (q > 0 || ks > 0) ? 1u : 0u);
+                        // S of the step after the next one over P of this one: the products run in order.  (The
+                        // commit for step ns has no scores: it tells that the PV product of step ns - 2 is complete.)
+                        if (q + 2 < ns) {
+                            ok = i > 0 || k_ready(q + 2);
                             if (!ok) break;
-                            qk(i, j + 1);
-                        } else {
-                            mma_commit(&c.odone[i]);
+                            qk(i, q + 2);
                         }
+                        if (q + 2 <= ns) mma_commit(&c.sfull[i][b2]);
+                        if (q + 1 == ns) mma_commit(&c.odone[i]);
                     }
-                    if (ok) {
-                        mma_commit(&c.vempty[sv]);
-                        if (j + 1 < n) mma_commit(&c.kempty[(j + 1) % C::kStagesK]);
-                    }
+                    if (ok && last_of(q)) mma_commit(&c.vempty[sv]);
+                    if (ok && q + 2 < ns && last_of(q + 2)) mma_commit(&c.kempty[tile_of(q + 2) % C::kStagesK]);
                 }
                 if (!ok) give_up();
                 mma_commit(&c.done);
@@ -414,49 +435,58 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1)
     // -------------------------------------------------------------- softmax and output (thread = row)
     if (warp >= kOtherWarps) {
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + lane_off + rt * kKeys;
+        const uint32_t ts = tmem + lane_off + rt * 2 * kStep;
         const uint32_t to = tmem + lane_off + C::kOCol + rt * D;
         const Score sc = make_score(a, a.mods.slopes && m < m_end ? a.mods.slopes[h] : 0.f);
         float m_used = -INFINITY, l_run = 0.f;
         bool ok = n > 0 && !bad;
-        for (int j = 0; ok && j < n; ++j) {
-            if (__any_sync(0xffffffffu, *(volatile int*)&c.abort != 0) || !warp_wait(&c.sfull[rt], (uint32_t)(j & 1))) {
-                *(volatile int*)&c.abort = 1;
-                flag(g.status, IDX_ERR_TIMEOUT);
-                ok = false;
+        auto timed_out = [&] {
+            *(volatile int*)&c.abort = 1;
+            flag(g.status, IDX_ERR_TIMEOUT);
+            ok = false;
+        };
+        const uint64_t c2 = pair(sc.c, sc.c);
+        for (int q = 0; ok && q < ns; ++q) {
+            const int b2 = q & 1;
+            if (__any_sync(0xffffffffu, *(volatile int*)&c.abort != 0) ||
+                !warp_wait(&c.sfull[rt][b2], (uint32_t)((q >> 1) & 1))) {
+                timed_out();
                 break;
             }
             tc_fence_after();
-            const int key0 = (t0 + j) * kKeys;
-            const bool masked = key0 < wlo || key0 < s0 || key0 + kKeys > whi || key0 + kKeys > s1;
-            // visible columns [a0, a1) of this row
-            const int a0 = max(max(iv.lo, k0) - key0, 0), a1 = min(min(iv.hi, k1) - key0, kKeys);
-            float s[32];
-            auto load = [&](int cb) {
-                tmem_ld_32x32b_x32(ts + cb * 32, s);
-                tmem_ld_wait();
-                if (kMods) modify(s, sc, (float)(iv.pos - key0 - cb * 32));
-                if (masked) {
+            const int key0 = (st0 + q) * kStep;
+            const uint32_t tq = ts + b2 * kStep;
+            float s[kStep];
+            {
+                uint32_t x[32], y[32];
+                tmem_ld_32x32b_x32_raw(tq, x);
+                tmem_ld_32x32b_x32_raw(tq + 32, y);
+                tmem_ld_wait_for(x);
+                tmem_ld_wait_for(y);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (cb * 32 + i < a0 || cb * 32 + i >= a1) s[i] = -INFINITY;
+                for (int i = 0; i < 32; ++i) {
+                    s[i] = __uint_as_float(x[i]);
+                    s[32 + i] = __uint_as_float(y[i]);
                 }
-            };
-            // the row's maximum
-            float mt = -INFINITY;
-#pragma unroll
-            for (int cb = 0; cb < kKeys / 32; ++cb) {
-                load(cb);
-                float x0 = s[0], x1 = s[1], x2 = s[2], x3 = s[3];
-#pragma unroll
-                for (int i = 4; i < 32; i += 4) {
-                    x0 = fmaxf(x0, s[i]);
-                    x1 = fmaxf(x1, s[i + 1]);
-                    x2 = fmaxf(x2, s[i + 2]);
-                    x3 = fmaxf(x3, s[i + 3]);
-                }
-                mt = fmaxf(mt, fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)));
             }
+            if (kMods) modify(s, sc, (float)(iv.pos - key0));
+            if (key0 < wlo || key0 < k0 || key0 + kStep > whi || key0 + kStep > k1) {
+                // visible columns [a0, a1) of this row
+                const int a0 = max(iv.lo, k0) - key0, a1 = min(iv.hi, k1) - key0;
+#pragma unroll
+                for (int i = 0; i < kStep; ++i)
+                    if (i < a0 || i >= a1) s[i] = -INFINITY;
+            }
+            // the row's maximum
+            float x0 = fmaxf(s[0], s[1]), x1 = fmaxf(s[2], s[3]), x2 = fmaxf(s[4], s[5]), x3 = fmaxf(s[6], s[7]);
+#pragma unroll
+            for (int i = 8; i < kStep; i += 8) {
+                x0 = fmaxf(fmaxf(x0, s[i]), s[i + 1]);
+                x1 = fmaxf(fmaxf(x1, s[i + 2]), s[i + 3]);
+                x2 = fmaxf(fmaxf(x2, s[i + 4]), s[i + 5]);
+                x3 = fmaxf(fmaxf(x3, s[i + 6]), s[i + 7]);
+            }
+            float mt = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
             if (!kMods) mt *= sc.c;     // c > 0 here: the largest product gives the largest score
             const bool rise = mt > m_used + kTop || (m_used == -INFINITY && mt > -INFINITY);
             if (__any_sync(0xffffffffu, rise)) {
@@ -467,40 +497,49 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1)
                     m_used = to_m;
                     l_run *= al;
                 }
-                if (j > 0) {
+                if (q > 0 && __any_sync(0xffffffffu, al != 1.f)) {
+                    // the products up to the last step's: complete once the next step's S is
+                    if (!warp_wait(&c.sfull[rt][b2 ^ 1], (uint32_t)(((q + 1) >> 1) & 1))) {
+                        timed_out();
+                        break;
+                    }
+                    tc_fence_after();
 #pragma unroll 1
                     for (int cb = 0; cb < D / 32; ++cb) {
-                        float o[32];
-                        tmem_ld_32x32b_x32(to + cb * 32, o);
-                        tmem_ld_wait();
-                        uint32_t w[32];
+                        uint32_t o[32];
+                        tmem_ld_32x32b_x32_raw(to + cb * 32, o);
+                        tmem_ld_wait_for(o);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(o[i] * al);
-                        tmem_st_32x32b_x32(to + cb * 32, w);
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+                        tmem_st_32x32b_x32(to + cb * 32, o);
                     }
                 }
             }
             const float nm = m_used == -INFINITY ? 0.f : -m_used;
-            float l0 = 0.f, l1 = 0.f;
+            const uint64_t nm2 = pair(nm, nm);
+            uint64_t la = 0ull, lb = 0ull;
+            uint32_t w[32];
 #pragma unroll
-            for (int cb = 0; cb < kKeys / 32; ++cb) {
-                load(cb);
-                uint32_t w[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float p0 = ex2_approx(kMods ? s[2 * i] + nm : fmaf(s[2 * i], sc.c, nm));
-                    const float p1 = ex2_approx(kMods ? s[2 * i + 1] + nm : fmaf(s[2 * i + 1], sc.c, nm));
-                    l0 += p0;
-                    l1 += p1;
-                    w[i] = pack2<T>(p0, p1);
-                }
-                tmem_st_32x32b_x16(ts + cb * 16, w);
+            for (int i = 0; i < kStep; i += 2) {
+                const uint64_t e = kMods ? add2(pair(s[i], s[i + 1]), nm2) : fma2(pair(s[i], s[i + 1]), c2, nm2);
+                float p0, p1;
+                unpair(e, p0, p1);
+                p0 = ex2_approx(p0);
+                p1 = ex2_approx(p1);
+                if (i & 2)
+                    la = add2(la, pair(p0, p1));
+                else
+                    lb = add2(lb, pair(p0, p1));
+                w[i / 2] = pack2<T>(p0, p1);
             }
+            tmem_st_32x32b_x32(tq, w);
+            float l0, l1;
+            unpair(add2(la, lb), l0, l1);
             l_run += l0 + l1;
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&c.pready[rt]);
+            if (lane == 0) mbar_arrive(&c.pready[rt][b2]);
         }
         if (ok) ok = warp_wait(&c.odone[rt], 0);
         tc_fence_after();
@@ -532,8 +571,11 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 32; ++i) o[i] = cb * 32 + i < a.dv ? acc[cb * 32 + i] : 0.f;
             } else if (ok) {
-                tmem_ld_32x32b_x32(to + cb * 32, o);
-                tmem_ld_wait();
+                uint32_t x[32];
+                tmem_ld_32x32b_x32_raw(to + cb * 32, x);
+                tmem_ld_wait_for(x);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(x[i]);
             }
             if (l == 0.f || (!ok && !by_key)) {
 #pragma unroll

@@ -185,6 +185,25 @@ def test_decode(dtype, heads, page):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", [32, 64, 80, 128])
+@pytest.mark.parametrize("T", [1, 16, 17, 40])
+@pytest.mark.parametrize("cap", [0.0, 1000.0])
+def test_every_column_counts_once(dtype, d, T, cap):
+    # query rows that are basis vectors against one key: row m's score is the key's column m % d, and lse is the score
+    c = Case([1], T, 8, 1, d, dtype=dtype, causal=False, cap=cap, seed=21)
+    c.scale = 1.0
+    c.k[0, 0] = (torch.arange(1, d + 1) / 8).to(dtype)
+    at = torch.arange(T * 8) % d
+    c.q = torch.nn.functional.one_hot(at, d).to(dtype).view(1, T, 8, d)
+    out, lse = c.run()
+    want = c.k[0, 0].double()[at]
+    want = cap * torch.tanh(want / cap) if cap else want
+    assert ((lse.view(-1).cpu().double() - want).abs() <= 2.0 ** -20 * want).all()
+    assert torch.equal(out.view(T * 8, d).cpu(), c.v[0, 0].expand(T * 8, d))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("T", [2, 17, 100])
 @pytest.mark.parametrize("heads", [(4, 1, 32), (8, 2, 64), (16, 2, 128), (5, 1, 72)])
 @pytest.mark.parametrize("page", [0, 32])
