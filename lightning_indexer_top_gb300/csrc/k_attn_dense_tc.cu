@@ -328,74 +328,89 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
                     warp_wait(&c.vfull[j % C::kStagesV], (uint32_t)((j / C::kStagesV) & 1));
             }
         } else if (warp == 1) {
-            if (lane == 0) {
-                // ---------------------------------------------- MMA issuer
-                const uint32_t id_qk = idesc_f16_f32_major(kRows, kStep, kBf16 ? 1 : 0, 0, 0);
-                const uint32_t id_pv = idesc_f16_f32_major(kRows, (a.dv + 15) & ~15, kBf16 ? 1 : 0, 0, 1);
-                const uint32_t qb = smem_u32(smem), kb = smem_u32(kt), vb = smem_u32(vt);
-                // step q is half (st0 + q) & 1 of tile (st0 + q) / 2 - t0
-                auto tile_of = [&](int q) { return ((st0 + q) >> 1) - t0; };
-                auto first_of = [&](int q) { return q == 0 || ((st0 + q) & 1) == 0; };
-                auto last_of = [&](int q) { return q == ns - 1 || ((st0 + q) & 1) == 1; };
-                auto qk = [&](int i, int q) {
-                    // descriptors of the first k-step; a later one adds its offset to the start address (16-byte units).
-                    // All D / 16 steps run (columns past dk are zero): stopped at dk by a run-time bound, the unrolled
-                    // chain's last descriptor came out wrong (nvcc 13.0; the basis-vector test shows it)
-                    const uint64_t qd = desc_sw128_kmajor(qb + i * (kRows * D * 2), 1024);
-                    const uint64_t kd = desc_sw128_kmajor(
-                        kb + (tile_of(q) % C::kStagesK) * C::kTileBytes + ((st0 + q) & 1) * (kStep * 128), 1024);
-                    const uint32_t d = tmem + (2 * i + (q & 1)) * kStep;
+            // -------------------------------------------------- MMA issuer: the warp walks together, a lane issues
+            // (operands that all lanes share stay in uniform registers; with one lane on its own the issue took
+            // about 100 cycles a product, more than the products)
+            const uint32_t id_qk = idesc_f16_f32_major(kRows, kStep, kBf16 ? 1 : 0, 0, 0);
+            const uint32_t id_pv = idesc_f16_f32_major(kRows, (a.dv + 15) & ~15, kBf16 ? 1 : 0, 0, 1);
+            const uint64_t kmajor = desc_sw128_kmajor(0, 1024), mnmajor = desc_sw128_mnmajor(0, kColBlock, 1024);
+            const uint32_t k_hi = desc_hi(kmajor), v_hi = desc_hi(mnmajor), k_lo = (uint32_t)kmajor, v_lo = (uint32_t)mnmajor;
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint32_t qb = k_lo + (smem_u32(smem) >> 4), kb = k_lo + (smem_u32(kt) >> 4), vb = v_lo + (smem_u32(vt) >> 4);
+            // step q is half (st0 + q) & 1 of tile (st0 + q) / 2 - t0
+            auto tile_of = [&](int q) { return ((st0 + q) >> 1) - t0; };
+            auto first_of = [&](int q) { return q == 0 || ((st0 + q) & 1) == 0; };
+            auto last_of = [&](int q) { return q == ns - 1 || ((st0 + q) & 1) == 1; };
+            // S = Q K^T of row tile i.  All D / 16 products run (columns past dk are zero): an unrolled chain that
+            // stopped at dk by a run-time bound got a wrong last descriptor (nvcc 13.0; the basis-vector test shows it)
+            auto qk = [&](int i, int q, int stage) {
+                const uint32_t ka = __shfl_sync(0xffffffffu, kb + ((stage * C::kTileBytes + ((st0 + q) & 1) * (kStep * 128)) >> 4), 0);
+                const uint32_t qa = qb + i * (kRows * D * 2 >> 4), d = tm + (2 * i + (q & 1)) * kStep;
+                if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks) {
-                        const uint64_t o = ((ks >> 2) * kColBlock + (ks & 3) * 32) >> 4;
-                        mma_f16_ss(d, qd + o, kd + o, id_qk, ks > 0 ? 1u : 0u);
+                        const uint32_t o = ((ks >> 2) * kColBlock + (ks & 3) * 32) >> 4;
+                        mma_f16_ss_lo(d, qa + o, k_hi, ka + o, k_hi, id_qk, ks > 0 ? 1u : 0u);
                     }
-                };
-                auto k_ready = [&](int q) {
-                    const int j = tile_of(q);
-                    return !first_of(q) || mbar_wait(&c.kfull[j % C::kStagesK], (uint32_t)((j / C::kStagesK) & 1));
-                };
-                bool ok = true;
-                for (int q = 0; ok && q < 2; ++q) {
-                    if (q < ns && !(ok = k_ready(q))) break;
-                    tc_fence_after();
-                    for (int i = 0; i < kTiles; ++i) {
-                        if (q < ns) qk(i, q);
-                        mma_commit(&c.sfull[i][q]);
-                    }
-                    if (q < ns && last_of(q)) mma_commit(&c.kempty[tile_of(q) % C::kStagesK]);
+                    mma_commit(&c.sfull[i][q & 1]);
                 }
-                for (int q = 0; ok && q < ns && !aborted(); ++q) {
-                    const int j = tile_of(q), sv = j % C::kStagesV, b2 = q & 1;
-                    for (int i = 0; ok && i < kTiles; ++i) {
-                        ok = mbar_wait(&c.pready[i][b2], (uint32_t)((q >> 1) & 1)) &&
-                             (i > 0 || !first_of(q) || mbar_wait(&c.vok[sv], (uint32_t)((j / C::kStagesV) & 1)));
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t vd = desc_sw128_mnmajor(
-                            vb + sv * C::kTileBytes + ((st0 + q) & 1) * (kStep * 128), kColBlock, 1024);
+                __syncwarp();
+            };
+            auto commit = [&](uint64_t* bar) {
+                if (elect_one()) mma_commit(bar);
+                __syncwarp();
+            };
+            auto k_ready = [&](int q) {
+                const int j = tile_of(q);
+                return !first_of(q) || warp_wait(&c.kfull[j % C::kStagesK], (uint32_t)((j / C::kStagesK) & 1));
+            };
+            bool ok = true;
+            for (int q = 0; ok && q < 2; ++q) {
+                if (q >= ns) {
+                    for (int i = 0; i < kTiles; ++i) commit(&c.sfull[i][q]);
+                    continue;
+                }
+                ok = k_ready(q);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int i = 0; i < kTiles; ++i) qk(i, q, tile_of(q) % C::kStagesK);
+                if (last_of(q)) commit(&c.kempty[tile_of(q) % C::kStagesK]);
+            }
+            for (int q = 0; ok && q < ns && !warp_aborted(); ++q) {
+                const int j = tile_of(q), sv = j % C::kStagesV, b2 = q & 1, sk2 = tile_of(q + 2) % C::kStagesK;
+                const uint32_t va = __shfl_sync(0xffffffffu, vb + ((sv * C::kTileBytes + ((st0 + q) & 1) * (kStep * 128)) >> 4), 0);
+                const uint32_t acc = __shfl_sync(0xffffffffu, q > 0 ? 1u : 0u, 0);
+#pragma unroll
+                for (int i = 0; i < kTiles; ++i) {
+                    ok = ok && warp_wait(&c.pready[i][b2], (uint32_t)((q >> 1) & 1)) &&
+                         (i > 0 || !first_of(q) || warp_wait(&c.vok[sv], (uint32_t)((j / C::kStagesV) & 1)));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t pa = tm + (2 * i + b2) * kStep, d = tm + C::kOCol + i * D;
+                    if (elect_one()) {
 #pragma unroll
                         for (int ks = 0; ks < kStep / 16; ++ks)
-                            mma_f16_ts(tmem + C::kOCol + i * D, tmem + (2 * i + b2) * kStep + ks * 8,
-                                       vd + (uint64_t)(ks * 2048 >> 4), id_pv, (q > 0 || ks > 0) ? 1u : 0u);
-                        // S of the step after the next one over P of this one: the products run in order.  (The
-                        // commit for step ns has no scores: it tells that the PV product of step ns - 2 is complete.)
-                        if (q + 2 < ns) {
-                            ok = i > 0 || k_ready(q + 2);
-                            if (!ok) break;
-                            qk(i, q + 2);
-                        }
-                        if (q + 2 <= ns) mma_commit(&c.sfull[i][b2]);
-                        if (q + 1 == ns) mma_commit(&c.odone[i]);
+                            mma_f16_ts_lo(d, pa + ks * 8, va + (ks * 2048 >> 4), v_hi, id_pv, ks > 0 ? 1u : acc);
                     }
-                    if (ok && last_of(q)) mma_commit(&c.vempty[sv]);
-                    if (ok && q + 2 < ns && last_of(q + 2)) mma_commit(&c.kempty[tile_of(q + 2) % C::kStagesK]);
+                    __syncwarp();
+                    // S of the step after the next one over P of this one: the products run in order.  (The
+                    // commit for step ns has no scores: it tells that the PV product of step ns - 2 is complete.)
+                    if (q + 2 < ns) {
+                        ok = i > 0 || k_ready(q + 2);
+                        if (!ok) break;
+                        qk(i, q + 2, sk2);
+                    } else if (q + 2 == ns) {
+                        commit(&c.sfull[i][b2]);
+                    }
+                    if (q + 1 == ns) commit(&c.odone[i]);
                 }
-                if (!ok) give_up();
-                mma_commit(&c.done);
-                mbar_wait(&c.done, 0);
+                if (ok && last_of(q)) commit(&c.vempty[sv]);
+                if (ok && q + 2 < ns && last_of(q + 2)) commit(&c.kempty[sk2]);
             }
-            __syncwarp();
+            if (!ok) give_up();
+            commit(&c.done);
+            warp_wait(&c.done, 0);
         } else if (warp < kOtherWarps) {
             // -------------------------------------------------- V checkers: tiles that some row sees in part
             const int w = warp - 2;
