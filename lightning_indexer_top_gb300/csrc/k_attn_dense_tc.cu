@@ -13,7 +13,7 @@
 // when the softmax of one ends: the softmax warps never wait for the tensor core
 // (one 128-key buffer, no lookahead: 1.03 ms on 4096 rows x 16384 keys, the
 // tensor pipe 42 % busy and nothing else above 33 %).
-// Warps 0-3: TMA producer, MMA issuer, two V checkers; then four softmax warps
+// Warps 0-3: TMA producer, an MMA issuer per row tile, V checker; then four softmax warps
 // per row tile (thread = row = TMEM lane), which also write the output.  With
 // two row tiles per CTA a K/V tile is read for 256 rows; with one (few rows: a
 // decode step) two CTAs share an SM and the walk is bound by the stream of K and V.
@@ -63,11 +63,11 @@ struct Cfg {
 struct Ctl {
     uint64_t kfull[3], kempty[3];
     uint64_t vfull[3], vempty[3];
-    uint64_t vok[3];              // V looked over (both checker warps)
+    uint64_t vok[3];              // V looked over
     uint64_t sfull[2][2];         // S buffer of a row tile written (and the PV products of two steps before complete)
     uint64_t pready[2][2];        // P written over it, O rescaled
     uint64_t odone[2];            // every product of a row tile complete
-    uint64_t done;
+    uint64_t done[2];
     uint32_t tmem_base;
     int abort;
     int dirty;                    // a NaN or infinity in a V row that only some rows see
@@ -176,10 +176,10 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     if (threadIdx.x == 0) {
         for (int i = 0; i < 3; ++i) {
             mbar_init(&c.kfull[i], 1);
-            mbar_init(&c.kempty[i], 1);
+            mbar_init(&c.kempty[i], kTiles);
             mbar_init(&c.vfull[i], 1);
-            mbar_init(&c.vempty[i], 1);
-            mbar_init(&c.vok[i], 2);
+            mbar_init(&c.vempty[i], kTiles);
+            mbar_init(&c.vok[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             for (int x = 0; x < 2; ++x) {
@@ -187,8 +187,8 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
                 mbar_init(&c.pready[i][x], 4);
             }
             mbar_init(&c.odone[i], 1);
+            mbar_init(&c.done[i], 1);
         }
-        mbar_init(&c.done, 1);
         c.abort = 0;
         c.dirty = 0;
         c.k0 = INT32_MAX;
@@ -327,25 +327,41 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
                 for (int j = max(0, nv - C::kStagesV); j < nv; ++j)
                     warp_wait(&c.vfull[j % C::kStagesV], (uint32_t)((j / C::kStagesV) & 1));
             }
-        } else if (warp == 1) {
-            // -------------------------------------------------- MMA issuer: the warp walks together, a lane issues
-            // (operands that all lanes share stay in uniform registers; with one lane on its own the issue took
-            // about 100 cycles a product, more than the products)
+        } else if (warp <= kTiles) {
+            // -------------------------------------------------- MMA issuers, one warp per row tile.  The warp walks
+            // together and a lane issues: operands that all lanes share stay in uniform registers (with one lane on
+            // its own a product took about 100 cycles to issue, more than it takes).  The queue of issued products is
+            // short, so the tensor pipe idles while an issuer waits or commits: with a warp for each row tile it has
+            // the other one's (one warp for both: 2050 cycles a step against 1244 of products).
+            const int i = warp - 1;
             const uint32_t id_qk = idesc_f16_f32_major(kRows, kStep, kBf16 ? 1 : 0, 0, 0);
             const uint32_t id_pv = idesc_f16_f32_major(kRows, (a.dv + 15) & ~15, kBf16 ? 1 : 0, 0, 1);
             const uint64_t kmajor = desc_sw128_kmajor(0, 1024), mnmajor = desc_sw128_mnmajor(0, kColBlock, 1024);
             const uint32_t k_hi = desc_hi(kmajor), v_hi = desc_hi(mnmajor), k_lo = (uint32_t)kmajor, v_lo = (uint32_t)mnmajor;
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-            const uint32_t qb = k_lo + (smem_u32(smem) >> 4), kb = k_lo + (smem_u32(kt) >> 4), vb = v_lo + (smem_u32(vt) >> 4);
+            const uint32_t qa = __shfl_sync(0xffffffffu, k_lo + ((smem_u32(smem) + i * (kRows * D * 2)) >> 4), 0);
+            const uint32_t kb = k_lo + (smem_u32(kt) >> 4), vb = v_lo + (smem_u32(vt) >> 4);
+            const uint32_t ts = __shfl_sync(0xffffffffu, tm + 2 * i * kStep, 0);
+            const uint32_t to = __shfl_sync(0xffffffffu, tm + C::kOCol + i * D, 0);
             // step q is half (st0 + q) & 1 of tile (st0 + q) / 2 - t0
-            auto tile_of = [&](int q) { return ((st0 + q) >> 1) - t0; };
             auto first_of = [&](int q) { return q == 0 || ((st0 + q) & 1) == 0; };
             auto last_of = [&](int q) { return q == ns - 1 || ((st0 + q) & 1) == 1; };
-            // S = Q K^T of row tile i.  All D / 16 products run (columns past dk are zero): an unrolled chain that
+            int ks_ = 0, kph = 0, vs_ = 0, vph = 0;     // ring positions of the K tile and the V tile to use next
+            bool ok = true;
+            auto commit = [&](uint64_t* bar) {
+                if (elect_one()) mma_commit(bar);
+                __syncwarp();
+            };
+            // S = Q K^T of step q.  All D / 16 products run (columns past dk are zero): an unrolled chain that
             // stopped at dk by a run-time bound got a wrong last descriptor (nvcc 13.0; the basis-vector test shows it)
-            auto qk = [&](int i, int q, int stage) {
-                const uint32_t ka = __shfl_sync(0xffffffffu, kb + ((stage * C::kTileBytes + ((st0 + q) & 1) * (kStep * 128)) >> 4), 0);
-                const uint32_t qa = qb + i * (kRows * D * 2 >> 4), d = tm + (2 * i + (q & 1)) * kStep;
+            auto qk = [&](int q) {
+                if (first_of(q)) {
+                    ok = warp_wait(&c.kfull[ks_], (uint32_t)kph);
+                    if (!ok) return;
+                }
+                const uint32_t ka = __shfl_sync(0xffffffffu, kb + ((ks_ * C::kTileBytes + ((st0 + q) & 1) * (kStep * 128)) >> 4), 0);
+                const uint32_t d = __shfl_sync(0xffffffffu, ts + (q & 1) * kStep, 0);
+                const bool last = last_of(q);
                 if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks) {
@@ -353,67 +369,53 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
                         mma_f16_ss_lo(d, qa + o, k_hi, ka + o, k_hi, id_qk, ks > 0 ? 1u : 0u);
                     }
                     mma_commit(&c.sfull[i][q & 1]);
+                    if (last) mma_commit(&c.kempty[ks_]);
                 }
                 __syncwarp();
-            };
-            auto commit = [&](uint64_t* bar) {
-                if (elect_one()) mma_commit(bar);
-                __syncwarp();
-            };
-            auto k_ready = [&](int q) {
-                const int j = tile_of(q);
-                return !first_of(q) || warp_wait(&c.kfull[j % C::kStagesK], (uint32_t)((j / C::kStagesK) & 1));
-            };
-            bool ok = true;
-            for (int q = 0; ok && q < 2; ++q) {
-                if (q >= ns) {
-                    for (int i = 0; i < kTiles; ++i) commit(&c.sfull[i][q]);
-                    continue;
+                if (last && ++ks_ == C::kStagesK) {
+                    ks_ = 0;
+                    kph ^= 1;
                 }
-                ok = k_ready(q);
+            };
+            tc_fence_after();
+            qk(0);
+            if (ok) {
+                if (ns > 1) qk(1);
+                else commit(&c.sfull[i][1]);
+            }
+            for (int q = 0; ok && q < ns; ++q) {
+                const int b2 = q & 1;
+                const uint32_t va = __shfl_sync(0xffffffffu, vb + ((vs_ * C::kTileBytes + ((st0 + q) & 1) * (kStep * 128)) >> 4), 0);
+                const uint32_t acc = __shfl_sync(0xffffffffu, q > 0 ? 1u : 0u, 0);
+                const uint32_t pa = __shfl_sync(0xffffffffu, ts + b2 * kStep, 0);
+                ok = (!first_of(q) || warp_wait(&c.vok[vs_], (uint32_t)vph)) &&
+                     warp_wait(&c.pready[i][b2], (uint32_t)((q >> 1) & 1));
                 if (!ok) break;
                 tc_fence_after();
+                const bool last = last_of(q);
+                if (elect_one()) {
 #pragma unroll
-                for (int i = 0; i < kTiles; ++i) qk(i, q, tile_of(q) % C::kStagesK);
-                if (last_of(q)) commit(&c.kempty[tile_of(q) % C::kStagesK]);
-            }
-            for (int q = 0; ok && q < ns && !warp_aborted(); ++q) {
-                const int j = tile_of(q), sv = j % C::kStagesV, b2 = q & 1, sk2 = tile_of(q + 2) % C::kStagesK;
-                const uint32_t va = __shfl_sync(0xffffffffu, vb + ((sv * C::kTileBytes + ((st0 + q) & 1) * (kStep * 128)) >> 4), 0);
-                const uint32_t acc = __shfl_sync(0xffffffffu, q > 0 ? 1u : 0u, 0);
-#pragma unroll
-                for (int i = 0; i < kTiles; ++i) {
-                    ok = ok && warp_wait(&c.pready[i][b2], (uint32_t)((q >> 1) & 1)) &&
-                         (i > 0 || !first_of(q) || warp_wait(&c.vok[sv], (uint32_t)((j / C::kStagesV) & 1)));
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t pa = tm + (2 * i + b2) * kStep, d = tm + C::kOCol + i * D;
-                    if (elect_one()) {
-#pragma unroll
-                        for (int ks = 0; ks < kStep / 16; ++ks)
-                            mma_f16_ts_lo(d, pa + ks * 8, va + (ks * 2048 >> 4), v_hi, id_pv, ks > 0 ? 1u : acc);
-                    }
-                    __syncwarp();
-                    // S of the step after the next one over P of this one: the products run in order.  (The
-                    // commit for step ns has no scores: it tells that the PV product of step ns - 2 is complete.)
-                    if (q + 2 < ns) {
-                        ok = i > 0 || k_ready(q + 2);
-                        if (!ok) break;
-                        qk(i, q + 2, sk2);
-                    } else if (q + 2 == ns) {
-                        commit(&c.sfull[i][b2]);
-                    }
-                    if (q + 1 == ns) commit(&c.odone[i]);
+                    for (int ks = 0; ks < kStep / 16; ++ks)
+                        mma_f16_ts_lo(to, pa + ks * 8, va + (ks * 2048 >> 4), v_hi, id_pv, ks > 0 ? 1u : acc);
+                    if (last) mma_commit(&c.vempty[vs_]);
                 }
-                if (ok && last_of(q)) commit(&c.vempty[sv]);
-                if (ok && q + 2 < ns && last_of(q + 2)) commit(&c.kempty[sk2]);
+                __syncwarp();
+                if (last && ++vs_ == C::kStagesV) {
+                    vs_ = 0;
+                    vph ^= 1;
+                }
+                // S of the step after the next one over P of this one: a tile's products run in order.  (The commit
+                // for step ns has no scores: it tells that the PV product of step ns - 2 is complete.)
+                if (q + 2 < ns)
+                    qk(q + 2);
+                else
+                    commit(q + 2 == ns ? &c.sfull[i][b2] : &c.odone[i]);
             }
             if (!ok) give_up();
-            commit(&c.done);
-            warp_wait(&c.done, 0);
-        } else if (warp < kOtherWarps) {
-            // -------------------------------------------------- V checkers: tiles that some row sees in part
-            const int w = warp - 2;
+            commit(&c.done[i]);
+            warp_wait(&c.done[i], 0);
+        } else if (warp == kOtherWarps - 1) {
+            // -------------------------------------------------- V checker: tiles that some row sees in part
             for (int j = 0; j < n; ++j) {
                 const int sv = j % C::kStagesV;
                 if (warp_aborted() || !warp_wait(&c.vfull[sv], (uint32_t)((j / C::kStagesV) & 1))) {
@@ -425,7 +427,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
                     uint8_t* v = vt + sv * C::kTileBytes;
                     bool found = false;
                     // four lanes per V row and column block (rows of 128 bytes)
-                    for (int e = w * 32 + lane; e < kKeys * 4 * (D / 64); e += 64) {
+                    for (int e = lane; e < kKeys * 4 * (D / 64); e += 32) {
                         const int row = (e >> 2) & (kKeys - 1), cb = e / (kKeys * 4);
                         uint4* x = reinterpret_cast<uint4*>(v + cb * kColBlock + row * 128 + (e & 3) * 32);
                         if (key0 + row < k0 || key0 + row >= k1) {
@@ -463,8 +465,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         const uint64_t c2 = pair(sc.c, sc.c);
         for (int q = 0; ok && q < ns; ++q) {
             const int b2 = q & 1;
-            if (__any_sync(0xffffffffu, *(volatile int*)&c.abort != 0) ||
-                !warp_wait(&c.sfull[rt][b2], (uint32_t)((q >> 1) & 1))) {
+            if (!warp_wait(&c.sfull[rt][b2], (uint32_t)((q >> 1) & 1))) {
                 timed_out();
                 break;
             }
