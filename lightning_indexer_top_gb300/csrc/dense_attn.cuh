@@ -94,47 +94,45 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-// k * tanh of two numbers in [-1/2, 1/2] by its Taylor series up to x^13 (the next term is below 2^-23 of x there)
-__device__ __forceinline__ uint64_t tanh_small2(uint64_t x, uint64_t k) {
-    auto both = [](float c) { return pair(c, c); };
-    const uint64_t y = mul2(x, x);
-    uint64_t p = both(21844.f / 6081075.f);
-    p = fma2(p, y, both(-1382.f / 155925.f));
-    p = fma2(p, y, both(62.f / 2835.f));
-    p = fma2(p, y, both(-17.f / 315.f));
-    p = fma2(p, y, both(2.f / 15.f));
-    p = fma2(p, y, both(-1.f / 3.f));
-    return mul2(fma2(mul2(p, y), x, x), k);
-}
-
-// 1 - 2 / (1 + e^(2x)): for |x| > 1/2, where it does not cancel
+// 1 - 2 / (1 + e^(2x)): for |x| > 0.3, where it does not cancel
 __device__ __forceinline__ float tanh_large(float x) {
     return fmaf(-2.f, rcp_approx(1.f + sm100::ex2_approx(x * (2.f * kLog2e))), 1.f);
 }
 
 // N raw products of consecutive keys -> scores in log2 units; d0 = the row's position minus the first key's.
 // Every lane of a warp comes here together.
+// A capped score is cap * tanh(x), x = s * scale / softcap: for |x| <= 0.3 by the Taylor series of tanh up to x^9
+// (the next term is below 2^-24 of x there), as s times a polynomial in s^2 whose coefficients hold the factors (six
+// packed operations for two scores; the exponential form takes two special functions for each).
 template <int N>
 __device__ __forceinline__ void modify(float (&s)[N], const Score& sc, float d0) {
     if (sc.inv_cap != 0.f) {
         float big = 0.f;
 #pragma unroll
-        for (int i = 0; i < N; ++i) big = fmaxf(big, fabsf(s[i]));
-        const uint64_t k = pair(sc.cap, sc.cap), ic = pair(sc.inv_cap, sc.inv_cap);
+        for (int i = 0; i < N; i += 2) big = fmaxf(fmaxf(big, fabsf(s[i])), fabsf(s[i + 1]));
         // (a NaN is no larger than anything and goes through the series)
-        if (__any_sync(0xffffffffu, big * fabsf(sc.inv_cap) > 0.5f)) {
+        const bool large = big * fabsf(sc.inv_cap) > 0.3f;
+        const float i2 = sc.inv_cap * sc.inv_cap;
+        auto both = [](float x) { return pair(x, x); };
+        const uint64_t c1 = both(sc.c), c3 = both(sc.c * i2 * (-1.f / 3.f)), c5 = both(sc.c * i2 * i2 * (2.f / 15.f)),
+                       c7 = both(sc.c * i2 * i2 * i2 * (-17.f / 315.f)),
+                       c9 = both(sc.c * i2 * i2 * i2 * i2 * (62.f / 2835.f));
+        auto series = [&](float x, float y, float& rx, float& ry) {
+            const uint64_t v = pair(x, y), z = mul2(v, v);
+            unpair(mul2(v, fma2(fma2(fma2(fma2(c9, z, c7), z, c5), z, c3), z, c1)), rx, ry);
+        };
+        if (__any_sync(0xffffffffu, large)) {
 #pragma unroll
             for (int i = 0; i < N; i += 2) {
                 const float x0 = s[i] * sc.inv_cap, x1 = s[i + 1] * sc.inv_cap;
                 float y0, y1;
-                unpair(tanh_small2(pair(x0, x1), k), y0, y1);
-                s[i] = fabsf(x0) > 0.5f ? sc.cap * tanh_large(x0) : y0;
-                s[i + 1] = fabsf(x1) > 0.5f ? sc.cap * tanh_large(x1) : y1;
+                series(s[i], s[i + 1], y0, y1);
+                s[i] = fabsf(x0) > 0.3f ? sc.cap * tanh_large(x0) : y0;
+                s[i + 1] = fabsf(x1) > 0.3f ? sc.cap * tanh_large(x1) : y1;
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < N; i += 2)
-                unpair(tanh_small2(mul2(pair(s[i], s[i + 1]), ic), k), s[i], s[i + 1]);
+            for (int i = 0; i < N; i += 2) series(s[i], s[i + 1], s[i], s[i + 1]);
         }
     } else {
         const uint64_t c = pair(sc.c, sc.c);

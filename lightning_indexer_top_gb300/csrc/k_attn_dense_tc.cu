@@ -5,18 +5,25 @@
 // into rows m = t*G + h, 128 to a tile (the M side of the MMAs), so a K or V
 // tile that is read once serves every head of the group.  A CTA owns kTiles
 // such tiles of one (sequence, kv head) and one split of the key line, and
-// walks it in steps of 64 keys (K and V come in tiles of 128):
-//     S = Q K^T       [128 x 64] f32 in TMEM      (Q, K from shared memory)
-//     P = 2^(S*c - m) bf16/f16, written over S in TMEM
-//     O = O + P V     [128 x dv] f32 in TMEM      (P from TMEM, V from shared memory)
-// S has two buffers per row tile, so that the scores of the next step are there
-// when the softmax of one ends: the softmax warps never wait for the tensor core
-// (one 128-key buffer, no lookahead: 1.03 ms on 4096 rows x 16384 keys, the
-// tensor pipe 42 % busy and nothing else above 33 %).
-// Warps 0-3: TMA producer, an MMA issuer per row tile, V checker; then four softmax warps
-// per row tile (thread = row = TMEM lane), which also write the output.  With
-// two row tiles per CTA a K/V tile is read for 256 rows; with one (few rows: a
-// decode step) two CTAs share an SM and the walk is bound by the stream of K and V.
+// walks it in tiles of 128 keys:
+//     S = Q K^T       [128 x 128] f32 in TMEM     (Q, K from shared memory)
+//     P = 2^(S*c - m) bf16/f16, written over S in TMEM, 64 keys at a time
+//     O = O + P V     [128 x dv] f32 in TMEM      (P from TMEM, V from shared memory),
+//                     64 keys at a time: the first half's product runs while the
+//                     softmax is on the second half
+// Warps 0-3: TMA producer, an MMA issuer per row tile, V checker; then four
+// softmax warps per row tile (thread = row = TMEM lane), which also write the
+// output.  With two row tiles per CTA a K/V tile is read for 256 rows and the
+// tensor core works on one tile while the other's softmax runs; with one (up to
+// 48 packed rows: a decode step) two CTAs share an SM and the walk is bound by the
+// stream of K and V.
+//
+// What the shape follows from, measured on a GB300: a 128 x 128 x 16 product takes
+// 64 cycles (128 x 64 x 16 with both operands in shared memory 48, so scores are
+// made for 128 keys at a time), the issuers' queue is short, and a softmax of 128
+// rows x 64 keys takes 650 to 800 cycles.  On 4096 rows x 16384 keys (32 / 4 heads
+// of 128, causal): one issuer, a lane on its own 1.17 ms; the warp together 0.99;
+// an issuer per row tile 0.80 (64-key scores, double buffered); this form 0.XX.
 //
 // A row's maximum follows its scores lazily: O is rescaled (by the softmax
 // warps, in TMEM) only when a score passes it by 2^8, so P stays <= 2^8.
@@ -40,32 +47,38 @@ namespace {
 using namespace sm100;
 
 constexpr int kKeys = 128;             // keys per K/V tile
-constexpr int kStep = 64;              // keys per softmax step
+constexpr int kHalf = 64;              // keys per softmax step and second product
 constexpr int kRows = 128;             // packed query rows per row tile
 constexpr int kColBlock = 128 * 128;   // 64 columns x 128 rows of a tile, in the 128-byte swizzle
+constexpr int kFewRows = 48;           // packed rows up to which a CTA has one row tile and half an SM
 constexpr int kOtherWarps = 4;
 
 template <int D, int kTiles>
 struct Cfg {
     static constexpr int kTileBytes = kKeys * D * 2;
-    static constexpr int kQBytes = kTiles * kRows * D * 2;
-    // one row tile: two CTAs per SM share its shared memory
+    // rows of Q kept per row tile.  With kFewRows the M = 128 products read on into the K tile: what they
+    // make of it stays in TMEM lanes that nobody reads.
+    static constexpr int kQRows = kTiles == 2 ? kRows : kFewRows;
+    static constexpr int kQTile = kQRows * D * 2;
+    static constexpr int kQBlock = kQRows * 128;      // 64 columns of it
     static constexpr int kStagesK = kTiles == 2 ? 2 : D == 64 ? 2 : 1;
-    static constexpr int kStagesV = kTiles == 2 ? 3 : D == 64 ? 2 : 1;
+    static constexpr int kStagesV = kTiles == 2 ? 3 : D == 64 ? 3 : 2;
     static constexpr int kCtas = kTiles == 2 ? 1 : 2;
-    static constexpr int kVOff = kQBytes + kStagesK * kTileBytes;
+    static constexpr int kKOff = kTiles * kQTile;
+    static constexpr int kVOff = kKOff + kStagesK * kTileBytes;
     static constexpr int kCtlOff = kVOff + kStagesV * kTileBytes;
     static constexpr int kThreads = 32 * kOtherWarps + kRows * kTiles;
     static constexpr int kTmemCols = kTiles == 2 ? 512 : 256;
-    static constexpr int kOCol = kTiles * 2 * kStep;  // S buffer b of row tile i at (2*i + b)*kStep; O at kOCol + i*D
+    static constexpr int kOCol = kTiles * kKeys;      // S of row tile i at i*kKeys, O at kOCol + i*D
 };
 
 struct Ctl {
     uint64_t kfull[3], kempty[3];
     uint64_t vfull[3], vempty[3];
     uint64_t vok[3];              // V looked over
-    uint64_t sfull[2][2];         // S buffer of a row tile written (and the PV products of two steps before complete)
-    uint64_t pready[2][2];        // P written over it, O rescaled
+    uint64_t sfull[2];            // S of a row tile written (and the PV products of the tile before complete)
+    uint64_t pready[2][2];        // a half of P written over it, O rescaled
+    uint64_t pvdone[2];           // the first half's PV product complete
     uint64_t odone[2];            // every product of a row tile complete
     uint64_t done[2];
     uint32_t tmem_base;
@@ -74,7 +87,7 @@ struct Ctl {
     int k0, k1, full0, full1;     // the CTA's keys, and those that each of its rows sees
 };
 
-template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float hi);   // two rounded to T
 template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
     const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&x);
@@ -126,25 +139,41 @@ __device__ __noinline__ void scalar_row(const TcArgs& p, const Geom& g, int b, i
     *l_out = l;
 }
 
-// columns [c0, c0 + n) of a row's result, n a multiple of 8 and at most 32: normalised to the output, or a
-// split's partial
-template <typename T>
-__device__ __forceinline__ void store_cols(const DenseArgs& a, int64_t rh, int split, int c0, int n, const float (&v)[32],
-                                           float inv) {
-    if (a.splits > 1) {
-        float4* d = reinterpret_cast<float4*>(a.part_o + (rh * a.splits + split) * a.dv + c0);
+// 32 columns of a row into its warp's staging rows of W columns (16-byte pieces, swizzled by the row)
+template <typename E, int W>
+__device__ __forceinline__ void stage_cols(uint8_t* rows, int row, int c0, const float (&v)[32]) {
+    constexpr int kPer = 16 / (int)sizeof(E);
+    uint8_t* r = rows + row * (W * (int)sizeof(E));
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (4 * i < n) d[i] = make_float4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
-    } else {
-        uint4* d = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + rh * a.dv + c0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (8 * i < n)
-                d[i] = make_uint4(pack2<T>(v[8 * i] * inv, v[8 * i + 1] * inv), pack2<T>(v[8 * i + 2] * inv, v[8 * i + 3] * inv),
-                                  pack2<T>(v[8 * i + 4] * inv, v[8 * i + 5] * inv),
-                                  pack2<T>(v[8 * i + 6] * inv, v[8 * i + 7] * inv));
+    for (int i = 0; i < 32 / kPer; ++i) {
+        uint4 x;
+        if constexpr (sizeof(E) == 4)
+            x = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                           __float_as_uint(v[4 * i + 3]));
+        else
+            x = make_uint4(pack2<E>(v[8 * i], v[8 * i + 1]), pack2<E>(v[8 * i + 2], v[8 * i + 3]),
+                           pack2<E>(v[8 * i + 4], v[8 * i + 5]), pack2<E>(v[8 * i + 6], v[8 * i + 7]));
+        *reinterpret_cast<uint4*>(r + (((c0 / kPer + i) ^ (row & 7)) << 4)) = x;
     }
+}
+
+// the first n columns of the warp's staged rows to out (row r at out + at_r, elements), whole rows at a time
+template <typename E, int W>
+__device__ __forceinline__ void store_rows(E* out, int64_t at, bool valid, const uint8_t* rows, int n) {
+    constexpr int kPer = 16 / (int)sizeof(E);
+    const int lane = threadIdx.x & 31;
+    const int pieces = n / kPer;
+    __syncwarp();
+    for (int k = 0; k < pieces; ++k) {
+        const int e = k * 32 + lane;
+        const int row = e / pieces, pc = e - row * pieces;
+        const int64_t to = __shfl_sync(0xffffffffu, at, row);
+        const bool ok = __shfl_sync(0xffffffffu, (int)valid, row) != 0;
+        if (ok)
+            *reinterpret_cast<uint4*>(out + to + pc * kPer) =
+                *reinterpret_cast<const uint4*>(rows + row * (W * (int)sizeof(E)) + ((pc ^ (row & 7)) << 4));
+    }
+    __syncwarp();
 }
 
 template <typename T, int D, int kTiles, bool kMods>
@@ -156,7 +185,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     constexpr float kTop = kShift + 8.f;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* kt = smem + C::kQBytes;
+    uint8_t* kt = smem + C::kKOff;
     uint8_t* vt = smem + C::kVOff;
     Ctl& c = *reinterpret_cast<Ctl*>(smem + C::kCtlOff);
     const DenseArgs& a = p.a;
@@ -170,22 +199,23 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     const int bg = (int)(u % ((int64_t)g.B * a.Hkv));
     const int tile = p.tiles - 1 - (int)(u / ((int64_t)g.B * a.Hkv));
     const int gkv = bg % a.Hkv, b = bg / a.Hkv;
-    const int64_t m0 = (int64_t)tile * (kTiles * kRows), m_end = (int64_t)g.T * G;
+    const int64_t m0 = (int64_t)tile * (kTiles * kRows);
+    const int n_rows = (int)min((int64_t)g.T * G - m0, (int64_t)kTiles * kRows);   // packed rows of this CTA
+    const int n_tiles = (n_rows + kRows - 1) / kRows;                              // row tiles with rows
 
     pdl_trigger();
     if (threadIdx.x == 0) {
         for (int i = 0; i < 3; ++i) {
             mbar_init(&c.kfull[i], 1);
-            mbar_init(&c.kempty[i], kTiles);
+            mbar_init(&c.kempty[i], n_tiles);
             mbar_init(&c.vfull[i], 1);
-            mbar_init(&c.vempty[i], kTiles);
+            mbar_init(&c.vempty[i], n_tiles);
             mbar_init(&c.vok[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            for (int x = 0; x < 2; ++x) {
-                mbar_init(&c.sfull[i][x], 1);
-                mbar_init(&c.pready[i][x], 4);
-            }
+        for (int i = 0; i < n_tiles; ++i) {
+            mbar_init(&c.sfull[i], 1);
+            for (int x = 0; x < 2; ++x) mbar_init(&c.pready[i][x], min(4, (n_rows - i * kRows + 31) / 32));   // warps with rows
+            mbar_init(&c.pvdone[i], 1);
             mbar_init(&c.odone[i], 1);
             mbar_init(&c.done[i], 1);
         }
@@ -209,14 +239,17 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     // ---- the rows: interval, position, slope; the CTA's keys
     const int n_kv = seq_n_kv(g, b);
     const int rt = (warp - kOtherWarps) >> 2;                       // this thread's row tile (softmax warps)
-    const int64_t m = m0 + (int64_t)threadIdx.x - 32 * kOtherWarps; // ... and packed row
+    const int r = (int)threadIdx.x - 32 * kOtherWarps;              // ... and row of the CTA
+    const bool has_row = r >= 0 && r < n_rows;
+    const bool warp_rows = warp >= kOtherWarps && r - lane < n_rows;  // some row of the warp is one
+    const int t00 = (int)(m0 / G), h00 = (int)(m0 - (int64_t)t00 * G);   // token and head of the CTA's first row
     Interval iv = {0, 0, 0};
     int64_t qrow = 0;
     int h = 0, wlo = 0, whi = INT32_MAX;    // keys that every row of the warp sees
-    if (warp >= kOtherWarps) {
-        if (m < m_end) {
-            const int t = (int)(m / G);
-            h = gkv * G + (int)(m - (int64_t)t * G);
+    if (warp_rows) {
+        if (has_row) {
+            const int t = t00 + (h00 + r) / G;
+            h = gkv * G + (h00 + r) % G;
             qrow = (int64_t)b * g.T + t;
             iv = row_interval(g, a.mods, qrow, b, n_kv);
         }
@@ -233,18 +266,19 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         }
     }
     // Q: 16-byte pieces into the swizzled K-major layout; rows and columns past the end are zero
-    for (int i = threadIdx.x; i < kTiles * kRows * (D / 8); i += C::kThreads) {
-        const int r = i / (D / 8), cc = i % (D / 8);
-        const int64_t mm = m0 + r;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (mm < m_end && cc * 8 < a.dk) {
-            const int64_t t = mm / G;
-            x = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) +
-                                                (((int64_t)b * g.T + t) * a.Hq + gkv * G + (mm - t * G)) * a.dk + cc * 8);
+    {
+        const T* q = static_cast<const T*>(a.q) + ((int64_t)b * g.T * a.Hq + gkv * G) * a.dk;
+        for (int i = threadIdx.x; i < kTiles * C::kQRows * (D / 8); i += C::kThreads) {
+            const int rr = i / (D / 8), cc = i % (D / 8);
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            if (rr < n_rows && cc * 8 < a.dk) {
+                const int t = (h00 + rr) / G;
+                x = *reinterpret_cast<const uint4*>(q + ((int64_t)(t00 + t) * a.Hq + (h00 + rr - t * G)) * a.dk + cc * 8);
+            }
+            const int r0 = rr % C::kQRows;
+            *reinterpret_cast<uint4*>(smem + rr / C::kQRows * C::kQTile + (cc >> 3) * C::kQBlock + r0 * 128 +
+                                      (((cc & 7) ^ (r0 & 7)) << 4)) = x;
         }
-        const int rr = r & (kRows - 1);
-        *reinterpret_cast<uint4*>(smem + (r / kRows) * (kRows * D * 2) + (cc >> 3) * kColBlock + rr * 128 +
-                                  (((cc & 7) ^ (rr & 7)) << 4)) = x;
     }
     __syncthreads();
     // this split's keys, from a whole tile on (tiles are cuts of the position line)
@@ -252,8 +286,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     int k0 = c.k0, k1 = c.k1;
     if (k0 < s0) k0 = (int)(s0 < INT32_MAX ? s0 : INT32_MAX);
     if (k1 > s1) k1 = (int)s1;
-    const int t0 = k0 / kKeys, st0 = k0 / kStep;
-    const int ns = k1 > k0 ? (k1 + kStep - 1) / kStep - st0 : 0;
+    const int t0 = k0 / kKeys;
     const int n = k1 > k0 ? (k1 + kKeys - 1) / kKeys - t0 : 0;
     // every cache row of them exists?
     bool bad = false;
@@ -327,92 +360,80 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
                 for (int j = max(0, nv - C::kStagesV); j < nv; ++j)
                     warp_wait(&c.vfull[j % C::kStagesV], (uint32_t)((j / C::kStagesV) & 1));
             }
-        } else if (warp <= kTiles) {
+        } else if (warp <= n_tiles) {
             // -------------------------------------------------- MMA issuers, one warp per row tile.  The warp walks
             // together and a lane issues: operands that all lanes share stay in uniform registers (with one lane on
             // its own a product took about 100 cycles to issue, more than it takes).  The queue of issued products is
-            // short, so the tensor pipe idles while an issuer waits or commits: with a warp for each row tile it has
-            // the other one's (one warp for both: 2050 cycles a step against 1244 of products).
+            // short, so the tensor pipe idles while an issuer waits or commits: it has the other issuer's then.
             const int i = warp - 1;
-            const uint32_t id_qk = idesc_f16_f32_major(kRows, kStep, kBf16 ? 1 : 0, 0, 0);
+            const uint32_t id_qk = idesc_f16_f32_major(kRows, kKeys, kBf16 ? 1 : 0, 0, 0);
             const uint32_t id_pv = idesc_f16_f32_major(kRows, (a.dv + 15) & ~15, kBf16 ? 1 : 0, 0, 1);
             const uint64_t kmajor = desc_sw128_kmajor(0, 1024), mnmajor = desc_sw128_mnmajor(0, kColBlock, 1024);
             const uint32_t k_hi = desc_hi(kmajor), v_hi = desc_hi(mnmajor), k_lo = (uint32_t)kmajor, v_lo = (uint32_t)mnmajor;
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-            const uint32_t qa = __shfl_sync(0xffffffffu, k_lo + ((smem_u32(smem) + i * (kRows * D * 2)) >> 4), 0);
+            const uint32_t qa = __shfl_sync(0xffffffffu, k_lo + ((smem_u32(smem) + i * C::kQTile) >> 4), 0);
             const uint32_t kb = k_lo + (smem_u32(kt) >> 4), vb = v_lo + (smem_u32(vt) >> 4);
-            const uint32_t ts = __shfl_sync(0xffffffffu, tm + 2 * i * kStep, 0);
+            const uint32_t ts = __shfl_sync(0xffffffffu, tm + i * kKeys, 0);
             const uint32_t to = __shfl_sync(0xffffffffu, tm + C::kOCol + i * D, 0);
-            // step q is half (st0 + q) & 1 of tile (st0 + q) / 2 - t0
-            auto first_of = [&](int q) { return q == 0 || ((st0 + q) & 1) == 0; };
-            auto last_of = [&](int q) { return q == ns - 1 || ((st0 + q) & 1) == 1; };
-            int ks_ = 0, kph = 0, vs_ = 0, vph = 0;     // ring positions of the K tile and the V tile to use next
+            int sk = 0, kph = 0, sv = 0, vph = 0;     // ring positions of the K tile and the V tile to use next
             bool ok = true;
-            auto commit = [&](uint64_t* bar) {
-                if (elect_one()) mma_commit(bar);
-                __syncwarp();
-            };
-            // S = Q K^T of step q.  All D / 16 products run (columns past dk are zero): an unrolled chain that
-            // stopped at dk by a run-time bound got a wrong last descriptor (nvcc 13.0; the basis-vector test shows it)
-            auto qk = [&](int q) {
-                if (first_of(q)) {
-                    ok = warp_wait(&c.kfull[ks_], (uint32_t)kph);
-                    if (!ok) return;
-                }
-                const uint32_t ka = __shfl_sync(0xffffffffu, kb + ((ks_ * C::kTileBytes + ((st0 + q) & 1) * (kStep * 128)) >> 4), 0);
-                const uint32_t d = __shfl_sync(0xffffffffu, ts + (q & 1) * kStep, 0);
-                const bool last = last_of(q);
+            // S = Q K^T.  All D / 16 products run (columns past dk are zero): an unrolled chain that stopped at dk by
+            // a run-time bound got a wrong last descriptor (nvcc 13.0; the basis-vector test shows it)
+            auto qk = [&] {
+                const uint32_t ka = __shfl_sync(0xffffffffu, kb + (sk * C::kTileBytes >> 4), 0);
+                tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        const uint32_t o = ((ks >> 2) * kColBlock + (ks & 3) * 32) >> 4;
-                        mma_f16_ss_lo(d, qa + o, k_hi, ka + o, k_hi, id_qk, ks > 0 ? 1u : 0u);
-                    }
-                    mma_commit(&c.sfull[i][q & 1]);
-                    if (last) mma_commit(&c.kempty[ks_]);
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        mma_f16_ss_lo(ts, qa + (((ks >> 2) * C::kQBlock + (ks & 3) * 32) >> 4), k_hi,
+                                      ka + (((ks >> 2) * kColBlock + (ks & 3) * 32) >> 4), k_hi, id_qk, ks > 0 ? 1u : 0u);
+                    mma_commit(&c.sfull[i]);
+                    mma_commit(&c.kempty[sk]);
                 }
                 __syncwarp();
-                if (last && ++ks_ == C::kStagesK) {
-                    ks_ = 0;
+                if (++sk == C::kStagesK) {
+                    sk = 0;
                     kph ^= 1;
                 }
             };
-            tc_fence_after();
-            qk(0);
-            if (ok) {
-                if (ns > 1) qk(1);
-                else commit(&c.sfull[i][1]);
-            }
-            for (int q = 0; ok && q < ns; ++q) {
-                const int b2 = q & 1;
-                const uint32_t va = __shfl_sync(0xffffffffu, vb + ((vs_ * C::kTileBytes + ((st0 + q) & 1) * (kStep * 128)) >> 4), 0);
-                const uint32_t acc = __shfl_sync(0xffffffffu, q > 0 ? 1u : 0u, 0);
-                const uint32_t pa = __shfl_sync(0xffffffffu, ts + b2 * kStep, 0);
-                ok = (!first_of(q) || warp_wait(&c.vok[vs_], (uint32_t)vph)) &&
-                     warp_wait(&c.pready[i][b2], (uint32_t)((q >> 1) & 1));
+            ok = warp_wait(&c.kfull[0], 0u);
+            if (ok) qk();
+            for (int j = 0; ok && j < n; ++j) {
+                const uint32_t va = __shfl_sync(0xffffffffu, vb + (sv * C::kTileBytes >> 4), 0);
+                const uint32_t acc = __shfl_sync(0xffffffffu, j > 0 ? 1u : 0u, 0);
+                ok = warp_wait(&c.vok[sv], (uint32_t)vph) && warp_wait(&c.pready[i][0], (uint32_t)(j & 1));
                 if (!ok) break;
                 tc_fence_after();
-                const bool last = last_of(q);
                 if (elect_one()) {
 #pragma unroll
-                    for (int ks = 0; ks < kStep / 16; ++ks)
-                        mma_f16_ts_lo(to, pa + ks * 8, va + (ks * 2048 >> 4), v_hi, id_pv, ks > 0 ? 1u : acc);
-                    if (last) mma_commit(&c.vempty[vs_]);
+                    for (int ks = 0; ks < kHalf / 16; ++ks)
+                        mma_f16_ts_lo(to, ts + ks * 8, va + (ks * 2048 >> 4), v_hi, id_pv, ks > 0 ? 1u : acc);
+                    mma_commit(&c.pvdone[i]);
                 }
                 __syncwarp();
-                if (last && ++vs_ == C::kStagesV) {
-                    vs_ = 0;
+                // the next tile's S follows the second half's product over the same columns: a row tile's products
+                // run in order
+                ok = (j + 1 == n || warp_wait(&c.kfull[sk], (uint32_t)kph)) && warp_wait(&c.pready[i][1], (uint32_t)(j & 1));
+                if (!ok) break;
+                tc_fence_after();
+                const bool last = j + 1 == n;
+                if (elect_one()) {
+#pragma unroll
+                    for (int ks = kHalf / 16; ks < kKeys / 16; ++ks)
+                        mma_f16_ts_lo(to, ts + ks * 8, va + (ks * 2048 >> 4), v_hi, id_pv, 1u);
+                    mma_commit(&c.vempty[sv]);
+                    if (last) mma_commit(&c.odone[i]);
+                }
+                __syncwarp();
+                if (!last) qk();
+                if (++sv == C::kStagesV) {
+                    sv = 0;
                     vph ^= 1;
                 }
-                // S of the step after the next one over P of this one: a tile's products run in order.  (The commit
-                // for step ns has no scores: it tells that the PV product of step ns - 2 is complete.)
-                if (q + 2 < ns)
-                    qk(q + 2);
-                else
-                    commit(q + 2 == ns ? &c.sfull[i][b2] : &c.odone[i]);
             }
             if (!ok) give_up();
-            commit(&c.done[i]);
+            if (elect_one()) mma_commit(&c.done[i]);
+            __syncwarp();
             warp_wait(&c.done[i], 0);
         } else if (warp == kOtherWarps - 1) {
             // -------------------------------------------------- V checker: tiles that some row sees in part
@@ -450,11 +471,11 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         }
     }
     // -------------------------------------------------------------- softmax and output (thread = row)
-    if (warp >= kOtherWarps) {
+    if (warp_rows) {
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + lane_off + rt * 2 * kStep;
+        const uint32_t ts = tmem + lane_off + rt * kKeys;
         const uint32_t to = tmem + lane_off + C::kOCol + rt * D;
-        const Score sc = make_score(a, a.mods.slopes && m < m_end ? a.mods.slopes[h] : 0.f);
+        const Score sc = make_score(a, a.mods.slopes && has_row ? a.mods.slopes[h] : 0.f);
         float m_used = -INFINITY, l_run = 0.f;
         bool ok = n > 0 && !bad;
         auto timed_out = [&] {
@@ -463,20 +484,21 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
             ok = false;
         };
         const uint64_t c2 = pair(sc.c, sc.c);
-        for (int q = 0; ok && q < ns; ++q) {
-            const int b2 = q & 1;
-            if (!warp_wait(&c.sfull[rt][b2], (uint32_t)((q >> 1) & 1))) {
-                timed_out();
-                break;
+        for (int q = 0; ok && q < 2 * n; ++q) {
+            const int j = q >> 1, half = q & 1;
+            if (half == 0) {
+                if (!warp_wait(&c.sfull[rt], (uint32_t)(j & 1))) {
+                    timed_out();
+                    break;
+                }
+                tc_fence_after();
             }
-            tc_fence_after();
-            const int key0 = (st0 + q) * kStep;
-            const uint32_t tq = ts + b2 * kStep;
-            float s[kStep];
+            const int key0 = (t0 + j) * kKeys + half * kHalf;
+            float s[kHalf];
             {
                 uint32_t x[32], y[32];
-                tmem_ld_32x32b_x32_raw(tq, x);
-                tmem_ld_32x32b_x32_raw(tq + 32, y);
+                tmem_ld_32x32b_x32_raw(ts + half * kHalf, x);
+                tmem_ld_32x32b_x32_raw(ts + half * kHalf + 32, y);
                 tmem_ld_wait_for(x);
                 tmem_ld_wait_for(y);
 #pragma unroll
@@ -486,17 +508,17 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
                 }
             }
             if (kMods) modify(s, sc, (float)(iv.pos - key0));
-            if (key0 < wlo || key0 < k0 || key0 + kStep > whi || key0 + kStep > k1) {
+            if (key0 < wlo || key0 < k0 || key0 + kHalf > whi || key0 + kHalf > k1) {
                 // visible columns [a0, a1) of this row
                 const int a0 = max(iv.lo, k0) - key0, a1 = min(iv.hi, k1) - key0;
 #pragma unroll
-                for (int i = 0; i < kStep; ++i)
+                for (int i = 0; i < kHalf; ++i)
                     if (i < a0 || i >= a1) s[i] = -INFINITY;
             }
             // the row's maximum
             float x0 = fmaxf(s[0], s[1]), x1 = fmaxf(s[2], s[3]), x2 = fmaxf(s[4], s[5]), x3 = fmaxf(s[6], s[7]);
 #pragma unroll
-            for (int i = 8; i < kStep; i += 8) {
+            for (int i = 8; i < kHalf; i += 8) {
                 x0 = fmaxf(fmaxf(x0, s[i]), s[i + 1]);
                 x1 = fmaxf(fmaxf(x1, s[i + 2]), s[i + 3]);
                 x2 = fmaxf(fmaxf(x2, s[i + 4]), s[i + 5]);
@@ -514,8 +536,9 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
                     l_run *= al;
                 }
                 if (q > 0 && __any_sync(0xffffffffu, al != 1.f)) {
-                    // the products up to the last step's: complete once the next step's S is
-                    if (!warp_wait(&c.sfull[rt][b2 ^ 1], (uint32_t)(((q + 1) >> 1) & 1))) {
+                    // O's products up to here: those of the tile before are complete (its S came after them), the
+                    // first half's of this one has to be waited for
+                    if (half == 1 && !warp_wait(&c.pvdone[rt], (uint32_t)(j & 1))) {
                         timed_out();
                         break;
                     }
@@ -536,7 +559,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
             uint64_t la = 0ull, lb = 0ull;
             uint32_t w[32];
 #pragma unroll
-            for (int i = 0; i < kStep; i += 2) {
+            for (int i = 0; i < kHalf; i += 2) {
                 const uint64_t e = kMods ? add2(pair(s[i], s[i + 1]), nm2) : fma2(pair(s[i], s[i + 1]), c2, nm2);
                 float p0, p1;
                 unpair(e, p0, p1);
@@ -548,31 +571,32 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
                     lb = add2(lb, pair(p0, p1));
                 w[i / 2] = pack2<T>(p0, p1);
             }
-            tmem_st_32x32b_x32(tq, w);
+            tmem_st_32x32b_x32(ts + half * (kHalf / 2), w);
             float l0, l1;
             unpair(add2(la, lb), l0, l1);
             l_run += l0 + l1;
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&c.pready[rt][b2]);
+            if (lane == 0) mbar_arrive(&c.pready[rt][half]);
         }
         if (ok) ok = warp_wait(&c.odone[rt], 0);
         tc_fence_after();
         const bool some = iv.lo < iv.hi;
         const int64_t rh = qrow * a.Hq + h;
-        // the V checkers have seen every tile by now: each PV product waited for them
+        // the V checker has seen every tile by now: each PV product waited for it
         const bool by_key = bad || (n > 0 && *(volatile int*)&c.dirty != 0);
         float acc[D];
         if (by_key) {
             float mm = -INFINITY, ll = 0.f;
-            if (m < m_end && some) scalar_row<T>(p, g, b, gkv, qrow, h, iv, s0, s1, acc, &mm, &ll);
+            if (has_row && some) scalar_row<T>(p, g, b, gkv, qrow, h, iv, s0, s1, acc, &mm, &ll);
             m_used = mm;
             l_run = ll;
         }
+        __syncwarp();
         const float l = some && n > 0 ? l_run : 0.f;
         const float inv = l == 0.f ? 0.f : a.splits > 1 ? 1.f : 1.f / l;
-        if (m < m_end) {
+        if (has_row) {
             if (a.splits > 1) {
                 a.part_ml[(rh * a.splits + split) * 2] = m_used * kLn2;
                 a.part_ml[(rh * a.splits + split) * 2 + 1] = l;
@@ -580,25 +604,44 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
                 a.lse[rh] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * kLn2;
             }
         }
-#pragma unroll
-        for (int cb = 0; cb < D / 32; ++cb) {
-            float o[32];
+        // 32 columns of the row, normalised (a split's partial: as they are)
+        auto columns = [&](int cb, float (&o)[32]) {
             if (by_key) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = cb * 32 + i < a.dv ? acc[cb * 32 + i] : 0.f;
+                for (int i = 0; i < 32; ++i) o[i] = cb * 32 + i < a.dv ? acc[cb * 32 + i] * inv : 0.f;
             } else if (ok) {
                 uint32_t x[32];
                 tmem_ld_32x32b_x32_raw(to + cb * 32, x);
                 tmem_ld_wait_for(x);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(x[i]);
+                for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(x[i]) * inv;
             }
             if (l == 0.f || (!ok && !by_key)) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) o[i] = 0.f;
             }
-            const int cols = min(32, a.dv - cb * 32);
-            if (m < m_end && cols > 0) store_cols<T>(a, rh, split, cb * 32, cols, o, inv);
+        };
+        // through shared memory (Q's, and past it K's: no product reads them any more), so that whole rows are written
+        uint8_t* rows = smem + rt * C::kQTile + (warp & 3) * (32 * D * 2);
+        if (a.splits > 1) {
+            constexpr int W = D / 2;
+            for (int c0 = 0; c0 < a.dv; c0 += W) {
+#pragma unroll
+                for (int x = 0; x < W; x += 32) {
+                    float o[32];
+                    columns((c0 + x) / 32, o);
+                    stage_cols<float, W>(rows, lane, x, o);
+                }
+                store_rows<float, W>(a.part_o + c0, (rh * a.splits + split) * a.dv, has_row, rows, min(W, a.dv - c0));
+            }
+        } else {
+#pragma unroll
+            for (int x = 0; x < D; x += 32) {
+                float o[32];
+                columns(x / 32, o);
+                stage_cols<T, D>(rows, lane, x, o);
+            }
+            store_rows<T, D>(static_cast<T*>(a.out), rh * a.dv, has_row, rows, a.dv);
         }
         tc_fence_before();
     }
@@ -613,15 +656,15 @@ int box_rows(int page_size) {
     return b < kKeys ? b : kKeys;
 }
 
-// row tiles per CTA: two when the packed rows do not fit one
-int row_tiles(int64_t packed) { return packed > kRows ? 2 : 1; }
+// row tiles per CTA
+int row_tiles(int64_t packed) { return packed > kFewRows ? 2 : 1; }
 
 template <typename T, int D, int kTiles, bool kMods>
 cudaError_t go(const TcArgs& p, const Geom& g, const CUtensorMap& km, const CUtensorMap& vm, int64_t grid,
                cudaStream_t st) {
     using C = Cfg<D, kTiles>;
     constexpr size_t sm = 1024 + (size_t)C::kCtlOff + sizeof(Ctl);
-    static_assert(sm <= 232448, "shared memory");
+    static_assert((sm + 1024) * C::kCtas <= 233472, "shared memory of an SM");
     auto kern = dense_tc_kernel<T, D, kTiles, kMods>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
     if (e != cudaSuccess) return e;
