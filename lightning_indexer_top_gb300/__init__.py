@@ -11,7 +11,6 @@ Build with ``lightning_indexer_top_gb300.build()`` (nvcc, sm_103a).
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -144,8 +143,9 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(device) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+def _stream(device) -> int:
+    """The current stream of a tensor's device (as an address, without the Stream object around it: 2 us less a call)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _dtype(t: torch.Tensor) -> int:
@@ -194,13 +194,14 @@ class Batch:
         return self.n_seq * self.n_q_per_seq
 
     def c(self) -> _Batch:
+        ptrs = []
         for t in (self.n_kv, self.kv_start, self.q_pos, self.page_table):
             if t is not None and (t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous()):
                 raise ValueError("batch arrays must be contiguous int32 CUDA tensors")
+            ptrs.append(None if t is None else t.data_ptr())
         pt_stride = self.page_table.shape[-1] if self.page_table is not None else 0
-        return _Batch(self.n_seq, self.n_q_per_seq, _ptr(self.n_kv), _ptr(self.kv_start),
-                      self.kv_seq_stride, _ptr(self.q_pos), self.max_n_kv, _ptr(self.page_table), pt_stride,
-                      self.page_size if self.page_table is not None else 0)
+        return _Batch(self.n_seq, self.n_q_per_seq, ptrs[0], ptrs[1], self.kv_seq_stride, ptrs[2], self.max_n_kv,
+                      ptrs[3], pt_stride, self.page_size if self.page_table is not None else 0)
 
 
 IDX_DEFAULT_TOP_K = 2048   # top_k = -1: the model's configured indexer top_k
@@ -511,22 +512,32 @@ def sparse_attn_decode_noalloc(q, latent, batch, idx, n_sel, scale, *, out=None,
     return out
 
 
-def _on(device):
-    """Makes `device` current for a call (nothing to do where it is)."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+class _On:
+    """Makes `device` current for a call."""
+
+    def __init__(self, device):
+        self.prev, self.idx = torch.cuda.current_device(), device.index
+
+    def __enter__(self):
+        if self.prev != self.idx:
+            torch.cuda.set_device(self.idx)
+
+    def __exit__(self, *exc):
+        if self.prev != self.idx:
+            torch.cuda.set_device(self.prev)
 
 
-def _same_device(device, *ts):
+def _all_on(device, *ts):
     for t in ts:
         if t is not None and t.device != device:
+            _need_cuda(t)
             raise ValueError(f"tensors on {device} and {t.device}: lidx works on one device per call")
 
 
-def _i32(name: str, t: Optional[torch.Tensor], n: int):
-    if t is not None and (t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < n):
+def _i32(name: str, t: torch.Tensor, n: int):
+    if t.dtype is not torch.int32 or t.numel() < n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor of at least {n} entries")
+    return t.data_ptr()
 
 
 def dense_attn_workspace_size(dtype: torch.dtype, n_seq: int, n_q_per_seq: int, max_n_kv: int, n_q_heads: int,
@@ -550,79 +561,100 @@ def dense_attn(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tensor], batc
     zero), or up to prefix_len[b] where that is further; not before doc_start[r]; with window, at most
     that many positions up to its own.  softcap c > 0: scores x become c * tanh(x / c); slopes (f32 [Hq]):
     minus slopes[h] * |q_pos[r] - j| for key j."""
-    _need_cuda(q, k, v, slopes, prefix_len, doc_start, out, lse, workspace)
-    _same_device(q.device, k, v, slopes, prefix_len, doc_start, out, lse, workspace, batch.n_kv)
-    if q.dim() != 3 or not q.is_contiguous() or q.shape[0] != batch.n_rows:
+    dev = q.device
+    _need_cuda(q)
+    _all_on(dev, k, v, out, lse, workspace, batch.n_kv, batch.q_pos, batch.page_table, batch.kv_start)
+    b = batch.c()
+    rows = b.n_seq * b.n_q_per_seq
+    if q.dim() != 3 or q.shape[0] != rows or not q.is_contiguous():
         raise ValueError("q must be a contiguous [n_seq * n_q_per_seq, heads, dk] tensor")
-    rows, Hq, dk = q.shape
+    _, Hq, dk = q.shape
     if v is None:
         if k.dim() == 3 and k.shape[1] == 1:
             k = k[:, 0]
         if k.dim() != 2 or k.shape[1] < dk or k.stride(1) != 1:
             raise ValueError("the latent cache must be [rows, dk] with contiguous rows")
-        hkv, dv, v_row_stride = 1, (512 if dv is None else dv), 0
+        hkv, dv, v_row_stride, v_ptr = 1, (512 if dv is None else dv), 0, None
     else:
-        if k.dim() != 3 or v.dim() != 3 or k.shape[:2] != v.shape[:2] or k.shape[2] != dk:
+        if k.dim() != 3 or v.dim() != 3:
             raise ValueError("k and v must be [rows, kv heads, dk] and [rows, kv heads, dv]")
-        if dv is not None and dv != v.shape[2]:
+        n, hkv, d = k.shape
+        nv, hkv_v, d_v = v.shape
+        if n != nv or hkv != hkv_v or d != dk:
+            raise ValueError("k and v must be [rows, kv heads, dk] and [rows, kv heads, dv]")
+        if dv is not None and dv != d_v:
             raise ValueError("dv differs from v's last dimension")
-        hkv, dv = k.shape[1], v.shape[2]
-        for t in (k, v):
-            if t.stride(2) != 1 or (hkv > 1 and t.stride(1) != t.shape[2]):
-                raise ValueError("the heads of a cache row must be contiguous")
-        v_row_stride = v.stride(0)
-    if k.dtype != q.dtype or (v is not None and v.dtype != q.dtype):
+        dv = d_v
+        ks, vs = k.stride(), v.stride()
+        if ks[2] != 1 or vs[2] != 1 or (hkv > 1 and (ks[1] != dk or vs[1] != dv)):
+            raise ValueError("the heads of a cache row must be contiguous")
+        # an empty cache has no address; v's tells the latent form apart and is not read
+        v_row_stride, v_ptr = vs[0], v.data_ptr() or q.data_ptr()
+    dt = _dtype(q)
+    if k.dtype is not q.dtype or (v is not None and v.dtype is not q.dtype):
         raise ValueError("q, k and v must have the same dtype")
-    if slopes is not None and (slopes.dtype != torch.float32 or not slopes.is_contiguous() or slopes.numel() != Hq):
-        raise ValueError("slopes must be a contiguous float32 tensor with one entry per query head")
-    _i32("prefix_len", prefix_len, batch.n_seq)
-    _i32("doc_start", doc_start, rows)
+    mods = None
+    if softcap or window or slopes is not None or prefix_len is not None or doc_start is not None:
+        _all_on(dev, slopes, prefix_len, doc_start)
+        if slopes is not None and (slopes.dtype is not torch.float32 or not slopes.is_contiguous() or
+                                   slopes.numel() != Hq):
+            raise ValueError("slopes must be a contiguous float32 tensor with one entry per query head")
+        mods = _Mods(softcap, None if slopes is None else slopes.data_ptr(), window,
+                     None if prefix_len is None else _i32("prefix_len", prefix_len, b.n_seq),
+                     None if doc_start is None else _i32("doc_start", doc_start, rows))
     if out is None:
-        out = torch.empty(rows, Hq, dv, device=q.device, dtype=q.dtype)
-    elif out.shape != (rows, Hq, dv) or out.dtype != q.dtype or not out.is_contiguous():
+        out = torch.empty((rows, Hq, dv), device=dev, dtype=q.dtype)
+    elif out.shape != (rows, Hq, dv) or out.dtype is not q.dtype or not out.is_contiguous():
         raise ValueError("out must be a contiguous [rows, heads, dv] tensor of q's dtype")
-    if lse is not None and (lse.shape != (rows, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous()):
+    if lse is not None and (lse.shape != (rows, Hq) or lse.dtype is not torch.float32 or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 [rows, heads] tensor")
     lib = load()
-    mods = None
-    if softcap or slopes is not None or window or prefix_len is not None or doc_start is not None:
-        mods = ctypes.byref(_Mods(softcap, _ptr(slopes), window, _ptr(prefix_len), _ptr(doc_start)))
-    with _on(q.device):
-        dt = _dtype(q)
+    with _On(dev):
         if workspace is None:
-            need = lib.dense_attn_workspace_size(dt, batch.n_seq, batch.n_q_per_seq, batch.max_n_kv, Hq, hkv, dk, dv)
+            need = lib.dense_attn_workspace_size(dt, b.n_seq, b.n_q_per_seq, b.max_n_kv, Hq, hkv, dk, dv)
             if need:
-                workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        # an empty cache has no address; v's tells the latent form apart and is not read
-        v_ptr = None if v is None else v.data_ptr() or q.data_ptr()
+                workspace = torch.empty(need, device=dev, dtype=torch.uint8)
         _check(lib.dense_attn(q.data_ptr(), dt, Hq, hkv, dk, dv, k.data_ptr(), v_ptr, k.stride(0), v_row_stride, k.shape[0],
-                              batch.c(), mods, scale, out.data_ptr(), _ptr(lse), _ptr(workspace), ws_bytes,
-                              _stream(q.device)))
+                              b, mods, scale, out.data_ptr(), None if lse is None else lse.data_ptr(), *_space(workspace),
+                              _stream(dev)))
     return out
 
 
-def _page_caches(caches, page_size: int):
+def _space(workspace: Optional[torch.Tensor]):
+    """(address, bytes) of a workspace."""
+    return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+
+
+def _page_caches(caches, page_size: int, device):
     """(ctypes array of cache descriptions, pages in each) of caches sharing page numbers."""
-    if not 1 <= len(caches) <= IDX_MAX_PAGE_CACHES:
+    n = len(caches)
+    if not 1 <= n <= IDX_MAX_PAGE_CACHES:
         raise ValueError(f"1 to {IDX_MAX_PAGE_CACHES} caches share a page table")
     if page_size < 1:
         raise ValueError("page_size < 1")
-    arr = (_PageCache * len(caches))()
-    n_pages = caches[0].shape[0] // page_size
-    for i, c in enumerate(caches):
-        if c.dim() < 1 or c.shape[0] // page_size != n_pages:
+    flat = []
+    n_pages = -1
+    for c in caches:
+        if c.device != device:
+            _all_on(device, c)
+        rows, *shape = c.shape
+        stride, *inner = c.stride()
+        if n_pages < 0:
+            n_pages = rows // page_size
+        elif rows // page_size != n_pages:
             raise ValueError("the caches must hold the same number of pages")
-        inner = 1
-        for d in range(c.dim() - 1, 0, -1):
-            if c.shape[d] != 1 and c.stride(d) != inner:
+        width = 1
+        for d, st in zip(reversed(shape), reversed(inner)):
+            if d != 1 and st != width:
                 raise ValueError("the elements of a cache row must be contiguous")
-            inner *= c.shape[d]
-        if c.shape[0] > 1 and c.stride(0) < inner:
-            raise ValueError("the rows of a cache must not overlap")
+            width *= d
+        if stride < width:
+            if rows > 1:
+                raise ValueError("the rows of a cache must not overlap")
+            stride = width
         size = c.element_size()
-        arr[i] = _PageCache(c.data_ptr(), max(c.stride(0), inner) * size, inner * size)
-    return arr, n_pages
+        flat.append((c.data_ptr(), stride * size, width * size))
+    return (_PageCache * n)(*flat), n_pages
 
 
 def idx_page_workspace_size(n_seq: int, n_pages: int) -> int:
@@ -632,29 +664,35 @@ def idx_page_workspace_size(n_seq: int, n_pages: int) -> int:
 def idx_page_copy(caches, page_size: int, src: torch.Tensor, dst: torch.Tensor) -> None:
     """Copies page src[i] to page dst[i] in every cache (tensors whose dim 0 is the cache row), in place.
     The pages of dst must differ from one another and from those of src; entries below 0 are skipped."""
-    _need_cuda(src, dst, *caches)
-    _same_device(src.device, dst, *caches)
-    arr, n_pages = _page_caches(caches, page_size)
-    _i32("src", src, 0)
-    _i32("dst", dst, 0)
-    if src.numel() != dst.numel():
+    dev = src.device
+    _need_cuda(src)
+    _all_on(dev, dst)
+    arr, n_pages = _page_caches(caches, page_size, dev)
+    n = src.numel()
+    if dst.numel() != n:
         raise ValueError("src and dst must have the same length")
-    with _on(src.device):
-        _check(load().idx_page_copy(arr, len(caches), page_size, n_pages, src.data_ptr(), dst.data_ptr(), src.numel(),
-                                    _stream(src.device)))
+    s, d = _i32("src", src, n), _i32("dst", dst, n)
+    with _On(dev):
+        _check(load().idx_page_copy(arr, len(caches), page_size, n_pages, s, d, n,
+                                    _stream(dev)))
 
 
 def _table(name: str, t: torch.Tensor):
-    if t.dim() != 2 or t.dtype != torch.int32 or (t.shape[1] > 1 and t.stride(1) != 1) or \
-            (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+    if t.dim() != 2 or t.dtype is not torch.int32:
         raise ValueError(f"{name} must be an int32 [sequences, pages] tensor with contiguous rows")
-    return max(t.stride(0), t.shape[1])
+    rows, cols = t.shape
+    s0, s1 = t.stride()
+    if (cols > 1 and s1 != 1) or (rows > 1 and s0 < cols):
+        raise ValueError(f"{name} must be an int32 [sequences, pages] tensor with contiguous rows")
+    return t.data_ptr(), max(s0, cols), rows, cols
 
 
 def _held(held, n_pages):
-    if held is not None and (held.dtype not in (torch.uint8, torch.bool) or not held.is_contiguous() or
-                             held.numel() != n_pages):
+    if held is None:
+        return None
+    if held.dtype not in (torch.uint8, torch.bool) or not held.is_contiguous() or held.numel() != n_pages:
         raise ValueError("held must be a contiguous uint8 or bool tensor with one entry per page")
+    return held.data_ptr()
 
 
 def idx_page_update(page_table: torch.Tensor, parent: torch.Tensor, n_keep: torch.Tensor, n_new: torch.Tensor,
@@ -667,34 +705,30 @@ def idx_page_update(page_table: torch.Tensor, parent: torch.Tensor, n_keep: torc
     are the lowest free ones (neither named by a new row nor held).  Returns (new_table, n_free): n_free
     (int32 [1], on the device) is the number of pages left, minus the number missing if there were too few
     (new_table is then not written), or -2**31 if a request was impossible."""
-    _need_cuda(page_table, parent, n_keep, n_new, held, new_table, n_free, workspace, *caches)
-    _same_device(page_table.device, parent, n_keep, n_new, held, new_table, n_free, workspace, *caches)
-    arr, n_pages = _page_caches(caches, page_size)
-    stride = _table("page_table", page_table)
+    dev = page_table.device
+    _need_cuda(page_table)
+    _all_on(dev, parent, n_keep, n_new, held, new_table, n_free, workspace)
+    arr, n_pages = _page_caches(caches, page_size, dev)
+    old, stride, n_old, cols = _table("page_table", page_table)
     n = parent.numel()
-    for name, t in (("parent", parent), ("n_keep", n_keep), ("n_new", n_new)):
-        _i32(name, t, n)
     if n_keep.numel() != n or n_new.numel() != n:
         raise ValueError("parent, n_keep and n_new must have the same length")
-    _held(held, n_pages)
+    par, keep, new = _i32("parent", parent, n), _i32("n_keep", n_keep, n), _i32("n_new", n_new, n)
+    h = _held(held, n_pages)
     if new_table is None:
-        new_table = torch.empty(n, page_table.shape[1], device=page_table.device, dtype=torch.int32)
-    elif new_table.shape[0] != n:
+        new_table = torch.empty((n, cols), device=dev, dtype=torch.int32)
+    out, new_stride, n_rows, new_cols = _table("new_table", new_table)
+    if n_rows != n:
         raise ValueError("new_table must have one row per entry of parent")
-    new_stride = _table("new_table", new_table)
-    _i32("n_free", n_free, 1)
     if n_free is None:
-        n_free = torch.empty(1, device=page_table.device, dtype=torch.int32)
+        n_free = torch.empty(1, device=dev, dtype=torch.int32)
     lib = load()
-    with _on(page_table.device):
+    with _On(dev):
         if workspace is None:
-            workspace = torch.empty(max(lib.idx_page_workspace_size(n, n_pages), 16), device=page_table.device,
-                                    dtype=torch.uint8)
-        _check(lib.idx_page_update(page_table.data_ptr(), stride, page_table.shape[1], page_table.shape[0],
-                                   parent.data_ptr(), n_keep.data_ptr(), n_new.data_ptr(), n, page_size, n_pages,
-                                   _ptr(held), new_table.data_ptr(), new_stride, new_table.shape[1], n_free.data_ptr(),
-                                   arr, len(caches), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                   _stream(page_table.device)))
+            workspace = torch.empty(max(lib.idx_page_workspace_size(n, n_pages), 16), device=dev, dtype=torch.uint8)
+        _check(lib.idx_page_update(old, stride, cols, n_old, par, keep, new, n, page_size, n_pages, h, out, new_stride,
+                                   new_cols, _i32("n_free", n_free, 1), arr, len(caches), *_space(workspace),
+                                   _stream(dev)))
     return new_table, n_free
 
 
@@ -706,35 +740,31 @@ def idx_page_compact(page_table: torch.Tensor, n_len: torch.Tensor, page_size: i
     are) to the lowest numbers, in every cache.  Returns (new_table, n_used, remap): n_used (int32 [1], on
     the device) counts the used and held pages, remap[p] is the new number of page p.  new_table may be
     page_table itself."""
-    _need_cuda(page_table, n_len, held, new_table, n_used, remap, workspace, *caches)
-    _same_device(page_table.device, n_len, held, new_table, n_used, remap, workspace, *caches)
-    arr, n_pages = _page_caches(caches, page_size)
-    stride = _table("page_table", page_table)
-    n = page_table.shape[0]
-    _i32("n_len", n_len, n)
+    dev = page_table.device
+    _need_cuda(page_table)
+    _all_on(dev, n_len, held, new_table, n_used, remap, workspace)
+    arr, n_pages = _page_caches(caches, page_size, dev)
+    old, stride, n, cols = _table("page_table", page_table)
     if n_len.numel() != n:
         raise ValueError("n_len must have one entry per row of page_table")
-    _held(held, n_pages)
-    dev = page_table.device
+    lens = _i32("n_len", n_len, n)
+    h = _held(held, n_pages)
     if new_table is None:
-        new_table = torch.empty(n, page_table.shape[1], device=dev, dtype=torch.int32)
+        new_table = torch.empty((n, cols), device=dev, dtype=torch.int32)
     elif new_table.shape != page_table.shape:
         raise ValueError("new_table must have page_table's shape")
-    new_stride = _table("new_table", new_table)
-    _i32("n_used", n_used, 1)
-    _i32("remap", remap, n_pages)
+    out, new_stride, _, _ = _table("new_table", new_table)
     if n_used is None:
         n_used = torch.empty(1, device=dev, dtype=torch.int32)
     if remap is None:
         remap = torch.empty(n_pages, device=dev, dtype=torch.int32)
     lib = load()
-    with _on(dev):
+    with _On(dev):
         if workspace is None:
             workspace = torch.empty(max(lib.idx_page_workspace_size(n, n_pages), 16), device=dev, dtype=torch.uint8)
-        _check(lib.idx_page_compact(page_table.data_ptr(), stride, page_table.shape[1], n, n_len.data_ptr(), page_size,
-                                    n_pages, _ptr(held), new_table.data_ptr(), new_stride, n_used.data_ptr(),
-                                    remap.data_ptr(), arr, len(caches), workspace.data_ptr(),
-                                    workspace.numel() * workspace.element_size(), _stream(dev)))
+        _check(lib.idx_page_compact(old, stride, cols, n, lens, page_size, n_pages, h, out, new_stride,
+                                    _i32("n_used", n_used, 1), _i32("remap", remap, n_pages), arr, len(caches),
+                                    *_space(workspace), _stream(dev)))
     return new_table, n_used, remap
 
 

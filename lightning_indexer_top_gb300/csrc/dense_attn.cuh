@@ -7,6 +7,8 @@
 
 namespace lidx {
 
+constexpr int kDenseMaxSplits = 128;   // key splits, at most (the merge keeps their weights in a warp)
+
 struct DenseArgs {
     const void* q;
     int32_t Hq, Hkv, dk, dv;

@@ -365,32 +365,78 @@ __global__ void __launch_bounds__(kThreads) dense_generic_kernel(DenseArgs a, Ge
     }
 }
 
-// one warp per (row, head): out = sum_s e^(m_s - M) o_s / sum_s e^(m_s - M) l_s
-template <typename T>
+// one warp per (row, head): out = sum_s e^(m_s - M) o_s / sum_s e^(m_s - M) l_s.  Lane s holds the weights of
+// splits s, s + 32, ...; a lane sums V consecutive columns, the splits' loads issued kBatch at a time.
+template <typename T, int V>
 __global__ void __launch_bounds__(128) dense_combine_kernel(DenseArgs a, int64_t n) {
+    constexpr int kSplits = kDenseMaxSplits / 32, kBatch = 8;
     pdl_trigger();
     pdl_wait();
     const int64_t rh = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (rh >= n) return;
     const float* ml = a.part_ml + rh * a.splits * 2;
-    float M = -INFINITY;
-    for (int s = lane; s < a.splits; s += 32)
-        if (ml[2 * s + 1] != 0.f) M = fmaxf(M, ml[2 * s]);
+    float m[kSplits], l[kSplits], M = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kSplits; ++i) {
+        const int s = lane + 32 * i;
+        m[i] = s < a.splits ? ml[2 * s] : 0.f;
+        l[i] = s < a.splits ? ml[2 * s + 1] : 0.f;
+        if (l[i] != 0.f) M = fmaxf(M, m[i]);      // (a split without keys has l = 0; a NaN counts)
+    }
 #pragma unroll
     for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
     float den = 0.f;
-    for (int s = lane; s < a.splits; s += 32)
-        if (ml[2 * s + 1] != 0.f) den += expf(ml[2 * s] - M) * ml[2 * s + 1];
+#pragma unroll
+    for (int i = 0; i < kSplits; ++i) {
+        m[i] = l[i] != 0.f ? expf(m[i] - M) : 0.f;
+        den += m[i] * l[i];
+    }
 #pragma unroll
     for (int off = 16; off; off >>= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
     if (a.lse && lane == 0) a.lse[rh] = den == 0.f ? -INFINITY : M + logf(den);
-    const float inv = 1.f / den;
-    for (int c = lane; c < a.dv; c += 32) {
-        float acc = 0.f;
-        for (int s = 0; s < a.splits; ++s)
-            if (ml[2 * s + 1] != 0.f) acc += expf(ml[2 * s] - M) * a.part_o[(rh * a.splits + s) * a.dv + c];
-        static_cast<T*>(a.out)[rh * a.dv + c] = from_f32<T>(den == 0.f ? 0.f : acc * inv);
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    for (int c0 = 0; c0 < a.dv; c0 += 32 * V) {
+        const int c = c0 + lane * V;
+        float acc[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = 0.f;
+#pragma unroll
+        for (int i = 0; i < kSplits; ++i) {
+            for (int s0 = 0; s0 < 32 && 32 * i + s0 < a.splits; s0 += kBatch) {
+                float x[kBatch][V];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) x[k][v] = 0.f;
+                    const int s = 32 * i + s0 + k;
+                    if (s < a.splits && c < a.dv) {
+                        const float* p = a.part_o + (rh * a.splits + s) * a.dv + c;
+                        if constexpr (V == 4) {
+                            const float4 y = *reinterpret_cast<const float4*>(p);
+                            x[k][0] = y.x;
+                            x[k][1] = y.y;
+                            x[k][2] = y.z;
+                            x[k][3] = y.w;
+                        } else {
+                            x[k][0] = *p;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const float w = __shfl_sync(0xffffffffu, m[i], s0 + k);
+                    // (a split without keys wrote zeros)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) acc[v] = fmaf(w, x[k][v], acc[v]);
+                }
+            }
+        }
+        if (c < a.dv) {
+            T* o = static_cast<T*>(a.out) + rh * a.dv + c;
+#pragma unroll
+            for (int v = 0; v < V; ++v) o[v] = from_f32<T>(acc[v] * inv);
+        }
     }
 }
 
@@ -421,7 +467,8 @@ cudaError_t run(const DenseArgs& a, const Geom& g, cudaStream_t st) {
 
 }  // namespace
 
-// enough CTAs to cover the SMs four times, at least 128 keys per split
+// enough CTAs to cover the SMs four times, at least a tile of keys each: a tile takes about 4 us whatever it holds
+// (256 keys for one token of four f32 heads: 24 us in two splits, XX in eight)
 int dense_generic_splits(int64_t n_seq, int64_t n_q, int64_t max_n_kv, int Hq, int Hkv, int dk, int dv) {
     (void)dk;
     const int64_t packed = n_q * (Hq / Hkv);
@@ -431,9 +478,9 @@ int dense_generic_splits(int64_t n_seq, int64_t n_q, int64_t max_n_kv, int Hq, i
     if (sms < 2) sms = 152;
     if (units < 1) return 1;
     int64_t s = 4 * (int64_t)sms / units;
-    const int64_t by_keys = (max_n_kv + 127) / 128;
+    const int64_t by_keys = (max_n_kv + kKeys - 1) / kKeys;
     if (s > by_keys) s = by_keys;
-    if (s > 128) s = 128;
+    if (s > kDenseMaxSplits) s = kDenseMaxSplits;
     return s < 1 ? 1 : (int)s;
 }
 
@@ -445,13 +492,19 @@ cudaError_t launch_dense_generic(const DenseArgs& a, int dtype, const Geom& g, c
     }
 }
 
+template <typename T>
+static cudaError_t combine(const DenseArgs& a, int64_t n, cudaStream_t st) {
+    const dim3 grid((unsigned)((n + 3) / 4));
+    return a.dv % 4 == 0 ? launch_pdl(dense_combine_kernel<T, 4>, grid, dim3(128), 0, st, a, n)
+                         : launch_pdl(dense_combine_kernel<T, 1>, grid, dim3(128), 0, st, a, n);
+}
+
 cudaError_t launch_dense_combine(const DenseArgs& a, int dtype, int64_t n_rows, cudaStream_t st) {
     const int64_t n = n_rows * a.Hq;
-    const dim3 grid((unsigned)((n + 3) / 4));
     switch (dtype) {
-        case IDX_F16: return launch_pdl(dense_combine_kernel<__half>, grid, dim3(128), 0, st, a, n);
-        case IDX_BF16: return launch_pdl(dense_combine_kernel<__nv_bfloat16>, grid, dim3(128), 0, st, a, n);
-        default: return launch_pdl(dense_combine_kernel<float>, grid, dim3(128), 0, st, a, n);
+        case IDX_F16: return combine<__half>(a, n, st);
+        case IDX_BF16: return combine<__nv_bfloat16>(a, n, st);
+        default: return combine<float>(a, n, st);
     }
 }
 

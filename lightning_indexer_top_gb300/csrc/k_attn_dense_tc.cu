@@ -718,7 +718,7 @@ int dense_tc_splits(int64_t n_seq, int64_t n_q, int64_t max_n_kv, int Hq, int Hk
     int64_t s = 2 * (int64_t)sms / units;
     const int64_t by_keys = (max_n_kv + 511) / 512;
     if (s > by_keys) s = by_keys;
-    if (s > 128) s = 128;
+    if (s > kDenseMaxSplits) s = kDenseMaxSplits;
     return s < 1 ? 1 : (int)s;
 }
 

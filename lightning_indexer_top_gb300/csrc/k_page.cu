@@ -4,9 +4,10 @@
 // A page is owned by the table rows that name it, so the plan of an update or a
 // compaction starts from a bitmap of the named pages; ranks in the bitmap (a
 // prefix sum of its words' zero counts) give the k-th free page, so the result
-// depends on nothing but the inputs.  The plan runs on one CTA; the page
+// depends on nothing but the inputs.  The plan runs on one cluster; the page
 // contents then move in a second launch over all SMs.
 #include "lidx_internal.cuh"
+#include "sm100_ptx.cuh"
 
 namespace lidx {
 namespace {
@@ -86,11 +87,34 @@ __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(Caches cs, Move
     }
 }
 
-// ---------------------------------------------------------------- the plan's pieces (one CTA)
+// ---------------------------------------------------------------- the plan: one cluster of kCl CTAs
+//
+// Each CTA holds a slice of the bitmap in shared memory (in the workspace when it
+// is too long), marks pages in all of them, and walks its share of the rows.  A
+// step ends with a cluster barrier, whose release and acquire also cover the
+// global arrays.  (One CTA with the bitmap in global memory took 50 us for 256
+// rows of 256 pages, and 248 us to plan a compaction of 32768 pages.)
+constexpr int kCl = 8;
+constexpr int kWarps = kPlanThreads / 32;
+constexpr int kSliceWords = 48 * 1024;     // words of a slice that fit shared memory
+
+struct Plan {
+    int cnt[4][kCl];       // counts that the CTAs tell one another
+    int scan[32];
+};
+
+__device__ __forceinline__ uint32_t cta_rank() { return sm100::cluster_ctarank(); }
+
+// the same variable of CTA `rank`, as a generic address
+template <typename T>
+__device__ __forceinline__ T* of_cta(T* p, uint32_t rank) {
+    uint64_t r;
+    asm volatile("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
+    return reinterpret_cast<T*>(r);
+}
 
 // the exclusive prefix sum of x over the CTA's threads; *total gets the sum
-__device__ __forceinline__ int block_scan(int x, int* total) {
-    __shared__ int part[32];
+__device__ __forceinline__ int block_scan(Plan& s, int x, int* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int inc = x;
 #pragma unroll
@@ -98,38 +122,87 @@ __device__ __forceinline__ int block_scan(int x, int* total) {
         const int y = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += y;
     }
-    __syncthreads();   // part of the last call has been read
-    if (lane == 31) part[warp] = inc;
+    __syncthreads();   // the last call's sums have been read
+    if (lane == 31) s.scan[warp] = inc;
     __syncthreads();
-    if (warp == 0) {
-        int v = part[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v += y;
-        }
-        part[lane] = v;
+    int before = 0, all = 0;
+    const int v = lane < kWarps ? s.scan[lane] : 0;
+    before = lane < warp ? v : 0;
+    all = v;
+    before = __reduce_add_sync(0xffffffffu, before);
+    all = __reduce_add_sync(0xffffffffu, all);
+    *total = all;
+    return inc - x + before;
+}
+
+// tells every CTA x of this one in cnt[k]; after the next cluster barrier, the sum before this CTA and in all
+__device__ __forceinline__ void tell(Plan& s, int k, int x) {
+    if (threadIdx.x < kCl) of_cta(&s.cnt[k][0], threadIdx.x)[cta_rank()] = x;
+}
+__device__ __forceinline__ int told(const Plan& s, int k, int* total) {
+    int before = 0, all = 0;
+    for (int i = 0; i < kCl; ++i) {
+        if (i < (int)cta_rank()) before += s.cnt[k][i];
+        all += s.cnt[k][i];
     }
-    __syncthreads();
-    *total = part[31];
-    return inc - x + (warp ? part[warp - 1] : 0);
+    *total = all;
+    return before;
+}
+
+// the bitmap of the pages: word w is word w - rank * slice of CTA w / slice
+struct Bitmap {
+    uint32_t* mine;        // this CTA's slice
+    uint32_t* global;      // the whole bitmap in the workspace, or NULL: slices in shared memory
+    int slice;             // words per slice
+    int words;
+
+    __device__ __forceinline__ uint32_t* word(int w) const {
+        return global ? global + w : of_cta(mine, (uint32_t)(w / slice)) + w % slice;
+    }
+    __device__ __forceinline__ void set(int32_t p) const { atomicOr(word(p >> 5), 1u << (p & 31)); }
+    __device__ __forceinline__ bool get(int32_t p) const {
+        return (*(volatile uint32_t*)word(p >> 5) >> (p & 31)) & 1u;
+    }
+    // words of this CTA's slice
+    __device__ __forceinline__ int n_mine() const {
+        const int left = words - (int)cta_rank() * slice;
+        return left < 0 ? 0 : left < slice ? left : slice;
+    }
+};
+
+__device__ __forceinline__ Bitmap make_bitmap(uint32_t* ws, uint32_t* smem, int32_t n_pages) {
+    Bitmap m;
+    m.words = (int)(((int64_t)n_pages + 31) / 32);
+    m.slice = (m.words + kCl - 1) / kCl;
+    if (m.slice < 1) m.slice = 1;
+    m.global = m.slice > kSliceWords ? ws : nullptr;
+    m.mine = m.global ? ws + (int64_t)cta_rank() * m.slice : smem;
+    return m;
 }
 
 // bits of word w that are pages (the last word may be short)
-__device__ __forceinline__ uint32_t page_bits(int w, int32_t n_pages) {
-    const int64_t left = (int64_t)n_pages - (int64_t)w * 32;
-    return left >= 32 ? 0xffffffffu : (1u << left) - 1u;
+__device__ __forceinline__ uint32_t page_bits(int64_t w, int32_t n_pages) {
+    const int64_t left = (int64_t)n_pages - w * 32;
+    return left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
 }
 
-__device__ __forceinline__ uint32_t held_bits(const uint8_t* held, int w, int32_t n_pages) {
+// bits of word w that are below n
+__device__ __forceinline__ uint32_t low_bits(int64_t w, int32_t n) { return page_bits(w, n); }
+
+__device__ __forceinline__ uint32_t held_bits(const uint8_t* held, int64_t w, int32_t n_pages) {
     if (!held) return 0u;
     uint32_t x = 0u;
-    const int64_t p0 = (int64_t)w * 32;
-    for (int i = 0; i < 32 && p0 + i < n_pages; ++i) x |= (held[p0 + i] ? 1u : 0u) << i;
+    const int64_t p0 = w * 32;
+    if (p0 + 32 <= n_pages && !(reinterpret_cast<uintptr_t>(held) & 15u)) {
+        const uint4 a = reinterpret_cast<const uint4*>(held + p0)[0], b = reinterpret_cast<const uint4*>(held + p0)[1];
+        const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x |= ((v[i >> 2] >> (8 * (i & 3))) & 0xffu ? 1u : 0u) << i;
+    } else {
+        for (int i = 0; i < 32 && p0 + i < n_pages; ++i) x |= (held[p0 + i] ? 1u : 0u) << i;
+    }
     return x;
 }
-
-__device__ __forceinline__ bool bit(const uint32_t* bm, int32_t p) { return (bm[p >> 5] >> (p & 31)) & 1u; }
 
 struct UpdateArgs {
     const int32_t* table;
@@ -143,72 +216,102 @@ struct UpdateArgs {
     int32_t out_cols;
     int32_t* n_free;
     uint32_t* bm;          // [words]
-    int32_t* list;         // [n_pages] free pages in order
+    int32_t* list;         // [n_pages] who wants a page kept in part, then the free pages in order
     int32_t* offset;       // [n_seq] first new page of the row in the list
-    int32_t *src, *dst, *rows;   // [n_seq] the copies (-1: none)
+    int32_t *src, *dst, *rows;   // [n_seq] the copies (src -1: none)
     int* status;
 };
 
-__global__ void __launch_bounds__(kPlanThreads) page_update_kernel(UpdateArgs a) {
-    const int words = (int)(((int64_t)a.n_pages + 31) / 32);
-    const int tid = threadIdx.x;
+// calls f(entry, index) for the first n entries of a row, the lanes of a warp together
+template <typename F>
+__device__ __forceinline__ void each_entry(const int32_t* row, int n, F f) {
+    constexpr int kBatch = 8;
+    const int lane = threadIdx.x & 31;
+    for (int i0 = lane; i0 < n; i0 += 32 * kBatch) {
+        int32_t v[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) v[k] = i0 + 32 * k < n ? row[i0 + 32 * k] : 0;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (i0 + 32 * k < n) f(v[k], i0 + 32 * k);
+    }
+}
+
+__global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kPlanThreads) page_update_kernel(UpdateArgs a) {
+    extern __shared__ uint32_t slice_s[];
+    __shared__ Plan s;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rank = (int)cta_rank();
+    const Bitmap bm = make_bitmap(a.bm, slice_s, a.n_pages);
+    const int gtid = rank * kPlanThreads + tid;            // of the cluster: rows are dealt out by thread ...
+    const int gwarp = rank * kWarps + warp;                // ... or by warp
+    constexpr int kAll = kCl * kPlanThreads, kAllWarps = kCl * kWarps;
     pdl_trigger();
     pdl_wait();
-    // nothing moves unless the plan says so
-    for (int b = tid; b < a.n_seq; b += kPlanThreads) a.src[b] = a.dst[b] = -1;
-    // ---- the requests
+    // ---- the requests; the held pages.  Nothing is copied unless the plan says so.
     bool bad = false;
-    for (int b = tid; b < a.n_seq; b += kPlanThreads) {
+    for (int b = gtid; b < a.n_seq; b += kAll) {
         const int32_t p = a.parent[b], k = a.keep[b], n = a.len[b];
         bad |= p < -1 || p >= a.n_old || k < 0 || n < k || (p < 0 && k > 0) ||
                (int64_t)k > (int64_t)a.cols * a.ps || (int64_t)n > (int64_t)a.out_cols * a.ps;
+        a.src[b] = -1;
     }
-    if (__syncthreads_or(bad)) {
-        if (tid == 0) {
+    for (int w = tid; w < bm.n_mine(); w += kPlanThreads)
+        bm.mine[w] = held_bits(a.held, (int64_t)rank * bm.slice + w, a.n_pages);
+    bad = __syncthreads_or(bad);
+    tell(s, 0, bad ? 1 : 0);
+    sm100::cluster_sync();
+    int any;
+    told(s, 0, &any);
+    auto impossible = [&] {
+        for (int b = gtid; b < a.n_seq; b += kAll) a.src[b] = -1;
+        if (gtid == 0) {
             *a.n_free = INT32_MIN;
             flag(a.status, IDX_ERR_DEVICE_BOUNDS);
         }
+    };
+    if (any) {
+        impossible();
         return;
     }
-    // ---- pages kept whole (and the held ones)
-    for (int w = tid; w < words; w += kPlanThreads) a.bm[w] = held_bits(a.held, w, a.n_pages);
-    __syncthreads();
-    const int warp = tid >> 5, lane = tid & 31;
-    for (int b = warp; b < a.n_seq; b += kPlanThreads / 32) {
+    // ---- pages kept whole
+    for (int b = gwarp; b < a.n_seq; b += kAllWarps) {
         const int whole = a.keep[b] / a.ps, part = a.keep[b] % a.ps;
         const int n = whole + (part ? 1 : 0);
-        const int32_t* row = a.table + (int64_t)(n ? a.parent[b] : 0) * a.stride;
-        for (int i = lane; i < n; i += 32) {
-            const int32_t p = row[i];
+        if (n == 0) continue;
+        each_entry(a.table + (int64_t)a.parent[b] * a.stride, n, [&](int32_t p, int i) {
             if (p < 0 || p >= a.n_pages)
                 bad = true;
             else if (i < whole)
-                atomicOr(a.bm + (p >> 5), 1u << (p & 31));
-            else
+                bm.set(p);
+            else {
                 a.src[b] = p;
-        }
+                a.list[p] = INT32_MAX;      // wanted by nobody yet (the same value from every row that names it)
+            }
+        });
     }
-    if (__syncthreads_or(bad)) {
-        for (int b = tid; b < a.n_seq; b += kPlanThreads) a.src[b] = -1;
-        if (tid == 0) {
-            *a.n_free = INT32_MIN;
-            flag(a.status, IDX_ERR_DEVICE_BOUNDS);
-        }
+    bad = __syncthreads_or(bad);
+    tell(s, 1, bad ? 1 : 0);
+    sm100::cluster_sync();
+    told(s, 1, &any);
+    if (any) {
+        impossible();
         return;
     }
     // ---- the pages kept in part: the first row that wants one has it, unless it is kept whole or held
-    for (int b = tid; b < a.n_seq; b += kPlanThreads) {
+    for (int b = gtid; b < a.n_seq; b += kAll) {
         const int32_t p = a.src[b];
-        bool stays = p >= 0 && !bit(a.bm, p);
-        for (int o = 0; stays && o < b; ++o) stays = a.src[o] != p;
+        if (p >= 0 && !bm.get(p)) atomicMin(a.list + p, b);
+    }
+    sm100::cluster_sync();
+    for (int b = gtid; b < a.n_seq; b += kAll) {
+        const int32_t p = a.src[b];
+        const bool stays = p >= 0 && *(volatile int32_t*)(a.list + p) == b;
         a.rows[b] = p < 0 || stays ? 0 : a.keep[b] % a.ps;   // rows to copy
     }
-    __syncthreads();
-    for (int b = tid; b < a.n_seq; b += kPlanThreads) {
-        const int32_t p = a.src[b];
-        if (p >= 0 && a.rows[b] == 0) atomicOr(a.bm + (p >> 5), 1u << (p & 31));
-    }
-    // ---- new pages of each row, in order
+    sm100::cluster_sync();      // (every bit has been read)
+    for (int b = gtid; b < a.n_seq; b += kAll)
+        if (a.src[b] >= 0 && a.rows[b] == 0) bm.set(a.src[b]);
+    // ---- new pages of each row, in order (every CTA adds up all of them)
     int need = 0;
     for (int b0 = 0; b0 < a.n_seq; b0 += kPlanThreads) {
         const int b = b0 + tid;
@@ -218,42 +321,53 @@ __global__ void __launch_bounds__(kPlanThreads) page_update_kernel(UpdateArgs a)
             x = pages - a.keep[b] / a.ps - (a.src[b] >= 0 && a.rows[b] == 0 ? 1 : 0);
         }
         int total;
-        const int at = block_scan(x, &total);
-        if (b < a.n_seq) a.offset[b] = need + at;
+        const int at = block_scan(s, x, &total);
+        if (b < a.n_seq && b % kAllWarps / kWarps == rank) a.offset[b] = need + at;   // (its own rows)
         need += total;
     }
+    sm100::cluster_sync();
     // ---- the free pages, in order, as many as are needed
-    __syncthreads();
-    int n_free = 0;
-    for (int w0 = 0; w0 < words; w0 += kPlanThreads) {
-        const int w = w0 + tid;
-        uint32_t z = w < words ? ~a.bm[w] & page_bits(w, a.n_pages) : 0u;
-        int total;
-        int at = n_free + block_scan(__popc(z), &total);
-        for (; z && at < need; z &= z - 1, ++at) a.list[at] = w * 32 + __ffs((int)z) - 1;
-        n_free += total;
-    }
-    if (tid == 0) *a.n_free = n_free - need;
+    int zeros = 0;
+    for (int w = tid; w < bm.n_mine(); w += kPlanThreads)
+        zeros += __popc(~bm.mine[w] & page_bits((int64_t)rank * bm.slice + w, a.n_pages));
+    int mine;
+    block_scan(s, zeros, &mine);
+    tell(s, 2, mine);
+    sm100::cluster_sync();
+    int n_free;
+    int at0 = told(s, 2, &n_free);
+    if (gtid == 0) *a.n_free = n_free - need;
     if (n_free < need) {
-        for (int b = tid; b < a.n_seq; b += kPlanThreads) a.src[b] = -1;
+        for (int b = gtid; b < a.n_seq; b += kAll) a.src[b] = -1;
         return;
     }
-    __syncthreads();
+    for (int w0 = 0; w0 < bm.n_mine() && at0 < need; w0 += kPlanThreads) {
+        const int w = w0 + tid;
+        const int64_t gw = (int64_t)rank * bm.slice + w;
+        uint32_t z = w < bm.n_mine() ? ~bm.mine[w] & page_bits(gw, a.n_pages) : 0u;
+        int total;
+        int at = at0 + block_scan(s, __popc(z), &total);
+        for (; z && at < need; z &= z - 1, ++at) a.list[at] = (int32_t)(gw * 32) + __ffs((int)z) - 1;
+        at0 += total;
+    }
+    sm100::cluster_sync();
     // ---- the new rows
-    for (int b = warp; b < a.n_seq; b += kPlanThreads / 32) {
+    for (int b = gwarp; b < a.n_seq; b += kAllWarps) {
         const int whole = a.keep[b] / a.ps;
         const int pages = (int)(((int64_t)a.len[b] + a.ps - 1) / a.ps);
-        const bool stays = a.src[b] >= 0 && a.rows[b] == 0;
+        const int32_t last = a.src[b];
+        const bool stays = last >= 0 && a.rows[b] == 0;
         const int kept = whole + (stays ? 1 : 0);
         const int32_t* row = a.table + (int64_t)(kept ? a.parent[b] : 0) * a.stride;
         const int32_t* list = a.list + a.offset[b] - kept;
         int32_t* out = a.out + (int64_t)b * a.out_stride;
-        for (int i = lane; i < a.out_cols; i += 32) out[i] = i < kept ? row[i] : i < pages ? list[i] : -1;
+        each_entry(row, kept, [&](int32_t p, int i) { out[i] = p; });
+        for (int i = kept + lane; i < a.out_cols; i += 32) out[i] = i < pages ? list[i] : -1;
         __syncwarp();
         if (lane == 0) {
             if (stays)
                 a.src[b] = -1;
-            else if (a.src[b] >= 0)
+            else if (last >= 0)
                 a.dst[b] = list[whole];
         }
     }
@@ -270,7 +384,6 @@ struct CompactArgs {
     int64_t out_stride;
     int32_t *n_used, *remap;
     uint32_t* bm;       // [words] used or held
-    int32_t* rank;      // [words] moving pages before the word
     int32_t *src, *dst; // [n_pages / 2 + 1] the moves
     int32_t* n_moves;
     int* status;
@@ -286,80 +399,110 @@ __device__ __forceinline__ int live_pages(const CompactArgs& a, int b) {
     return (int)((n + a.ps - 1) / a.ps);
 }
 
-__global__ void __launch_bounds__(kPlanThreads) page_compact_kernel(CompactArgs a) {
-    const int words = (int)(((int64_t)a.n_pages + 31) / 32);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+__global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kPlanThreads) page_compact_kernel(CompactArgs a) {
+    extern __shared__ uint32_t slice_s[];
+    __shared__ Plan s;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rank = (int)cta_rank();
+    const Bitmap bm = make_bitmap(a.bm, slice_s, a.n_pages);
+    const int gwarp = rank * kWarps + warp;
+    constexpr int kAllWarps = kCl * kWarps;
+    const int64_t w_base = (int64_t)rank * bm.slice;
     pdl_trigger();
     pdl_wait();
-    for (int w = tid; w < words; w += kPlanThreads) a.bm[w] = held_bits(a.held, w, a.n_pages);
-    __syncthreads();
-    for (int b = warp; b < a.n_seq; b += kPlanThreads / 32) {
-        const int n = live_pages(a, b);
-        for (int i = lane; i < n; i += 32) {
-            const int32_t p = a.table[(int64_t)b * a.stride + i];
+    for (int w = tid; w < bm.n_mine(); w += kPlanThreads) bm.mine[w] = held_bits(a.held, w_base + w, a.n_pages);
+    sm100::cluster_sync();
+    for (int b = gwarp; b < a.n_seq; b += kAllWarps)
+        each_entry(a.table + (int64_t)b * a.stride, live_pages(a, b), [&](int32_t p, int) {
             if (p >= 0 && p < a.n_pages)
-                atomicOr(a.bm + (p >> 5), 1u << (p & 31));
+                bm.set(p);
             else
                 flag(a.status, IDX_ERR_DEVICE_BOUNDS);
-        }
-    }
-    __syncthreads();
-    int n_used = 0;
-    for (int w0 = 0; w0 < words; w0 += kPlanThreads) {
-        int total;
-        block_scan(w0 + tid < words ? __popc(a.bm[w0 + tid]) : 0, &total);
-        n_used += total;
-    }
+        });
+    sm100::cluster_sync();
+    int x = 0, total;
+    for (int w = tid; w < bm.n_mine(); w += kPlanThreads) x += __popc(bm.mine[w]);
+    block_scan(s, x, &total);
+    tell(s, 0, total);
+    sm100::cluster_sync();
+    int n_used;
+    told(s, 0, &n_used);
     // the moving pages (used, not held, numbered n_used or higher) and the free numbers below, in order
-    int n_moves = 0, n_holes = 0;
-    for (int w0 = 0; w0 < words; w0 += kPlanThreads) {
-        const int w = w0 + tid;
-        uint32_t mv = 0u, ho = 0u;
-        if (w < words) {
-            const int64_t below = (int64_t)n_used - (int64_t)w * 32;
-            const uint32_t low = below >= 32 ? 0xffffffffu : below <= 0 ? 0u : (1u << below) - 1u;
-            mv = a.bm[w] & ~held_bits(a.held, w, a.n_pages) & ~low;
-            ho = ~a.bm[w] & low;
-        }
-        int total;
-        int at = n_moves + block_scan(__popc(mv), &total);
-        if (w < words) a.rank[w] = at;
-        for (; mv; mv &= mv - 1, ++at) a.src[at] = w * 32 + __ffs((int)mv) - 1;
-        n_moves += total;
-        at = n_holes + block_scan(__popc(ho), &total);
-        for (; ho; ho &= ho - 1, ++at) a.dst[at] = w * 32 + __ffs((int)ho) - 1;
-        n_holes += total;
+    auto moving = [&](int w) {
+        const int64_t gw = w_base + w;
+        return bm.mine[w] & ~held_bits(a.held, gw, a.n_pages) & ~low_bits(gw, n_used);
+    };
+    auto holes = [&](int w) { return ~bm.mine[w] & low_bits(w_base + w, n_used); };
+    int y = 0;
+    x = 0;
+    for (int w = tid; w < bm.n_mine(); w += kPlanThreads) {
+        x += __popc(moving(w));
+        y += __popc(holes(w));
     }
-    if (tid == 0) {
+    block_scan(s, x, &total);
+    tell(s, 1, total);
+    block_scan(s, y, &total);
+    tell(s, 2, total);
+    sm100::cluster_sync();
+    int n_moves, n_holes;
+    const int mv0 = told(s, 1, &n_moves);
+    int ho0 = told(s, 2, &n_holes);
+    int at0 = mv0;
+    for (int w0 = 0; w0 < bm.n_mine(); w0 += kPlanThreads) {
+        const int w = w0 + tid;
+        const bool in = w < bm.n_mine();
+        uint32_t m = in ? moving(w) : 0u;
+        int at = at0 + block_scan(s, __popc(m), &total);
+        at0 += total;
+        for (; m; m &= m - 1, ++at) a.src[at] = (int32_t)((w_base + w) * 32) + __ffs((int)m) - 1;
+        m = in ? holes(w) : 0u;
+        at = ho0 + block_scan(s, __popc(m), &total);
+        ho0 += total;
+        for (; m; m &= m - 1, ++at) a.dst[at] = (int32_t)((w_base + w) * 32) + __ffs((int)m) - 1;
+    }
+    if (rank == 0 && tid == 0) {
         *a.n_used = n_used;
         *a.n_moves = n_moves;
     }
-    __syncthreads();
-    // rank of a moving page: those before its word, and those before it in the word
-    auto renumber = [&](int32_t p) -> int32_t {
-        if (p < n_used || !bit(a.bm, p) || (a.held && a.held[p])) return p;
-        const int w = p >> 5;
-        const int64_t below = (int64_t)n_used - (int64_t)w * 32;
-        const uint32_t low = below <= 0 ? 0u : (1u << below) - 1u;
-        const uint32_t mv = a.bm[w] & ~held_bits(a.held, w, a.n_pages) & ~low;
-        return a.dst[a.rank[w] + __popc(mv & ((1u << (p & 31)) - 1u))];
-    };
-    for (int b = warp; b < a.n_seq; b += kPlanThreads / 32) {
-        const int n = live_pages(a, b);
-        for (int i = lane; i < a.cols; i += 32) {
-            int32_t p = -1;
-            if (i < n) {
-                p = a.table[(int64_t)b * a.stride + i];
-                p = p >= 0 && p < a.n_pages ? renumber(p) : -1;
-            }
-            a.out[(int64_t)b * a.out_stride + i] = p;
-        }
+    sm100::cluster_sync();
+    // the new number of every page of the slice
+    at0 = mv0;
+    for (int w0 = 0; w0 < bm.n_mine(); w0 += kPlanThreads) {
+        const int w = w0 + tid;
+        const uint32_t m = w < bm.n_mine() ? moving(w) : 0u;
+        const int at = at0 + block_scan(s, __popc(m), &total);
+        at0 += total;
+        const int64_t p0 = (w_base + w) * 32;
+        if (w < bm.n_mine())
+            for (int i = 0; i < 32 && p0 + i < a.n_pages; ++i)
+                a.remap[p0 + i] = (m >> i) & 1u ? a.dst[at + __popc(m & ((1u << i) - 1u))] : (int32_t)(p0 + i);
     }
-    if (a.remap)
-        for (int32_t p = tid; p < a.n_pages; p += kPlanThreads) a.remap[p] = renumber(p);
+    sm100::cluster_sync();
+    for (int b = gwarp; b < a.n_seq; b += kAllWarps) {
+        const int n = live_pages(a, b);
+        int32_t* out = a.out + (int64_t)b * a.out_stride;
+        each_entry(a.table + (int64_t)b * a.stride, n, [&](int32_t p, int i) {
+            out[i] = p >= 0 && p < a.n_pages ? *(volatile int32_t*)(a.remap + p) : -1;
+        });
+        for (int i = n + lane; i < a.cols; i += 32) out[i] = -1;
+    }
 }
 
 size_t align16(size_t x) { return (x + 15) & ~size_t(15); }
+
+size_t bitmap_bytes(int64_t n_pages) {
+    const size_t slice = ((size_t)(n_pages + 31) / 32 + kCl - 1) / kCl;
+    return align16((slice ? slice : 1) * kCl * 4);
+}
+
+// launches a plan: the bitmap's slices in shared memory where they fit
+template <typename Args>
+cudaError_t launch_plan(void (*kern)(Args), const Args& a, int32_t n_pages, cudaStream_t st) {
+    const size_t slice = bitmap_bytes(n_pages) / kCl;
+    const size_t sm = slice <= (size_t)kSliceWords * 4 ? slice : 0;
+    cudaError_t e = cudaSuccess;
+    if (sm > 32 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+    return e != cudaSuccess ? e : launch_pdl(kern, dim3(kCl), dim3(kPlanThreads), sm, st, a);
+}
 
 bool make_caches(Caches* out, const idx_page_cache* caches, int n, int page_size) {
     *out = {};
@@ -389,11 +532,10 @@ cudaError_t copy_pages(const Caches& cs, const Moves& m, int64_t most, int32_t n
 }  // namespace
 
 size_t page_workspace_bytes(int64_t n_seq, int64_t n_pages) {
-    const size_t words = (size_t)(n_pages + 31) / 32;
-    // bitmap, then the update's free list and per-row arrays, or the compaction's ranks and moves
+    // bitmap (whole slices), then the update's free list and per-row arrays, or the compaction's moves and numbers
     const size_t update = align16((size_t)n_pages * 4) + 4 * align16((size_t)n_seq * 4);
-    const size_t compact = align16(words * 4) + 2 * align16(((size_t)n_pages / 2 + 1) * 4) + 16;
-    return align16(words * 4) + (update > compact ? update : compact);
+    const size_t compact = align16((size_t)n_pages * 4) + 2 * align16(((size_t)n_pages / 2 + 1) * 4) + 16;
+    return bitmap_bytes(n_pages) + (update > compact ? update : compact);
 }
 
 bool page_caches_fit(const idx_page_cache* caches, int n, int page_size) {
@@ -423,14 +565,14 @@ cudaError_t launch_page_update(const int32_t* table, int64_t stride, int32_t col
     };
     UpdateArgs a = {table, stride, cols, n_old, parent, keep, len, n_seq, ps, n_pages, held, out, out_stride, out_cols,
                     n_free};
-    a.bm = static_cast<uint32_t*>(take(((size_t)n_pages + 31) / 32 * 4));
+    a.bm = static_cast<uint32_t*>(take(bitmap_bytes(n_pages)));
     a.list = static_cast<int32_t*>(take((size_t)n_pages * 4));
     a.offset = static_cast<int32_t*>(take((size_t)n_seq * 4));
     a.src = static_cast<int32_t*>(take((size_t)n_seq * 4));
     a.dst = static_cast<int32_t*>(take((size_t)n_seq * 4));
     a.rows = static_cast<int32_t*>(take((size_t)n_seq * 4));
     a.status = device_status_ptr();
-    cudaError_t e = launch_pdl(page_update_kernel, dim3(1), dim3(kPlanThreads), 0, st, a);
+    const cudaError_t e = launch_plan(page_update_kernel, a, n_pages, st);
     if (e != cudaSuccess) return e;
     Moves m = {a.src, a.dst, a.rows, nullptr, n_seq};
     return copy_pages(cs, m, n_seq, n_pages, st);
@@ -448,15 +590,15 @@ cudaError_t launch_page_compact(const int32_t* table, int64_t stride, int32_t co
         w += align16(bytes);
         return p;
     };
-    const size_t words = ((size_t)n_pages + 31) / 32;
     CompactArgs a = {table, stride, cols, n_seq, len, ps, n_pages, held, out, out_stride, n_used, remap};
-    a.bm = static_cast<uint32_t*>(take(words * 4));
-    a.rank = static_cast<int32_t*>(take(words * 4));
+    a.bm = static_cast<uint32_t*>(take(bitmap_bytes(n_pages)));
+    int32_t* numbers = static_cast<int32_t*>(take((size_t)n_pages * 4));
+    if (!remap) a.remap = numbers;
     a.src = static_cast<int32_t*>(take(((size_t)n_pages / 2 + 1) * 4));
     a.dst = static_cast<int32_t*>(take(((size_t)n_pages / 2 + 1) * 4));
     a.n_moves = static_cast<int32_t*>(take(4));
     a.status = device_status_ptr();
-    cudaError_t e = launch_pdl(page_compact_kernel, dim3(1), dim3(kPlanThreads), 0, st, a);
+    const cudaError_t e = launch_plan(page_compact_kernel, a, n_pages, st);
     if (e != cudaSuccess) return e;
     Moves m = {a.src, a.dst, nullptr, a.n_moves, 0};
     return copy_pages(cs, m, n_pages / 2, n_pages, st);
