@@ -13,7 +13,7 @@ namespace lidx {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kCopyThreads = 256;
+constexpr int kCopyThreads = 128;
 constexpr int kSegBytes = 16384;   // bytes of a page that a CTA copies at a time
 
 struct Caches {
@@ -36,22 +36,28 @@ struct Moves {
 
 template <typename V>
 __device__ __forceinline__ void copy_piece(const uint8_t* src, uint8_t* dst, int64_t row_bytes, int64_t stride,
-                                           int64_t o0, int64_t o1) {
-    constexpr int kBatch = 4;
+                                           int o0, int o1) {
+    constexpr int kBatch = 8;
     constexpr int S = (int)sizeof(V);
-    const bool flat = row_bytes == stride;
-    for (int64_t o = o0 + (int64_t)threadIdx.x * S; o < o1; o += (int64_t)kCopyThreads * S * kBatch) {
-        V v[kBatch];
-        int64_t at[kBatch];
+    if (row_bytes == stride) {
+        const V* s = reinterpret_cast<const V*>(src + o0) + threadIdx.x;
+        V* d = reinterpret_cast<V*>(dst + o0) + threadIdx.x;
+        const int n = (o1 - o0) / S - (int)threadIdx.x;     // this thread's share ends n elements on
+        int i0 = 0;
+        for (; i0 + (kBatch - 1) * kCopyThreads < n; i0 += kBatch * kCopyThreads) {
+            V v[kBatch];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int64_t p = o + (int64_t)i * kCopyThreads * S;
-            at[i] = flat ? p : (p / row_bytes) * stride + p % row_bytes;
-            if (p < o1) v[i] = *reinterpret_cast<const V*>(src + at[i]);
+            for (int i = 0; i < kBatch; ++i) v[i] = __ldcs(s + i0 + i * kCopyThreads);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) __stcs(d + i0 + i * kCopyThreads, v[i]);
         }
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-            if (o + (int64_t)i * kCopyThreads * S < o1) *reinterpret_cast<V*>(dst + at[i]) = v[i];
+        for (; i0 < n; i0 += kCopyThreads) __stcs(d + i0, __ldcs(s + i0));
+    } else {
+        // rows with bytes between them that are not the cache's
+        for (int o = o0 + (int)threadIdx.x * S; o < o1; o += kCopyThreads * S) {
+            const int64_t at = o / row_bytes * stride + o % row_bytes;
+            __stcs(reinterpret_cast<V*>(dst + at), __ldcs(reinterpret_cast<const V*>(src + at)));
+        }
     }
 }
 
@@ -72,9 +78,11 @@ __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(Caches cs, Move
         int c = 0;
         while (seg >= cs.segs[c]) seg -= cs.segs[c++];
         const int64_t stride = cs.c[c].row_stride_bytes, rb = cs.c[c].row_bytes;
-        const int64_t end = (int64_t)(m.rows ? m.rows[item] : cs.page_size) * rb;
-        const int64_t o0 = (int64_t)seg * kSegBytes;
-        const int64_t o1 = o0 + kSegBytes < end ? o0 + kSegBytes : end;
+        // (a page's payload is below 2^31 bytes)
+        const int end = (int)((int64_t)(m.rows ? m.rows[item] : cs.page_size) * rb);
+        const int o0 = seg * kSegBytes;
+        const int o1 = min(o0 + kSegBytes, end);
+        if (o0 >= o1) continue;
         const uint8_t* sp = static_cast<const uint8_t*>(cs.c[c].data) + (int64_t)s * cs.page_size * stride;
         uint8_t* dp = static_cast<uint8_t*>(cs.c[c].data) + (int64_t)d * cs.page_size * stride;
         switch (cs.vec[c]) {
@@ -96,7 +104,7 @@ __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(Caches cs, Move
 // rows of 256 pages, and 248 us to plan a compaction of 32768 pages.)
 constexpr int kCl = 8;
 constexpr int kWarps = kPlanThreads / 32;
-constexpr int kSliceWords = 48 * 1024;     // words of a slice that fit shared memory
+constexpr int kSliceWords = 24 * 1024;     // words of a slice up to which it is kept (twice) in shared memory
 
 struct Plan {
     int cnt[4][kCl];       // counts that the CTAs tell one another
@@ -383,7 +391,7 @@ struct CompactArgs {
     int32_t* out;
     int64_t out_stride;
     int32_t *n_used, *remap;
-    uint32_t* bm;       // [words] used or held
+    uint32_t *bm, *moving;   // [words] used or held; moving (unused where both fit shared memory)
     int32_t *src, *dst; // [n_pages / 2 + 1] the moves
     int32_t* n_moves;
     int* status;
@@ -427,15 +435,14 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kPlanThreads) page
     int n_used;
     told(s, 0, &n_used);
     // the moving pages (used, not held, numbered n_used or higher) and the free numbers below, in order
-    auto moving = [&](int w) {
-        const int64_t gw = w_base + w;
-        return bm.mine[w] & ~held_bits(a.held, gw, a.n_pages) & ~low_bits(gw, n_used);
-    };
+    uint32_t* moving = bm.global ? a.moving + w_base : slice_s + bm.slice;
     auto holes = [&](int w) { return ~bm.mine[w] & low_bits(w_base + w, n_used); };
     int y = 0;
     x = 0;
-    for (int w = tid; w < bm.n_mine(); w += kPlanThreads) {
-        x += __popc(moving(w));
+    for (int w = tid; w < bm.n_mine(); w += kPlanThreads) {     // (each word by the same thread from here on)
+        const int64_t gw = w_base + w;
+        moving[w] = bm.mine[w] & ~held_bits(a.held, gw, a.n_pages) & ~low_bits(gw, n_used);
+        x += __popc(moving[w]);
         y += __popc(holes(w));
     }
     block_scan(s, x, &total);
@@ -450,7 +457,7 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kPlanThreads) page
     for (int w0 = 0; w0 < bm.n_mine(); w0 += kPlanThreads) {
         const int w = w0 + tid;
         const bool in = w < bm.n_mine();
-        uint32_t m = in ? moving(w) : 0u;
+        uint32_t m = in ? moving[w] : 0u;
         int at = at0 + block_scan(s, __popc(m), &total);
         at0 += total;
         for (; m; m &= m - 1, ++at) a.src[at] = (int32_t)((w_base + w) * 32) + __ffs((int)m) - 1;
@@ -464,17 +471,31 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kPlanThreads) page
         *a.n_moves = n_moves;
     }
     sm100::cluster_sync();
-    // the new number of every page of the slice
+    // the new number of every page of the slice: a thread per word, then the warp walks its 32 words together
     at0 = mv0;
     for (int w0 = 0; w0 < bm.n_mine(); w0 += kPlanThreads) {
         const int w = w0 + tid;
-        const uint32_t m = w < bm.n_mine() ? moving(w) : 0u;
+        const uint32_t m = w < bm.n_mine() ? moving[w] : 0u;
         const int at = at0 + block_scan(s, __popc(m), &total);
         at0 += total;
-        const int64_t p0 = (w_base + w) * 32;
-        if (w < bm.n_mine())
-            for (int i = 0; i < 32 && p0 + i < a.n_pages; ++i)
-                a.remap[p0 + i] = (m >> i) & 1u ? a.dst[at + __popc(m & ((1u << i) - 1u))] : (int32_t)(p0 + i);
+        const int64_t p0 = (w_base + w0 + warp * 32) * 32 + lane;
+        const int n_words = min(32, bm.n_mine() - w0 - warp * 32);
+        constexpr int kBatch = 8;
+        for (int k0 = 0; k0 < n_words; k0 += kBatch) {
+            int32_t to[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const uint32_t mk = __shfl_sync(0xffffffffu, m, k0 + k);
+                const int ak = __shfl_sync(0xffffffffu, at, k0 + k);
+                const int64_t p = p0 + (int64_t)(k0 + k) * 32;
+                to[k] = (mk >> lane) & 1u ? a.dst[ak + __popc(mk & ((1u << lane) - 1u))] : (int32_t)p;
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int64_t p = p0 + (int64_t)(k0 + k) * 32;
+                if (k0 + k < n_words && p < a.n_pages) a.remap[p] = to[k];
+            }
+        }
     }
     sm100::cluster_sync();
     for (int b = gwarp; b < a.n_seq; b += kAllWarps) {
@@ -498,7 +519,7 @@ size_t bitmap_bytes(int64_t n_pages) {
 template <typename Args>
 cudaError_t launch_plan(void (*kern)(Args), const Args& a, int32_t n_pages, cudaStream_t st) {
     const size_t slice = bitmap_bytes(n_pages) / kCl;
-    const size_t sm = slice <= (size_t)kSliceWords * 4 ? slice : 0;
+    const size_t sm = slice <= (size_t)kSliceWords * 4 ? 2 * slice : 0;
     cudaError_t e = cudaSuccess;
     if (sm > 32 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
     return e != cudaSuccess ? e : launch_pdl(kern, dim3(kCl), dim3(kPlanThreads), sm, st, a);
@@ -513,8 +534,8 @@ bool make_caches(Caches* out, const idx_page_cache* caches, int n, int page_size
         out->c[i] = c;
         const uint64_t all = reinterpret_cast<uintptr_t>(c.data) | (uint64_t)c.row_stride_bytes | (uint64_t)c.row_bytes;
         out->vec[i] = all % 16 == 0 ? 16 : all % 8 == 0 ? 8 : all % 4 == 0 ? 4 : all % 2 == 0 ? 2 : 1;
+        if (c.row_bytes > (INT32_MAX - kSegBytes) / page_size) return false;
         const int64_t segs = ((int64_t)page_size * c.row_bytes + kSegBytes - 1) / kSegBytes;
-        if (segs + out->segs_total > INT32_MAX) return false;
         out->segs[i] = (int32_t)segs;
         out->segs_total += (int32_t)segs;
     }
@@ -524,7 +545,9 @@ bool make_caches(Caches* out, const idx_page_cache* caches, int n, int page_size
 cudaError_t copy_pages(const Caches& cs, const Moves& m, int64_t most, int32_t n_pages, cudaStream_t st) {
     if (cs.segs_total == 0 || most == 0) return cudaSuccess;
     const int64_t work = most > INT64_MAX / cs.segs_total ? INT64_MAX : most * cs.segs_total;
-    const int64_t grid = (int64_t)sm_count() * 8;
+    // many short CTAs: 4096 pages of 90112 bytes take 111 us (6.65 TB/s, 98 % of a plain copy) as 400 per SM, 116 as
+    // 16, 122 with 256 threads and 8
+    const int64_t grid = (int64_t)sm_count() * 400;
     return launch_pdl(page_copy_kernel, dim3((unsigned)(work < grid ? work : grid)), dim3(kCopyThreads), 0, st, cs, m,
                       n_pages, device_status_ptr());
 }
@@ -534,7 +557,7 @@ cudaError_t copy_pages(const Caches& cs, const Moves& m, int64_t most, int32_t n
 size_t page_workspace_bytes(int64_t n_seq, int64_t n_pages) {
     // bitmap (whole slices), then the update's free list and per-row arrays, or the compaction's moves and numbers
     const size_t update = align16((size_t)n_pages * 4) + 4 * align16((size_t)n_seq * 4);
-    const size_t compact = align16((size_t)n_pages * 4) + 2 * align16(((size_t)n_pages / 2 + 1) * 4) + 16;
+    const size_t compact = bitmap_bytes(n_pages) + align16((size_t)n_pages * 4) + 2 * align16(((size_t)n_pages / 2 + 1) * 4) + 16;
     return bitmap_bytes(n_pages) + (update > compact ? update : compact);
 }
 
@@ -592,6 +615,7 @@ cudaError_t launch_page_compact(const int32_t* table, int64_t stride, int32_t co
     };
     CompactArgs a = {table, stride, cols, n_seq, len, ps, n_pages, held, out, out_stride, n_used, remap};
     a.bm = static_cast<uint32_t*>(take(bitmap_bytes(n_pages)));
+    a.moving = static_cast<uint32_t*>(take(bitmap_bytes(n_pages)));
     int32_t* numbers = static_cast<int32_t*>(take((size_t)n_pages * 4));
     if (!remap) a.remap = numbers;
     a.src = static_cast<int32_t*>(take(((size_t)n_pages / 2 + 1) * 4));
