@@ -123,6 +123,8 @@ __device__ __forceinline__ void modify(float (&s)[N], const Score& sc, float d0)
             const uint64_t v = pair(x, y), z = mul2(v, v);
             unpair(mul2(v, fma2(fma2(fma2(fma2(c9, z, c7), z, c5), z, c3), z, c1)), rx, ry);
         };
+        // (the x^9 term is below 2^-27 of x up to 0.15)
+        const bool some = big * fabsf(sc.inv_cap) > 0.15f;
         if (__any_sync(0xffffffffu, large)) {
 #pragma unroll
             for (int i = 0; i < N; i += 2) {
@@ -132,9 +134,15 @@ __device__ __forceinline__ void modify(float (&s)[N], const Score& sc, float d0)
                 s[i] = fabsf(x0) > 0.3f ? sc.cap * tanh_large(x0) : y0;
                 s[i + 1] = fabsf(x1) > 0.3f ? sc.cap * tanh_large(x1) : y1;
             }
-        } else {
+        } else if (__any_sync(0xffffffffu, some)) {
 #pragma unroll
             for (int i = 0; i < N; i += 2) series(s[i], s[i + 1], s[i], s[i + 1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; i += 2) {
+                const uint64_t v = pair(s[i], s[i + 1]), z = mul2(v, v);
+                unpair(mul2(v, fma2(fma2(fma2(c7, z, c5), z, c3), z, c1)), s[i], s[i + 1]);
+            }
         }
     } else {
         const uint64_t c = pair(sc.c, sc.c);

@@ -37,7 +37,7 @@
 // that nobody sees (a page's unwritten end) are zeroed in shared memory, and a
 // NaN or infinity in any other row of it - 0 times which would reach rows that
 // do not see it - sends the CTA's rows to a scalar loop over their own keys,
-// as does a page number out of range (found before anything is loaded).
+// as does a page number out of range.
 // Every wait is bounded; a timeout records IDX_ERR_TIMEOUT and the CTA winds down.
 #include "dense_attn.cuh"
 #include "sm100_ptx.cuh"
@@ -52,6 +52,12 @@ constexpr int kRows = 128;             // packed query rows per row tile
 constexpr int kColBlock = 128 * 128;   // 64 columns x 128 rows of a tile, in the 128-byte swizzle
 constexpr int kFewRows = 48;           // packed rows up to which a CTA has one row tile and half an SM
 constexpr int kOtherWarps = 4;
+
+// Scores of 64 keys in two buffers per row tile instead of 128 in one: S of the next step is made while the softmax is
+// on this one.  It costs the tensor pipe a fifth (see above), so it is for where the softmax takes longer than the
+// products: capped or biased scores, and narrow heads.
+template <int D, bool kMods>
+constexpr bool kDoubleS = kMods || D == 64;
 
 template <int D, int kTiles>
 struct Cfg {
@@ -76,14 +82,15 @@ struct Ctl {
     uint64_t kfull[3], kempty[3];
     uint64_t vfull[3], vempty[3];
     uint64_t vok[3];              // V looked over
-    uint64_t sfull[2];            // S of a row tile written (and the PV products of the tile before complete)
+    uint64_t sfull[2][2];         // S of a row tile written; one buffer: [i][0], and its PV products before are complete;
+                                  // two: and those of two steps before
     uint64_t pready[2][2];        // a half of P written over it, O rescaled
     uint64_t pvdone[2];           // the first half's PV product complete
     uint64_t odone[2];            // every product of a row tile complete
     uint64_t done[2];
     uint32_t tmem_base;
     int abort;
-    int dirty;                    // a NaN or infinity in a V row that only some rows see
+    int dirty;                    // a NaN or infinity in a V row that only some rows see, or a page out of range
     int k0, k1, full0, full1;     // the CTA's keys, and those that each of its rows sees
 };
 
@@ -157,21 +164,34 @@ __device__ __forceinline__ void stage_cols(uint8_t* rows, int row, int c0, const
     }
 }
 
-// the first n columns of the warp's staged rows to out (row r at out + at_r, elements), whole rows at a time
+// the first n columns of the warp's first n_rows staged rows to out (row r at out + at_r, elements), whole rows at a
+// time
 template <typename E, int W>
-__device__ __forceinline__ void store_rows(E* out, int64_t at, bool valid, const uint8_t* rows, int n) {
+__device__ __forceinline__ void store_rows(E* out, int64_t at, int n_rows, const uint8_t* rows, int n) {
     constexpr int kPer = 16 / (int)sizeof(E);
     const int lane = threadIdx.x & 31;
-    const int pieces = n / kPer;
-    __syncwarp();
-    for (int k = 0; k < pieces; ++k) {
-        const int e = k * 32 + lane;
-        const int row = e / pieces, pc = e - row * pieces;
+    auto piece = [&](int row, int pc, bool ok) {
         const int64_t to = __shfl_sync(0xffffffffu, at, row);
-        const bool ok = __shfl_sync(0xffffffffu, (int)valid, row) != 0;
         if (ok)
             *reinterpret_cast<uint4*>(out + to + pc * kPer) =
                 *reinterpret_cast<const uint4*>(rows + row * (W * (int)sizeof(E)) + ((pc ^ (row & 7)) << 4));
+    };
+    __syncwarp();
+    if (n == W) {
+        constexpr int kPieces = W / kPer, kStep = 32 / kPieces;    // rows per instruction
+        static_assert(32 % kPieces == 0, "whole rows");
+#pragma unroll
+        for (int r0 = 0; r0 < 32; r0 += kStep) {
+            if (r0 >= n_rows) break;
+            const int row = r0 + lane / kPieces;
+            piece(row, lane % kPieces, row < n_rows);
+        }
+    } else {
+        const int pieces = n / kPer;
+        for (int e = lane; e - lane < n_rows * pieces; e += 32) {
+            const int row = e / pieces;
+            piece(row & 31, e - row * pieces, row < n_rows);
+        }
     }
     __syncwarp();
 }
@@ -183,6 +203,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr float kShift = kBf16 ? 0.f : 7.f;     // P is kept this much (log2) larger
     constexpr float kTop = kShift + 8.f;
+    constexpr bool kDouble = kDoubleS<D, kMods>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* kt = smem + C::kKOff;
@@ -213,8 +234,10 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
             mbar_init(&c.vok[i], 1);
         }
         for (int i = 0; i < n_tiles; ++i) {
-            mbar_init(&c.sfull[i], 1);
-            for (int x = 0; x < 2; ++x) mbar_init(&c.pready[i][x], min(4, (n_rows - i * kRows + 31) / 32));   // warps with rows
+            for (int x = 0; x < 2; ++x) {
+                mbar_init(&c.sfull[i][x], 1);
+                mbar_init(&c.pready[i][x], min(4, (n_rows - i * kRows + 31) / 32));   // warps with rows
+            }
             mbar_init(&c.pvdone[i], 1);
             mbar_init(&c.odone[i], 1);
             mbar_init(&c.done[i], 1);
@@ -236,13 +259,29 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     pdl_wait();
     __syncthreads();
 
+    // ---- Q's rows on their way (they are stored below, after the other loads have been waited for)
+    constexpr int kPieces = kTiles * C::kQRows * (D / 8), kPer = (kPieces + C::kThreads - 1) / C::kThreads;
+    const int t00 = (int)(m0 / G), h00 = (int)(m0 - (int64_t)t00 * G);   // token and head of the CTA's first row
+    uint4 qv[kPer];
+    {
+        const T* q = static_cast<const T*>(a.q) + ((int64_t)b * g.T * a.Hq + gkv * G) * a.dk;
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) {
+            const int i = threadIdx.x + x * C::kThreads;
+            const int rr = i / (D / 8), cc = i % (D / 8);
+            qv[x] = make_uint4(0u, 0u, 0u, 0u);
+            if (rr < n_rows && cc * 8 < a.dk) {
+                const int t = (h00 + rr) / G;
+                qv[x] = *reinterpret_cast<const uint4*>(q + ((int64_t)(t00 + t) * a.Hq + (h00 + rr - t * G)) * a.dk + cc * 8);
+            }
+        }
+    }
     // ---- the rows: interval, position, slope; the CTA's keys
     const int n_kv = seq_n_kv(g, b);
     const int rt = (warp - kOtherWarps) >> 2;                       // this thread's row tile (softmax warps)
     const int r = (int)threadIdx.x - 32 * kOtherWarps;              // ... and row of the CTA
     const bool has_row = r >= 0 && r < n_rows;
     const bool warp_rows = warp >= kOtherWarps && r - lane < n_rows;  // some row of the warp is one
-    const int t00 = (int)(m0 / G), h00 = (int)(m0 - (int64_t)t00 * G);   // token and head of the CTA's first row
     Interval iv = {0, 0, 0};
     int64_t qrow = 0;
     int h = 0, wlo = 0, whi = INT32_MAX;    // keys that every row of the warp sees
@@ -266,19 +305,13 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         }
     }
     // Q: 16-byte pieces into the swizzled K-major layout; rows and columns past the end are zero
-    {
-        const T* q = static_cast<const T*>(a.q) + ((int64_t)b * g.T * a.Hq + gkv * G) * a.dk;
-        for (int i = threadIdx.x; i < kTiles * C::kQRows * (D / 8); i += C::kThreads) {
-            const int rr = i / (D / 8), cc = i % (D / 8);
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (rr < n_rows && cc * 8 < a.dk) {
-                const int t = (h00 + rr) / G;
-                x = *reinterpret_cast<const uint4*>(q + ((int64_t)(t00 + t) * a.Hq + (h00 + rr - t * G)) * a.dk + cc * 8);
-            }
-            const int r0 = rr % C::kQRows;
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) {
+        const int i = threadIdx.x + x * C::kThreads;
+        const int rr = i / (D / 8), cc = i % (D / 8), r0 = rr % C::kQRows;
+        if (i < kPieces)
             *reinterpret_cast<uint4*>(smem + rr / C::kQRows * C::kQTile + (cc >> 3) * C::kQBlock + r0 * 128 +
-                                      (((cc & 7) ^ (r0 & 7)) << 4)) = x;
-        }
+                                      (((cc & 7) ^ (r0 & 7)) << 4)) = qv[x];
     }
     __syncthreads();
     // this split's keys, from a whole tile on (tiles are cuts of the position line)
@@ -288,29 +321,14 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     if (k1 > s1) k1 = (int)s1;
     const int t0 = k0 / kKeys;
     const int n = k1 > k0 ? (k1 + kKeys - 1) / kKeys - t0 : 0;
-    // every cache row of them exists?
-    bool bad = false;
-    if (n > 0) {
-        if (g.page_table) {
-            const int64_t p1 = ((int64_t)k1 - 1) / g.page_size;
-            for (int64_t pg = k0 / g.page_size + threadIdx.x; pg <= p1; pg += C::kThreads) {
-                const int64_t row = (int64_t)g.page_table[(int64_t)b * g.page_table_stride + pg] * g.page_size;
-                const int64_t last = pg == p1 ? (k1 - 1) % g.page_size : g.page_size - 1;
-                bad |= row < 0 || row + last >= a.kv_rows;
-            }
-        } else {
-            const int64_t row = seq_row0(g, b);
-            bad = row + k0 < 0 || row + k1 > a.kv_rows;
-        }
-    }
     fence_proxy_async_smem();   // Q before the MMAs read it
     tc_fence_before();
-    bad = __syncthreads_or(bad);
+    __syncthreads();
     tc_fence_after();
     const uint32_t tmem = c.tmem_base;
     const int full0 = c.full0, full1 = c.full1;
 
-    if (n > 0 && !bad) {
+    if (n > 0) {
         auto aborted = [&] { return *(volatile int*)&c.abort != 0; };
         auto warp_aborted = [&] { return __any_sync(0xffffffffu, aborted()); };
         auto give_up = [&] {
@@ -329,10 +347,16 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
                 if (lane < pieces * (D / 64)) {
                     const int pc = lane / (D / 64), cb = lane % (D / 64);
                     const int64_t key = (int64_t)(t0 + j) * kKeys + pc * p.box;
-                    // a piece that holds none of the keys is filled with zeros (a row past the cache)
+                    // a piece that holds none of the keys is filled with zeros (a row past the cache), and so is
+                    // one whose rows do not exist: the CTA's rows are redone key by key then
                     int64_t row = a.kv_rows;
-                    if (key < k1 && key + p.box > k0)
+                    if (key < k1 && key + p.box > k0) {
                         row = g.page_table ? key_row(g, b, key) : row_base + key;
+                        if (row + max(k0 - key, (int64_t)0) < 0 || row + min(k1 - key, (int64_t)p.box) > a.kv_rows) {
+                            row = a.kv_rows;
+                            *(volatile int*)&c.dirty = 1;
+                        }
+                    }
                     tma_load_3d(dst + cb * kColBlock + pc * p.box * 128, map, bar, cb * 64, gkv, (int32_t)row);
                 }
             };
@@ -366,7 +390,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
             // its own a product took about 100 cycles to issue, more than it takes).  The queue of issued products is
             // short, so the tensor pipe idles while an issuer waits or commits: it has the other issuer's then.
             const int i = warp - 1;
-            const uint32_t id_qk = idesc_f16_f32_major(kRows, kKeys, kBf16 ? 1 : 0, 0, 0);
+            const uint32_t id_qk = idesc_f16_f32_major(kRows, kDouble ? kHalf : kKeys, kBf16 ? 1 : 0, 0, 0);
             const uint32_t id_pv = idesc_f16_f32_major(kRows, (a.dv + 15) & ~15, kBf16 ? 1 : 0, 0, 1);
             const uint64_t kmajor = desc_sw128_kmajor(0, 1024), mnmajor = desc_sw128_mnmajor(0, kColBlock, 1024);
             const uint32_t k_hi = desc_hi(kmajor), v_hi = desc_hi(mnmajor), k_lo = (uint32_t)kmajor, v_lo = (uint32_t)mnmajor;
@@ -379,53 +403,67 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
             bool ok = true;
             // S = Q K^T.  All D / 16 products run (columns past dk are zero): an unrolled chain that stopped at dk by
             // a run-time bound got a wrong last descriptor (nvcc 13.0; the basis-vector test shows it)
-            auto qk = [&] {
-                const uint32_t ka = __shfl_sync(0xffffffffu, kb + (sk * C::kTileBytes >> 4), 0);
+            auto qk = [&](int half) {
+                const uint32_t ka = __shfl_sync(0xffffffffu, kb + ((sk * C::kTileBytes + half * (kHalf * 128)) >> 4), 0);
+                const uint32_t d = __shfl_sync(0xffffffffu, ts + half * kHalf, 0);
+                const bool last = !kDouble || half == 1;      // of the K tile
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks)
-                        mma_f16_ss_lo(ts, qa + (((ks >> 2) * C::kQBlock + (ks & 3) * 32) >> 4), k_hi,
+                        mma_f16_ss_lo(d, qa + (((ks >> 2) * C::kQBlock + (ks & 3) * 32) >> 4), k_hi,
                                       ka + (((ks >> 2) * kColBlock + (ks & 3) * 32) >> 4), k_hi, id_qk, ks > 0 ? 1u : 0u);
-                    mma_commit(&c.sfull[i]);
-                    mma_commit(&c.kempty[sk]);
+                    mma_commit(&c.sfull[i][half]);
+                    if (last) mma_commit(&c.kempty[sk]);
                 }
                 __syncwarp();
-                if (++sk == C::kStagesK) {
+                if (last && ++sk == C::kStagesK) {
                     sk = 0;
                     kph ^= 1;
                 }
             };
-            ok = warp_wait(&c.kfull[0], 0u);
-            if (ok) qk();
-            for (int j = 0; ok && j < n; ++j) {
-                const uint32_t va = __shfl_sync(0xffffffffu, vb + (sv * C::kTileBytes >> 4), 0);
-                const uint32_t acc = __shfl_sync(0xffffffffu, j > 0 ? 1u : 0u, 0);
-                ok = warp_wait(&c.vok[sv], (uint32_t)vph) && warp_wait(&c.pready[i][0], (uint32_t)(j & 1));
-                if (!ok) break;
+            // O += P V of half a tile, and the commits that follow it
+            auto pv = [&](int half, uint32_t first, uint64_t* b0, uint64_t* b1) {
+                const uint32_t va = __shfl_sync(0xffffffffu, vb + ((sv * C::kTileBytes + half * (kHalf * 128)) >> 4), 0);
+                const uint32_t pa = __shfl_sync(0xffffffffu, ts + half * (kDouble ? kHalf : kHalf / 2), 0);
+                const uint32_t acc = __shfl_sync(0xffffffffu, first ? 0u : 1u, 0);
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < kHalf / 16; ++ks)
-                        mma_f16_ts_lo(to, ts + ks * 8, va + (ks * 2048 >> 4), v_hi, id_pv, ks > 0 ? 1u : acc);
-                    mma_commit(&c.pvdone[i]);
+                        mma_f16_ts_lo(to, pa + ks * 8, va + (ks * 2048 >> 4), v_hi, id_pv, ks > 0 ? 1u : acc);
+                    if (b0) mma_commit(b0);
+                    if (b1) mma_commit(b1);
                 }
                 __syncwarp();
-                // the next tile's S follows the second half's product over the same columns: a row tile's products
-                // run in order
-                ok = (j + 1 == n || warp_wait(&c.kfull[sk], (uint32_t)kph)) && warp_wait(&c.pready[i][1], (uint32_t)(j & 1));
-                if (!ok) break;
-                tc_fence_after();
+            };
+            ok = warp_wait(&c.kfull[0], 0u);
+            if (ok) {
+                qk(0);
+                if (kDouble) qk(1);
+            }
+            for (int j = 0; ok && j < n; ++j) {
                 const bool last = j + 1 == n;
-                if (elect_one()) {
-#pragma unroll
-                    for (int ks = kHalf / 16; ks < kKeys / 16; ++ks)
-                        mma_f16_ts_lo(to, ts + ks * 8, va + (ks * 2048 >> 4), v_hi, id_pv, 1u);
-                    mma_commit(&c.vempty[sv]);
-                    if (last) mma_commit(&c.odone[i]);
+                ok = warp_wait(&c.vok[sv], (uint32_t)vph) && warp_wait(&c.pready[i][0], (uint32_t)(j & 1));
+                if (!ok) break;
+                // new scores follow the product over the weights that they replace: a row tile's products run in order.
+                // (Two buffers: the commit after the last tile's first half has no scores; it tells that the products
+                // of the step before are complete, as scores would.)
+                if (kDouble) {
+                    pv(0, j == 0, last ? &c.sfull[i][0] : nullptr, nullptr);
+                    if (!last) {
+                        ok = warp_wait(&c.kfull[sk], (uint32_t)kph);
+                        if (!ok) break;
+                        qk(0);
+                    }
+                } else {
+                    pv(0, j == 0, &c.pvdone[i], nullptr);
+                    ok = last || warp_wait(&c.kfull[sk], (uint32_t)kph);
                 }
-                __syncwarp();
-                if (!last) qk();
+                ok = ok && warp_wait(&c.pready[i][1], (uint32_t)(j & 1));
+                if (!ok) break;
+                pv(1, false, &c.vempty[sv], last ? &c.odone[i] : nullptr);
+                if (!last) qk(kDouble ? 1 : 0);
                 if (++sv == C::kStagesV) {
                     sv = 0;
                     vph ^= 1;
@@ -477,7 +515,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         const uint32_t to = tmem + lane_off + C::kOCol + rt * D;
         const Score sc = make_score(a, a.mods.slopes && has_row ? a.mods.slopes[h] : 0.f);
         float m_used = -INFINITY, l_run = 0.f;
-        bool ok = n > 0 && !bad;
+        bool ok = n > 0;
         auto timed_out = [&] {
             *(volatile int*)&c.abort = 1;
             flag(g.status, IDX_ERR_TIMEOUT);
@@ -486,8 +524,8 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         const uint64_t c2 = pair(sc.c, sc.c);
         for (int q = 0; ok && q < 2 * n; ++q) {
             const int j = q >> 1, half = q & 1;
-            if (half == 0) {
-                if (!warp_wait(&c.sfull[rt], (uint32_t)(j & 1))) {
+            if (kDouble || half == 0) {
+                if (!warp_wait(&c.sfull[rt][kDouble ? half : 0], (uint32_t)(j & 1))) {
                     timed_out();
                     break;
                 }
@@ -536,9 +574,11 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
                     l_run *= al;
                 }
                 if (q > 0 && __any_sync(0xffffffffu, al != 1.f)) {
-                    // O's products up to here: those of the tile before are complete (its S came after them), the
-                    // first half's of this one has to be waited for
-                    if (half == 1 && !warp_wait(&c.pvdone[rt], (uint32_t)(j & 1))) {
+                    // O's products up to here.  One buffer: those of the tile before are complete (this S came after
+                    // them), the first half's of this one has to be waited for.  Two: the next step's scores came
+                    // after the last step's product.
+                    if (kDouble ? !warp_wait(&c.sfull[rt][half ^ 1], (uint32_t)(((q + 1) >> 1) & 1))
+                                : half == 1 && !warp_wait(&c.pvdone[rt], (uint32_t)(j & 1))) {
                         timed_out();
                         break;
                     }
@@ -571,7 +611,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
                     lb = add2(lb, pair(p0, p1));
                 w[i / 2] = pack2<T>(p0, p1);
             }
-            tmem_st_32x32b_x32(ts + half * (kHalf / 2), w);
+            tmem_st_32x32b_x32(ts + half * (kDouble ? kHalf : kHalf / 2), w);
             float l0, l1;
             unpair(add2(la, lb), l0, l1);
             l_run += l0 + l1;
@@ -584,8 +624,8 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         tc_fence_after();
         const bool some = iv.lo < iv.hi;
         const int64_t rh = qrow * a.Hq + h;
-        // the V checker has seen every tile by now: each PV product waited for it
-        const bool by_key = bad || (n > 0 && *(volatile int*)&c.dirty != 0);
+        // every tile has been loaded and looked over by now: each PV product waited for that
+        const bool by_key = ok && *(volatile int*)&c.dirty != 0;
         float acc[D];
         if (by_key) {
             float mm = -INFINITY, ll = 0.f;
@@ -632,7 +672,8 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
                     columns((c0 + x) / 32, o);
                     stage_cols<float, W>(rows, lane, x, o);
                 }
-                store_rows<float, W>(a.part_o + c0, (rh * a.splits + split) * a.dv, has_row, rows, min(W, a.dv - c0));
+                store_rows<float, W>(a.part_o + c0, (rh * a.splits + split) * a.dv, n_rows - (r - lane), rows,
+                                     min(W, a.dv - c0));
             }
         } else {
 #pragma unroll
@@ -641,7 +682,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
                 columns(x / 32, o);
                 stage_cols<T, D>(rows, lane, x, o);
             }
-            store_rows<T, D>(static_cast<T*>(a.out), rh * a.dv, has_row, rows, a.dv);
+            store_rows<T, D>(static_cast<T*>(a.out), rh * a.dv, n_rows - (r - lane), rows, a.dv);
         }
         tc_fence_before();
     }
