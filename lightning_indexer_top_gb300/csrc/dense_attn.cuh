@@ -101,13 +101,14 @@ __device__ __forceinline__ float tanh_large(float x) {
     return fmaf(-2.f, rcp_approx(1.f + sm100::ex2_approx(x * (2.f * kLog2e))), 1.f);
 }
 
-// N raw products of consecutive keys -> scores in log2 units; d0 = the row's position minus the first key's.
+// N raw products of consecutive keys -> scores in log2 units; d0 = the row's position minus the first key's; past:
+// no key that the warp's rows see lies past their positions (no absolute value to take, one operation less).
 // Every lane of a warp comes here together.
 // A capped score is cap * tanh(x), x = s * scale / softcap: for |x| <= 0.3 by the Taylor series of tanh up to x^9
 // (the next term is below 2^-24 of x there), as s times a polynomial in s^2 whose coefficients hold the factors (six
 // packed operations for two scores; the exponential form takes two special functions for each).
 template <int N>
-__device__ __forceinline__ void modify(float (&s)[N], const Score& sc, float d0) {
+__device__ __forceinline__ void modify(float (&s)[N], const Score& sc, float d0, bool past) {
     if (sc.inv_cap != 0.f) {
         float big = 0.f;
 #pragma unroll
@@ -150,12 +151,14 @@ __device__ __forceinline__ void modify(float (&s)[N], const Score& sc, float d0)
         for (int i = 0; i < N; i += 2) unpair(mul2(pair(s[i], s[i + 1]), c), s[i], s[i + 1]);
     }
     if (sc.biased) {
-        const uint64_t sl = pair(-sc.slope, -sc.slope), d = pair(d0, d0);
+        if (past) {
+            const uint64_t sl = pair(sc.slope, sc.slope), base = pair(-sc.slope * d0, -sc.slope * d0);
 #pragma unroll
-        for (int i = 0; i < N; i += 2) {
-            float x0, x1;
-            unpair(add2(d, pair(-(float)i, -(float)(i + 1))), x0, x1);
-            unpair(fma2(sl, pair(fabsf(x0), fabsf(x1)), pair(s[i], s[i + 1])), s[i], s[i + 1]);
+            for (int i = 0; i < N; i += 2)
+                unpair(add2(pair(s[i], s[i + 1]), fma2(sl, pair((float)i, (float)(i + 1)), base)), s[i], s[i + 1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) s[i] = fmaf(-sc.slope, fabsf(d0 - (float)i), s[i]);
         }
     }
 }

@@ -95,8 +95,9 @@ struct DenseFeed {
         (void)u;
         const Score sc = make_score(p->a, p->a.mods.slopes ? p->a.mods.slopes[h] : 0.f);
         const float d = (float)(pos - (base + t * kKeys));
-        lidx::modify(s0, sc, d);
-        lidx::modify(s1, sc, d - 32.f);
+        const bool past = base + (t + 1) * kKeys <= pos + 1;      // (every head of the row alike)
+        lidx::modify(s0, sc, d, past);
+        lidx::modify(s1, sc, d - 32.f, past);
     }
 
     __device__ __forceinline__ void store_lse(int64_t rh, float m, float l) const {

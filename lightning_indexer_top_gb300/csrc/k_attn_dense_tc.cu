@@ -55,9 +55,9 @@ constexpr int kOtherWarps = 4;
 
 // Scores of 64 keys in two buffers per row tile instead of 128 in one: S of the next step is made while the softmax is
 // on this one.  It costs the tensor pipe a fifth (see above), so it is for where the softmax takes longer than the
-// products: capped or biased scores, and narrow heads.
-template <int D, bool kMods>
-constexpr bool kDoubleS = kMods || D == 64;
+// products: capped or biased scores, narrow heads, and a CTA with one row tile, whose steps nothing else overlaps.
+template <int D, int kTiles, bool kMods>
+constexpr bool kDoubleS = kMods || D == 64 || kTiles == 1;
 
 template <int D, int kTiles>
 struct Cfg {
@@ -110,16 +110,17 @@ struct TcArgs {
     int box;          // rows per TMA box: 128, or the largest power of two that divides the page
 };
 
-// The rows' attention key by key, each thread its own row: the rare way, see the top.  q, K and V as
-// stored, f32 sums.  Returns the maximum (log2 units) and the sum; acc gets the weighted values.
+// A row's attention key by key, for the thread that owns it: the rare way, see the top.  q, K and V as stored, f32
+// sums; writes the output (or the split's partial result) and lse.
 template <typename T>
-__device__ __noinline__ void scalar_row(const TcArgs& p, const Geom& g, int b, int gkv, int64_t qrow, int h, Interval iv,
-                                        int64_t s0, int64_t s1, float* acc, float* m_out, float* l_out) {
-    const DenseArgs& a = p.a;
-    const T* q = static_cast<const T*>(a.q) + (qrow * a.Hq + h) * a.dk;
+__device__ __noinline__ void scalar_row(const DenseArgs& a, const Geom& g, int b, int gkv, int64_t rh, int h, Interval iv,
+                                        int split) {
+    float acc[128];
+    const T* q = static_cast<const T*>(a.q) + rh * a.dk;
     for (int c = 0; c < a.dv; ++c) acc[c] = 0.f;
     float m = -INFINITY, l = 0.f;
-    const int64_t lo = iv.lo > s0 ? iv.lo : s0, hi = iv.hi < s1 ? iv.hi : s1;
+    const int64_t s0 = (int64_t)split * a.kps;
+    const int64_t lo = iv.lo > s0 ? iv.lo : s0, hi = iv.hi < s0 + a.kps ? iv.hi : s0 + a.kps;
     for (int64_t j = lo; j < hi; ++j) {
         const int64_t row = key_row(g, b, j);
         if (row < 0 || row >= a.kv_rows) {
@@ -142,8 +143,15 @@ __device__ __noinline__ void scalar_row(const TcArgs& p, const Geom& g, int b, i
         l = fmaf(l, al, w);
         for (int c = 0; c < a.dv; ++c) acc[c] = fmaf(w, to_f32(v[c]), al == 1.f ? acc[c] : acc[c] * al);
     }
-    *m_out = m;
-    *l_out = l;
+    if (a.splits > 1) {
+        const int64_t u = rh * a.splits + split;
+        a.part_ml[u * 2] = m * kLn2;
+        a.part_ml[u * 2 + 1] = l;
+        for (int c = 0; c < a.dv; ++c) a.part_o[u * a.dv + c] = l == 0.f ? 0.f : acc[c];
+    } else {
+        if (a.lse) a.lse[rh] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        for (int c = 0; c < a.dv; ++c) static_cast<T*>(a.out)[rh * a.dv + c] = from_f32<T>(l == 0.f ? 0.f : acc[c] / l);
+    }
 }
 
 // 32 columns of a row into its warp's staging rows of W columns (16-byte pieces, swizzled by the row)
@@ -180,7 +188,7 @@ __device__ __forceinline__ void store_rows(E* out, int64_t at, int n_rows, const
     if (n == W) {
         constexpr int kPieces = W / kPer, kStep = 32 / kPieces;    // rows per instruction
         static_assert(32 % kPieces == 0, "whole rows");
-#pragma unroll
+#pragma unroll 4
         for (int r0 = 0; r0 < 32; r0 += kStep) {
             if (r0 >= n_rows) break;
             const int row = r0 + lane / kPieces;
@@ -203,7 +211,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr float kShift = kBf16 ? 0.f : 7.f;     // P is kept this much (log2) larger
     constexpr float kTop = kShift + 8.f;
-    constexpr bool kDouble = kDoubleS<D, kMods>;
+    constexpr bool kDouble = kDoubleS<D, kTiles, kMods>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* kt = smem + C::kKOff;
@@ -261,18 +269,24 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
 
     // ---- Q's rows on their way (they are stored below, after the other loads have been waited for)
     constexpr int kPieces = kTiles * C::kQRows * (D / 8), kPer = (kPieces + C::kThreads - 1) / C::kThreads;
+    constexpr int kRowStep = C::kThreads / (D / 8);              // a thread's pieces: one column, rows this far apart
     const int t00 = (int)(m0 / G), h00 = (int)(m0 - (int64_t)t00 * G);   // token and head of the CTA's first row
+    const int qr = threadIdx.x / (D / 8), qc = threadIdx.x % (D / 8);
     uint4 qv[kPer];
     {
-        const T* q = static_cast<const T*>(a.q) + ((int64_t)b * g.T * a.Hq + gkv * G) * a.dk;
+        int t = (h00 + qr) / G, hh = (h00 + qr) - t * G;
+        const int step_t = kRowStep / G, step_h = kRowStep - step_t * G;
+        const T* q = static_cast<const T*>(a.q) + (((int64_t)b * g.T + t00) * a.Hq + gkv * G) * a.dk + qc * 8;
 #pragma unroll
         for (int x = 0; x < kPer; ++x) {
-            const int i = threadIdx.x + x * C::kThreads;
-            const int rr = i / (D / 8), cc = i % (D / 8);
             qv[x] = make_uint4(0u, 0u, 0u, 0u);
-            if (rr < n_rows && cc * 8 < a.dk) {
-                const int t = (h00 + rr) / G;
-                qv[x] = *reinterpret_cast<const uint4*>(q + ((int64_t)(t00 + t) * a.Hq + (h00 + rr - t * G)) * a.dk + cc * 8);
+            if (qr + x * kRowStep < n_rows && qc * 8 < a.dk)
+                qv[x] = *reinterpret_cast<const uint4*>(q + ((int64_t)t * a.Hq + hh) * a.dk);
+            t += step_t;
+            hh += step_h;
+            if (hh >= G) {
+                hh -= G;
+                ++t;
             }
         }
     }
@@ -305,13 +319,14 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         }
     }
     // Q: 16-byte pieces into the swizzled K-major layout; rows and columns past the end are zero
+    {
+        uint8_t* qs = smem + (qc >> 3) * C::kQBlock;
 #pragma unroll
-    for (int x = 0; x < kPer; ++x) {
-        const int i = threadIdx.x + x * C::kThreads;
-        const int rr = i / (D / 8), cc = i % (D / 8), r0 = rr % C::kQRows;
-        if (i < kPieces)
-            *reinterpret_cast<uint4*>(smem + rr / C::kQRows * C::kQTile + (cc >> 3) * C::kQBlock + r0 * 128 +
-                                      (((cc & 7) ^ (r0 & 7)) << 4)) = qv[x];
+        for (int x = 0; x < kPer; ++x) {
+            const int rr = qr + x * kRowStep, r0 = rr % C::kQRows;
+            if (rr < kTiles * C::kQRows)
+                *reinterpret_cast<uint4*>(qs + rr / C::kQRows * C::kQTile + r0 * 128 + (((qc & 7) ^ (r0 & 7)) << 4)) = qv[x];
+        }
     }
     __syncthreads();
     // this split's keys, from a whole tile on (tiles are cuts of the position line)
@@ -522,6 +537,9 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
             ok = false;
         };
         const uint64_t c2 = pair(sc.c, sc.c);
+        // the warp's rows see nothing past their own positions; its first position
+        const bool past = __all_sync(0xffffffffu, iv.hi <= iv.pos + 1 || iv.lo >= iv.hi);
+        const int first_pos = __reduce_min_sync(0xffffffffu, iv.lo < iv.hi ? iv.pos : INT32_MAX);
         for (int q = 0; ok && q < 2 * n; ++q) {
             const int j = q >> 1, half = q & 1;
             if (kDouble || half == 0) {
@@ -545,13 +563,17 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
                     s[32 + i] = __uint_as_float(y[i]);
                 }
             }
-            if (kMods) modify(s, sc, (float)(iv.pos - key0));
+            if (kMods) modify(s, sc, (float)(iv.pos - key0), past || key0 + kHalf <= first_pos);
             if (key0 < wlo || key0 < k0 || key0 + kHalf > whi || key0 + kHalf > k1) {
-                // visible columns [a0, a1) of this row
-                const int a0 = max(iv.lo, k0) - key0, a1 = min(iv.hi, k1) - key0;
+                // visible columns [a0, a1) of this row, as bits
+                const int a0 = min(max(max(iv.lo, k0) - key0, 0), kHalf), a1 = max(min(min(iv.hi, k1) - key0, kHalf), 0);
+                const uint64_t up = a0 >= kHalf ? 0ull : ~0ull << a0, down = a1 >= kHalf ? ~0ull : (1ull << a1) - 1ull;
+                const uint32_t m0 = (uint32_t)(up & down), m1 = (uint32_t)((up & down) >> 32);
 #pragma unroll
-                for (int i = 0; i < kHalf; ++i)
-                    if (i < a0 || i >= a1) s[i] = -INFINITY;
+                for (int i = 0; i < 32; ++i) {
+                    s[i] = (m0 >> i) & 1u ? s[i] : -INFINITY;
+                    s[32 + i] = (m1 >> i) & 1u ? s[32 + i] : -INFINITY;
+                }
             }
             // the row's maximum
             float x0 = fmaxf(s[0], s[1]), x1 = fmaxf(s[2], s[3]), x2 = fmaxf(s[4], s[5]), x3 = fmaxf(s[6], s[7]);
@@ -626,63 +648,48 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         const int64_t rh = qrow * a.Hq + h;
         // every tile has been loaded and looked over by now: each PV product waited for that
         const bool by_key = ok && *(volatile int*)&c.dirty != 0;
-        float acc[D];
         if (by_key) {
-            float mm = -INFINITY, ll = 0.f;
-            if (has_row && some) scalar_row<T>(p, g, b, gkv, qrow, h, iv, s0, s1, acc, &mm, &ll);
-            m_used = mm;
-            l_run = ll;
-        }
-        __syncwarp();
-        const float l = some && n > 0 ? l_run : 0.f;
-        const float inv = l == 0.f ? 0.f : a.splits > 1 ? 1.f : 1.f / l;
-        if (has_row) {
-            if (a.splits > 1) {
-                a.part_ml[(rh * a.splits + split) * 2] = m_used * kLn2;
-                a.part_ml[(rh * a.splits + split) * 2 + 1] = l;
-            } else if (a.lse) {
-                a.lse[rh] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * kLn2;
-            }
-        }
-        // 32 columns of the row, normalised (a split's partial: as they are)
-        auto columns = [&](int cb, float (&o)[32]) {
-            if (by_key) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = cb * 32 + i < a.dv ? acc[cb * 32 + i] * inv : 0.f;
-            } else if (ok) {
-                uint32_t x[32];
-                tmem_ld_32x32b_x32_raw(to + cb * 32, x);
-                tmem_ld_wait_for(x);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(x[i]) * inv;
-            }
-            if (l == 0.f || (!ok && !by_key)) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = 0.f;
-            }
-        };
-        // through shared memory (Q's, and past it K's: no product reads them any more), so that whole rows are written
-        uint8_t* rows = smem + rt * C::kQTile + (warp & 3) * (32 * D * 2);
-        if (a.splits > 1) {
-            constexpr int W = D / 2;
-            for (int c0 = 0; c0 < a.dv; c0 += W) {
-#pragma unroll
-                for (int x = 0; x < W; x += 32) {
-                    float o[32];
-                    columns((c0 + x) / 32, o);
-                    stage_cols<float, W>(rows, lane, x, o);
-                }
-                store_rows<float, W>(a.part_o + c0, (rh * a.splits + split) * a.dv, n_rows - (r - lane), rows,
-                                     min(W, a.dv - c0));
-            }
+            if (has_row) scalar_row<T>(a, g, b, gkv, rh, h, iv, split);
+            __syncwarp();
         } else {
-#pragma unroll
-            for (int x = 0; x < D; x += 32) {
-                float o[32];
-                columns(x / 32, o);
-                stage_cols<T, D>(rows, lane, x, o);
+            const float l = some && ok ? l_run : 0.f;
+            const float inv = l == 0.f ? 0.f : a.splits > 1 ? 1.f : 1.f / l;
+            if (has_row) {
+                if (a.splits > 1) {
+                    a.part_ml[(rh * a.splits + split) * 2] = m_used * kLn2;
+                    a.part_ml[(rh * a.splits + split) * 2 + 1] = l;
+                } else if (a.lse) {
+                    a.lse[rh] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * kLn2;
+                }
             }
-            store_rows<T, D>(static_cast<T*>(a.out), rh * a.dv, n_rows - (r - lane), rows, a.dv);
+            // through shared memory (Q's, and past it K's: no product reads them any more), so that whole rows are
+            // written; normalised (a split's partial: as they are)
+            uint8_t* rows = smem + rt * C::kQTile + (warp & 3) * (32 * D * 2);
+            const bool parts = a.splits > 1;
+            const int W = parts ? D / 2 : D;
+#pragma unroll 1
+            for (int c0 = 0; c0 < a.dv; c0 += W) {
+#pragma unroll 1
+                for (int x = 0; x < W; x += 32) {
+                    uint32_t u32[32];
+                    float o[32];
+                    if (ok) {
+                        tmem_ld_32x32b_x32_raw(to + c0 + x, u32);
+                        tmem_ld_wait_for(u32);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0.f : __uint_as_float(u32[i]) * inv;
+                    if (parts)
+                        stage_cols<float, D / 2>(rows, lane, x, o);
+                    else
+                        stage_cols<T, D>(rows, lane, x, o);
+                }
+                if (parts)
+                    store_rows<float, D / 2>(a.part_o + c0, (rh * a.splits + split) * a.dv, n_rows - (r - lane), rows,
+                                             min(W, a.dv - c0));
+                else
+                    store_rows<T, D>(static_cast<T*>(a.out), rh * a.dv, n_rows - (r - lane), rows, a.dv);
+            }
         }
         tc_fence_before();
     }
