@@ -350,6 +350,37 @@ __device__ __forceinline__ void mla_run(const MlaSmem& sm, uint32_t tmem, uint32
             else
                 gather_tiles<kDkBlocks * 8, kStagesK, kKTileBytes>(c, xtiles, lat, lat_row_stride, u, rows_s, producer,
                                                                    g.status);
+        } else if (Feed::kDense && warp == 1) {
+            // -------------------------------------------------------- S = Q K^T issuer of the dense feed: the warp
+            // walks together and a lane issues (operands that all lanes share stay in uniform registers; a lane on
+            // its own takes about 100 cycles for each of a tile's 36 products, which take 33)
+            const uint32_t idesc = idesc_f16_f32_major(kHq, kKeys, 1, 0, 0);
+            const uint64_t kd = desc_sw128_kmajor(0, 1024);
+            const uint32_t k_hi = desc_hi(kd), tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint32_t kb = (uint32_t)kd + desc_addr(xtiles);
+            bool ok = u.n_tiles == 0 || warp_wait(&c.qready, 0);
+            for (int t = 0; ok && t < u.n_tiles; ++t) {
+                const int stage = t % kStagesK, sb = t & 1;
+                ok = warp_wait(&c.xfull[stage], (uint32_t)((t / kStagesK) & 1)) &&
+                     warp_wait(&c.sempty[sb], (uint32_t)((t >> 1) & 1) ^ 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t ka = __shfl_sync(0xffffffffu, kb + (stage * kKTileBytes >> 4), 0);
+                const uint32_t d = __shfl_sync(0xffffffffu, tm + kSCol0 + sb * kKeys, 0);
+                if (elect_one()) {
+#pragma unroll
+                    for (int ks = 0; ks < kDk / 16; ++ks)
+                        mma_f16_ts_lo(d, tm + ks * 8, ka + (((ks >> 2) * kBlockBytes + (ks & 3) * 32) >> 4), k_hi, idesc,
+                                      ks > 0 ? 1u : 0u);
+                    mma_commit(&c.xempty[stage]);
+                    mma_commit(&c.sfull[sb]);
+                }
+                __syncwarp();
+            }
+            if (!ok) abort_cta(c, g.status);
+            if (elect_one()) mma_commit(&c.done);
+            __syncwarp();
+            warp_wait(&c.done, 0);
         } else if (warp == 1) {
             if (lane == 0) {
                 // ---------------------------------------------------- S = Q K^T issuer
@@ -495,6 +526,40 @@ __device__ __forceinline__ void mla_run(const MlaSmem& sm, uint32_t tmem, uint32
                 gather_tiles<kDvBlocks * 8, kStagesV, kVTileBytes>(c, xtiles, lat, lat_row_stride, u, rows_s, producer,
                                                                    g.status);
             }
+        } else if (Feed::kDense && warp == 1) {
+            // -------------------------------------------------------- O += P V issuer of the dense feed
+            const uint32_t idesc = idesc_f16_f32_major(kHq, 256, 1, 0, 1);
+            const uint64_t pd = desc_sw128_kmajor(0, 1024), vd = desc_sw128_mnmajor(0, kBlockBytes, 1024);
+            const uint32_t p_hi = desc_hi(pd), v_hi = desc_hi(vd), tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint32_t pb = (uint32_t)pd + desc_addr(pkts), vb = (uint32_t)vd + desc_addr(xtiles);
+            bool ok = true;
+            for (int t = 0; ok && t < u.n_tiles; ++t) {
+                const int stage = t % kStagesV, j = t & 1;
+                ok = warp_wait(&c.vok[stage], (uint32_t)((t / kStagesV) & 1)) &&
+                     warp_wait(&c.cdone[j], (uint32_t)((t >> 1) & 1));
+                if (!ok) break;
+                fence_proxy_async_smem();
+                tc_fence_after();
+                const uint32_t pa = __shfl_sync(0xffffffffu, pb + (j * kPktStride >> 4), 0);
+                const uint32_t va = __shfl_sync(0xffffffffu, vb + (stage * kVTileBytes >> 4), 0);
+                const uint32_t acc = __shfl_sync(0xffffffffu, t > 0 ? 1u : 0u, 0);
+                if (elect_one()) {
+#pragma unroll
+                    for (int ks = 0; ks < kKeys / 16; ++ks)
+#pragma unroll
+                        for (int nh = 0; nh < 2; ++nh)
+                            mma_f16_ss_lo(tm + nh * 256, pa + (ks * 32 >> 4), p_hi,
+                                          va + ((nh * 4 * kBlockBytes + ks * 2 * 1024) >> 4), v_hi, idesc, ks > 0 ? 1u : acc);
+                    mma_commit(&c.xempty[stage]);
+                    mma_commit(&c.pvdone[j]);
+                    mma_commit_multicast(&c.pfree[j], (uint16_t)0x1);
+                }
+                __syncwarp();
+            }
+            if (!ok) abort_cta(c, g.status);
+            if (elect_one()) mma_commit(&c.done);
+            __syncwarp();
+            warp_wait(&c.done, 0);
         } else if (warp == 1) {
             if (lane == 0) {
                 const uint32_t idesc = idesc_f16_f32_major(kHq, 256, 1, 0, 1);

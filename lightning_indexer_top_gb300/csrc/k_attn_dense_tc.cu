@@ -410,8 +410,8 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
             const uint64_t kmajor = desc_sw128_kmajor(0, 1024), mnmajor = desc_sw128_mnmajor(0, kColBlock, 1024);
             const uint32_t k_hi = desc_hi(kmajor), v_hi = desc_hi(mnmajor), k_lo = (uint32_t)kmajor, v_lo = (uint32_t)mnmajor;
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-            const uint32_t qa = __shfl_sync(0xffffffffu, k_lo + ((smem_u32(smem) + i * C::kQTile) >> 4), 0);
-            const uint32_t kb = k_lo + (smem_u32(kt) >> 4), vb = v_lo + (smem_u32(vt) >> 4);
+            const uint32_t qa = __shfl_sync(0xffffffffu, k_lo + desc_addr(smem) + (i * C::kQTile >> 4), 0);
+            const uint32_t kb = k_lo + desc_addr(kt), vb = v_lo + desc_addr(vt);
             const uint32_t ts = __shfl_sync(0xffffffffu, tm + i * kKeys, 0);
             const uint32_t to = __shfl_sync(0xffffffffu, tm + C::kOCol + i * D, 0);
             int sk = 0, kph = 0, sv = 0, vph = 0;     // ring positions of the K tile and the V tile to use next

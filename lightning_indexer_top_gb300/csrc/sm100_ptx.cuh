@@ -363,6 +363,7 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32_major(int M, int N, int ab_
 // The MMA forms with a descriptor as two words (the low one holds the address, the high one is a constant), for
 // a warp that runs its issue loop together and elects a lane for each group of products: operands that the
 // compiler can see to be the same in all lanes stay in uniform registers from one product to the next.
+__device__ __forceinline__ uint32_t desc_addr(const void* p) { return (smem_u32(p) & 0x3FFFFu) >> 4; }   // (the CTA's rank is above)
 __device__ __forceinline__ uint32_t desc_hi(uint64_t d) { return (uint32_t)(d >> 32); }
 
 __device__ __forceinline__ void mma_f16_ss_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
