@@ -78,7 +78,7 @@ size_t dense_attn_workspace_size(idx_dtype dtype, int32_t n_seq, int32_t n_q_per
     // (a call whose pages or addresses the tensor-core kernel does not take splits as far as this reaches)
     const bool tc = dtype != IDX_F32 && dk <= 128 && dv <= 128 && dk % 8 == 0 && dv % 8 == 0;
     const int splits = want_splits(dtype, n_seq, n_q_per_seq, max_n_kv, n_q_heads, n_kv_heads, dk, dv, tc);
-    return splits > 1 ? splits * split_bytes((int64_t)n_seq * n_q_per_seq, n_q_heads, dv) : 0;
+    return splits > kDenseCluster ? splits * split_bytes((int64_t)n_seq * n_q_per_seq, n_q_heads, dv) : 0;
 }
 
 idx_status dense_attn(const void* q, idx_dtype dtype, int32_t n_q_heads, int32_t n_kv_heads, int32_t dk, int32_t dv,
@@ -138,8 +138,8 @@ idx_status dense_attn(const void* q, idx_dtype dtype, int32_t n_q_heads, int32_t
     const int64_t fit = workspace ? (int64_t)(workspace_bytes / per_split) : 0;
     const bool tc = dense_tc_supported(a, dtype, g);
     int64_t splits = want_splits(dtype, batch.n_seq, batch.n_q_per_seq, batch.max_n_kv, n_q_heads, n_kv_heads, dk, dv, tc);
-    if (splits > fit) splits = fit;
-    if (splits < 1) splits = 1;
+    // up to kDenseCluster splits are a cluster and need no workspace
+    if (splits > kDenseCluster && splits > fit) splits = fit > kDenseCluster ? fit : kDenseCluster;
     // keys per split: whole tiles; fewer splits where that leaves some without keys
     const int64_t unit = tc ? kDenseTcKeys : 1;
     int64_t kps = ((int64_t)batch.max_n_kv + splits - 1) / splits;
@@ -149,11 +149,12 @@ idx_status dense_attn(const void* q, idx_dtype dtype, int32_t n_q_heads, int32_t
     if (kps > INT32_MAX) kps = INT32_MAX;   // (one split)
     a.splits = (int32_t)splits;
     a.kps = (int32_t)kps;
-    a.part_o = splits > 1 ? static_cast<float*>(workspace) : nullptr;
-    a.part_ml = splits > 1 ? a.part_o + (size_t)n_rows * n_q_heads * dv * splits : nullptr;
+    const bool apart = splits > kDenseCluster;
+    a.part_o = apart ? static_cast<float*>(workspace) : nullptr;
+    a.part_ml = apart ? a.part_o + (size_t)n_rows * n_q_heads * dv * splits : nullptr;
     cudaError_t e = tc ? launch_dense_tc(a, dtype, g, st) : cudaErrorNotSupported;
     if (e == cudaErrorNotSupported) e = launch_dense_generic(a, dtype, g, st);
-    if (e == cudaSuccess && splits > 1) e = launch_dense_combine(a, dtype, n_rows, st);
+    if (e == cudaSuccess && apart) e = launch_dense_combine(a, dtype, n_rows, st);
     return cuda_status(e, what);
 }
 

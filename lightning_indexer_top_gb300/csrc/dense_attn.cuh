@@ -9,6 +9,16 @@ namespace lidx {
 
 constexpr int kDenseMaxSplits = 128;   // key splits, at most (the merge keeps their weights in a warp)
 
+constexpr int kDenseCluster = 8;       // splits that a cluster merges itself, at most
+
+// the same shared-memory variable of the cluster's CTA `rank`, as a generic address
+template <typename T>
+__device__ __forceinline__ T* of_cta(T* p, uint32_t rank) {
+    uint64_t r;
+    asm("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
+    return reinterpret_cast<T*>(r);
+}
+
 struct DenseArgs {
     const void* q;
     int32_t Hq, Hkv, dk, dv;
@@ -20,7 +30,8 @@ struct DenseArgs {
     idx_attn_mods mods;
     void* out;                // of q's type
     float* lse;               // or NULL
-    int32_t splits;           // key splits; > 1: partial results go to part_o / part_ml
+    int32_t splits;           // key splits; > 1: partial results go to part_o / part_ml, or, without those (at most
+                              // kDenseCluster splits), the splits are a cluster that merges them
     int32_t kps;              // keys of the position line per split
     float* part_o;            // [row * Hq + head][split][dv] unnormalised
     float* part_ml;           // [row * Hq + head][split][2]: maximum (natural-log units), sum

@@ -324,14 +324,18 @@ __global__ void __launch_bounds__(kThreads) dense_generic_kernel(DenseArgs a, Ge
             values(std::true_type{});
     }
 
-    // ---- output: l per row through shared memory
+    // ---- output: m and l per row through shared memory
+    const bool merge = a.splits > 1 && !a.part_o;       // the splits are the CTAs of a cluster
+    float* m_s = slope_s;
+    float* l_s = alpha_s;
     __syncthreads();
     if (sk == 0) {
         const bool none = lo_s[srow] >= hi_s[srow];
         const float l = none ? 0.f : l_run;
-        alpha_s[srow] = l;
+        l_s[srow] = l;
+        m_s[srow] = m_run;
         const int64_t m = m0 + srow;
-        if (m < m_end) {
+        if (m < m_end && !merge) {
             const int64_t rh = ((int64_t)b * g.T + m / G) * a.Hq + gkv * G + m % G;
             if (a.splits > 1) {
                 a.part_ml[(rh * a.splits + split) * 2] = m_run;
@@ -342,13 +346,14 @@ __global__ void __launch_bounds__(kThreads) dense_generic_kernel(DenseArgs a, Ge
         }
     }
     __syncthreads();
+    float* o_s = qs;                                    // [R][DV], merge: over Q, K and V, which nobody reads any more
 #pragma unroll
     for (int i = 0; i < S::kRowsPer; ++i) {
         const int rr = vg * S::kRowsPer + i;
         const int64_t m = m0 + rr;
         if (m >= m_end) continue;
         const int64_t rh = ((int64_t)b * g.T + m / G) * a.Hq + gkv * G + m % G;
-        const float l = alpha_s[rr];
+        const float l = l_s[rr];
         const float inv = a.splits > 1 ? 1.f : 1.f / l;
 #pragma unroll
         for (int c = 0; c < S::kCol4; ++c)
@@ -357,11 +362,45 @@ __global__ void __launch_bounds__(kThreads) dense_generic_kernel(DenseArgs a, Ge
                 const int col = 4 * cg + 4 * S::kColGroups * c + e;
                 if (col >= a.dv) continue;
                 const float x = l == 0.f ? 0.f : o[i][4 * c + e] * inv;
-                if (a.splits > 1)
+                if (merge)
+                    o_s[rr * DV + col] = x;
+                else if (a.splits > 1)
                     a.part_o[(rh * a.splits + split) * a.dv + col] = x;
                 else
                     static_cast<T*>(a.out)[rh * a.dv + col] = from_f32<T>(x);
             }
+    }
+    if (merge) {
+        // each CTA merges its share of the elements, in the order of the splits
+        sm100::cluster_sync();
+        const int rows = (int)min((int64_t)R, m_end - m0);
+        for (int e = split * kThreads + tid; e < rows * a.dv; e += a.splits * kThreads) {
+            const int rr = e / a.dv, col = e - rr * a.dv;
+            float mx[kDenseCluster], lx[kDenseCluster], ox[kDenseCluster];
+#pragma unroll
+            for (int s = 0; s < kDenseCluster; ++s) {
+                const int from = s < a.splits ? s : 0;
+                mx[s] = *of_cta(m_s + rr, from);
+                lx[s] = s < a.splits ? *of_cta(l_s + rr, from) : 0.f;
+                ox[s] = *of_cta(o_s + rr * DV + col, from);
+            }
+            float M = -INFINITY, den = 0.f, acc = 0.f;
+#pragma unroll
+            for (int s = 0; s < kDenseCluster; ++s)
+                if (lx[s] != 0.f) M = fmaxf(M, mx[s]);
+#pragma unroll
+            for (int s = 0; s < kDenseCluster; ++s)
+                if (lx[s] != 0.f) {
+                    const float w = expf(mx[s] - M);
+                    den = fmaf(w, lx[s], den);
+                    acc = fmaf(w, ox[s], acc);
+                }
+            const int64_t m = m0 + rr;
+            const int64_t rh = ((int64_t)b * g.T + m / G) * a.Hq + gkv * G + m % G;
+            static_cast<T*>(a.out)[rh * a.dv + col] = from_f32<T>(den == 0.f ? 0.f : acc / den);
+            if (a.lse && col == 0) a.lse[rh] = den == 0.f ? -INFINITY : M + logf(den);
+        }
+        sm100::cluster_sync();      // no CTA leaves while another reads its memory
     }
 }
 
@@ -459,7 +498,8 @@ cudaError_t run(const DenseArgs& a, const Geom& g, cudaStream_t st) {
         const size_t sm = smem_bytes(R, dvp, a.dk, !a.v);
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
         if (e != cudaSuccess) return e;
-        return launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), sm, st, a, g, (int)tiles, vec);
+        return launch_pdl_cluster(kern, dim3((unsigned)grid), dim3(kThreads), sm, st,
+                                  a.splits > 1 && !a.part_o ? a.splits : 1, a, g, (int)tiles, vec);
     };
     if (R == 64) return a.dv <= 64 ? go(dense_generic_kernel<T, 64, 64>, 64) : go(dense_generic_kernel<T, 64, 128>, 128);
     return a.dv <= 128 ? go(dense_generic_kernel<T, 16, 128>, 128) : go(dense_generic_kernel<T, 16, 512>, 512);

@@ -55,9 +55,10 @@ constexpr int kOtherWarps = 4;
 
 // Scores of 64 keys in two buffers per row tile instead of 128 in one: S of the next step is made while the softmax is
 // on this one.  It costs the tensor pipe a fifth (see above), so it is for where the softmax takes longer than the
-// products: capped or biased scores, narrow heads, and a CTA with one row tile, whose steps nothing else overlaps.
-template <int D, int kTiles, bool kMods>
-constexpr bool kDoubleS = kMods || D == 64 || kTiles == 1;
+// products: capped or biased scores, and narrow heads.  (A decode step's CTA, one row tile and bound by its loads: 150 us
+// with one buffer, 156 with two.)
+template <int D, bool kMods>
+constexpr bool kDoubleS = kMods || D == 64;
 
 template <int D, int kTiles>
 struct Cfg {
@@ -73,6 +74,10 @@ struct Cfg {
     static constexpr int kKOff = kTiles * kQTile;
     static constexpr int kVOff = kKOff + kStagesK * kTileBytes;
     static constexpr int kCtlOff = kVOff + kStagesV * kTileBytes;
+    // merged splits: the rows' results over the rings, then their maxima (log2 units) and sums
+    static constexpr int kMergeRows = kTiles * ((kQRows + 31) / 32 * 32);
+    static constexpr int kMlOff = kMergeRows * D * 4;
+    static_assert(kMlOff + kMergeRows * 8 <= kCtlOff, "rows kept for the merge");
     static constexpr int kThreads = 32 * kOtherWarps + kRows * kTiles;
     static constexpr int kTmemCols = kTiles == 2 ? 512 : 256;
     static constexpr int kOCol = kTiles * kKeys;      // S of row tile i at i*kKeys, O at kOCol + i*D
@@ -111,11 +116,10 @@ struct TcArgs {
 };
 
 // A row's attention key by key, for the thread that owns it: the rare way, see the top.  q, K and V as stored, f32
-// sums; writes the output (or the split's partial result) and lse.
+// sums.  acc gets the unnormalised values, ml the maximum (log2 units) and the sum.
 template <typename T>
 __device__ __noinline__ void scalar_row(const DenseArgs& a, const Geom& g, int b, int gkv, int64_t rh, int h, Interval iv,
-                                        int split) {
-    float acc[128];
+                                        int split, float* acc, float* ml) {
     const T* q = static_cast<const T*>(a.q) + rh * a.dk;
     for (int c = 0; c < a.dv; ++c) acc[c] = 0.f;
     float m = -INFINITY, l = 0.f;
@@ -143,15 +147,8 @@ __device__ __noinline__ void scalar_row(const DenseArgs& a, const Geom& g, int b
         l = fmaf(l, al, w);
         for (int c = 0; c < a.dv; ++c) acc[c] = fmaf(w, to_f32(v[c]), al == 1.f ? acc[c] : acc[c] * al);
     }
-    if (a.splits > 1) {
-        const int64_t u = rh * a.splits + split;
-        a.part_ml[u * 2] = m * kLn2;
-        a.part_ml[u * 2 + 1] = l;
-        for (int c = 0; c < a.dv; ++c) a.part_o[u * a.dv + c] = l == 0.f ? 0.f : acc[c];
-    } else {
-        if (a.lse) a.lse[rh] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-        for (int c = 0; c < a.dv; ++c) static_cast<T*>(a.out)[rh * a.dv + c] = from_f32<T>(l == 0.f ? 0.f : acc[c] / l);
-    }
+    ml[0] = m;
+    ml[1] = l;
 }
 
 // 32 columns of a row into its warp's staging rows of W columns (16-byte pieces, swizzled by the row)
@@ -211,7 +208,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr float kShift = kBf16 ? 0.f : 7.f;     // P is kept this much (log2) larger
     constexpr float kTop = kShift + 8.f;
-    constexpr bool kDouble = kDoubleS<D, kTiles, kMods>;
+    constexpr bool kDouble = kDoubleS<D, kMods>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* kt = smem + C::kKOff;
@@ -220,14 +217,15 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     const DenseArgs& a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = a.Hq / a.Hkv;
-    // units: key split fastest, then (sequence, kv head), then the row tiles from the last one on (under
-    // the causal bound they see the most keys)
+    // units: key split fastest (the splits may be a cluster), then kv head (the heads of a cache row are neighbours), then
+    // sequence, then the row tiles from the last one on (under the causal bound they see the most keys)
     int64_t u = blockIdx.x;
     const int split = (int)(u % a.splits);
     u /= a.splits;
-    const int bg = (int)(u % ((int64_t)g.B * a.Hkv));
-    const int tile = p.tiles - 1 - (int)(u / ((int64_t)g.B * a.Hkv));
-    const int gkv = bg % a.Hkv, b = bg / a.Hkv;
+    const int gkv = (int)(u % a.Hkv);
+    u /= a.Hkv;
+    const int b = (int)(u % g.B);
+    const int tile = p.tiles - 1 - (int)(u / g.B);
     const int64_t m0 = (int64_t)tile * (kTiles * kRows);
     const int n_rows = (int)min((int64_t)g.T * G - m0, (int64_t)kTiles * kRows);   // packed rows of this CTA
     const int n_tiles = (n_rows + kRows - 1) / kRows;                              // row tiles with rows
@@ -524,13 +522,14 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         }
     }
     // -------------------------------------------------------------- softmax and output (thread = row)
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t to = tmem + lane_off + C::kOCol + rt * D;
+    const bool merge = a.splits > 1 && !a.part_o;     // the splits are the CTAs of a cluster
+    float m_used = -INFINITY, l_run = 0.f;
+    bool ok = n > 0;
     if (warp_rows) {
-        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lane_off + rt * kKeys;
-        const uint32_t to = tmem + lane_off + C::kOCol + rt * D;
         const Score sc = make_score(a, a.mods.slopes && has_row ? a.mods.slopes[h] : 0.f);
-        float m_used = -INFINITY, l_run = 0.f;
-        bool ok = n > 0;
         auto timed_out = [&] {
             *(volatile int*)&c.abort = 1;
             flag(g.status, IDX_ERR_TIMEOUT);
@@ -644,54 +643,110 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         }
         if (ok) ok = warp_wait(&c.odone[rt], 0);
         tc_fence_after();
+    }
+    // merged in the cluster, the rows' unnormalised results are kept over all of the ring
+    if (merge) __syncthreads();
+    if (warp_rows) {
         const bool some = iv.lo < iv.hi;
         const int64_t rh = qrow * a.Hq + h;
         // every tile has been loaded and looked over by now: each PV product waited for that
         const bool by_key = ok && *(volatile int*)&c.dirty != 0;
+        float acc[D];
         if (by_key) {
-            if (has_row) scalar_row<T>(a, g, b, gkv, rh, h, iv, split);
+            float ml[2] = {-INFINITY, 0.f};
+            if (has_row && some) scalar_row<T>(a, g, b, gkv, rh, h, iv, split, acc, ml);
+            m_used = ml[0];
+            l_run = ml[1];
             __syncwarp();
-        } else {
-            const float l = some && ok ? l_run : 0.f;
-            const float inv = l == 0.f ? 0.f : a.splits > 1 ? 1.f : 1.f / l;
-            if (has_row) {
-                if (a.splits > 1) {
-                    a.part_ml[(rh * a.splits + split) * 2] = m_used * kLn2;
-                    a.part_ml[(rh * a.splits + split) * 2 + 1] = l;
-                } else if (a.lse) {
-                    a.lse[rh] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * kLn2;
-                }
-            }
-            // through shared memory (Q's, and past it K's: no product reads them any more), so that whole rows are
-            // written; normalised (a split's partial: as they are)
-            uint8_t* rows = smem + rt * C::kQTile + (warp & 3) * (32 * D * 2);
-            const bool parts = a.splits > 1;
-            const int W = parts ? D / 2 : D;
-#pragma unroll 1
-            for (int c0 = 0; c0 < a.dv; c0 += W) {
-#pragma unroll 1
-                for (int x = 0; x < W; x += 32) {
-                    uint32_t u32[32];
-                    float o[32];
-                    if (ok) {
-                        tmem_ld_32x32b_x32_raw(to + c0 + x, u32);
-                        tmem_ld_wait_for(u32);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0.f : __uint_as_float(u32[i]) * inv;
-                    if (parts)
-                        stage_cols<float, D / 2>(rows, lane, x, o);
-                    else
-                        stage_cols<T, D>(rows, lane, x, o);
-                }
-                if (parts)
-                    store_rows<float, D / 2>(a.part_o + c0, (rh * a.splits + split) * a.dv, n_rows - (r - lane), rows,
-                                             min(W, a.dv - c0));
-                else
-                    store_rows<T, D>(static_cast<T*>(a.out), rh * a.dv, n_rows - (r - lane), rows, a.dv);
+        }
+        const float l = some && ok ? l_run : 0.f;
+        const float inv = l == 0.f ? 0.f : a.splits > 1 ? 1.f : 1.f / l;
+        if (merge) {
+            *reinterpret_cast<float2*>(smem + C::kMlOff + r * 8) = make_float2(m_used, l);
+        } else if (has_row) {
+            if (a.splits > 1) {
+                a.part_ml[(rh * a.splits + split) * 2] = m_used * kLn2;
+                a.part_ml[(rh * a.splits + split) * 2 + 1] = l;
+            } else if (a.lse) {
+                a.lse[rh] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * kLn2;
             }
         }
+        // through shared memory (Q's, and past it K's: no product reads them any more), so that whole rows are written;
+        // normalised (a split's partial: as they are)
+        uint8_t* rows = merge ? smem + (rt * kRows + (warp & 3) * 32) * (D * 4) : smem + rt * C::kQTile + (warp & 3) * (32 * D * 2);
+        const bool parts = a.splits > 1;
+        const int W = merge || !parts ? D : D / 2;
+#pragma unroll 1
+        for (int c0 = 0; c0 < a.dv; c0 += W) {
+#pragma unroll 1
+            for (int x = 0; x < W; x += 32) {
+                uint32_t u32[32];
+                float o[32];
+                if (by_key) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) u32[i] = __float_as_uint(acc[c0 + x + i]);
+                } else if (ok) {
+                    tmem_ld_32x32b_x32_raw(to + c0 + x, u32);
+                    tmem_ld_wait_for(u32);
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0.f : __uint_as_float(u32[i]) * inv;
+                if (merge)
+                    stage_cols<float, D>(rows, lane, x, o);
+                else if (parts)
+                    stage_cols<float, D / 2>(rows, lane, x, o);
+                else
+                    stage_cols<T, D>(rows, lane, x, o);
+            }
+            if (merge) break;
+            if (parts)
+                store_rows<float, D / 2>(a.part_o + c0, (rh * a.splits + split) * a.dv, n_rows - (r - lane), rows,
+                                         min(W, a.dv - c0));
+            else
+                store_rows<T, D>(static_cast<T*>(a.out), rh * a.dv, n_rows - (r - lane), rows, a.dv);
+        }
         tc_fence_before();
+    }
+    if (merge) {
+        // ---------------------------------------------------------- the splits' results: each CTA merges its share of
+        // the rows' 8-column pieces, in the order of the splits
+        cluster_sync();
+        const int pieces = a.dv / 8;
+        for (int e = split * C::kThreads + threadIdx.x; e < n_rows * pieces; e += a.splits * C::kThreads) {
+            const int row = e / pieces, pc = e - row * pieces;
+            float M = -INFINITY;
+            for (int s = 0; s < a.splits; ++s) {
+                const float2 ml = *reinterpret_cast<const float2*>(of_cta(smem + C::kMlOff + row * 8, s));
+                if (ml.y != 0.f) M = fmaxf(M, ml.x);
+            }
+            float den = 0.f, o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = 0.f;
+            for (int s = 0; s < a.splits; ++s) {
+                const float2 ml = *reinterpret_cast<const float2*>(of_cta(smem + C::kMlOff + row * 8, s));
+                if (ml.y == 0.f) continue;
+                const float w = exp2f(ml.x - M);
+                den = fmaf(w, ml.y, den);
+                const uint8_t* x = of_cta(smem + row * (D * 4), s);
+                const float4 x0 = *reinterpret_cast<const float4*>(x + (((2 * pc) ^ (row & 7)) << 4));
+                const float4 x1 = *reinterpret_cast<const float4*>(x + (((2 * pc + 1) ^ (row & 7)) << 4));
+                o[0] = fmaf(w, x0.x, o[0]);
+                o[1] = fmaf(w, x0.y, o[1]);
+                o[2] = fmaf(w, x0.z, o[2]);
+                o[3] = fmaf(w, x0.w, o[3]);
+                o[4] = fmaf(w, x1.x, o[4]);
+                o[5] = fmaf(w, x1.y, o[5]);
+                o[6] = fmaf(w, x1.z, o[6]);
+                o[7] = fmaf(w, x1.w, o[7]);
+            }
+            const float inv = den == 0.f ? 0.f : 1.f / den;
+            const int64_t rh = ((int64_t)b * g.T + t00 + (h00 + row) / G) * a.Hq + gkv * G + (h00 + row) % G;
+            if (a.lse && pc == 0) a.lse[rh] = den == 0.f ? -INFINITY : (M + log2f(den)) * kLn2;
+            *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + rh * a.dv + pc * 8) =
+                make_uint4(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv),
+                           pack2<T>(o[4] * inv, o[5] * inv), pack2<T>(o[6] * inv, o[7] * inv));
+        }
+        cluster_sync();     // no CTA leaves while another reads its memory
     }
     __syncthreads();
     tc_fence_after();
@@ -716,7 +771,8 @@ cudaError_t go(const TcArgs& p, const Geom& g, const CUtensorMap& km, const CUte
     auto kern = dense_tc_kernel<T, D, kTiles, kMods>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3((unsigned)grid), dim3(C::kThreads), sm, st, p, g, km, vm);
+    return launch_pdl_cluster(kern, dim3((unsigned)grid), dim3(C::kThreads), sm, st,
+                              p.a.splits > 1 && !p.a.part_o ? p.a.splits : 1, p, g, km, vm);
 }
 
 template <typename T>

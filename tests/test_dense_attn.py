@@ -391,7 +391,7 @@ def test_ragged_starts_and_neighbours_untouched():
 @pytest.mark.gpu
 def test_workspace_sizes_change_splits_not_results():
     for dtype, heads in ((torch.bfloat16, (8, 2, 128)), (torch.float32, (8, 2, 64)), (torch.bfloat16, (4, 1, 40))):
-        c = Case([3000, 1700], 1, *heads, dtype=dtype, page=64, seed=14)
+        c = Case([9000, 1700], 1, *heads, dtype=dtype, page=64, seed=14)      # more splits than a cluster merges
         need = L.dense_attn_workspace_size(dtype, 2, 1, c.N, heads[0], heads[1], heads[2], heads[2])
         assert need > 0
         for n in (16, need // 3 // 16 * 16, need // 2 // 16 * 16, need):
