@@ -501,7 +501,9 @@ __device__ __forceinline__ void mla_run(const MlaSmem& sm, uint32_t tmem, uint32
                 }
                 const uint32_t slot = mapa(pkts + j * kPktStride, 1);
                 const uint32_t rbar = mapa(&c.pfull[j], 1);
-                if (h == 0) mbar_arrive_expect_tx_remote(rbar, kPktBytes);
+                // (the dense feed's sum and maximum go with the last packet alone)
+                const bool totals = !Feed::kDense || t == u.n_tiles - 1;
+                if (h == 0) mbar_arrive_expect_tx_remote(rbar, kPktBytes - (totals ? 0 : 2 * kHq * 4));
                 const uint32_t rowp = slot + (uint32_t)((h >> 3) * 1024 + (h & 7) * 128);
 #pragma unroll
                 for (int ch = 0; ch < 8; ++ch)
@@ -509,8 +511,10 @@ __device__ __forceinline__ void mla_run(const MlaSmem& sm, uint32_t tmem, uint32
                                 make_uint4(pk[4 * ch], pk[4 * ch + 1], pk[4 * ch + 2], pk[4 * ch + 3]), rbar);
                 const uint32_t tail = slot + kPBytes + (uint32_t)h * 4;
                 st_async_f32(tail + offsetof(PktTail, alpha), alpha, rbar);
-                st_async_f32(tail + offsetof(PktTail, l), lsum, rbar);
-                st_async_f32(tail + offsetof(PktTail, m), m_used, rbar);
+                if (totals) {
+                    st_async_f32(tail + offsetof(PktTail, l), lsum, rbar);
+                    st_async_f32(tail + offsetof(PktTail, m), m_used, rbar);
+                }
             }
             // rank 1's last arrivals on pfree land before this CTA may leave
             const int n = min(u.n_tiles, 2);

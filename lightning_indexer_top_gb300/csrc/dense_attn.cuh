@@ -162,19 +162,14 @@ __device__ __forceinline__ void modify(float (&s)[N], const Score& sc, float d0,
         for (int i = 0; i < N; i += 2) unpair(mul2(pair(s[i], s[i + 1]), c), s[i], s[i + 1]);
     }
     if (sc.biased) {
-        // key minus position, counted up in exact steps
-        uint64_t d = pair(-d0, 1.f - d0);
-        const uint64_t two = pair(2.f, 2.f), sl = past ? pair(sc.slope, sc.slope) : pair(-sc.slope, -sc.slope);
+        if (past) {
+            const uint64_t sl = pair(sc.slope, sc.slope), base = pair(-sc.slope * d0, -sc.slope * d0);
 #pragma unroll
-        for (int i = 0; i < N; i += 2) {
-            uint64_t e = d;
-            if (!past) {
-                float x, y;
-                unpair(d, x, y);
-                e = pair(fabsf(x), fabsf(y));
-            }
-            unpair(fma2(sl, e, pair(s[i], s[i + 1])), s[i], s[i + 1]);
-            d = add2(d, two);
+            for (int i = 0; i < N; i += 2)
+                unpair(add2(pair(s[i], s[i + 1]), fma2(sl, pair((float)i, (float)(i + 1)), base)), s[i], s[i + 1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) s[i] = fmaf(-sc.slope, fabsf(d0 - (float)i), s[i]);
         }
     }
 }

@@ -186,45 +186,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
 
-// out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s, block (row, 16 columns), thread = head
+// out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s, block (row, kCols columns), thread = head
+constexpr int kCols = 8;
 __global__ void __launch_bounds__(kHq) dense_mla_combine_kernel(DenseArgs a) {
     pdl_trigger();
     pdl_wait();
     const int64_t r = blockIdx.x;
     const int h = threadIdx.x;
+    // the splits' loads kBatch at a time
+    constexpr int kBatch = 8;
     float M = -INFINITY;
-    for (int s = 0; s < a.splits; ++s) {
-        const float* ml = a.part_ml + ((r * a.splits + s) * kHq + h) * 2;
-        if (ml[1] != 0.f) M = fmaxf(M, ml[0]);
+    for (int s0 = 0; s0 < a.splits; s0 += kBatch) {
+        float2 ml[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            ml[k] = s0 + k < a.splits ? reinterpret_cast<const float2*>(a.part_ml)[(r * a.splits + s0 + k) * kHq + h]
+                                      : make_float2(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (ml[k].y != 0.f) M = fmaxf(M, ml[k].x);
     }
-    float acc[16], den = 0.f;
+    float acc[kCols], den = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-    for (int s = 0; s < a.splits; ++s) {
-        const int64_t u = r * a.splits + s;
-        const float l = a.part_ml[(u * kHq + h) * 2 + 1];
-        if (l == 0.f) continue;
-        const float w = exp2f(a.part_ml[(u * kHq + h) * 2] - M);
-        den += w * l;
-        const float4* o = reinterpret_cast<const float4*>(a.part_o + u * (int64_t)kDv * kHq) + (int64_t)blockIdx.y * 4 * kHq + h;
+    for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
+    for (int s0 = 0; s0 < a.splits; s0 += kBatch) {
+        float2 ml[kBatch];
+        float4 x[kBatch][kCols / 4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float4 x = o[i * kHq];
-            acc[4 * i] = fmaf(w, x.x, acc[4 * i]);
-            acc[4 * i + 1] = fmaf(w, x.y, acc[4 * i + 1]);
-            acc[4 * i + 2] = fmaf(w, x.z, acc[4 * i + 2]);
-            acc[4 * i + 3] = fmaf(w, x.w, acc[4 * i + 3]);
+        for (int k = 0; k < kBatch; ++k) {
+            const int64_t u = r * a.splits + min(s0 + k, a.splits - 1);
+            ml[k] = reinterpret_cast<const float2*>(a.part_ml)[u * kHq + h];
+#pragma unroll
+            for (int i = 0; i < kCols / 4; ++i)
+                x[k][i] = reinterpret_cast<const float4*>(a.part_o + u * (int64_t)kDv * kHq)[(int64_t)(blockIdx.y * (kCols / 4) + i) * kHq + h];
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const bool in = s0 + k < a.splits && ml[k].y != 0.f;
+            const float w = in ? exp2f(ml[k].x - M) : 0.f;
+            den += in ? w * ml[k].y : 0.f;
+#pragma unroll
+            for (int i = 0; i < kCols / 4; ++i) {
+                // (a split without keys wrote zeros)
+                acc[4 * i] = fmaf(w, x[k][i].x, acc[4 * i]);
+                acc[4 * i + 1] = fmaf(w, x[k][i].y, acc[4 * i + 1]);
+                acc[4 * i + 2] = fmaf(w, x[k][i].z, acc[4 * i + 2]);
+                acc[4 * i + 3] = fmaf(w, x[k][i].w, acc[4 * i + 3]);
+            }
         }
     }
     const float inv = den == 0.f ? 0.f : 1.f / den;
     if (a.lse && blockIdx.y == 0) a.lse[r * kHq + h] = den == 0.f ? -INFINITY : (M + log2f(den)) * kLn2;
-    uint4 w[2];
-    __nv_bfloat162* b = reinterpret_cast<__nv_bfloat162*>(w);
+    uint4 w;
+    __nv_bfloat162* b = reinterpret_cast<__nv_bfloat162*>(&w);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = __floats2bfloat162_rn(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-    uint4* d = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (r * kHq + h) * (int64_t)kDv + blockIdx.y * 16);
-    d[0] = w[0];
-    d[1] = w[1];
+    for (int i = 0; i < 4; ++i) b[i] = __floats2bfloat162_rn(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (r * kHq + h) * (int64_t)kDv + blockIdx.y * kCols) = w;
 }
 
 int box_rows(int page_size) {
@@ -295,7 +312,7 @@ cudaError_t launch_dense_mla(const DenseArgs& args, const Geom& g, void* ws, siz
     if (2 * clusters > INT32_MAX) return cudaErrorNotSupported;
     e = launch_pdl(kern, dim3((unsigned)(2 * clusters)), dim3(kThreads), kSmemBytes, st, p, g, n_units, map);
     if (e != cudaSuccess || splits == 1) return e;
-    return launch_pdl(dense_mla_combine_kernel, dim3((unsigned)n_rows, kDv / 16), dim3(kHq), 0, st, a);
+    return launch_pdl(dense_mla_combine_kernel, dim3((unsigned)n_rows, kDv / kCols), dim3(kHq), 0, st, a);
 }
 
 }  // namespace lidx
