@@ -469,17 +469,22 @@ int32_t sparse_decode_step_fused(int64_t n_rows, int32_t n_q_per_seq, int32_t ma
  *   q, k, v, dtype, strides, kv_rows   as sparse_attn_decode (v NULL: the MLA
  *              latent form), K and V rows addressed by batch.
  *   mods       HOST pointer to the options below, or NULL for none of them.
- *   out        [B*T, Hq, dv] contiguous, of q's dtype.
+ *   out        [B*T, Hq, dv] contiguous, of q's dtype; no input may overlap it.
  *   lse        f32 [B*T, Hq] or NULL.
  *   workspace  dense_attn_workspace_size(...) bytes, 16-byte aligned: the partial
- *              results of key splits.  With less (or NULL) the keys are split
- *              less or not at all, with the same results up to rounding.  Calls
- *              whose work overlaps on the GPU need workspaces of their own.
+ *              results of more key splits than one launch merges itself (for the
+ *              latent of 128 heads, of any).  With less (or NULL) the keys are
+ *              split less, with the same results up to rounding.  Calls whose
+ *              work overlaps on the GPU need workspaces of their own.
  * Sums, maxima and outputs are accumulated in f32.  A key row outside the cache
  * (a page number out of range) is skipped and flagged (IDX_ERR_DEVICE_BOUNDS).
+ * 16-bit K and V of at most 128 columns (a multiple of 8) and the bf16 latent of 128
+ * heads (576 / 512) run on the tensor cores, given 16-byte aligned tensors and rows
+ * and pages of a multiple of 8 rows; the weights are then rounded to dtype for the
+ * second product.  Everything else runs on the CUDA cores.
  * Errors: those of sparse_attn_decode's arguments; softcap or window negative,
- * softcap not finite, window, slopes or prefix_len without q_pos: INVALID_ARG;
- * max_n_kv > 2^31 - 1025: UNSUPPORTED.
+ * softcap or scale / softcap not finite, window, slopes or prefix_len without
+ * q_pos: INVALID_ARG; max_n_kv > 2^31 - 1025: UNSUPPORTED.
  */
 typedef struct idx_attn_mods {
     float softcap;             /* 0: scores are not capped */

@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kThreads) dense_generic_kernel(DenseArgs a, Ge
     const int b = (int)(u / a.Hkv);
     const int64_t m0 = (int64_t)tile * R;        // first packed row
     const int64_t m_end = (int64_t)g.T * G;
-    pdl_trigger();
+    if (a.part_o) pdl_trigger();     // (the merge follows; results are not handed on early, see lidx_internal.cuh)
     pdl_wait();
     const int n_kv = seq_n_kv(g, b);
 
@@ -409,7 +409,6 @@ __global__ void __launch_bounds__(kThreads) dense_generic_kernel(DenseArgs a, Ge
 template <typename T, int V>
 __global__ void __launch_bounds__(128) dense_combine_kernel(DenseArgs a, int64_t n) {
     constexpr int kSplits = kDenseMaxSplits / 32, kBatch = 8;
-    pdl_trigger();
     pdl_wait();
     const int64_t rh = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;

@@ -137,7 +137,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5;
     const int64_t n_clusters = gridDim.x >> 1;
     const DenseArgs& a = p.a;
-    pdl_trigger();
+    if (a.part_o) pdl_trigger();     // (the merge follows; results are not handed on early, see lidx_internal.cuh)
     if (threadIdx.x == 0) {
         mla_init(c, 1);
         tma_prefetch_desc(&map);
@@ -189,7 +189,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s, block (row, kCols columns), thread = head
 constexpr int kCols = 8;
 __global__ void __launch_bounds__(kHq) dense_mla_combine_kernel(DenseArgs a) {
-    pdl_trigger();
     pdl_wait();
     const int64_t r = blockIdx.x;
     const int h = threadIdx.x;

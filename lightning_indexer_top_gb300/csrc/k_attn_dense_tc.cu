@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     const int n_rows = (int)min((int64_t)g.T * G - m0, (int64_t)kTiles * kRows);   // packed rows of this CTA
     const int n_tiles = (n_rows + kRows - 1) / kRows;                              // row tiles with rows
 
-    pdl_trigger();
+    if (a.part_o) pdl_trigger();     // (the merge follows; results are not handed on early, see lidx_internal.cuh)
     if (threadIdx.x == 0) {
         for (int i = 0; i < 3; ++i) {
             mbar_init(&c.kfull[i], 1);

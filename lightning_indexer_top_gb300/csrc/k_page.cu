@@ -63,7 +63,6 @@ __device__ __forceinline__ void copy_piece(const uint8_t* src, uint8_t* dst, int
 
 // a stream of reads and writes: HBM is what bounds it
 __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(Caches cs, Moves m, int32_t n_pages, int* status) {
-    pdl_trigger();
     pdl_wait();
     const int64_t n = m.n_dev ? *m.n_dev : m.n;
     for (int64_t w = blockIdx.x; w < n * cs.segs_total; w += gridDim.x) {
@@ -253,7 +252,6 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kPlanThreads) page
     const int gtid = rank * kPlanThreads + tid;            // of the cluster: rows are dealt out by thread ...
     const int gwarp = rank * kWarps + warp;                // ... or by warp
     constexpr int kAll = kCl * kPlanThreads, kAllWarps = kCl * kWarps;
-    pdl_trigger();
     pdl_wait();
     // ---- the requests; the held pages.  Nothing is copied unless the plan says so.
     bool bad = false;
@@ -415,7 +413,6 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kPlanThreads) page
     const int gwarp = rank * kWarps + warp;
     constexpr int kAllWarps = kCl * kWarps;
     const int64_t w_base = (int64_t)rank * bm.slice;
-    pdl_trigger();
     pdl_wait();
     for (int w = tid; w < bm.n_mine(); w += kPlanThreads) bm.mine[w] = held_bits(a.held, w_base + w, a.n_pages);
     sm100::cluster_sync();

@@ -45,6 +45,8 @@ struct Geom {
 // whole kernel, so its loads may move above pdl_wait or take the
 // non-coherent read-only path, and would then see the predecessor's data
 // before it is written.
+// A kernel whose results another call may read as a "pure input" (dense attention's output as a later call's q;
+// caches and tables after page operations) does not trigger: the next kernel then starts when it has ended.
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

@@ -238,6 +238,73 @@ def test_latent(dtype, T, Hq, page):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("mods", [dict(cap=4.0), dict(window=70), dict(slopes=True), dict(docs=50), dict(prefix=[300, 0, 20]),
+                                  dict(cap=30.0, slopes=True, prefix=[200, 60, 0], docs=20)])
+@pytest.mark.parametrize("T", [1, 4])
+def test_latent_modified_scores(mods, T):
+    for Hq in (128, 8):
+        c = Case([300, 65, 130], T, Hq, 1, 576, dv=512, dtype=torch.bfloat16, page=16, n_new=[T, 1, T], latent=True, seed=19,
+                 spread=2.0, **mods)
+        c.check(*c.run(), what=(mods, Hq))
+
+
+@pytest.mark.gpu
+def test_long_latent_without_a_workspace_and_with_one():
+    # more keys than one unit of the tensor-core kernel takes: split with a workspace, on the CUDA cores without
+    c = Case([5000, 2100], 1, 128, 1, 576, dv=512, dtype=torch.bfloat16, page=64, latent=True, seed=20)
+    c.check(*c.run())
+    c.check(*c.run(workspace=torch.empty(16, dtype=torch.uint8, device="cuda")))
+    n = L.dense_attn_workspace_size(torch.bfloat16, 2, 1, c.N, 128, 1, 576, 512)
+    c.check(*c.run(workspace=torch.empty(n // 2 // 16 * 16, dtype=torch.uint8, device="cuda")))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("page", [24, 192, 256, 8])
+@pytest.mark.parametrize("heads", [(4, 2, 128), (3, 1, 8)])
+def test_other_pages_and_narrow_heads(dtype, page, heads):
+    for T in (1, 70):
+        c = Case([500, 131, T], T, *heads, dtype=dtype, page=page, seed=22)
+        c.check(*c.run(), what=(page, T))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("scale", [0.0, -0.1])
+@pytest.mark.parametrize("cap", [0.0, 3.0])
+def test_scales_that_are_not_positive(dtype, scale, cap):
+    for T in (1, 30):
+        c = Case([200, 77], T, 4, 2, 64, dtype=dtype, cap=cap, seed=23)
+        c.scale = scale
+        c.check(*c.run(), what=T)
+
+
+@pytest.mark.gpu
+def test_results_feed_the_next_call():
+    # the output is the next call's q, with nothing between them; a later call sees it whole
+    for T in (1, 96):
+        c = Case([4000, 3000], T, 32, 4, 128, page=64, seed=24)
+        q = c.q.reshape(-1, 32, 128).cuda()
+        k, v, b = c.k.cuda(), c.v.cuda(), c.batch()
+        idx = torch.arange(512, dtype=torch.int32, device="cuda").repeat(2 * T, 1)
+        n_sel = torch.full((2 * T,), 512, dtype=torch.int32, device="cuda")
+        out = torch.empty_like(q)
+        L.dense_attn(q, k, v, b, c.scale, out=out)
+        torch.cuda.synchronize()
+        want = L.sparse_attn_decode(out, k, v, b, idx, n_sel, c.scale)
+        want2 = L.dense_attn(out, k, v, b, c.scale)
+        torch.cuda.synchronize()
+        for _ in range(20):
+            out.fill_(float("nan"))
+            L.dense_attn(q, k, v, b, c.scale, out=out)
+            got = L.sparse_attn_decode(out, k, v, b, idx, n_sel, c.scale)
+            out.fill_(float("nan"))
+            L.dense_attn(q, k, v, b, c.scale, out=out)
+            got2 = L.dense_attn(out, k, v, b, c.scale)
+            assert torch.equal(got, want) and torch.equal(got2, want2)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_latent_other_widths(dtype):
     c = Case([200, 1, 64], 3, 8, 1, 96, dv=40, dtype=dtype, page=8, latent=True, n_new=[3, 1, 2], seed=5)
@@ -479,7 +546,7 @@ def _call(**kw):
     (dict(scale=float("nan")), "scale"), (dict(scale=float("inf")), "scale"), (dict(q=None), "NULL"),
     (dict(k=None), "NULL"), (dict(out=None), "NULL"), (dict(ws=ctypes.c_void_p(24), wb=64), "aligned"),
     (dict(mods=dict(softcap=-1.0)), "softcap"), (dict(mods=dict(softcap=float("inf"))), "softcap"),
-    (dict(mods=dict(softcap=float("nan"))), "softcap"), (dict(mods=dict(window=-1)), "window"),
+    (dict(mods=dict(softcap=float("nan"))), "softcap"), (dict(mods=dict(softcap=1e-40)), "softcap"), (dict(mods=dict(window=-1)), "window"),
     (dict(b=L._Batch(1, 0, ctypes.c_void_p(16), None, 16, None, 16)), "n_q_per_seq"),
     (dict(b=L._Batch(-1, 1, ctypes.c_void_p(16), None, 16, None, 16)), "n_seq"),
     (dict(b=L._Batch(1, 1, None, None, 16, None, 16)), "n_kv"),
