@@ -37,26 +37,29 @@ struct Shape {
     static_assert(kRowGroups * 4 == R && kRowsPer % 4 == 0 && kCol4 >= 1, "thread layout");
 };
 
-size_t smem_bytes(int R, int DV, int dk, bool latent) {
+// bufs: K and V tiles in flight (2: the next one is loaded under this one's arithmetic)
+size_t smem_bytes(int R, int DV, int dk, bool latent, int bufs) {
     const int kp = round_up(dk, 4) + 4;
     const int vp = DV + 4;
-    return sizeof(float) * ((size_t)R * kp + (size_t)kKeys * kp + (latent ? 0 : (size_t)kKeys * vp) +
-                            (size_t)kKeys * (R + 4) + 2 * R) +
-           sizeof(int) * 3 * R + sizeof(int64_t) * kKeys;
+    return sizeof(float) * ((size_t)R * kp + (size_t)bufs * kKeys * (kp + (latent ? 0 : vp)) + (size_t)kKeys * (R + 4) + 2 * R) +
+           sizeof(int) * 3 * R + sizeof(int64_t) * kKeys * 2;
 }
 
-template <typename T, int R, int DV>
+// kAhead (f32, 16-byte aligned rows and widths): K and V go straight to shared memory by asynchronous copies, a tile
+// ahead.  Otherwise each tile is loaded, widened and stored before its arithmetic.
+template <typename T, int R, int DV, bool kAhead>
 __global__ void __launch_bounds__(kThreads) dense_generic_kernel(DenseArgs a, Geom g, int tiles, bool vec) {
     using S = Shape<R, DV>;
     extern __shared__ __align__(16) unsigned char sm_raw[];
     const int kp = round_up(a.dk, 4) + 4;       // K and Q pitch: rows 4 banks apart
     const bool latent = a.v == nullptr;
     const int vp = latent ? kp : DV + 4;
-    int64_t* rows_s = reinterpret_cast<int64_t*>(sm_raw);
-    float* qs = reinterpret_cast<float*>(rows_s + kKeys);       // [R][kp]
-    float* ks = qs + R * kp;                                    // [kKeys][kp]
-    float* vs = latent ? ks : ks + kKeys * kp;                  // [kKeys][vp]
-    float* ss = (latent ? ks + kKeys * kp : vs + kKeys * vp);   // [kKeys][R + 4] scores, then weights
+    constexpr int kBufs = kAhead ? 2 : 1;
+    int64_t* rows_all = reinterpret_cast<int64_t*>(sm_raw);     // [2][kKeys] cache rows, negative: none
+    float* qs = reinterpret_cast<float*>(rows_all + 2 * kKeys); // [R][kp]
+    float* ks_all = qs + R * kp;                                // [kBufs][kKeys][kp]
+    float* vs_all = ks_all + kBufs * kKeys * kp;                // [kBufs][kKeys][vp], unless latent
+    float* ss = latent ? vs_all : vs_all + kBufs * kKeys * vp;  // [kKeys][R + 4] scores, then weights
     float* alpha_s = ss + kKeys * (R + 4);                      // [R]
     float* slope_s = alpha_s + R;                               // [R]
     int* lo_s = reinterpret_cast<int*>(slope_s + R);
@@ -102,10 +105,11 @@ __global__ void __launch_bounds__(kThreads) dense_generic_kernel(DenseArgs a, Ge
         qs[i] = x;
     }
     // the columns that a tile's rows do not fill
-    for (int i = tid; i < kKeys * (kp - a.dk); i += kThreads) ks[i / (kp - a.dk) * kp + a.dk + i % (kp - a.dk)] = 0.f;
+    for (int i = tid; i < kBufs * kKeys * (kp - a.dk); i += kThreads)
+        ks_all[i / (kp - a.dk) * kp + a.dk + i % (kp - a.dk)] = 0.f;
     if (!latent && a.dv < vp)
-        for (int i = tid; i < kKeys * (vp - a.dv); i += kThreads)
-            vs[i / (vp - a.dv) * vp + a.dv + i % (vp - a.dv)] = 0.f;
+        for (int i = tid; i < kBufs * kKeys * (vp - a.dv); i += kThreads)
+            vs_all[i / (vp - a.dv) * vp + a.dv + i % (vp - a.dv)] = 0.f;
     __syncthreads();
     int k0 = INT32_MAX, k1 = 0, full0 = 0, full1 = INT32_MAX;
     for (int i = 0; i < R; ++i) {
@@ -124,28 +128,61 @@ __global__ void __launch_bounds__(kThreads) dense_generic_kernel(DenseArgs a, Ge
     const int cg = tid % S::kColGroups, vg = tid / S::kColGroups;     // values
     constexpr int kPerRow = kThreads / R;                             // threads of a row's softmax
     const int srow = tid / kPerRow, sk = tid % kPerRow;
-    float o[S::kRowsPer][4 * S::kCol4];
+    uint64_t o[S::kRowsPer][2 * S::kCol4];                            // pairs of columns
 #pragma unroll
     for (int i = 0; i < S::kRowsPer; ++i)
 #pragma unroll
-        for (int c = 0; c < 4 * S::kCol4; ++c) o[i][c] = 0.f;
+        for (int c = 0; c < 2 * S::kCol4; ++c) o[i][c] = 0ull;
     float m_run = -INFINITY, l_run = 0.f;
     const float cap = a.mods.softcap, inv_cap = cap > 0.f ? 1.f / cap : 0.f;
 
-    for (int t0 = k0; t0 < k1; t0 += kKeys) {
-        __syncthreads();
-        if (tid < kKeys) {
-            int64_t row = -1;
-            if (t0 + tid < k1) {
-                row = key_row(g, b, t0 + tid);
-                if (row < 0 || row >= a.kv_rows) {
-                    flag(g.status, IDX_ERR_DEVICE_BOUNDS);
-                    row = -1;
-                }
-            }
-            rows_s[tid] = row;
+    // cache row of position j of the split, -1 past its end or outside the cache
+    auto row_of = [&](int j) -> int64_t {
+        if (j >= k1) return -1;
+        const int64_t row = key_row(g, b, j);
+        if (row >= 0 && row < a.kv_rows) return row;
+        flag(g.status, IDX_ERR_DEVICE_BOUNDS);
+        return -1;
+    };
+    // kAhead: four threads to a key, each every fourth 16-byte piece of its K and V rows (zeros for no row)
+    auto send = [&](int t0, int buf) {
+        const int key = tid >> 2, sub = tid & 3;
+        const int64_t row = t0 < k1 ? row_of(t0 + key) : -1;
+        if (sub == 0) rows_all[buf * kKeys + key] = row;
+        if (t0 < k1) {
+            auto pieces = [&](const float* src, float* dst, int n) {
+                const uint32_t d = sm100::smem_u32(dst);
+                const int size = row >= 0 ? 16 : 0;
+                for (int i = sub; i < n; i += 4)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d + i * 16), "l"(src + i * 4), "r"(size)
+                                 : "memory");
+            };
+            const int64_t at = row < 0 ? 0 : row;
+            pieces(static_cast<const float*>(a.k) + at * a.k_stride + (int64_t)gkv * a.dk, ks_all + (buf * kKeys + key) * kp,
+                   a.dk / 4);
+            if (!latent)
+                pieces(static_cast<const float*>(a.v) + at * a.v_stride + (int64_t)gkv * a.dv,
+                       vs_all + (buf * kKeys + key) * vp, a.dv / 4);
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if (kAhead) send(k0, 0);
+    int buf = 0;
+    for (int t0 = k0; t0 < k1; t0 += kKeys) {
+        float* ks = ks_all + buf * kKeys * kp;
+        float* vs = latent ? ks : vs_all + buf * kKeys * vp;
+        int64_t* rows_s = rows_all + buf * kKeys;
+        __syncthreads();      // the last tile is done with
+        if (kAhead) {
+            send(t0 + kKeys, buf ^ 1);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            buf ^= 1;
+        } else if (tid < kKeys) {
+            rows_s[tid] = row_of(t0 + tid);
+        }
+        if (kAhead) __syncthreads();
         const bool bad = __syncthreads_or(tid < kKeys && rows_s[tid < kKeys ? tid : 0] < 0);
+        if constexpr (!kAhead) {
         // K and V rows, widened
         if (vec) {
             constexpr int E = 16 / (int)sizeof(T);
@@ -196,39 +233,39 @@ __global__ void __launch_bounds__(kThreads) dense_generic_kernel(DenseArgs a, Ge
                 }
         }
         __syncthreads();
+        }
         // ---- scores
         const bool whole = !bad && t0 >= full0 && t0 + kKeys <= min(full1, k1);
         {
-            float acc[4][S::kKeysPer];
+            uint64_t acc[4][S::kKeysPer];       // sums over even and over odd columns, packed
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < S::kKeysPer; ++j) acc[i][j] = 0.f;
+                for (int j = 0; j < S::kKeysPer; ++j) acc[i][j] = 0ull;
             const float* qr = qs + rg * kp;
             const float* kr = ks + kg * kp;
+#pragma unroll 2
             for (int c = 0; c < kp - 4; c += 4) {
-                float4 kk[S::kKeysPer], qq[4];
+                ulonglong2 kk[S::kKeysPer], qq[4];
 #pragma unroll
                 for (int j = 0; j < S::kKeysPer; ++j)
-                    kk[j] = *reinterpret_cast<const float4*>(kr + j * S::kKeyGroups * kp + c);
+                    kk[j] = *reinterpret_cast<const ulonglong2*>(kr + j * S::kKeyGroups * kp + c);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) qq[i] = *reinterpret_cast<const float4*>(qr + i * S::kRowGroups * kp + c);
+                for (int i = 0; i < 4; ++i) qq[i] = *reinterpret_cast<const ulonglong2*>(qr + i * S::kRowGroups * kp + c);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int j = 0; j < S::kKeysPer; ++j) {
-                        acc[i][j] = fmaf(qq[i].x, kk[j].x, acc[i][j]);
-                        acc[i][j] = fmaf(qq[i].y, kk[j].y, acc[i][j]);
-                        acc[i][j] = fmaf(qq[i].z, kk[j].z, acc[i][j]);
-                        acc[i][j] = fmaf(qq[i].w, kk[j].w, acc[i][j]);
-                    }
+                    for (int j = 0; j < S::kKeysPer; ++j)
+                        acc[i][j] = fma2(qq[i].y, kk[j].y, fma2(qq[i].x, kk[j].x, acc[i][j]));
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int rr = rg + i * S::kRowGroups;
 #pragma unroll
                 for (int j = 0; j < S::kKeysPer; ++j) {
-                    float x = acc[i][j] * a.scale;
+                    float even, odd;
+                    unpair(acc[i][j], even, odd);
+                    float x = (even + odd) * a.scale;
                     if (cap > 0.f) x = cap * tanhf(x * inv_cap);
                     const int kl = kg + j * S::kKeyGroups;
                     if (a.mods.slopes) x -= slope_s[rr] * fabsf((float)((int64_t)pos_s[rr] - (t0 + kl)));
@@ -286,7 +323,7 @@ __global__ void __launch_bounds__(kThreads) dense_generic_kernel(DenseArgs a, Ge
             for (int i = 0; i < S::kRowsPer; ++i) {
                 const float al = alpha_s[vg * S::kRowsPer + i];
 #pragma unroll
-                for (int c = 0; c < 4 * S::kCol4; ++c) o[i][c] *= al;
+                for (int c = 0; c < 2 * S::kCol4; ++c) o[i][c] = mul2(o[i][c], pair(al, al));
             }
         }
         const int n_keys = min(kKeys, k1 - t0);
@@ -306,14 +343,13 @@ __global__ void __launch_bounds__(kThreads) dense_generic_kernel(DenseArgs a, Ge
                 for (int c = 0; c < S::kCol4; ++c) {
                     const int col = 4 * cg + 4 * S::kColGroups * c;
                     if (col >= a.dv) continue;
-                    const float4 x = *reinterpret_cast<const float4*>(vs + kl * vp + col);
+                    const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(vs + kl * vp + col);
 #pragma unroll
                     for (int i = 0; i < S::kRowsPer; ++i) {
                         if (decltype(masked)::value && p[i] < 0.f) continue;
-                        o[i][4 * c] = fmaf(p[i], x.x, o[i][4 * c]);
-                        o[i][4 * c + 1] = fmaf(p[i], x.y, o[i][4 * c + 1]);
-                        o[i][4 * c + 2] = fmaf(p[i], x.z, o[i][4 * c + 2]);
-                        o[i][4 * c + 3] = fmaf(p[i], x.w, o[i][4 * c + 3]);
+                        const uint64_t pp = pair(p[i], p[i]);
+                        o[i][2 * c] = fma2(pp, x.x, o[i][2 * c]);
+                        o[i][2 * c + 1] = fma2(pp, x.y, o[i][2 * c + 1]);
                     }
                 }
             }
@@ -324,6 +360,7 @@ __global__ void __launch_bounds__(kThreads) dense_generic_kernel(DenseArgs a, Ge
             values(std::true_type{});
     }
 
+    if (kAhead) sm100::cp_async_wait_all();
     // ---- output: m and l per row through shared memory
     const bool merge = a.splits > 1 && !a.part_o;       // the splits are the CTAs of a cluster
     float* m_s = slope_s;
@@ -356,12 +393,15 @@ __global__ void __launch_bounds__(kThreads) dense_generic_kernel(DenseArgs a, Ge
         const float l = l_s[rr];
         const float inv = a.splits > 1 ? 1.f : 1.f / l;
 #pragma unroll
-        for (int c = 0; c < S::kCol4; ++c)
+        for (int c = 0; c < S::kCol4; ++c) {
+            float oc[4];
+            unpair(o[i][2 * c], oc[0], oc[1]);
+            unpair(o[i][2 * c + 1], oc[2], oc[3]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int col = 4 * cg + 4 * S::kColGroups * c + e;
                 if (col >= a.dv) continue;
-                const float x = l == 0.f ? 0.f : o[i][4 * c + e] * inv;
+                const float x = l == 0.f ? 0.f : oc[e] * inv;
                 if (merge)
                     o_s[rr * DV + col] = x;
                 else if (a.splits > 1)
@@ -369,6 +409,7 @@ __global__ void __launch_bounds__(kThreads) dense_generic_kernel(DenseArgs a, Ge
                 else
                     static_cast<T*>(a.out)[rh * a.dv + col] = from_f32<T>(x);
             }
+        }
     }
     if (merge) {
         // each CTA merges its share of the elements, in the order of the splits
@@ -493,15 +534,25 @@ cudaError_t run(const DenseArgs& a, const Geom& g, cudaStream_t st) {
                          (uint64_t)a.k_stride * sizeof(T) | (a.v ? (uint64_t)a.v_stride * sizeof(T) : 0) |
                          (uint64_t)a.dk * sizeof(T) | (a.v ? (uint64_t)a.dv * sizeof(T) : 0);
     const bool vec = all % 16 == 0;
-    auto go = [&](auto kern, int dvp) {
-        const size_t sm = smem_bytes(R, dvp, a.dk, !a.v);
+    auto go = [&](auto kern, int dvp, int bufs) {
+        const size_t sm = smem_bytes(R, dvp, a.dk, !a.v, bufs);
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
         if (e != cudaSuccess) return e;
         return launch_pdl_cluster(kern, dim3((unsigned)grid), dim3(kThreads), sm, st,
                                   a.splits > 1 && !a.part_o ? a.splits : 1, a, g, (int)tiles, vec);
     };
-    if (R == 64) return a.dv <= 64 ? go(dense_generic_kernel<T, 64, 64>, 64) : go(dense_generic_kernel<T, 64, 128>, 128);
-    return a.dv <= 128 ? go(dense_generic_kernel<T, 16, 128>, 128) : go(dense_generic_kernel<T, 16, 512>, 512);
+    if constexpr (sizeof(T) == 4) {
+        // a tile ahead where two CTAs fit an SM with it (wider rows would be alone there)
+        const int dvp = R == 64 && a.dv <= 64 ? 64 : a.dv <= 128 ? 128 : 512;
+        if (vec && smem_bytes(R, dvp, a.dk, !a.v, 2) <= 113 * 1024) {
+            if (R == 64)
+                return dvp == 64 ? go(dense_generic_kernel<T, 64, 64, true>, 64, 2) : go(dense_generic_kernel<T, 64, 128, true>, 128, 2);
+            if (dvp == 128) return go(dense_generic_kernel<T, 16, 128, true>, 128, 2);
+        }
+    }
+    if (R == 64)
+        return a.dv <= 64 ? go(dense_generic_kernel<T, 64, 64, false>, 64, 1) : go(dense_generic_kernel<T, 64, 128, false>, 128, 1);
+    return a.dv <= 128 ? go(dense_generic_kernel<T, 16, 128, false>, 128, 1) : go(dense_generic_kernel<T, 16, 512, false>, 512, 1);
 }
 
 }  // namespace
