@@ -11,7 +11,13 @@
 //   softmax: running maximum and sum per row (natural logarithm), f32;
 //   values: thread = (row group, 4-column groups), a register block of the
 //           output rescaled by the rows' factors each tile.
-// Bound by the f32 FMAs (and, for few rows, by the latency of a tile's loads).
+// A warp has the same R/4 rows in all three, so that only the tiles' arrival is a barrier of the CTA.
+// Sums, products, maxima and weights are f32 throughout; products run as packed pairs of FMAs.
+// Measured in f32: 512 tokens on 4096 cached keys, two sequences of 32 heads of 128 on 4, 2.43 ms = 26.6 TFLOP/s,
+// bound by the instructions beside the FMAs (shared-memory reads, the softmax) with two CTAs of four warps to an SM,
+// which is what 181 registers and 110 KB leave room for; one token on 16384 keys, eight sequences of 32 heads on 8,
+// 0.61 ms = 1.8 TB/s, bound by the latency of a tile's loads and its softmax.
+// Loading a tile ahead of the arithmetic (f32, aligned): heads of 64, 256 tokens on 2048 keys 260 -> 194 us.
 // A key that only some rows of a tile see is skipped, not multiplied by zero,
 // for the others, so that NaN or infinity in it cannot reach them.
 #include <float.h>
@@ -29,12 +35,12 @@ __host__ __device__ constexpr int round_up(int x, int m) { return (x + m - 1) / 
 template <int R, int DV>
 struct Shape {
     static constexpr int kKeyGroups = R == 64 ? 8 : 32;      // threads along the keys (scores)
-    static constexpr int kRowGroups = kThreads / kKeyGroups; // R / 4
+    static constexpr int kRowStep = 32 / kKeyGroups;         // a thread's four rows are this far apart
     static constexpr int kKeysPer = kKeys / kKeyGroups;
     static constexpr int kColGroups = R == 64 ? 16 : 32;     // threads along the columns (values)
     static constexpr int kRowsPer = R / (kThreads / kColGroups);
     static constexpr int kCol4 = DV / (4 * kColGroups);      // 4-column groups per thread
-    static_assert(kRowGroups * 4 == R && kRowsPer % 4 == 0 && kCol4 >= 1, "thread layout");
+    static_assert(kThreads / kKeyGroups * 4 == R && kRowsPer % 4 == 0 && kCol4 >= 1, "thread layout");
 };
 
 // bufs: K and V tiles in flight (2: the next one is loaded under this one's arithmetic)
@@ -48,7 +54,7 @@ size_t smem_bytes(int R, int DV, int dk, bool latent, int bufs) {
 // kAhead (f32, 16-byte aligned rows and widths): K and V go straight to shared memory by asynchronous copies, a tile
 // ahead.  Otherwise each tile is loaded, widened and stored before its arithmetic.
 template <typename T, int R, int DV, bool kAhead>
-__global__ void __launch_bounds__(kThreads) dense_generic_kernel(DenseArgs a, Geom g, int tiles, bool vec) {
+__global__ void __launch_bounds__(kThreads, DV == 64 ? 3 : 0) dense_generic_kernel(DenseArgs a, Geom g, int tiles, bool vec) {
     using S = Shape<R, DV>;
     extern __shared__ __align__(16) unsigned char sm_raw[];
     const int kp = round_up(a.dk, 4) + 4;       // K and Q pitch: rows 4 banks apart
@@ -124,7 +130,9 @@ __global__ void __launch_bounds__(kThreads) dense_generic_kernel(DenseArgs a, Ge
     if (s0 > k0) k0 = (int)min(s0, (int64_t)INT32_MAX);
     if (s0 + a.kps < k1) k1 = (int)(s0 + a.kps);
 
-    const int kg = tid % S::kKeyGroups, rg = tid / S::kKeyGroups;     // scores
+    // a warp's rows are the same R / 4 in the scores, the softmax and the values: no barrier between them
+    const int kg = tid % S::kKeyGroups;                               // scores
+    const int r0 = tid / 32 * (R / 4) + tid % 32 / S::kKeyGroups;
     const int cg = tid % S::kColGroups, vg = tid / S::kColGroups;     // values
     constexpr int kPerRow = kThreads / R;                             // threads of a row's softmax
     const int srow = tid / kPerRow, sk = tid % kPerRow;
@@ -144,7 +152,7 @@ __global__ void __launch_bounds__(kThreads) dense_generic_kernel(DenseArgs a, Ge
         flag(g.status, IDX_ERR_DEVICE_BOUNDS);
         return -1;
     };
-    // kAhead: four threads to a key, each every fourth 16-byte piece of its K and V rows (zeros for no row)
+    // kAhead: four threads to a key, each every fourth 16-byte piece of its K and V rows (zeros for no row, and true)
     auto send = [&](int t0, int buf) {
         const int key = tid >> 2, sub = tid & 3;
         const int64_t row = t0 < k1 ? row_of(t0 + key) : -1;
@@ -164,25 +172,25 @@ __global__ void __launch_bounds__(kThreads) dense_generic_kernel(DenseArgs a, Ge
                 pieces(static_cast<const float*>(a.v) + at * a.v_stride + (int64_t)gkv * a.dv,
                        vs_all + (buf * kKeys + key) * vp, a.dv / 4);
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
+        return row < 0;
     };
-    if (kAhead) send(k0, 0);
+    bool lost = false;                                                // this thread's key of the tile to come has no row
+    if (kAhead) lost = send(k0, 0);
     int buf = 0;
     for (int t0 = k0; t0 < k1; t0 += kKeys) {
         float* ks = ks_all + buf * kKeys * kp;
         float* vs = latent ? ks : vs_all + buf * kKeys * vp;
         int64_t* rows_s = rows_all + buf * kKeys;
-        __syncthreads();      // the last tile is done with
-        if (kAhead) {
-            send(t0 + kKeys, buf ^ 1);
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        bool bad;
+        if constexpr (kAhead) {
+            sm100::cp_async_wait_all();
+            bad = __syncthreads_or(lost);       // this tile is there, and the last one is done with
+            lost = send(t0 + kKeys, buf ^ 1);
             buf ^= 1;
-        } else if (tid < kKeys) {
-            rows_s[tid] = row_of(t0 + tid);
-        }
-        if (kAhead) __syncthreads();
-        const bool bad = __syncthreads_or(tid < kKeys && rows_s[tid < kKeys ? tid : 0] < 0);
-        if constexpr (!kAhead) {
+        } else {
+        __syncthreads();      // the last tile is done with
+        if (tid < kKeys) rows_s[tid] = row_of(t0 + tid);
+        bad = __syncthreads_or(tid < kKeys && rows_s[tid < kKeys ? tid : 0] < 0);
         // K and V rows, widened
         if (vec) {
             constexpr int E = 16 / (int)sizeof(T);
@@ -242,16 +250,16 @@ __global__ void __launch_bounds__(kThreads) dense_generic_kernel(DenseArgs a, Ge
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < S::kKeysPer; ++j) acc[i][j] = 0ull;
-            const float* qr = qs + rg * kp;
+            const float* qr = qs + r0 * kp;
             const float* kr = ks + kg * kp;
-#pragma unroll 2
+#pragma unroll 8
             for (int c = 0; c < kp - 4; c += 4) {
                 ulonglong2 kk[S::kKeysPer], qq[4];
 #pragma unroll
                 for (int j = 0; j < S::kKeysPer; ++j)
                     kk[j] = *reinterpret_cast<const ulonglong2*>(kr + j * S::kKeyGroups * kp + c);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) qq[i] = *reinterpret_cast<const ulonglong2*>(qr + i * S::kRowGroups * kp + c);
+                for (int i = 0; i < 4; ++i) qq[i] = *reinterpret_cast<const ulonglong2*>(qr + i * S::kRowStep * kp + c);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -260,7 +268,7 @@ __global__ void __launch_bounds__(kThreads) dense_generic_kernel(DenseArgs a, Ge
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int rr = rg + i * S::kRowGroups;
+                const int rr = r0 + i * S::kRowStep;
 #pragma unroll
                 for (int j = 0; j < S::kKeysPer; ++j) {
                     float even, odd;
@@ -273,7 +281,7 @@ __global__ void __launch_bounds__(kThreads) dense_generic_kernel(DenseArgs a, Ge
                 }
             }
         }
-        __syncthreads();
+        __syncwarp();
         // ---- softmax: kPerRow threads of a warp per row; a masked key's weight is marked by -1
         {
             const int lo = lo_s[srow], hi = hi_s[srow];
@@ -313,7 +321,7 @@ __global__ void __launch_bounds__(kThreads) dense_generic_kernel(DenseArgs a, Ge
             m_run = m_new;
             if (sk == 0) alpha_s[srow] = alpha;
         }
-        __syncthreads();
+        __syncwarp();
         // ---- values
         bool scaled = false;
 #pragma unroll
@@ -328,7 +336,7 @@ __global__ void __launch_bounds__(kThreads) dense_generic_kernel(DenseArgs a, Ge
         }
         const int n_keys = min(kKeys, k1 - t0);
         auto values = [&](auto masked) {
-#pragma unroll 4
+#pragma unroll 8
             for (int kl = 0; kl < n_keys; ++kl) {
                 float p[S::kRowsPer];
 #pragma unroll
@@ -558,7 +566,7 @@ cudaError_t run(const DenseArgs& a, const Geom& g, cudaStream_t st) {
 }  // namespace
 
 // enough CTAs to cover the SMs four times, at least a tile of keys each: a tile takes about 4 us whatever it holds
-// (256 keys for one token of four f32 heads: 24 us in two splits, XX in eight)
+// (256 keys for one token of four f32 heads: 19.7 us in two splits, 10.5 in eight)
 int dense_generic_splits(int64_t n_seq, int64_t n_q, int64_t max_n_kv, int Hq, int Hkv, int dk, int dv) {
     (void)dk;
     const int64_t packed = n_q * (Hq / Hkv);
