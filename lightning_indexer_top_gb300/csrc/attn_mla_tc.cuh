@@ -100,7 +100,6 @@ struct Ctl {
     uint64_t pfull[2];         // rank 1: packet j landed (rank 0 posts its byte count, its stores complete it)
     uint64_t cdone[2];         // rank 1: O corrected for packet j
     uint64_t pvdone[2];        // rank 1: PV MMAs that read packet j completed
-    uint64_t vok[kStagesV];    // rank 1, dense feed: the tile's unseen rows zeroed
     uint64_t done;
     uint32_t tmem_base;
     int abort;
@@ -210,10 +209,10 @@ __device__ __forceinline__ MlaSmem mla_smem(uint8_t* smem) {
     return s;
 }
 
-// one thread: the unit's barriers (a tile's announcement counts every producer lane, or one when TMA loads it)
-__device__ __forceinline__ void mla_init(Ctl& c, int producers = 32 * kProducerWarps) {
+// one thread: the unit's barriers
+__device__ __forceinline__ void mla_init(Ctl& c) {
     for (int i = 0; i < kStagesK; ++i) {
-        mbar_init(&c.xfull[i], producers);
+        mbar_init(&c.xfull[i], 32 * kProducerWarps);
         mbar_init(&c.xempty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -224,7 +223,6 @@ __device__ __forceinline__ void mla_init(Ctl& c, int producers = 32 * kProducerW
         mbar_init(&c.cdone[i], 4);
         mbar_init(&c.pvdone[i], 1);
     }
-    for (int i = 0; i < kStagesV; ++i) mbar_init(&c.vok[i], 1);
     mbar_init(&c.qready, 4);
     mbar_init(&c.qbulk, 1);
     mbar_init(&c.done, 1);
@@ -317,21 +315,12 @@ __device__ __forceinline__ void mla_stage_rows(const MlaSmem& sm, uint32_t rank,
     }
 }
 
-// Where a unit's key tiles come from, and what its softmax does to the scores.
-// The selected rows, gathered one by one:
-struct GatherFeed {
-    static constexpr bool kDense = false;
-    static constexpr bool kMods = false;
-};
-
 // the unit after its Q load and index staging (both CTAs past a cluster_sync): gathers,
 // QK^T, softmax, PV and the output (or the split's partial result)
-template <typename Feed = GatherFeed>
 __device__ __forceinline__ void mla_run(const MlaSmem& sm, uint32_t tmem, uint32_t rank, const Unit& u, int64_t unit,
                                         const __nv_bfloat16* __restrict__ lat, int64_t lat_row_stride, const Geom& g,
                                         float scale_log2, int splits, void* __restrict__ out, int out_dtype,
-                                        float* __restrict__ part_o, float* __restrict__ part_ml,
-                                        const Feed& feed = Feed()) {
+                                        float* __restrict__ part_o, float* __restrict__ part_ml) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quad = warp & 3;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
@@ -345,42 +334,8 @@ __device__ __forceinline__ void mla_run(const MlaSmem& sm, uint32_t tmem, uint32
         if (producer >= 0) {
             // Q's staging area is the ring's first stages: gather once Q is in TMEM
             if (u.n_tiles > 0 && !warp_wait(&c.qready, 0)) abort_cta(c, g.status);
-            if constexpr (Feed::kDense)
-                feed.template load_tiles<kDkBlocks, kStagesK, kKTileBytes>(c, xtiles, u, vmask, producer, g);
-            else
-                gather_tiles<kDkBlocks * 8, kStagesK, kKTileBytes>(c, xtiles, lat, lat_row_stride, u, rows_s, producer,
-                                                                   g.status);
-        } else if (Feed::kDense && warp == 1) {
-            // -------------------------------------------------------- S = Q K^T issuer of the dense feed: the warp
-            // walks together and a lane issues (operands that all lanes share stay in uniform registers; a lane on
-            // its own takes about 100 cycles for each of a tile's 36 products, which take 33)
-            const uint32_t idesc = idesc_f16_f32_major(kHq, kKeys, 1, 0, 0);
-            const uint64_t kd = desc_sw128_kmajor(0, 1024);
-            const uint32_t k_hi = desc_hi(kd), tm = __shfl_sync(0xffffffffu, tmem, 0);
-            const uint32_t kb = (uint32_t)kd + desc_addr(xtiles);
-            bool ok = u.n_tiles == 0 || warp_wait(&c.qready, 0);
-            for (int t = 0; ok && t < u.n_tiles; ++t) {
-                const int stage = t % kStagesK, sb = t & 1;
-                ok = warp_wait(&c.xfull[stage], (uint32_t)((t / kStagesK) & 1)) &&
-                     warp_wait(&c.sempty[sb], (uint32_t)((t >> 1) & 1) ^ 1);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t ka = __shfl_sync(0xffffffffu, kb + (stage * kKTileBytes >> 4), 0);
-                const uint32_t d = __shfl_sync(0xffffffffu, tm + kSCol0 + sb * kKeys, 0);
-                if (elect_one()) {
-#pragma unroll
-                    for (int ks = 0; ks < kDk / 16; ++ks)
-                        mma_f16_ts_lo(d, tm + ks * 8, ka + (((ks >> 2) * kBlockBytes + (ks & 3) * 32) >> 4), k_hi, idesc,
-                                      ks > 0 ? 1u : 0u);
-                    mma_commit(&c.xempty[stage]);
-                    mma_commit(&c.sfull[sb]);
-                }
-                __syncwarp();
-            }
-            if (!ok) abort_cta(c, g.status);
-            if (elect_one()) mma_commit(&c.done);
-            __syncwarp();
-            warp_wait(&c.done, 0);
+            gather_tiles<kDkBlocks * 8, kStagesK, kKTileBytes>(c, xtiles, lat, lat_row_stride, u, rows_s, producer,
+                                                               g.status);
         } else if (warp == 1) {
             if (lane == 0) {
                 // ---------------------------------------------------- S = Q K^T issuer
@@ -435,14 +390,11 @@ __device__ __forceinline__ void mla_run(const MlaSmem& sm, uint32_t tmem, uint32
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&c.sempty[sb]);
 
-                if constexpr (Feed::kMods) feed.modify(s0, s1, u, t, h);   // scores in log2 units
-                const float sl2 = Feed::kMods ? 1.f : scale_log2;
-
                 // the tile's largest scaled logit: for a full tile and a positive scale, the scaled
                 // largest logit (the same value: rounding a product by a positive factor is monotone)
                 const bool full = (ma & mb) == 0xffffffffu;
                 float mt = -3.0e38f;
-                if (full && sl2 > 0.f) {
+                if (full && scale_log2 > 0.f) {
                     float a0 = fmaxf(s0[0], s0[1]), a1 = fmaxf(s0[2], s0[3]);
                     float a2 = fmaxf(s1[0], s1[1]), a3 = fmaxf(s1[2], s1[3]);
 #pragma unroll
@@ -452,12 +404,12 @@ __device__ __forceinline__ void mla_run(const MlaSmem& sm, uint32_t tmem, uint32
                         a2 = fmaxf(a2, fmaxf(s1[i], s1[i + 1]));
                         a3 = fmaxf(a3, fmaxf(s1[i + 2], s1[i + 3]));
                     }
-                    mt = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3)) * sl2;
+                    mt = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3)) * scale_log2;
                 } else {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        if ((ma >> i) & 1u) mt = fmaxf(mt, s0[i] * sl2);
-                        if ((mb >> i) & 1u) mt = fmaxf(mt, s1[i] * sl2);
+                        if ((ma >> i) & 1u) mt = fmaxf(mt, s0[i] * scale_log2);
+                        if ((mb >> i) & 1u) mt = fmaxf(mt, s1[i] * scale_log2);
                     }
                 }
                 float alpha = 1.f;
@@ -478,10 +430,10 @@ __device__ __forceinline__ void mla_run(const MlaSmem& sm, uint32_t tmem, uint32
                 const uint32_t ka = full ? 0xffffffffu : ma, kb = full ? 0xffffffffu : mb;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float e0 = ex2_approx(fmaf(s0[2 * i], sl2, nm));
-                    const float e1 = ex2_approx(fmaf(s0[2 * i + 1], sl2, nm));
-                    const float e2 = ex2_approx(fmaf(s1[2 * i], sl2, nm));
-                    const float e3 = ex2_approx(fmaf(s1[2 * i + 1], sl2, nm));
+                    const float e0 = ex2_approx(fmaf(s0[2 * i], scale_log2, nm));
+                    const float e1 = ex2_approx(fmaf(s0[2 * i + 1], scale_log2, nm));
+                    const float e2 = ex2_approx(fmaf(s1[2 * i], scale_log2, nm));
+                    const float e3 = ex2_approx(fmaf(s1[2 * i + 1], scale_log2, nm));
                     const float p0 = ((ka >> (2 * i)) & 1u) ? e0 : 0.f;
                     const float p1 = ((ka >> (2 * i + 1)) & 1u) ? e1 : 0.f;
                     const float p2 = ((kb >> (2 * i)) & 1u) ? e2 : 0.f;
@@ -501,9 +453,7 @@ __device__ __forceinline__ void mla_run(const MlaSmem& sm, uint32_t tmem, uint32
                 }
                 const uint32_t slot = mapa(pkts + j * kPktStride, 1);
                 const uint32_t rbar = mapa(&c.pfull[j], 1);
-                // (the dense feed's sum and maximum go with the last packet alone)
-                const bool totals = !Feed::kDense || t == u.n_tiles - 1;
-                if (h == 0) mbar_arrive_expect_tx_remote(rbar, kPktBytes - (totals ? 0 : 2 * kHq * 4));
+                if (h == 0) mbar_arrive_expect_tx_remote(rbar, kPktBytes);
                 const uint32_t rowp = slot + (uint32_t)((h >> 3) * 1024 + (h & 7) * 128);
 #pragma unroll
                 for (int ch = 0; ch < 8; ++ch)
@@ -511,10 +461,8 @@ __device__ __forceinline__ void mla_run(const MlaSmem& sm, uint32_t tmem, uint32
                                 make_uint4(pk[4 * ch], pk[4 * ch + 1], pk[4 * ch + 2], pk[4 * ch + 3]), rbar);
                 const uint32_t tail = slot + kPBytes + (uint32_t)h * 4;
                 st_async_f32(tail + offsetof(PktTail, alpha), alpha, rbar);
-                if (totals) {
-                    st_async_f32(tail + offsetof(PktTail, l), lsum, rbar);
-                    st_async_f32(tail + offsetof(PktTail, m), m_used, rbar);
-                }
+                st_async_f32(tail + offsetof(PktTail, l), lsum, rbar);
+                st_async_f32(tail + offsetof(PktTail, m), m_used, rbar);
             }
             // rank 1's last arrivals on pfree land before this CTA may leave
             const int n = min(u.n_tiles, 2);
@@ -523,47 +471,8 @@ __device__ __forceinline__ void mla_run(const MlaSmem& sm, uint32_t tmem, uint32
         }
     } else {
         if (producer >= 0) {
-            if constexpr (Feed::kDense) {
-                feed.template load_tiles<kDvBlocks, kStagesV, kVTileBytes>(c, xtiles, u, vmask, producer, g);
-                if (producer == 1) feed.zero_unseen(c, xtiles, u, vmask, g);
-            } else {
-                gather_tiles<kDvBlocks * 8, kStagesV, kVTileBytes>(c, xtiles, lat, lat_row_stride, u, rows_s, producer,
-                                                                   g.status);
-            }
-        } else if (Feed::kDense && warp == 1) {
-            // -------------------------------------------------------- O += P V issuer of the dense feed
-            const uint32_t idesc = idesc_f16_f32_major(kHq, 256, 1, 0, 1);
-            const uint64_t pd = desc_sw128_kmajor(0, 1024), vd = desc_sw128_mnmajor(0, kBlockBytes, 1024);
-            const uint32_t p_hi = desc_hi(pd), v_hi = desc_hi(vd), tm = __shfl_sync(0xffffffffu, tmem, 0);
-            const uint32_t pb = (uint32_t)pd + desc_addr(pkts), vb = (uint32_t)vd + desc_addr(xtiles);
-            bool ok = true;
-            for (int t = 0; ok && t < u.n_tiles; ++t) {
-                const int stage = t % kStagesV, j = t & 1;
-                ok = warp_wait(&c.vok[stage], (uint32_t)((t / kStagesV) & 1)) &&
-                     warp_wait(&c.cdone[j], (uint32_t)((t >> 1) & 1));
-                if (!ok) break;
-                fence_proxy_async_smem();
-                tc_fence_after();
-                const uint32_t pa = __shfl_sync(0xffffffffu, pb + (j * kPktStride >> 4), 0);
-                const uint32_t va = __shfl_sync(0xffffffffu, vb + (stage * kVTileBytes >> 4), 0);
-                const uint32_t acc = __shfl_sync(0xffffffffu, t > 0 ? 1u : 0u, 0);
-                if (elect_one()) {
-#pragma unroll
-                    for (int ks = 0; ks < kKeys / 16; ++ks)
-#pragma unroll
-                        for (int nh = 0; nh < 2; ++nh)
-                            mma_f16_ss_lo(tm + nh * 256, pa + (ks * 32 >> 4), p_hi,
-                                          va + ((nh * 4 * kBlockBytes + ks * 2 * 1024) >> 4), v_hi, idesc, ks > 0 ? 1u : acc);
-                    mma_commit(&c.xempty[stage]);
-                    mma_commit(&c.pvdone[j]);
-                    mma_commit_multicast(&c.pfree[j], (uint16_t)0x1);
-                }
-                __syncwarp();
-            }
-            if (!ok) abort_cta(c, g.status);
-            if (elect_one()) mma_commit(&c.done);
-            __syncwarp();
-            warp_wait(&c.done, 0);
+            gather_tiles<kDvBlocks * 8, kStagesV, kVTileBytes>(c, xtiles, lat, lat_row_stride, u, rows_s, producer,
+                                                               g.status);
         } else if (warp == 1) {
             if (lane == 0) {
                 const uint32_t idesc = idesc_f16_f32_major(kHq, 256, 1, 0, 1);
@@ -571,8 +480,7 @@ __device__ __forceinline__ void mla_run(const MlaSmem& sm, uint32_t tmem, uint32
                     const int stage = t % kStagesV, j = t & 1;
                     const uint32_t ph = (uint32_t)((t >> 1) & 1);
                     if (aborted(c)) break;
-                    if (!mbar_wait(Feed::kDense ? &c.vok[stage] : &c.xfull[stage], (uint32_t)((t / kStagesV) & 1)) ||
-                        !mbar_wait(&c.cdone[j], ph)) {
+                    if (!mbar_wait(&c.xfull[stage], (uint32_t)((t / kStagesV) & 1)) || !mbar_wait(&c.cdone[j], ph)) {
                         abort_cta(c, g.status);
                         break;
                     }
@@ -655,11 +563,7 @@ __device__ __forceinline__ void mla_run(const MlaSmem& sm, uint32_t tmem, uint32
         }
         const bool read_o = have && !warp_aborted(c);
         if (splits == 1) {
-            // (a NaN sum passes the dense feed's test: the row is NaN then)
-            const float inv = (Feed::kDense ? lsum != 0.f : lsum > 0.f) ? 1.f / lsum : 0.f;
-            if constexpr (Feed::kDense) {
-                if (part == 0) feed.store_lse(u.r * kHq + h, mrow, read_o ? lsum : 0.f);
-            }
+            const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
             const int64_t base = (u.r * kHq + h) * (int64_t)kDv;
             for (int cb = part; cb < kDv / 32; cb += kThreads / 128) {
                 float v[32];

@@ -23,7 +23,7 @@
 // made for 128 keys at a time), the issuers' queue is short, and a softmax of 128
 // rows x 64 keys takes 650 to 800 cycles.  On 4096 rows x 16384 keys (32 / 4 heads
 // of 128, causal): one issuer, a lane on its own 1.17 ms; the warp together 0.99;
-// an issuer per row tile 0.80 (64-key scores, double buffered); this form 0.XX.
+// an issuer per row tile 0.80 (64-key scores, double buffered); this form 0.74.
 //
 // A row's maximum follows its scores lazily: O is rescaled (by the softmax
 // warps, in TMEM) only when a score passes it by 2^8, so P stays <= 2^8.
