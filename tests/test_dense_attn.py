@@ -259,6 +259,26 @@ def test_long_latent_without_a_workspace_and_with_one():
 
 
 @pytest.mark.gpu
+def test_latent_beyond_one_split():
+    # 8192 keys are the most that a unit takes: splits they are with a workspace, the CUDA cores without
+    c = Case([9000, 2100], 1, 128, 1, 576, dv=512, dtype=torch.bfloat16, page=64, latent=True, seed=31)
+    c.check(*c.run())
+    c.check(*c.run(workspace=torch.empty(16, dtype=torch.uint8, device="cuda")))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page", [0, 8, 64])
+def test_latent_more_rows_than_clusters(page):
+    # a cluster takes several units in turn; some rows see nothing, one tile, an odd number of tiles
+    c = Case([700, 130], 100, 128, 1, 576, dv=512, dtype=torch.bfloat16, page=page, n_new=[100, 37], latent=True, seed=32)
+    c.check(*c.run())
+    c = Case([700, 130], 100, 128, 1, 576, dv=512, dtype=torch.bfloat16, page=page, n_new=[100, 37], latent=True, seed=33,
+             window=60)
+    c.check(*c.run())
+    assert L.idx_device_status(reset=True) == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("page", [24, 192, 256, 8])
 @pytest.mark.parametrize("heads", [(4, 2, 128), (3, 1, 8)])
