@@ -594,6 +594,8 @@ def dense_attn(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tensor], batc
     if k.dtype is not q.dtype or (v is not None and v.dtype is not q.dtype):
         raise ValueError("q, k and v must have the same dtype")
     mods = None
+    if window > 2**31 - 1:
+        raise ValueError("window must be below 2**31")
     if softcap or window or slopes is not None or prefix_len is not None or doc_start is not None:
         _all_on(dev, slopes, prefix_len, doc_start)
         if slopes is not None and (slopes.dtype is not torch.float32 or not slopes.is_contiguous() or

@@ -434,7 +434,7 @@ __device__ __forceinline__ void softmax(Ctl& c, uint8_t* smem, uint32_t tmem, co
                 a2 = fmaxf(a2, fmaxf(s1[i], s1[i + 1]));
                 a3 = fmaxf(a3, fmaxf(s1[i + 2], s1[i + 3]));
             }
-            mt = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3)) * sl2;
+            mt = fmaxf(mt, fmaxf(fmaxf(a0, a1), fmaxf(a2, a3)) * sl2);     // (finite where every score is -inf)
         } else {
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
@@ -693,20 +693,9 @@ __global__ void __launch_bounds__(kHq) dense_mla_combine_kernel(DenseArgs a) {
     pdl_wait();
     const int64_t r = blockIdx.x;
     const int h = threadIdx.x;
-    // the splits' loads kBatch at a time
-    constexpr int kBatch = 8;
-    float M = -INFINITY;
-    for (int s0 = 0; s0 < a.splits; s0 += kBatch) {
-        float2 ml[kBatch];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-            ml[k] = s0 + k < a.splits ? reinterpret_cast<const float2*>(a.part_ml)[(r * a.splits + s0 + k) * kHq + h]
-                                      : make_float2(0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-            if (ml[k].y != 0.f) M = fmaxf(M, ml[k].x);
-    }
-    float acc[kCols], den = 0.f;
+    // kBatch splits at a time, all of their loads in flight together (a call rarely has more: one pass)
+    constexpr int kBatch = 16;
+    float M = -INFINITY, acc[kCols], den = 0.f;
 #pragma unroll
     for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
     for (int s0 = 0; s0 < a.splits; s0 += kBatch) {
@@ -714,20 +703,32 @@ __global__ void __launch_bounds__(kHq) dense_mla_combine_kernel(DenseArgs a) {
         float4 x[kBatch][kCols / 4];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            const int64_t u = r * a.splits + min(s0 + k, a.splits - 1);
+            ml[k] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < kCols / 4; ++i) x[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (s0 + k >= a.splits) continue;
+            const int64_t u = r * a.splits + s0 + k;
             ml[k] = reinterpret_cast<const float2*>(a.part_ml)[u * kHq + h];
 #pragma unroll
             for (int i = 0; i < kCols / 4; ++i)
                 x[k][i] = reinterpret_cast<const float4*>(a.part_o + u * (int64_t)kDv * kHq)[(int64_t)(blockIdx.y * (kCols / 4) + i) * kHq + h];
         }
+        float m_new = M;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (ml[k].y != 0.f) m_new = fmaxf(m_new, ml[k].x);
+        const float old = M == m_new ? 1.f : exp2f(M - m_new);
+        M = m_new;
+        den *= old;
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) acc[i] *= old;
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            const bool in = s0 + k < a.splits && ml[k].y != 0.f;
+            const bool in = ml[k].y != 0.f;      // (a split without keys wrote zeros)
             const float w = in ? exp2f(ml[k].x - M) : 0.f;
             den += in ? w * ml[k].y : 0.f;
 #pragma unroll
             for (int i = 0; i < kCols / 4; ++i) {
-                // (a split without keys wrote zeros)
                 acc[4 * i] = fmaf(w, x[k][i].x, acc[4 * i]);
                 acc[4 * i + 1] = fmaf(w, x[k][i].y, acc[4 * i + 1]);
                 acc[4 * i + 2] = fmaf(w, x[k][i].z, acc[4 * i + 2]);

@@ -267,6 +267,24 @@ def test_latent_beyond_one_split():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("Hq", [128, 5])
+def test_latent_infinite_scores(Hq):
+    # column 550 is no part of the values: scores of -inf in the first tiles, or everywhere
+    for keys in (128, 300):
+        c = Case([300], 1, Hq, 1, 576, dv=512, dtype=torch.bfloat16, page=64, latent=True, seed=35)
+        c.q[..., 550] = 0.5
+        c.k[c.rows[0][:keys], 0, 550] = -math.inf
+        out, lse = c.run()
+        if keys == 300:
+            assert (out == 0).all() and torch.isneginf(lse).all()
+            continue
+        ref, ref_lse, tol, tol_lse = reference(c.q, c.k, c.v, [c.rows[0][keys:]], c.lo, c.hi.clamp(max=300 - keys), c.pos,
+                                               c.scale)
+        assert ((out.cpu().double() - ref[0]).abs() <= tol[0]).all()
+        assert ((lse.cpu().double() - ref_lse[0]).abs() <= tol_lse[0]).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("page", [0, 8, 64])
 def test_latent_more_rows_than_clusters(page):
     # a cluster takes several units in turn; some rows see nothing, one tile, an odd number of tiles
@@ -618,3 +636,14 @@ def test_binding_refuses_mismatched_tensors():
             ok(**kw)
     with pytest.raises(L.LidxError):
         ok(softcap=-1.0)
+
+
+@pytest.mark.gpu
+def test_binding_refuses_a_window_beyond_int32():
+    q, k = torch.zeros(1, 4, 64, device="cuda"), torch.zeros(16, 2, 64, device="cuda")
+    b = L.Batch(torch.tensor([16], dtype=torch.int32, device="cuda"), 1, 16,
+                q_pos=torch.tensor([15], dtype=torch.int32, device="cuda"))
+    L.dense_attn(q, k, k, b, 1.0, window=2**31 - 1)
+    for window in (2**31, 2**32 + 4):
+        with pytest.raises(ValueError, match="window"):
+            L.dense_attn(q, k, k, b, 1.0, window=window)
