@@ -15,12 +15,13 @@
 // loaded again as soon as its products are done), V in one of 32 KB halves, each for
 // a product 256 columns wide.
 //
-// Eight sequences of up to 8192 keys (one token each, 64-row pages): 35 us, 27 of them
-// this kernel: 4 us to the first tile (lengths, page numbers and rows are read one
-// after the other), 15 tiles of 64 keys at 1 us, 4 us to write 256 KB of O from each
-// SM that holds one; then the merge.  A tile is bound by rank 0's scores: 36 products
-// that take 35 cycles each to issue, and the waits between them, which stand where
-// the pipe has work.  64 tokens on 16384 keys each: 306 us = 0.95 PFLOP/s.
+// Eight sequences of up to 8192 keys (one token each, 64-row pages): 29 us (972 as plain
+// tensor operations): 4 us to the first tile (lengths, page numbers and rows are read
+// one after the other), 15 tiles of 64 keys at 1 us, 4 us to write 256 KB of O from each
+// SM that holds one, and the launches and the merge.  A tile is bound by rank 0's
+// scores: 36 products that take 35 cycles each to issue, and the waits between them,
+// which stand where the pipe has work.  64 tokens on 16384 keys each: 297 us = 0.98
+// PFLOP/s.
 //
 // Every head of a query row sees the same keys, so a tile needs one bit per key;
 // rows without their bit (a page's unwritten end, a page out of range) are zeroed
@@ -620,14 +621,14 @@ __device__ __forceinline__ void output(Ctl& c, uint8_t* smem, uint32_t tmem, con
 
 template <bool kMods>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    dense_mla_kernel(DenseParams p, Geom g, int64_t n_units, const __grid_constant__ CUtensorMap map) {
+    dense_mla_kernel(DenseParams p, Geom g, int n_units, const __grid_constant__ CUtensorMap map) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint32_t* vmask = reinterpret_cast<uint32_t*>(smem + kRegion);
     Ctl& c = *reinterpret_cast<Ctl*>(vmask + kMaxKps / 32);
     const uint32_t rank = cluster_ctarank();
     const int warp = threadIdx.x >> 5;
-    const int64_t n_clusters = gridDim.x >> 1;
+    const int n_clusters = gridDim.x >> 1;
     const DenseArgs& a = p.a;
     if (a.part_o) pdl_trigger();     // (the merge follows; results are not handed on early, see lidx_internal.cuh)
     if (threadIdx.x == 0) {
@@ -643,40 +644,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = c.tmem_base;
     pdl_wait();
-    for (int64_t unit = blockIdx.x >> 1; unit < n_units; unit += n_clusters) {
-        if (unit != (int64_t)(blockIdx.x >> 1)) {
+    for (int64_t next = blockIdx.x >> 1; next < n_units; next += n_clusters) {
+        const int unit = (int)next;
+        if (next != blockIdx.x >> 1) {
             if (threadIdx.x == 0) init(c, rank);
             __syncthreads();
         }
         cluster_arrive();      // (this CTA's barriers are ready)
         Unit u;
-        u.r = unit / a.splits;
-        u.b = (int)(u.r / g.T);
+        const int row = unit / a.splits;
+        u.r = row;
+        u.b = row / g.T;
         const Interval iv = row_interval(g, a.mods, u.r, u.b, seq_n_kv(g, u.b));
-        const int64_t s0 = (int64_t)(unit % a.splits) * p.kps;
+        const int64_t s0 = (int64_t)(unit - row * a.splits) * p.kps;
         u.lo = (int)max((int64_t)iv.lo, s0);
         u.hi = (int)min((int64_t)iv.hi, s0 + p.kps);
         u.base = u.lo / kKeys * kKeys;
         u.n_tiles = u.hi > u.lo ? (u.hi - u.base + kKeys - 1) / kKeys : 0;
         u.pos = iv.pos;
-        cluster_wait();
+        // (what loads and what looks at page numbers does not wait for the other CTA)
         if (rank == 0) {
-            if (warp == 1) {
-                issue_qk(c, smem, tmem, u, g);
-            } else if (warp >= 2 && warp <= 5) {
-                if (u.n_tiles > 0) load_q(c, smem, tmem, a.q, u, g.status);
-                softmax<kMods>(c, smem, tmem, p, u, vmask, g);
-            } else if (warp < first_bit_warp(0)) {
+            if (warp == 0 || warp == 6 || warp == 7) {
                 load_k(c, smem, &map, p, u, g, warp == 0 ? 0 : warp - 5);
-            } else {
+                cluster_wait();
+            } else if (warp >= first_bit_warp(0)) {
                 stage_bits(c, vmask, rank, u, g, a.kv_rows);
+                cluster_wait();
+            } else if (warp == 1) {
+                cluster_wait();
+                issue_qk(c, smem, tmem, u, g);
+            } else {
+                if (u.n_tiles > 0) load_q(c, smem, tmem, a.q, u, g.status);
+                cluster_wait();
+                softmax<kMods>(c, smem, tmem, p, u, vmask, g);
             }
         } else {
             if (warp == 0) load_v(c, smem, &map, p, u, g);
-            else if (warp == 1) issue_pv(c, smem, smem + kVRing * kGroupBytes, tmem, u, g);
-            else if (warp <= 5) correct(c, smem + kVRing * kGroupBytes, tmem, u, g);
+            else if (warp >= first_bit_warp(1)) stage_bits(c, vmask, rank, u, g, a.kv_rows);
+            cluster_wait();
+            if (warp == 1) issue_pv(c, smem, smem + kVRing * kGroupBytes, tmem, u, g);
+            else if (warp >= 2 && warp <= 5) correct(c, smem + kVRing * kGroupBytes, tmem, u, g);
             else if (warp == 6) zero_unseen(c, smem, u, vmask, g);
-            else stage_bits(c, vmask, rank, u, g, a.kv_rows);
             output(c, smem, tmem, a, u, unit, g);
         }
         tc_fence_before();
@@ -823,9 +831,10 @@ cudaError_t launch_dense_mla(const DenseArgs& args, const Geom& g, void* ws, siz
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
     if (e != cudaSuccess) return e;
     const int64_t n_units = n_rows * splits, resident = resident_clusters();
+    if (n_units > INT32_MAX) return cudaErrorNotSupported;
     const int64_t clusters = resident > 0 && resident < n_units ? resident : n_units;
     if (2 * clusters > INT32_MAX) return cudaErrorNotSupported;
-    e = launch_pdl(kern, dim3((unsigned)(2 * clusters)), dim3(kThreads), kSmemBytes, st, p, g, n_units, map);
+    e = launch_pdl(kern, dim3((unsigned)(2 * clusters)), dim3(kThreads), kSmemBytes, st, p, g, (int)n_units, map);
     if (e != cudaSuccess || splits == 1) return e;
     return launch_pdl(dense_mla_combine_kernel, dim3((unsigned)n_rows, kDv / kCols), dim3(kHq), 0, st, a);
 }
