@@ -11,7 +11,7 @@
 //     O = O + P V     [128 x dv] f32 in TMEM      (P from TMEM, V from shared memory),
 //                     64 keys at a time: the first half's product runs while the
 //                     softmax is on the second half
-// Warps 0-3: TMA producer, an MMA issuer per row tile, V checker; then four
+// Warps 0-3: TMA producer, an MMA issuer per row tile, V inspector; then four
 // softmax warps per row tile (thread = row = TMEM lane), which also write the
 // output.  With two row tiles per CTA a K/V tile is read for 256 rows and the
 // tensor core works on one tile while the other's softmax runs; with one (up to
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
             __syncwarp();
             warp_wait(&c.done[i], 0);
         } else if (warp == kOtherWarps - 1) {
-            // -------------------------------------------------- V checker: tiles that some row sees in part
+            // -------------------------------------------------- V inspector: tiles that some row sees in part
             for (int j = 0; j < n; ++j) {
                 const int sv = j % C::kStagesV;
                 if (warp_aborted() || !warp_wait(&c.vfull[sv], (uint32_t)((j / C::kStagesV) & 1))) {
