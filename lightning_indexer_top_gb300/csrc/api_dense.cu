@@ -142,15 +142,11 @@ idx_status dense_attn(const void* q, idx_dtype dtype, int32_t n_q_heads, int32_t
     int64_t splits = want_splits(dtype, batch.n_seq, batch.n_q_per_seq, batch.max_n_kv, n_q_heads, n_kv_heads, dk, dv, tc);
     // up to kDenseCluster splits are a cluster and need no workspace
     if (splits > kDenseCluster && splits > fit) splits = fit > kDenseCluster ? fit : kDenseCluster;
-    // keys per split: whole tiles; fewer splits where that leaves some without keys
-    const int64_t unit = tc ? kDenseTcKeys : 1;
-    int64_t kps = ((int64_t)batch.max_n_kv + splits - 1) / splits;
-    kps = kps < 1 ? unit : (kps + unit - 1) / unit * unit;
-    splits = ((int64_t)batch.max_n_kv + kps - 1) / kps;
+    // a split gets whole tiles of the keys that its rows see: no more splits than tiles
+    const int64_t tiles = ((int64_t)batch.max_n_kv + (tc ? kDenseTcKeys : 1) - 1) / (tc ? kDenseTcKeys : 1);
+    if (splits > tiles) splits = tiles;
     if (splits < 1) splits = 1;
-    if (kps > INT32_MAX) kps = INT32_MAX;   // (one split)
     a.splits = (int32_t)splits;
-    a.kps = (int32_t)kps;
     const bool apart = splits > kDenseCluster;
     a.part_o = apart ? static_cast<float*>(workspace) : nullptr;
     a.part_ml = apart ? a.part_o + (size_t)n_rows * n_q_heads * dv * splits : nullptr;

@@ -32,7 +32,6 @@ struct DenseArgs {
     float* lse;               // or NULL
     int32_t splits;           // key splits; > 1: partial results go to part_o / part_ml, or, without those (at most
                               // kDenseCluster splits), the splits are a cluster that merges them
-    int32_t kps;              // keys of the position line per split
     float* part_o;            // [row * Hq + head][split][dv] unnormalised
     float* part_ml;           // [row * Hq + head][split][2]: maximum (natural-log units), sum
 };

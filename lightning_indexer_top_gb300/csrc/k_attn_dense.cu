@@ -4,7 +4,7 @@
 // The T query rows and the G = Hq / Hkv heads that share kv head g are packed
 // into rows m = t*G + h, so that a tile of R packed rows reads each K and V row
 // once for all of them.  A CTA of 128 threads owns R rows (64 for wide chunks,
-// 16 for few rows or values wider than 128) and one split of the key line, and
+// 16 for few rows or values wider than 128) and one split of its keys, and
 // walks it in tiles of 32 keys held in shared memory as f32:
 //   scores: thread = (row group, key group), a register block of 4 rows x
 //           (R/16) keys fed by 16-byte reads; masked by the rows' intervals;
@@ -126,9 +126,13 @@ __global__ void __launch_bounds__(kThreads, DV == 64 ? 3 : 0) dense_generic_kern
         full0 = max(full0, lo);
         full1 = min(full1, hi);
     }
-    const int64_t s0 = (int64_t)split * a.kps;
-    if (s0 > k0) k0 = (int)min(s0, (int64_t)INT32_MAX);
-    if (s0 + a.kps < k1) k1 = (int)(s0 + a.kps);
+    // this split's share of them, in whole tiles
+    if (k0 < k1) {
+        const int64_t share = ((int64_t)(k1 - k0) + (int64_t)a.splits * kKeys - 1) / ((int64_t)a.splits * kKeys) * kKeys;
+        const int64_t s0 = k0 + split * share, s1 = s0 + share;
+        k0 = (int)min(s0, (int64_t)INT32_MAX);
+        k1 = (int)min(s1, (int64_t)k1);
+    }
 
     // a warp's rows are the same R / 4 in the scores, the softmax and the values: no barrier between them
     const int kg = tid % S::kKeyGroups;                               // scores

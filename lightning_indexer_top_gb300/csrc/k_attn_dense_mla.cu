@@ -2,7 +2,7 @@
 // heads, bf16 rows of 576 columns, value = the first 512 (dense_attn in lidx.h).
 //
 // The output O [128 heads x 512] f32 fills all of an SM's tensor memory, so a work
-// unit (query row, split of the key line) runs on a cluster of two CTAs and walks
+// unit (query row, split of its keys) runs on a cluster of two CTAs and walks
 // tiles of 64 consecutive positions:
 //   rank 0: Q [128 x 576] lies in TMEM; S = Q K^T (two buffers of 64 columns),
 //           softmax (thread = head), P = 2^(S*c - m) as bf16, put together in
@@ -97,7 +97,6 @@ static_assert(kSmemBytes <= 232448, "shared memory");
 struct DenseParams {
     DenseArgs a;
     int box;          // rows per TMA box: 64, or the largest power of two that divides the page
-    int kps;          // keys of the position line per split
 };
 
 struct Unit {
@@ -656,11 +655,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         u.r = row;
         u.b = row / g.T;
         const Interval iv = row_interval(g, a.mods, u.r, u.b, seq_n_kv(g, u.b));
-        const int64_t s0 = (int64_t)(unit - row * a.splits) * p.kps;
-        u.lo = (int)max((int64_t)iv.lo, s0);
-        u.hi = (int)min((int64_t)iv.hi, s0 + p.kps);
-        u.base = u.lo / kKeys * kKeys;
-        u.n_tiles = u.hi > u.lo ? (u.hi - u.base + kKeys - 1) / kKeys : 0;
+        // the split's share of the tiles (cuts of the position line) that the row sees part of
+        const int first = iv.lo / kKeys, seen = iv.hi > iv.lo ? (iv.hi + kKeys - 1) / kKeys - first : 0;
+        const int share = (seen + a.splits - 1) / a.splits, at = min((unit - row * a.splits) * share, seen);
+        u.base = (first + at) * kKeys;
+        u.n_tiles = max(0, min(share, seen - at));
+        u.lo = max(iv.lo, u.base);
+        u.hi = min(iv.hi, u.base + u.n_tiles * kKeys);
         u.pos = iv.pos;
         // (what loads and what looks at page numbers does not wait for the other CTA)
         if (rank == 0) {
@@ -808,7 +809,7 @@ size_t dense_mla_workspace_bytes(int64_t n_rows, int64_t max_n_kv) {
 
 cudaError_t launch_dense_mla(const DenseArgs& args, const Geom& g, void* ws, size_t ws_bytes, cudaStream_t st) {
     const int64_t n_rows = (int64_t)g.B * g.T;
-    DenseParams p = {args, box_rows(g.page_size), 0};
+    DenseParams p = {args, box_rows(g.page_size)};
     DenseArgs& a = p.a;
     int64_t splits = dense_mla_splits(n_rows, g.max_n_kv);
     const int64_t per_split = n_rows * kHq * (kDv + 2) * (int64_t)sizeof(float);
@@ -821,7 +822,6 @@ cudaError_t launch_dense_mla(const DenseArgs& args, const Geom& g, void* ws, siz
     splits = ((int64_t)g.max_n_kv + kps - 1) / kps;
     if (splits < 1) splits = 1;
     a.splits = (int)splits;
-    p.kps = (int)kps;
     a.part_o = splits > 1 ? static_cast<float*>(ws) : nullptr;
     a.part_ml = splits > 1 ? a.part_o + (size_t)n_rows * splits * kHq * kDv : nullptr;
     CUtensorMap map;

@@ -4,7 +4,7 @@
 // The T query rows and the G = Hq / Hkv heads that share a kv head are packed
 // into rows m = t*G + h, 128 to a tile (the M side of the MMAs), so a K or V
 // tile that is read once serves every head of the group.  A CTA owns kTiles
-// such tiles of one (sequence, kv head) and one split of the key line, and
+// such tiles of one (sequence, kv head) and one split of its keys, and
 // walks it in tiles of 128 keys:
 //     S = Q K^T       [128 x 128] f32 in TMEM     (Q, K from shared memory)
 //     P = 2^(S*c - m) bf16/f16, written over S in TMEM, 64 keys at a time
@@ -119,12 +119,11 @@ struct TcArgs {
 // sums.  acc gets the unnormalised values, ml the maximum (log2 units) and the sum.
 template <typename T>
 __device__ __noinline__ void scalar_row(const DenseArgs& a, const Geom& g, int b, int gkv, int64_t rh, int h, Interval iv,
-                                        int split, float* acc, float* ml) {
+                                        int64_t s0, int64_t s1, float* acc, float* ml) {
     const T* q = static_cast<const T*>(a.q) + rh * a.dk;
     for (int c = 0; c < a.dv; ++c) acc[c] = 0.f;
     float m = -INFINITY, l = 0.f;
-    const int64_t s0 = (int64_t)split * a.kps;
-    const int64_t lo = iv.lo > s0 ? iv.lo : s0, hi = iv.hi < s0 + a.kps ? iv.hi : s0 + a.kps;
+    const int64_t lo = iv.lo > s0 ? iv.lo : s0, hi = iv.hi < s1 ? iv.hi : s1;
     for (int64_t j = lo; j < hi; ++j) {
         const int64_t row = key_row(g, b, j);
         if (row < 0 || row >= a.kv_rows) {
@@ -327,9 +326,15 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         }
     }
     __syncthreads();
-    // this split's keys, from a whole tile on (tiles are cuts of the position line)
-    const int64_t s0 = (int64_t)split * a.kps, s1 = s0 + a.kps;
+    // this split's keys: its share of the tiles (cuts of the position line) that some row of the CTA sees part of
     int k0 = c.k0, k1 = c.k1;
+    const int64_t first = k0 / kKeys, tiles_seen = k1 > k0 ? (k1 + kKeys - 1) / kKeys - first : 0;
+    // (where that is little of the line, as under a window, an equal share: 16 sequences of up to 32768 keys, window
+    // 4096, 74 us in cuts of the line, 35 in equal shares; without a window 146 and 152: CTAs that end early leave
+    // their SM's loads to the other there)
+    const int64_t line = (g.max_n_kv + kKeys - 1) / kKeys;
+    const int64_t share = ((2 * tiles_seen > line ? line : tiles_seen) + a.splits - 1) / a.splits;
+    const int64_t s0 = (first + split * share) * kKeys, s1 = s0 + share * kKeys;
     if (k0 < s0) k0 = (int)(s0 < INT32_MAX ? s0 : INT32_MAX);
     if (k1 > s1) k1 = (int)s1;
     const int t0 = k0 / kKeys;
@@ -654,7 +659,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
         float acc[D];
         if (by_key) {
             float ml[2] = {-INFINITY, 0.f};
-            if (has_row && some) scalar_row<T>(a, g, b, gkv, rh, h, iv, split, acc, ml);
+            if (has_row && some) scalar_row<T>(a, g, b, gkv, rh, h, iv, s0, s1, acc, ml);
             m_used = ml[0];
             l_run = ml[1];
             __syncwarp();

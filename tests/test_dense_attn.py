@@ -647,3 +647,17 @@ def test_binding_refuses_a_window_beyond_int32():
     for window in (2**31, 2**32 + 4):
         with pytest.raises(ValueError, match="window"):
             L.dense_attn(q, k, k, b, 1.0, window=window)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("window", [1, 130, 1000, 2600])
+@pytest.mark.parametrize("dtype,heads", [(torch.bfloat16, (8, 2, 128)), (torch.float32, (8, 2, 64))])
+def test_key_splits_share_what_a_window_leaves(dtype, heads, window):
+    # a row's splits divide the tiles that it sees, wherever they lie in a long cache; latent: the same
+    for T in (1, 3):
+        c = Case([5000, 900, 2049], T, *heads, dtype=dtype, page=16, window=window, seed=36)
+        c.check(*c.run(), what=T)
+    if dtype is torch.bfloat16:
+        c = Case([5000, 900], 1, 128, 1, 576, dv=512, dtype=dtype, page=64, window=window, latent=True, seed=37)
+        c.check(*c.run())
+    assert L.idx_device_status(reset=True) == 0
