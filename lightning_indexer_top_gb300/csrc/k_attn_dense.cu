@@ -43,12 +43,18 @@ struct Shape {
     static_assert(kThreads / kKeyGroups * 4 == R && kRowsPer % 4 == 0 && kCol4 >= 1, "thread layout");
 };
 
-// bufs: K and V tiles in flight (2: the next one is loaded under this one's arithmetic)
-size_t smem_bytes(int R, int DV, int dk, bool latent, int bufs) {
-    const int kp = round_up(dk, 4) + 4;
-    const int vp = DV + 4;
-    return sizeof(float) * ((size_t)R * kp + (size_t)bufs * kKeys * (kp + (latent ? 0 : vp)) + (size_t)kKeys * (R + 4) + 2 * R) +
-           sizeof(int) * 3 * R + sizeof(int64_t) * kKeys * 2;
+// floats of a CTA's shared memory in front of its rows' statistics: Q, the K and V tiles in flight (bufs of them; 2: the
+// next one is loaded under this one's arithmetic) and the scores, over which the merge of key splits lays R rows of dv
+// (narrow keys beside wide values: the rows are what is longer)
+__host__ __device__ constexpr int rows_floats(int R, int DV, int dk, int dv, bool latent, int bufs) {
+    const int kp = round_up(dk, 4) + 4;     // K and Q pitch: rows 4 banks apart
+    const int walk = R * kp + bufs * kKeys * (kp + (latent ? 0 : DV + 4)) + kKeys * (R + 4);
+    return walk > R * dv ? walk : R * dv;
+}
+
+size_t smem_bytes(int R, int DV, int dk, int dv, bool latent, int bufs) {
+    return sizeof(int64_t) * kKeys * 2 + sizeof(float) * ((size_t)rows_floats(R, DV, dk, dv, latent, bufs) + 2 * R) +
+           sizeof(int) * 3 * R;
 }
 
 // kAhead (f32, 16-byte aligned rows and widths): K and V go straight to shared memory by asynchronous copies, a tile
@@ -68,7 +74,7 @@ __global__ void __launch_bounds__(kThreads, DV == 64 ? 3 : 0) dense_generic_kern
     float* ks_all = qs + R * kp;                                // [kBufs][kKeys][kp]
     float* vs_all = ks_all + kBufs * kKeys * kp;                // [kBufs][kKeys][vp], unless latent
     float* ss = latent ? vs_all : vs_all + kBufs * kKeys * vp;  // [kKeys][R + 4] scores, then weights
-    float* alpha_s = ss + kKeys * (R + 4);                      // [R]
+    float* alpha_s = qs + rows_floats(R, DV, a.dk, a.dv, latent, kBufs);   // [R]
     float* slope_s = alpha_s + R;                               // [R]
     int* lo_s = reinterpret_cast<int*>(slope_s + R);
     int* hi_s = lo_s + R;
@@ -397,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, DV == 64 ? 3 : 0) dense_generic_kern
         }
     }
     __syncthreads();
-    float* o_s = qs;                                    // [R][DV], merge: over Q, K and V, which nobody reads any more
+    float* o_s = qs;                                    // [R][dv], merge: over what nobody reads any more (rows_floats)
 #pragma unroll
     for (int i = 0; i < S::kRowsPer; ++i) {
         const int rr = vg * S::kRowsPer + i;
@@ -417,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, DV == 64 ? 3 : 0) dense_generic_kern
                 if (col >= a.dv) continue;
                 const float x = l == 0.f ? 0.f : oc[e] * inv;
                 if (merge)
-                    o_s[rr * DV + col] = x;
+                    o_s[rr * a.dv + col] = x;
                 else if (a.splits > 1)
                     a.part_o[(rh * a.splits + split) * a.dv + col] = x;
                 else
@@ -437,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, DV == 64 ? 3 : 0) dense_generic_kern
                 const int from = s < a.splits ? s : 0;
                 mx[s] = *of_cta(m_s + rr, from);
                 lx[s] = s < a.splits ? *of_cta(l_s + rr, from) : 0.f;
-                ox[s] = *of_cta(o_s + rr * DV + col, from);
+                ox[s] = *of_cta(o_s + e, from);
             }
             float M = -INFINITY, den = 0.f, acc = 0.f;
 #pragma unroll
@@ -549,7 +555,7 @@ cudaError_t run(const DenseArgs& a, const Geom& g, cudaStream_t st) {
                          (uint64_t)a.dk * sizeof(T) | (a.v ? (uint64_t)a.dv * sizeof(T) : 0);
     const bool vec = all % 16 == 0;
     auto go = [&](auto kern, int dvp, int bufs) {
-        const size_t sm = smem_bytes(R, dvp, a.dk, !a.v, bufs);
+        const size_t sm = smem_bytes(R, dvp, a.dk, a.dv, !a.v, bufs);
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
         if (e != cudaSuccess) return e;
         return launch_pdl_cluster(kern, dim3((unsigned)grid), dim3(kThreads), sm, st,
@@ -558,7 +564,7 @@ cudaError_t run(const DenseArgs& a, const Geom& g, cudaStream_t st) {
     if constexpr (sizeof(T) == 4) {
         // a tile ahead where two CTAs fit an SM with it (wider rows would be alone there)
         const int dvp = R == 64 && a.dv <= 64 ? 64 : a.dv <= 128 ? 128 : 512;
-        if (vec && smem_bytes(R, dvp, a.dk, !a.v, 2) <= 113 * 1024) {
+        if (vec && smem_bytes(R, dvp, a.dk, a.dv, !a.v, 2) <= 113 * 1024) {
             if (R == 64)
                 return dvp == 64 ? go(dense_generic_kernel<T, 64, 64, true>, 64, 2) : go(dense_generic_kernel<T, 64, 128, true>, 128, 2);
             if (dvp == 128) return go(dense_generic_kernel<T, 16, 128, true>, 128, 2);
