@@ -253,6 +253,7 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kPlanThreads) page
     const int gtid = rank * kPlanThreads + tid;            // of the cluster: rows are dealt out by thread ...
     const int gwarp = rank * kWarps + warp;                // ... or by warp
     constexpr int kAll = kCl * kPlanThreads, kAllWarps = kCl * kWarps;
+    sm100::cluster_arrive();        // this CTA has started: from the wait on, the others may write to its memory
     pdl_wait();
     // ---- the requests; the held pages.  Nothing is copied unless the plan says so.
     bool bad = false;
@@ -265,6 +266,7 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kPlanThreads) page
     for (int w = tid; w < bm.n_mine(); w += kPlanThreads)
         bm.mine[w] = held_bits(a.held, (int64_t)rank * bm.slice + w, a.n_pages);
     bad = __syncthreads_or(bad);
+    sm100::cluster_wait();
     tell(s, 0, bad ? 1 : 0);
     sm100::cluster_sync();
     int any;
