@@ -539,14 +539,15 @@ __global__ void __launch_bounds__(128) dense_combine_kernel(DenseArgs a, int64_t
     }
 }
 
-// rows of a CTA's tile: 64 when the sequence's packed rows fill more than one tile of 16 and the
-// values are at most 128 wide (the wider output block needs the registers)
-int tile_rows(int64_t packed, int dv) { return dv <= 128 && packed > 16 ? 64 : 16; }
+// rows of a CTA's tile: 64 when the sequence's packed rows fill more than one tile of 16, the values are at most 128 wide
+// (the wider output block needs the registers) and the keys at most 528 (231,680 bytes of shared memory with values of
+// 128 beside them; 529 columns take 233,216, more than the 232,448 that a CTA may have)
+int tile_rows(int64_t packed, int dk, int dv) { return dv <= 128 && dk <= 528 && packed > 16 ? 64 : 16; }
 
 template <typename T>
 cudaError_t run(const DenseArgs& a, const Geom& g, cudaStream_t st) {
     const int64_t packed = (int64_t)g.T * (a.Hq / a.Hkv);
-    const int R = tile_rows(packed, a.dv);
+    const int R = tile_rows(packed, a.dk, a.dv);
     const int64_t tiles = (packed + R - 1) / R;
     const int64_t grid = (int64_t)g.B * a.Hkv * tiles * a.splits;
     if (grid > INT32_MAX || tiles > INT32_MAX) return cudaErrorNotSupported;
@@ -580,9 +581,8 @@ cudaError_t run(const DenseArgs& a, const Geom& g, cudaStream_t st) {
 // enough CTAs to cover the SMs four times, at least a tile of keys each: a tile takes about 4 us whatever it holds
 // (256 keys for one token of four f32 heads: 19.7 us in two splits, 10.5 in eight)
 int dense_generic_splits(int64_t n_seq, int64_t n_q, int64_t max_n_kv, int Hq, int Hkv, int dk, int dv) {
-    (void)dk;
     const int64_t packed = n_q * (Hq / Hkv);
-    const int R = tile_rows(packed, dv);
+    const int R = tile_rows(packed, dk, dv);
     const int64_t units = n_seq * Hkv * ((packed + R - 1) / R);
     int sms = sm_count();
     if (sms < 2) sms = 152;

@@ -30,3 +30,14 @@ def test_merged_rows_of_narrow_latents(dtype, dk, dv):
         c = Case(n_kv, T, Hq, 1, dk, dv=dv, dtype=dtype, latent=True, seed=42)
         c.check(*c.run(), what=(T, Hq, n_kv))
     assert L.idx_device_status(reset=True) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dk,dv,latent", [(576, 128, False), (576, 64, False), (529, 128, False), (528, 128, False),
+                                          (549, 64, False), (576, 128, True), (573, 40, True), (576, 512, False)])
+def test_wide_keys_of_many_rows(dtype, dk, dv, latent):
+    # 64 rows of keys this wide are more than a CTA's shared memory holds
+    for T, Hq in ((5, 8), (17, 1)):
+        c = Case([150, 33], T, Hq, 1, dk, dv=dv, dtype=dtype, page=16, latent=latent, seed=43)
+        c.check(*c.run(), what=(T, Hq))
