@@ -483,8 +483,8 @@ int32_t sparse_decode_step_fused(int64_t n_rows, int32_t n_q_per_seq, int32_t ma
  * and pages of a multiple of 8 rows; the weights are then rounded to dtype for the
  * second product.  Everything else runs on the CUDA cores.
  * Errors: those of sparse_attn_decode's arguments; softcap or window negative,
- * softcap or scale / softcap not finite, window, slopes or prefix_len without
- * q_pos: INVALID_ARG; max_n_kv > 2^31 - 1025: UNSUPPORTED.
+ * |scale| or softcap above 2^127, scale / softcap not finite, window, slopes or
+ * prefix_len without q_pos: INVALID_ARG; max_n_kv > 2^31 - 1025: UNSUPPORTED.
  */
 typedef struct idx_attn_mods {
     float softcap;             /* 0: scores are not capped */

@@ -100,11 +100,12 @@ idx_status dense_attn(const void* q, idx_dtype dtype, int32_t n_q_heads, int32_t
     if (v && v_row_stride < (int64_t)n_kv_heads * dv)
         return bad(IDX_ERR_INVALID_ARG, "%s: v_row_stride < Hkv*dv", what);
     if (kv_rows < 0) return bad(IDX_ERR_INVALID_ARG, "%s: kv_rows < 0", what);
-    if (!std::isfinite(scale)) return bad(IDX_ERR_INVALID_ARG, "%s: scale not finite", what);
+    // (the tensor-core kernels hold both times log2(e))
+    if (!(std::fabs(scale) <= 0x1p127f)) return bad(IDX_ERR_INVALID_ARG, "%s: scale not finite or above 2^127", what);
     DenseArgs a = {};
     if (mods) a.mods = *mods;
-    if (!std::isfinite(a.mods.softcap) || a.mods.softcap < 0.f)
-        return bad(IDX_ERR_INVALID_ARG, "%s: softcap must be finite and >= 0", what);
+    if (!(a.mods.softcap >= 0.f && a.mods.softcap <= 0x1p127f))
+        return bad(IDX_ERR_INVALID_ARG, "%s: softcap must be finite and >= 0, at most 2^127", what);
     if (a.mods.softcap > 0.f && !std::isfinite(scale / a.mods.softcap))
         return bad(IDX_ERR_INVALID_ARG, "%s: scale / softcap must be finite", what);
     if (a.mods.window < 0) return bad(IDX_ERR_INVALID_ARG, "%s: window < 0", what);

@@ -77,6 +77,7 @@ struct Score {
     float c;            // scale * log2(e)
     float inv_cap;      // scale / softcap (0: no cap)
     float cap;          // softcap * log2(e)
+    float series;       // the largest product whose capped score is the series in it; below 0: none is
     float slope;        // the row's slope * log2(e)
     bool biased;        // slopes are given
 };
@@ -116,38 +117,42 @@ __device__ __forceinline__ float tanh_large(float x) {
 // Every lane of a warp comes here together.
 // A capped score is cap * tanh(x), x = s * scale / softcap: for |x| <= 0.3 by the Taylor series of tanh up to x^9
 // (the next term is below 2^-24 of x there), as s times a polynomial in s^2 whose coefficients hold the factors (six
-// packed operations for two scores; the exponential form takes two special functions for each).
+// packed operations for two scores; the exponential form takes two special functions for each).  Where those
+// coefficients, scale * (scale / softcap)^8 the farthest, leave f32's normal range, the series is taken in x itself.
 template <int N>
 __device__ __forceinline__ void modify(float (&s)[N], const Score& sc, float d0, bool past) {
     if (sc.inv_cap != 0.f) {
         float big = 0.f;
 #pragma unroll
         for (int i = 0; i < N; i += 2) big = fmaxf(fmaxf(big, fabsf(s[i])), fabsf(s[i + 1]));
-        // (a NaN is no larger than anything and goes through the series)
-        const bool large = big * fabsf(sc.inv_cap) > 0.3f;
         const float i2 = sc.inv_cap * sc.inv_cap;
+        // (a NaN is no larger than anything and goes through the series)
+        const bool large = big > sc.series;
         auto both = [](float x) { return pair(x, x); };
         const uint64_t c1 = both(sc.c), c3 = both(sc.c * i2 * (-1.f / 3.f)), c5 = both(sc.c * i2 * i2 * (2.f / 15.f)),
                        c7 = both(sc.c * i2 * i2 * i2 * (-17.f / 315.f)),
                        c9 = both(sc.c * i2 * i2 * i2 * i2 * (62.f / 2835.f));
-        auto series = [&](float x, float y, float& rx, float& ry) {
-            const uint64_t v = pair(x, y), z = mul2(v, v);
-            unpair(mul2(v, fma2(fma2(fma2(fma2(c9, z, c7), z, c5), z, c3), z, c1)), rx, ry);
-        };
         // (the x^9 term is below 2^-27 of x up to 0.15)
-        const bool some = big * fabsf(sc.inv_cap) > 0.15f;
+        const bool some = big > 0.5f * sc.series;
         if (__any_sync(0xffffffffu, large)) {
+            const uint64_t inv = both(sc.inv_cap), one = both(1.f);
 #pragma unroll
             for (int i = 0; i < N; i += 2) {
-                const float x0 = s[i] * sc.inv_cap, x1 = s[i + 1] * sc.inv_cap;
-                float y0, y1;
-                series(s[i], s[i + 1], y0, y1);
+                const uint64_t v = pair(s[i], s[i + 1]), x = mul2(v, inv), z = mul2(x, x);
+                const uint64_t p = fma2(fma2(fma2(fma2(both(62.f / 2835.f), z, both(-17.f / 315.f)), z, both(2.f / 15.f)), z,
+                                             both(-1.f / 3.f)), z, one);
+                float x0, x1, y0, y1;
+                unpair(x, x0, x1);
+                unpair(mul2(mul2(v, c1), p), y0, y1);
                 s[i] = fabsf(x0) > 0.3f ? sc.cap * tanh_large(x0) : y0;
                 s[i + 1] = fabsf(x1) > 0.3f ? sc.cap * tanh_large(x1) : y1;
             }
         } else if (__any_sync(0xffffffffu, some)) {
 #pragma unroll
-            for (int i = 0; i < N; i += 2) series(s[i], s[i + 1], s[i], s[i + 1]);
+            for (int i = 0; i < N; i += 2) {
+                const uint64_t v = pair(s[i], s[i + 1]), z = mul2(v, v);
+                unpair(mul2(v, fma2(fma2(fma2(fma2(c9, z, c7), z, c5), z, c3), z, c1)), s[i], s[i + 1]);
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < N; i += 2) {
@@ -178,6 +183,8 @@ __device__ __forceinline__ Score make_score(const DenseArgs& a, float slope) {
     s.c = a.scale * kLog2e;
     s.inv_cap = a.mods.softcap > 0.f ? a.scale / a.mods.softcap : 0.f;
     s.cap = a.mods.softcap * kLog2e;
+    const float i2 = s.inv_cap * s.inv_cap, c9 = fabsf(s.c * i2 * i2 * i2 * i2 * (62.f / 2835.f));
+    s.series = c9 >= 0x1p-126f && c9 <= 0x1p100f ? 0.3f / fabsf(s.inv_cap) : -1.f;
     s.slope = slope * kLog2e;
     s.biased = a.mods.slopes != nullptr;
     return s;

@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, DV == 64 ? 3 : 0) dense_generic_kern
 #pragma unroll
         for (int c = 0; c < 2 * S::kCol4; ++c) o[i][c] = 0ull;
     float m_run = -INFINITY, l_run = 0.f;
-    const float cap = a.mods.softcap, inv_cap = cap > 0.f ? 1.f / cap : 0.f;
+    const float cap = a.mods.softcap, inv_cap = cap > 0.f ? fminf(1.f / cap, FLT_MAX) : 0.f;   // (finite: 0 stays 0)
 
     // cache row of position j of the split, -1 past its end or outside the cache
     auto row_of = [&](int j) -> int64_t {

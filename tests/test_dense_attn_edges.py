@@ -1,5 +1,8 @@
 """dense_attn at widths, caps and masks where its kernels' limits lie; tolerances as in test_dense_attn.py."""
 
+import ctypes
+import math
+
 import pytest
 import torch
 
@@ -41,3 +44,57 @@ def test_wide_keys_of_many_rows(dtype, dk, dv, latent):
     for T, Hq in ((5, 8), (17, 1)):
         c = Case([150, 33], T, Hq, 1, dk, dv=dv, dtype=dtype, page=16, latent=latent, seed=43)
         c.check(*c.run(), what=(T, Hq))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", [64, 128, 576])
+@pytest.mark.parametrize("cap", [1e-40, 1e-30, 1e-7, 1e-5, 1e-4, 1e-2])
+def test_small_caps(dtype, d, cap):
+    # every score is within the cap of 0, to which a product of exactly 0 belongs beside large ones
+    c = Case([150, 40], 3, 128 if d == 576 else 4, 1, d, dv=min(d, 512), dtype=dtype, latent=d == 576, cap=cap, seed=44)
+    c.scale = 1.0 if cap > 1e-38 else 1e-3      # (scale / softcap has to be finite)
+    c.q[0, 1] = 0
+    for r in c.rows:
+        c.k[r[3:20]] = 0
+    c.v = c.k[..., :c.dv] if c.latent else c.v
+    c.check(*c.run(), what=cap)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T", [1, 40])
+@pytest.mark.parametrize("d", [64, 128, 576])
+@pytest.mark.parametrize("top", [0.14, 0.29, 0.9, 1e-3])
+def test_large_caps(dtype, T, d, top):
+    # one key, query rows that are multiples of basis vectors: lse is the score, up to `top` of a cap of millions.
+    # tanh by its series is off by 2^-24 of the score and the roundings of its dozen operations, by the exponential
+    # within a few of them of the cap, which is below 1 / top of the score
+    Hq = 128 if d == 576 else 8
+    c = Case([1], T, Hq, 1, d, dv=min(d, 512), dtype=dtype, latent=d == 576, causal=False, seed=45)
+    c.scale = 1.0
+    c.k[0, 0] = (torch.arange(1, d + 1) * (2.0 ** 15 / d)).to(dtype)
+    at = (torch.arange(T * Hq) * 7 + d - 1) % d
+    c.q = (torch.nn.functional.one_hot(at, d) * 256).to(dtype).view(1, T, Hq, d)
+    c.v = c.k[..., :c.dv] if c.latent else c.v
+    c.cap = float((c.k[0, 0].double().max() * 256 / top).float())
+    out, lse = c.run()
+    x = c.k[0, 0].double()[at] * 256
+    want = c.cap * torch.tanh(x / c.cap)
+    tol = 2.0 ** -20 * want + (2.0 ** -20 * c.cap if top > 0.3 else 0.0)
+    assert ((lse.view(-1).cpu().double() - want).abs() <= tol).all()
+    assert torch.equal(out.view(T * Hq, -1).cpu(), c.v[0, 0].expand(T * Hq, c.dv))
+
+
+def _call(scale, softcap):
+    m = L._Mods(softcap, None, 0, None, None)
+    one = ctypes.c_void_p(16)
+    b = L._Batch(1, 1, one, None, 8, None, 8, None, 0, 0)
+    return L.load().dense_attn(one, 1, 1, 1, 64, 64, one, one, 64, 64, 8, b, m, scale, one, None, None, 0, None)
+
+
+@pytest.mark.parametrize("scale,softcap,word", [(3e38, 0.0, "scale"), (-3e38, 0.0, "scale"), (math.inf, 0.0, "scale"),
+                                                (1.0, 3e38, "softcap"), (1.0, math.nan, "softcap")])
+def test_scales_and_caps_beyond_the_kernels_range_are_refused(scale, softcap, word):
+    assert _call(scale, softcap) == L.IDX_ERR_INVALID_ARG
+    assert word in L.load().idx_last_error().decode()
