@@ -459,8 +459,13 @@ int32_t sparse_decode_step_fused(int64_t n_rows, int32_t n_q_per_seq, int32_t ma
  * over the keys lo(r) <= j < hi(r):
  *     hi(r) = n_kv[b]                                        without q_pos
  *           = 0                                              p < 0 (a padding row)
- *           = min(n_kv[b], max(p + 1, prefix_len[b]))        else (prefix_len NULL: 0)
+ *           = min(n_kv[b], max(p + 1, prefix_len[b], prefix_end[r]))   else (NULL: 0)
  *     lo(r) = max(0, doc_start[r], p - window + 1)           (each where given)
+ * prefix_len is one prefix of the whole sequence: beside doc_start it lets the rows
+ * of an early document see later documents' keys up to it.  Packed documents, each
+ * with a prefix of its own (row and key of one document, and the key no later than
+ * the row or in the document's prefix), take prefix_end: the position behind the
+ * prefix of the row's document.
  * Chunks of unequal length are padded to n_q_per_seq rows with q_pos = -1.  A row
  * that sees no key, or whose every score is -inf, gets zeros and lse = -inf.
  * Keys outside a row's interval never reach its result, whatever bytes they hold
@@ -483,15 +488,17 @@ int32_t sparse_decode_step_fused(int64_t n_rows, int32_t n_q_per_seq, int32_t ma
  * and pages of a multiple of 8 rows; the weights are then rounded to dtype for the
  * second product.  Everything else runs on the CUDA cores.
  * Errors: those of sparse_attn_decode's arguments; softcap or window negative,
- * |scale| or softcap above 2^127, scale / softcap not finite, window, slopes or
- * prefix_len without q_pos: INVALID_ARG; max_n_kv > 2^31 - 1025: UNSUPPORTED.
+ * |scale| or softcap above 2^127, scale / softcap not finite, window, slopes,
+ * prefix_len or prefix_end without q_pos: INVALID_ARG; max_n_kv > 2^31 - 1025:
+ * UNSUPPORTED.
  */
 typedef struct idx_attn_mods {
     float softcap;             /* 0: scores are not capped */
     const float* slopes;       /* device f32 [n_q_heads] or NULL: distance bias of each head */
     int32_t window;            /* 0: none; else a row sees at most this many positions up to its own */
-    const int32_t* prefix_len; /* device int32 [n_seq] or NULL: positions every row of the sequence sees */
+    const int32_t* prefix_len; /* device int32 [n_seq] or NULL: a sequence's rows see up to here, if not further */
     const int32_t* doc_start;  /* device int32 [n_seq*n_q_per_seq] or NULL: first position of the row's document */
+    const int32_t* prefix_end; /* device int32 [n_seq*n_q_per_seq] or NULL: the row sees up to here, if not further */
 } idx_attn_mods;
 
 idx_status dense_attn(const void* q, idx_dtype dtype, int32_t n_q_heads, int32_t n_kv_heads, int32_t dk, int32_t dv,

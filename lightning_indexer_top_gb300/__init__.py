@@ -66,6 +66,7 @@ class _Mods(ctypes.Structure):
         ("window", ctypes.c_int32),
         ("prefix_len", ctypes.c_void_p),
         ("doc_start", ctypes.c_void_p),
+        ("prefix_end", ctypes.c_void_p),
     ]
 
 
@@ -550,6 +551,7 @@ def dense_attn_workspace_size(dtype: torch.dtype, n_seq: int, n_q_per_seq: int, 
 def dense_attn(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tensor], batch: Batch, scale: float, *,
                softcap: float = 0.0, slopes: Optional[torch.Tensor] = None, window: int = 0,
                prefix_len: Optional[torch.Tensor] = None, doc_start: Optional[torch.Tensor] = None,
+               prefix_end: Optional[torch.Tensor] = None,
                out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                workspace: Optional[torch.Tensor] = None, dv: Optional[int] = None) -> torch.Tensor:
     """Attention of a chunk of new tokens (batch.n_q_per_seq rows per sequence, 1 = decode) over every key
@@ -558,8 +560,9 @@ def dense_attn(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tensor], batc
     [B*T, Hq, dv] of q's dtype; lse, if given (f32 [B*T, Hq]), gets the log of the rows' softmax sums.
 
     Row r sees positions up to batch.q_pos[r] (none if that is negative: a padding row, whose out is
-    zero), or up to prefix_len[b] where that is further; not before doc_start[r]; with window, at most
-    that many positions up to its own.  softcap c > 0: scores x become c * tanh(x / c); slopes (f32 [Hq]):
+    zero), or up to prefix_len[b] or prefix_end[r] where that is further; not before doc_start[r]; with window,
+    at most that many positions up to its own.  (prefix_len is the sequence's and runs on into later documents;
+    documents with prefixes of their own take prefix_end, the position behind that of the row's document.)  softcap c > 0: scores x become c * tanh(x / c); slopes (f32 [Hq]):
     minus slopes[h] * |q_pos[r] - j| for key j."""
     dev = q.device
     _need_cuda(q)
@@ -596,14 +599,15 @@ def dense_attn(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tensor], batc
     mods = None
     if window > 2**31 - 1:
         raise ValueError("window must be below 2**31")
-    if softcap or window or slopes is not None or prefix_len is not None or doc_start is not None:
-        _all_on(dev, slopes, prefix_len, doc_start)
+    if softcap or window or not (slopes is prefix_len is doc_start is prefix_end is None):
+        _all_on(dev, slopes, prefix_len, doc_start, prefix_end)
         if slopes is not None and (slopes.dtype is not torch.float32 or not slopes.is_contiguous() or
                                    slopes.numel() != Hq):
             raise ValueError("slopes must be a contiguous float32 tensor with one entry per query head")
         mods = _Mods(softcap, None if slopes is None else slopes.data_ptr(), window,
                      None if prefix_len is None else _i32("prefix_len", prefix_len, b.n_seq),
-                     None if doc_start is None else _i32("doc_start", doc_start, rows))
+                     None if doc_start is None else _i32("doc_start", doc_start, rows),
+                     None if prefix_end is None else _i32("prefix_end", prefix_end, rows))
     if out is None:
         out = torch.empty((rows, Hq, dv), device=dev, dtype=q.dtype)
     elif out.shape != (rows, Hq, dv) or out.dtype is not q.dtype or not out.is_contiguous():

@@ -109,8 +109,8 @@ idx_status dense_attn(const void* q, idx_dtype dtype, int32_t n_q_heads, int32_t
     if (a.mods.softcap > 0.f && !std::isfinite(scale / a.mods.softcap))
         return bad(IDX_ERR_INVALID_ARG, "%s: scale / softcap must be finite", what);
     if (a.mods.window < 0) return bad(IDX_ERR_INVALID_ARG, "%s: window < 0", what);
-    if (!batch.q_pos && (a.mods.window > 0 || a.mods.slopes || a.mods.prefix_len))
-        return bad(IDX_ERR_INVALID_ARG, "%s: window, slopes and prefix_len need q_pos", what);
+    if (!batch.q_pos && (a.mods.window > 0 || a.mods.slopes || a.mods.prefix_len || a.mods.prefix_end))
+        return bad(IDX_ERR_INVALID_ARG, "%s: window, slopes, prefix_len and prefix_end need q_pos", what);
     if (workspace && !aligned16(workspace))
         return bad(IDX_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", what);
     if (batch.max_n_kv > INT32_MAX - 1024)

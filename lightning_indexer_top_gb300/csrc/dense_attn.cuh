@@ -55,6 +55,7 @@ __device__ __forceinline__ Interval row_interval(const Geom& g, const idx_attn_m
         } else {
             int h = p < INT32_MAX ? p + 1 : p;
             if (m.prefix_len) h = max(h, m.prefix_len[b]);
+            if (m.prefix_end) h = max(h, m.prefix_end[r]);
             v.hi = min(n_kv, h);
             if (m.window > 0) v.lo = max(0, p - m.window + 1);
         }

@@ -86,6 +86,51 @@ def test_large_caps(dtype, T, d, top):
     assert torch.equal(out.view(T * Hq, -1).cpu(), c.v[0, 0].expand(T * Hq, c.dv))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,heads", [(200, (4, 2, 128)), (70, (3, 3, 64)), (1, (8, 1, 128)), (9, (128, 1, 576))])
+@pytest.mark.parametrize("window", [0, 50])
+def test_packed_documents_with_prefixes(dtype, T, heads, window):
+    # rows i, keys j of one sequence: j is seen if it is of i's document, and no later than i or in the document's prefix
+    n_kv = [200, 133, 64 if T <= 64 else T]
+    c = Case(n_kv, T, *heads, dv=min(heads[2], 512), dtype=dtype, page=16, n_new=[T, min(T, 100), T], latent=heads[2] == 576,
+             seed=46)
+    g = torch.Generator().manual_seed(7)
+    seen = torch.zeros(c.B, T, c.N, dtype=torch.bool)
+    start, end = torch.zeros(c.B, T, dtype=torch.int32), torch.zeros(c.B, T, dtype=torch.int32)
+    for b, n in enumerate(n_kv):
+        doc = (torch.rand(n, generator=g) < 0.03).cumsum(0)
+        first = torch.searchsorted(doc, doc)
+        length = torch.bincount(doc)[doc]
+        prefix = (torch.rand(int(doc[-1]) + 1, generator=g)[doc] * (length + 1)).long()     # none of it to all of it
+        j = torch.arange(n)
+        for t in range(T):
+            i = int(c.pos[b, t])
+            if i < 0:
+                continue
+            seen[b, t, :n] = (doc == doc[i]) & ((j <= i) | (j - first[i] < prefix[i]))
+            if window:
+                seen[b, t, :n] &= j > i - window
+            start[b, t], end[b, t] = first[i], first[i] + prefix[i]
+    some = seen.any(-1)
+    c.lo = torch.where(some, seen.long().argmax(-1), 0)
+    c.hi = torch.where(some, c.N - seen.flip(-1).long().argmax(-1), 0)
+    assert torch.equal(seen.sum(-1), c.hi - c.lo) and (T == 1 or (c.hi > c.pos + 1).any())
+    q = c.q.reshape(c.B * T, *c.q.shape[2:]).cuda()
+    lse = torch.empty(q.shape[:2], device="cuda")
+    out = L.dense_attn(q, c.k.cuda(), None if c.latent else c.v.cuda(), c.batch(), c.scale, dv=c.dv, lse=lse, window=window,
+                       doc_start=start.cuda().view(-1), prefix_end=end.cuda().view(-1))
+    c.check(out, lse)
+
+
+@pytest.mark.gpu
+def test_the_further_of_two_prefixes():
+    c = Case([150, 90], 20, 4, 2, 64, dtype=torch.bfloat16, prefix=[140, 20], seed=47)
+    ends = torch.arange(40, dtype=torch.int32).view(2, 20) * 9 - 30
+    c.hi = torch.minimum(torch.maximum(c.hi, ends.long()), torch.tensor(c.n_kv)[:, None])
+    c.check(*c.run(prefix_end=ends.cuda().view(-1)))
+
+
 def _call(scale, softcap):
     m = L._Mods(softcap, None, 0, None, None)
     one = ctypes.c_void_p(16)
@@ -98,3 +143,11 @@ def _call(scale, softcap):
 def test_scales_and_caps_beyond_the_kernels_range_are_refused(scale, softcap, word):
     assert _call(scale, softcap) == L.IDX_ERR_INVALID_ARG
     assert word in L.load().idx_last_error().decode()
+
+
+def test_a_prefix_by_row_needs_positions():
+    one = ctypes.c_void_p(16)
+    m = L._Mods(prefix_end=16)
+    b = L._Batch(1, 1, one, None, 8, None, 8, None, 0, 0)
+    st = L.load().dense_attn(one, 1, 1, 1, 64, 64, one, one, 64, 64, 8, b, m, 1.0, one, None, None, 0, None)
+    assert st == L.IDX_ERR_INVALID_ARG and "q_pos" in L.load().idx_last_error().decode()
