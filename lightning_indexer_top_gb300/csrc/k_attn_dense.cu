@@ -43,26 +43,26 @@ struct Shape {
     static_assert(kThreads / kKeyGroups * 4 == R && kRowsPer % 4 == 0 && kCol4 >= 1, "thread layout");
 };
 
-// floats of a CTA's shared memory in front of its rows' statistics: Q, the K and V tiles in flight (bufs of them; 2: the
-// next one is loaded under this one's arithmetic) and the scores, over which the merge of key splits lays R rows of dv
-// (narrow keys beside wide values: the rows are what is longer)
-__host__ __device__ constexpr int rows_floats(int R, int DV, int dk, int dv, bool latent, int bufs) {
-    const int kp = round_up(dk, 4) + 4;     // K and Q pitch: rows 4 banks apart
-    const int walk = R * kp + bufs * kKeys * (kp + (latent ? 0 : DV + 4)) + kKeys * (R + 4);
-    return walk > R * dv ? walk : R * dv;
-}
-
+// bufs: K and V tiles in flight (2: the next one is loaded under this one's arithmetic).  The rows' statistics come
+// first; the merge of key splits lays R rows of dv over Q, K, V and the scores, which narrow keys beside wide values are
+// shorter than.
 size_t smem_bytes(int R, int DV, int dk, int dv, bool latent, int bufs) {
-    return sizeof(int64_t) * kKeys * 2 + sizeof(float) * ((size_t)rows_floats(R, DV, dk, dv, latent, bufs) + 2 * R) +
-           sizeof(int) * 3 * R;
+    const int kp = round_up(dk, 4) + 4;
+    const int vp = DV + 4;
+    const int walk = R * kp + bufs * kKeys * (kp + (latent ? 0 : vp)) + kKeys * (R + 4);
+    return sizeof(int64_t) * kKeys * 2 + (sizeof(float) * 2 + sizeof(int) * 3) * R +
+           sizeof(float) * (walk > R * dv ? walk : R * dv);
 }
 
 // kAhead (f32, 16-byte aligned rows and widths): K and V go straight to shared memory by asynchronous copies, a tile
 // ahead.  Otherwise each tile is loaded, widened and stored before its arithmetic.
 // Narrow values: registers for three CTAs to an SM (256 tokens on 2048 keys, heads of 64: 193 -> 187 us); for 128 columns
-// neither shared memory nor registers leave room for a third.
+// neither shared memory nor registers leave room for a third.  There, and for the widest values, the compiler is told of
+// two, which it makes use of: 252 registers for 186 (512 tokens on 4096 keys: 2.48 -> 2.39 ms), 223 for 167 (256 tokens on
+// 2048 keys, heads of 256: 1.88 -> 1.80 ms).
 template <typename T, int R, int DV, bool kAhead>
-__global__ void __launch_bounds__(kThreads, DV == 64 ? 3 : 0) dense_generic_kernel(DenseArgs a, Geom g, int tiles, bool vec) {
+__global__ void __launch_bounds__(kThreads, DV == 64 ? 3 : DV == 512 || (R == 64 && kAhead) ? 2 : 0)
+    dense_generic_kernel(DenseArgs a, Geom g, int tiles, bool vec) {
     using S = Shape<R, DV>;
     extern __shared__ __align__(16) unsigned char sm_raw[];
     const int kp = round_up(a.dk, 4) + 4;       // K and Q pitch: rows 4 banks apart
@@ -70,15 +70,15 @@ __global__ void __launch_bounds__(kThreads, DV == 64 ? 3 : 0) dense_generic_kern
     const int vp = latent ? kp : DV + 4;
     constexpr int kBufs = kAhead ? 2 : 1;
     int64_t* rows_all = reinterpret_cast<int64_t*>(sm_raw);     // [2][kKeys] cache rows, negative: none
-    float* qs = reinterpret_cast<float*>(rows_all + 2 * kKeys); // [R][kp]
-    float* ks_all = qs + R * kp;                                // [kBufs][kKeys][kp]
-    float* vs_all = ks_all + kBufs * kKeys * kp;                // [kBufs][kKeys][vp], unless latent
-    float* ss = latent ? vs_all : vs_all + kBufs * kKeys * vp;  // [kKeys][R + 4] scores, then weights
-    float* alpha_s = qs + rows_floats(R, DV, a.dk, a.dv, latent, kBufs);   // [R]
+    float* alpha_s = reinterpret_cast<float*>(rows_all + 2 * kKeys);   // [R]
     float* slope_s = alpha_s + R;                               // [R]
     int* lo_s = reinterpret_cast<int*>(slope_s + R);
     int* hi_s = lo_s + R;
     int* pos_s = hi_s + R;
+    float* qs = reinterpret_cast<float*>(pos_s + R);            // [R][kp]
+    float* ks_all = qs + R * kp;                                // [kBufs][kKeys][kp]
+    float* vs_all = ks_all + kBufs * kKeys * kp;                // [kBufs][kKeys][vp], unless latent
+    float* ss = latent ? vs_all : vs_all + kBufs * kKeys * vp;  // [kKeys][R + 4] scores, then weights
 
     const int tid = threadIdx.x;
     const int G = a.Hq / a.Hkv;
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, DV == 64 ? 3 : 0) dense_generic_kern
         }
     }
     __syncthreads();
-    float* o_s = qs;                                    // [R][dv], merge: over what nobody reads any more (rows_floats)
+    float* o_s = qs;                                    // [R][dv], merge: over what nobody reads any more
 #pragma unroll
     for (int i = 0; i < S::kRowsPer; ++i) {
         const int rr = vg * S::kRowsPer + i;
