@@ -482,7 +482,8 @@ int32_t sparse_decode_step_fused(int64_t n_rows, int32_t n_q_per_seq, int32_t ma
  *              split less, with the same results up to rounding.  Calls whose
  *              work overlaps on the GPU need workspaces of their own.
  * Sums, maxima and outputs are accumulated in f32.  A key row outside the cache
- * (a page number out of range) is skipped and flagged (IDX_ERR_DEVICE_BOUNDS).
+ * (a page number out of range) is skipped, and flagged (IDX_ERR_DEVICE_BOUNDS) if
+ * some row sees it.
  * 16-bit K and V of at most 128 columns (a multiple of 8) and the bf16 latent of 128
  * heads (576 / 512) run on the tensor cores, given 16-byte aligned tensors and rows
  * and pages of a multiple of 8 rows; the weights are then rounded to dtype for the

@@ -160,9 +160,7 @@ __global__ void __launch_bounds__(kThreads, DV == 64 ? 3 : DV == 512 || (R == 64
     auto row_of = [&](int j) -> int64_t {
         if (j >= k1) return -1;
         const int64_t row = key_row(g, b, j);
-        if (row >= 0 && row < a.kv_rows) return row;
-        flag(g.status, IDX_ERR_DEVICE_BOUNDS);
-        return -1;
+        return row >= 0 && row < a.kv_rows ? row : -1;
     };
     // kAhead: four threads to a key, each every fourth 16-byte piece of its K and V rows (zeros for no row, and true)
     auto send = [&](int t0, int buf) {
@@ -312,6 +310,10 @@ __global__ void __launch_bounds__(kThreads, DV == 64 ? 3 : DV == 512 || (R == 64
             }
 #pragma unroll
             for (int off = 1; off < kPerRow; off <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, off));
+            if (bad) {      // a key outside the cache counts where a row sees it
+                for (int kl = sk; kl < kKeys; kl += kPerRow)
+                    if (rows_s[kl] < 0 && t0 + kl >= lo && t0 + kl < min(hi, k1)) flag(g.status, IDX_ERR_DEVICE_BOUNDS);
+            }
             const float m_new = fmaxf(m_run, mt);
             const float m_ref = m_new == -INFINITY ? 0.f : m_new;
             const float alpha = m_run == m_new ? 1.f : expf(m_run - m_ref);

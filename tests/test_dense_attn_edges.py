@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import lightning_indexer_top_gb300 as L
-from test_dense_attn import DTYPES, Case
+from test_dense_attn import DTYPES, Case, intervals
 
 # dk, dv of K and V apart / of a latent; every one with two to eight key splits that a cluster merges.  Narrow keys
 # beside wide values, and latents just past a step of the value width: the merged rows are longer than Q, K, V and the
@@ -121,6 +121,27 @@ def test_packed_documents_with_prefixes(dtype, T, heads, window):
     out = L.dense_attn(q, c.k.cuda(), None if c.latent else c.v.cuda(), c.batch(), c.scale, dv=c.dv, lse=lse, window=window,
                        doc_start=start.cuda().view(-1), prefix_end=end.cuda().view(-1))
     c.check(out, lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("heads", [(4, 2, 128), (8, 1, 40), (128, 1, 576)])
+def test_pages_that_no_row_sees_may_be_gone(dtype, heads):
+    # rows at far apart positions under a window: the pages between are not in the cache, and nothing says so
+    c = Case([400], 3, *heads, dv=min(heads[2], 512), dtype=dtype, page=16, n_new=[3], window=20, latent=heads[2] == 576,
+             seed=48)
+    c.pos = torch.tensor([[30, 200, 399]])
+    c.lo, c.hi = intervals(c.n_kv, c.pos, window=20)
+    for gone in (-1, 1 << 20):
+        used = {j // 16 for t in range(3) for j in range(int(c.lo[0, t]), int(c.hi[0, t]))}
+        for p in range(c.table.shape[1]):
+            if p not in used:
+                c.table[0, p] = gone
+        c.check(*c.run(), what=gone)
+        assert L.idx_device_status(reset=True) == 0
+    c.table[0, 199 // 16] = -1
+    c.run()
+    assert L.idx_device_status(reset=True) == L.IDX_ERR_DEVICE_BOUNDS
 
 
 @pytest.mark.gpu
