@@ -144,9 +144,15 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# the current stream of a device as an address, without the Stream object around it (2 us less a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device) -> int:
-    """The current stream of a tensor's device (as an address, without the Stream object around it: 2 us less a call)."""
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    """The current stream of a tensor's device."""
+    if _raw_stream is None:     # (not part of torch's public interface)
+        return torch.cuda.current_stream(device).cuda_stream
+    return _raw_stream(device.index)
 
 
 def _dtype(t: torch.Tensor) -> int:
