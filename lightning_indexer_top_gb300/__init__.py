@@ -634,7 +634,11 @@ def dense_attn(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tensor], batc
 
 def _space(workspace: Optional[torch.Tensor]):
     """(address, bytes) of a workspace."""
-    return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    if workspace is None:
+        return None, 0
+    if not workspace.is_contiguous():
+        raise ValueError("a workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _page_caches(caches, page_size: int, device):

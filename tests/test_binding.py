@@ -30,3 +30,17 @@ def test_both_ways_to_the_current_stream_agree(monkeypatch):
             with monkeypatch.context() as m:
                 m.setattr(L, "_raw_stream", None)
                 assert L._stream(dev) == here == stream.cuda_stream
+
+
+@pytest.mark.gpu
+def test_a_workspace_that_only_looks_large_is_refused():
+    thin = torch.empty(16, dtype=torch.uint8, device="cuda").expand(1 << 20, 16)     # 16 bytes
+    q, k = torch.zeros(1, 4, 64, device="cuda"), torch.zeros(16, 2, 64, device="cuda")
+    b = L.Batch(torch.tensor([16], dtype=torch.int32, device="cuda"), 1, 16)
+    x = torch.zeros(32, 4, device="cuda")
+    t, i = torch.zeros(1, 4, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    for f in (lambda: L.dense_attn(q, k, k, b, 1.0, workspace=thin),
+              lambda: L.idx_page_update(t, i, i, i, 4, [x], workspace=thin),
+              lambda: L.idx_page_compact(t, i, 4, [x], workspace=thin)):
+        with pytest.raises(ValueError, match="workspace"):
+            f()
