@@ -575,6 +575,9 @@ def dense_attn(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tensor], batc
     _all_on(dev, k, v, out, lse, workspace, batch.n_kv, batch.q_pos, batch.page_table, batch.kv_start)
     b = batch.c()
     rows = b.n_seq * b.n_q_per_seq
+    for t, n in ((batch.q_pos, rows), (batch.kv_start, b.n_seq), (batch.page_table, b.n_seq * b.page_table_stride)):
+        if t is not None and t.numel() < n:
+            raise ValueError("q_pos, kv_start or page_table has fewer entries than the batch")
     if q.dim() != 3 or q.shape[0] != rows or not q.is_contiguous():
         raise ValueError("q must be a contiguous [n_seq * n_q_per_seq, heads, dk] tensor")
     _, Hq, dk = q.shape

@@ -44,3 +44,14 @@ def test_a_workspace_that_only_looks_large_is_refused():
               lambda: L.idx_page_compact(t, i, 4, [x], workspace=thin)):
         with pytest.raises(ValueError, match="workspace"):
             f()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name,shape", [("q_pos", (5,)), ("kv_start", (2,)), ("page_table", (2, 4))])
+def test_batch_arrays_shorter_than_the_batch_are_refused(name, shape):
+    # three sequences of two rows
+    q, k = torch.zeros(6, 4, 64, device="cuda"), torch.zeros(64, 2, 64, device="cuda")
+    n_kv = torch.full((3,), 16, dtype=torch.int32, device="cuda")
+    b = L.Batch(n_kv, 2, 16, page_size=4, **{name: torch.zeros(shape, dtype=torch.int32, device="cuda")})
+    with pytest.raises(ValueError, match=name):
+        L.dense_attn(q, k, k, b, 1.0)
