@@ -606,8 +606,10 @@ def dense_attn(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tensor], batc
     if k.dtype is not q.dtype or (v is not None and v.dtype is not q.dtype):
         raise ValueError("q, k and v must have the same dtype")
     mods = None
-    if window > 2**31 - 1:
+    if not -2**31 <= window < 2**31:
         raise ValueError("window must be below 2**31")
+    if softcap and not ctypes.c_float(softcap).value:
+        raise ValueError("softcap is 0 in float32, which is no cap")
     if softcap or window or not (slopes is prefix_len is doc_start is prefix_end is None):
         _all_on(dev, slopes, prefix_len, doc_start, prefix_end)
         if slopes is not None and (slopes.dtype is not torch.float32 or not slopes.is_contiguous() or

@@ -55,3 +55,13 @@ def test_batch_arrays_shorter_than_the_batch_are_refused(name, shape):
     b = L.Batch(n_kv, 2, 16, page_size=4, **{name: torch.zeros(shape, dtype=torch.int32, device="cuda")})
     with pytest.raises(ValueError, match=name):
         L.dense_attn(q, k, k, b, 1.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kw", [dict(window=4 - 2**32), dict(window=-2**31 - 1), dict(softcap=1e-60), dict(softcap=-1e-60)])
+def test_options_that_change_on_their_way_to_32_bits_are_refused(kw):
+    q, k = torch.zeros(1, 4, 64, device="cuda"), torch.zeros(16, 2, 64, device="cuda")
+    b = L.Batch(torch.tensor([16], dtype=torch.int32, device="cuda"), 1, 16,
+                q_pos=torch.tensor([15], dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError, match=next(iter(kw))):
+        L.dense_attn(q, k, k, b, 1.0, **kw)
