@@ -46,3 +46,51 @@ def test_updates_beside_other_work():
             assert int(n_free) == left and table.tolist() == (want if want is not None else table.tolist())
     assert all(w is not None for _, _, w, _ in jobs)
     assert L.idx_device_status(reset=True) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n_pages", [6291456, 6500001])
+def test_pools_around_the_largest_bitmap_in_shared_memory(n_pages):
+    # a slice of the plans' bitmap is kept in shared memory up to 24576 words: 6291456 pages; beyond, in the workspace
+    ps, B, cols = 2, 30, 40
+    r = np.random.RandomState(5)
+    cache = torch.randint(0, 256, (n_pages * ps, 1), dtype=torch.uint8, device="cuda",
+                          generator=torch.Generator("cuda").manual_seed(6))
+    lens = r.randint(1, cols * ps + 1, B)
+    need = -(-lens // ps)
+    order = np.unique(np.concatenate([r.randint(0, n_pages, 3000), [0, 31, 32, n_pages - 1]]))
+    r.shuffle(order)
+    table = np.full((B, cols), -1, np.int64)
+    at = 0
+    for b in range(B):
+        table[b, :need[b]] = order[at:at + need[b]]
+        at += need[b]
+    held = [int(p) for p in order[at:at + 3]]
+    h = torch.zeros(n_pages, dtype=torch.uint8, device="cuda")
+    h[held] = 1
+    parent = r.randint(0, B, B)
+    keep = (lens[parent] * r.choice([0.5, 1.0], B)).astype(np.int64)
+    new = np.minimum(keep + 5, cols * ps)
+    want, left, copies = host_update(table.tolist(), parent, keep, new, ps, n_pages, held, cols)
+    rows = cache.clone()
+    out, n_free = L.idx_page_update(_i32(table), _i32(parent), _i32(keep), _i32(new), ps, [rows], held=h)
+    assert int(n_free) == left and out.tolist() == want
+    expect = cache.clone()
+    for a, b, n in copies:
+        expect[b * ps:b * ps + n] = cache[a * ps:a * ps + n]
+    assert copies and torch.equal(rows, expect)
+    rows.copy_(cache)
+    out, n_used, remap = L.idx_page_compact(_i32(table), _i32(lens), ps, [rows], held=h)
+    used = np.unique(np.concatenate([table[b, :need[b]] for b in range(B)] + [held]))
+    n = len(used)
+    moves = np.setdiff1d(used[used >= n], held)
+    holes = np.setdiff1d(np.arange(n), used)[:len(moves)]
+    to = np.arange(n_pages)
+    to[moves] = holes
+    assert int(n_used) == n and np.array_equal(remap.cpu().numpy(), to)
+    assert np.array_equal(out.cpu().numpy(), np.where(table >= 0, to[table], -1))
+    expect = cache.clone()
+    for a, b in zip(moves, holes):
+        expect[b * ps:(b + 1) * ps] = cache[a * ps:(a + 1) * ps]
+    assert torch.equal(rows, expect)
+    assert L.idx_device_status(reset=True) == 0
