@@ -116,10 +116,14 @@ __device__ __forceinline__ void abort_cta(Ctl& c, int* status) {
 // the whole warp sees the same answer
 __device__ __forceinline__ bool warp_aborted(Ctl& c) { return __any_sync(0xffffffffu, *(volatile int*)&c.abort != 0); }
 
-// one thread
-__device__ __forceinline__ void init(Ctl& c, uint32_t rank) {
-    auto all = [](uint64_t* bars, int n, int count) {
-        for (int i = 0; i < n; ++i) mbar_init(bars + i, count);
+// a unit's barriers, by one warp (a lane per barrier); again: they were another unit's
+__device__ __forceinline__ void init(Ctl& c, uint32_t rank, bool again) {
+    const int lane = threadIdx.x & 31;
+    auto all = [again, lane](uint64_t* bars, int n, int count) {
+        if (lane < n) {
+            if (again) mbar_inval(bars + lane);
+            mbar_init(bars + lane, count);
+        }
     };
     if (rank == 0) {
         all(c.kfull, kKRing, 1);
@@ -630,10 +634,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int n_clusters = gridDim.x >> 1;
     const DenseArgs& a = p.a;
     if (a.part_o) pdl_trigger();     // (the merge follows; results are not handed on early, see lidx_internal.cuh)
-    if (threadIdx.x == 0) {
-        init(c, rank);
-        tma_prefetch_desc(&map);
-    }
+    if (warp == 0) init(c, rank, false);
+    if (threadIdx.x == 0) tma_prefetch_desc(&map);
     if (warp == 1) {
         tmem_alloc(&c.tmem_base, kTmemCols);
         tmem_relinquish();
@@ -645,10 +647,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     pdl_wait();
     for (int64_t next = blockIdx.x >> 1; next < n_units; next += n_clusters) {
         const int unit = (int)next;
-        if (next != blockIdx.x >> 1) {
-            if (threadIdx.x == 0) init(c, rank);
-            __syncthreads();
-        }
         cluster_arrive();      // (this CTA's barriers are ready)
         Unit u;
         const int row = unit / a.splits;
@@ -690,6 +688,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         __syncthreads();
+        // (nothing of the other CTA's is on its way to this one's barriers: what it sent has been waited for)
+        if (warp == 0 && next + n_clusters < n_units) init(c, rank, true);
         cluster_sync();
         tc_fence_after();
     }
