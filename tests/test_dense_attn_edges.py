@@ -172,3 +172,36 @@ def test_a_prefix_by_row_needs_positions():
     b = L._Batch(1, 1, one, None, 8, None, 8, None, 0, 0)
     st = L.load().dense_attn(one, 1, 1, 1, 64, 64, one, one, 64, 64, 8, b, m, 1.0, one, None, None, 0, None)
     assert st == L.IDX_ERR_INVALID_ARG and "q_pos" in L.load().idx_last_error().decode()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,heads,T,page", [(torch.bfloat16, (4, 2, 128), 1, 64), (torch.float16, (8, 2, 64), 70, 32),
+                                                (torch.bfloat16, (128, 1, 576), 2, 64), (torch.float32, (4, 2, 128), 3, 16),
+                                                (torch.bfloat16, (4, 2, 40), 3, 0)])
+def test_rows_beyond_32_bit_offsets(dtype, heads, T, page):
+    # a cache of more than 2^31 elements, the sequences' rows at its two ends
+    Hq, Hkv, d = heads
+    rows = ((1 << 31) // (Hkv * d) + 4096) // 64 * 64
+    c = Case([200, 150], T, Hq, Hkv, d, dv=min(d, 512), dtype=dtype, page=page, latent=d == 576, seed=49)
+    b = c.batch()
+    if page:
+        far = c.table.long() + torch.where(c.table >= c.table.numel() // 2, rows // page - c.table.numel(), 0)
+        b.page_table = far.to(torch.int32).cuda()
+        at = (far[:, torch.arange(c.N) // page] * page + torch.arange(c.N) % page)
+    else:
+        b.kv_start = torch.tensor([0, rows - 150], dtype=torch.int32, device="cuda")
+        at = torch.arange(c.N) + b.kv_start.cpu().long()[:, None]
+
+    def spread(x):
+        big = torch.empty((rows, *x.shape[1:]), dtype=dtype, device="cuda")
+        for i, n in enumerate(c.n_kv):
+            big[at[i, :n].cuda()] = x[c.rows[i]].cuda()
+        return big
+    k = spread(c.k)
+    assert k.numel() > 1 << 31 and max(int(at[i, :n].max()) for i, n in enumerate(c.n_kv)) > rows - 4096
+    v = None if c.latent else spread(c.v)
+    q = c.q.reshape(c.B * T, Hq, d).cuda()
+    lse = torch.empty(q.shape[:2], device="cuda")
+    out = L.dense_attn(q, k, v, b, c.scale, dv=c.dv, lse=lse)
+    c.check(out, lse)
+    assert L.idx_device_status(reset=True) == 0

@@ -94,3 +94,26 @@ def test_pools_around_the_largest_bitmap_in_shared_memory(n_pages):
         expect[b * ps:(b + 1) * ps] = cache[a * ps:(a + 1) * ps]
     assert torch.equal(rows, expect)
     assert L.idx_device_status(reset=True) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("wide", [0, 8])
+def test_pages_beyond_32_bit_offsets(wide):
+    # pages at both ends of a cache of more than 2^32 bytes; wide: rows with bytes between them that stay as they are
+    ps, row = 64, 1152
+    n_pages = (1 << 32) // (ps * row) + 200
+    cache = torch.empty(n_pages * ps, row + wide, dtype=torch.uint8, device="cuda")
+    for p in range(8):
+        cache[p * ps:(p + 1) * ps] = p
+        cache[(n_pages - 1 - p) * ps:(n_pages - p) * ps] = 100 + p
+    view = cache[:, :row]
+    L.idx_page_copy([view], ps, _i32([0, n_pages - 1]), _i32([n_pages - 3, 2]))
+    for p, want in ((n_pages - 3, 0), (2, 100), (n_pages - 2, 101), (n_pages - 4, 103), (1, 1), (3, 3)):
+        assert (view[p * ps:(p + 1) * ps] == want).all()
+    if wide:
+        assert (cache[2 * ps:3 * ps, row:] == 2).all() and (cache[(n_pages - 3) * ps:(n_pages - 2) * ps, row:] == 102).all()
+    # the used pages at the far end come down
+    table = _i32([[n_pages - 1, n_pages - 2], [n_pages - 1, -1]])
+    new, n_used, _ = L.idx_page_compact(table, _i32([2 * ps, ps]), ps, [view])
+    assert new.tolist() == [[1, 0], [1, -1]] and int(n_used) == 2
+    assert (view[:ps] == 101).all() and (view[ps:2 * ps] == 100).all()
