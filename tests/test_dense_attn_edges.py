@@ -205,3 +205,14 @@ def test_rows_beyond_32_bit_offsets(dtype, heads, T, page):
     out = L.dense_attn(q, k, v, b, c.scale, dv=c.dv, lse=lse)
     c.check(out, lse)
     assert L.idx_device_status(reset=True) == 0
+
+
+@pytest.mark.gpu
+def test_long_latent_in_a_workspace_of_too_few_splits():
+    # a unit of the tensor-core kernel takes 8192 keys: 20000 of them need three splits, and with room for fewer the call
+    # runs on the CUDA cores, in as many splits as the room holds
+    c = Case([20000, 900], 1, 128, 1, 576, dv=512, dtype=torch.bfloat16, page=64, latent=True, seed=50)
+    split = 2 * 128 * (512 + 2) * 4
+    for n in (3, 2, 1):
+        c.check(*c.run(workspace=torch.empty(n * split, dtype=torch.uint8, device="cuda")), what=n)
+    assert L.idx_device_status(reset=True) == 0
