@@ -11,14 +11,6 @@ constexpr int kDenseMaxSplits = 128;   // key splits, at most (the merge keeps t
 
 constexpr int kDenseCluster = 8;       // splits that a cluster merges itself, at most
 
-// the same shared-memory variable of the cluster's CTA `rank`, as a generic address
-template <typename T>
-__device__ __forceinline__ T* of_cta(T* p, uint32_t rank) {
-    uint64_t r;
-    asm("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
-    return reinterpret_cast<T*>(r);
-}
-
 struct DenseArgs {
     const void* q;
     int32_t Hq, Hkv, dk, dv;
@@ -62,6 +54,13 @@ __device__ __forceinline__ Interval row_interval(const Geom& g, const idx_attn_m
     }
     if (m.doc_start) v.lo = max(v.lo, m.doc_start[r]);
     return v;
+}
+
+// rows per TMA box of a tile of `keys` positions: all of them, or the largest power of two that divides the page
+inline int box_rows(int page_size, int keys) {
+    if (!page_size) return keys;
+    const int b = page_size & -page_size;
+    return b < keys ? b : keys;
 }
 
 constexpr float kLog2e = 1.4426950408889634f;

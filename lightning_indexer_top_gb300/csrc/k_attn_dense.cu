@@ -198,59 +198,59 @@ __global__ void __launch_bounds__(kThreads, DV == 64 ? 3 : DV == 512 || (R == 64
             lost = send(t0 + kKeys, buf ^ 1);
             buf ^= 1;
         } else {
-        __syncthreads();      // the last tile is done with
-        if (tid < kKeys) rows_s[tid] = row_of(t0 + tid);
-        bad = __syncthreads_or(tid < kKeys && rows_s[tid < kKeys ? tid : 0] < 0);
-        // K and V rows, widened
-        if (vec) {
-            constexpr int E = 16 / (int)sizeof(T);
-            const int wk = a.dk / E, wv = latent ? 0 : a.dv / E;
-            const int total = kKeys * (wk + wv);
-            constexpr int kBatch = 4;
-            for (int e0 = tid; e0 < total; e0 += kThreads * kBatch) {
-                uint4 x[kBatch];
+            __syncthreads();      // the last tile is done with
+            if (tid < kKeys) rows_s[tid] = row_of(t0 + tid);
+            bad = __syncthreads_or(tid < kKeys && rows_s[tid < kKeys ? tid : 0] < 0);
+            // K and V rows, widened
+            if (vec) {
+                constexpr int E = 16 / (int)sizeof(T);
+                const int wk = a.dk / E, wv = latent ? 0 : a.dv / E;
+                const int total = kKeys * (wk + wv);
+                constexpr int kBatch = 4;
+                for (int e0 = tid; e0 < total; e0 += kThreads * kBatch) {
+                    uint4 x[kBatch];
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const int e = e0 + i * kThreads;
-                    x[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (e < total) {
-                        const bool isk = e < kKeys * wk;
-                        const int ee = isk ? e : e - kKeys * wk, w = isk ? wk : wv;
-                        const int64_t row = rows_s[ee / w];
-                        if (row >= 0)
-                            x[i] = *reinterpret_cast<const uint4*>(
-                                isk ? static_cast<const T*>(a.k) + row * a.k_stride + (int64_t)gkv * a.dk + ee % w * E
-                                    : static_cast<const T*>(a.v) + row * a.v_stride + (int64_t)gkv * a.dv + ee % w * E);
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int e = e0 + i * kThreads;
+                        x[i] = make_uint4(0u, 0u, 0u, 0u);
+                        if (e < total) {
+                            const bool isk = e < kKeys * wk;
+                            const int ee = isk ? e : e - kKeys * wk, w = isk ? wk : wv;
+                            const int64_t row = rows_s[ee / w];
+                            if (row >= 0)
+                                x[i] = *reinterpret_cast<const uint4*>(
+                                    isk ? static_cast<const T*>(a.k) + row * a.k_stride + (int64_t)gkv * a.dk + ee % w * E
+                                        : static_cast<const T*>(a.v) + row * a.v_stride + (int64_t)gkv * a.dv + ee % w * E);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int e = e0 + i * kThreads;
+                        if (e < total) {
+                            const bool isk = e < kKeys * wk;
+                            const int ee = isk ? e : e - kKeys * wk, w = isk ? wk : wv;
+                            float* d = isk ? ks + ee / w * kp + ee % w * E : vs + ee / w * vp + ee % w * E;
+                            const T* p = reinterpret_cast<const T*>(&x[i]);
+#pragma unroll
+                            for (int j = 0; j < E; ++j) d[j] = to_f32(p[j]);
+                        }
                     }
                 }
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const int e = e0 + i * kThreads;
-                    if (e < total) {
-                        const bool isk = e < kKeys * wk;
-                        const int ee = isk ? e : e - kKeys * wk, w = isk ? wk : wv;
-                        float* d = isk ? ks + ee / w * kp + ee % w * E : vs + ee / w * vp + ee % w * E;
-                        const T* p = reinterpret_cast<const T*>(&x[i]);
-#pragma unroll
-                        for (int j = 0; j < E; ++j) d[j] = to_f32(p[j]);
+            } else {
+                for (int e = tid; e < kKeys * a.dk; e += kThreads) {
+                    const int64_t row = rows_s[e / a.dk];
+                    ks[e / a.dk * kp + e % a.dk] =
+                        row >= 0 ? to_f32(static_cast<const T*>(a.k)[row * a.k_stride + (int64_t)gkv * a.dk + e % a.dk]) : 0.f;
+                }
+                if (!latent)
+                    for (int e = tid; e < kKeys * a.dv; e += kThreads) {
+                        const int64_t row = rows_s[e / a.dv];
+                        vs[e / a.dv * vp + e % a.dv] =
+                            row >= 0 ? to_f32(static_cast<const T*>(a.v)[row * a.v_stride + (int64_t)gkv * a.dv + e % a.dv])
+                                     : 0.f;
                     }
-                }
             }
-        } else {
-            for (int e = tid; e < kKeys * a.dk; e += kThreads) {
-                const int64_t row = rows_s[e / a.dk];
-                ks[e / a.dk * kp + e % a.dk] =
-                    row >= 0 ? to_f32(static_cast<const T*>(a.k)[row * a.k_stride + (int64_t)gkv * a.dk + e % a.dk]) : 0.f;
-            }
-            if (!latent)
-                for (int e = tid; e < kKeys * a.dv; e += kThreads) {
-                    const int64_t row = rows_s[e / a.dv];
-                    vs[e / a.dv * vp + e % a.dv] =
-                        row >= 0 ? to_f32(static_cast<const T*>(a.v)[row * a.v_stride + (int64_t)gkv * a.dv + e % a.dv])
-                                 : 0.f;
-                }
-        }
-        __syncthreads();
+            __syncthreads();
         }
         // ---- scores
         const bool whole = !bad && t0 >= full0 && t0 + kKeys <= min(full1, k1);
@@ -443,9 +443,9 @@ __global__ void __launch_bounds__(kThreads, DV == 64 ? 3 : DV == 512 || (R == 64
 #pragma unroll
             for (int s = 0; s < kDenseCluster; ++s) {
                 const int from = s < a.splits ? s : 0;
-                mx[s] = *of_cta(m_s + rr, from);
-                lx[s] = s < a.splits ? *of_cta(l_s + rr, from) : 0.f;
-                ox[s] = *of_cta(o_s + e, from);
+                mx[s] = *sm100::of_cta(m_s + rr, from);
+                lx[s] = s < a.splits ? *sm100::of_cta(l_s + rr, from) : 0.f;
+                ox[s] = *sm100::of_cta(o_s + e, from);
             }
             float M = -INFINITY, den = 0.f, acc = 0.f;
 #pragma unroll

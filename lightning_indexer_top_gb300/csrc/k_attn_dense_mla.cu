@@ -754,12 +754,6 @@ __global__ void __launch_bounds__(kHq) dense_mla_combine_kernel(DenseArgs a) {
     *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (r * kHq + h) * (int64_t)kDv + blockIdx.y * kCols) = w;
 }
 
-int box_rows(int page_size) {
-    if (!page_size) return kKeys;
-    const int b = page_size & -page_size;
-    return b < kKeys ? b : kKeys;
-}
-
 // clusters that can be resident at once (0: unknown)
 int64_t resident_clusters() {
     static int cache[64] = {};
@@ -784,7 +778,7 @@ int64_t resident_clusters() {
 
 bool dense_mla_supported(const DenseArgs& a, int dtype, const Geom& g) {
     return mla_tc_supported(dtype, a.Hq, a.Hkv, a.dk, a.dv, a.k, a.v, a.k_stride, a.kv_rows, a.q, a.out) &&
-           a.kv_rows <= INT32_MAX - kKeys && (!g.page_table || box_rows(g.page_size) >= 8);
+           a.kv_rows <= INT32_MAX - kKeys && (!g.page_table || box_rows(g.page_size, kKeys) >= 8);
 }
 
 // key splits per query row: the fewest rounds of the clusters x tiles of a unit, which has about 10 tiles' time of
@@ -809,7 +803,7 @@ size_t dense_mla_workspace_bytes(int64_t n_rows, int64_t max_n_kv) {
 
 cudaError_t launch_dense_mla(const DenseArgs& args, const Geom& g, void* ws, size_t ws_bytes, cudaStream_t st) {
     const int64_t n_rows = (int64_t)g.B * g.T;
-    DenseParams p = {args, box_rows(g.page_size)};
+    DenseParams p = {args, box_rows(g.page_size, kKeys)};
     DenseArgs& a = p.a;
     int64_t splits = dense_mla_splits(n_rows, g.max_n_kv);
     const int64_t per_split = n_rows * kHq * (kDv + 2) * (int64_t)sizeof(float);

@@ -758,12 +758,6 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
     if (warp == 0) tmem_dealloc(tmem, C::kTmemCols);
 }
 
-int box_rows(int page_size) {
-    if (!page_size) return kKeys;
-    int b = page_size & -page_size;
-    return b < kKeys ? b : kKeys;
-}
-
 // row tiles per CTA
 int row_tiles(int64_t packed) { return packed > kFewRows ? 2 : 1; }
 
@@ -784,7 +778,7 @@ template <typename T>
 cudaError_t run(const DenseArgs& a, const Geom& g, cudaStream_t st) {
     const int64_t packed = (int64_t)g.T * (a.Hq / a.Hkv);
     const int tiles = row_tiles(packed);
-    TcArgs p = {a, (int)((packed + tiles * kRows - 1) / (tiles * kRows)), box_rows(g.page_size)};
+    TcArgs p = {a, (int)((packed + tiles * kRows - 1) / (tiles * kRows)), box_rows(g.page_size, kKeys)};
     const int64_t grid = (int64_t)g.B * a.Hkv * p.tiles * a.splits;
     if (grid > INT32_MAX) return cudaErrorNotSupported;
     CUtensorMap km, vm;
@@ -810,7 +804,7 @@ bool dense_tc_supported(const DenseArgs& a, int dtype, const Geom& g) {
     if (dtype == IDX_F32 || !a.v || a.dk > 128 || a.dv > 128 || a.dk % 8 || a.dv % 8) return false;
     if (a.kv_rows < 1 || a.kv_rows > INT32_MAX - kKeys || a.k_stride % 8 || a.v_stride % 8) return false;
     // pages are loaded in boxes of whole 8-row swizzle groups
-    if (g.page_table && box_rows(g.page_size) < 8) return false;
+    if (g.page_table && box_rows(g.page_size, kKeys) < 8) return false;
     const uint64_t all = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) |
                          reinterpret_cast<uintptr_t>(a.v) | reinterpret_cast<uintptr_t>(a.out);
     return all % 16 == 0;

@@ -113,14 +113,6 @@ struct Plan {
 
 __device__ __forceinline__ uint32_t cta_rank() { return sm100::cluster_ctarank(); }
 
-// the same variable of CTA `rank`, as a generic address
-template <typename T>
-__device__ __forceinline__ T* of_cta(T* p, uint32_t rank) {
-    uint64_t r;
-    asm volatile("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
-    return reinterpret_cast<T*>(r);
-}
-
 // the exclusive prefix sum of x over the CTA's threads; *total gets the sum
 __device__ __forceinline__ int block_scan(Plan& s, int x, int* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -145,7 +137,7 @@ __device__ __forceinline__ int block_scan(Plan& s, int x, int* total) {
 
 // tells every CTA x of this one in cnt[k]; after the next cluster barrier, the sum before this CTA and in all
 __device__ __forceinline__ void tell(Plan& s, int k, int x) {
-    if (threadIdx.x < kCl) of_cta(&s.cnt[k][0], threadIdx.x)[cta_rank()] = x;
+    if (threadIdx.x < kCl) sm100::of_cta(&s.cnt[k][0], threadIdx.x)[cta_rank()] = x;
 }
 __device__ __forceinline__ int told(const Plan& s, int k, int* total) {
     int before = 0, all = 0;
@@ -165,7 +157,7 @@ struct Bitmap {
     int words;
 
     __device__ __forceinline__ uint32_t* word(int w) const {
-        return global ? global + w : of_cta(mine, (uint32_t)(w / slice)) + w % slice;
+        return global ? global + w : sm100::of_cta(mine, (uint32_t)(w / slice)) + w % slice;
     }
     __device__ __forceinline__ void set(int32_t p) const { atomicOr(word(p >> 5), 1u << (p & 31)); }
     __device__ __forceinline__ bool get(int32_t p) const {
@@ -188,14 +180,11 @@ __device__ __forceinline__ Bitmap make_bitmap(uint32_t* ws, uint32_t* smem, int3
     return m;
 }
 
-// bits of word w that are pages (the last word may be short)
-__device__ __forceinline__ uint32_t page_bits(int64_t w, int32_t n_pages) {
-    const int64_t left = (int64_t)n_pages - w * 32;
+// bits of word w that are numbers below n
+__device__ __forceinline__ uint32_t page_bits(int64_t w, int32_t n) {
+    const int64_t left = (int64_t)n - w * 32;
     return left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
 }
-
-// bits of word w that are below n
-__device__ __forceinline__ uint32_t low_bits(int64_t w, int32_t n) { return page_bits(w, n); }
 
 __device__ __forceinline__ uint32_t held_bits(const uint8_t* held, int64_t w, int32_t n_pages) {
     if (!held) return 0u;
@@ -436,12 +425,12 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kPlanThreads) page
     told(s, 0, &n_used);
     // the moving pages (used, not held, numbered n_used or higher) and the free numbers below, in order
     uint32_t* moving = bm.global ? a.moving + w_base : slice_s + bm.slice;
-    auto holes = [&](int w) { return ~bm.mine[w] & low_bits(w_base + w, n_used); };
+    auto holes = [&](int w) { return ~bm.mine[w] & page_bits(w_base + w, n_used); };
     int y = 0;
     x = 0;
     for (int w = tid; w < bm.n_mine(); w += kPlanThreads) {     // (each word by the same thread from here on)
         const int64_t gw = w_base + w;
-        moving[w] = bm.mine[w] & ~held_bits(a.held, gw, a.n_pages) & ~low_bits(gw, n_used);
+        moving[w] = bm.mine[w] & ~held_bits(a.held, gw, a.n_pages) & ~page_bits(gw, n_used);
         x += __popc(moving[w]);
         y += __popc(holes(w));
     }

@@ -419,6 +419,14 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
+// the same shared-memory variable of the cluster's CTA `rank`, as a generic address
+template <typename T>
+__device__ __forceinline__ T* of_cta(T* p, uint32_t rank) {
+    uint64_t r;
+    asm("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
+    return reinterpret_cast<T*>(r);
+}
+
 // shared::cluster address of the same variable in CTA `rank` of this cluster
 __device__ __forceinline__ uint32_t mapa(const void* p, uint32_t rank) {
     uint32_t r;
