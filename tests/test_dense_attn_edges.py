@@ -216,3 +216,32 @@ def test_long_latent_in_a_workspace_of_too_few_splits():
     for n in (3, 2, 1):
         c.check(*c.run(workspace=torch.empty(n * split, dtype=torch.uint8, device="cuda")), what=n)
     assert L.idx_device_status(reset=True) == 0
+
+
+@pytest.mark.gpu
+def test_calls_on_several_streams_at_once():
+    # every kernel and way of merging, each on a stream of its own with its own workspace, against the calls one by one
+    cases = [Case([900, 300], 1, 32, 4, 128, page=64, seed=51), Case([700, 500], 200, 8, 2, 128, seed=52),
+             Case([300] * 8, 60, 6, 2, 64, dtype=torch.float16, slopes=True, seed=53), Case([30000], 1, 8, 2, 64, page=16, seed=54),
+             Case([4000, 900], 2, 128, 1, 576, dv=512, page=64, latent=True, seed=55),
+             Case([2000, 100], 1, 8, 2, 128, dtype=torch.float32, seed=56),
+             Case([400], 50, 4, 1, 64, dtype=torch.float32, seed=57)]
+    jobs = []
+    for c in cases:
+        q = c.q.reshape(c.B * c.T, *c.q.shape[2:]).cuda()
+        need = L.dense_attn_workspace_size(q.dtype, c.B, c.T, c.N, q.shape[1], c.k.shape[1], q.shape[2], c.dv)
+        kw = dict(dv=c.dv, workspace=torch.empty(max(need, 16), dtype=torch.uint8, device="cuda"), **c.mods())
+        jobs.append((q, c.k.cuda(), None if c.latent else c.v.cuda(), c.batch(), c.scale, kw))
+    want = [L.dense_attn(*j[:5], **j[5]) for j in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    got = [[] for _ in jobs]
+    for _ in range(25):
+        for i, j in enumerate(jobs):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(L.dense_attn(*j[:5], **j[5]))
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        for x in g:
+            assert torch.equal(x, w)
+    assert L.idx_device_status(reset=True) == 0
