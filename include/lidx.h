@@ -470,7 +470,9 @@ int32_t sparse_decode_step_fused(int64_t n_rows, int32_t n_q_per_seq, int32_t ma
  * that sees no key, or whose every score is -inf, gets zeros and lse = -inf.
  * Keys outside a row's interval never reach its result, whatever bytes they hold
  * (rows of a page past the sequence's end, other documents, later tokens): NaN
- * and infinities there included.
+ * and infinities there included.  (The tensor-core kernel works rows off key by key
+ * where a value row that only some of their tile's rows see holds one, or a page
+ * between them is out of range: right, and some hundred times slower.)
  *   q, k, v, dtype, strides, kv_rows   as sparse_attn_decode (v NULL: the MLA
  *              latent form), K and V rows addressed by batch.
  *   mods       HOST pointer to the options below, or NULL for none of them.

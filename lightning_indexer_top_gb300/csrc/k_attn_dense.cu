@@ -13,10 +13,10 @@
 //           output rescaled by the rows' factors each tile.
 // A warp has the same R/4 rows in all three, so that only the tiles' arrival is a barrier of the CTA.
 // Sums, products, maxima and weights are f32 throughout; products run as packed pairs of FMAs.
-// Measured in f32: 512 tokens on 4096 cached keys, two sequences of 32 heads of 128 on 4, 2.43 ms = 26.6 TFLOP/s,
-// bound by the instructions beside the FMAs (shared-memory reads, the softmax) with two CTAs of four warps to an SM,
-// which is what 181 registers and 110 KB leave room for; one token on 16384 keys, eight sequences of 32 heads on 8,
-// 0.61 ms = 1.8 TB/s, bound by the latency of a tile's loads and its softmax.
+// Measured in f32: 512 tokens on 4096 cached keys, two sequences of 32 heads of 128 on 4, 2.39 ms = 27.0 TFLOP/s.  The
+// FMA pipe is active on 41 % of the cycles and a scheduler issues on 35 %: its two warps (two CTAs of four to an SM, all
+// that 252 registers and 110 KB leave room for) wait for results and for shared memory.  One token on 16384 keys, eight
+// sequences of 32 heads on 8: 0.59 ms = 1.8 TB/s, bound by the latency of a tile's loads and its softmax.
 // Loading a tile ahead of the arithmetic (f32, aligned): heads of 64, 256 tokens on 2048 keys 260 -> 194 us.
 // A key that only some rows of a tile see is skipped, not multiplied by zero,
 // for the others, so that NaN or infinity in it cannot reach them.

@@ -70,7 +70,7 @@ struct Cfg {
     static constexpr int kQBlock = kQRows * 128;      // 64 columns of it
     static constexpr int kStagesK = kTiles == 2 ? 2 : D == 64 ? 2 : 1;
     static constexpr int kStagesV = kTiles == 2 ? 3 : D == 64 ? 3 : 2;
-    static constexpr int kCtas = kTiles == 2 ? 1 : 2;
+    static constexpr int kCtas = kTiles == 2 ? 1 : 2;   // (two: 128 registers; with options 28 to 40 bytes are spilled)
     static constexpr int kKOff = kTiles * kQTile;
     static constexpr int kVOff = kKOff + kStagesK * kTileBytes;
     static constexpr int kCtlOff = kVOff + kStagesV * kTileBytes;
@@ -810,7 +810,8 @@ bool dense_tc_supported(const DenseArgs& a, int dtype, const Geom& g) {
     return all % 16 == 0;
 }
 
-// one CTA per SM: split the keys until the CTAs cover the SMs twice, at least 512 keys each
+// as many splits as keep the CTAs within twice the SMs (one round for calls of few rows, with two CTAs to an SM), and no
+// more than there are pieces of 512 keys; 513 keys are two pieces
 int dense_tc_splits(int64_t n_seq, int64_t n_q, int64_t max_n_kv, int Hq, int Hkv) {
     const int64_t packed = n_q * (Hq / Hkv);
     const int64_t rows = row_tiles(packed) * kRows;
