@@ -575,9 +575,10 @@ def dense_attn(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tensor], batc
     _all_on(dev, k, v, out, lse, workspace, batch.n_kv, batch.q_pos, batch.page_table, batch.kv_start)
     b = batch.c()
     rows = b.n_seq * b.n_q_per_seq
-    for t, n in ((batch.q_pos, rows), (batch.kv_start, b.n_seq), (batch.page_table, b.n_seq * b.page_table_stride)):
-        if t is not None and t.numel() < n:
-            raise ValueError("q_pos, kv_start or page_table has fewer entries than the batch")
+    # (kv_start is not read beside a page table)
+    where, n = (batch.kv_start, b.n_seq) if batch.page_table is None else (batch.page_table, b.n_seq * b.page_table_stride)
+    if batch.q_pos is not None and batch.q_pos.numel() < rows or where is not None and where.numel() < n:
+        raise ValueError("q_pos, kv_start or page_table has fewer entries than the batch")
     if q.dim() != 3 or q.shape[0] != rows or not q.is_contiguous():
         raise ValueError("q must be a contiguous [n_seq * n_q_per_seq, heads, dk] tensor")
     _, Hq, dk = q.shape

@@ -55,6 +55,9 @@ def test_batch_arrays_shorter_than_the_batch_are_refused(name, shape):
     b = L.Batch(n_kv, 2, 16, page_size=4, **{name: torch.zeros(shape, dtype=torch.int32, device="cuda")})
     with pytest.raises(ValueError, match=name):
         L.dense_attn(q, k, k, b, 1.0)
+    if name == "kv_start":      # not read beside a page table
+        b.page_table = torch.arange(12, dtype=torch.int32, device="cuda").view(3, 4)
+        assert (L.dense_attn(q, k, k, b, 1.0) == 0).all()
 
 
 @pytest.mark.gpu
