@@ -612,6 +612,185 @@ idx_status idx_page_compact(const int32_t* page_table, int64_t table_stride, int
 /* Bytes of device workspace of idx_page_update and idx_page_compact; host arithmetic, 0 for nonsense sizes. */
 size_t idx_page_workspace_size(int32_t n_seq, int32_t n_pages);
 
+/*
+ * Writing the rows of new tokens into caches.
+ *
+ * idx_new_rows: what a layer's projections give for the batch's rows, described on
+ * the HOST; row r = b*T + t at base + r*stride (elements; heads one behind the other
+ * within the row, so slices of one wider projection output serve).
+ *   k, v       [B*T] rows of n_kv_heads*dk and n_kv_heads*dv elements.  v NULL with dv
+ *              0: rows of one cache only (the MLA latent, indexer keys).
+ *   q, q_out   [B*T] rows of n_q_heads*dk elements, rotated like k; NULL with n_q_heads
+ *              0: no queries.  q_out may be q itself with the same stride; other
+ *              overlap is not allowed, of any tensor written with any other.
+ */
+typedef struct idx_new_rows {
+    const void* k;
+    int64_t k_stride;
+    const void* v;
+    int64_t v_stride;
+    const void* q;
+    int64_t q_stride;
+    void* q_out;
+    int64_t q_out_stride;
+} idx_new_rows;
+
+/*
+ * idx_rope: the rotation of a head's columns start .. start + n_rot - 1 by the row's
+ * position p, on the HOST.  Pair i < n_rot/2 is the columns (start + i, start + n_rot/2 + i),
+ * or with `interleaved` (start + 2i, start + 2i + 1); (u, w) becomes
+ *     (u cos - w sin, w cos + u sin)   of the angle p * inv_freq[i].
+ *   inv_freq   device f32 [n_rot/2], radians per position (scaled variants of the
+ *              rotation are other numbers here), finite.
+ * The angle is reduced in turns, as a 64-bit fraction times the position, so far
+ * positions are as exact as near ones: its error is below 2^-52 of p * inv_freq, and f32's.
+ */
+typedef struct idx_rope {
+    const float* inv_freq;
+    int32_t n_rot;
+    int32_t start;
+    int32_t interleaved;
+} idx_rope;
+
+/*
+ * idx_cache_append -- the rotation and the cache write of a batch's new tokens in one
+ * launch ("decode-correct via persistent indexer-K cache", ik_llama.cpp PR #2058: a row
+ * is written, rotated, before it is scored): row r at position p goes to cache row p of
+ * its sequence (see idx_batch), K rotated, V as it is; q_out[r] = q[r] rotated.
+ *   position   p = batch.q_pos[r]; without q_pos the T rows are the last ones,
+ *              p = n_kv[b] - T + t.  A row with p < 0 (padding) writes no cache row, and
+ *              its q_out is q as it is.  A row with p >= n_kv[b] (n_kv counts the new
+ *              tokens), or whose cache row is outside [0, kv_rows), writes no cache row
+ *              and is flagged (IDX_ERR_DEVICE_BOUNDS).  The rows of a call must go to
+ *              different cache rows (of two that do not, either may stay, or a mix).
+ *   rope       NULL or n_rot 0: no rotation.
+ *   k_cache, v_cache  [kv_rows] rows of n_kv_heads*dk and n_kv_heads*dv elements of
+ *              dtype, strides in elements.  Everything but the rows named stays as it is.
+ * The rotation runs in f32 and is rounded once to dtype.
+ * Errors: n_kv_heads < 1, n_q_heads < 0, dk outside [1, 576], dv outside [0, 512], a
+ * stride below its row, n_rot odd, negative or beyond the head, NULL where a tensor is
+ * needed, v and v_cache not both given or both NULL: INVALID_ARG.
+ */
+idx_status idx_cache_append(const idx_new_rows* rows, idx_dtype dtype, int32_t n_q_heads, int32_t n_kv_heads,
+                            int32_t dk, int32_t dv, idx_batch batch, const idx_rope* rope, void* k_cache,
+                            int64_t k_row_stride, void* v_cache, int64_t v_row_stride, int64_t kv_rows,
+                            idx_stream_t stream);
+
+/*
+ * 4-bit caches.  A cache row of n heads of d columns (d a multiple of 8):
+ *   - for each head d/2 bytes of codes, column c in byte c/2, the even one in the low half;
+ *   - then for each head two f32, scale and minimum (native byte order);
+ *   - then padding to the row stride.
+ * Code n stands for scale*n + minimum.  idx_q4_row_bytes: n*(d/2 + 8) rounded up to 16
+ * (0 for nonsense sizes); base and row stride are multiples of 4 bytes (of 16 for the
+ * fast kernels).  A 4-bit cache is rows of bytes to the page operations.
+ *
+ * idx_cache_append_q4 -- idx_cache_append into 4-bit caches.  Of a head row x (K after
+ * the rotation):
+ *     minimum = min x, scale = (max x - min x) / 15, code = rint(15 (x - min) / (max - min))
+ * (half to even; codes 0 where all are equal).  The codes are those of the unrounded
+ * rotation: where f32 cannot tell two codes apart, 64 bits decide.  scale and minimum are
+ * rounded to f32.  A head row that holds a NaN or infinity gets NaN for both: it stands for
+ * NaN.  (A row quantised by itself has no use for a common scale: rows whose outliers
+ * cost too much are best rotated first, as idx_hadamard does for both sides of a product.)
+ *   k_cache, v_cache  rows of bytes, strides in BYTES; v_cache NULL with v NULL.
+ * dk and dv must be multiples of 8; other arguments and errors as idx_cache_append.
+ */
+size_t idx_q4_row_bytes(int32_t n_heads, int32_t d);
+
+idx_status idx_cache_append_q4(const idx_new_rows* rows, idx_dtype dtype, int32_t n_q_heads, int32_t n_kv_heads,
+                               int32_t dk, int32_t dv, idx_batch batch, const idx_rope* rope, void* k_cache,
+                               int64_t k_row_stride, void* v_cache, int64_t v_row_stride, int64_t kv_rows,
+                               idx_stream_t stream);
+
+/*
+ * idx_cache_read_q4 -- the values that rows of 4-bit caches stand for: row r of k_out
+ * [B*T, n_kv_heads, dk] and v_out [B*T, n_kv_heads, dv] (contiguous, of dtype) becomes
+ * position p of the row's sequence, positions as idx_cache_append takes them.  Padding
+ * rows, and rows that are out of range (flagged), stay as they were.
+ *   v_cache, v_out  both NULL with dv 0: one cache.
+ */
+idx_status idx_cache_read_q4(const void* k_cache, int64_t k_row_stride, const void* v_cache, int64_t v_row_stride,
+                             int64_t kv_rows, int32_t n_kv_heads, int32_t dk, int32_t dv, idx_batch batch,
+                             idx_dtype dtype, void* k_out, void* v_out, idx_stream_t stream);
+
+/*
+ * dense_attn_q4 -- dense_attn over 4-bit caches of K and V: its formula, options, masks,
+ * results and errors, K and V being the values that the codes stand for.
+ *   k_cache, v_cache  rows of bytes, strides in BYTES (see above); dk and dv multiples of
+ *              8.  There is no latent form.
+ *   workspace  dense_attn_q4_workspace_size(...) bytes, 16-byte aligned.  With less (or
+ *              NULL) the call takes another way, with the same results up to rounding:
+ *              fewer key splits, or codes that each tile of rows expands for itself
+ *              instead of once for all.
+ * 16-bit q and heads of 64 or 128 columns (dk == dv), given 16-byte aligned tensors and
+ * rows, run on the tensor cores: few rows on the codes themselves, many rows on K and V
+ * expanded to dtype in the workspace.  The weights (few rows: times the values' scale, in
+ * bf16; many rows: in dtype) are then rounded for the second product.
+ */
+idx_status dense_attn_q4(const void* q, idx_dtype dtype, int32_t n_q_heads, int32_t n_kv_heads, int32_t dk, int32_t dv,
+                         const void* k_cache, int64_t k_row_stride, const void* v_cache, int64_t v_row_stride,
+                         int64_t kv_rows, idx_batch batch, const idx_attn_mods* mods, float scale, void* out,
+                         float* lse, void* workspace, size_t workspace_bytes, idx_stream_t stream);
+
+size_t dense_attn_q4_workspace_size(idx_dtype dtype, int32_t n_seq, int32_t n_q_per_seq, int32_t max_n_kv,
+                                    int32_t n_q_heads, int32_t n_kv_heads, int32_t dk, int32_t dv);
+
+/*
+ * idx_beam_step -- one step of a beam search over n_seq sequences of n_beams beams
+ * each: beam i of sequence s is row s*n_beams + i of logits, scores, done, lengths and
+ * history.  A beam that goes on has the continuations (beam, token), worth
+ *     scores[beam] + logits[beam][token] - log(sum_t exp(logits[beam][t])),
+ * one that is done has one: (beam, end_token), worth scores[beam].  The n_out best of
+ * each sequence are kept, best first, ties to the lower beam, then to the lower token;
+ * logits of -inf, and beams whose score is -inf, have no continuations.  Worths are compared in
+ * 64 bits (the sum of exponentials is f32's), out_scores are rounded to f32.
+ * parent is what idx_page_update takes to let the pages follow.
+ *   logits     [n_seq*n_beams] rows of n_vocab, row stride in elements, F32/F16/BF16.
+ *   scores     f32 [n_seq*n_beams], done uint8 [n_seq*n_beams] or NULL (none is).
+ *   end_token  the token that ends a beam; -1: none does (done must be NULL then).
+ *   out_scores f32, parent int32 (row of the beam continued), token int32, out_done uint8
+ *              (done before, or token == end_token) [n_seq*n_out].  Places without a
+ *              continuation: -inf, -1, -1, 1.
+ *   history    int32 [n_seq*n_beams] rows of history_cols tokens, lengths int32
+ *              [n_seq*n_beams] how many of them count; or both NULL.  Row r of out_history
+ *              becomes the parent's tokens and, unless that was done, the new one behind
+ *              them; out_lengths[r] their number (0 without a continuation).  Entries
+ *              past it stay as they were.  A length outside [0, history_cols], or without
+ *              room for the new token, is clamped, the token dropped, and flagged
+ *              (IDX_ERR_DEVICE_BOUNDS).
+ *   workspace  idx_beam_workspace_size(...) bytes, 16-byte aligned, not shared with
+ *              calls whose work overlaps this one's.
+ * What is written must not overlap what is read.  A row of logits that holds a NaN or
+ * +inf, or whose score is NaN or +inf, has no continuations and is flagged (IDX_ERR_INEXACT).
+ * Errors: n_seq < 0, n_beams < 1, n_vocab < 1, n_out outside [1, 32], n_beams*n_vocab >
+ * 2^31 - 1, end_token outside [-1, n_vocab), NULL where a tensor is needed: INVALID_ARG;
+ * n_beams > 1024: UNSUPPORTED.
+ */
+typedef struct idx_beam {
+    const void* logits;
+    int64_t logit_stride;
+    const float* scores;
+    const uint8_t* done;
+    const int32_t* lengths;
+    const int32_t* history;
+    int64_t history_stride;
+    float* out_scores;
+    int32_t* parent;
+    int32_t* token;
+    uint8_t* out_done;
+    int32_t* out_lengths;
+    int32_t* out_history;
+    int64_t out_history_stride;
+    int32_t history_cols;
+} idx_beam;
+
+idx_status idx_beam_step(const idx_beam* beam, idx_dtype dtype, int32_t n_seq, int32_t n_beams, int32_t n_out,
+                         int32_t n_vocab, int32_t end_token, void* workspace, size_t workspace_bytes,
+                         idx_stream_t stream);
+
+size_t idx_beam_workspace_size(int32_t n_seq, int32_t n_beams, int32_t n_out, int32_t n_vocab);
+
 /* Operation selectors for idx_workspace_size. */
 enum {
     IDX_OP_SCORE = 0,

@@ -14,7 +14,7 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -27,7 +27,8 @@ __all__ = [
     "idx_topk", "sparse_attn_decode", "sparse_attn_prefill", "idx_workspace_size",
     "idx_device_status", "topk_capacity", "sparse_attn_decode_noalloc", "idx_score_topk", "idx_block_score_topk", "sparse_decode_step", "sparse_decode_step_fused",
     "dense_attn", "dense_attn_workspace_size", "idx_page_copy", "idx_page_update", "idx_page_compact",
-    "idx_page_workspace_size",
+    "idx_page_workspace_size", "idx_cache_append", "idx_cache_append_q4", "idx_cache_read_q4", "idx_q4_row_bytes",
+    "dense_attn_q4", "dense_attn_q4_workspace_size", "idx_beam_step", "idx_beam_workspace_size", "BeamStep",
 ]
 
 IDX_OK, IDX_ERR_INVALID_ARG, IDX_ERR_UNSUPPORTED, IDX_ERR_CUDA, IDX_ERR_TIMEOUT, IDX_ERR_DEVICE_BOUNDS, IDX_ERR_INEXACT = range(7)
@@ -78,6 +79,48 @@ class _PageCache(ctypes.Structure):
     ]
 
 
+class _NewRows(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("k_stride", ctypes.c_int64),
+        ("v", ctypes.c_void_p),
+        ("v_stride", ctypes.c_int64),
+        ("q", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64),
+        ("q_out", ctypes.c_void_p),
+        ("q_out_stride", ctypes.c_int64),
+    ]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [
+        ("inv_freq", ctypes.c_void_p),
+        ("n_rot", ctypes.c_int32),
+        ("start", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+    ]
+
+
+class _Beam(ctypes.Structure):
+    _fields_ = [
+        ("logits", ctypes.c_void_p),
+        ("logit_stride", ctypes.c_int64),
+        ("scores", ctypes.c_void_p),
+        ("done", ctypes.c_void_p),
+        ("lengths", ctypes.c_void_p),
+        ("history", ctypes.c_void_p),
+        ("history_stride", ctypes.c_int64),
+        ("out_scores", ctypes.c_void_p),
+        ("parent", ctypes.c_void_p),
+        ("token", ctypes.c_void_p),
+        ("out_done", ctypes.c_void_p),
+        ("out_lengths", ctypes.c_void_p),
+        ("out_history", ctypes.c_void_p),
+        ("out_history_stride", ctypes.c_int64),
+        ("history_cols", ctypes.c_int32),
+    ]
+
+
 IDX_MAX_PAGE_CACHES = 8
 
 _lib = None
@@ -121,6 +164,17 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
                             P, SZ, P],
         "idx_page_compact": [P, I64, I32, I32, P, I32, I32, P, P, I64, P, P, ctypes.POINTER(_PageCache), I32, P, SZ, P],
         "idx_page_workspace_size": [I32, I32],
+        "idx_cache_append": [ctypes.POINTER(_NewRows), I32, I32, I32, I32, I32, _Batch, ctypes.POINTER(_Rope), P, I64, P,
+                             I64, I64, P],
+        "idx_cache_append_q4": [ctypes.POINTER(_NewRows), I32, I32, I32, I32, I32, _Batch, ctypes.POINTER(_Rope), P, I64,
+                                P, I64, I64, P],
+        "idx_q4_row_bytes": [I32, I32],
+        "idx_cache_read_q4": [P, I64, P, I64, I64, I32, I32, I32, _Batch, I32, P, P, P],
+        "dense_attn_q4": [P, I32, I32, I32, I32, I32, P, I64, P, I64, I64, _Batch, ctypes.POINTER(_Mods), F, P, P, P, SZ,
+                          P],
+        "dense_attn_q4_workspace_size": [I32, I32, I32, I32, I32, I32, I32, I32],
+        "idx_beam_step": [ctypes.POINTER(_Beam), I32, I32, I32, I32, I32, I32, P, SZ, P],
+        "idx_beam_workspace_size": [I32, I32, I32, I32],
         "idx_last_error": [],
         "idx_device_status": [I32],
     }
@@ -128,7 +182,8 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = ctypes.c_int
-    for name in ("idx_workspace_size", "dense_attn_workspace_size", "idx_page_workspace_size"):
+    for name in ("idx_workspace_size", "dense_attn_workspace_size", "idx_page_workspace_size", "idx_q4_row_bytes",
+                 "dense_attn_q4_workspace_size", "idx_beam_workspace_size"):
         getattr(lib, name).restype = ctypes.c_size_t
     lib.idx_last_error.restype = ctypes.c_char_p
     _lib = lib
@@ -547,6 +602,32 @@ def _i32(name: str, t: torch.Tensor, n: int):
     return t.data_ptr()
 
 
+def _batch_lengths(batch: Batch, b: _Batch, rows: int) -> None:
+    """Refuses batch arrays that are shorter than the batch."""
+    # (kv_start is not read beside a page table)
+    where, n = (batch.kv_start, b.n_seq) if batch.page_table is None else (batch.page_table, b.n_seq * b.page_table_stride)
+    if batch.q_pos is not None and batch.q_pos.numel() < rows or where is not None and where.numel() < n:
+        raise ValueError("q_pos, kv_start or page_table has fewer entries than the batch")
+
+
+def _mods(dev, b: _Batch, rows: int, Hq: int, softcap, slopes, window, prefix_len, doc_start, prefix_end):
+    """The options of a dense attention call, or None for none of them."""
+    if not -2**31 <= window < 2**31:
+        raise ValueError("window must be below 2**31")
+    if softcap and not ctypes.c_float(softcap).value:
+        raise ValueError("softcap is 0 in float32, which is no cap")
+    if not (softcap or window) and slopes is prefix_len is doc_start is prefix_end is None:
+        return None
+    _all_on(dev, slopes, prefix_len, doc_start, prefix_end)
+    if slopes is not None and (slopes.dtype is not torch.float32 or not slopes.is_contiguous() or
+                               slopes.numel() != Hq):
+        raise ValueError("slopes must be a contiguous float32 tensor with one entry per query head")
+    return _Mods(softcap, None if slopes is None else slopes.data_ptr(), window,
+                 None if prefix_len is None else _i32("prefix_len", prefix_len, b.n_seq),
+                 None if doc_start is None else _i32("doc_start", doc_start, rows),
+                 None if prefix_end is None else _i32("prefix_end", prefix_end, rows))
+
+
 def dense_attn_workspace_size(dtype: torch.dtype, n_seq: int, n_q_per_seq: int, max_n_kv: int, n_q_heads: int,
                               n_kv_heads: int, dk: int, dv: int) -> int:
     """Bytes of workspace with which dense_attn splits the keys as it would like to."""
@@ -575,10 +656,7 @@ def dense_attn(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tensor], batc
     _all_on(dev, k, v, out, lse, workspace, batch.n_kv, batch.q_pos, batch.page_table, batch.kv_start)
     b = batch.c()
     rows = b.n_seq * b.n_q_per_seq
-    # (kv_start is not read beside a page table)
-    where, n = (batch.kv_start, b.n_seq) if batch.page_table is None else (batch.page_table, b.n_seq * b.page_table_stride)
-    if batch.q_pos is not None and batch.q_pos.numel() < rows or where is not None and where.numel() < n:
-        raise ValueError("q_pos, kv_start or page_table has fewer entries than the batch")
+    _batch_lengths(batch, b, rows)
     if q.dim() != 3 or q.shape[0] != rows or not q.is_contiguous():
         raise ValueError("q must be a contiguous [n_seq * n_q_per_seq, heads, dk] tensor")
     _, Hq, dk = q.shape
@@ -606,20 +684,7 @@ def dense_attn(q: torch.Tensor, k: torch.Tensor, v: Optional[torch.Tensor], batc
     dt = _dtype(q)
     if k.dtype is not q.dtype or (v is not None and v.dtype is not q.dtype):
         raise ValueError("q, k and v must have the same dtype")
-    mods = None
-    if not -2**31 <= window < 2**31:
-        raise ValueError("window must be below 2**31")
-    if softcap and not ctypes.c_float(softcap).value:
-        raise ValueError("softcap is 0 in float32, which is no cap")
-    if softcap or window or not (slopes is prefix_len is doc_start is prefix_end is None):
-        _all_on(dev, slopes, prefix_len, doc_start, prefix_end)
-        if slopes is not None and (slopes.dtype is not torch.float32 or not slopes.is_contiguous() or
-                                   slopes.numel() != Hq):
-            raise ValueError("slopes must be a contiguous float32 tensor with one entry per query head")
-        mods = _Mods(softcap, None if slopes is None else slopes.data_ptr(), window,
-                     None if prefix_len is None else _i32("prefix_len", prefix_len, b.n_seq),
-                     None if doc_start is None else _i32("doc_start", doc_start, rows),
-                     None if prefix_end is None else _i32("prefix_end", prefix_end, rows))
+    mods = _mods(dev, b, rows, Hq, softcap, slopes, window, prefix_len, doc_start, prefix_end)
     if out is None:
         out = torch.empty((rows, Hq, dv), device=dev, dtype=q.dtype)
     elif out.shape != (rows, Hq, dv) or out.dtype is not q.dtype or not out.is_contiguous():
@@ -788,6 +853,292 @@ def idx_page_compact(page_table: torch.Tensor, n_len: torch.Tensor, page_size: i
                                     _i32("n_used", n_used, 1), _i32("remap", remap, n_pages), arr, len(caches),
                                     *_space(workspace), _stream(dev)))
     return new_table, n_used, remap
+
+
+def idx_q4_row_bytes(n_heads: int, d: int) -> int:
+    """Bytes of a 4-bit cache row of n_heads heads of d columns (d a multiple of 8): codes, then scale and minimum of each
+    head, rounded up to 16."""
+    n = int(load().idx_q4_row_bytes(n_heads, d))
+    if not n:
+        raise ValueError("a 4-bit cache row holds at least one head of a multiple of 8 columns")
+    return n
+
+
+def _new_rows(name: str, t: torch.Tensor, rows: int):
+    """(address, row stride, heads, columns) of [rows, heads, columns] whose rows may lie apart."""
+    if t.dim() != 3 or t.shape[0] != rows:
+        raise ValueError(f"{name} must be a [n_seq * n_q_per_seq, heads, columns] tensor")
+    _, h, d = t.shape
+    s0, s1, s2 = t.stride()
+    if (d > 1 and s2 != 1) or (h > 1 and s1 != d):
+        raise ValueError(f"the heads of a row of {name} must be contiguous")
+    if rows > 1 and s0 < h * d:
+        raise ValueError(f"the rows of {name} must not overlap")
+    return t.data_ptr(), max(s0, h * d), h, d
+
+
+def _q4_cache(name: str, t: torch.Tensor, heads: int, d: int):
+    """(address, row stride) of a 4-bit cache."""
+    if t.dtype is not torch.uint8 or t.dim() != 2 or t.shape[1] < heads * (d // 2 + 8) or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a uint8 [rows, idx_q4_row_bytes(heads, columns)] tensor with contiguous rows")
+    s = t.stride(0)
+    if t.shape[0] > 1 and s < t.shape[1]:
+        raise ValueError(f"the rows of {name} must not overlap")
+    return t.data_ptr(), max(s, t.shape[1])
+
+
+def _append(fn, q4: bool, k, v, k_cache, v_cache, batch, q, q_out, inv_freq, rot_start, interleaved):
+    dev = k.device
+    _need_cuda(k)
+    _all_on(dev, v, q, q_out, k_cache, v_cache, inv_freq, batch.n_kv, batch.q_pos, batch.page_table, batch.kv_start)
+    b = batch.c()
+    rows = b.n_seq * b.n_q_per_seq
+    _batch_lengths(batch, b, rows)
+    dt = _dtype(k)
+    k_ptr, k_stride, hkv, dk = _new_rows("k", k, rows)
+    v_ptr, v_stride, dv = None, 0, 0
+    if (v is None) != (v_cache is None):
+        raise ValueError("v and v_cache come together")
+    if v is not None:
+        v_ptr, v_stride, hv, dv = _new_rows("v", v, rows)
+        if hv != hkv or v.dtype is not k.dtype:
+            raise ValueError("k and v must have the same heads and dtype")
+    q_ptr = qo_ptr = None
+    q_stride = qo_stride = hq = 0
+    if q is not None:
+        q_ptr, q_stride, hq, dq = _new_rows("q", q, rows)
+        if dq != dk or q.dtype is not k.dtype:
+            raise ValueError("q and k must have the same columns and dtype")
+        if q_out is None:
+            q_out = torch.empty((rows, hq, dk), device=dev, dtype=q.dtype)
+        qo_ptr, qo_stride, ho, do = _new_rows("q_out", q_out, rows)
+        if (ho, do) != (hq, dk) or q_out.dtype is not q.dtype:
+            raise ValueError("q_out must have q's shape and dtype")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if q4:
+        if dk % 8 or dv % 8:
+            raise ValueError("the heads of a 4-bit cache have a multiple of 8 columns")
+        kc_ptr, kc_stride = _q4_cache("k_cache", k_cache, hkv, dk)
+        vc_ptr, vc_stride = (None, 0) if v is None else _q4_cache("v_cache", v_cache, hkv, dv)
+    else:
+        caches = []
+        for name, c, d in (("k_cache", k_cache, dk), ("v_cache", v_cache, dv)):
+            if c is None:
+                caches.append((None, 0))
+                continue
+            if c.dim() == 2 and hkv == 1:
+                c = c[:, None]
+            if c.dim() != 3 or c.shape[1:] != (hkv, d) or c.dtype is not k.dtype:
+                raise ValueError(f"{name} must be a [rows, heads, columns] tensor of the new rows' heads and dtype")
+            caches.append(_new_rows(name, c, c.shape[0])[:2])
+        (kc_ptr, kc_stride), (vc_ptr, vc_stride) = caches
+    if v_cache is not None and v_cache.shape[0] != k_cache.shape[0]:
+        raise ValueError("k_cache and v_cache must have the same rows")
+    rope = None
+    if inv_freq is not None:
+        if inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+            raise ValueError("inv_freq must be a contiguous float32 tensor of one dimension")
+        rope = _Rope(inv_freq.data_ptr(), 2 * inv_freq.numel(), rot_start, 1 if interleaved else 0)
+    with _On(dev):
+        _check(fn(_NewRows(k_ptr, k_stride, v_ptr, v_stride, q_ptr, q_stride, qo_ptr, qo_stride), dt, hq, hkv, dk, dv, b,
+                  rope, kc_ptr, kc_stride, vc_ptr, vc_stride, k_cache.shape[0], _stream(dev)))
+    return q_out
+
+
+def idx_cache_append(k: torch.Tensor, v: Optional[torch.Tensor], k_cache: torch.Tensor, v_cache: Optional[torch.Tensor],
+                     batch: Batch, *, q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                     inv_freq: Optional[torch.Tensor] = None, rot_start: int = 0,
+                     interleaved: bool = False) -> Optional[torch.Tensor]:
+    """Writes the rows of a batch's new tokens into its caches, rotated by their positions, in one launch.
+    k [B*T, Hkv, dk], v [B*T, Hkv, dv] and q [B*T, Hq, dk] may be slices of one projection's output (rows apart, heads
+    contiguous); k_cache [rows, Hkv, dk] and v_cache [rows, Hkv, dv] ([rows, dk] for one head); v and v_cache None for a
+    cache without values (the latent).  Row r goes to position batch.q_pos[r] of its sequence (negative: a padding row,
+    which writes nothing), without q_pos the T rows are the sequence's last ones; batch.n_kv counts them.  Returns q_out:
+    q rotated (q itself as q_out: in place), None without q.
+
+    inv_freq (f32 [n_rot / 2], radians per position; None: no rotation) turns columns rot_start .. rot_start + n_rot - 1 of
+    each head of q and k: pairs n_rot / 2 apart, or neighbours with `interleaved`."""
+    return _append(load().idx_cache_append, False, k, v, k_cache, v_cache, batch, q, q_out, inv_freq, rot_start, interleaved)
+
+
+def idx_cache_append_q4(k: torch.Tensor, v: Optional[torch.Tensor], k_cache: torch.Tensor, v_cache: Optional[torch.Tensor],
+                        batch: Batch, *, q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                        inv_freq: Optional[torch.Tensor] = None, rot_start: int = 0,
+                        interleaved: bool = False) -> Optional[torch.Tensor]:
+    """idx_cache_append into 4-bit caches: uint8 [rows, idx_q4_row_bytes(Hkv, d)].  Each head's row is quantised by itself,
+    K after the rotation: codes 0 .. 15 over its range, with scale and minimum in f32.  dk and dv are multiples of 8."""
+    return _append(load().idx_cache_append_q4, True, k, v, k_cache, v_cache, batch, q, q_out, inv_freq, rot_start, interleaved)
+
+
+def idx_cache_read_q4(k_cache: torch.Tensor, v_cache: Optional[torch.Tensor], batch: Batch, n_kv_heads: int, dk: int,
+                      dv: int = 0, *, dtype: Optional[torch.dtype] = None, k_out: Optional[torch.Tensor] = None,
+                      v_out: Optional[torch.Tensor] = None):
+    """The values that rows of 4-bit caches stand for: (k_out [B*T, Hkv, dk], v_out [B*T, Hkv, dv]) of the batch's rows,
+    whose positions are as in idx_cache_append.  Rows that are padding stay as they were (zeros in a new output).
+    v_cache None with dv 0: v_out is None.  dtype: of new outputs, torch.bfloat16 unless k_out is given."""
+    dev = k_cache.device
+    _need_cuda(k_cache)
+    _all_on(dev, v_cache, k_out, v_out, batch.n_kv, batch.q_pos, batch.page_table, batch.kv_start)
+    b = batch.c()
+    rows = b.n_seq * b.n_q_per_seq
+    _batch_lengths(batch, b, rows)
+    if (v_cache is None) != (dv == 0) or (v_cache is None and v_out is not None):
+        raise ValueError("v_cache and dv come together")
+    if n_kv_heads < 1 or dk < 8 or dv < 0 or dk % 8 or dv % 8:
+        raise ValueError("the heads of a 4-bit cache have a multiple of 8 columns")
+    if dtype is None:
+        dtype = torch.bfloat16 if k_out is None else k_out.dtype
+    outs = []
+    for name, t, d in (("k_out", k_out, dk), ("v_out", v_out, dv)):
+        if t is None and d:
+            t = torch.zeros((rows, n_kv_heads, d), device=dev, dtype=dtype)
+        elif t is not None and (t.shape != (rows, n_kv_heads, d) or t.dtype is not dtype or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous [rows, heads, columns] tensor of one dtype with the other")
+        outs.append(t)
+    kc, kc_stride = _q4_cache("k_cache", k_cache, n_kv_heads, dk)
+    vc, vc_stride = (None, 0) if v_cache is None else _q4_cache("v_cache", v_cache, n_kv_heads, dv)
+    if v_cache is not None and v_cache.shape[0] != k_cache.shape[0]:
+        raise ValueError("k_cache and v_cache must have the same rows")
+    with _On(dev):
+        _check(load().idx_cache_read_q4(kc, kc_stride, vc, vc_stride, k_cache.shape[0], n_kv_heads, dk, dv, b,
+                                        _dtype(outs[0]), outs[0].data_ptr(), None if outs[1] is None else outs[1].data_ptr(),
+                                        _stream(dev)))
+    return outs[0], outs[1]
+
+
+def dense_attn_q4_workspace_size(dtype: torch.dtype, n_seq: int, n_q_per_seq: int, max_n_kv: int, n_q_heads: int,
+                                 n_kv_heads: int, dk: int, dv: int) -> int:
+    """Bytes of workspace with which dense_attn_q4 works as it would like to."""
+    return int(load().dense_attn_q4_workspace_size(_DTYPES[dtype], n_seq, n_q_per_seq, max_n_kv, n_q_heads, n_kv_heads,
+                                                   dk, dv))
+
+
+def dense_attn_q4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, batch: Batch, scale: float,
+                  n_kv_heads: int, *, dv: Optional[int] = None, softcap: float = 0.0,
+                  slopes: Optional[torch.Tensor] = None, window: int = 0, prefix_len: Optional[torch.Tensor] = None,
+                  doc_start: Optional[torch.Tensor] = None, prefix_end: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dense_attn over 4-bit caches (uint8 [rows, idx_q4_row_bytes(n_kv_heads, d)], see idx_cache_append_q4): the
+    attention of q [B*T, Hq, dk] over the values that the codes stand for, with dense_attn's options.  dv: columns of V, dk
+    unless given.  Returns out [B*T, Hq, dv] of q's dtype."""
+    dev = q.device
+    _need_cuda(q)
+    _all_on(dev, k_cache, v_cache, out, lse, workspace, batch.n_kv, batch.q_pos, batch.page_table, batch.kv_start)
+    b = batch.c()
+    rows = b.n_seq * b.n_q_per_seq
+    _batch_lengths(batch, b, rows)
+    if q.dim() != 3 or q.shape[0] != rows or not q.is_contiguous():
+        raise ValueError("q must be a contiguous [n_seq * n_q_per_seq, heads, dk] tensor")
+    _, Hq, dk = q.shape
+    if dv is None:
+        dv = dk
+    if n_kv_heads < 1 or dk % 8 or dv < 8 or dv % 8:
+        raise ValueError("the heads of a 4-bit cache have a multiple of 8 columns")
+    dt = _dtype(q)
+    kc, kc_stride = _q4_cache("k_cache", k_cache, n_kv_heads, dk)
+    vc, vc_stride = _q4_cache("v_cache", v_cache, n_kv_heads, dv)
+    if v_cache.shape[0] != k_cache.shape[0]:
+        raise ValueError("k_cache and v_cache must have the same rows")
+    mods = _mods(dev, b, rows, Hq, softcap, slopes, window, prefix_len, doc_start, prefix_end)
+    if out is None:
+        out = torch.empty((rows, Hq, dv), device=dev, dtype=q.dtype)
+    elif out.shape != (rows, Hq, dv) or out.dtype is not q.dtype or not out.is_contiguous():
+        raise ValueError("out must be a contiguous [rows, heads, dv] tensor of q's dtype")
+    if lse is not None and (lse.shape != (rows, Hq) or lse.dtype is not torch.float32 or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 [rows, heads] tensor")
+    lib = load()
+    with _On(dev):
+        if workspace is None:
+            need = lib.dense_attn_q4_workspace_size(dt, b.n_seq, b.n_q_per_seq, b.max_n_kv, Hq, n_kv_heads, dk, dv)
+            if need:
+                workspace = torch.empty(need, device=dev, dtype=torch.uint8)
+        # (an empty cache has no address)
+        _check(lib.dense_attn_q4(q.data_ptr(), dt, Hq, n_kv_heads, dk, dv, kc or q.data_ptr(), kc_stride, vc or q.data_ptr(),
+                                 vc_stride, k_cache.shape[0], b, mods, scale, out.data_ptr(),
+                                 None if lse is None else lse.data_ptr(), *_space(workspace), _stream(dev)))
+    return out
+
+
+class BeamStep(NamedTuple):
+    """What idx_beam_step gives, [n_seq * n_out] each: scores f32, parent (row of the beam continued, -1: none), token,
+    done (uint8), and, where histories were given, lengths and history."""
+    scores: torch.Tensor
+    parent: torch.Tensor
+    token: torch.Tensor
+    done: torch.Tensor
+    lengths: Optional[torch.Tensor]
+    history: Optional[torch.Tensor]
+
+
+def idx_beam_workspace_size(n_seq: int, n_beams: int, n_out: int, n_vocab: int) -> int:
+    return int(load().idx_beam_workspace_size(n_seq, n_beams, n_out, n_vocab))
+
+
+def idx_beam_step(logits: torch.Tensor, scores: torch.Tensor, n_beams: int, *, n_out: Optional[int] = None,
+                  done: Optional[torch.Tensor] = None, end_token: int = -1, lengths: Optional[torch.Tensor] = None,
+                  history: Optional[torch.Tensor] = None, history_out: Optional[torch.Tensor] = None,
+                  out: Optional[BeamStep] = None, workspace: Optional[torch.Tensor] = None) -> BeamStep:
+    """One step of a beam search: of the continuations of each sequence's n_beams beams (logits [n_seq * n_beams, vocab], f32
+    scores [n_seq * n_beams]) the n_out (at most 32; n_beams unless given) best by score plus log-probability, best first,
+    ties to the lower beam, then to the lower token.  A beam marked in `done` (uint8 or bool) is continued by end_token
+    alone, its score unchanged; end_token (-1: none) marks a beam done.  With lengths (int32 [rows]) and history (int32
+    [rows, columns]), row r of the new history is the parent's, the token behind it unless the parent was done; entries past
+    the new length stay as they were (zeros in a new tensor).  parent serves idx_page_update as it is.  out: tensors of an
+    earlier step to write to (none of them read by this one)."""
+    dev = logits.device
+    _need_cuda(logits)
+    _all_on(dev, scores, done, lengths, history, history_out, workspace, *(out or ()))
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be a [n_seq * n_beams, vocab] tensor with contiguous rows")
+    rows, vocab = logits.shape
+    if n_beams < 1 or rows % n_beams:
+        raise ValueError("logits must have n_beams rows for each sequence")
+    stride = max(logits.stride(0), vocab)
+    if rows > 1 and logits.stride(0) < vocab:
+        raise ValueError("the rows of logits must not overlap")
+    n_seq, n_out = rows // n_beams, n_beams if n_out is None else n_out
+    dt = _dtype(logits)
+    if scores.dtype is not torch.float32 or scores.numel() != rows or not scores.is_contiguous():
+        raise ValueError("scores must be a contiguous float32 tensor with one entry per row of logits")
+    if done is not None and (done.dtype not in (torch.uint8, torch.bool) or done.numel() != rows or not done.is_contiguous()):
+        raise ValueError("done must be a contiguous uint8 or bool tensor with one entry per row of logits")
+    if (lengths is None) != (history is None):
+        raise ValueError("lengths and history come together")
+    new = n_seq * n_out
+    if out is None:
+        f = torch.empty((4, new), device=dev, dtype=torch.int32)
+        out = BeamStep(f[0].view(torch.float32), f[1], f[2], torch.empty(new, device=dev, dtype=torch.uint8),
+                       None if lengths is None else f[3], history_out)
+    for name, t, d in (("scores", out.scores, torch.float32), ("parent", out.parent, torch.int32),
+                       ("token", out.token, torch.int32), ("done", out.done, torch.uint8)):
+        if t.dtype is not d or t.numel() != new or not t.is_contiguous():
+            raise ValueError(f"out.{name} must be a contiguous {d} tensor with n_out entries for each sequence")
+    cols = h_stride = o_stride = 0
+    l_ptr = h_ptr = lo_ptr = ho_ptr = None
+    if history is not None:
+        if out.history is None:
+            out = out._replace(history=torch.zeros((new, history.shape[-1]), device=dev, dtype=torch.int32))
+        if out.lengths is None:
+            raise ValueError("out.lengths is needed beside a history")
+        h_ptr, h_stride, n, cols = _table("history", history)
+        ho_ptr, o_stride, no, co = _table("history_out", out.history)
+        if n != rows or no != new or co != cols:
+            raise ValueError("history must have one row per row of logits, history_out n_out for each sequence, of its width")
+        l_ptr, lo_ptr = _i32("lengths", lengths, rows), _i32("out.lengths", out.lengths, new)
+        # (an empty tensor has no address)
+        h_ptr, ho_ptr, lo_ptr = h_ptr or l_ptr, ho_ptr or lo_ptr, lo_ptr
+    lib = load()
+    with _On(dev):
+        if workspace is None:
+            workspace = torch.empty(max(lib.idx_beam_workspace_size(n_seq, n_beams, n_out, vocab), 16), device=dev,
+                                    dtype=torch.uint8)
+        _check(lib.idx_beam_step(_Beam(logits.data_ptr(), stride, scores.data_ptr(), None if done is None else done.data_ptr(),
+                                       l_ptr, h_ptr, h_stride, out.scores.data_ptr(), out.parent.data_ptr(),
+                                       out.token.data_ptr(), out.done.data_ptr(), lo_ptr, ho_ptr, o_stride, cols), dt, n_seq,
+                                 n_beams, n_out, vocab, end_token, *_space(workspace), _stream(dev)))
+    return out
 
 
 def idx_device_status(reset: bool = True) -> int:

@@ -26,6 +26,7 @@ struct DenseArgs {
                               // kDenseCluster splits), the splits are a cluster that merges them
     float* part_o;            // [row * Hq + head][split][dv] unnormalised
     float* part_ml;           // [row * Hq + head][split][2]: maximum (natural-log units), sum
+    const int* only_if;       // or NULL; given and 0 on the device: the launch has nothing to do (CUDA cores, 4 bits)
 };
 
 struct Interval {
@@ -193,6 +194,8 @@ __device__ __forceinline__ Score make_score(const DenseArgs& a, float slope) {
 // CUDA cores: every type, width and alignment
 cudaError_t launch_dense_generic(const DenseArgs& a, int dtype, const Geom& g, cudaStream_t st);
 int dense_generic_splits(int64_t n_seq, int64_t n_q, int64_t max_n_kv, int Hq, int Hkv, int dk, int dv);
+// the same over 4-bit caches (k and v: bytes, strides in bytes; dk and dv multiples of 8)
+cudaError_t launch_dense_generic_q4(const DenseArgs& a, int dtype, const Geom& g, cudaStream_t st);
 
 // tensor cores: 16-bit K and V of at most 128 columns each, 16-byte aligned, pages of a multiple of 8 rows
 bool dense_tc_supported(const DenseArgs& a, int dtype, const Geom& g);

@@ -60,7 +60,8 @@ size_t smem_bytes(int R, int DV, int dk, int dv, bool latent, int bufs) {
 // neither shared memory nor registers leave room for a third.  There, and for the widest values, the compiler is told of
 // two, which it makes use of: 252 registers for 186 (512 tokens on 4096 keys: 2.48 -> 2.39 ms), 223 for 167 (256 tokens on
 // 2048 keys, heads of 256: 1.88 -> 1.80 ms).
-template <typename T, int R, int DV, bool kAhead>
+// kQ4: K and V are rows of 4-bit caches, widened to scale * code + minimum.
+template <typename T, int R, int DV, bool kAhead, bool kQ4 = false>
 __global__ void __launch_bounds__(kThreads, DV == 64 ? 3 : DV == 512 || (R == 64 && kAhead) ? 2 : 0)
     dense_generic_kernel(DenseArgs a, Geom g, int tiles, bool vec) {
     using S = Shape<R, DV>;
@@ -93,6 +94,7 @@ __global__ void __launch_bounds__(kThreads, DV == 64 ? 3 : DV == 512 || (R == 64
     const int64_t m_end = (int64_t)g.T * G;
     if (a.part_o) pdl_trigger();     // (the merge follows; results are not handed on early, see lidx_internal.cuh)
     pdl_wait();
+    if (kQ4 && a.only_if && *a.only_if == 0) return;      // (no splits then: every CTA leaves)
     const int n_kv = seq_n_kv(g, b);
 
     // the rows' intervals, and the CTA's: the keys that some row sees
@@ -202,7 +204,44 @@ __global__ void __launch_bounds__(kThreads, DV == 64 ? 3 : DV == 512 || (R == 64
             if (tid < kKeys) rows_s[tid] = row_of(t0 + tid);
             bad = __syncthreads_or(tid < kKeys && rows_s[tid < kKeys ? tid : 0] < 0);
             // K and V rows, widened
-            if (vec) {
+            if constexpr (kQ4) {
+                const int wk = a.dk / 8, wv = a.dv / 8, total = kKeys * (wk + wv);
+                constexpr int kBatch = 4;
+                for (int e0 = tid; e0 < total; e0 += kThreads * kBatch) {
+                    uint32_t x[kBatch];
+                    float scale[kBatch], low[kBatch];
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int e = e0 + i * kThreads;
+                        x[i] = 0u;
+                        scale[i] = low[i] = 0.f;
+                        if (e < total) {
+                            const bool isk = e < kKeys * wk;
+                            const int ee = isk ? e : e - kKeys * wk, w = isk ? wk : wv;
+                            const int64_t row = rows_s[ee / w];
+                            if (row >= 0) {
+                                const uint8_t* src = isk ? static_cast<const uint8_t*>(a.k) + row * a.k_stride
+                                                         : static_cast<const uint8_t*>(a.v) + row * a.v_stride;
+                                x[i] = reinterpret_cast<const uint32_t*>(src)[gkv * w + ee % w];
+                                const float* pr = reinterpret_cast<const float*>(src + a.Hkv * w * 4) + 2 * gkv;
+                                scale[i] = pr[0];
+                                low[i] = pr[1];
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int e = e0 + i * kThreads;
+                        if (e < total) {
+                            const bool isk = e < kKeys * wk;
+                            const int ee = isk ? e : e - kKeys * wk, w = isk ? wk : wv;
+                            float* d = isk ? ks + ee / w * kp + ee % w * 8 : vs + ee / w * vp + ee % w * 8;
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) d[j] = fmaf((float)((x[i] >> (4 * j)) & 15u), scale[i], low[i]);
+                        }
+                    }
+                }
+            } else if (vec) {
                 constexpr int E = 16 / (int)sizeof(T);
                 const int wk = a.dk / E, wv = latent ? 0 : a.dv / E;
                 const int total = kKeys * (wk + wv);
@@ -546,7 +585,7 @@ __global__ void __launch_bounds__(128) dense_combine_kernel(DenseArgs a, int64_t
 // 128 beside them; 529 columns take 233,216, more than the 232,448 that a CTA may have)
 int tile_rows(int64_t packed, int dk, int dv) { return dv <= 128 && dk <= 528 && packed > 16 ? 64 : 16; }
 
-template <typename T>
+template <typename T, bool kQ4 = false>
 cudaError_t run(const DenseArgs& a, const Geom& g, cudaStream_t st) {
     const int64_t packed = (int64_t)g.T * (a.Hq / a.Hkv);
     const int R = tile_rows(packed, a.dk, a.dv);
@@ -564,7 +603,13 @@ cudaError_t run(const DenseArgs& a, const Geom& g, cudaStream_t st) {
         return launch_pdl_cluster(kern, dim3((unsigned)grid), dim3(kThreads), sm, st,
                                   a.splits > 1 && !a.part_o ? a.splits : 1, a, g, (int)tiles, vec);
     };
-    if constexpr (sizeof(T) == 4) {
+    if constexpr (kQ4) {
+        if (R == 64)
+            return a.dv <= 64 ? go(dense_generic_kernel<T, 64, 64, false, true>, 64, 1)
+                              : go(dense_generic_kernel<T, 64, 128, false, true>, 128, 1);
+        return a.dv <= 128 ? go(dense_generic_kernel<T, 16, 128, false, true>, 128, 1)
+                           : go(dense_generic_kernel<T, 16, 512, false, true>, 512, 1);
+    } else if constexpr (sizeof(T) == 4) {
         // a tile ahead where two CTAs fit an SM with it (wider rows would be alone there)
         const int dvp = R == 64 && a.dv <= 64 ? 64 : a.dv <= 128 ? 128 : 512;
         if (vec && smem_bytes(R, dvp, a.dk, a.dv, !a.v, 2) <= 113 * 1024) {
@@ -601,6 +646,14 @@ cudaError_t launch_dense_generic(const DenseArgs& a, int dtype, const Geom& g, c
         case IDX_F16: return run<__half>(a, g, st);
         case IDX_BF16: return run<__nv_bfloat16>(a, g, st);
         default: return run<float>(a, g, st);
+    }
+}
+
+cudaError_t launch_dense_generic_q4(const DenseArgs& a, int dtype, const Geom& g, cudaStream_t st) {
+    switch (dtype) {
+        case IDX_F16: return run<__half, true>(a, g, st);
+        case IDX_BF16: return run<__nv_bfloat16, true>(a, g, st);
+        default: return run<float, true>(a, g, st);
     }
 }
 
