@@ -721,12 +721,14 @@ idx_status idx_cache_read_q4(const void* k_cache, int64_t k_row_stride, const vo
  *              8.  There is no latent form.
  *   workspace  dense_attn_q4_workspace_size(...) bytes, 16-byte aligned.  With less (or
  *              NULL) the call takes another way, with the same results up to rounding:
- *              fewer key splits, or codes that each tile of rows expands for itself
- *              instead of once for all.
- * 16-bit q and heads of 64 or 128 columns (dk == dv), given 16-byte aligned tensors and
- * rows, run on the tensor cores: few rows on the codes themselves, many rows on K and V
- * expanded to dtype in the workspace.  The weights (few rows: times the values' scale, in
- * bf16; many rows: in dtype) are then rounded for the second product.
+ *              fewer key splits, codes that each tile of rows expands for itself instead
+ *              of once for all, or the CUDA cores.
+ * 16-bit q runs on the tensor cores, given 16-byte aligned tensors and rows: up to 256 packed
+ * rows (tokens x heads of a kv head) of heads of 64 or 128 columns (dk == dv) on the codes
+ * themselves; more rows, and other heads of at most 128 columns, on K and V expanded in the
+ * workspace, K in two parts (16 bits of significand together in BF16, 22 in F16), V rounded to
+ * dtype.  Weights are rounded for the second product: to f16 with the values' scale (codes), or
+ * to dtype.  Everything else runs on the CUDA cores in f32.
  */
 idx_status dense_attn_q4(const void* q, idx_dtype dtype, int32_t n_q_heads, int32_t n_kv_heads, int32_t dk, int32_t dv,
                          const void* k_cache, int64_t k_row_stride, const void* v_cache, int64_t v_row_stride,

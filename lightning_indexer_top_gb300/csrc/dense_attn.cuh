@@ -26,6 +26,7 @@ struct DenseArgs {
                               // kDenseCluster splits), the splits are a cluster that merges them
     float* part_o;            // [row * Hq + head][split][dv] unnormalised
     float* part_ml;           // [row * Hq + head][split][2]: maximum (natural-log units), sum
+    const void* k_rest;       // or NULL.  Given (tensor cores): K is the sum of k and this, laid out alike
     const int* only_if;       // or NULL; given and 0 on the device: the launch has nothing to do (CUDA cores, 4 bits)
 };
 

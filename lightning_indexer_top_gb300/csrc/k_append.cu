@@ -334,11 +334,12 @@ cudaError_t run(const AppendArgs& a, const Geom& g, cudaStream_t st) {
 
 // ------------------------------------------------------------------------------------------- reading back
 
-// a thread per word of eight codes, or per piece of 32 (kWide)
-template <typename T, bool kWide>
-__global__ void __launch_bounds__(kThreads) read_q4_kernel(ReadArgs a, Geom g, int per_cta, int64_t n_rows) {
+// a thread per word of eight codes, or per piece of 32 (kWide); kExpand: for the attention (ExpandArgs)
+template <typename T, bool kWide, bool kExpand>
+__global__ void __launch_bounds__(kThreads) read_q4_kernel(ExpandArgs p, Geom g, int per_cta, int64_t n_rows) {
     __shared__ int64_t at[kThreads];
     constexpr int kCols = kWide ? 32 : 8;
+    const ReadArgs& a = p.r;
     const int tid = threadIdx.x;
     pdl_wait();
     const int64_t r0 = (int64_t)blockIdx.x * per_cta;
@@ -347,18 +348,19 @@ __global__ void __launch_bounds__(kThreads) read_q4_kernel(ReadArgs a, Geom g, i
         const int64_t r = r0 + tid;
         const int b = (int)(r / g.T), t = (int)(r - (int64_t)b * g.T);
         int64_t row = -1;
-        if (a.lost) {
-            if (t < seq_n_kv(g, b)) {
+        if (kExpand) {
+            const int2 span = p.span[b];
+            if (t >= span.x && t < span.y) {
                 row = key_row(g, b, t);
                 if (row < 0 || row >= a.kv_rows) {
-                    *a.lost = 1;
+                    *p.lost = 1;
                     row = -1;
                 }
             }
         } else {
-            int p;
+            int pos;
             bool flagged;
-            row = new_row(g, a.kv_rows, r, b, t, &p, &flagged);
+            row = new_row(g, a.kv_rows, r, b, t, &pos, &flagged);
             if (flagged) flag(g.status, IDX_ERR_DEVICE_BOUNDS);
         }
         at[tid] = row;
@@ -376,6 +378,7 @@ __global__ void __launch_bounds__(kThreads) read_q4_kernel(ReadArgs a, Geom g, i
         const uint8_t* src = is_k ? static_cast<const uint8_t*>(a.k_cache) + row * a.kc_stride
                                   : static_cast<const uint8_t*>(a.v_cache) + row * a.vc_stride;
         T* dst = (is_k ? static_cast<T*>(a.k_out) : static_cast<T*>(a.v_out)) + ((r0 + i) * a.Hkv * w + u * kCols);
+        T* rest = kExpand ? static_cast<T*>(p.k_rest) + (dst - static_cast<T*>(a.k_out)) : nullptr;
         const float* pair = reinterpret_cast<const float*>(src + a.Hkv * (w / 2)) + 2 * h;
         const float scale = pair[0], low = pair[1];
         uint32_t x[kCols / 8];
@@ -386,17 +389,22 @@ __global__ void __launch_bounds__(kThreads) read_q4_kernel(ReadArgs a, Geom g, i
         constexpr int E = 16 / (int)sizeof(T);
 #pragma unroll
         for (int c = 0; c < kCols; c += E) {
-            T y[E];
+            T y[E], z[E];
 #pragma unroll
-            for (int j = 0; j < E; ++j)
-                y[j] = from_f32<T>(fmaf((float)((x[(c + j) / 8] >> (4 * ((c + j) % 8))) & 15u), scale, low));
+            for (int j = 0; j < E; ++j) {
+                const float v = fmaf((float)((x[(c + j) / 8] >> (4 * ((c + j) % 8))) & 15u), scale, low);
+                y[j] = from_f32<T>(v);
+                if (kExpand) z[j] = from_f32<T>(v - to_f32(y[j]));
+            }
+            if (kExpand && is_k) *reinterpret_cast<uint4*>(rest + c) = *reinterpret_cast<const uint4*>(z);
             *reinterpret_cast<uint4*>(dst + c) = *reinterpret_cast<const uint4*>(y);
         }
     }
 }
 
-template <typename T>
-cudaError_t run_read(const ReadArgs& a, const Geom& g, cudaStream_t st) {
+template <typename T, bool kExpand>
+cudaError_t run_read(const ExpandArgs& p, const Geom& g, cudaStream_t st) {
+    const ReadArgs& a = p.r;
     const int64_t n = (int64_t)g.B * g.T;
     const uint64_t all = reinterpret_cast<uintptr_t>(a.k_cache) | reinterpret_cast<uintptr_t>(a.v_cache) | (uint64_t)a.kc_stride |
                          (a.v_cache ? (uint64_t)a.vc_stride : 0) | (uint64_t)(a.dk / 2) | (uint64_t)(a.dv / 2);
@@ -406,8 +414,8 @@ cudaError_t run_read(const ReadArgs& a, const Geom& g, cudaStream_t st) {
     while (per < kThreads && per_row * per < 2 * kThreads && n / per > 2 * 152) per *= 2;
     const int64_t ctas = (n + per - 1) / per;
     if (ctas > INT32_MAX) return cudaErrorNotSupported;
-    return wide ? launch_pdl(read_q4_kernel<T, true>, dim3((unsigned)ctas), dim3(kThreads), 0, st, a, g, per, n)
-                : launch_pdl(read_q4_kernel<T, false>, dim3((unsigned)ctas), dim3(kThreads), 0, st, a, g, per, n);
+    return wide ? launch_pdl(read_q4_kernel<T, true, kExpand>, dim3((unsigned)ctas), dim3(kThreads), 0, st, p, g, per, n)
+                : launch_pdl(read_q4_kernel<T, false, kExpand>, dim3((unsigned)ctas), dim3(kThreads), 0, st, p, g, per, n);
 }
 
 }  // namespace
@@ -421,11 +429,17 @@ cudaError_t launch_append(const AppendArgs& a, int dtype, bool q4, const Geom& g
 }
 
 cudaError_t launch_read_q4(const ReadArgs& a, int dtype, const Geom& g, cudaStream_t st) {
+    ExpandArgs p = {};
+    p.r = a;
     switch (dtype) {
-        case IDX_F16: return run_read<__half>(a, g, st);
-        case IDX_BF16: return run_read<__nv_bfloat16>(a, g, st);
-        default: return run_read<float>(a, g, st);
+        case IDX_F16: return run_read<__half, false>(p, g, st);
+        case IDX_BF16: return run_read<__nv_bfloat16, false>(p, g, st);
+        default: return run_read<float, false>(p, g, st);
     }
+}
+
+cudaError_t launch_expand_q4(const ExpandArgs& a, int dtype, const Geom& g, cudaStream_t st) {
+    return dtype == IDX_BF16 ? run_read<__nv_bfloat16, true>(a, g, st) : run_read<__half, true>(a, g, st);
 }
 
 }  // namespace lidx

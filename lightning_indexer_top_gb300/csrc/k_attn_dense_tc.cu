@@ -60,7 +60,8 @@ constexpr int kOtherWarps = 4;
 template <int D, bool kMods>
 constexpr bool kDoubleS = kMods || D == 64;
 
-template <int D, int kTiles>
+// kTwo (see the kernel): a key tile is two entries of K's ring
+template <int D, int kTiles, bool kTwo = false>
 struct Cfg {
     static constexpr int kTileBytes = kKeys * D * 2;
     // rows of Q kept per row tile.  With kFewRows the M = 128 products read on into the K tile: what they
@@ -68,8 +69,8 @@ struct Cfg {
     static constexpr int kQRows = kTiles == 2 ? kRows : kFewRows;
     static constexpr int kQTile = kQRows * D * 2;
     static constexpr int kQBlock = kQRows * 128;      // 64 columns of it
-    static constexpr int kStagesK = kTiles == 2 ? 2 : D == 64 ? 2 : 1;
-    static constexpr int kStagesV = kTiles == 2 ? 3 : D == 64 ? 3 : 2;
+    static constexpr int kStagesK = kTwo ? (kTiles == 2 || D == 64 ? 3 : 2) : kTiles == 2 ? 2 : D == 64 ? 2 : 1;
+    static constexpr int kStagesV = kTwo && D == 128 ? (kTiles == 2 ? 2 : 1) : kTiles == 2 ? 3 : D == 64 ? 3 : 2;
     static constexpr int kCtas = kTiles == 2 ? 1 : 2;   // (two: 128 registers; with options 28 to 40 bytes are spilled)
     static constexpr int kKOff = kTiles * kQTile;
     static constexpr int kVOff = kKOff + kStagesK * kTileBytes;
@@ -132,8 +133,9 @@ __device__ __noinline__ void scalar_row(const DenseArgs& a, const Geom& g, int b
         }
         const T* k = static_cast<const T*>(a.k) + row * a.k_stride + (int64_t)gkv * a.dk;
         const T* v = static_cast<const T*>(a.v) + row * a.v_stride + (int64_t)gkv * a.dv;
+        const T* rest = a.k_rest ? static_cast<const T*>(a.k_rest) + row * a.k_stride + (int64_t)gkv * a.dk : nullptr;
         float x = 0.f;
-        for (int c = 0; c < a.dk; ++c) x = fmaf(to_f32(q[c]), to_f32(k[c]), x);
+        for (int c = 0; c < a.dk; ++c) x = fmaf(to_f32(q[c]), to_f32(k[c]) + (rest ? to_f32(rest[c]) : 0.f), x);
         x *= a.scale;
         if (a.mods.softcap > 0.f) x = a.mods.softcap * tanhf(x / a.mods.softcap);
         if (a.mods.slopes) x -= a.mods.slopes[h] * fabsf((float)(iv.pos - j));
@@ -200,10 +202,13 @@ __device__ __forceinline__ void store_rows(E* out, int64_t at, int n_rows, const
     __syncwarp();
 }
 
-template <typename T, int D, int kTiles, bool kMods>
-__global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCtas)
-    dense_tc_kernel(TcArgs p, Geom g, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
-    using C = Cfg<D, kTiles>;
+// kTwo: K is the sum of two tensors of T, for keys that T alone does not hold (values of 4-bit codes): the scores are two
+// products into the same accumulators.
+template <typename T, int D, int kTiles, bool kMods, bool kTwo>
+__global__ void __launch_bounds__(Cfg<D, kTiles, kTwo>::kThreads, Cfg<D, kTiles, kTwo>::kCtas)
+    dense_tc_kernel(TcArgs p, Geom g, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                    const __grid_constant__ CUtensorMap rmap) {
+    using C = Cfg<D, kTiles, kTwo>;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr float kShift = kBf16 ? 0.f : 7.f;     // P is kept this much (log2) larger
     constexpr float kTop = kShift + 8.f;
@@ -357,8 +362,8 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
             // -------------------------------------------------- producer: a lane per (piece, 64 columns)
             const int pieces = kKeys / p.box;
             const int64_t row_base = g.page_table ? 0 : seq_row0(g, b);
-            int sent = 0;     // tiles whose loads were issued (K and V alike)
-            bool sent_v = true;
+            constexpr int kEntries = kTwo ? 2 : 1;     // of K's ring for a tile
+            int sent_k = 0, sent_v = 0;                // entries and tiles whose loads were issued
             auto load = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* bar, int j) {
                 if (lane == 0) mbar_arrive_expect_tx(bar, C::kTileBytes);
                 __syncwarp();
@@ -379,27 +384,28 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
                 }
             };
             for (int j = 0; j < n; ++j) {
-                const int sk = j % C::kStagesK, sv = j % C::kStagesV;
-                if (warp_aborted() || !warp_wait(&c.kempty[sk], (uint32_t)((j / C::kStagesK) & 1) ^ 1)) {
-                    give_up();
-                    break;
+                const int sv = j % C::kStagesV;
+                bool ok = true;
+#pragma unroll
+                for (int x = 0; ok && x < kEntries; ++x) {
+                    const int sk = sent_k % C::kStagesK;
+                    ok = !warp_aborted() && warp_wait(&c.kempty[sk], (uint32_t)((sent_k / C::kStagesK) & 1) ^ 1);
+                    if (!ok) break;
+                    load(x ? &rmap : &kmap, kt + sk * C::kTileBytes, &c.kfull[sk], j);
+                    ++sent_k;
                 }
-                load(&kmap, kt + sk * C::kTileBytes, &c.kfull[sk], j);
-                sent = j + 1;
-                sent_v = false;
-                if (warp_aborted() || !warp_wait(&c.vempty[sv], (uint32_t)((j / C::kStagesV) & 1) ^ 1)) {
+                if (!ok || warp_aborted() || !warp_wait(&c.vempty[sv], (uint32_t)((j / C::kStagesV) & 1) ^ 1)) {
                     give_up();
                     break;
                 }
                 load(&vmap, vt + sv * C::kTileBytes, &c.vfull[sv], j);
-                sent_v = true;
+                ++sent_v;
             }
             if (warp_aborted()) {
                 // no load may still be in flight when the CTA ends
-                for (int j = max(0, sent - C::kStagesK); j < sent; ++j)
+                for (int j = max(0, sent_k - C::kStagesK); j < sent_k; ++j)
                     warp_wait(&c.kfull[j % C::kStagesK], (uint32_t)((j / C::kStagesK) & 1));
-                const int nv = sent_v ? sent : sent - 1;
-                for (int j = max(0, nv - C::kStagesV); j < nv; ++j)
+                for (int j = max(0, sent_v - C::kStagesV); j < sent_v; ++j)
                     warp_wait(&c.vfull[j % C::kStagesV], (uint32_t)((j / C::kStagesV) & 1));
             }
         } else if (warp <= n_tiles) {
@@ -422,7 +428,9 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
             // S = Q K^T.  All D / 16 products run (columns past dk are zero): an unrolled chain that stopped at dk by
             // a run-time bound got a wrong last descriptor (nvcc 13.0; the basis-vector test shows it)
             auto qk = [&](int half) {
+                const int s2 = kTwo ? (sk + 1 == C::kStagesK ? 0 : sk + 1) : sk;      // the second entry
                 const uint32_t ka = __shfl_sync(0xffffffffu, kb + ((sk * C::kTileBytes + half * (kHalf * 128)) >> 4), 0);
+                const uint32_t kr = __shfl_sync(0xffffffffu, kb + ((s2 * C::kTileBytes + half * (kHalf * 128)) >> 4), 0);
                 const uint32_t d = __shfl_sync(0xffffffffu, ts + half * kHalf, 0);
                 const bool last = !kDouble || half == 1;      // of the K tile
                 tc_fence_after();
@@ -431,14 +439,30 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
                     for (int ks = 0; ks < D / 16; ++ks)
                         mma_f16_ss_lo(d, qa + (((ks >> 2) * C::kQBlock + (ks & 3) * 32) >> 4), k_hi,
                                       ka + (((ks >> 2) * kColBlock + (ks & 3) * 32) >> 4), k_hi, id_qk, ks > 0 ? 1u : 0u);
+                    if constexpr (kTwo) {
+                        if (last) mma_commit(&c.kempty[sk]);
+#pragma unroll
+                        for (int ks = 0; ks < D / 16; ++ks)
+                            mma_f16_ss_lo(d, qa + (((ks >> 2) * C::kQBlock + (ks & 3) * 32) >> 4), k_hi,
+                                          kr + (((ks >> 2) * kColBlock + (ks & 3) * 32) >> 4), k_hi, id_qk, 1u);
+                    }
                     mma_commit(&c.sfull[i][half]);
-                    if (last) mma_commit(&c.kempty[sk]);
+                    if (last) mma_commit(&c.kempty[s2]);
                 }
                 __syncwarp();
-                if (last && ++sk == C::kStagesK) {
-                    sk = 0;
-                    kph ^= 1;
-                }
+                if (last)
+                    for (int x = 0; x < (kTwo ? 2 : 1); ++x)
+                        if (++sk == C::kStagesK) {
+                            sk = 0;
+                            kph ^= 1;
+                        }
+            };
+            // the K tile to use next is there
+            auto wait_k = [&] {
+                bool there = warp_wait(&c.kfull[sk], (uint32_t)kph);
+                if (kTwo) there = there && (sk + 1 == C::kStagesK ? warp_wait(&c.kfull[0], (uint32_t)kph ^ 1)
+                                                                  : warp_wait(&c.kfull[sk + 1], (uint32_t)kph));
+                return there;
             };
             // O += P V of half a tile, and the commits that follow it
             auto pv = [&](int half, uint32_t first, uint64_t* b0, uint64_t* b1) {
@@ -455,7 +479,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
                 }
                 __syncwarp();
             };
-            ok = warp_wait(&c.kfull[0], 0u);
+            ok = wait_k();
             if (ok) {
                 qk(0);
                 if (kDouble) qk(1);
@@ -470,13 +494,13 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
                 if (kDouble) {
                     pv(0, j == 0, last ? &c.sfull[i][0] : nullptr, nullptr);
                     if (!last) {
-                        ok = warp_wait(&c.kfull[sk], (uint32_t)kph);
+                        ok = wait_k();
                         if (!ok) break;
                         qk(0);
                     }
                 } else {
                     pv(0, j == 0, &c.pvdone[i], nullptr);
-                    ok = last || warp_wait(&c.kfull[sk], (uint32_t)kph);
+                    ok = last || wait_k();
                 }
                 ok = ok && warp_wait(&c.pready[i][1], (uint32_t)(j & 1));
                 if (!ok) break;
@@ -761,41 +785,43 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, Cfg<D, kTiles>::kCta
 // row tiles per CTA
 int row_tiles(int64_t packed) { return packed > kFewRows ? 2 : 1; }
 
-template <typename T, int D, int kTiles, bool kMods>
-cudaError_t go(const TcArgs& p, const Geom& g, const CUtensorMap& km, const CUtensorMap& vm, int64_t grid,
-               cudaStream_t st) {
-    using C = Cfg<D, kTiles>;
+template <typename T, int D, int kTiles, bool kMods, bool kTwo>
+cudaError_t go(const TcArgs& p, const Geom& g, const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& rm,
+               int64_t grid, cudaStream_t st) {
+    using C = Cfg<D, kTiles, kTwo>;
     constexpr size_t sm = 1024 + (size_t)C::kCtlOff + sizeof(Ctl);
     static_assert((sm + 1024) * C::kCtas <= 233472, "shared memory of an SM");
-    auto kern = dense_tc_kernel<T, D, kTiles, kMods>;
+    auto kern = dense_tc_kernel<T, D, kTiles, kMods, kTwo>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
     if (e != cudaSuccess) return e;
     return launch_pdl_cluster(kern, dim3((unsigned)grid), dim3(C::kThreads), sm, st,
-                              p.a.splits > 1 && !p.a.part_o ? p.a.splits : 1, p, g, km, vm);
+                              p.a.splits > 1 && !p.a.part_o ? p.a.splits : 1, p, g, km, vm, rm);
 }
 
-template <typename T>
+template <typename T, bool kTwo>
 cudaError_t run(const DenseArgs& a, const Geom& g, cudaStream_t st) {
     const int64_t packed = (int64_t)g.T * (a.Hq / a.Hkv);
     const int tiles = row_tiles(packed);
     TcArgs p = {a, (int)((packed + tiles * kRows - 1) / (tiles * kRows)), box_rows(g.page_size, kKeys)};
     const int64_t grid = (int64_t)g.B * a.Hkv * p.tiles * a.splits;
     if (grid > INT32_MAX) return cudaErrorNotSupported;
-    CUtensorMap km, vm;
+    CUtensorMap km, vm, rm;
     constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
     if (!make_head_tmap(&km, a.k, bf16, a.dk, a.Hkv, a.k_stride, a.kv_rows, p.box) ||
         !make_head_tmap(&vm, a.v, bf16, a.dv, a.Hkv, a.v_stride, a.kv_rows, p.box))
         return cudaErrorNotSupported;
+    rm = km;
+    if (kTwo && !make_head_tmap(&rm, a.k_rest, bf16, a.dk, a.Hkv, a.k_stride, a.kv_rows, p.box)) return cudaErrorNotSupported;
     const bool small = a.dk <= 64 && a.dv <= 64;
     const bool mods = a.mods.softcap > 0.f || a.mods.slopes || a.scale <= 0.f;
     if (small) {
         if (tiles == 1)
-            return mods ? go<T, 64, 1, true>(p, g, km, vm, grid, st) : go<T, 64, 1, false>(p, g, km, vm, grid, st);
-        return mods ? go<T, 64, 2, true>(p, g, km, vm, grid, st) : go<T, 64, 2, false>(p, g, km, vm, grid, st);
+            return mods ? go<T, 64, 1, true, kTwo>(p, g, km, vm, rm, grid, st) : go<T, 64, 1, false, kTwo>(p, g, km, vm, rm, grid, st);
+        return mods ? go<T, 64, 2, true, kTwo>(p, g, km, vm, rm, grid, st) : go<T, 64, 2, false, kTwo>(p, g, km, vm, rm, grid, st);
     }
     if (tiles == 1)
-        return mods ? go<T, 128, 1, true>(p, g, km, vm, grid, st) : go<T, 128, 1, false>(p, g, km, vm, grid, st);
-    return mods ? go<T, 128, 2, true>(p, g, km, vm, grid, st) : go<T, 128, 2, false>(p, g, km, vm, grid, st);
+        return mods ? go<T, 128, 1, true, kTwo>(p, g, km, vm, rm, grid, st) : go<T, 128, 1, false, kTwo>(p, g, km, vm, rm, grid, st);
+    return mods ? go<T, 128, 2, true, kTwo>(p, g, km, vm, rm, grid, st) : go<T, 128, 2, false, kTwo>(p, g, km, vm, rm, grid, st);
 }
 
 }  // namespace
@@ -827,7 +853,8 @@ int dense_tc_splits(int64_t n_seq, int64_t n_q, int64_t max_n_kv, int Hq, int Hk
 }
 
 cudaError_t launch_dense_tc(const DenseArgs& a, int dtype, const Geom& g, cudaStream_t st) {
-    return dtype == IDX_BF16 ? run<__nv_bfloat16>(a, g, st) : run<__half>(a, g, st);
+    if (a.k_rest) return dtype == IDX_BF16 ? run<__nv_bfloat16, true>(a, g, st) : run<__half, true>(a, g, st);
+    return dtype == IDX_BF16 ? run<__nv_bfloat16, false>(a, g, st) : run<__half, false>(a, g, st);
 }
 
 }  // namespace lidx

@@ -249,6 +249,10 @@ bool make_w_tmap(CUtensorMap* m, const float* w, int64_t rows);
 bool make_key8_tmap(CUtensorMap* m, const int8_t* k, int64_t row_bytes, int64_t k_rows, int box_rows,
                     int payload, bool swizzle128 = false);
 
+// [rows, heads, inner] bytes of a 4-bit cache: boxes of box_inner bytes of one head x box_rows rows
+bool make_q4_tmap(CUtensorMap* m, const void* x, int inner, int heads, int64_t head_stride, int64_t row_stride, int64_t rows,
+                  int box_inner, int box_rows, bool swizzle64);
+
 // number of SMs of the current device (cached per device)
 int sm_count();
 

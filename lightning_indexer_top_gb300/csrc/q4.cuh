@@ -29,11 +29,21 @@ struct ReadArgs {
     int32_t Hkv, dk, dv;
     void* k_out;
     void* v_out;
-    int* lost;                       // or NULL.  Given: row t of a sequence is position t, rows whose cache row is out of
-                                     // range set it instead of the device status
 };
 
 cudaError_t launch_read_q4(const ReadArgs& a, int dtype, const Geom& g, cudaStream_t st);
+
+// The positions of each sequence's span (device, [lo, hi)) for the attention: the values of K and V in dtype, row b * g.T +
+// position, and in k_rest what K's lack of their f32.  A position whose cache row is out of range sets *lost, in place of the
+// device status.
+struct ExpandArgs {
+    ReadArgs r;
+    const int2* span;
+    int* lost;
+    void* k_rest;
+};
+
+cudaError_t launch_expand_q4(const ExpandArgs& a, int dtype, const Geom& g, cudaStream_t st);
 
 // dense_attn_q4 of checked arguments (k and v of a: bytes, strides in bytes)
 cudaError_t launch_attn_q4(DenseArgs a, int dtype, const Geom& g, void* ws, size_t ws_bytes, cudaStream_t st);

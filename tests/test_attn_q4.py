@@ -4,11 +4,12 @@ Tolerance of an output element, with u = 2^-24, half(T) = finfo(T).eps / 2, code
 that a value is s (n - 8) + m':
   scores   sums of dk terms in f32, either of q (s n + m) or as s sum q (n - 8) + m' sum q: off by at most (dk + 6) u A, where
            A = sum |q| (s |n - 8| + |m'|) (in which q's rounding to f16 at its row's scale, 2^-25 of its largest element, is
-           counted too); scaling, cap, bias and maximum 8 u (|x| + cap + slope * distance + 1): dx;
-           many rows of 16-bit inputs: K is rounded to their type first, half(T) sum |q k| more;
-  weights  off by a factor within e^(2 dx) (1 + 2^-20), and on the tensor cores by half a step of bf16 (few rows: the weight
-           times the value's scale) or of the inputs' type (many rows);
-  values   many rows of 16-bit inputs: half(T) of each;
+           counted too; an odd column's code is taken as 72 too much, which is taken off again: (dk + 6) u 72 sum |q| s more);
+           many rows, or other heads: K is a sum of two numbers of the inputs' type, half(T)^2 sum |q k| more;
+           scaling, cap, bias and maximum 8 u (|x| + cap + slope * distance + 1): dx;
+  weights  off by a factor within e^(2 dx) (1 + 2^-20), and on the tensor cores by half a step of the type they are rounded to
+           for the second product: f16 of the weight times the value's scale (few rows of 64 or 128 columns), the inputs' type;
+  values   16-bit inputs otherwise: half(T) of each;
   sums     n f32 additions: n u of the sum of magnitudes, S = sum p (s |n - 8| + |m'|).
 |error| <= 2 (2 dx + n u + 2^-20 + rounded weights and values) S + half(T) |out|.  lse: dx + n u + 2^-20 + u |lse|."""
 
@@ -90,9 +91,9 @@ class Case4(Case):
     def reference(self):
         B, T, Hq, dk = self.q.shape
         G = Hq // self.Hkv
-        half16 = 0.0 if self.dtype == torch.float32 else half(torch.bfloat16)
-        many = self.dtype != torch.float32 and T * G > 16        # (either way's tolerance then)
-        wide = half(self.dtype) if many else 0.0
+        small = self.dtype == torch.float32
+        codes = not small and T * G <= 256 and dk == self.dv and dk in (64, 128)      # (the codes themselves may be multiplied)
+        rounded = 0.0 if small else half(torch.float16) if codes and T * G <= 16 else 2 * half(self.dtype)
         out = torch.zeros(B, T, Hq, self.dv, dtype=torch.float64)
         lse = torch.full((B, T, Hq), -math.inf, dtype=torch.float64)
         tol, tol_lse = torch.zeros_like(out), torch.zeros_like(lse)
@@ -111,7 +112,8 @@ class Case4(Case):
                 k, v = kc * ks[..., None] + km[..., None], vc * vs[..., None] + vm[..., None]
                 x = torch.einsum("hd,nhd->hn", qq, k) * self.scale
                 A = torch.einsum("hd,nhd->hn", qq.abs(), (kc - 8).abs() * ks[..., None] + (km + 8 * ks).abs()[..., None]) * abs(self.scale)
-                K = torch.einsum("hd,nhd->hn", qq.abs(), k.abs()) * abs(self.scale)
+                if codes:
+                    A = A + 72 * torch.einsum("hd,nh->hn", qq.abs(), ks) * abs(self.scale)
                 size = x.abs() + 1
                 if self.cap:
                     x = self.cap * torch.tanh(x / self.cap)
@@ -120,13 +122,15 @@ class Case4(Case):
                     dist = (int(self.pos[b, t]) - torch.nonzero(self.rows[b][l:h] >= 0)[:, 0] - l).abs().double()
                     x = x - self.slopes.double()[:, None] * dist
                     size = size + self.slopes.double()[:, None] * dist
-                dx = ((dk + 6) * U * A + 8 * U * size + wide * K).amax(1, keepdim=True)
+                if not small:
+                    A = A + half(self.dtype) ** 2 / U / (dk + 6) * torch.einsum("hd,nhd->hn", qq.abs(), k.abs()) * abs(self.scale)
+                dx = ((dk + 6) * U * A + 8 * U * size).amax(1, keepdim=True)
                 lse[b, t] = torch.logsumexp(x, 1)
                 p = torch.softmax(x, 1)
                 out[b, t] = torch.einsum("hn,nhd->hd", p, v)
                 S = torch.einsum("hn,nhd->hd", p, (vc - 8).abs() * vs[..., None] + (vm + 8 * vs).abs()[..., None])
                 n = h - l
-                tol[b, t] = 2 * (2 * dx + n * U + 2.0 ** -20 + half16 + 2 * wide) * S + half(self.dtype) * out[b, t].abs() + 1e-30
+                tol[b, t] = 2 * (2 * dx + n * U + 2.0 ** -20 + rounded) * S + half(self.dtype) * out[b, t].abs() + 1e-30
                 tol_lse[b, t] = dx[:, 0] + n * U + 2.0 ** -20 + U * lse[b, t].abs()
         return out, lse, tol, tol_lse
 
@@ -176,7 +180,7 @@ def test_every_column_counts_once(dtype, d, T):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("T", [2, 5, 17, 100])
+@pytest.mark.parametrize("T", [2, 5, 17, 100, 140])
 @pytest.mark.parametrize("heads", [(4, 1, 32), (8, 2, 64), (16, 2, 128), (6, 1, 72), (4, 4, 128)])
 @pytest.mark.parametrize("page", [0, 32, 3])
 def test_chunks(dtype, T, heads, page):
