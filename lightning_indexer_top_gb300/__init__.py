@@ -256,14 +256,18 @@ class Batch:
         return self.n_seq * self.n_q_per_seq
 
     def c(self) -> _Batch:
+        n_kv, table, i32 = self.n_kv, self.page_table, torch.int32
         ptrs = []
-        for t in (self.n_kv, self.kv_start, self.q_pos, self.page_table):
-            if t is not None and (t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous()):
+        for t in (n_kv, self.kv_start, self.q_pos, table):
+            if t is None:
+                ptrs.append(None)
+                continue
+            if t.dtype is not i32 or not t.is_cuda or not t.is_contiguous():
                 raise ValueError("batch arrays must be contiguous int32 CUDA tensors")
-            ptrs.append(None if t is None else t.data_ptr())
-        pt_stride = self.page_table.shape[-1] if self.page_table is not None else 0
-        return _Batch(self.n_seq, self.n_q_per_seq, ptrs[0], ptrs[1], self.kv_seq_stride, ptrs[2], self.max_n_kv,
-                      ptrs[3], pt_stride, self.page_size if self.page_table is not None else 0)
+            ptrs.append(t.data_ptr())
+        stride, size = (0, 0) if table is None else (table.shape[-1], self.page_size)
+        return _Batch(n_kv.numel(), self.n_q_per_seq, ptrs[0], ptrs[1], self.kv_seq_stride, ptrs[2], self.max_n_kv,
+                      ptrs[3], stride, size)
 
 
 IDX_DEFAULT_TOP_K = 2048   # top_k = -1: the model's configured indexer top_k
@@ -574,11 +578,17 @@ def sparse_attn_decode_noalloc(q, latent, batch, idx, n_sel, scale, *, out=None,
     return out
 
 
+# the current device without the checks around it (1 us less a call; tensors on a device mean that CUDA is up)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 class _On:
     """Makes `device` current for a call."""
 
+    __slots__ = ("prev", "idx")
+
     def __init__(self, device):
-        self.prev, self.idx = torch.cuda.current_device(), device.index
+        self.prev, self.idx = _raw_device(), device.index
 
     def __enter__(self):
         if self.prev != self.idx:
@@ -866,25 +876,42 @@ def idx_q4_row_bytes(n_heads: int, d: int) -> int:
 
 def _new_rows(name: str, t: torch.Tensor, rows: int):
     """(address, row stride, heads, columns) of [rows, heads, columns] whose rows may lie apart."""
-    if t.dim() != 3 or t.shape[0] != rows:
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != rows:
         raise ValueError(f"{name} must be a [n_seq * n_q_per_seq, heads, columns] tensor")
-    _, h, d = t.shape
+    _, h, d = shape
     s0, s1, s2 = t.stride()
-    if (d > 1 and s2 != 1) or (h > 1 and s1 != d):
+    width = h * d
+    if (s2 != 1 and d > 1) or (s1 != d and h > 1):
         raise ValueError(f"the heads of a row of {name} must be contiguous")
-    if rows > 1 and s0 < h * d:
-        raise ValueError(f"the rows of {name} must not overlap")
-    return t.data_ptr(), max(s0, h * d), h, d
+    if s0 < width:
+        if rows > 1:
+            raise ValueError(f"the rows of {name} must not overlap")
+        s0 = width
+    return t.data_ptr(), s0, h, d
 
 
 def _q4_cache(name: str, t: torch.Tensor, heads: int, d: int):
     """(address, row stride) of a 4-bit cache."""
-    if t.dtype is not torch.uint8 or t.dim() != 2 or t.shape[1] < heads * (d // 2 + 8) or (t.shape[1] > 1 and t.stride(1) != 1):
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not torch.uint8 or len(shape) != 2 or shape[1] < heads * (d // 2 + 8) or stride[1] != 1:
         raise ValueError(f"{name} must be a uint8 [rows, idx_q4_row_bytes(heads, columns)] tensor with contiguous rows")
-    s = t.stride(0)
-    if t.shape[0] > 1 and s < t.shape[1]:
-        raise ValueError(f"the rows of {name} must not overlap")
-    return t.data_ptr(), max(s, t.shape[1])
+    s = stride[0]
+    if s < shape[1]:
+        if shape[0] > 1:
+            raise ValueError(f"the rows of {name} must not overlap")
+        s = shape[1]
+    return t.data_ptr(), s
+
+
+def _cache_rows(name: str, c: torch.Tensor, n: int, heads: int, d: int, dtype):
+    """(address, row stride) of a cache of rows of heads x d elements."""
+    if heads == 1 and c.dim() == 2:
+        c = c[:, None]
+    ptr, stride, h, w = _new_rows(name, c, n)
+    if h != heads or w != d or c.dtype is not dtype:
+        raise ValueError(f"{name} must be a [rows, heads, columns] tensor of the new rows' heads and dtype")
+    return ptr, stride
 
 
 def _append(fn, q4: bool, k, v, k_cache, v_cache, batch, q, q_out, inv_freq, rot_start, interleaved):
@@ -911,29 +938,26 @@ def _append(fn, q4: bool, k, v, k_cache, v_cache, batch, q, q_out, inv_freq, rot
             raise ValueError("q and k must have the same columns and dtype")
         if q_out is None:
             q_out = torch.empty((rows, hq, dk), device=dev, dtype=q.dtype)
-        qo_ptr, qo_stride, ho, do = _new_rows("q_out", q_out, rows)
-        if (ho, do) != (hq, dk) or q_out.dtype is not q.dtype:
-            raise ValueError("q_out must have q's shape and dtype")
+            qo_ptr, qo_stride = q_out.data_ptr(), hq * dk
+        else:
+            qo_ptr, qo_stride, ho, do = _new_rows("q_out", q_out, rows)
+            if (ho, do) != (hq, dk) or q_out.dtype is not q.dtype:
+                raise ValueError("q_out must have q's shape and dtype")
     elif q_out is not None:
         raise ValueError("q_out without q")
+    n = k_cache.shape[0]
+    vc_ptr, vc_stride = None, 0
     if q4:
         if dk % 8 or dv % 8:
             raise ValueError("the heads of a 4-bit cache have a multiple of 8 columns")
         kc_ptr, kc_stride = _q4_cache("k_cache", k_cache, hkv, dk)
-        vc_ptr, vc_stride = (None, 0) if v is None else _q4_cache("v_cache", v_cache, hkv, dv)
+        if v is not None:
+            vc_ptr, vc_stride = _q4_cache("v_cache", v_cache, hkv, dv)
     else:
-        caches = []
-        for name, c, d in (("k_cache", k_cache, dk), ("v_cache", v_cache, dv)):
-            if c is None:
-                caches.append((None, 0))
-                continue
-            if c.dim() == 2 and hkv == 1:
-                c = c[:, None]
-            if c.dim() != 3 or c.shape[1:] != (hkv, d) or c.dtype is not k.dtype:
-                raise ValueError(f"{name} must be a [rows, heads, columns] tensor of the new rows' heads and dtype")
-            caches.append(_new_rows(name, c, c.shape[0])[:2])
-        (kc_ptr, kc_stride), (vc_ptr, vc_stride) = caches
-    if v_cache is not None and v_cache.shape[0] != k_cache.shape[0]:
+        kc_ptr, kc_stride = _cache_rows("k_cache", k_cache, n, hkv, dk, k.dtype)
+        if v is not None:
+            vc_ptr, vc_stride = _cache_rows("v_cache", v_cache, v_cache.shape[0], hkv, dv, k.dtype)
+    if v is not None and v_cache.shape[0] != n:
         raise ValueError("k_cache and v_cache must have the same rows")
     rope = None
     if inv_freq is not None:
@@ -942,7 +966,7 @@ def _append(fn, q4: bool, k, v, k_cache, v_cache, batch, q, q_out, inv_freq, rot
         rope = _Rope(inv_freq.data_ptr(), 2 * inv_freq.numel(), rot_start, 1 if interleaved else 0)
     with _On(dev):
         _check(fn(_NewRows(k_ptr, k_stride, v_ptr, v_stride, q_ptr, q_stride, qo_ptr, qo_stride), dt, hq, hkv, dk, dv, b,
-                  rope, kc_ptr, kc_stride, vc_ptr, vc_stride, k_cache.shape[0], _stream(dev)))
+                  rope, kc_ptr, kc_stride, vc_ptr, vc_stride, n, _stream(dev)))
     return q_out
 
 
@@ -1108,13 +1132,16 @@ def idx_beam_step(logits: torch.Tensor, scores: torch.Tensor, n_beams: int, *, n
         raise ValueError("lengths and history come together")
     new = n_seq * n_out
     if out is None:
-        f = torch.empty((4, new), device=dev, dtype=torch.int32)
-        out = BeamStep(f[0].view(torch.float32), f[1], f[2], torch.empty(new, device=dev, dtype=torch.uint8),
-                       None if lengths is None else f[3], history_out)
-    for name, t, d in (("scores", out.scores, torch.float32), ("parent", out.parent, torch.int32),
-                       ("token", out.token, torch.int32), ("done", out.done, torch.uint8)):
-        if t.dtype is not d or t.numel() != new or not t.is_contiguous():
-            raise ValueError(f"out.{name} must be a contiguous {d} tensor with n_out entries for each sequence")
+        value, parent, token, length = torch.empty((4, max(new, 0)), device=dev, dtype=torch.int32).unbind(0)
+        out = BeamStep(value.view(torch.float32), parent, token, torch.empty(max(new, 0), device=dev, dtype=torch.uint8),
+                       None if lengths is None else length, history_out)
+    elif history_out is not None:
+        raise ValueError("history_out is out.history where out is given")
+    else:
+        for name, t, d in (("scores", out.scores, torch.float32), ("parent", out.parent, torch.int32),
+                           ("token", out.token, torch.int32), ("done", out.done, torch.uint8)):
+            if t.dtype is not d or t.numel() != new or not t.is_contiguous():
+                raise ValueError(f"out.{name} must be a contiguous {d} tensor with n_out entries for each sequence")
     cols = h_stride = o_stride = 0
     l_ptr = h_ptr = lo_ptr = ho_ptr = None
     if history is not None:
@@ -1128,7 +1155,7 @@ def idx_beam_step(logits: torch.Tensor, scores: torch.Tensor, n_beams: int, *, n
             raise ValueError("history must have one row per row of logits, history_out n_out for each sequence, of its width")
         l_ptr, lo_ptr = _i32("lengths", lengths, rows), _i32("out.lengths", out.lengths, new)
         # (an empty tensor has no address)
-        h_ptr, ho_ptr, lo_ptr = h_ptr or l_ptr, ho_ptr or lo_ptr, lo_ptr
+        h_ptr, ho_ptr = h_ptr or l_ptr, ho_ptr or lo_ptr
     lib = load()
     with _On(dev):
         if workspace is None:

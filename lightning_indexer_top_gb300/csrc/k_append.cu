@@ -21,14 +21,29 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxTokens = 8;      // per CTA
+constexpr int kMaxTokens = 16;     // per CTA
+constexpr int kMaxCs = 2048;       // pairs of cosine and sine per CTA
 constexpr int kMaxD = 576;
 
-// phase of position p in turns of 2^64
+// Phase of position p in turns of 2^64: the fraction of f / 2 pi, times p.  In whole numbers: f = m 2^e with |m| < 2^24, and
+// 1 / 2 pi to 96 bits, good to 2^-64 of a turn for |f| < 2^24 (64-bit floats, which are scarce here, beyond).
 __device__ __forceinline__ uint64_t phase(float f, int p) {
-    const double turns = (double)f * 0.15915494309189533577;     // 1 / 2 pi
-    const double part = turns - floor(turns);
-    return (uint64_t)(part * 18446744073709551616.0) * (uint64_t)(uint32_t)p;     // (a part of 1 saturates)
+    const uint32_t bits = __float_as_uint(f);
+    const int e = max((int)(bits >> 23 & 255u), 1) - 150;            // f = m 2^e
+    const uint64_t m = (bits & 0x7fffffu) | (bits & 0x7f800000u ? 0x800000u : 0u);
+    uint64_t u;
+    if (e <= 0) {
+        // m * (2^96 / 2 pi): bits 0 .. 63 and 64 .. 127
+        const uint64_t p0 = m * 0x7f09d5f4u, p1 = m * 0x9391054au + (p0 >> 32), p2 = m * 0x28be60dbu + (p1 >> 32);
+        const uint64_t low = p1 << 32 | (uint32_t)p0;
+        const int s = 32 - e;                                        // the fraction's top 64 bits: from bit s on
+        u = s < 64 ? (s ? p2 << (64 - s) : 0) | low >> s : s < 128 ? p2 >> (s - 64) : 0;
+        if (bits >> 31) u = 0 - u;
+    } else {
+        const double turns = (double)f * 0.15915494309189533577;     // 1 / 2 pi
+        u = (uint64_t)((turns - floor(turns)) * 18446744073709551616.0);     // (a fraction of 1 saturates)
+    }
+    return u * (uint64_t)(uint32_t)p;
 }
 
 __device__ __forceinline__ float2 cos_sin(float f, int p) {
@@ -68,44 +83,61 @@ struct Token {
     int pos;          // < 0: padding
 };
 
+// A thread's piece of work: one piece of E columns, or two that are turned together.
+template <typename T>
+struct Unit {
+    const T* src;          // NULL: nothing
+    T* dst;
+    const float2* cs;      // NULL: as it is
+    int apart;             // the second piece, 0: none
+};
+
 // Unit u of a head row of w columns (rot: rotated): with the pairs apart, first the n_rot / 2 / E pairs of pieces, then the
 // columns that stay; with the pairs side by side, pieces of E columns.
 template <typename T, int E, bool kInter>
-__device__ __forceinline__ void head_unit(const AppendArgs& a, const T* src, T* dst, int u, bool rot, const float2* cs) {
+__device__ __forceinline__ Unit<T> head_unit(const AppendArgs& a, const T* src, T* dst, int u, bool rot, const float2* cs) {
     const int n = rot ? a.n_rot : 0;
+    int c;
+    Unit<T> x = {src, dst, nullptr, 0};
     if (kInter && E > 1) {
-        const int c = u * E;
-        Piece<T, E> v = load<T, E>(src + c);
-        if (c >= a.start && c < a.start + n) {
-            const float2* t = cs + (c - a.start) / 2;
+        c = u * E;
+        if (c >= a.start && c < a.start + n) x.cs = cs + (c - a.start) / 2;
+    } else if (u < n / (2 * E)) {
+        c = kInter ? a.start + 2 * u : a.start + u * E;
+        x.cs = cs + u * E;
+        x.apart = kInter ? 1 : n / 2;
+    } else {
+        c = (u - n / (2 * E)) * E;
+        if (c >= a.start) c += n;
+    }
+    x.src += c;
+    x.dst += c;
+    return x;
+}
+
+template <typename T, int E, bool kInter>
+__device__ __forceinline__ void finish(const Unit<T>& x, Piece<T, E>& v, Piece<T, E>& w) {
+    if (x.cs) {
+        if (kInter && E > 1) {
 #pragma unroll
             for (int i = 0; i < E / 2; ++i) {
-                const float x = to_f32(v.x[2 * i]), y = to_f32(v.x[2 * i + 1]);
-                v.x[2 * i] = from_f32<T>(fmaf(x, t[i].x, -(y * t[i].y)));
-                v.x[2 * i + 1] = from_f32<T>(fmaf(y, t[i].x, x * t[i].y));
+                const float2 t = x.cs[i];
+                const float y = to_f32(v.x[2 * i]), z = to_f32(v.x[2 * i + 1]);
+                v.x[2 * i] = from_f32<T>(fmaf(y, t.x, -(z * t.y)));
+                v.x[2 * i + 1] = from_f32<T>(fmaf(z, t.x, y * t.y));
             }
-        }
-        store<T, E>(dst + c, v);
-        return;
-    }
-    const int pairs = n / (2 * E);
-    if (u < pairs) {
-        const int c0 = kInter ? a.start + 2 * u : a.start + u * E, c1 = kInter ? c0 + 1 : c0 + n / 2;
-        Piece<T, E> v = load<T, E>(src + c0), w = load<T, E>(src + c1);
+        } else {
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const float2 t = cs[u * E + i];
-            const float x = to_f32(v.x[i]), y = to_f32(w.x[i]);
-            v.x[i] = from_f32<T>(fmaf(x, t.x, -(y * t.y)));
-            w.x[i] = from_f32<T>(fmaf(y, t.x, x * t.y));
+            for (int i = 0; i < E; ++i) {
+                const float2 t = x.cs[i];
+                const float y = to_f32(v.x[i]), z = to_f32(w.x[i]);
+                v.x[i] = from_f32<T>(fmaf(y, t.x, -(z * t.y)));
+                w.x[i] = from_f32<T>(fmaf(z, t.x, y * t.y));
+            }
+            store<T, E>(x.dst + x.apart, w);
         }
-        store<T, E>(dst + c0, v);
-        store<T, E>(dst + c1, w);
-    } else {
-        int c = (u - pairs) * E;
-        if (c >= a.start) c += n;
-        store<T, E>(dst + c, load<T, E>(src + c));
     }
+    store<T, E>(x.dst, v);
 }
 
 // units of a head row of w columns
@@ -118,7 +150,7 @@ __device__ __forceinline__ int head_units(const AppendArgs& a, int w, bool rot) 
 
 // column c of a head row after the rotation in 64 bits
 template <typename T>
-__device__ __forceinline__ double exact_column(const AppendArgs& a, const T* src, int c, bool rot, int p) {
+__device__ __noinline__ double exact_column(const AppendArgs& a, const T* src, int c, bool rot, int p) {
     const double x = (double)to_f32(src[c]);
     if (!rot || p < 0 || c < a.start || c >= a.start + a.n_rot) return x;
     const int i = c - a.start, half = a.n_rot / 2;
@@ -130,11 +162,78 @@ __device__ __forceinline__ double exact_column(const AppendArgs& a, const T* src
     return second ? x * co + y * s : x * co - y * s;
 }
 
-// A warp's head row of w columns into 4 bits at `codes` and `pair`.
-// Rotated in f32 a column is off by at most 1.25 * 2^-22 of its pair's |u| + |w| (the angle by pi * 2^-25, cosine and sine by
-// an ulp, three roundings), so t = 15 (x - min) / (max - min) by at most 60 such errors over max - min, and 15 * 2^-22 for
-// its own roundings.  A row with a column that lies nearer than that to a border between codes is done again in 64 bits
-// (one head row of 128 in about 200).
+// A warp's head row of w columns into 4 bits at `codes` and `pair`, in 64 bits (buf: w floats of shared memory).
+template <typename T>
+__device__ __noinline__ void exact_row(const AppendArgs& a, const T* src, int w, bool rot, int p, float* buf, uint8_t* codes, float* pair) {
+    const int lane = threadIdx.x & 31;
+    double lo = INFINITY, hi = -INFINITY;
+    bool fine = true;
+    for (int c = lane; c < w; c += 32) {
+        fine &= fabsf(to_f32(src[c])) <= FLT_MAX;
+        const double y = exact_column(a, src, c, rot, p);
+        lo = fmin(lo, y);
+        hi = fmax(hi, y);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        lo = fmin(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = fmax(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+    fine = __all_sync(0xffffffffu, fine);
+    const double span = hi - lo;
+    for (int c = lane; c < w; c += 32)
+        buf[c] = fine && span > 0.0 ? (float)rint((exact_column(a, src, c, rot, p) - lo) * 15.0 / span) : 0.f;
+    __syncwarp();
+    for (int word = lane; word < w / 8; word += 32) {
+        uint32_t x = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x |= (uint32_t)(int)buf[word * 8 + i] << (4 * i);
+        reinterpret_cast<uint32_t*>(codes)[word] = x;
+    }
+    if (lane == 0) {
+        pair[0] = fine ? (float)(span / 15.0) : __int_as_float(0x7fc00000);
+        pair[1] = fine ? (float)lo : __int_as_float(0x7fc00000);
+    }
+    __syncwarp();      // buf is free
+}
+
+// Codes from f32.  Rotated, a column is off by at most 1.25 * 2^-22 of its pair's |u| + |w| (the angle by pi * 2^-25, cosine and
+// sine by an ulp, three roundings), so t = 15 (x - min) / (max - min) by at most 60 such errors over max - min, and
+// 15 * 2^-22 for its own roundings.  A row with a column that lies nearer than that to a border between codes is done again in
+// 64 bits (one head row of 128 in about 200), and so is one whose span, or its inverse, is no number above 0.
+struct Scale {
+    float lo, span, inv, eps;
+    bool sure;
+    __device__ __forceinline__ Scale(float low, float high, float big) {
+        lo = low;
+        span = high - low;
+        inv = 15.f / span;
+        eps = (60.f * 1.25f * 0x1p-22f) * big / span + 15.f * 0x1p-22f;
+        sure = inv <= FLT_MAX && inv > 0.f && span <= FLT_MAX && eps < 0.25f;
+    }
+    // The code of y, in the low bits of kRound's (kRound + code is the nearest whole number to t); near: f32 does not tell
+    static constexpr float kRound = 12582912.f;                 // 1.5 * 2^23
+    static constexpr uint32_t kRoundBits = 0x4B400000u;
+    __device__ __forceinline__ uint32_t code(float y, bool& near) const {
+        const float d = y - lo, r = fmaf(d, inv, kRound);
+        near = !(fabsf(fmaf(d, inv, kRound - r)) <= 0.5f - eps);
+        return __float_as_uint(r);
+    }
+    // The code of a column near a border where columns are exact (not rotated): the sign of 15 (y - lo) - (k + 1/2) (hi - lo), in
+    // f32 where both differences are f32s.  Values on a coarse grid, as 16-bit ones are, meet borders often: a quarter of the
+    // rows of 128 bf16 columns have one that lies on a border exactly.
+    __device__ __forceinline__ int border(float y, float high, bool& near) const {
+        auto rest = [](float x, float z, float d) {       // of d = x - z rounded: 0 where it is exact
+            const float v = d - x;
+            return (x - (d - v)) - (z + v);
+        };
+        const float d = y - lo, k = floorf(d * inv), p = 15.f * d, e = fmaf(15.f, d, -p), q = fmaf(k + 0.5f, span, -p);
+        near = rest(y, lo, d) != 0.f || rest(high, lo, span) != 0.f || !(e == 0.f || fabsf(q) > 2.f * fabsf(e));
+        return (int)k + (q < 0.f || (q == 0.f && ((int)k & 1)) ? 1 : 0);
+    }
+};
+
+// a warp's head row, of any width, start and alignment
 template <typename T>
 __device__ __forceinline__ void quantize_row(const AppendArgs& a, const T* src, int w, bool rot, int p, const float2* cs,
                                              float* buf, uint8_t* codes, float* pair) {
@@ -142,12 +241,10 @@ __device__ __forceinline__ void quantize_row(const AppendArgs& a, const T* src, 
     const int n = rot ? a.n_rot : 0, half = n / 2;
     float big = 0.f;       // the largest |u| + |w|
     float lo = INFINITY, hi = -INFINITY;
-    bool fine = true;
     auto take = [&](int c, float y) {
         buf[c] = y;
         lo = fminf(lo, y);
         hi = fmaxf(hi, y);
-        fine &= fabsf(y) <= FLT_MAX;
     };
     for (int i = lane; i < half; i += 32) {
         const int c0 = a.interleaved ? a.start + 2 * i : a.start + i, c1 = a.interleaved ? c0 + 1 : c0 + half;
@@ -167,70 +264,207 @@ __device__ __forceinline__ void quantize_row(const AppendArgs& a, const T* src, 
         hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
         big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
     }
-    fine = __all_sync(0xffffffffu, fine);       // (and buf is written)
-    const float span = hi - lo, inv = 15.f / span;
-    const float eps = (60.f * 1.25f * 0x1p-22f) * big / span + 15.f * 0x1p-22f;
-    // (a span of 0, or one whose inverse is no f32, is told apart below)
-    bool sure = fine && inv <= FLT_MAX && inv > 0.f && span <= FLT_MAX && eps < 0.25f;
-    bool same = fine && span == 0.f && !(big > 0.f);      // every column the same, exactly
-    for (int word = lane; word - lane < w / 8; word += 32) {
-        bool near = false;
+    __syncwarp();
+    const Scale s(lo, hi, big);
+    bool near = !s.sure;       // (a NaN is near any border)
+    for (int word = lane; word < w / 8; word += 32) {
+        const float4 y0 = *reinterpret_cast<const float4*>(buf + word * 8), y1 = *reinterpret_cast<const float4*>(buf + word * 8 + 4);
+        const float y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
         uint32_t x = 0u;
-        if (word < w / 8 && sure) {
-            const float4 y0 = *reinterpret_cast<const float4*>(buf + word * 8), y1 = *reinterpret_cast<const float4*>(buf + word * 8 + 4);
-            const float y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float t = (y[i] - lo) * inv, r = rintf(t);
-                near |= fabsf(t - r) > 0.5f - eps;
-                x |= (uint32_t)(int)fminf(fmaxf(r, 0.f), 15.f) << (4 * i);
-            }
+        for (int i = 0; i < 8; ++i) {
+            bool n8;
+            x |= (s.code(y[i], n8) & 15u) << (4 * i);
+            near |= n8;
         }
-        sure = !__any_sync(0xffffffffu, near) && sure;
-        if (!sure) break;
-        if (word < w / 8) reinterpret_cast<uint32_t*>(codes)[word] = x;
+        if (!near) reinterpret_cast<uint32_t*>(codes)[word] = x;
     }
-    float scale = span / 15.f, low = lo;
-    if (!sure) {
-        if (!fine) scale = low = __int_as_float(0x7fc00000);
-        double dlo = 0.0, dspan = 0.0;
-        if (fine && !same) {
-            double a0 = INFINITY, a1 = -INFINITY;
-            for (int c = lane; c < w; c += 32) {
-                const double y = exact_column(a, src, c, rot, p);
-                a0 = fmin(a0, y);
-                a1 = fmax(a1, y);
-            }
-#pragma unroll
-            for (int o = 16; o; o >>= 1) {
-                a0 = fmin(a0, __shfl_xor_sync(0xffffffffu, a0, o));
-                a1 = fmax(a1, __shfl_xor_sync(0xffffffffu, a1, o));
-            }
-            dlo = a0;
-            dspan = a1 - a0;
-            scale = (float)(dspan / 15.0);
-            low = (float)dlo;
-        }
-        __syncwarp();
-        for (int c = lane; c < w; c += 32)
-            buf[c] = dspan > 0.0 ? (float)rint((exact_column(a, src, c, rot, p) - dlo) * 15.0 / dspan) : 0.f;
-        __syncwarp();
-        for (int word = lane; word < w / 8; word += 32) {
-            uint32_t x = 0u;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x |= (uint32_t)(int)buf[word * 8 + i] << (4 * i);
-            reinterpret_cast<uint32_t*>(codes)[word] = x;
-        }
+    if (__any_sync(0xffffffffu, near)) {
+        exact_row(a, src, w, rot, p, buf, codes, pair);
+        return;
     }
     if (lane == 0) {
-        pair[0] = scale;
-        pair[1] = low;
+        pair[0] = s.span / 15.f;
+        pair[1] = lo;
     }
     __syncwarp();      // buf is free
 }
 
+// eight columns at p
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
+    T v[8];
+#pragma unroll
+    for (int i = 0; i < 8; i += 16 / (int)sizeof(T)) *reinterpret_cast<uint4*>(v + i) = *reinterpret_cast<const uint4*>(p + i);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = to_f32(v[i]);
+}
+
+// Head rows whose columns come in aligned eights: a lane has two of those, the ones that are turned together or neighbours, and
+// `lanes` (a power of two, at least w / 16) of them a row.  src NULL: no row for this lane.  False: the row is to be done in
+// 64 bits.
+template <typename T>
+__device__ __forceinline__ bool quantize_group(const AppendArgs& a, const T* src, int w, int lanes, bool rot, int p, const float2* cs,
+                                               uint8_t* codes, float* pair) {
+    const int li = threadIdx.x & (lanes - 1);
+    const int n = rot ? a.n_rot : 0;
+    const bool on = src && li < w / 16;
+    float x[2][8], big = 0.f, lo = INFINITY, hi = -INFINITY;
+    int c[2] = {16 * li, 16 * li + 8};
+    if (n && !a.interleaved) {
+        if (li < n / 16) {
+            c[0] = a.start + 8 * li;
+            c[1] = c[0] + n / 2;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                c[e] -= n;
+                if (c[e] >= a.start) c[e] += n;
+            }
+        }
+    }
+    if (on) {
+        load8(src + c[0], x[0]);
+        load8(src + c[1], x[1]);
+        if (n && a.interleaved) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if (c[e] < a.start || c[e] >= a.start + n) continue;
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    const float2 t = cs[(c[e] - a.start + i) / 2];
+                    const float u = x[e][i], v = x[e][i + 1];
+                    big = fmaxf(big, fabsf(u) + fabsf(v));
+                    x[e][i] = fmaf(u, t.x, -(v * t.y));
+                    x[e][i + 1] = fmaf(v, t.x, u * t.y);
+                }
+            }
+        } else if (li < n / 16) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 t = cs[8 * li + i];
+                const float u = x[0][i], v = x[1][i];
+                big = fmaxf(big, fabsf(u) + fabsf(v));
+                x[0][i] = fmaf(u, t.x, -(v * t.y));
+                x[1][i] = fmaf(v, t.x, u * t.y);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                lo = fminf(lo, x[e][i]);
+                hi = fmaxf(hi, x[e][i]);
+            }
+    }
+    for (int o = lanes >> 1; o; o >>= 1) {
+        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+    }
+    const uint32_t mine = lanes == 32 ? ~0u : ((1u << lanes) - 1u) << (threadIdx.x & 31 & ~(lanes - 1));
+    const Scale s(lo, hi, big);
+    float scale = s.span / 15.f, low = lo;
+    uint32_t word[2] = {0u, 0u};
+    bool any = false;          // a column that f32 does not tell
+    bool other = false;        // neither a span to divide by nor the same number throughout (whose codes are 0)
+    if (on && !s.sure) {
+        other = big > 0.f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) other |= !(x[e][i] == lo);
+    } else if (on) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                bool near;
+                word[e] += s.code(x[e][i], near) << (4 * i);
+                any |= near;
+            }
+            word[e] -= 0x11111111u * Scale::kRoundBits;
+        }
+    }
+    const bool sure = !(__ballot_sync(0xffffffffu, other) & mine);
+    if (__any_sync(0xffffffffu, any)) {
+        // (one place for each kind of work: bit 8 e + i for column c[e] + i)
+        uint64_t w = (uint64_t)word[1] << 32 | word[0];
+        auto put = [&](int at, int k) { w = (w & ~(15ull << (4 * at))) | (uint64_t)k << (4 * at); };
+        auto column = [&](int at) { return (at < 8 ? c[0] : c[1]) + (at & 7); };
+        uint32_t nears = 0u;
+        if (any) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    bool near;
+                    s.code(x[e][i], near);
+                    nears |= near ? 1u << (8 * e + i) : 0u;
+                }
+            if (big == 0.f)
+                for (uint32_t left = nears; left; left &= left - 1) {
+                    const int at = __ffs(left) - 1;
+                    bool near;
+                    put(at, s.border(to_f32(src[column(at)]), hi, near));
+                    if (!near) nears &= ~(1u << at);
+                }
+        }
+        __syncwarp();
+        const bool hit = __ballot_sync(0xffffffffu, nears) & mine;
+        if (__any_sync(0xffffffffu, hit)) {
+            // In 64 bits: the columns that may be the row's least and largest, and those near a border (a row of 128 rotated
+            // columns has one in 200 times).
+            const float err = 2.f * 1.25f * 0x1p-22f * big;
+            double least = INFINITY, most = -INFINITY;
+            uint32_t low_at = 0u, high_at = 0u;
+            if (hit && on) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        low_at |= x[e][i] <= lo + err ? 1u << (8 * e + i) : 0u;
+                        high_at |= x[e][i] >= hi - err ? 1u << (8 * e + i) : 0u;
+                    }
+            }
+            for (uint32_t left = low_at | high_at; left; left &= left - 1) {
+                const int at = __ffs(left) - 1;
+                const double y = exact_column(a, src, column(at), rot, p);
+                if ((low_at >> at) & 1u) least = fmin(least, y);
+                if ((high_at >> at) & 1u) most = fmax(most, y);
+            }
+            __syncwarp();
+            for (int o = lanes >> 1; o; o >>= 1) {
+                least = fmin(least, __shfl_xor_sync(0xffffffffu, least, o));
+                most = fmax(most, __shfl_xor_sync(0xffffffffu, most, o));
+            }
+            if (hit) {
+                scale = (float)((most - least) / 15.0);
+                low = (float)least;
+            }
+            for (uint32_t left = nears; left; left &= left - 1) {
+                const int at = __ffs(left) - 1;
+                const double t = rint((exact_column(a, src, column(at), rot, p) - least) * 15.0 / (most - least));
+                put(at, (int)fmin(fmax(t, 0.0), 15.0));
+            }
+            __syncwarp();
+        }
+        word[0] = (uint32_t)w;
+        word[1] = (uint32_t)(w >> 32);
+    }
+    if (on && sure) {
+        reinterpret_cast<uint32_t*>(codes)[c[0] / 8] = word[0];
+        reinterpret_cast<uint32_t*>(codes)[c[1] / 8] = word[1];
+        if (li == 0) {
+            pair[0] = scale;
+            pair[1] = low;
+        }
+    }
+    return sure || !src;
+}
+
 template <typename T, int E, bool kInter, bool kQ4>
-__global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a, Geom g, int per_cta, int64_t n_tokens) {
+__global__ void __launch_bounds__(kThreads, kQ4 ? 4 : 6) append_kernel(AppendArgs a, Geom g, int per_cta, int64_t n_tokens) {
     extern __shared__ __align__(16) float2 cs_all[];         // [per_cta][n_rot / 2]
     __shared__ Token tok[kMaxTokens];
     __shared__ __align__(16) float buf[kQ4 ? kWarps : 1][kQ4 ? kMaxD : 4];
@@ -261,38 +495,77 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a, Geom g, 
     // a token's units are shared by the CTAs along y
     const int y0 = (int)((int64_t)per * blockIdx.y / gridDim.y), y1 = (int)((int64_t)per * (blockIdx.y + 1) / gridDim.y);
     const int mine = y1 - y0;
-    for (int e = tid; e < n_tok * mine; e += kThreads) {
+    auto unit = [&](int e) -> Unit<T> {
         const int i = e / mine;
         int u = e - i * mine + y0;
         const Token& t = tok[i];
-        const float2* cs = cs_all + i * half;
-        const bool is_q = u < nq;
-        if (is_q || u < nq + nk) {
-            if (!is_q) u -= nq;
+        if (u < nq) {
             const int h = u / uq;
-            u -= h * uq;
-            const T* src = is_q ? static_cast<const T*>(a.rows.q) + t.row * a.rows.q_stride : static_cast<const T*>(a.rows.k) + t.row * a.rows.k_stride;
-            T* dst = is_q ? static_cast<T*>(a.rows.q_out) + t.row * a.rows.q_out_stride : static_cast<T*>(a.k_cache) + t.to * a.kc_stride;
-            if (is_q || t.to >= 0) head_unit<T, E, kInter>(a, src + h * a.dk, dst + h * a.dk, u, a.n_rot > 0, cs);
-        } else if (t.to >= 0) {
-            u -= nq + nk;       // (the heads of V lie one behind the other: pieces of the whole row)
-            store<T, E>(static_cast<T*>(a.v_cache) + t.to * a.vc_stride + u * E,
-                        load<T, E>(static_cast<const T*>(a.rows.v) + t.row * a.rows.v_stride + u * E));
+            return head_unit<T, E, kInter>(a, static_cast<const T*>(a.rows.q) + t.row * a.rows.q_stride + h * a.dk,
+                                           static_cast<T*>(a.rows.q_out) + t.row * a.rows.q_out_stride + h * a.dk, u - h * uq, a.n_rot > 0,
+                                           cs_all + i * half);
         }
+        if (t.to < 0) return {nullptr, nullptr, nullptr, 0};
+        u -= nq;
+        if (u < nk) {
+            const int h = u / uq;
+            return head_unit<T, E, kInter>(a, static_cast<const T*>(a.rows.k) + t.row * a.rows.k_stride + h * a.dk,
+                                           static_cast<T*>(a.k_cache) + t.to * a.kc_stride + h * a.dk, u - h * uq, a.n_rot > 0, cs_all + i * half);
+        }
+        u -= nk;       // (the heads of V lie one behind the other: pieces of the whole row)
+        return {static_cast<const T*>(a.rows.v) + t.row * a.rows.v_stride + u * E, static_cast<T*>(a.v_cache) + t.to * a.vc_stride + u * E, nullptr, 0};
+    };
+    // (two or three units' loads at a time measured slower: 27 and 34 us for 19 of a 4096-token chunk, for the CTAs that their
+    // registers cost)
+    for (int e = tid; e < n_tok * mine; e += kThreads) {
+        const Unit<T> x = unit(e);
+        if (!x.src) continue;
+        Piece<T, E> v = load<T, E>(x.src), w;
+        if (x.apart) w = load<T, E>(x.src + x.apart);
+        finish<T, E, kInter>(x, v, w);
     }
     if constexpr (kQ4) {
-        const int heads = a.Hkv * (a.rows.v ? 2 : 1);
-        const int w0 = (blockIdx.y * kWarps) + (tid >> 5);
-        for (int e = w0; e < n_tok * heads; e += kWarps * gridDim.y) {
-            const int i = e / heads, hh = e - i * heads;
-            const Token& t = tok[i];
-            if (t.to < 0) continue;
-            const bool is_k = hh < a.Hkv;
-            const int h = is_k ? hh : hh - a.Hkv, w = is_k ? a.dk : a.dv;
-            const T* src = is_k ? static_cast<const T*>(a.rows.k) + t.row * a.rows.k_stride : static_cast<const T*>(a.rows.v) + t.row * a.rows.v_stride;
-            uint8_t* row = is_k ? static_cast<uint8_t*>(a.k_cache) + t.to * a.kc_stride : static_cast<uint8_t*>(a.v_cache) + t.to * a.vc_stride;
-            quantize_row<T>(a, src + h * w, w, is_k && a.n_rot > 0, t.pos, cs_all + i * half, buf[tid >> 5], row + h * (w / 2),
-                            reinterpret_cast<float*>(row + a.Hkv * (w / 2)) + 2 * h);
+        const int warp = tid >> 5, lane = tid & 31;
+        for (int kind = 0; kind < (a.rows.v ? 2 : 1); ++kind) {
+            const bool is_k = kind == 0, rot = is_k && a.n_rot > 0;
+            const int w = is_k ? a.dk : a.dv, rows = n_tok * a.Hkv;
+            struct Row {
+                const T* src;
+                uint8_t* codes;
+                float* pair;
+                int i;
+            };
+            auto row_at = [&](int e) -> Row {
+                Row r = {nullptr, nullptr, nullptr, e / a.Hkv};
+                if (e >= rows || tok[r.i].to < 0) return r;
+                const int h = e - r.i * a.Hkv;
+                const Token& t = tok[r.i];
+                uint8_t* c = is_k ? static_cast<uint8_t*>(a.k_cache) + t.to * a.kc_stride : static_cast<uint8_t*>(a.v_cache) + t.to * a.vc_stride;
+                r.src = (is_k ? static_cast<const T*>(a.rows.k) + t.row * a.rows.k_stride : static_cast<const T*>(a.rows.v) + t.row * a.rows.v_stride) + h * w;
+                r.codes = c + h * (w / 2);
+                r.pair = reinterpret_cast<float*>(c + a.Hkv * (w / 2)) + 2 * h;
+                return r;
+            };
+            int lanes = is_k ? a.k_lanes : a.v_lanes;
+            if (lanes) {
+                const int per = 32 / lanes;
+                for (int e = (blockIdx.y * kWarps + warp) * per; e < rows; e += kWarps * gridDim.y * per) {
+                    const Row r = row_at(e + lane / lanes);
+                    const int tk = min(r.i, n_tok - 1);
+                    const bool done = quantize_group(a, r.src, w, lanes, rot, tok[tk].pos, cs_all + tk * half, r.codes, r.pair);
+                    // (a lane of each row that is not)
+                    uint32_t left = __ballot_sync(0xffffffffu, !done && (lane & (lanes - 1)) == 0);
+                    for (; left; left &= left - 1) {
+                        const Row x = row_at(e + (__ffs(left) - 1) / lanes);
+                        exact_row(a, x.src, w, rot, tok[x.i].pos, buf[warp], x.codes, x.pair);
+                    }
+                }
+            } else {
+                for (int e = blockIdx.y * kWarps + warp; e < rows; e += kWarps * gridDim.y) {
+                    const Row r = row_at(e);
+                    if (r.src) quantize_row(a, r.src, w, rot, tok[r.i].pos, cs_all + r.i * half, buf[warp], r.codes, r.pair);
+                }
+            }
         }
     }
 }
@@ -300,10 +573,13 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a, Geom g, 
 template <typename T, int E, bool kInter, bool kQ4>
 cudaError_t go(const AppendArgs& a, const Geom& g, cudaStream_t st) {
     const int64_t n = (int64_t)g.B * g.T;
-    // tokens per CTA: one while there are few, more where a CTA would have little to do
+    // Tokens per CTA: one while there are few, then what makes a round of CTAs: a token's first loads (lengths, positions,
+    // pages) and its cosines take longer than its rows.
     const int64_t per_tok = ((int64_t)a.Hq * a.dk + (int64_t)a.Hkv * (a.dk + a.dv)) / E;
-    int per = 1;
-    while (per < kMaxTokens && n / per > 8 * 152 && per_tok * per < 4 * kThreads) per *= 2;
+    int per = (int)(n / (152 * (kQ4 ? 8 : 4)));
+    if (per > kMaxTokens) per = kMaxTokens;
+    if (per * a.n_rot > kMaxCs * 2) per = kMaxCs * 2 / a.n_rot;
+    if (per < 1) per = 1;
     const int64_t ctas = (n + per - 1) / per;
     // few tokens: several CTAs to one
     int parts = 1;
@@ -328,8 +604,21 @@ cudaError_t run(const AppendArgs& a, const Geom& g, cudaStream_t st) {
         if (r.v && a.dv % E) el |= 1;      // (units count whole pieces of a head)
     }
     const bool vec = all % 16 == 0 && el % E == 0;
-    if (a.interleaved) return vec ? go<T, E, true, kQ4>(a, g, st) : go<T, 1, true, kQ4>(a, g, st);
-    return vec ? go<T, E, false, kQ4>(a, g, st) : go<T, 1, false, kQ4>(a, g, st);
+    AppendArgs b = a;
+    if (kQ4) {
+        // lanes of a head row whose columns come in aligned eights, up to a warp
+        auto lanes = [&](const void* x, int64_t stride, int w, bool rot) {
+            if (!x || reinterpret_cast<uintptr_t>(x) % 16 || stride * (int64_t)sizeof(T) % 16 || w * (int64_t)sizeof(T) % 16 || w % 16 || w > 512) return 0;
+            if (rot && (a.start % 8 || a.n_rot % (a.interleaved ? 8 : 16))) return 0;
+            int n = 1;
+            while (n < w / 16) n *= 2;
+            return n;
+        };
+        b.k_lanes = lanes(r.k, r.k_stride, a.dk, a.n_rot > 0);
+        b.v_lanes = lanes(r.v, r.v_stride, a.dv, false);
+    }
+    if (a.interleaved) return vec ? go<T, E, true, kQ4>(b, g, st) : go<T, 1, true, kQ4>(b, g, st);
+    return vec ? go<T, E, false, kQ4>(b, g, st) : go<T, 1, false, kQ4>(b, g, st);
 }
 
 // ------------------------------------------------------------------------------------------- reading back

@@ -6,12 +6,17 @@
 // row goes with its logit, so the chunk's list needs no normalisation; a second kernel,
 // a CTA per sequence, joins the sums and takes the n_out best of all lists, in 64 bits.
 //
-// The best K of N keys, K <= 32: a bound that at least K keys reach is cheap - the
-// least over W warps of the (K/W)-th best of the lanes' maxima, or the K-th best lane of
-// one warp, whichever is higher; each is a sort of 32 lanes in registers.  The few keys
-// that reach it go to a list in shared memory and are ranked by counting.  Keys hold
-// the column below the logit, so that they differ and ties go to the lower token.  Where
-// too many reach the bound (a row of equal logits) K rounds of a maximum are taken instead.
+// The best K of N keys, K <= 32: a bound that at least K keys reach is cheap, the least over W warps of the (K/W)-th best
+// of the lanes' maxima.  The few keys that reach it go to a list in shared memory and are ranked by counting.  Keys hold
+// the column below the logit, so that they differ and ties go to the lower token.  Where too many reach the bound (a row
+// of equal logits) K rounds of a maximum are taken instead.
+//
+// The scan waits more than it works (seven instructions a logit): 16-bit logits stay packed so that more CTAs are at it,
+// sums run against the warp's maximum so that two barriers are enough.
+// 512 rows of 131072 bf16 logits, 16 kept of each eight: 68 us, some 50 of them the scan (2.4 TB/s), in which schedulers issue on 58 % of
+// the cycles; the merge waits for one load after another.
+#include <float.h>
+
 #include "beam.cuh"
 #include "sm100_ptx.cuh"
 
@@ -37,37 +42,74 @@ struct BeamArgs {
 
 __device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
 
-// The bound from the lanes' best keys of all W warps (0: an empty lane); tops[2 * W] in shared memory
-template <int W, typename K>
-__device__ __forceinline__ K reached_by(K best, int k, K* tops) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // bitonic sort, largest in lane 0
+// The lanes' n-th best key, n <= 32 (0: fewer are above 0); first: the best
+template <typename K>
+__device__ __forceinline__ K nth_of_lanes(K mine, int n, K& first) {
+    const int lane = threadIdx.x & 31;
+    K best = 0;
+    for (int i = 0; i < n; ++i) {
+        if constexpr (sizeof(K) == 4) {
+            best = __reduce_max_sync(0xffffffffu, mine);
+        } else {
+            best = mine;
 #pragma unroll
-    for (int size = 2; size <= 32; size <<= 1)
-#pragma unroll
-        for (int d = size >> 1; d; d >>= 1) {
-            const K other = __shfl_xor_sync(0xffffffffu, best, d);
-            const bool keep_large = ((lane & d) == 0) == ((lane & size) == 0);
-            best = keep_large == (best > other) ? best : other;
+            for (int o = 16; o; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
         }
-    if (lane == (k + W - 1) / W - 1) tops[warp] = best;
-    if (lane == k - 1) tops[W + warp] = best;
-    __syncthreads();
-    K least = tops[0], high = tops[W];
-#pragma unroll
-    for (int i = 1; i < W; ++i) {
-        least = min(least, tops[i]);
-        high = max(high, tops[W + i]);
+        if (i == 0) first = best;
+        if (lane == __ffs(__ballot_sync(0xffffffffu, mine == best)) - 1) mine = 0;
     }
-    return max(least, high);
+    return best;
+}
+
+__device__ __forceinline__ float max_of(const float* v, int n) {
+    float m = v[0];
+#pragma unroll
+    for (int i = 1; i < n; ++i) m = fmaxf(m, v[i]);
+    return m;
+}
+__device__ __forceinline__ float max_of(const __half* v, int n) {
+    __half2 m = *reinterpret_cast<const __half2*>(v);
+#pragma unroll
+    for (int i = 2; i < n; i += 2) m = __hmax2(m, *reinterpret_cast<const __half2*>(v + i));
+    return __half2float(__hmax(__low2half(m), __high2half(m)));
+}
+__device__ __forceinline__ float max_of(const __nv_bfloat16* v, int n) {
+    __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(v);
+#pragma unroll
+    for (int i = 2; i < n; i += 2) m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(v + i));
+    return __bfloat162float(__hmax(__low2bfloat16(m), __high2bfloat16(m)));
+}
+
+// Bits of the elements that reach r (a number): element e at bit e; of 16-bit ones e / 2 + 16 (e % 2)
+template <int E>
+__device__ __forceinline__ uint32_t reaching(const float (&v)[E], float r) {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int e = 0; e < E; ++e) m |= v[e] >= r ? 1u << e : 0u;
+    return m;
+}
+template <int E>
+__device__ __forceinline__ uint32_t reaching(const __half (&v)[E], float r) {
+    const __half2 r2 = __float2half2_rn(fmaxf(r, -65504.f));
+    uint32_t m = 0u;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) m |= __hge2_mask(*reinterpret_cast<const __half2*>(v + e), r2) & (0x10001u << (e / 2));
+    return m;
+}
+template <int E>
+__device__ __forceinline__ uint32_t reaching(const __nv_bfloat16 (&v)[E], float r) {
+    const __nv_bfloat162 r2 = __float2bfloat162_rn(fmaxf(r, __uint_as_float(0xff7f0000u)));      // (the lowest finite one)
+    uint32_t m = 0u;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) m |= __hge2_mask(*reinterpret_cast<const __nv_bfloat162*>(v + e), r2) & (0x10001u << (e / 2));
+    return m;
 }
 
 // E logits a thread; V of them to a load
 template <typename T, int E, int V>
-__global__ void __launch_bounds__(kThreads) beam_scan_kernel(BeamArgs a) {
-    __shared__ uint32_t tops[2 * kWarps];
-    __shared__ float red[kWarps];
-    __shared__ float sums[kWarps];
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) beam_scan_kernel(BeamArgs a) {
+    __shared__ uint32_t tops[kWarps];
+    __shared__ float maxima[kWarps], sums[kWarps];
     __shared__ unsigned long long list[kList];
     __shared__ unsigned long long best_s[kWarps];
     __shared__ int count;
@@ -78,75 +120,63 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(BeamArgs a) {
     pdl_wait();
     if (a.b.done && a.b.done[row]) return;
     const T* x = static_cast<const T*>(a.b.logits) + row * a.b.logit_stride;
-    float v[E];
+    __align__(16) T v[E];
 #pragma unroll
     for (int p = 0; p < E / V; ++p) {
         const int c = c0 + (p * kThreads + tid) * V;
-        if constexpr (V > 1) {
-            T y[V];
-            if (c + V <= a.vocab) {
-                *reinterpret_cast<uint4*>(y) = *reinterpret_cast<const uint4*>(x + c);
-#pragma unroll
-                for (int i = 0; i < V; ++i) v[p * V + i] = to_f32(y[i]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < V; ++i) v[p * V + i] = c + i < a.vocab ? to_f32(x[c + i]) : -INFINITY;
-            }
+        if (V > 1 && c + V <= a.vocab) {
+            *reinterpret_cast<uint4*>(v + p * V) = *reinterpret_cast<const uint4*>(x + c);
         } else {
-            v[p] = c < a.vocab ? to_f32(x[c]) : -INFINITY;
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[p * V + i] = c + i < a.vocab ? x[c + i] : from_f32<T>(-INFINITY);
         }
     }
     auto column = [&](int e) { return c0 + (e / V * kThreads + tid) * V + e % V; };
-    float m = -INFINITY;
-    bool bad = false;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        bad |= !(v[e] < INFINITY);
-        m = fmaxf(m, v[e]);
-    }
+    const float m = max_of(v, E);       // (of the numbers; a NaN shows in the sum)
     const uint32_t mine = m > -INFINITY ? order_key(m) : 0u;
-    const uint32_t wbest = __reduce_max_sync(0xffffffffu, mine);
-    if (lane == 0) red[warp] = wbest ? key_value(wbest) : -INFINITY;
-    if (tid == 0) count = 0;
-    bad = __syncthreads_or(bad);
-    if (bad) {
-        if (tid == 0) a.parts[at] = {INFINITY, 0.f};
-        return;
-    }
-    float M = red[0];
-#pragma unroll
-    for (int i = 1; i < kWarps; ++i) M = fmaxf(M, red[i]);
-    if (M == -INFINITY) {
-        if (tid == 0) a.parts[at] = {-INFINITY, 0.f};
-        for (int i = tid; i < a.out; i += kThreads) a.cand[at * a.out + i] = 0ull;
-        return;
-    }
-    // sum of exponentials (four chains; the differences are exact enough: |x - M| * 2^-24 of a weight e^-|x - M|)
+    uint32_t first = 0u;
+    // (a row's last chunk may leave warps without columns: the others' bound)
+    const int full = max(min(kThreads, (a.vocab - c0 + V - 1) / V) / 32, 1);
+    const uint32_t nth = nth_of_lanes(mine, (a.out + full - 1) / full, first);
+    const float wm = first ? key_value(first) : -INFINITY;
+    // sum of exponentials against the warp's maximum (four chains; |x - wm| * 2^-24 of a weight e^-|x - wm|)
+    const float ref = first ? wm : 0.f;
     float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int e = 0; e < E; ++e) s4[e & 3] += sm100::ex2_approx((v[e] - M) * kLog2e);
+    for (int e = 0; e < E; ++e) s4[e & 3] += sm100::ex2_approx((to_f32(v[e]) - ref) * kLog2e);
     float s = (s4[0] + s4[1]) + (s4[2] + s4[3]);
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) sums[warp] = s;
-    // the best
-    const uint32_t bound = max(reached_by<kWarps>(mine, a.out, tops), 1u);
-    if (mine >= bound) {
+    if (lane == 0) {
+        maxima[warp] = wm;
+        sums[warp] = s;
+        tops[warp] = nth;
+    }
+    if (tid == 0) count = 0;
+    __syncthreads();
+    float M = maxima[0];
+    uint32_t bound = tops[0];
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const uint32_t k = v[e] > -INFINITY ? order_key(v[e]) : 0u;
-            if (k >= bound) {
-                const int i = atomicAdd(&count, 1);
-                if (i < kList) list[i] = (unsigned long long)k << 32 | (uint32_t)~column(e);
-            }
+    for (int i = 1; i < kWarps; ++i) {
+        M = fmaxf(M, maxima[i]);
+        if (i < full) bound = min(bound, tops[i]);
+    }
+    // (as a number, at least the lowest finite one: neither -inf nor a NaN reaches it)
+    const float reach = key_value(max(bound, order_key(-FLT_MAX)));
+    if (m >= reach) {
+        for (uint32_t left = reaching(v, reach); left; left &= left - 1) {
+            const int bit = __ffs(left) - 1, e = sizeof(T) == 2 ? 2 * (bit & 15) + (bit >> 4) : bit;
+            const int c = c0 + (e / V * kThreads + tid) * V + e % V;
+            const int i = atomicAdd(&count, 1);
+            if (i < kList) list[i] = (unsigned long long)order_key(to_f32(x[c])) << 32 | (uint32_t)~c;      // (read again: few are)
         }
     }
     __syncthreads();
     if (tid == 0) {
         float t = 0.f;
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) t += sums[i];
-        a.parts[at] = {M, t};
+        for (int i = 0; i < kWarps; ++i) t += sums[i] * (maxima[i] > -INFINITY ? sm100::ex2_approx((maxima[i] - M) * kLog2e) : sums[i] != sums[i] ? 1.f : 0.f);
+        a.parts[at] = {M < INFINITY && t == t ? M : INFINITY, t};
     }
     const int n = count;
     unsigned long long* out = a.cand + at * a.out;
@@ -165,7 +195,8 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(BeamArgs a) {
         unsigned long long best = 0ull;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const unsigned long long k = v[e] > -INFINITY ? (unsigned long long)order_key(v[e]) << 32 | (uint32_t)~column(e) : 0ull;
+            const float y = to_f32(v[e]);
+            const unsigned long long k = y > -INFINITY ? (unsigned long long)order_key(y) << 32 | (uint32_t)~column(e) : 0ull;
             if (k < last && k > best) best = k;
         }
 #pragma unroll
@@ -196,10 +227,14 @@ struct Cont {          // a continuation: worth, and beam * vocab + token
 };
 
 __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamArgs a) {
-    __shared__ double lse[kBeamMax];
+    __shared__ double lse[kBeamMax];       // of a beam's logits; 0 of one that is done; NaN: no continuations
+    __shared__ float base[kBeamMax];       // its score
+    __shared__ uint8_t ended[kBeamMax];    // whether it is done
+    __shared__ float top[kBeamMax];        // its largest logit
+    __shared__ int lens[kBeamMax];         // its history's length
     __shared__ unsigned long long keys[kMergeList];
     __shared__ uint32_t ats[kMergeList];
-    __shared__ unsigned long long tops[2 * kMergeWarps];
+    __shared__ unsigned long long tops[kMergeWarps];
     __shared__ Cont won[kBeamOutMax];
     __shared__ Cont best_s[kMergeWarps];
     __shared__ int count;
@@ -208,63 +243,97 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamArgs a) {
     const int64_t row0 = (int64_t)seq * a.beams;
     pdl_wait();
     if (tid == 0) count = 0;
-    // each beam's log of the sum (NaN: no continuations)
+    const int lists = a.beams * a.chunks;
+    // lists are dealt to as many warps as they fill, one after the other, so that the warps have about as many
+    const int warps = min((lists + 31) / 32, kMergeWarps);
+    const int mine_at = warp + warps * lane;
+    const bool has = warp < warps && mine_at < lists;
+    const unsigned long long head = has ? a.cand[(row0 * a.chunks + mine_at) * a.out] : 0ull;      // (on its way meanwhile)
     for (int w = warp; w < a.beams; w += kMergeWarps) {
         const int64_t row = row0 + w;
         const float score = a.b.scores[row];
         const bool done = a.b.done && a.b.done[row];
-        bool wrong = !(score < INFINITY);
         float m = -INFINITY;
         const Part* p = a.parts + row * a.chunks;
+        // (what a beam that is done has there is not looked at, but not waited for either)
+        Part first = lane < a.chunks ? p[lane] : Part{-INFINITY, 0.f};
+        const int len = a.b.lengths ? a.b.lengths[row] : 0;
+        if (done) first.m = -INFINITY;
+        m = first.m;
         if (!done)
-            for (int c = lane; c < a.chunks; c += 32) m = fmaxf(m, p[c].m);
+            for (int c = lane + 32; c < a.chunks; c += 32) m = fmaxf(m, p[c].m);
 #pragma unroll
         for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         double s = 0.0;
-        if (!done && m > -INFINITY && m < INFINITY)
-            for (int c = lane; c < a.chunks; c += 32)
-                if (p[c].m > -INFINITY) s += (double)p[c].s * (double)exp2f((p[c].m - m) * kLog2e);
+        if (m > -INFINITY && m < INFINITY) {
+            if (first.m > -INFINITY) s = (double)(first.s * exp2f((first.m - m) * kLog2e));
+            for (int c = lane + 32; c < a.chunks; c += 32)
+                if (p[c].m > -INFINITY) s += (double)(p[c].s * exp2f((p[c].m - m) * kLog2e));
 #pragma unroll
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        wrong |= m == INFINITY;
+            for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        }
         if (lane == 0) {
-            if (wrong) flag(a.status, IDX_ERR_INEXACT);
-            const bool none = wrong || score == -INFINITY || (!done && m == -INFINITY);
-            lse[w] = none ? __longlong_as_double(0x7ff8000000000000ll) : done ? 0.0 : (double)m + log(s);
+            base[w] = score;
+            ended[w] = done;
+            lens[w] = len;
+            top[w] = m;
+            lse[w] = s;
         }
     }
     __syncthreads();
+    // (64-bit logarithms are slow here: a lane to a beam)
+    for (int w = tid; w < a.beams; w += kMergeThreads) {
+        const float score = base[w], m = top[w];
+        const bool wrong = !(score < INFINITY) || m == INFINITY, none = wrong || score == -INFINITY || (!ended[w] && m == -INFINITY);
+        if (wrong) flag(a.status, IDX_ERR_INEXACT);
+        lse[w] = none ? __longlong_as_double(0x7ff8000000000000ll) : ended[w] ? 0.0 : (double)m + log(lse[w]);
+    }
+    __syncthreads();
     // lists: one per (beam, chunk), for a beam that is done a single entry
-    const int lists = a.beams * a.chunks;
-    auto entry = [&](int l, int i) -> Cont {
+    auto value = [&](int l, int i, unsigned long long k) -> Cont {       // k: what the list has there
         const int w = l / a.chunks, c = l - w * a.chunks;
         const double z = lse[w];
         if (z != z) return {0ull, 0u};
-        const int64_t row = row0 + w;
-        const double base = (double)a.b.scores[row];
-        if (a.b.done && a.b.done[row]) {
+        if (ended[w]) {
             if (c || i) return {0ull, 0u};
-            return {order_key64(base), (uint32_t)w * (uint32_t)a.vocab + (uint32_t)a.end};
+            return {order_key64((double)base[w]), (uint32_t)w * (uint32_t)a.vocab + (uint32_t)a.end};
         }
-        const unsigned long long k = a.cand[(row * a.chunks + c) * a.out + i];
         if (!k) return {0ull, 0u};
-        return {order_key64(base + ((double)key_value((uint32_t)(k >> 32)) - z)),
+        return {order_key64((double)base[w] + ((double)key_value((uint32_t)(k >> 32)) - z)),
                 (uint32_t)w * (uint32_t)a.vocab + ~(uint32_t)k};
     };
-    unsigned long long mine = 0ull;
-    for (int l = tid; l < lists; l += kMergeThreads) mine = max(mine, entry(l, 0).key);
-    const unsigned long long bound = max(reached_by<kMergeWarps>(mine, a.out, tops), 1ull);
-    if (mine >= bound)
-        for (int l = tid; l < lists; l += kMergeThreads)
-            for (int i = 0; i < a.out; ++i) {
-                const Cont e = entry(l, i);
-                if (e.key < bound) break;
-                const int j = atomicAdd(&count, 1);
-                if (j < kMergeList) {
-                    keys[j] = e.key;
-                    ats[j] = e.at;
+    const unsigned long long* cand = a.cand + row0 * a.chunks * a.out;
+    auto entry = [&](int l, int i) -> Cont { return value(l, i, cand[(int64_t)l * a.out + i]); };
+    unsigned long long mine = has ? value(mine_at, 0, head).key : 0ull, first = 0ull;
+    if (warp < warps)
+        for (int l = mine_at + warps * 32; l < lists; l += warps * 32) mine = max(mine, entry(l, 0).key);
+    const unsigned long long nth = nth_of_lanes(mine, (a.out + warps - 1) / warps, first);
+    if (lane == 0) tops[warp] = nth;
+    __syncthreads();
+    unsigned long long bound = tops[0];
+    for (int i = 1; i < warps; ++i) bound = min(bound, tops[i]);
+    bound = max(bound, 1ull);
+    if (mine >= bound && warp < warps)
+        for (int l = mine_at; l < lists; l += warps * 32) {
+            bool on = true;
+            for (int i0 = 0; on && i0 < a.out; i0 += 4) {
+                unsigned long long k[4];      // four at a time
+#pragma unroll
+                for (int i = 0; i < 4; ++i) k[i] = i0 + i < a.out ? cand[(int64_t)l * a.out + i0 + i] : 0ull;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (!on || i0 + i >= a.out) break;
+                    const Cont e = value(l, i0 + i, k[i]);
+                    on = e.key >= bound;
+                    if (!on) break;
+                    const int j = atomicAdd(&count, 1);
+                    if (j < kMergeList) {
+                        keys[j] = e.key;
+                        ats[j] = e.at;
+                    }
                 }
             }
+        }
     if (tid < a.out) won[tid] = {0ull, 0u};
     __syncthreads();
     const int n = count;
@@ -313,7 +382,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamArgs a) {
         const bool none = e.key == 0ull;
         const int w = none ? 0 : (int)(e.at / (uint32_t)a.vocab), token = none ? -1 : (int)(e.at - (uint32_t)w * (uint32_t)a.vocab);
         const int64_t row = row0 + w;
-        const bool was = !none && a.b.done && a.b.done[row];
+        const bool was = !none && ended[w];
         if (lane == 0) {
             a.b.out_scores[to] = none ? -INFINITY : (float)key_value64(e.key);
             a.b.parent[to] = none ? -1 : (int32_t)row;
@@ -321,7 +390,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamArgs a) {
             a.b.out_done[to] = none || was || token == a.end;
         }
         if (!a.b.lengths) continue;
-        int len = none ? 0 : a.b.lengths[row];
+        int len = none ? 0 : lens[w];
         const int room = a.b.history_cols;
         bool grows = !none && !was;
         if (len < 0 || len > room || (grows && len >= room)) {
@@ -331,8 +400,14 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamArgs a) {
         }
         const int32_t* src = a.b.history + row * a.b.history_stride;
         int32_t* dst = a.b.out_history + to * a.b.out_history_stride;
+        int from = 0;
+        if (((reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst)) & 15u) == 0) {
 #pragma unroll 4
-        for (int i = lane; i < len; i += 32) dst[i] = src[i];
+            for (int i = lane; i < len / 4; i += 32) reinterpret_cast<int4*>(dst)[i] = reinterpret_cast<const int4*>(src)[i];
+            from = len / 4 * 4;
+        }
+#pragma unroll 4
+        for (int i = from + lane; i < len; i += 32) dst[i] = src[i];
         if (lane == 0) {
             if (grows) dst[len] = token;
             a.b.out_lengths[to] = len + grows;

@@ -17,6 +17,7 @@ struct AppendArgs {
     void* v_cache;
     int64_t kc_stride, vc_stride;    // elements; 4-bit caches: bytes
     int64_t kv_rows;
+    int32_t k_lanes, v_lanes;        // lanes of a head row that is quantised from registers, 0: through shared memory (set by the launch)
 };
 
 cudaError_t launch_append(const AppendArgs& a, int dtype, bool q4, const Geom& g, cudaStream_t st);
