@@ -18,7 +18,7 @@
 #include <float.h>
 
 #include "beam.cuh"
-#include "sm100_ptx.cuh"
+#include "dense_attn.cuh"
 
 namespace lidx {
 namespace {
@@ -26,7 +26,6 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;             // scan
 constexpr int kMergeThreads = 512, kMergeWarps = kMergeThreads / 32;
 constexpr int kList = 1024, kMergeList = 2048;
-constexpr float kLog2e = 1.4426950408889634f;
 
 struct Part {
     float m, s;      // maximum (+inf: the row has no worths), sum of exp(x - m)
@@ -34,7 +33,7 @@ struct Part {
 
 struct BeamArgs {
     idx_beam b;
-    int32_t seqs, beams, out, vocab, end, chunks;
+    int32_t seqs, beams, out, vocab, end, chunks, per_thread;
     Part* parts;               // [row][chunk]
     unsigned long long* cand;  // [row][chunk][out]: order_key << 32 | ~column, best first; 0: none
     int* status;
@@ -80,41 +79,53 @@ __device__ __forceinline__ float max_of(const __nv_bfloat16* v, int n) {
     return __bfloat162float(__hmax(__low2bfloat16(m), __high2bfloat16(m)));
 }
 
-// Bits of the elements that reach r (a number): element e at bit e; of 16-bit ones e / 2 + 16 (e % 2)
-template <int E>
-__device__ __forceinline__ uint32_t reaching(const float (&v)[E], float r) {
+// Bits of those of the 32 (or fewer) elements from v on that reach r (a number): element e at bit e; of 16-bit ones
+// e / 2 + 16 (e % 2)
+template <int N>
+__device__ __forceinline__ uint32_t reaching(const float* v, float r) {
     uint32_t m = 0u;
 #pragma unroll
-    for (int e = 0; e < E; ++e) m |= v[e] >= r ? 1u << e : 0u;
+    for (int e = 0; e < N; ++e) m |= v[e] >= r ? 1u << e : 0u;
     return m;
 }
-template <int E>
-__device__ __forceinline__ uint32_t reaching(const __half (&v)[E], float r) {
+template <int N>
+__device__ __forceinline__ uint32_t reaching(const __half* v, float r) {
     const __half2 r2 = __float2half2_rn(fmaxf(r, -65504.f));
     uint32_t m = 0u;
 #pragma unroll
-    for (int e = 0; e < E; e += 2) m |= __hge2_mask(*reinterpret_cast<const __half2*>(v + e), r2) & (0x10001u << (e / 2));
+    for (int e = 0; e < N; e += 2) m |= __hge2_mask(*reinterpret_cast<const __half2*>(v + e), r2) & (0x10001u << (e / 2));
     return m;
 }
-template <int E>
-__device__ __forceinline__ uint32_t reaching(const __nv_bfloat16 (&v)[E], float r) {
+template <int N>
+__device__ __forceinline__ uint32_t reaching(const __nv_bfloat16* v, float r) {
     const __nv_bfloat162 r2 = __float2bfloat162_rn(fmaxf(r, __uint_as_float(0xff7f0000u)));      // (the lowest finite one)
     uint32_t m = 0u;
 #pragma unroll
-    for (int e = 0; e < E; e += 2) m |= __hge2_mask(*reinterpret_cast<const __nv_bfloat162*>(v + e), r2) & (0x10001u << (e / 2));
+    for (int e = 0; e < N; e += 2) m |= __hge2_mask(*reinterpret_cast<const __nv_bfloat162*>(v + e), r2) & (0x10001u << (e / 2));
     return m;
+}
+
+// two numbers as a packed pair of f32
+__device__ __forceinline__ uint64_t two(const float* v) { return (uint64_t)__float_as_uint(v[1]) << 32 | __float_as_uint(v[0]); }
+__device__ __forceinline__ uint64_t two(const __half* v) {
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(v));
+    return (uint64_t)__float_as_uint(x.y) << 32 | __float_as_uint(x.x);
+}
+__device__ __forceinline__ uint64_t two(const __nv_bfloat16* v) {
+    const uint32_t x = *reinterpret_cast<const uint32_t*>(v);
+    return (uint64_t)(x & 0xffff0000u) << 32 | (x << 16);
 }
 
 // E logits a thread; V of them to a load
 template <typename T, int E, int V>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) beam_scan_kernel(BeamArgs a) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && E < 64 ? 4 : 3) beam_scan_kernel(BeamArgs a) {
     __shared__ uint32_t tops[kWarps];
     __shared__ float maxima[kWarps], sums[kWarps];
     __shared__ unsigned long long list[kList];
     __shared__ unsigned long long best_s[kWarps];
     __shared__ int count;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t at = blockIdx.x, row = at / a.chunks;
+    const int64_t at = blockIdx.x, row = blockIdx.x / (unsigned)a.chunks;
     const int c0 = (int)(at - row * a.chunks) * (kThreads * E);
     pdl_trigger();     // (the merge waits for this kernel's end)
     pdl_wait();
@@ -131,7 +142,6 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) beam_scan_ke
             for (int i = 0; i < V; ++i) v[p * V + i] = c + i < a.vocab ? x[c + i] : from_f32<T>(-INFINITY);
         }
     }
-    auto column = [&](int e) { return c0 + (e / V * kThreads + tid) * V + e % V; };
     const float m = max_of(v, E);       // (of the numbers; a NaN shows in the sum)
     const uint32_t mine = m > -INFINITY ? order_key(m) : 0u;
     uint32_t first = 0u;
@@ -141,10 +151,17 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) beam_scan_ke
     const float wm = first ? key_value(first) : -INFINITY;
     // sum of exponentials against the warp's maximum (four chains; |x - wm| * 2^-24 of a weight e^-|x - wm|)
     const float ref = first ? wm : 0.f;
-    float s4[4] = {0.f, 0.f, 0.f, 0.f};
+    const uint64_t ref2 = pair(-ref, -ref), log2e2 = pair(kLog2e, kLog2e);
+    uint64_t s2[2] = {0ull, 0ull};
 #pragma unroll
-    for (int e = 0; e < E; ++e) s4[e & 3] += sm100::ex2_approx((to_f32(v[e]) - ref) * kLog2e);
-    float s = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+    for (int e = 0; e < E; e += 2) {
+        float x0, x1;
+        unpair(mul2(add2(two(v + e), ref2), log2e2), x0, x1);
+        s2[e / 2 & 1] = add2(s2[e / 2 & 1], pair(sm100::ex2_approx(x0), sm100::ex2_approx(x1)));
+    }
+    float s, s_odd;
+    unpair(add2(s2[0], s2[1]), s, s_odd);
+    s += s_odd;
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane == 0) {
@@ -164,12 +181,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) beam_scan_ke
     // (as a number, at least the lowest finite one: neither -inf nor a NaN reaches it)
     const float reach = key_value(max(bound, order_key(-FLT_MAX)));
     if (m >= reach) {
-        for (uint32_t left = reaching(v, reach); left; left &= left - 1) {
-            const int bit = __ffs(left) - 1, e = sizeof(T) == 2 ? 2 * (bit & 15) + (bit >> 4) : bit;
-            const int c = c0 + (e / V * kThreads + tid) * V + e % V;
-            const int i = atomicAdd(&count, 1);
-            if (i < kList) list[i] = (unsigned long long)order_key(to_f32(x[c])) << 32 | (uint32_t)~c;      // (read again: few are)
-        }
+        constexpr int kGroup = E < 32 ? E : 32;
+#pragma unroll
+        for (int g = 0; g < E; g += kGroup)
+            for (uint32_t left = reaching<kGroup>(v + g, reach); left; left &= left - 1) {
+                const int bit = __ffs(left) - 1, e = g + (sizeof(T) == 2 ? 2 * (bit & 15) + (bit >> 4) : bit);
+                const int c = c0 + (e / V * kThreads + tid) * V + e % V;
+                const int i = atomicAdd(&count, 1);
+                if (i < kList) list[i] = (unsigned long long)order_key(to_f32(x[c])) << 32 | (uint32_t)~c;      // (read again: few are)
+            }
     }
     __syncthreads();
     if (tid == 0) {
@@ -184,19 +204,20 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) beam_scan_ke
         for (int i = tid; i < n; i += kThreads) {
             const unsigned long long k = list[i];
             int rank = 0;
+#pragma unroll 4
             for (int j = 0; j < n; ++j) rank += list[j] > k;
             if (rank < a.out) out[rank] = k;
         }
         for (int i = n + tid; i < a.out; i += kThreads) out[i] = 0ull;
         return;
     }
+    // (the logits are read again: kept until here they would cost every CTA registers)
     unsigned long long last = ~0ull;
     for (int r = 0; r < a.out; ++r) {
         unsigned long long best = 0ull;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float y = to_f32(v[e]);
-            const unsigned long long k = y > -INFINITY ? (unsigned long long)order_key(y) << 32 | (uint32_t)~column(e) : 0ull;
+        for (int i = tid; i < kThreads * E && c0 + i < a.vocab; i += kThreads) {
+            const float y = to_f32(x[c0 + i]);
+            const unsigned long long k = y > -INFINITY ? (unsigned long long)order_key(y) << 32 | (uint32_t)~(c0 + i) : 0ull;
             if (k < last && k > best) best = k;
         }
 #pragma unroll
@@ -244,7 +265,8 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamArgs a) {
     pdl_wait();
     if (tid == 0) count = 0;
     const int lists = a.beams * a.chunks;
-    // lists are dealt to as many warps as they fill, one after the other, so that the warps have about as many
+    // lists are dealt to as many warps as they fill, one after the other, so that the warps have about as many.  (To all warps, with
+    // fewer lists each: a bound so low that 110 us were taken for 64.)
     const int warps = min((lists + 31) / 32, kMergeWarps);
     const int mine_at = warp + warps * lane;
     const bool has = warp < warps && mine_at < lists;
@@ -341,6 +363,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamArgs a) {
         for (int i = tid; i < n; i += kMergeThreads) {
             const Cont e = {keys[i], ats[i]};
             int rank = 0;
+#pragma unroll 4
             for (int j = 0; j < n; ++j) rank += Cont{keys[j], ats[j]}.better(e);
             if (rank < a.out) won[rank] = e;
         }
@@ -415,9 +438,11 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamArgs a) {
     }
 }
 
-int64_t chunk_of(int64_t rows, int64_t vocab) {
-    // short chunks while long ones would leave SMs without work
-    return rows * ((vocab + 32 * kThreads - 1) / (32 * kThreads)) < 2 * 152 ? 8 * kThreads : 32 * kThreads;
+// Logits to a thread: few while more would leave SMs without work, many where there is plenty (a CTA's barriers and its list
+// take as long whatever it holds)
+int logits_of(int64_t rows, int64_t vocab, int dtype) {
+    auto ctas = [&](int n) { return rows * ((vocab + n * kThreads - 1) / (n * kThreads)); };
+    return ctas(32) < 2 * 152 ? 8 : dtype != IDX_F32 && ctas(64) >= 8 * 152 ? 64 : 32;
 }
 
 template <typename T, int E>
@@ -433,7 +458,12 @@ template <typename T>
 cudaError_t run(const BeamArgs& a, cudaStream_t st) {
     // (one order of a row's elements for every row of the call: equal rows get equal sums)
     const bool vec = reinterpret_cast<uintptr_t>(a.b.logits) % 16 == 0 && a.b.logit_stride * (int64_t)sizeof(T) % 16 == 0;
-    cudaError_t e = chunk_of((int64_t)a.seqs * a.beams, a.vocab) == 8 * kThreads ? scan<T, 8>(a, vec, st) : scan<T, 32>(a, vec, st);
+    cudaError_t e;
+    switch (a.per_thread) {
+        case 8: e = scan<T, 8>(a, vec, st); break;
+        case 32: e = scan<T, 32>(a, vec, st); break;
+        default: e = scan<T, sizeof(T) == 2 ? 64 : 32>(a, vec, st);
+    }
     if (e != cudaSuccess) return e;
     return launch_pdl(beam_merge_kernel, dim3((unsigned)a.seqs), dim3(kMergeThreads), 0, st, a);
 }
@@ -441,7 +471,8 @@ cudaError_t run(const BeamArgs& a, cudaStream_t st) {
 }  // namespace
 
 int64_t beam_workspace_bytes(int64_t seqs, int64_t beams, int64_t out, int64_t vocab) {
-    const int64_t rows = seqs * beams, chunk = chunk_of(rows, vocab), chunks = (vocab + chunk - 1) / chunk;
+    // (of the type that takes the shorter chunks)
+    const int64_t rows = seqs * beams, chunk = logits_of(rows, vocab, IDX_F32) * kThreads, chunks = (vocab + chunk - 1) / chunk;
     return rows * chunks * (int64_t)(sizeof(Part) + out * sizeof(unsigned long long));
 }
 
@@ -453,7 +484,9 @@ cudaError_t launch_beam(const idx_beam& b, int dtype, int seqs, int beams, int o
     a.out = out;
     a.vocab = vocab;
     a.end = end;
-    const int64_t rows = (int64_t)seqs * beams, chunk = chunk_of(rows, vocab);
+    const int64_t rows = (int64_t)seqs * beams;
+    a.per_thread = logits_of(rows, vocab, dtype);
+    const int64_t chunk = a.per_thread * kThreads;
     a.chunks = (int)((vocab + chunk - 1) / chunk);
     a.parts = static_cast<Part*>(ws);
     a.cand = reinterpret_cast<unsigned long long*>(a.parts + rows * a.chunks);
