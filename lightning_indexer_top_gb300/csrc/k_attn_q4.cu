@@ -9,6 +9,8 @@
 // weights p_j s_j are rounded to f16 at a running maximum of theirs; centring the codes keeps that rounding as small as
 // the values' own.  The order of columns within a product is free, so a lane takes 16 bytes of a key's codes as they lie and q is laid
 // out to match.
+#include <algorithm>
+
 #include "q4.cuh"
 #include "sm100_ptx.cuh"
 
@@ -64,22 +66,23 @@ __device__ __forceinline__ Cut cut_of(const Geom& g, const Q4Args& p, int at, bo
         return c;
     }
     const int64_t columns = (int64_t)p.a.Hkv * p.row_tiles;
+    const int few = lane < g.B ? est_tiles(g, p.a.mods, lane) : 0;      // (the first 32 sequences' stay at hand)
+    auto est = [&](int b0) { return b0 == 0 ? few : b0 + lane < g.B ? est_tiles(g, p.a.mods, b0 + lane) : 0; };
     int64_t total = 0;
-    for (int b0 = 0; b0 < g.B; b0 += 32)
-        total += __reduce_add_sync(0xffffffffu, b0 + lane < g.B ? est_tiles(g, p.a.mods, b0 + lane) : 0);
+    for (int b0 = 0; b0 < g.B; b0 += 32) total += __reduce_add_sync(0xffffffffu, est(b0));
     int len = (int)min((total * columns + p.slots - 1) / p.slots, (int64_t)1 << 25);
     if (len < kMinTiles) len = kMinTiles;
-    auto pieces_of = [&](int q) { return q < g.B ? max((est_tiles(g, p.a.mods, q) + len - 1) / len, 1) : 0; };
+    auto pieces_of = [&](int b0) { return b0 + lane < g.B ? max((est(b0) + len - 1) / len, 1) : 0; };
     // (rounding up each row's pieces takes more than the slots: longer ones, a few tries)
     for (int i = 0; i < 4; ++i) {
         int64_t n = 0;
-        for (int b0 = 0; b0 < g.B; b0 += 32) n += __reduce_add_sync(0xffffffffu, pieces_of(b0 + lane));
+        for (int b0 = 0; b0 < g.B; b0 += 32) n += __reduce_add_sync(0xffffffffu, pieces_of(b0));
         if (n * columns <= p.slots) break;
         len += (len + 15) / 16;
     }
     int before = 0;
     for (int b0 = 0; b0 < g.B; b0 += 32) {
-        const int mine = pieces_of(b0 + lane);
+        const int mine = pieces_of(b0);
         int incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -700,77 +703,71 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NB>::kCtas) q4_kernel(const
     }
 }
 
-// a CTA per packed row: its pieces shared by the warps, in a fixed order
+// A CTA per packed row: its pieces shared by the warps, in a fixed order, four columns to a lane (heads of 64: half a warp to a
+// piece) and kAtOnce pieces' loads on their way together.
+constexpr int kMergeWarps = 16, kAtOnce = 4;
+
 template <typename T, int D, int NB>
-__global__ void __launch_bounds__(kThreads) q4_merge_kernel(Q4Args p, Geom g) {
-    constexpr int R = 8 * NB, C = D / 32;
-    __shared__ float m_s[kWarps], l_s[kWarps], o_s[kWarps][D];
+__global__ void __launch_bounds__(32 * kMergeWarps) q4_merge_kernel(Q4Args p, Geom g) {
+    constexpr int R = 8 * NB, L = D / 4;       // lanes of a piece
+    __shared__ float m_s[kMergeWarps * 2], l_s[kMergeWarps * 2];
+    __shared__ __align__(16) float o_s[kMergeWarps * 2][D];
     const DenseArgs& a = p.a;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int lane = threadIdx.x % L, part = threadIdx.x / L, parts = blockDim.x / L;
     const int G = a.Hq / a.Hkv;
-    const int64_t rh = blockIdx.x, row = rh / a.Hq;
-    const int h = (int)(rh - row * a.Hq), gkv = h / G, b = (int)(row / g.T);
-    const int64_t m = (row - (int64_t)b * g.T) * G + h % G;
+    const int rh = blockIdx.x, row = rh / a.Hq, h = rh - row * a.Hq, gkv = h / G, b = row / g.T;
+    const int64_t m = (int64_t)(row - b * g.T) * G + h % G;
     pdl_wait();
     const Cut cut = cut_of(g, p, b, false);
     const int columns = a.Hkv * p.row_tiles;
     const int64_t first = ((int64_t)cut.first * columns + (m / R) * a.Hkv + gkv) * R + m % R, step = (int64_t)columns * R;
-    float M = -INFINITY, l = 0.f, acc[C];
+    float M = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = part * kAtOnce; s0 < cut.pieces; s0 += parts * kAtOnce) {
+        float2 ml[kAtOnce];
+        float4 x[kAtOnce];
 #pragma unroll
-    for (int i = 0; i < C; ++i) acc[i] = 0.f;
-    for (int s0 = warp * 4; s0 < cut.pieces; s0 += kWarps * 4) {
-        float2 ml[4];
-        float x[4][C];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kAtOnce; ++i) {
             const int64_t at = first + (int64_t)min(s0 + i, cut.pieces - 1) * step;
             ml[i] = *reinterpret_cast<const float2*>(p.part_ml + 2 * at);
             if (s0 + i >= cut.pieces) ml[i].y = 0.f;
-#pragma unroll
-            for (int k = 0; k < C; ++k) x[i][k] = p.part_o[at * D + lane + 32 * k];
+            x[i] = *reinterpret_cast<const float4*>(p.part_o + at * D + 4 * lane);
         }
         float top = M;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < kAtOnce; ++i)
             if (ml[i].y != 0.f) top = fmaxf(top, ml[i].x);
         const float al = M == -INFINITY ? 0.f : exp2f(M - top);
         M = top;
         l *= al;
+        acc = make_float4(acc.x * al, acc.y * al, acc.z * al, acc.w * al);
 #pragma unroll
-        for (int k = 0; k < C; ++k) acc[k] *= al;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kAtOnce; ++i) {
             if (ml[i].y == 0.f) continue;      // (a piece without keys)
             const float w = exp2f(ml[i].x - M);
             l = fmaf(w, ml[i].y, l);
-#pragma unroll
-            for (int k = 0; k < C; ++k) acc[k] = fmaf(w, x[i][k], acc[k]);
+            acc = make_float4(fmaf(w, x[i].x, acc.x), fmaf(w, x[i].y, acc.y), fmaf(w, x[i].z, acc.z), fmaf(w, x[i].w, acc.w));
         }
     }
     if (lane == 0) {
-        m_s[warp] = M;
-        l_s[warp] = l;
+        m_s[part] = M;
+        l_s[part] = l;
     }
-#pragma unroll
-    for (int k = 0; k < C; ++k) o_s[warp][lane + 32 * k] = acc[k];
+    *reinterpret_cast<float4*>(&o_s[part][4 * lane]) = acc;
     __syncthreads();
+    if (threadIdx.x >= D) return;
+    const int used = min(parts, (cut.pieces + kAtOnce - 1) / kAtOnce);
     M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w)
+    for (int w = 0; w < used; ++w)
         if (l_s[w] != 0.f) M = fmaxf(M, m_s[w]);
-    float den = 0.f, f[kWarps];
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        f[w] = l_s[w] != 0.f ? exp2f(m_s[w] - M) : 0.f;
-        den = fmaf(f[w], l_s[w], den);
+    float den = 0.f, y = 0.f;
+    for (int w = 0; w < used; ++w) {
+        if (l_s[w] == 0.f) continue;
+        const float f = exp2f(m_s[w] - M);
+        den = fmaf(f, l_s[w], den);
+        y = fmaf(f, o_s[w][threadIdx.x], y);
     }
-    for (int cc = threadIdx.x; cc < D; cc += kThreads) {
-        float y = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w)
-            if (l_s[w] != 0.f) y = fmaf(f[w], o_s[w][cc], y);
-        static_cast<T*>(a.out)[rh * D + cc] = from_f32<T>(den == 0.f ? 0.f : y / den);
-    }
+    static_cast<T*>(a.out)[(int64_t)rh * D + threadIdx.x] = from_f32<T>(den == 0.f ? 0.f : y / den);
     if (threadIdx.x == 0 && a.lse) a.lse[rh] = den == 0.f ? -INFINITY : (M + log2f(den)) * kLn2;
 }
 
@@ -778,6 +775,8 @@ size_t split_bytes(int64_t n_rows, int Hq, int dv) { return (size_t)n_rows * Hq 
 
 int n_blocks(int64_t packed) { return packed <= 8 ? 1 : 2; }
 
+// The pieces of all rows: as many as the SMs hold at once.  (Three times as many: 16 x 32768 keys 76 us for 65 with a packed row
+// tile, 278 for 300 with four; one sequence of these 50 for 39.)
 int slots_of(int nb) {
     int sms = sm_count();
     return (sms < 2 ? 152 : sms) * (nb == 1 ? Shape<128, 1>::kCtas : Shape<128, 2>::kCtas);
@@ -847,7 +846,11 @@ cudaError_t go(const DenseArgs& a, const Geom& g, void* ws, size_t ws_bytes, cud
     const cudaError_t e = mods ? launch(q4_kernel<T, D, NB, true>) : launch(q4_kernel<T, D, NB, false>);
     if (e != cudaSuccess || !p.part_o) return e;
     const int64_t n = (int64_t)g.B * g.T * a.Hq;
-    return launch_pdl(q4_merge_kernel<T, D, NB>, dim3((unsigned)n), dim3(kThreads), 0, st, p, g);
+    // as many threads as the longest row's pieces may need, and as the columns of a row
+    const int64_t most = std::min<int64_t>(slots / columns + 1, ((int64_t)g.max_n_kv + kTile * kMinTiles - 1) / (kTile * kMinTiles));
+    int threads = (int)std::min<int64_t>((most + kAtOnce - 1) / kAtOnce * (D / 4), 32 * kMergeWarps);
+    threads = std::max((threads + 31) / 32 * 32, D);
+    return launch_pdl(q4_merge_kernel<T, D, NB>, dim3((unsigned)n), dim3(threads), 0, st, p, g);
 }
 
 // The positions that some row of a sequence sees, and nothing lost yet
