@@ -708,7 +708,7 @@ idx_status idx_cache_append_q4(const idx_new_rows* rows, idx_dtype dtype, int32_
  * [B*T, n_kv_heads, dk] and v_out [B*T, n_kv_heads, dv] (contiguous, of dtype) becomes
  * position p of the row's sequence, positions as idx_cache_append takes them.  Padding
  * rows, and rows that are out of range (flagged), stay as they were.
- *   v_cache, v_out  both NULL with dv 0: one cache.
+ *   k_out, v_out  16-byte aligned.  v_cache and v_out both NULL with dv 0: one cache.
  */
 idx_status idx_cache_read_q4(const void* k_cache, int64_t k_row_stride, const void* v_cache, int64_t v_row_stride,
                              int64_t kv_rows, int32_t n_kv_heads, int32_t dk, int32_t dv, idx_batch batch,
@@ -719,15 +719,16 @@ idx_status idx_cache_read_q4(const void* k_cache, int64_t k_row_stride, const vo
  * results and errors, K and V being the values that the codes stand for.
  *   k_cache, v_cache  rows of bytes, strides in BYTES (see above); dk and dv multiples of
  *              8.  There is no latent form.
- *   workspace  dense_attn_q4_workspace_size(...) bytes, 16-byte aligned.  With less (or
- *              NULL) the call takes another way, with the same results up to rounding:
+ *   workspace  dense_attn_q4_workspace_size(...) bytes, 16-byte aligned, not shared with
+ *              calls whose work overlaps this one's.  With less (or NULL) the call takes
+ *              another way, with the same results up to rounding:
  *              fewer key splits, codes that each tile of rows expands for itself instead
  *              of once for all, or the CUDA cores.
  * 16-bit q runs on the tensor cores, given 16-byte aligned tensors and rows: up to 256 packed
  * rows (tokens x heads of a kv head) of heads of 64 or 128 columns (dk == dv) on the codes
  * themselves; more rows, and other heads of at most 128 columns, on K and V expanded in the
- * workspace, K in two parts (16 bits of significand together in BF16, 22 in F16), V rounded to
- * dtype.  Weights are rounded for the second product: to f16 with the values' scale (codes), or
+ * workspace (to 64 GB, counted by max_n_kv), K in two parts (16 bits of significand together in
+ * BF16, 22 in F16, nothing below F16's least number), V rounded to dtype.  Weights are rounded for the second product: to f16 with the values' scale (codes), or
  * to dtype.  Everything else runs on the CUDA cores in f32.
  */
 idx_status dense_attn_q4(const void* q, idx_dtype dtype, int32_t n_q_heads, int32_t n_kv_heads, int32_t dk, int32_t dv,

@@ -963,6 +963,8 @@ def _append(fn, q4: bool, k, v, k_cache, v_cache, batch, q, q_out, inv_freq, rot
     if inv_freq is not None:
         if inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
             raise ValueError("inv_freq must be a contiguous float32 tensor of one dimension")
+        if not 0 <= rot_start <= dk:
+            raise ValueError("rot_start must be a column of the head")
         rope = _Rope(inv_freq.data_ptr(), 2 * inv_freq.numel(), rot_start, 1 if interleaved else 0)
     with _On(dev):
         _check(fn(_NewRows(k_ptr, k_stride, v_ptr, v_stride, q_ptr, q_stride, qo_ptr, qo_stride), dt, hq, hkv, dk, dv, b,
@@ -1123,6 +1125,8 @@ def idx_beam_step(logits: torch.Tensor, scores: torch.Tensor, n_beams: int, *, n
     if rows > 1 and logits.stride(0) < vocab:
         raise ValueError("the rows of logits must not overlap")
     n_seq, n_out = rows // n_beams, n_beams if n_out is None else n_out
+    if not -2**31 <= end_token < 2**31:
+        raise ValueError("end_token must be below 2**31")
     dt = _dtype(logits)
     if scores.dtype is not torch.float32 or scores.numel() != rows or not scores.is_contiguous():
         raise ValueError("scores must be a contiguous float32 tensor with one entry per row of logits")

@@ -670,6 +670,9 @@ __global__ void __launch_bounds__(kThreads) read_q4_kernel(ExpandArgs p, Geom g,
         T* rest = kExpand ? static_cast<T*>(p.k_rest) + (dst - static_cast<T*>(a.k_out)) : nullptr;
         const float* pair = reinterpret_cast<const float*>(src + a.Hkv * (w / 2)) + 2 * h;
         const float scale = pair[0], low = pair[1];
+        if (kExpand && isfinite(scale) && isfinite(low) &&
+            isinf(to_f32(from_f32<T>(fmaxf(fabsf(low), fabsf(fmaf(15.f, scale, low)))))))
+            *p.lost = 1;      // (numbers, but not of type T)
         uint32_t x[kCols / 8];
         if constexpr (kWide)
             *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(src + u * 16);

@@ -896,9 +896,12 @@ struct Expanded {
 };
 
 // Whether a call of these sizes expands K and V (given the workspace): where the codes would be expanded for many tiles of rows,
-// or for heads that the few-rows kernel does not take.
-bool expands(int dtype, int64_t packed, int dk, int dv) {
+// or for heads that the few-rows kernel does not take; up to 64 GB of them (the bound max_n_kv counts, not what it turns out).
+constexpr int64_t kMaxExpanded = (int64_t)1 << 36;
+
+bool expands(int dtype, int64_t n_seq, int64_t packed, int64_t max_n_kv, int Hkv, int dk, int dv) {
     if (dtype == IDX_F32 || dk > 128 || dv > 128) return false;
+    if (n_seq * max_n_kv > kMaxExpanded / (Hkv * (4 * (int64_t)dk + 2 * dv))) return false;
     return packed > kManyRows || dk != dv || (dk != 64 && dk != 128);
 }
 
@@ -912,7 +915,7 @@ cudaError_t run_few(const DenseArgs& a, const Geom& g, void* ws, size_t ws_bytes
 }  // namespace
 
 size_t q4_attn_workspace_bytes(int dtype, int64_t n_seq, int64_t n_q, int64_t max_n_kv, int Hq, int Hkv, int dk, int dv) {
-    if (expands(dtype, n_q * (Hq / Hkv), dk, dv)) return Expanded(n_seq, max_n_kv, Hkv, dk, dv).bytes;
+    if (expands(dtype, n_seq, n_q * (Hq / Hkv), max_n_kv, Hkv, dk, dv)) return Expanded(n_seq, max_n_kv, Hkv, dk, dv).bytes;
     if (dtype != IDX_F32 && dk == dv && (dk == 64 || dk == 128)) {
         const int64_t packed = n_q * (Hq / Hkv);
         const int nb = n_blocks(packed);
@@ -926,7 +929,8 @@ size_t q4_attn_workspace_bytes(int dtype, int64_t n_seq, int64_t n_q, int64_t ma
 // K and V of the span that some row sees, expanded, then dense_attn's tensor-core kernel on them: V rounded to dtype, K as a
 // sum of two (16 or 22 bits), since the log of the weights' sum is f32.  (Scales applied to the products of exact codes, in
 // the softmax: 4096 rows on 16384 keys 1455 us, for 740 without; it is the softmax that the kernel waits for.)  What that kernel cannot know
-// of, keys without a row in the cache, sends everything through the CUDA cores again, which skip and flag them one by one.
+// of, keys without a row in the cache and values beyond dtype's range, sends everything through the CUDA cores again, which skip
+// and flag the one and hold the other in f32.
 static cudaError_t run_expanded(DenseArgs a, int dtype, const Geom& g, uint8_t* ws, cudaStream_t st) {
     const Expanded e(g.B, g.max_n_kv, a.Hkv, a.dk, a.dv);
     int2* span = reinterpret_cast<int2*>(ws);
@@ -975,7 +979,7 @@ static cudaError_t run_expanded(DenseArgs a, int dtype, const Geom& g, uint8_t* 
 }
 
 cudaError_t launch_attn_q4(DenseArgs a, int dtype, const Geom& g, void* ws, size_t ws_bytes, cudaStream_t st) {
-    if (g.max_n_kv > 0 && expands(dtype, (int64_t)g.T * (a.Hq / a.Hkv), a.dk, a.dv) &&
+    if (g.max_n_kv > 0 && expands(dtype, g.B, (int64_t)g.T * (a.Hq / a.Hkv), g.max_n_kv, a.Hkv, a.dk, a.dv) &&
         ws_bytes >= Expanded(g.B, g.max_n_kv, a.Hkv, a.dk, a.dv).bytes) {
         const cudaError_t e = run_expanded(a, dtype, g, static_cast<uint8_t*>(ws), st);
         if (e != cudaErrorNotSupported) return e;

@@ -419,6 +419,7 @@ def test_binding_refuses():
                 dict(kc=x(8, 2, 32)), dict(kc=x(8, 2, 64, dtype=torch.bfloat16)), dict(kc=x(6, 2, 64)), dict(kc=x(8, 64, 2).transpose(1, 2)),
                 dict(k=x(4, 2, 128)[..., ::2]), dict(k=x(1, 2, 64).expand(4, 2, 64)), dict(q=x(4, 3, 32)), dict(q_out=x(4, 3, 64)),
                 dict(q=x(4, 3, 64), q_out=x(4, 2, 64)), dict(inv_freq=f.double()), dict(inv_freq=f[::2]), dict(k=k.cpu()), dict(v=v.cpu()),
+                dict(inv_freq=f, rot_start=2 ** 32), dict(inv_freq=f, rot_start=-1),
                 dict(b=L.Batch(n_kv, 2, 4, kv_start=torch.zeros(1, dtype=torch.int32, device="cuda"))),
                 dict(b=L.Batch(n_kv, 2, 4, q_pos=torch.zeros(3, dtype=torch.int32, device="cuda")))):
         with pytest.raises(ValueError):

@@ -297,6 +297,60 @@ def test_pages_out_of_range_are_skipped_and_flagged_where_seen(dtype, T, page):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("page", [16, 5])
+def test_many_rows_and_pages_out_of_range(dtype, page):
+    c = Case4([200, 180], 70, 8, 2, 128, dtype=dtype, page=page, window=75, seed=9)
+    lost = 130 // page
+    c.table[0, lost], c.table[0, 0], c.table[1, lost] = -1, c.k.shape[0] // page, 10 ** 6      # page 0 is seen by nobody
+    for b in (0, 1):
+        c.rows[b] = c.rows[b].clone()
+        c.rows[b][lost * page:(lost + 1) * page] = -1
+    c.check(*c.run())
+    assert L.idx_device_status(reset=True) == L.IDX_ERR_DEVICE_BOUNDS
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,d", [(1, 128), (40, 64), (70, 128), (70, 64), (3, 80)])
+def test_values_beyond_half_precision(dtype, T, d):
+    c = Case4([200, 180], T, 8, 2, d, dtype=dtype, seed=11)
+    c.q = (c.q * 1e-4).to(c.q.dtype)
+    c.recode(0, int(c.rows[0][5]), 1, None, 1e4, -2e4)
+    c.recode(1, int(c.rows[1][6]), 0, None, 1e4, -2e4)
+    c.check(*c.run())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_many_rows_captured_with_a_page_that_comes_back(dtype):
+    c = Case4([200, 180], 70, 8, 2, 128, dtype=dtype, page=16, seed=12)
+    q = c.q.reshape(c.B * c.T, 8, 128).cuda()
+    caches, batch, lse = [x.cuda() for x in c.caches], c.batch(), torch.zeros(c.B * c.T, 8, device="cuda")
+    ws = torch.empty(L.dense_attn_q4_workspace_size(dtype, 2, 70, batch.max_n_kv, 8, 2, 128, 128), dtype=torch.uint8, device="cuda")
+    call = lambda: L.dense_attn_q4(q, *caches, batch, c.scale, 2, lse=lse, workspace=ws)  # noqa: E731
+    first, first_lse = call().clone(), lse.clone()
+    c.check(first, first_lse)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call()
+    entry = batch.page_table[1, 3].clone()
+    batch.page_table[1, 3] = -1
+    graph.replay()
+    torch.cuda.synchronize()
+    assert L.idx_device_status(reset=True) == L.IDX_ERR_DEVICE_BOUNDS
+    kept = c.rows[1]
+    c.rows[1] = kept.clone()
+    c.rows[1][48:64] = -1
+    c.check(out, lse)
+    c.rows[1] = kept
+    batch.page_table[1, 3] = entry
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, first) and torch.equal(lse, first_lse) and L.idx_device_status(reset=True) == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [1, 40])
 def test_rows_past_a_contiguous_cache_are_skipped(T):
     c = Case4([120, 120], T, 8, 2, 64, dtype=torch.bfloat16, seed=10)
@@ -399,6 +453,11 @@ def test_workspace_of_nonsense_sizes_is_0():
         a = list(good)
         a[i] = x
         assert L.dense_attn_q4_workspace_size(*a) == 0
+
+
+def test_the_workspace_is_bounded():
+    for n, h in ((1, 1), (64, 8), (2 ** 20, 128), (2 ** 31 - 1, 2 ** 20)):
+        assert 0 <= L.dense_attn_q4_workspace_size(torch.bfloat16, n, 4096, 2 ** 31 - 1025, 8 * h, h, 128, 128) <= 2 ** 36 + 16 * n + 16
 
 
 @pytest.mark.gpu

@@ -358,7 +358,7 @@ def test_binding_refuses():
     i = lambda *a: torch.zeros(*a, dtype=torch.int32, device="cuda")  # noqa: E731
     L.idx_beam_step(x, s, 4)
     for bad in (dict(x=x[:7]), dict(x=x.T), dict(x=x[:1].expand(8, 50)), dict(x=x.int()), dict(s=s[:7]), dict(s=s.double()), dict(s=s.cpu()),
-                dict(W=0), dict(W=3), dict(done=s, end_token=3), dict(done=torch.zeros(7, dtype=torch.uint8, device="cuda"), end_token=3),
+                dict(W=0), dict(W=3), dict(end_token=2 ** 32 + 3), dict(done=s, end_token=3), dict(done=torch.zeros(7, dtype=torch.uint8, device="cuda"), end_token=3),
                 dict(lengths=i(8)), dict(history=i(8, 4)), dict(lengths=i(7), history=i(8, 4)), dict(lengths=i(8), history=i(7, 4)),
                 dict(lengths=i(8), history=i(8, 4), history_out=i(8, 5)), dict(lengths=i(8), history=i(8, 4), history_out=i(7, 4)),
                 dict(out=L.BeamStep(s, i(7), i(8), torch.zeros(8, dtype=torch.uint8, device="cuda"), None, None)),
