@@ -26,9 +26,16 @@ struct DenseArgs {
                               // kDenseCluster splits), the splits are a cluster that merges them
     float* part_o;            // [row * Hq + head][split][dv] unnormalised
     float* part_ml;           // [row * Hq + head][split][2]: maximum (natural-log units), sum
-    const void* k_rest;       // or NULL.  Given (tensor cores): K is the sum of k and this, laid out alike
+    const void* k_rest;       // or NULL.  Given (tensor cores): K is the sum of k and this, laid out alike, and V f16
+    const int* v_top;         // ... at the power of two that v_exponent makes of this [B, Hkv]
     const int* only_if;       // or NULL; given and 0 on the device: the launch has nothing to do (CUDA cores, 4 bits)
 };
+
+// The power of two at which f16 holds numbers of magnitudes up to top (a float's bits) as numbers below 2^15, so that those
+// 2^28 below the largest keep f16's eleven bits: -126 .. 113; and 2^n, n in [-126, 127]
+__device__ __forceinline__ int v_exponent(int top) { return max((top >> 23) - 127, -112) - 14; }
+
+__device__ __forceinline__ float exp2_whole(int n) { return __int_as_float((n + 127) << 23); }
 
 struct Interval {
     int lo, hi;               // visible positions [lo, hi); lo >= hi: none

@@ -670,7 +670,7 @@ __global__ void __launch_bounds__(kThreads) read_q4_kernel(ExpandArgs p, Geom g,
         T* rest = kExpand ? static_cast<T*>(p.k_rest) + (dst - static_cast<T*>(a.k_out)) : nullptr;
         const float* pair = reinterpret_cast<const float*>(src + a.Hkv * (w / 2)) + 2 * h;
         const float scale = pair[0], low = pair[1];
-        if (kExpand && isfinite(scale) && isfinite(low) &&
+        if (kExpand && is_k && isfinite(scale) && isfinite(low) &&
             isinf(to_f32(from_f32<T>(fmaxf(fabsf(low), fabsf(fmaf(15.f, scale, low)))))))
             *p.lost = 1;      // (numbers, but not of type T)
         uint32_t x[kCols / 8];
@@ -679,6 +679,18 @@ __global__ void __launch_bounds__(kThreads) read_q4_kernel(ExpandArgs p, Geom g,
         else
             x[0] = *reinterpret_cast<const uint32_t*>(src + u * 4);
         constexpr int E = 16 / (int)sizeof(T);
+        if (kExpand && !is_k) {
+            const float f = exp2_whole(-v_exponent(p.v_top[(r0 + i) / g.T * a.Hkv + h]));
+#pragma unroll
+            for (int c = 0; c < kCols; c += 8) {
+                __half y[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    y[j] = from_f32<__half>(fmaf((float)((x[c / 8] >> (4 * j)) & 15u), scale, low) * f);
+                *reinterpret_cast<uint4*>(dst + c) = *reinterpret_cast<const uint4*>(y);
+            }
+            continue;
+        }
 #pragma unroll
         for (int c = 0; c < kCols; c += E) {
             T y[E], z[E];
@@ -688,7 +700,7 @@ __global__ void __launch_bounds__(kThreads) read_q4_kernel(ExpandArgs p, Geom g,
                 y[j] = from_f32<T>(v);
                 if (kExpand) z[j] = from_f32<T>(v - to_f32(y[j]));
             }
-            if (kExpand && is_k) *reinterpret_cast<uint4*>(rest + c) = *reinterpret_cast<const uint4*>(z);
+            if (kExpand) *reinterpret_cast<uint4*>(rest + c) = *reinterpret_cast<const uint4*>(z);
             *reinterpret_cast<uint4*>(dst + c) = *reinterpret_cast<const uint4*>(y);
         }
     }

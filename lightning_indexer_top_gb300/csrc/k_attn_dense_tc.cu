@@ -118,7 +118,7 @@ struct TcArgs {
 
 // A row's attention key by key, for the thread that owns it: the rare way, see the top.  q, K and V as stored, f32
 // sums.  acc gets the unnormalised values, ml the maximum (log2 units) and the sum.
-template <typename T>
+template <typename T, typename V>
 __device__ __noinline__ void scalar_row(const DenseArgs& a, const Geom& g, int b, int gkv, int64_t rh, int h, Interval iv,
                                         int64_t s0, int64_t s1, float* acc, float* ml) {
     const T* q = static_cast<const T*>(a.q) + rh * a.dk;
@@ -132,7 +132,7 @@ __device__ __noinline__ void scalar_row(const DenseArgs& a, const Geom& g, int b
             continue;
         }
         const T* k = static_cast<const T*>(a.k) + row * a.k_stride + (int64_t)gkv * a.dk;
-        const T* v = static_cast<const T*>(a.v) + row * a.v_stride + (int64_t)gkv * a.dv;
+        const V* v = static_cast<const V*>(a.v) + row * a.v_stride + (int64_t)gkv * a.dv;
         const T* rest = a.k_rest ? static_cast<const T*>(a.k_rest) + row * a.k_stride + (int64_t)gkv * a.dk : nullptr;
         float x = 0.f;
         for (int c = 0; c < a.dk; ++c) x = fmaf(to_f32(q[c]), to_f32(k[c]) + (rest ? to_f32(rest[c]) : 0.f), x);
@@ -203,14 +203,16 @@ __device__ __forceinline__ void store_rows(E* out, int64_t at, int n_rows, const
 }
 
 // kTwo: K is the sum of two tensors of T, for keys that T alone does not hold (values of 4-bit codes): the scores are two
-// products into the same accumulators.
+// products into the same accumulators.  V and the weights are f16 then, V at a power of two.
 template <typename T, int D, int kTiles, bool kMods, bool kTwo>
 __global__ void __launch_bounds__(Cfg<D, kTiles, kTwo>::kThreads, Cfg<D, kTiles, kTwo>::kCtas)
     dense_tc_kernel(TcArgs p, Geom g, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                     const __grid_constant__ CUtensorMap rmap) {
     using C = Cfg<D, kTiles, kTwo>;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-    constexpr float kShift = kBf16 ? 0.f : 7.f;     // P is kept this much (log2) larger
+    using V = std::conditional_t<kTwo, __half, T>;
+    constexpr bool kBf16V = std::is_same<V, __nv_bfloat16>::value;
+    constexpr float kShift = kBf16V ? 0.f : 7.f;    // P is kept this much (log2) larger
     constexpr float kTop = kShift + 8.f;
     constexpr bool kDouble = kDoubleS<D, kMods>;
     extern __shared__ uint8_t smem_raw[];
@@ -415,7 +417,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kTwo>::kThreads, Cfg<D, kTiles,
             // short, so the tensor pipe idles while an issuer waits or commits: it has the other issuer's then.
             const int i = warp - 1;
             const uint32_t id_qk = idesc_f16_f32_major(kRows, kDouble ? kHalf : kKeys, kBf16 ? 1 : 0, 0, 0);
-            const uint32_t id_pv = idesc_f16_f32_major(kRows, (a.dv + 15) & ~15, kBf16 ? 1 : 0, 0, 1);
+            const uint32_t id_pv = idesc_f16_f32_major(kRows, (a.dv + 15) & ~15, kBf16V ? 1 : 0, 0, 1);
             const uint64_t kmajor = desc_sw128_kmajor(0, 1024), mnmajor = desc_sw128_mnmajor(0, kColBlock, 1024);
             const uint32_t k_hi = desc_hi(kmajor), v_hi = desc_hi(mnmajor), k_lo = (uint32_t)kmajor, v_lo = (uint32_t)mnmajor;
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -536,7 +538,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kTwo>::kThreads, Cfg<D, kTiles,
                         } else if (key0 + row < full0 || key0 + row >= full1) {
                             const uint4 y[2] = {x[0], x[1]};
                             const uint32_t* z = reinterpret_cast<const uint32_t*>(y);
-                            constexpr uint32_t kExp = kBf16 ? 0x7F80u : 0x7C00u;
+                            constexpr uint32_t kExp = kBf16V ? 0x7F80u : 0x7C00u;
 #pragma unroll
                             for (int i = 0; i < 8; ++i)
                                 found |= (z[i] & kExp) == kExp || (z[i] & (kExp << 16)) == (kExp << 16);
@@ -659,7 +661,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kTwo>::kThreads, Cfg<D, kTiles,
                     la = add2(la, pair(p0, p1));
                 else
                     lb = add2(lb, pair(p0, p1));
-                w[i / 2] = pack2<T>(p0, p1);
+                w[i / 2] = pack2<V>(p0, p1);
             }
             tmem_st_32x32b_x32(ts + half * (kDouble ? kHalf : kHalf / 2), w);
             float l0, l1;
@@ -683,13 +685,14 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kTwo>::kThreads, Cfg<D, kTiles,
         float acc[D];
         if (by_key) {
             float ml[2] = {-INFINITY, 0.f};
-            if (has_row && some) scalar_row<T>(a, g, b, gkv, rh, h, iv, s0, s1, acc, ml);
+            if (has_row && some) scalar_row<T, V>(a, g, b, gkv, rh, h, iv, s0, s1, acc, ml);
             m_used = ml[0];
             l_run = ml[1];
             __syncwarp();
         }
         const float l = some && ok ? l_run : 0.f;
-        const float inv = l == 0.f ? 0.f : a.splits > 1 ? 1.f : 1.f / l;
+        const float unit = kTwo ? exp2_whole(v_exponent(a.v_top[(int64_t)b * a.Hkv + gkv])) : 1.f;
+        const float inv = l == 0.f ? 0.f : a.splits > 1 ? unit : unit / l;
         if (merge) {
             *reinterpret_cast<float2*>(smem + C::kMlOff + r * 8) = make_float2(m_used, l);
         } else if (has_row) {
@@ -808,7 +811,7 @@ cudaError_t run(const DenseArgs& a, const Geom& g, cudaStream_t st) {
     CUtensorMap km, vm, rm;
     constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
     if (!make_head_tmap(&km, a.k, bf16, a.dk, a.Hkv, a.k_stride, a.kv_rows, p.box) ||
-        !make_head_tmap(&vm, a.v, bf16, a.dv, a.Hkv, a.v_stride, a.kv_rows, p.box))
+        !make_head_tmap(&vm, a.v, bf16 && !kTwo, a.dv, a.Hkv, a.v_stride, a.kv_rows, p.box))
         return cudaErrorNotSupported;
     rm = km;
     if (kTwo && !make_head_tmap(&rm, a.k_rest, bf16, a.dk, a.Hkv, a.k_stride, a.kv_rows, p.box)) return cudaErrorNotSupported;

@@ -853,11 +853,12 @@ cudaError_t go(const DenseArgs& a, const Geom& g, void* ws, size_t ws_bytes, cud
     return launch_pdl(q4_merge_kernel<T, D, NB>, dim3((unsigned)n), dim3(threads), 0, st, p, g);
 }
 
-// The positions that some row of a sequence sees, and nothing lost yet
-__global__ void __launch_bounds__(256) span_kernel(idx_attn_mods mods, Geom g, int2* span, int* lost) {
+// The positions that some row of a sequence sees, and nothing lost or found yet
+__global__ void __launch_bounds__(256) span_kernel(idx_attn_mods mods, Geom g, int2* span, int* lost, int* top, int Hkv) {
     __shared__ int lo_s[8], hi_s[8];
     pdl_wait();
     const int b = blockIdx.x, warp = threadIdx.x >> 5;
+    for (int h = threadIdx.x; h < Hkv; h += 256) top[(int64_t)b * Hkv + h] = 0;
     const int n_kv = seq_n_kv(g, b);
     int lo = INT32_MAX, hi = 0;
     for (int t = threadIdx.x; t < g.T; t += 256) {
@@ -883,12 +884,42 @@ __global__ void __launch_bounds__(256) span_kernel(idx_attn_mods mods, Geom g, i
     if (b == 0) *lost = 0;
 }
 
-// where the expanded K (in two parts) and V lie in the workspace, behind the spans and the mark of lost keys
+// The largest magnitude of V in each (sequence, kv head)'s span, as a float's bits: what f16 is scaled by.  Values that are no
+// numbers say nothing; numbers past f32's go the CUDA cores' way.  The maximum does not depend on the order.
+constexpr int kTopKeys = 8;      // positions of a thread
+
+__global__ void __launch_bounds__(256) v_top_kernel(ExpandArgs p, Geom g, int* top, int chunks) {
+    pdl_wait();
+    const ReadArgs& a = p.r;
+    const int b = blockIdx.x / chunks, heads = min(a.Hkv, 256), at_once = 256 / heads;
+    const int2 span = p.span[b];
+    const int64_t first = (int64_t)(blockIdx.x - b * chunks) * (at_once * kTopKeys) + threadIdx.x / heads;
+    if (threadIdx.x >= heads * at_once) return;
+    for (int h = threadIdx.x % heads; h < a.Hkv; h += heads) {
+        float most = 0.f;
+#pragma unroll
+        for (int i = 0; i < kTopKeys; ++i) {
+            const int64_t pos = first + i * at_once;
+            if (pos < span.x || pos >= span.y) continue;
+            const int64_t row = key_row(g, b, pos);
+            if (row < 0 || row >= a.kv_rows) continue;
+            const float* pair = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.v_cache) + row * a.vc_stride + a.Hkv * (a.dv / 2)) + 2 * h;
+            const float scale = pair[0], low = pair[1];
+            if (isfinite(scale) && isfinite(low)) most = fmaxf(most, fmaxf(fabsf(low), fabsf(fmaf(15.f, scale, low))));
+        }
+        if (isinf(most)) *p.lost = 1;
+        int* to = top + (int64_t)b * a.Hkv + h;
+        if (__float_as_int(most) > *(volatile int*)to) atomicMax(to, __float_as_int(most));
+    }
+}
+
+// where the expanded K (in two parts) and V lie in the workspace, behind the spans, the largest values and the mark of lost keys
 struct Expanded {
-    size_t k_at, rest_at, v_at, bytes;
+    size_t top_at, k_at, rest_at, v_at, bytes;
     Expanded(int64_t n_seq, int64_t max_n_kv, int Hkv, int dk, int dv) {
         const size_t rows = (size_t)n_seq * max_n_kv * Hkv;
-        k_at = (n_seq * sizeof(int2) + sizeof(int) + 15) / 16 * 16;
+        top_at = n_seq * sizeof(int2) + sizeof(int);
+        k_at = (top_at + n_seq * Hkv * sizeof(int) + 15) / 16 * 16;
         rest_at = k_at + rows * dk * 2;
         v_at = rest_at + rows * dk * 2;
         bytes = v_at + rows * dv * 2;
@@ -926,10 +957,11 @@ size_t q4_attn_workspace_bytes(int dtype, int64_t n_seq, int64_t n_q, int64_t ma
     return splits > kDenseCluster ? splits * split_bytes(n_seq * n_q, Hq, dv) : 0;
 }
 
-// K and V of the span that some row sees, expanded, then dense_attn's tensor-core kernel on them: V rounded to dtype, K as a
-// sum of two (16 or 22 bits), since the log of the weights' sum is f32.  (Scales applied to the products of exact codes, in
+// K and V of the span that some row sees, expanded, then dense_attn's tensor-core kernel on them: V rounded to f16 (and the
+// weights with it: bf16 for both leaves 4096 rows on 16384 keys with errors of 0.0029 of the result, 0.0017 is the result's
+// own rounding) at a power of two, K as a sum of two of dtype (16 or 22 bits), since the log of the weights' sum is f32.  (Scales applied to the products of exact codes, in
 // the softmax: 4096 rows on 16384 keys 1455 us, for 740 without; it is the softmax that the kernel waits for.)  What that kernel cannot know
-// of, keys without a row in the cache and values beyond dtype's range, sends everything through the CUDA cores again, which skip
+// of, keys without a row in the cache and numbers beyond dtype's range in K, sends everything through the CUDA cores again, which skip
 // and flag the one and hold the other in f32.
 static cudaError_t run_expanded(DenseArgs a, int dtype, const Geom& g, uint8_t* ws, cudaStream_t st) {
     const Expanded e(g.B, g.max_n_kv, a.Hkv, a.dk, a.dv);
@@ -967,9 +999,14 @@ static cudaError_t run_expanded(DenseArgs a, int dtype, const Geom& g, uint8_t* 
     x.lost = lost;
     x.k_rest = ws + e.rest_at;
     d.k_rest = x.k_rest;
+    int* top = reinterpret_cast<int*>(ws + e.top_at);
+    x.v_top = d.v_top = top;
     Geom all = g;
     all.T = g.max_n_kv;
-    cudaError_t err = launch_pdl(span_kernel, dim3((unsigned)g.B), dim3(256), 0, st, a.mods, g, span, lost);
+    const int64_t chunk = 256 / std::min(a.Hkv, 256) * kTopKeys, chunks = (g.max_n_kv + chunk - 1) / chunk;
+    if (chunks * g.B > INT32_MAX) return cudaErrorNotSupported;
+    cudaError_t err = launch_pdl(span_kernel, dim3((unsigned)g.B), dim3(256), 0, st, a.mods, g, span, lost, top, a.Hkv);
+    if (err == cudaSuccess) err = launch_pdl(v_top_kernel, dim3((unsigned)(chunks * g.B)), dim3(256), 0, st, x, g, top, (int)chunks);
     if (err == cudaSuccess) err = launch_expand_q4(x, dtype, all, st);
     if (err == cudaSuccess) err = launch_dense_tc(d, dtype, flat, st);
     if (err != cudaSuccess) return err;

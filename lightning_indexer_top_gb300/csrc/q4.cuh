@@ -42,6 +42,7 @@ struct ExpandArgs {
     const int2* span;
     int* lost;
     void* k_rest;
+    const int* v_top;      // [B, Hkv]: V becomes f16 times 2^-v_exponent of this
 };
 
 cudaError_t launch_expand_q4(const ExpandArgs& a, int dtype, const Geom& g, cudaStream_t st);

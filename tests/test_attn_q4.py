@@ -7,9 +7,9 @@ that a value is s (n - 8) + m':
            counted too; an odd column's code is taken as 72 too much, which is taken off again: (dk + 6) u 72 sum |q| s more);
            many rows, or other heads: K is a sum of two numbers of the inputs' type, half(T)^2 sum |q k| more;
            scaling, cap, bias and maximum 8 u (|x| + cap + slope * distance + 1): dx;
-  weights  off by a factor within e^(2 dx) (1 + 2^-20), and on the tensor cores by half a step of the type they are rounded to
-           for the second product: f16 of the weight times the value's scale (few rows of 64 or 128 columns), the inputs' type;
-  values   16-bit inputs otherwise: half(T) of each;
+  weights  off by a factor within e^(2 dx) (1 + 2^-20), and on the tensor cores by half a step of f16, to which they (few rows
+           of 64 or 128 columns: their product with the value's scale) are rounded for the second product;
+  values   many rows, or other heads: half a step of f16 each;
   sums     n f32 additions: n u of the sum of magnitudes, S = sum p (s |n - 8| + |m'|).
 |error| <= 2 (2 dx + n u + 2^-20 + rounded weights and values) S + half(T) |out|.  lse: dx + n u + 2^-20 + u |lse|."""
 
@@ -93,7 +93,7 @@ class Case4(Case):
         G = Hq // self.Hkv
         small = self.dtype == torch.float32
         codes = not small and T * G <= 256 and dk == self.dv and dk in (64, 128)      # (the codes themselves may be multiplied)
-        rounded = 0.0 if small else half(torch.float16) if codes and T * G <= 16 else 2 * half(self.dtype)
+        rounded = 0.0 if small else (1 if codes else 2) * half(torch.float16)
         out = torch.zeros(B, T, Hq, self.dv, dtype=torch.float64)
         lse = torch.full((B, T, Hq), -math.inf, dtype=torch.float64)
         tol, tol_lse = torch.zeros_like(out), torch.zeros_like(lse)
@@ -308,6 +308,23 @@ def test_many_rows_and_pages_out_of_range(dtype, page):
         c.rows[b][lost * page:(lost + 1) * page] = -1
     c.check(*c.run())
     assert L.idx_device_status(reset=True) == L.IDX_ERR_DEVICE_BOUNDS
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,d", [(1, 128), (5, 64), (70, 128), (70, 64), (3, 80)])
+@pytest.mark.parametrize("page", [0, 16])
+def test_values_of_any_size(dtype, T, d, page):
+    # (f16: its results have to hold them)
+    c = Case4([300, 41], T, 8, 2, d, dtype=dtype, seed=13, page=page)
+    big = 2.0 ** (6 if dtype == torch.float16 else 60)
+    for h, f in ((0, 1 / big), (1, big)):
+        for x in c.coded[1][1:]:
+            x[:, h] *= f
+    codes, scale, low = c.coded[1]
+    c.caches[1] = pack(codes, scale.float(), low.float())
+    c.sync()
+    c.check(*c.run())
 
 
 @pytest.mark.gpu
