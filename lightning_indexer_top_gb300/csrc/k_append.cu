@@ -510,10 +510,12 @@ __global__ void __launch_bounds__(kThreads, kQ4 ? 4 : 6) append_kernel(AppendArg
         if (u < nk) {
             const int h = u / uq;
             return head_unit<T, E, kInter>(a, static_cast<const T*>(a.rows.k) + t.row * a.rows.k_stride + h * a.dk,
-                                           static_cast<T*>(a.k_cache) + t.to * a.kc_stride + h * a.dk, u - h * uq, a.n_rot > 0, cs_all + i * half);
+                                           static_cast<T*>(a.k_cache) + t.to * a.kc_stride + h * a.dk, u - h * uq, a.n_rot > 0,
+                                           cs_all + i * half);
         }
         u -= nk;       // (the heads of V lie one behind the other: pieces of the whole row)
-        return {static_cast<const T*>(a.rows.v) + t.row * a.rows.v_stride + u * E, static_cast<T*>(a.v_cache) + t.to * a.vc_stride + u * E, nullptr, 0};
+        return {static_cast<const T*>(a.rows.v) + t.row * a.rows.v_stride + u * E,
+                static_cast<T*>(a.v_cache) + t.to * a.vc_stride + u * E, nullptr, 0};
     };
     // (two or three units' loads at a time measured slower: 27 and 34 us for 19 of a 4096-token chunk, for the CTAs that their
     // registers cost)
@@ -540,8 +542,10 @@ __global__ void __launch_bounds__(kThreads, kQ4 ? 4 : 6) append_kernel(AppendArg
                 if (e >= rows || tok[r.i].to < 0) return r;
                 const int h = e - r.i * a.Hkv;
                 const Token& t = tok[r.i];
-                uint8_t* c = is_k ? static_cast<uint8_t*>(a.k_cache) + t.to * a.kc_stride : static_cast<uint8_t*>(a.v_cache) + t.to * a.vc_stride;
-                r.src = (is_k ? static_cast<const T*>(a.rows.k) + t.row * a.rows.k_stride : static_cast<const T*>(a.rows.v) + t.row * a.rows.v_stride) + h * w;
+                uint8_t* c = is_k ? static_cast<uint8_t*>(a.k_cache) + t.to * a.kc_stride
+                                  : static_cast<uint8_t*>(a.v_cache) + t.to * a.vc_stride;
+                r.src = (is_k ? static_cast<const T*>(a.rows.k) + t.row * a.rows.k_stride
+                              : static_cast<const T*>(a.rows.v) + t.row * a.rows.v_stride) + h * w;
                 r.codes = c + h * (w / 2);
                 r.pair = reinterpret_cast<float*>(c + a.Hkv * (w / 2)) + 2 * h;
                 return r;
@@ -608,7 +612,9 @@ cudaError_t run(const AppendArgs& a, const Geom& g, cudaStream_t st) {
     if (kQ4) {
         // lanes of a head row whose columns come in aligned eights, up to a warp
         auto lanes = [&](const void* x, int64_t stride, int w, bool rot) {
-            if (!x || reinterpret_cast<uintptr_t>(x) % 16 || stride * (int64_t)sizeof(T) % 16 || w * (int64_t)sizeof(T) % 16 || w % 16 || w > 512) return 0;
+            if (!x || reinterpret_cast<uintptr_t>(x) % 16 || stride * (int64_t)sizeof(T) % 16 || w * (int64_t)sizeof(T) % 16 ||
+                w % 16 || w > 512)
+                return 0;
             if (rot && (a.start % 8 || a.n_rot % (a.interleaved ? 8 : 16))) return 0;
             int n = 1;
             while (n < w / 16) n *= 2;

@@ -220,7 +220,8 @@ struct Shape {
 };
 
 template <typename T, int D, int NB, bool kMods>
-__global__ void __launch_bounds__(kThreads, Shape<D, NB>::kCtas) q4_kernel(const __grid_constant__ Q4Args p, const __grid_constant__ Geom g, const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__(kThreads, Shape<D, NB>::kCtas) 
+    q4_kernel(const __grid_constant__ Q4Args p, const __grid_constant__ Geom g, const __grid_constant__ Maps maps) {
     using S = Shape<D, NB>;
     constexpr int R = S::R;
     extern __shared__ uint8_t smem_raw[];
@@ -541,7 +542,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NB>::kCtas) q4_kernel(const
                     for (int d = 4; d < 32; d <<= 1) by = fmaxf(by, __shfl_xor_sync(0xffffffffu, by, d));
                     const bool first = (r ? __high2float(top[nb]) : __low2float(top[nb])) < 0.f;
                     if (by == -INFINITY || (!first && by < 0.f)) by = 0.f;
-                    else if (first) top[nb] = r ? __halves2half2(__low2half(top[nb]), __float2half(32768.f)) : __halves2half2(__float2half(32768.f), __high2half(top[nb]));
+                    else if (first) top[nb] = r ? __halves2half2(__low2half(top[nb]), __float2half(32768.f))
+                                                : __halves2half2(__float2half(32768.f), __high2half(top[nb]));
                     const float al = first ? 0.f : ex2_approx(-by);
                     m[nb][r] += by;
 #pragma unroll
@@ -661,7 +663,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NB>::kCtas) q4_kernel(const
             }
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
-                *reinterpret_cast<float2*>(o_s + (warp * R + r) * S::kPitch + gq * (D / 8) + 2 * k) = make_float2(o[nb][k][e], o[nb][k][e + 2]);
+                *reinterpret_cast<float2*>(o_s + (warp * R + r) * S::kPitch + gq * (D / 8) + 2 * k) =
+                    make_float2(o[nb][k][e], o[nb][k][e + 2]);
         }
     __syncthreads();
     for (int e = threadIdx.x; e < n_rows * (D / 4); e += kThreads) {
@@ -903,7 +906,8 @@ __global__ void __launch_bounds__(256) v_top_kernel(ExpandArgs p, Geom g, int* t
             if (pos < span.x || pos >= span.y) continue;
             const int64_t row = key_row(g, b, pos);
             if (row < 0 || row >= a.kv_rows) continue;
-            const float* pair = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.v_cache) + row * a.vc_stride + a.Hkv * (a.dv / 2)) + 2 * h;
+            const uint8_t* pairs = static_cast<const uint8_t*>(a.v_cache) + row * a.vc_stride + a.Hkv * (a.dv / 2);
+            const float* pair = reinterpret_cast<const float*>(pairs) + 2 * h;
             const float scale = pair[0], low = pair[1];
             if (isfinite(scale) && isfinite(low)) most = fmaxf(most, fmaxf(fabsf(low), fabsf(fmaf(15.f, scale, low))));
         }
@@ -959,10 +963,12 @@ size_t q4_attn_workspace_bytes(int dtype, int64_t n_seq, int64_t n_q, int64_t ma
 
 // K and V of the span that some row sees, expanded, then dense_attn's tensor-core kernel on them: V rounded to f16 (and the
 // weights with it: bf16 for both leaves 4096 rows on 16384 keys with errors of 0.0029 of the result, 0.0017 is the result's
-// own rounding) at a power of two, K as a sum of two of dtype (16 or 22 bits), since the log of the weights' sum is f32.  (Scales applied to the products of exact codes, in
-// the softmax: 4096 rows on 16384 keys 1455 us, for 740 without; it is the softmax that the kernel waits for.)  What that kernel cannot know
-// of, keys without a row in the cache and numbers beyond dtype's range in K, sends everything through the CUDA cores again, which skip
-// and flag the one and hold the other in f32.
+// own rounding) at a power of two, K as a sum of two of dtype (16 or 22 bits), since the log of the weights' sum is f32.  Of
+// the 1004 us of 4096 tokens of 32 heads on 16384 keys the second product of K takes some 260 (K in bf16 alone: 740), the
+// expansion of 16384 rows under 10.  (Scales applied to the products of exact codes, in the softmax: 1455 us; it is the
+// softmax that the kernel waits for.)
+// What that kernel cannot know of, keys without a row in the cache and numbers beyond dtype's range in K, sends everything
+// through the CUDA cores again, which skip and flag the one and hold the other in f32.
 static cudaError_t run_expanded(DenseArgs a, int dtype, const Geom& g, uint8_t* ws, cudaStream_t st) {
     const Expanded e(g.B, g.max_n_kv, a.Hkv, a.dk, a.dv);
     int2* span = reinterpret_cast<int2*>(ws);

@@ -195,7 +195,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && E < 64 ? 4 : 3) be
     if (tid == 0) {
         float t = 0.f;
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) t += sums[i] * (maxima[i] > -INFINITY ? sm100::ex2_approx((maxima[i] - M) * kLog2e) : sums[i] != sums[i] ? 1.f : 0.f);
+        for (int i = 0; i < kWarps; ++i)
+            t += sums[i] * (maxima[i] > -INFINITY ? sm100::ex2_approx((maxima[i] - M) * kLog2e) : sums[i] != sums[i] ? 1.f : 0.f);
         a.parts[at] = {M < INFINITY && t == t ? M : INFINITY, t};
     }
     const int n = count;
