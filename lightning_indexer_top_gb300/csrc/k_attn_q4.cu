@@ -7,8 +7,14 @@
 //     output  O    = sum_j (p_j s_j) (n_j - 8) + sum_j p_j m'_j      columns are the M side, rows the N side
 // q is brought to f16 at a power of two of its row's (exact but for what lies 2^-27 below the row's largest), and the
 // weights p_j s_j are rounded to f16 at a running maximum of theirs; centring the codes keeps that rounding as small as
-// the values' own.  The order of columns within a product is free, so a lane takes 16 bytes of a key's codes as they lie and q is laid
-// out to match.
+// the values' own.  The order of columns within a product is free, so a lane takes 16 bytes of a key's codes as they lie and q
+// is laid out to match.
+//
+// 16 sequences of up to 32768 keys, 32 bf16 heads of 128 on 4, 64-row pages: 65 us for 231 MB, 3.6 TB/s.  Not memory bounds it
+// but the way from codes to operands: schedulers issue on half of the cycles, three warps to each, mostly waiting for their own
+// last result (tensor pipe 21 %, ALU 49 %).  No better: four CTAs to an SM at 128 registers, two to five blocks ahead, halves
+// of a block one after the other (66 to 68), V expanded before the softmax (69), eight warps to a CTA (79), scales by plain
+// copies instead of TMA's (66 to 69).
 #include <algorithm>
 
 #include "q4.cuh"
@@ -964,8 +970,8 @@ size_t q4_attn_workspace_bytes(int dtype, int64_t n_seq, int64_t n_q, int64_t ma
 // K and V of the span that some row sees, expanded, then dense_attn's tensor-core kernel on them: V rounded to f16 (and the
 // weights with it: bf16 for both leaves 4096 rows on 16384 keys with errors of 0.0029 of the result, 0.0017 is the result's
 // own rounding) at a power of two, K as a sum of two of dtype (16 or 22 bits), since the log of the weights' sum is f32.  Of
-// the 1004 us of 4096 tokens of 32 heads on 16384 keys the second product of K takes some 260 (K in bf16 alone: 740), the
-// expansion of 16384 rows under 10.  (Scales applied to the products of exact codes, in the softmax: 1455 us; it is the
+// the 1004 to 1025 us of 4096 tokens of 32 heads on 16384 keys the second product of K takes some 240 (K in bf16 alone: 740),
+// spans, largest values and expansion of 16384 rows some 30.  (Scales applied to the products of exact codes, in the softmax: 1455 us; it is the
 // softmax that the kernel waits for.)
 // What that kernel cannot know of, keys without a row in the cache and numbers beyond dtype's range in K, sends everything
 // through the CUDA cores again, which skip and flag the one and hold the other in f32.

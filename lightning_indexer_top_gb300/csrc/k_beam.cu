@@ -13,7 +13,7 @@
 //
 // The scan waits more than it works (seven instructions a logit): 16-bit logits stay packed so that more CTAs are at it,
 // sums run against the warp's maximum so that two barriers are enough.
-// 512 rows of 131072 bf16 logits, 16 kept of each eight: 68 us, some 50 of them the scan (2.4 TB/s), in which schedulers issue on 58 % of
+// 512 rows of 131072 bf16 logits, 16 kept of each eight: 65 us, two thirds of them the scan, in which schedulers issue on half of
 // the cycles; the merge waits for one load after another.
 #include <float.h>
 

@@ -34,9 +34,9 @@ struct ReadArgs {
 
 cudaError_t launch_read_q4(const ReadArgs& a, int dtype, const Geom& g, cudaStream_t st);
 
-// The positions of each sequence's span (device, [lo, hi)) for the attention: the values of K and V in dtype, row b * g.T +
-// position, and in k_rest what K's lack of their f32.  A position whose cache row is out of range sets *lost, in place of the
-// device status.
+// The positions of each sequence's span (device, [lo, hi)) for the attention: the values of K in dtype, row b * g.T + position,
+// what they lack of their f32 in k_rest, and V in f16.  A position whose cache row is out of range, or with a number of K beyond
+// dtype's, sets *lost, in place of the device status.
 struct ExpandArgs {
     ReadArgs r;
     const int2* span;
