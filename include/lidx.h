@@ -769,7 +769,7 @@ size_t dense_attn_q4_workspace_size(idx_dtype dtype, int32_t n_seq, int32_t n_q_
  * +inf, or whose score is NaN or +inf, has no continuations and is flagged (IDX_ERR_INEXACT).
  * Errors: n_seq < 0, n_beams < 1, n_vocab < 1, n_out outside [1, 32], n_beams*n_vocab >
  * 2^31 - 1, end_token outside [-1, n_vocab), NULL where a tensor is needed: INVALID_ARG;
- * n_beams > 1024: UNSUPPORTED.
+ * n_beams > 1024, n_vocab > 2^31 - 65537: UNSUPPORTED.
  */
 typedef struct idx_beam {
     const void* logits;

@@ -238,6 +238,8 @@ idx_status idx_beam_step(const idx_beam* beam, idx_dtype dtype, int32_t n_seq, i
                                                      beam->out_history_stride < beam->history_cols)))
         return bad(IDX_ERR_INVALID_ARG, "%s: need 0 <= history_cols <= both histories' strides", what);
     if (n_beams > kBeamMax) return bad(IDX_ERR_UNSUPPORTED, "%s: n_beams > %d", what, kBeamMax);
+    // (columns are counted in 32 bits up to the end of the last chunk)
+    if (n_vocab > INT32_MAX - 65536) return bad(IDX_ERR_UNSUPPORTED, "%s: n_vocab > 2^31 - 65537", what);
     if (n_seq == 0) return IDX_OK;
     if (!beam->logits || !beam->scores || !beam->out_scores || !beam->parent || !beam->token || !beam->out_done)
         return bad(IDX_ERR_INVALID_ARG, "%s: NULL logits, scores or outputs", what);

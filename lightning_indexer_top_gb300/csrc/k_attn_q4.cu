@@ -226,7 +226,7 @@ struct Shape {
 };
 
 template <typename T, int D, int NB, bool kMods>
-__global__ void __launch_bounds__(kThreads, Shape<D, NB>::kCtas) 
+__global__ void __launch_bounds__(kThreads, Shape<D, NB>::kCtas)
     q4_kernel(const __grid_constant__ Q4Args p, const __grid_constant__ Geom g, const __grid_constant__ Maps maps) {
     using S = Shape<D, NB>;
     constexpr int R = S::R;

@@ -336,7 +336,7 @@ HIST = dict(lengths=6 << 12, history=7 << 12, out_lengths=8 << 12, out_history=9
     (dict(dtype=7), b"dtype"), (dict(n=-1), b"n_seq"), (dict(W=0), b"n_beams"), (dict(V=0), b"n_vocab"), (dict(K=0), b"n_out"), (dict(K=33), b"n_out"),
     (dict(W=1 << 16, V=1 << 15, logit_stride=1 << 15), b"continuations"), (dict(n=1 << 20, W=1 << 12), b"rows"), (dict(end=-2), b"end_token"),
     (dict(end=100), b"end_token"), (dict(done=1 << 13), b"done"), (dict(logit_stride=99), b"logit_stride"), (dict(history_cols=-1), b"history_cols"),
-    (dict(HIST, history_cols=9), b"history_cols"), (dict(W=1025), b"n_beams"), (dict(logits=None), b"NULL"), (dict(scores=None), b"NULL"),
+    (dict(HIST, history_cols=9), b"history_cols"), (dict(W=1025), b"n_beams"), (dict(W=1, V=2 ** 31 - 1, logit_stride=2 ** 31), b"n_vocab"), (dict(logits=None), b"NULL"), (dict(scores=None), b"NULL"),
     (dict(out_scores=None), b"NULL"), (dict(parent=None), b"NULL"), (dict(token=None), b"NULL"), (dict(out_done=None), b"NULL"),
     (dict(HIST, history=None), b"together"), (dict(HIST, out_lengths=None), b"together"), (dict(HIST, out_history=None), b"together"),
     (dict(out_scores=(1 << 12) + 4), b"overlaps"), (dict(HIST, out_history=(7 << 12) + 64), b"overlaps"), (dict(token=(1 << 20) + 16), b"overlaps"),
