@@ -309,9 +309,16 @@ __device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
     for (int i = 0; i < 8; ++i) x[i] = to_f32(v[i]);
 }
 
+// the larger one, a NaN where either is one
+__device__ __forceinline__ float max_nan(float x, float y) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+
 // Head rows whose columns come in aligned eights: a lane has two of those, the ones that are turned together or neighbours, and
 // `lanes` (a power of two, at least w / 16) of them a row.  src NULL: no row for this lane.  False: the row is to be done in
-// 64 bits.
+// 64 bits, as is one that holds a NaN or an infinity: a NaN passes through the maximum, an infinity leaves no span.
 template <typename T>
 __device__ __forceinline__ bool quantize_group(const AppendArgs& a, const T* src, int w, int lanes, bool rot, int p, const float2* cs,
                                                uint8_t* codes, float* pair) {
@@ -363,12 +370,12 @@ __device__ __forceinline__ bool quantize_group(const AppendArgs& a, const T* src
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 lo = fminf(lo, x[e][i]);
-                hi = fmaxf(hi, x[e][i]);
+                hi = max_nan(hi, x[e][i]);
             }
     }
     for (int o = lanes >> 1; o; o >>= 1) {
         lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
         big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
     }
     const uint32_t mine = lanes == 32 ? ~0u : ((1u << lanes) - 1u) << (threadIdx.x & 31 & ~(lanes - 1));
@@ -378,7 +385,7 @@ __device__ __forceinline__ bool quantize_group(const AppendArgs& a, const T* src
     bool any = false;          // a column that f32 does not tell
     bool other = false;        // neither a span to divide by nor the same number throughout (whose codes are 0)
     if (on && !s.sure) {
-        other = big > 0.f;
+        other = big > 0.f || !(fabsf(lo) <= FLT_MAX);
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll

@@ -301,6 +301,38 @@ def test_q4_of_rows_that_f32_cannot_tell_apart():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d,n_rot,start,inter", [
+    (16, 0, 0, False), (16, 16, 0, False), (64, 32, 0, False), (64, 64, 0, True), (80, 80, 0, False), (80, 16, 8, True), (96, 0, 0, False),
+    (128, 128, 0, False), (128, 64, 64, True), (512, 64, 448, False), (576, 64, 512, False), (24, 10, 3, False)])
+def test_q4_rows_without_a_number_stand_for_nan_and_leave_the_others(dtype, d, n_rot, start, inter):
+    # a NaN or an infinity first, in the middle and last, and rows of nothing else, between rows of numbers (which share their warp)
+    values, n, h, dv = [math.nan, math.inf, -math.inf], 24, 3, min(d, 512)
+    c = Rows([n], n, 0, h, d, dv, dtype, 0, None, n_rot, start, inter, seed=8, apart=False)
+    bad = torch.zeros(n, h, dtype=torch.bool)
+    rows = [(v, at) for v in values for at in ([0], [-1], [d // 2], slice(None))]
+    c.k, c.v = c.k.clone(), c.v.clone()
+    good = [t.clone() for t in (c.k, c.v)]
+    for i, (value, at) in enumerate(rows):
+        bad[2 * i, i % h] = True
+        c.k[2 * i, i % h, at] = value
+        c.v[2 * i, i % h, at if at != [d // 2] else dv // 2] = value
+    new = lambda w: torch.zeros(n, L.idx_q4_row_bytes(h, w), dtype=torch.uint8, device="cuda")  # noqa: E731
+    got, want = (new(d), new(dv)), (new(d), new(dv))
+    L.idx_cache_append_q4(c.k.cuda(), c.v.cuda(), *got, c.batch(), **c.rope())
+    L.idx_cache_append_q4(*[t.cuda() for t in good], *want, c.batch(), **c.rope())
+    for a, b, w in zip(got, want, (d, dv)):
+        codes, s, m = parts(a, h, w)
+        assert torch.isnan(s[bad]).all() and torch.isnan(m[bad]).all() and (codes[bad] == 0).all()
+        for x, y in zip((codes, s, m), parts(b, h, w)):
+            assert torch.equal(x[~bad], y[~bad]) and torch.isfinite(x[~bad].float()).all()
+    k, v = L.idx_cache_read_q4(*got, c.batch(), h, d, dv, dtype=torch.float32)
+    for t in (k, v):
+        assert torch.isnan(t[bad.cuda()]).all() and torch.isfinite(t[~bad.cuda()]).all()
+    assert L.idx_device_status(reset=True) == 0
+
+
+@pytest.mark.gpu
 def test_many_rows_have_exact_codes():
     # half a million columns, some of which lie within f32's error of a border
     c = Rows([2048], 2048, 0, 2, 128, 128, torch.bfloat16, 0, None, 128, seed=5, base=1e6)
