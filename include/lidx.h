@@ -729,7 +729,8 @@ idx_status idx_cache_read_q4(const void* k_cache, int64_t k_row_stride, const vo
  * themselves; more rows, and other heads of at most 128 columns, on K and V expanded in the
  * workspace (to 64 GB, counted by max_n_kv): K in two parts (16 bits of significand together in
  * BF16, 22 in F16, nothing below F16's least number), V in f16 at a power of two of the
- * sequence's and head's largest.  The weights are rounded to f16 for the second product (with
+ * sequence's and head's largest (a call with a number of K beyond dtype's range, or with a key
+ * whose V is 2^-28 or less of that largest, goes to the CUDA cores).  The weights are rounded to f16 for the second product (with
  * the values' scale, on codes).  Everything else runs on the CUDA cores in f32.
  */
 idx_status dense_attn_q4(const void* q, idx_dtype dtype, int32_t n_q_heads, int32_t n_kv_heads, int32_t dk, int32_t dv,

@@ -704,6 +704,9 @@ __global__ void __launch_bounds__(kThreads) read_q4_kernel(ExpandArgs p, Geom g,
         constexpr int E = 16 / (int)sizeof(T);
         if (kExpand && !is_k) {
             const float f = exp2_whole(-v_exponent(p.v_top[(r0 + i) / g.T * a.Hkv + h]));
+            // (of a key far below the largest f16 would keep fewer bits, or none: rows that do not see the largest need them)
+            const float most = fmaxf(fabsf(low), fabsf(fmaf(15.f, scale, low)));
+            if (isfinite(scale) && isfinite(low) && most > 0.f && most * f < 0x1p-14f) *p.lost = 1;
 #pragma unroll
             for (int c = 0; c < kCols; c += 8) {
                 __half y[8];

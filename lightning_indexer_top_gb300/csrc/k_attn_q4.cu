@@ -973,8 +973,9 @@ size_t q4_attn_workspace_bytes(int dtype, int64_t n_seq, int64_t n_q, int64_t ma
 // the 1004 to 1025 us of 4096 tokens of 32 heads on 16384 keys the second product of K takes some 240 (K in bf16 alone: 740),
 // spans, largest values and expansion of 16384 rows some 30.  (Scales applied to the products of exact codes, in the softmax: 1455 us; it is the
 // softmax that the kernel waits for.)
-// What that kernel cannot know of, keys without a row in the cache and numbers beyond dtype's range in K, sends everything
-// through the CUDA cores again, which skip and flag the one and hold the other in f32.
+// What that kernel cannot know of or hold, keys without a row in the cache, numbers beyond dtype's range in K and keys whose V is
+// 2^-28 or less of the largest, sends everything through the CUDA cores again, which skip and flag the one and hold the others in
+// f32.
 static cudaError_t run_expanded(DenseArgs a, int dtype, const Geom& g, uint8_t* ws, cudaStream_t st) {
     const Expanded e(g.B, g.max_n_kv, a.Hkv, a.dk, a.dv);
     int2* span = reinterpret_cast<int2*>(ws);

@@ -35,8 +35,8 @@ struct ReadArgs {
 cudaError_t launch_read_q4(const ReadArgs& a, int dtype, const Geom& g, cudaStream_t st);
 
 // The positions of each sequence's span (device, [lo, hi)) for the attention: the values of K in dtype, row b * g.T + position,
-// what they lack of their f32 in k_rest, and V in f16.  A position whose cache row is out of range, or with a number of K beyond
-// dtype's, sets *lost, in place of the device status.
+// what they lack of their f32 in k_rest, and V in f16.  A position whose cache row is out of range, with a number of K beyond
+// dtype's, or whose largest of V is no normal f16 sets *lost, in place of the device status.
 struct ExpandArgs {
     ReadArgs r;
     const int2* span;

@@ -338,6 +338,44 @@ def test_values_beyond_half_precision(dtype, T, d):
     c.check(*c.run())
 
 
+def check_without_floor(c, out, lse):
+    """c.check, for results that 1e-30 is not small beside: their types' least numbers instead."""
+    ref, ref_lse, tol, tol_lse = c.reference()
+    out, lse = out.cpu().double().view(ref.shape), lse.cpu().double().view(ref_lse.shape)
+    none = torch.isneginf(ref_lse)
+    tol[none] = 1e-30
+    tol = tol - 1e-30 + {torch.float16: 2.0 ** -25}.get(c.dtype, 2.0 ** -134)
+    assert torch.isfinite(out).all()
+    bad = (out - ref).abs() > tol
+    assert not bad.any(), (int(bad.sum()), float(((out - ref).abs() / tol).max()))
+    assert (out[none] == 0).all() and torch.isneginf(lse[none]).all()
+    assert ((lse - ref_lse)[~none].abs() <= tol_lse[~none]).all(), float((lse - ref_lse)[~none].abs().max())
+
+
+def rescale(c, which, head, factors):
+    """Multiplies head `head` of K (0) or V (1) by factors [cache rows] (powers of two)."""
+    codes, scale, low = c.coded[which]
+    scale[:, head] = (scale[:, head].float() * factors.float()).double()
+    low[:, head] = (low[:, head].float() * factors.float()).double()
+    pad = c.caches[which].shape[1] - L.idx_q4_row_bytes(codes.shape[1], codes.shape[2])
+    c.caches[which] = pack(codes, scale.float(), low.float(), pad)
+    c.sync()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,d", [(70, 128), (70, 64), (130, 96), (3, 80)])
+def test_values_that_a_row_does_not_see_cost_it_nothing(dtype, T, d):
+    # the last key but one is far larger than the others, and far smaller ones lie between: seen by the last rows alone
+    for power in (20, 45, -45, 100):
+        c = Case4([200, 180], T, 8, 2, d, dtype=dtype, page=16, seed=14)
+        f = torch.ones(c.k.shape[0])
+        f[c.rows[0][198]] = 2.0 ** power
+        f[c.rows[1][10 if power < 0 else 178]] = 2.0 ** power
+        rescale(c, 1, 1, f)
+        check_without_floor(c, *c.run())
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 def test_many_rows_captured_with_a_page_that_comes_back(dtype):
