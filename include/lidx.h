@@ -724,14 +724,17 @@ idx_status idx_cache_read_q4(const void* k_cache, int64_t k_row_stride, const vo
  *              another way, with the same results up to rounding:
  *              fewer key splits, codes that each tile of rows expands for itself instead
  *              of once for all, or the CUDA cores.
- * 16-bit q runs on the tensor cores, given 16-byte aligned tensors and rows: up to 256 packed
- * rows (tokens x heads of a kv head) of heads of 64 or 128 columns (dk == dv) on the codes
- * themselves; more rows, and other heads of at most 128 columns, on K and V expanded in the
- * workspace (to 64 GB, counted by max_n_kv): K in two parts (16 bits of significand together in
- * BF16, 22 in F16, nothing below F16's least number), V in f16 at a power of two of the
- * sequence's and head's largest (a call with a number of K beyond dtype's range, or with a key
- * whose V is 2^-28 or less of that largest, goes to the CUDA cores).  The weights are rounded to f16 for the second product (with
- * the values' scale, on codes).  Everything else runs on the CUDA cores in f32.
+ * 16-bit q runs on the tensor cores, given 16-byte aligned tensors and rows:
+ *   - up to 256 packed rows (tokens x heads of a kv head) of heads of 64 or 128 columns (dk == dv)
+ *     on the codes themselves, the weights times the values' scale rounded to f16 for the second
+ *     product.  Where a row sees a scale or minimum above 2^32 or a scale of V below 2^-57 that is
+ *     not 0, or q reaches 2^70, a piece of its keys goes key by key in f32.
+ *   - more rows, and other heads of at most 128 columns, on K and V expanded in the workspace (to
+ *     64 GB, counted by max_n_kv): K in two parts (16 bits of significand together in BF16, 22 in
+ *     F16, nothing below F16's least number), V in f16 at a power of two of the sequence's and
+ *     head's largest, the weights in f16.  With a number of K beyond dtype's range, or a key whose V
+ *     is 2^-28 or less of that largest, the call goes to the CUDA cores after all.
+ * Everything else runs on the CUDA cores in f32.
  */
 idx_status dense_attn_q4(const void* q, idx_dtype dtype, int32_t n_q_heads, int32_t n_kv_heads, int32_t dk, int32_t dv,
                          const void* k_cache, int64_t k_row_stride, const void* v_cache, int64_t v_row_stride,

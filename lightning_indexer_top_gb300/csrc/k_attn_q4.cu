@@ -10,7 +10,7 @@
 // the values' own.  The order of columns within a product is free, so a lane takes 16 bytes of a key's codes as they lie and q
 // is laid out to match.
 //
-// 16 sequences of up to 32768 keys, 32 bf16 heads of 128 on 4, 64-row pages: 65 us for 231 MB, 3.6 TB/s.  Not memory bounds it
+// 16 sequences of up to 32768 keys, 32 bf16 heads of 128 on 4, 64-row pages: 67 us for 231 MB, 3.4 TB/s.  Not memory bounds it
 // but the way from codes to operands: schedulers issue on half of the cycles, three warps to each, mostly waiting for their own
 // last result (tensor pipe 21 %, ALU 49 %).  No better: four CTAs to an SM at 128 registers, two to five blocks ahead, halves
 // of a block one after the other (66 to 68), V expanded before the softmax (69), eight warps to a CTA (79), scales by plain
@@ -215,6 +215,72 @@ __device__ __noinline__ void flag_lost(const DenseArgs& a, const Geom& g, int b,
     }
 }
 
+// What the products hold.  A weight goes with its value's scale, p s <= 2^15 with p <= 2^64 (see the running maximum): V's scales
+// from 2^-57 on, or 0, keep every bit of both, and up to 2^32 neither the sum of the weights nor that of the minimums leaves f32.
+// Scores are products of a key's scale and sum, q's unit and the call's scale, one after the other: each at most 2^60 (few_rows)
+// has room.  Pieces of rows that see a key beyond that are done by rows_by_key.
+constexpr float kMost = 0x1p32f, kMostScale = 0x1p60f;
+constexpr int kMostUnit = 60;
+
+__device__ __forceinline__ bool beyond(float2 k, float2 v) {
+    constexpr uint32_t kLeast = 0x23000000u;      // 2^-57
+    return fmaxf(fmaxf(fabsf(k.x), fabsf(k.y)), fmaxf(fabsf(v.x), fabsf(v.y))) > kMost || 2u * __float_as_uint(v.x) - 1u < 2u * kLeast - 1u;
+}
+
+// The rows of a CTA's piece, keys [j0, j1), key by key and all in f32: a warp to a row, a lane to D / 32 columns.  Results go
+// where the first warp's would have gone (o_s, ml, low).
+template <typename T, int D, int R>
+__device__ __noinline__ void rows_by_key(const DenseArgs& a, const Geom& g, int b, int gkv, int64_t m0, int n_rows, int n_kv, int j0, int j1,
+                                         float* o_s, int pitch, float2* ml, float* low) {
+    constexpr int C = D / 32;
+    const int lane = threadIdx.x & 31, G = a.Hq / a.Hkv;
+    for (int r = threadIdx.x >> 5; r < R; r += kWarps) {
+        float M = -INFINITY, l = 0.f, acc[C];
+#pragma unroll
+        for (int i = 0; i < C; ++i) acc[i] = 0.f;
+        if (r < n_rows) {
+            const int64_t row = (int64_t)b * g.T + (m0 + r) / G;
+            const int h = gkv * G + (int)((m0 + r) % G);
+            const Interval iv = row_interval(g, a.mods, row, b, n_kv);
+            const T* q = static_cast<const T*>(a.q) + (row * a.Hq + h) * D + lane * C;
+            const float slope = a.mods.slopes ? a.mods.slopes[h] : 0.f;
+            const int end = min(iv.hi, j1);
+            for (int j = max(iv.lo, j0); j < end; ++j) {
+                const int64_t at = key_row(g, b, j);
+                if (at < 0 || at >= a.kv_rows) continue;      // (flagged when its block came)
+                auto load = [&](const void* cache, int64_t stride, float (&y)[C]) {
+                    const uint8_t* p = static_cast<const uint8_t*>(cache) + at * stride;
+                    const float2 pair = reinterpret_cast<const float2*>(p + a.Hkv * (D / 2))[gkv];
+                    const uint8_t* c = p + gkv * (D / 2) + lane * (C / 2);
+                    const uint32_t n = C == 4 ? *reinterpret_cast<const uint16_t*>(c) : *c;
+#pragma unroll
+                    for (int i = 0; i < C; ++i) y[i] = fmaf((float)((n >> (4 * i)) & 15u), pair.x, pair.y);
+                };
+                float k[C], v[C], x = 0.f;
+                load(a.k, a.k_stride, k);
+                load(a.v, a.v_stride, v);
+#pragma unroll
+                for (int i = 0; i < C; ++i) x = fmaf(to_f32(q[i]), k[i], x);
+#pragma unroll
+                for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+                x *= a.scale;
+                if (a.mods.softcap > 0.f) x = a.mods.softcap * tanhf(x / a.mods.softcap);
+                x = (x - slope * fabsf((float)(iv.pos - j))) * kLog2e;
+                if (x == -INFINITY) continue;
+                const float top = fmaxf(M, x), al = exp2f(M - top), w = exp2f(x - top);
+                M = top;
+                l = fmaf(l, al, w);
+#pragma unroll
+                for (int i = 0; i < C; ++i) acc[i] = fmaf(acc[i], al, w * v[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < C; ++i) o_s[r * pitch + lane * C + i] = acc[i];
+        if (lane < kWarps) ml[lane * R + r] = lane ? make_float2(0.f, 0.f) : make_float2(M, l);
+        if (lane == 0) low[r] = 0.f;
+    }
+}
+
 template <int D, int NB>
 struct Shape {
     static constexpr int R = 8 * NB;
@@ -236,6 +302,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NB>::kCtas)
     __shared__ float2 ml_s[kWarps][R];               // maximum, sum
     __shared__ float low_s[kWarps][R];               // sum of weight * m'
     __shared__ uint32_t valid_s[kWarps][S::kStages]; // keys of a block that have a row
+    __shared__ int wide_s[kWarps];                   // whether numbers came that the products do not hold
+    static_assert(kWarps == 4, "four marks");
     float* o_s = reinterpret_cast<float*>(smem);     // [warp][R][kPitch]
     const DenseArgs& a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, tq = lane & 3;
@@ -243,6 +311,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NB>::kCtas)
     const int columns = a.Hkv * p.row_tiles;
     if (p.part_o) pdl_trigger();     // (the merge follows)
     if (lane == 0) {
+        wide_s[warp] = 0;
         for (int i = 0; i < S::kStages; ++i) mbar_init(&full[warp][i], 1);
         fence_mbar_init();
     }
@@ -333,6 +402,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NB>::kCtas)
         }
         // 2^e with big / 2^e in [2^9, 2^10) (1 for a row of zeros or of no numbers; e kept where 2^e and 2^-e are normal)
         const int e = big > 0.f && big < INFINITY ? min(max((int)(__float_as_uint(big) >> 23) - 127 - 9, -126), 126) : 0;
+        if (e > kMostUnit) wide_s[warp] = 1;
         const float inv = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
         for (int w = 0; w < D / 32; ++w)
@@ -494,6 +564,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NB>::kCtas)
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int k = 0; k < 2; ++k) vp[h][k] = *reinterpret_cast<const float2*>(x + pair_off + kBlock * 16 + (16 * h + 8 * k) * 16);
+        // (each lane looks at one key's; 66.3 us without, 67.3 with, of 16 sequences of up to 32768 keys)
+        const int own = kq + 8 * tq;
+        const float2 own_k = *reinterpret_cast<const float2*>(x + pair_off + 8 * 16 * tq);
+        const float2 own_v = *reinterpret_cast<const float2*>(x + pair_off + 8 * 16 * tq + kBlock * 16);
+        if ((whole || (((valid >> own) & 1u) && key0 + own >= k0)) && beyond(own_k, own_v)) wide_s[warp] = 1;
         float pr[2][NB][4], sum[NB][2];
         uint32_t wh[2][NB][2];
         auto weigh = [&] {
@@ -653,25 +728,29 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NB>::kCtas)
     __syncthreads();       // the rings are done with
 
     // ---- the warps' results: sums over the lanes of a row, then over the warps
+    if (wide_s[0] | wide_s[1] | wide_s[2] | wide_s[3]) {
+        rows_by_key<T, D, R>(a, g, b, gkv, m0, n_rows, n_kv, base, base + blocks * kBlock, o_s, S::kPitch, &ml_s[0][0], low_s[0]);
+    } else {
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < 2; ++e) {
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) {
-                l_run[nb][e] += __shfl_xor_sync(0xffffffffu, l_run[nb][e], d);
-                low_run[nb][e] += __shfl_xor_sync(0xffffffffu, low_run[nb][e], d);
+                for (int d = 4; d < 32; d <<= 1) {
+                    l_run[nb][e] += __shfl_xor_sync(0xffffffffu, l_run[nb][e], d);
+                    low_run[nb][e] += __shfl_xor_sync(0xffffffffu, low_run[nb][e], d);
+                }
+                const int r = 8 * nb + 2 * tq + e;
+                if (gq == 0) {
+                    ml_s[warp][r] = make_float2(m[nb][e], l_run[nb][e]);
+                    low_s[warp][r] = low_run[nb][e];
+                }
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    *reinterpret_cast<float2*>(o_s + (warp * R + r) * S::kPitch + gq * (D / 8) + 2 * k) =
+                        make_float2(o[nb][k][e], o[nb][k][e + 2]);
             }
-            const int r = 8 * nb + 2 * tq + e;
-            if (gq == 0) {
-                ml_s[warp][r] = make_float2(m[nb][e], l_run[nb][e]);
-                low_s[warp][r] = low_run[nb][e];
-            }
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-                *reinterpret_cast<float2*>(o_s + (warp * R + r) * S::kPitch + gq * (D / 8) + 2 * k) =
-                    make_float2(o[nb][k][e], o[nb][k][e + 2]);
-        }
+    }
     __syncthreads();
     for (int e = threadIdx.x; e < n_rows * (D / 4); e += kThreads) {
         const int r = e / (D / 4), cc = e % (D / 4) * 4;
@@ -802,6 +881,7 @@ int64_t piece_ctas(int64_t n_seq, int64_t columns, int64_t max_n_kv, int slots) 
 bool few_rows(const DenseArgs& a, int dtype, const Geom& g) {
     if (dtype == IDX_F32 || a.dk != a.dv || (a.dk != 64 && a.dk != 128)) return false;
     if (a.kv_rows < 1 || a.kv_rows > INT32_MAX - kBlock || g.max_n_kv > INT32_MAX - 2 * kBlock) return false;
+    if (!(fabsf(a.scale) <= kMostScale)) return false;
     // (16 bytes of two heads' scales, which the last row may not have for the last of an odd number of heads; TMA's boxes do
     // without)
     if (g.page_table && box_rows(g.page_size, kBlock) < 8 && a.Hkv % 2) return false;

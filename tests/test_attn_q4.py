@@ -377,6 +377,55 @@ def test_values_that_a_row_does_not_see_cost_it_nothing(dtype, T, d):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,d", [(1, 128), (5, 64), (30, 128), (70, 128), (3, 80)])
+@pytest.mark.parametrize("page", [0, 16, 5])
+def test_values_of_every_size(dtype, T, d, page):
+    # head 0: all of one size; head 1: sizes that differ from key to key
+    for power in (-115, -90, -78, -63, -57, 60, 64, 90, 115):
+        c = Case4([300, 41], T, 8, 2, d, dtype=dtype, seed=15, page=page)
+        g = torch.Generator().manual_seed(abs(power))
+        n = c.k.shape[0]
+        rescale(c, 1, 0, torch.full((n,), 2.0 ** power))
+        rescale(c, 1, 1, torch.exp2(torch.randint(min(power, -power), abs(power) + 1, (n,), generator=g).float()))
+        check_without_floor(c, *c.run())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,d", [(1, 128), (5, 64), (70, 128), (3, 80)])
+def test_constant_values_of_every_size(dtype, T, d):
+    # rows without a span, beside rows with one
+    for power in (-115, -60, 30, 60, 115):
+        for share in (1.0, 0.5):
+            c = Case4([300, 41], T, 8, 2, d, dtype=dtype, seed=16)
+            g = torch.Generator().manual_seed(power + 200)
+            codes, scale, low = c.coded[1]
+            flat = torch.rand(scale.shape, generator=g) < share
+            codes[flat] = 0.0
+            scale[flat] = 0.0
+            low[flat] = (torch.where(torch.rand(scale.shape, generator=g) < 0.5, -1.0, 1.0) * 2.0 ** power).double()[flat]
+            c.caches[1] = pack(codes, scale.float(), low.float())
+            c.sync()
+            check_without_floor(c, *c.run())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,d", [(1, 128), (5, 64), (70, 128), (3, 80)])
+@pytest.mark.parametrize("mods", [{}, dict(cap=4.0)])
+def test_keys_and_queries_of_every_size(dtype, T, d, mods):
+    # (keys, queries, scale): together as they were
+    for k, q, s in ((100, -100, 0), (-100, 100, 0), (100, 0, -100), (-100, 0, 100), (0, 100, -100), (0, -100, 100), (55, 55, -110), (-55, -55, 110)):
+        c = Case4([300, 41], T, 8, 2, d, dtype=dtype, seed=17, **mods)
+        for h in (0, 1):
+            rescale(c, 0, h, torch.full((c.k.shape[0],), 2.0 ** k))
+        c.q = c.q * 2.0 ** q
+        c.scale *= 2.0 ** s
+        check_without_floor(c, *c.run())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 def test_many_rows_captured_with_a_page_that_comes_back(dtype):
     c = Case4([200, 180], 70, 8, 2, 128, dtype=dtype, page=16, seed=12)
