@@ -5,6 +5,9 @@
 // the sum of exponentials, and its n_out best tokens.  The worth of a token within a
 // row goes with its logit, so the chunk's list needs no normalisation; a second kernel,
 // a CTA per sequence, joins the sums and takes the n_out best of all lists, in 64 bits.
+// Where these round different logits to one worth (a beam's score of -3e38, say), lists may
+// have left out tokens that are worth as much as the last one kept: their chunks are then
+// looked through for the lowest ones.
 //
 // The best K of N keys, K <= 32: a bound that at least K keys reach is cheap, the least over W warps of the (K/W)-th best
 // of the lanes' maxima.  The few keys that reach it go to a list in shared memory and are ranked by counting.  Keys hold
@@ -33,7 +36,7 @@ struct Part {
 
 struct BeamArgs {
     idx_beam b;
-    int32_t seqs, beams, out, vocab, end, chunks, per_thread;
+    int32_t seqs, beams, out, vocab, end, chunks, per_thread, dtype;
     Part* parts;               // [row][chunk]
     unsigned long long* cand;  // [row][chunk][out]: order_key << 32 | ~column, best first; 0: none
     int* status;
@@ -260,11 +263,16 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamArgs a) {
     __shared__ Cont won[kBeamOutMax];
     __shared__ Cont best_s[kMergeWarps];
     __shared__ int count;
+    __shared__ unsigned long long hidden;      // the largest worth that full lists may have left out
+    __shared__ uint32_t marks[kMergeWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int seq = blockIdx.x;
     const int64_t row0 = (int64_t)seq * a.beams;
     pdl_wait();
-    if (tid == 0) count = 0;
+    if (tid == 0) {
+        count = 0;
+        hidden = 0ull;
+    }
     const int lists = a.beams * a.chunks;
     // lists are dealt to as many warps as they fill, one after the other, so that the warps have about as many.  (To all warps, with
     // fewer lists each: a bound so low that 110 us were taken for 64.)
@@ -354,6 +362,9 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamArgs a) {
                         keys[j] = e.key;
                         ats[j] = e.at;
                     }
+                    // (a list's last entry: whether the next logit below it would be worth as much)
+                    if (i0 + i == a.out - 1 && !ended[l / a.chunks] && value(l, 0, k[i] - (1ull << 32)).key == e.key)
+                        atomicMax(&hidden, e.key);
                 }
             }
         }
@@ -370,12 +381,13 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamArgs a) {
         }
         __syncthreads();
     } else {
+        // (by worth and place in the lists, which is the order that every list has)
         Cont last = {~0ull, 0u};
         for (int r = 0; r < a.out; ++r) {
             Cont best = {0ull, 0u};
             for (int l = tid; l < lists; l += kMergeThreads)
                 for (int i = 0; i < a.out; ++i) {
-                    const Cont e = entry(l, i);
+                    const Cont e = {entry(l, i).key, (uint32_t)l * a.out + i};
                     if (!e.key) break;
                     if (last.better(e)) {      // (a list's entries come best first: the first one below is its best)
                         if (e.better(best)) best = e;
@@ -393,9 +405,61 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamArgs a) {
             for (int i = 0; i < kMergeWarps; ++i)
                 if (best_s[i].better(best)) best = best_s[i];
             __syncthreads();
-            if (tid == 0) won[r] = best;
+            if (tid == 0) won[r] = {best.key, best.key ? entry(best.at / a.out, best.at % a.out).at : 0u};
             if (!best.key) break;
             last = best;
+        }
+        __syncthreads();
+    }
+    const unsigned long long least = won[a.out - 1].key;
+    if (least && (n > kMergeList || hidden == least)) {
+        // What is worth more than the last one kept is there; of what is worth as much, the lowest beams and tokens, from the
+        // logits.  A list whose first entry is worth that gives one at least, the others hold what is worth more: fewer than
+        // 2 out chunks are read.
+        Cont mine_won = {0ull, 0u};
+        int have = 0, rank = 0;
+        if (tid < a.out) mine_won = won[tid];
+        for (int r = 0; r < a.out; ++r) {
+            have += won[r].key > least;
+            rank += won[r].better(mine_won);
+        }
+        __syncthreads();
+        if (mine_won.key > least) won[rank] = mine_won;
+        const int chunk = a.per_thread * kThreads;
+        for (int l0 = 0; l0 < lists && have < a.out; l0 += kMergeThreads) {
+            __syncthreads();
+            const uint32_t mark = __ballot_sync(0xffffffffu, l0 + tid < lists && entry(l0 + tid, 0).key >= least);
+            if (lane == 0) best_s[warp].at = mark;
+            __syncthreads();
+            for (int i = 0; i < kMergeWarps; ++i)
+                for (uint32_t left = best_s[i].at; left && have < a.out; left &= left - 1) {
+                    const int l = l0 + 32 * i + __ffs(left) - 1, w = l / a.chunks;
+                    const int first = ended[w] ? 0 : (l - w * a.chunks) * chunk, past = ended[w] ? 1 : min(first + chunk, a.vocab);
+                    for (int t0 = first; t0 < past && have < a.out; t0 += kMergeThreads) {
+                        const int t = t0 + tid;
+                        Cont e = {0ull, 0u};
+                        if (t < past && ended[w]) {
+                            e = value(l, 0, 0ull);
+                        } else if (t < past) {
+                            const int64_t at = (row0 + w) * a.b.logit_stride + t;
+                            const float x = a.dtype == IDX_F32   ? static_cast<const float*>(a.b.logits)[at]
+                                            : a.dtype == IDX_F16 ? to_f32(static_cast<const __half*>(a.b.logits)[at])
+                                                                 : to_f32(static_cast<const __nv_bfloat16*>(a.b.logits)[at]);
+                            e = value(l, 0, x > -INFINITY ? (unsigned long long)order_key(x) << 32 | (uint32_t)~t : 0ull);
+                        }
+                        const uint32_t hit = __ballot_sync(0xffffffffu, e.key == least);
+                        if (lane == 0) marks[warp] = hit;
+                        __syncthreads();
+                        int at = have;
+                        for (int v = 0; v < kMergeWarps; ++v) {
+                            if (v < warp) at += __popc(marks[v]);
+                            have += __popc(marks[v]);
+                        }
+                        at += __popc(hit & ((1u << lane) - 1u));
+                        if (e.key == least && at < a.out) won[at] = e;
+                        __syncthreads();
+                    }
+                }
         }
         __syncthreads();
     }
@@ -485,6 +549,7 @@ cudaError_t launch_beam(const idx_beam& b, int dtype, int seqs, int beams, int o
     a.out = out;
     a.vocab = vocab;
     a.end = end;
+    a.dtype = dtype;
     const int64_t rows = (int64_t)seqs * beams;
     a.per_thread = logits_of(rows, vocab, dtype);
     const int64_t chunk = a.per_thread * kThreads;

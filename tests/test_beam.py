@@ -152,6 +152,41 @@ def test_ties_go_to_the_lower_beam_then_token(dtype, V, K):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("seqs,W,K,V", [(2, 4, 9, 5), (1, 4, 32, 40000), (3, 130, 32, 300), (1, 2, 1, 9001), (2, 3, 7, 131072)])
+@pytest.mark.parametrize("live", [0, 1])
+def test_worths_that_64_bits_do_not_tell_apart(dtype, seqs, W, K, V, live):
+    # beams kept out of the race by the lowest finite score: every token of theirs is worth the same
+    x, scores, _ = inputs(seqs * W, V, dtype, 9)
+    scores[:] = torch.finfo(torch.float32).min
+    if live:      # one beam lives, with fewer tokens than are kept
+        scores[::W] = -1.0
+        x[::W, max(K - 3, 1):] = -math.inf
+        x[::W, 0] = 30.0 if dtype != torch.float16 else 8.0
+    for done in (None, (torch.arange(seqs * W) % W == 1).to(torch.uint8)):      # (one that is done is worth as much)
+        end = -1 if done is None else 2
+        want, _ = reference(x, scores, W, K, done, end)
+        res = L.idx_beam_step(x.cuda(), scores.cuda(), W, n_out=K, done=None if done is None else done.cuda(), end_token=end)
+        check(res, want, K, end, done=done)
+    assert L.idx_device_status(reset=True) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("W,K,V", [(1, 4, 5000), (2, 32, 20000), (3, 1, 700)])
+@pytest.mark.parametrize("up", [1, -1])
+def test_logits_that_64_bits_do_not_tell_apart(W, K, V, up):
+    # tiny logits, all different, that the sum's logarithm swallows; the lower token, whatever its logit
+    x = torch.full((W, V), -20.0)
+    at = torch.arange(3, V, 61)
+    n = torch.arange(1.0, len(at) + 1)
+    x[:, at] = (n if up > 0 else n.flip(0)) * 1e-30
+    scores = torch.full((W,), -2.0)
+    want, _ = reference(x, scores, W, K)
+    assert [c[2] for c in want[0]][:3] == at[:min(K, 3)].tolist()
+    check(L.idx_beam_step(x.cuda(), scores.cuda(), W, n_out=K), want, K, -1)
+
+
+@pytest.mark.gpu
 def test_no_numbers_are_flagged():
     x, scores, _ = inputs(8, 3000, torch.float32, 4)
     x[1, 2999], x[2, 0] = math.nan, math.inf
