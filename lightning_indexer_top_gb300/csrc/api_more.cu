@@ -24,6 +24,22 @@ bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p)
 
 bool valid_dtype(int t) { return t == IDX_F32 || t == IDX_F16 || t == IDX_BF16; }
 
+// rows of `width` bytes, `pitch` apart, `bytes` from the first to the end of the last
+struct Bytes {
+    const void* p;
+    int64_t bytes, pitch, width;
+};
+
+// (rows that lie equally far apart may be columns of one matrix, beside each other)
+bool overlap(const Bytes& x, const Bytes& y) {
+    if (!x.p || !y.p || !x.bytes || !y.bytes) return false;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+    if (a >= b + y.bytes || b >= a + x.bytes) return false;
+    if (x.pitch != y.pitch || x.pitch <= 0) return true;
+    const int64_t off = a >= b ? (int64_t)((a - b) % x.pitch) : x.pitch - 1 - (int64_t)((b - a - 1) % x.pitch);
+    return off < y.width || off + x.width > x.pitch;
+}
+
 // a 4-bit cache of n heads of d columns
 idx_status check_q4(const char* what, const char* which, const void* cache, int64_t stride, int64_t n, int64_t d) {
     if (stride < q4_payload(n, d))
@@ -246,23 +262,20 @@ idx_status idx_beam_step(const idx_beam* beam, idx_dtype dtype, int32_t n_seq, i
     if (!beam->lengths != !beam->history || !beam->lengths != !beam->out_lengths || !beam->lengths != !beam->out_history)
         return bad(IDX_ERR_INVALID_ARG, "%s: lengths, history and their outputs come together", what);
     // outputs of n_out rows a sequence over inputs of n_beams rows a sequence: another sequence may still read them
-    struct Span {
-        const void* p;
-        int64_t bytes;
-    };
     const int64_t in = (int64_t)n_seq * n_beams, out = (int64_t)n_seq * n_out;
-    auto rows = [](int64_t n, int64_t stride, int64_t cols, int64_t size) { return cols ? ((n - 1) * stride + cols) * size : 0; };
-    const Span reads[] = {{beam->logits, rows(in, beam->logit_stride, n_vocab, dtype == IDX_F32 ? 4 : 2)},
-                          {beam->scores, 4 * in}, {beam->done, in}, {beam->lengths, 4 * in},
-                          {beam->history, rows(in, beam->history_stride, beam->history_cols, 4)}};
-    const Span writes[] = {{beam->out_scores, 4 * out}, {beam->parent, 4 * out}, {beam->token, 4 * out}, {beam->out_done, out},
-                           {beam->out_lengths, 4 * out},
-                           {beam->out_history, rows(out, beam->out_history_stride, beam->history_cols, 4)}};
-    for (const Span& w : writes)
-        for (const Span& r : reads)
-            if (w.p && r.p && static_cast<const char*>(w.p) < static_cast<const char*>(r.p) + r.bytes &&
-                static_cast<const char*>(r.p) < static_cast<const char*>(w.p) + w.bytes)
-                return bad(IDX_ERR_INVALID_ARG, "%s: an output overlaps an input", what);
+    auto one = [](const void* p, int64_t n) -> Bytes { return {p, n, n, n}; };
+    auto rows = [](const void* p, int64_t n, int64_t stride, int64_t cols, int64_t size) -> Bytes {
+        return {p, cols ? ((n - 1) * stride + cols) * size : 0, stride * size, cols * size};
+    };
+    const Bytes reads[] = {rows(beam->logits, in, beam->logit_stride, n_vocab, dtype == IDX_F32 ? 4 : 2), one(beam->scores, 4 * in),
+                           one(beam->done, in), one(beam->lengths, 4 * in),
+                           rows(beam->history, in, beam->history_stride, beam->history_cols, 4)};
+    const Bytes writes[] = {one(beam->out_scores, 4 * out), one(beam->parent, 4 * out), one(beam->token, 4 * out),
+                            one(beam->out_done, out), one(beam->out_lengths, 4 * out),
+                            rows(beam->out_history, out, beam->out_history_stride, beam->history_cols, 4)};
+    for (const Bytes& w : writes)
+        for (const Bytes& r : reads)
+            if (overlap(w, r)) return bad(IDX_ERR_INVALID_ARG, "%s: an output overlaps an input", what);
     const size_t need = (size_t)beam_workspace_bytes(n_seq, n_beams, n_out, n_vocab);
     if (!workspace || workspace_bytes < need || !aligned(workspace, 16))
         return bad(IDX_ERR_INVALID_ARG, "%s: needs a 16-byte aligned workspace of %zu bytes (idx_beam_workspace_size)", what, need);

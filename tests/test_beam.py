@@ -187,6 +187,21 @@ def test_logits_that_64_bits_do_not_tell_apart(W, K, V, up):
 
 
 @pytest.mark.gpu
+def test_histories_that_are_columns_of_one_tensor():
+    # a step reads one half of each row and writes the other: nothing written is read
+    x, scores, g = inputs(8, 500, torch.float32, 10)
+    both = torch.randint(0, 500, (8, 24), generator=g, dtype=torch.int32).cuda()
+    lengths = torch.full((8,), 5, dtype=torch.int32, device="cuda")
+    call = lambda new: L.idx_beam_step(x.cuda(), scores.cuda(), 4, lengths=lengths, history=both[:, :12], history_out=new)  # noqa: E731
+    want = call(both[:, 12:].clone())
+    before = both[:, :12].clone()
+    got = call(both[:, 12:])
+    assert torch.equal(both[:, 12:], want.history) and torch.equal(both[:, :12], before) and torch.equal(got.lengths, want.lengths)
+    with pytest.raises(L.LidxError):      # one column is in both
+        call(both[:, 11:23])
+
+
+@pytest.mark.gpu
 def test_no_numbers_are_flagged():
     x, scores, _ = inputs(8, 3000, torch.float32, 4)
     x[1, 2999], x[2, 0] = math.nan, math.inf
