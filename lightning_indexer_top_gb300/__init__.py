@@ -1048,7 +1048,11 @@ def dense_attn_q4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                   workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """dense_attn over 4-bit caches (uint8 [rows, idx_q4_row_bytes(n_kv_heads, d)], see idx_cache_append_q4): the
     attention of q [B*T, Hq, dk] over the values that the codes stand for, with dense_attn's options.  dv: columns of V, dk
-    unless given.  Returns out [B*T, Hq, dv] of q's dtype."""
+    unless given.  Returns out [B*T, Hq, dv] of q's dtype.
+
+    Without a workspace the call allocates the preferred one (dense_attn_q4_workspace_size): for more than 256 packed rows, and for
+    heads other than 64 or 128 columns, that is room for K and V in 16 bits, 2 (2 dk + dv) bytes a position and kv head up to
+    batch.max_n_kv.  Where the device has no room for it, or with a smaller workspace, the call works without, more slowly."""
     dev = q.device
     _need_cuda(q)
     _all_on(dev, k_cache, v_cache, out, lse, workspace, batch.n_kv, batch.q_pos, batch.page_table, batch.kv_start)
@@ -1079,7 +1083,10 @@ def dense_attn_q4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
         if workspace is None:
             need = lib.dense_attn_q4_workspace_size(dt, b.n_seq, b.n_q_per_seq, b.max_n_kv, Hq, n_kv_heads, dk, dv)
             if need:
-                workspace = torch.empty(need, device=dev, dtype=torch.uint8)
+                try:
+                    workspace = torch.empty(need, device=dev, dtype=torch.uint8)
+                except torch.cuda.OutOfMemoryError:
+                    pass      # (expanded caches may want more than there is: the ways without)
         # (an empty cache has no address)
         _check(lib.dense_attn_q4(q.data_ptr(), dt, Hq, n_kv_heads, dk, dv, kc or q.data_ptr(), kc_stride, vc or q.data_ptr(),
                                  vc_stride, k_cache.shape[0], b, mods, scale, out.data_ptr(),

@@ -14,6 +14,7 @@ that a value is s (n - 8) + m':
 |error| <= 2 (2 dx + n u + 2^-20 + rounded weights and values) S + half(T) |out|.  lse: dx + n u + 2^-20 + u |lse|."""
 
 import ctypes
+import dataclasses
 import math
 
 import pytest
@@ -423,6 +424,26 @@ def test_keys_and_queries_of_every_size(dtype, T, d, mods):
         c.q = c.q * 2.0 ** q
         c.scale *= 2.0 ** s
         check_without_floor(c, *c.run())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,d", [(3, 80), (70, 128)])
+def test_a_workspace_that_does_not_fit_is_done_without(T, d):
+    c = Case4([300, 41], T, 8, 2, d, dtype=torch.bfloat16, seed=18)
+    real = c.batch
+    c.batch = lambda: dataclasses.replace(real(), max_n_kv=2 ** 22)      # (gigabytes; the sequences are as short as they were)
+    n = L.dense_attn_q4_workspace_size(torch.bfloat16, 2, T, 2 ** 22, 8, 2, d, d)
+    assert n > 2 ** 32
+    torch.cuda.empty_cache()
+    torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + 2 ** 30) / torch.cuda.get_device_properties(0).total_memory)
+    try:
+        out, lse = c.run()
+        with pytest.raises(torch.cuda.OutOfMemoryError):
+            torch.empty(n, dtype=torch.uint8, device="cuda")
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    c.check(out, lse)
+    assert L.idx_device_status(reset=True) == 0
 
 
 @pytest.mark.gpu
