@@ -642,8 +642,9 @@ typedef struct idx_new_rows {
  *     (u cos - w sin, w cos + u sin)   of the angle p * inv_freq[i].
  *   inv_freq   device f32 [n_rot/2], radians per position (scaled variants of the
  *              rotation are other numbers here), finite.
- * The angle is reduced in turns, as a 64-bit fraction times the position, so far
- * positions are as exact as near ones: its error is below 2^-52 of p * inv_freq, and f32's.
+ * The angle is reduced in turns, as a 64-bit fraction times the position, so that far
+ * positions are as exact as near ones after f32's rounding: its error is below p * 2^-63 of a turn
+ * (|inv_freq| of 2^24 and more: 2^-51 of p * inv_freq), and f32's.
  */
 typedef struct idx_rope {
     const float* inv_freq;

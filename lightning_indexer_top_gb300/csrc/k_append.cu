@@ -35,7 +35,8 @@ constexpr int kMaxCs = 2048;       // pairs of cosine and sine per CTA
 constexpr int kMaxD = 576;
 
 // Phase of position p in turns of 2^64: the fraction of f / 2 pi, times p.  In whole numbers: f = m 2^e with |m| < 2^24, and
-// 1 / 2 pi to 96 bits, good to 2^-64 of a turn for |f| < 2^24 (64-bit floats, which are scarce here, beyond).
+// 1 / 2 pi to 96 bits, good to 2^-63 of a turn for |f| < 2^24 (64-bit floats, which are scarce here, beyond).  Cut off at 2^-64 of
+// a turn whatever f, so the phase is good to p times that, not to a part of p f.
 __device__ __forceinline__ uint64_t phase(float f, int p) {
     const uint32_t bits = __float_as_uint(f);
     const int e = max((int)(bits >> 23 & 255u), 1) - 150;            // f = m 2^e

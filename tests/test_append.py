@@ -157,6 +157,24 @@ def test_far_positions(p):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("base", [1e6, 5e8, 1e20])
+@pytest.mark.parametrize("p", [1, 65535, 16777217, 2 ** 31 - 1025])
+def test_low_frequencies_at_far_positions(base, p):
+    # each pair by itself: f32's part, and the phase's 2^-63 of a turn times the position, whatever the pair's frequency
+    c = Rows([3], 1, 2, 1, 128, 64, torch.float32, 0, [1], 128, base=base)
+    c.pos = torch.tensor([p])
+    kc, vc = torch.zeros(3, 1, 128, device="cuda"), torch.zeros(3, 1, 64, device="cuda")
+    b = L.Batch(torch.tensor([p + 1], dtype=torch.int32, device="cuda"), 1, p + 1,
+                kv_start=torch.tensor([1 - p], dtype=torch.int32, device="cuda"), q_pos=c.pos.to("cuda", torch.int32))
+    q, k, v = c.gpu()
+    out = L.idx_cache_append(k, v, kc, vc, b, q=q, **c.rope())
+    for got, x in ((out, c.q), (kc[1:2], c.k)):
+        want, size = c.turned(x)
+        tol = size * (1.25 * 2.0 ** -22 + 2 * math.pi * p * 2.0 ** -63) + 2.0 ** -24 * want.abs()
+        assert ((got.cpu().double() - want).abs() <= tol).all()
+
+
+@pytest.mark.gpu
 def test_frequencies_of_any_sign_and_size():
     c = Rows([40], 7, 1, 1, 16, 16, torch.float32, 0, None, 16)
     c.freq = torch.tensor([-1.0, 3.5, -100.25, 1e-20, 0.0, 6.2831855, 1e4, -1e-3])
