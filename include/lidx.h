@@ -728,7 +728,7 @@ idx_status idx_cache_read_q4(const void* k_cache, int64_t k_row_stride, const vo
  * 16-bit q runs on the tensor cores, given 16-byte aligned tensors and rows:
  *   - up to 256 packed rows (tokens x heads of a kv head) of heads of 64 or 128 columns (dk == dv)
  *     on the codes themselves, the weights times the values' scale rounded to f16 for the second
- *     product.  Where a row sees a scale or minimum above 2^32 or a scale of V below 2^-57 that is
+ *     product (F16 calls: kept in two f16 parts).  Where a row sees a scale or minimum above 2^32 or a scale of V below 2^-57 that is
  *     not 0, or q reaches 2^70, a piece of its keys goes key by key in f32.
  *   - more rows, and other heads of at most 128 columns, on K and V expanded in the workspace (to
  *     64 GB, counted by max_n_kv): K in two parts (16 bits of significand together in BF16, 22 in

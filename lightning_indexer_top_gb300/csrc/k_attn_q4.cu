@@ -7,7 +7,9 @@
 //     output  O    = sum_j (p_j s_j) (n_j - 8) + sum_j p_j m'_j      columns are the M side, rows the N side
 // q is brought to f16 at a power of two of its row's (exact but for what lies 2^-27 below the row's largest), and the
 // weights p_j s_j are rounded to f16 at a running maximum of theirs; centring the codes keeps that rounding as small as
-// the values' own.  The order of columns within a product is free, so a lane takes 16 bytes of a key's codes as they lie and q
+// the values' own.  For bf16 results that is little beside their own rounding (0.0017 of the result with and without); f16
+// results would be off by 1.3 times theirs, so there what the weights lack is a second operand (the decode below, in f16: 70 us
+// for 67).  The order of columns within a product is free, so a lane takes 16 bytes of a key's codes as they lie and q
 // is laid out to match.
 //
 // 16 sequences of up to 32768 keys, 32 bf16 heads of 128 on 4, 64-row pages: 67 us for 231 MB, 3.4 TB/s.  Not memory bounds it
@@ -296,6 +298,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NB>::kCtas)
     q4_kernel(const __grid_constant__ Q4Args p, const __grid_constant__ Geom g, const __grid_constant__ Maps maps) {
     using S = Shape<D, NB>;
     constexpr int R = S::R;
+    constexpr bool kRest = std::is_same<T, __half>::value;      // the weights in two parts
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ uint64_t full[kWarps][S::kStages];
@@ -648,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NB>::kCtas)
             for (int r = 0; r < 2; ++r) l_run[nb][r] += sum[nb][r];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            uint32_t pf[NB][2];
+            uint32_t pf[NB][2], pr_rest[kRest ? NB : 1][2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const float low = fmaf(8.f, vp[h][k].x, vp[h][k].y);
@@ -666,6 +669,16 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NB>::kCtas)
                             if (s[h][nb][2 * k + r] == -INFINITY) low_run[nb][r] = add[r];
                     }
                     pf[nb][k] = transpose8(wh[h][nb][k]);
+                    if constexpr (kRest) {
+                        const float2 w = __half22float2(as_h2(wh[h][nb][k]));
+                        float rest[2] = {fmaf(pr[h][nb][2 * k], vp[h][k].x, -w.x), fmaf(pr[h][nb][2 * k + 1], vp[h][k].x, -w.y)};
+                        if (!whole) {
+#pragma unroll
+                            for (int r = 0; r < 2; ++r)
+                                if (s[h][nb][2 * k + r] == -INFINITY) rest[r] = 0.f;
+                        }
+                        pr_rest[nb][k] = transpose8(h2(__floats2half2_rn(rest[0], rest[1])));
+                    }
                 }
             }
             uint32_t v[4][D / 64];
@@ -683,8 +696,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NB>::kCtas)
                 for (int k = 0; k < 4; ++k) {
                     const int hh = k & 2, j = 2 * (k & 1);
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
+                    for (int nb = 0; nb < NB; ++nb) {
                         mma(o[nb][4 * i + k], f[hh][j], f[hh][j + 1], f[hh + 1][j], f[hh + 1][j + 1], pf[nb][0], pf[nb][1]);
+                        if constexpr (kRest)
+                            mma(o[nb][4 * i + k], f[hh][j], f[hh][j + 1], f[hh + 1][j], f[hh + 1][j + 1], pr_rest[nb][0], pr_rest[nb][1]);
+                    }
                 }
             }
         }

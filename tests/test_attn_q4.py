@@ -427,6 +427,22 @@ def test_keys_and_queries_of_every_size(dtype, T, d, mods):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,heads", [(1, (8, 2, 64)), (1, (16, 2, 128)), (4, (24, 8, 64)), (20, (8, 1, 128))])
+@pytest.mark.parametrize("n_kv", [(400, 130), (1, 2), (17, 33)])
+@pytest.mark.parametrize("mods", [{}, dict(cap=3.0, slopes=True)])
+def test_f16_results_are_as_near_as_their_own_rounding(T, heads, n_kv, mods):
+    # What is not the result's rounding (2^-12 of an element at most, in the mean half of that) is f32's: sums of 128 terms, off by
+    # some 2^-24 sqrt(128) of scores of size 4, 2^-17.  Errors that know nothing of each other add in squares: 1 + 2^-8.
+    c = Case4([max(n, T) for n in n_kv], T, *heads, dtype=torch.float16, page=16, seed=19, **mods)
+    out, _ = c.run()
+    ref, ref_lse, _, _ = c.reference()
+    seen = ~torch.isneginf(ref_lse)
+    err = (out.cpu().double().view(ref.shape) - ref)[seen].square().mean().sqrt()
+    own = (ref.half().double() - ref)[seen].square().mean().sqrt()
+    assert err <= 1.05 * own, float(err / own)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T,d", [(3, 80), (70, 128)])
 def test_a_workspace_that_does_not_fit_is_done_without(T, d):
     c = Case4([300, 41], T, 8, 2, d, dtype=torch.bfloat16, seed=18)
