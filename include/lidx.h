@@ -733,7 +733,7 @@ idx_status idx_cache_read_q4(const void* k_cache, int64_t k_row_stride, const vo
  *   - more rows, and other heads of at most 128 columns, on K and V expanded in the workspace (to
  *     64 GB, counted by max_n_kv): K in two parts (16 bits of significand together in BF16, 22 in
  *     F16, nothing below F16's least number), V in f16 at a power of two of the sequence's and
- *     head's largest, the weights in f16.  With a number of K beyond dtype's range, or a key whose V
+ *     head's largest, the weights in f16 (F16 calls: both in two f16 parts).  With a number of K beyond dtype's range, or a key whose V
  *     is 2^-28 or less of that largest, the call goes to the CUDA cores after all.
  * Everything else runs on the CUDA cores in f32.
  */

@@ -1051,8 +1051,8 @@ def dense_attn_q4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     unless given.  Returns out [B*T, Hq, dv] of q's dtype.
 
     Without a workspace the call allocates the preferred one (dense_attn_q4_workspace_size): for more than 256 packed rows, and for
-    heads other than 64 or 128 columns, that is room for K and V in 16 bits, 2 (2 dk + dv) bytes a position and kv head up to
-    batch.max_n_kv.  Where the device has no room for it, or with a smaller workspace, the call works without, more slowly."""
+    heads other than 64 or 128 columns, that is room for K and V in 16 bits, 2 (2 dk + dv) bytes (float16: 4 (dk + dv)) a position
+    and kv head up to batch.max_n_kv.  Where the device has no room for it, or with a smaller workspace, the call works without, more slowly."""
     dev = q.device
     _need_cuda(q)
     _all_on(dev, k_cache, v_cache, out, lse, workspace, batch.n_kv, batch.q_pos, batch.page_table, batch.kv_start)

@@ -28,6 +28,7 @@ struct DenseArgs {
     float* part_ml;           // [row * Hq + head][split][2]: maximum (natural-log units), sum
     const void* k_rest;       // or NULL.  Given (tensor cores): K is the sum of k and this, laid out alike, and V f16
     const int* v_top;         // ... at the power of two that v_exponent makes of this [B, Hkv]
+    const void* v_rest;       // ... with f16 q: what V lacks of its f32, in f16, laid out alike
     const int* only_if;       // or NULL; given and 0 on the device: the launch has nothing to do (CUDA cores, 4 bits)
 };
 

@@ -710,11 +710,16 @@ __global__ void __launch_bounds__(kThreads) read_q4_kernel(ExpandArgs p, Geom g,
             if (isfinite(scale) && isfinite(low) && most > 0.f && most * f < 0x1p-14f) *p.lost = 1;
 #pragma unroll
             for (int c = 0; c < kCols; c += 8) {
-                __half y[8];
+                __half y[8], z[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    y[j] = from_f32<__half>(fmaf((float)((x[c / 8] >> (4 * j)) & 15u), scale, low) * f);
+                for (int j = 0; j < 8; ++j) {
+                    const float v = fmaf((float)((x[c / 8] >> (4 * j)) & 15u), scale, low) * f;
+                    y[j] = from_f32<__half>(v);
+                    z[j] = from_f32<__half>(v - to_f32(y[j]));
+                }
                 *reinterpret_cast<uint4*>(dst + c) = *reinterpret_cast<const uint4*>(y);
+                if (p.v_rest)
+                    *reinterpret_cast<uint4*>(static_cast<T*>(p.v_rest) + (dst - static_cast<T*>(a.v_out)) + c) = *reinterpret_cast<const uint4*>(z);
             }
             continue;
         }

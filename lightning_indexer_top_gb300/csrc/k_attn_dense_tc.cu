@@ -60,8 +60,8 @@ constexpr int kOtherWarps = 4;
 template <int D, bool kMods>
 constexpr bool kDoubleS = kMods || D == 64;
 
-// kTwo (see the kernel): a key tile is two entries of K's ring
-template <int D, int kTiles, bool kTwo = false>
+// kTwo (see the kernel): a key tile is two entries of K's ring; kBoth: and two of V's
+template <int D, int kTiles, bool kTwo = false, bool kBoth = false>
 struct Cfg {
     static constexpr int kTileBytes = kKeys * D * 2;
     // rows of Q kept per row tile.  With kFewRows the M = 128 products read on into the K tile: what they
@@ -69,9 +69,9 @@ struct Cfg {
     static constexpr int kQRows = kTiles == 2 ? kRows : kFewRows;
     static constexpr int kQTile = kQRows * D * 2;
     static constexpr int kQBlock = kQRows * 128;      // 64 columns of it
-    static constexpr int kStagesK = kTwo ? (kTiles == 2 || D == 64 ? 3 : 2) : kTiles == 2 ? 2 : D == 64 ? 2 : 1;
-    static constexpr int kStagesV = kTwo && D == 128 ? (kTiles == 2 ? 2 : 1) : kTiles == 2 ? 3 : D == 64 ? 3 : 2;
-    static constexpr int kCtas = kTiles == 2 ? 1 : 2;   // (two: 128 registers; with options 28 to 40 bytes are spilled)
+    static constexpr int kStagesK = kTwo ? (kTiles == 2 || D == 64 || kBoth ? 3 : 2) : kTiles == 2 ? 2 : D == 64 ? 2 : 1;
+    static constexpr int kStagesV = kTwo && D == 128 ? (kTiles == 2 || kBoth ? 2 : 1) : kTiles == 2 ? 3 : D == 64 ? 3 : 2;
+    static constexpr int kCtas = kTiles == 2 || (kBoth && D == 128) ? 1 : 2;   // (two: 128 registers; with options 28 to 40 bytes are spilled)
     static constexpr int kKOff = kTiles * kQTile;
     static constexpr int kVOff = kKOff + kStagesK * kTileBytes;
     static constexpr int kCtlOff = kVOff + kStagesV * kTileBytes;
@@ -134,6 +134,7 @@ __device__ __noinline__ void scalar_row(const DenseArgs& a, const Geom& g, int b
         const T* k = static_cast<const T*>(a.k) + row * a.k_stride + (int64_t)gkv * a.dk;
         const V* v = static_cast<const V*>(a.v) + row * a.v_stride + (int64_t)gkv * a.dv;
         const T* rest = a.k_rest ? static_cast<const T*>(a.k_rest) + row * a.k_stride + (int64_t)gkv * a.dk : nullptr;
+        const V* v_rest = a.v_rest ? static_cast<const V*>(a.v_rest) + row * a.v_stride + (int64_t)gkv * a.dv : nullptr;
         float x = 0.f;
         for (int c = 0; c < a.dk; ++c) x = fmaf(to_f32(q[c]), to_f32(k[c]) + (rest ? to_f32(rest[c]) : 0.f), x);
         x *= a.scale;
@@ -146,7 +147,7 @@ __device__ __noinline__ void scalar_row(const DenseArgs& a, const Geom& g, int b
         const float w = exp2f(x - ref);
         m = mn;
         l = fmaf(l, al, w);
-        for (int c = 0; c < a.dv; ++c) acc[c] = fmaf(w, to_f32(v[c]), al == 1.f ? acc[c] : acc[c] * al);
+        for (int c = 0; c < a.dv; ++c) acc[c] = fmaf(w, to_f32(v[c]) + (v_rest ? to_f32(v_rest[c]) : 0.f), al == 1.f ? acc[c] : acc[c] * al);
     }
     ml[0] = m;
     ml[1] = l;
@@ -205,17 +206,30 @@ __device__ __forceinline__ void store_rows(E* out, int64_t at, int n_rows, const
 // kTwo: K is the sum of two tensors of T, for keys that T alone does not hold (values of 4-bit codes): the scores are two
 // products into the same accumulators.  V and the weights are f16 then, V at a power of two.  4096 tokens of 32 heads of 128 on
 // 16384 keys: 969 us, tensor pipe busy on 72 % of the active cycles (57 % with K in one part).
+// With f16 q the results are f16 too, and roundings of V and of the weights would be as large as the results' own: both are in
+// two parts as well (kBoth), P's second one beside the first in TMEM, and O three products: with one part each results were off by
+// 1.7 times their rounding.  The same tokens take 1.5 ms; one row tile of heads above 64 columns has an SM to itself then (16 sequences
+// of up to 32768 keys, 20 heads of 80 on 4: 747 us with the expansion, for 531).
+template <typename T, bool kTwo>
+constexpr bool kBothParts = kTwo && std::is_same<T, __half>::value;
+
+template <typename T, int D, int kTiles, bool kTwo>
+using CfgOf = Cfg<D, kTiles, kTwo, kBothParts<T, kTwo>>;
+
 template <typename T, int D, int kTiles, bool kMods, bool kTwo>
-__global__ void __launch_bounds__(Cfg<D, kTiles, kTwo>::kThreads, Cfg<D, kTiles, kTwo>::kCtas)
+__global__ void __launch_bounds__(CfgOf<T, D, kTiles, kTwo>::kThreads, CfgOf<T, D, kTiles, kTwo>::kCtas)
     dense_tc_kernel(TcArgs p, Geom g, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                    const __grid_constant__ CUtensorMap rmap) {
-    using C = Cfg<D, kTiles, kTwo>;
+                    const __grid_constant__ CUtensorMap rmap, const __grid_constant__ CUtensorMap vrmap) {
+    using C = CfgOf<T, D, kTiles, kTwo>;
+    constexpr bool kBoth = kBothParts<T, kTwo>;
+    constexpr int kEntriesK = kTwo ? 2 : 1, kEntriesV = kBoth ? 2 : 1;      // of the rings for a tile
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     using V = std::conditional_t<kTwo, __half, T>;
     constexpr bool kBf16V = std::is_same<V, __nv_bfloat16>::value;
     constexpr float kShift = kBf16V ? 0.f : 7.f;    // P is kept this much (log2) larger
     constexpr float kTop = kShift + 8.f;
     constexpr bool kDouble = kDoubleS<D, kMods>;
+    constexpr int kPStep = kDouble || kBoth ? kHalf : kHalf / 2;      // TMEM columns from P's first half to its second
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* kt = smem + C::kKOff;
@@ -365,8 +379,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kTwo>::kThreads, Cfg<D, kTiles,
             // -------------------------------------------------- producer: a lane per (piece, 64 columns)
             const int pieces = kKeys / p.box;
             const int64_t row_base = g.page_table ? 0 : seq_row0(g, b);
-            constexpr int kEntries = kTwo ? 2 : 1;     // of K's ring for a tile
-            int sent_k = 0, sent_v = 0;                // entries and tiles whose loads were issued
+            int sent_k = 0, sent_v = 0;                // entries whose loads were issued
             auto load = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* bar, int j) {
                 if (lane == 0) mbar_arrive_expect_tx(bar, C::kTileBytes);
                 __syncwarp();
@@ -387,22 +400,27 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kTwo>::kThreads, Cfg<D, kTiles,
                 }
             };
             for (int j = 0; j < n; ++j) {
-                const int sv = j % C::kStagesV;
                 bool ok = true;
 #pragma unroll
-                for (int x = 0; ok && x < kEntries; ++x) {
+                for (int x = 0; ok && x < kEntriesK; ++x) {
                     const int sk = sent_k % C::kStagesK;
                     ok = !warp_aborted() && warp_wait(&c.kempty[sk], (uint32_t)((sent_k / C::kStagesK) & 1) ^ 1);
                     if (!ok) break;
                     load(x ? &rmap : &kmap, kt + sk * C::kTileBytes, &c.kfull[sk], j);
                     ++sent_k;
                 }
-                if (!ok || warp_aborted() || !warp_wait(&c.vempty[sv], (uint32_t)((j / C::kStagesV) & 1) ^ 1)) {
+#pragma unroll
+                for (int x = 0; ok && x < kEntriesV; ++x) {
+                    const int sv = sent_v % C::kStagesV;
+                    ok = !warp_aborted() && warp_wait(&c.vempty[sv], (uint32_t)((sent_v / C::kStagesV) & 1) ^ 1);
+                    if (!ok) break;
+                    load(x ? &vrmap : &vmap, vt + sv * C::kTileBytes, &c.vfull[sv], j);
+                    ++sent_v;
+                }
+                if (!ok) {
                     give_up();
                     break;
                 }
-                load(&vmap, vt + sv * C::kTileBytes, &c.vfull[sv], j);
-                ++sent_v;
             }
             if (warp_aborted()) {
                 // no load may still be in flight when the CTA ends
@@ -468,17 +486,28 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kTwo>::kThreads, Cfg<D, kTiles,
                 return there;
             };
             // O += P V of half a tile, and the commits that follow it
-            auto pv = [&](int half, uint32_t first, uint64_t* b0, uint64_t* b1) {
+            auto second_v = [&] { return kBoth ? (sv + 1 == C::kStagesV ? 0 : sv + 1) : sv; };      // the second entry
+            auto pv = [&](int half, uint32_t first, uint64_t* b0, uint64_t* b1, uint64_t* b2) {
                 const uint32_t va = __shfl_sync(0xffffffffu, vb + ((sv * C::kTileBytes + half * (kHalf * 128)) >> 4), 0);
-                const uint32_t pa = __shfl_sync(0xffffffffu, ts + half * (kDouble ? kHalf : kHalf / 2), 0);
+                const uint32_t vr = __shfl_sync(0xffffffffu, vb + ((second_v() * C::kTileBytes + half * (kHalf * 128)) >> 4), 0);
+                const uint32_t pa = __shfl_sync(0xffffffffu, ts + half * kPStep, 0);
                 const uint32_t acc = __shfl_sync(0xffffffffu, first ? 0u : 1u, 0);
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < kHalf / 16; ++ks)
                         mma_f16_ts_lo(to, pa + ks * 8, va + (ks * 2048 >> 4), v_hi, id_pv, ks > 0 ? 1u : acc);
+                    if constexpr (kBoth) {
+#pragma unroll
+                        for (int ks = 0; ks < kHalf / 16; ++ks)
+                            mma_f16_ts_lo(to, pa + kHalf / 2 + ks * 8, va + (ks * 2048 >> 4), v_hi, id_pv, 1u);
+#pragma unroll
+                        for (int ks = 0; ks < kHalf / 16; ++ks)
+                            mma_f16_ts_lo(to, pa + ks * 8, vr + (ks * 2048 >> 4), v_hi, id_pv, 1u);
+                    }
                     if (b0) mma_commit(b0);
                     if (b1) mma_commit(b1);
+                    if (b2) mma_commit(b2);
                 }
                 __syncwarp();
             };
@@ -489,30 +518,33 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kTwo>::kThreads, Cfg<D, kTiles,
             }
             for (int j = 0; ok && j < n; ++j) {
                 const bool last = j + 1 == n;
-                ok = warp_wait(&c.vok[sv], (uint32_t)vph) && warp_wait(&c.pready[i][0], (uint32_t)(j & 1));
+                ok = warp_wait(&c.vok[sv], (uint32_t)vph) &&
+                     (!kBoth || warp_wait(&c.vok[second_v()], (uint32_t)(second_v() > sv ? vph : vph ^ 1))) &&
+                     warp_wait(&c.pready[i][0], (uint32_t)(j & 1));
                 if (!ok) break;
                 // new scores follow the product over the weights that they replace: a row tile's products run in order.
                 // (Two buffers: the commit after the last tile's first half has no scores; it tells that the products
                 // of the step before are complete, as scores would.)
                 if (kDouble) {
-                    pv(0, j == 0, last ? &c.sfull[i][0] : nullptr, nullptr);
+                    pv(0, j == 0, last ? &c.sfull[i][0] : nullptr, nullptr, nullptr);
                     if (!last) {
                         ok = wait_k();
                         if (!ok) break;
                         qk(0);
                     }
                 } else {
-                    pv(0, j == 0, &c.pvdone[i], nullptr);
+                    pv(0, j == 0, &c.pvdone[i], nullptr, nullptr);
                     ok = last || wait_k();
                 }
                 ok = ok && warp_wait(&c.pready[i][1], (uint32_t)(j & 1));
                 if (!ok) break;
-                pv(1, false, &c.vempty[sv], last ? &c.odone[i] : nullptr);
+                pv(1, false, &c.vempty[sv], last ? &c.odone[i] : nullptr, kBoth ? &c.vempty[second_v()] : nullptr);
                 if (!last) qk(kDouble ? 1 : 0);
-                if (++sv == C::kStagesV) {
-                    sv = 0;
-                    vph ^= 1;
-                }
+                for (int x = 0; x < kEntriesV; ++x)
+                    if (++sv == C::kStagesV) {
+                        sv = 0;
+                        vph ^= 1;
+                    }
             }
             if (!ok) give_up();
             if (elect_one()) mma_commit(&c.done[i]);
@@ -520,24 +552,24 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kTwo>::kThreads, Cfg<D, kTiles,
             warp_wait(&c.done[i], 0);
         } else if (warp == kOtherWarps - 1) {
             // -------------------------------------------------- V inspector: tiles that some row sees in part
-            for (int j = 0; j < n; ++j) {
-                const int sv = j % C::kStagesV;
-                if (warp_aborted() || !warp_wait(&c.vfull[sv], (uint32_t)((j / C::kStagesV) & 1))) {
+            for (int x = 0; x < n * kEntriesV; ++x) {
+                const int sv = x % C::kStagesV;
+                if (warp_aborted() || !warp_wait(&c.vfull[sv], (uint32_t)((x / C::kStagesV) & 1))) {
                     give_up();
                     break;
                 }
-                const int key0 = (t0 + j) * kKeys;
+                const int key0 = (t0 + x / kEntriesV) * kKeys;
                 if (key0 < max(full0, k0) || key0 + kKeys > min(full1, k1)) {
                     uint8_t* v = vt + sv * C::kTileBytes;
                     bool found = false;
                     // four lanes per V row and column block (rows of 128 bytes)
                     for (int e = lane; e < kKeys * 4 * (D / 64); e += 32) {
                         const int row = (e >> 2) & (kKeys - 1), cb = e / (kKeys * 4);
-                        uint4* x = reinterpret_cast<uint4*>(v + cb * kColBlock + row * 128 + (e & 3) * 32);
+                        uint4* at = reinterpret_cast<uint4*>(v + cb * kColBlock + row * 128 + (e & 3) * 32);
                         if (key0 + row < k0 || key0 + row >= k1) {
-                            x[0] = x[1] = make_uint4(0u, 0u, 0u, 0u);
+                            at[0] = at[1] = make_uint4(0u, 0u, 0u, 0u);
                         } else if (key0 + row < full0 || key0 + row >= full1) {
-                            const uint4 y[2] = {x[0], x[1]};
+                            const uint4 y[2] = {at[0], at[1]};
                             const uint32_t* z = reinterpret_cast<const uint32_t*>(y);
                             constexpr uint32_t kExp = kBf16V ? 0x7F80u : 0x7C00u;
 #pragma unroll
@@ -663,8 +695,20 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kTwo>::kThreads, Cfg<D, kTiles,
                 else
                     lb = add2(lb, pair(p0, p1));
                 w[i / 2] = pack2<V>(p0, p1);
+                if constexpr (kBoth) {
+                    s[i] = p0;
+                    s[i + 1] = p1;
+                }
             }
-            tmem_st_32x32b_x32(ts + half * (kDouble ? kHalf : kHalf / 2), w);
+            tmem_st_32x32b_x32(ts + half * kPStep, w);
+            if constexpr (kBoth) {      // what the rounding took off
+#pragma unroll
+                for (int i = 0; i < kHalf; i += 2) {
+                    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[i / 2]));
+                    w[i / 2] = pack2<V>(s[i] - x.x, s[i + 1] - x.y);
+                }
+                tmem_st_32x32b_x32(ts + half * kPStep + kHalf / 2, w);
+            }
             float l0, l1;
             unpair(add2(la, lb), l0, l1);
             l_run += l0 + l1;
@@ -790,16 +834,15 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kTwo>::kThreads, Cfg<D, kTiles,
 int row_tiles(int64_t packed) { return packed > kFewRows ? 2 : 1; }
 
 template <typename T, int D, int kTiles, bool kMods, bool kTwo>
-cudaError_t go(const TcArgs& p, const Geom& g, const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& rm,
-               int64_t grid, cudaStream_t st) {
-    using C = Cfg<D, kTiles, kTwo>;
+cudaError_t go(const TcArgs& p, const Geom& g, const CUtensorMap* m, int64_t grid, cudaStream_t st) {
+    using C = CfgOf<T, D, kTiles, kTwo>;
     constexpr size_t sm = 1024 + (size_t)C::kCtlOff + sizeof(Ctl);
     static_assert((sm + 1024) * C::kCtas <= 233472, "shared memory of an SM");
     auto kern = dense_tc_kernel<T, D, kTiles, kMods, kTwo>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
     if (e != cudaSuccess) return e;
     return launch_pdl_cluster(kern, dim3((unsigned)grid), dim3(C::kThreads), sm, st,
-                              p.a.splits > 1 && !p.a.part_o ? p.a.splits : 1, p, g, km, vm, rm);
+                              p.a.splits > 1 && !p.a.part_o ? p.a.splits : 1, p, g, m[0], m[1], m[2], m[3]);
 }
 
 template <typename T, bool kTwo>
@@ -809,23 +852,26 @@ cudaError_t run(const DenseArgs& a, const Geom& g, cudaStream_t st) {
     TcArgs p = {a, (int)((packed + tiles * kRows - 1) / (tiles * kRows)), box_rows(g.page_size, kKeys)};
     const int64_t grid = (int64_t)g.B * a.Hkv * p.tiles * a.splits;
     if (grid > INT32_MAX) return cudaErrorNotSupported;
-    CUtensorMap km, vm, rm;
     constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
-    if (!make_head_tmap(&km, a.k, bf16, a.dk, a.Hkv, a.k_stride, a.kv_rows, p.box) ||
-        !make_head_tmap(&vm, a.v, bf16 && !kTwo, a.dv, a.Hkv, a.v_stride, a.kv_rows, p.box))
+    CUtensorMap m[4];      // K, V, and what they lack
+    if (!make_head_tmap(&m[0], a.k, bf16, a.dk, a.Hkv, a.k_stride, a.kv_rows, p.box) ||
+        !make_head_tmap(&m[1], a.v, bf16 && !kTwo, a.dv, a.Hkv, a.v_stride, a.kv_rows, p.box))
         return cudaErrorNotSupported;
-    rm = km;
-    if (kTwo && !make_head_tmap(&rm, a.k_rest, bf16, a.dk, a.Hkv, a.k_stride, a.kv_rows, p.box)) return cudaErrorNotSupported;
+    m[2] = m[0];
+    m[3] = m[1];
+    if (kTwo && !make_head_tmap(&m[2], a.k_rest, bf16, a.dk, a.Hkv, a.k_stride, a.kv_rows, p.box)) return cudaErrorNotSupported;
+    if (kBothParts<T, kTwo> && !make_head_tmap(&m[3], a.v_rest, false, a.dv, a.Hkv, a.v_stride, a.kv_rows, p.box))
+        return cudaErrorNotSupported;
     const bool small = a.dk <= 64 && a.dv <= 64;
     const bool mods = a.mods.softcap > 0.f || a.mods.slopes || a.scale <= 0.f;
     if (small) {
         if (tiles == 1)
-            return mods ? go<T, 64, 1, true, kTwo>(p, g, km, vm, rm, grid, st) : go<T, 64, 1, false, kTwo>(p, g, km, vm, rm, grid, st);
-        return mods ? go<T, 64, 2, true, kTwo>(p, g, km, vm, rm, grid, st) : go<T, 64, 2, false, kTwo>(p, g, km, vm, rm, grid, st);
+            return mods ? go<T, 64, 1, true, kTwo>(p, g, m, grid, st) : go<T, 64, 1, false, kTwo>(p, g, m, grid, st);
+        return mods ? go<T, 64, 2, true, kTwo>(p, g, m, grid, st) : go<T, 64, 2, false, kTwo>(p, g, m, grid, st);
     }
     if (tiles == 1)
-        return mods ? go<T, 128, 1, true, kTwo>(p, g, km, vm, rm, grid, st) : go<T, 128, 1, false, kTwo>(p, g, km, vm, rm, grid, st);
-    return mods ? go<T, 128, 2, true, kTwo>(p, g, km, vm, rm, grid, st) : go<T, 128, 2, false, kTwo>(p, g, km, vm, rm, grid, st);
+        return mods ? go<T, 128, 1, true, kTwo>(p, g, m, grid, st) : go<T, 128, 1, false, kTwo>(p, g, m, grid, st);
+    return mods ? go<T, 128, 2, true, kTwo>(p, g, m, grid, st) : go<T, 128, 2, false, kTwo>(p, g, m, grid, st);
 }
 
 }  // namespace

@@ -1019,16 +1019,17 @@ __global__ void __launch_bounds__(256) v_top_kernel(ExpandArgs p, Geom g, int* t
     }
 }
 
-// where the expanded K (in two parts) and V lie in the workspace, behind the spans, the largest values and the mark of lost keys
+// where the expanded K (in two parts) and V (f16 calls: in two) lie in the workspace, behind the spans, the largest values and the mark of lost keys
 struct Expanded {
-    size_t top_at, k_at, rest_at, v_at, bytes;
-    Expanded(int64_t n_seq, int64_t max_n_kv, int Hkv, int dk, int dv) {
+    size_t top_at, k_at, rest_at, v_at, v_rest_at, bytes;
+    Expanded(int dtype, int64_t n_seq, int64_t max_n_kv, int Hkv, int dk, int dv) {
         const size_t rows = (size_t)n_seq * max_n_kv * Hkv;
         top_at = n_seq * sizeof(int2) + sizeof(int);
         k_at = (top_at + n_seq * Hkv * sizeof(int) + 15) / 16 * 16;
         rest_at = k_at + rows * dk * 2;
         v_at = rest_at + rows * dk * 2;
-        bytes = v_at + rows * dv * 2;
+        v_rest_at = v_at + rows * dv * 2;
+        bytes = v_rest_at + (dtype == IDX_F16 ? rows * dv * 2 : 0);
     }
 };
 
@@ -1038,7 +1039,7 @@ constexpr int64_t kMaxExpanded = (int64_t)1 << 36;
 
 bool expands(int dtype, int64_t n_seq, int64_t packed, int64_t max_n_kv, int Hkv, int dk, int dv) {
     if (dtype == IDX_F32 || dk > 128 || dv > 128) return false;
-    if (n_seq * max_n_kv > kMaxExpanded / (Hkv * (4 * (int64_t)dk + 2 * dv))) return false;
+    if (n_seq * max_n_kv > kMaxExpanded / (Hkv * (4 * (int64_t)dk + (dtype == IDX_F16 ? 4 : 2) * dv))) return false;
     return packed > kManyRows || dk != dv || (dk != 64 && dk != 128);
 }
 
@@ -1052,7 +1053,7 @@ cudaError_t run_few(const DenseArgs& a, const Geom& g, void* ws, size_t ws_bytes
 }  // namespace
 
 size_t q4_attn_workspace_bytes(int dtype, int64_t n_seq, int64_t n_q, int64_t max_n_kv, int Hq, int Hkv, int dk, int dv) {
-    if (expands(dtype, n_seq, n_q * (Hq / Hkv), max_n_kv, Hkv, dk, dv)) return Expanded(n_seq, max_n_kv, Hkv, dk, dv).bytes;
+    if (expands(dtype, n_seq, n_q * (Hq / Hkv), max_n_kv, Hkv, dk, dv)) return Expanded(dtype, n_seq, max_n_kv, Hkv, dk, dv).bytes;
     if (dtype != IDX_F32 && dk == dv && (dk == 64 || dk == 128)) {
         const int64_t packed = n_q * (Hq / Hkv);
         const int nb = n_blocks(packed);
@@ -1068,12 +1069,12 @@ size_t q4_attn_workspace_bytes(int dtype, int64_t n_seq, int64_t n_q, int64_t ma
 // own rounding) at a power of two, K as a sum of two of dtype (16 or 22 bits), since the log of the weights' sum is f32.  Of
 // the 1004 to 1025 us of 4096 tokens of 32 heads on 16384 keys the second product of K takes some 240 (K in bf16 alone: 740),
 // spans, largest values and expansion of 16384 rows some 30.  (Scales applied to the products of exact codes, in the softmax: 1455 us; it is the
-// softmax that the kernel waits for.)
+// softmax that the kernel waits for.)  For f16 results the weights and V are in two parts too (1541 us).
 // What that kernel cannot know of or hold, keys without a row in the cache, numbers beyond dtype's range in K and keys whose V is
 // 2^-28 or less of the largest, sends everything through the CUDA cores again, which skip and flag the one and hold the others in
 // f32.
 static cudaError_t run_expanded(DenseArgs a, int dtype, const Geom& g, uint8_t* ws, cudaStream_t st) {
-    const Expanded e(g.B, g.max_n_kv, a.Hkv, a.dk, a.dv);
+    const Expanded e(dtype, g.B, g.max_n_kv, a.Hkv, a.dk, a.dv);
     int2* span = reinterpret_cast<int2*>(ws);
     int* lost = reinterpret_cast<int*>(ws + (size_t)g.B * sizeof(int2));
     DenseArgs d = a;
@@ -1108,6 +1109,7 @@ static cudaError_t run_expanded(DenseArgs a, int dtype, const Geom& g, uint8_t* 
     x.lost = lost;
     x.k_rest = ws + e.rest_at;
     d.k_rest = x.k_rest;
+    if (dtype == IDX_F16) d.v_rest = x.v_rest = ws + e.v_rest_at;
     int* top = reinterpret_cast<int*>(ws + e.top_at);
     x.v_top = d.v_top = top;
     Geom all = g;
@@ -1126,7 +1128,7 @@ static cudaError_t run_expanded(DenseArgs a, int dtype, const Geom& g, uint8_t* 
 
 cudaError_t launch_attn_q4(DenseArgs a, int dtype, const Geom& g, void* ws, size_t ws_bytes, cudaStream_t st) {
     if (g.max_n_kv > 0 && expands(dtype, g.B, (int64_t)g.T * (a.Hq / a.Hkv), g.max_n_kv, a.Hkv, a.dk, a.dv) &&
-        ws_bytes >= Expanded(g.B, g.max_n_kv, a.Hkv, a.dk, a.dv).bytes) {
+        ws_bytes >= Expanded(dtype, g.B, g.max_n_kv, a.Hkv, a.dk, a.dv).bytes) {
         const cudaError_t e = run_expanded(a, dtype, g, static_cast<uint8_t*>(ws), st);
         if (e != cudaErrorNotSupported) return e;
     }

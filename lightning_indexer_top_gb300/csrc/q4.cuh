@@ -35,13 +35,14 @@ struct ReadArgs {
 cudaError_t launch_read_q4(const ReadArgs& a, int dtype, const Geom& g, cudaStream_t st);
 
 // The positions of each sequence's span (device, [lo, hi)) for the attention: the values of K in dtype, row b * g.T + position,
-// what they lack of their f32 in k_rest, and V in f16.  A position whose cache row is out of range, with a number of K beyond
+// what they lack of their f32 in k_rest, and V in f16 (and v_rest).  A position whose cache row is out of range, with a number of K beyond
 // dtype's, or whose largest of V is no normal f16 sets *lost, in place of the device status.
 struct ExpandArgs {
     ReadArgs r;
     const int2* span;
     int* lost;
     void* k_rest;
+    void* v_rest;          // or NULL.  What V lacks
     const int* v_top;      // [B, Hkv]: V becomes f16 times 2^-v_exponent of this
 };
 

@@ -427,7 +427,8 @@ def test_keys_and_queries_of_every_size(dtype, T, d, mods):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T,heads", [(1, (8, 2, 64)), (1, (16, 2, 128)), (4, (24, 8, 64)), (20, (8, 1, 128))])
+@pytest.mark.parametrize("T,heads", [(1, (8, 2, 64)), (1, (16, 2, 128)), (4, (24, 8, 64)), (20, (8, 1, 128)), (1, (20, 4, 80)), (1, (8, 8, 96)),
+                                     (5, (4, 1, 32)), (70, (8, 2, 128)), (150, (4, 2, 64)), (90, (6, 2, 96)), (300, (2, 1, 128))])
 @pytest.mark.parametrize("n_kv", [(400, 130), (1, 2), (17, 33)])
 @pytest.mark.parametrize("mods", [{}, dict(cap=3.0, slopes=True)])
 def test_f16_results_are_as_near_as_their_own_rounding(T, heads, n_kv, mods):
