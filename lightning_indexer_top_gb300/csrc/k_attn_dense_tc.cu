@@ -69,9 +69,9 @@ struct Cfg {
     static constexpr int kQRows = kTiles == 2 ? kRows : kFewRows;
     static constexpr int kQTile = kQRows * D * 2;
     static constexpr int kQBlock = kQRows * 128;      // 64 columns of it
-    static constexpr int kStagesK = kTwo ? (kTiles == 2 || D == 64 || kBoth ? 3 : 2) : kTiles == 2 ? 2 : D == 64 ? 2 : 1;
+    static constexpr int kStagesK = kTwo ? (kTiles == 2 || D == 64 ? 3 : kBoth ? 1 : 2) : kTiles == 2 ? 2 : D == 64 ? 2 : 1;
     static constexpr int kStagesV = kTwo && D == 128 ? (kTiles == 2 || kBoth ? 2 : 1) : kTiles == 2 ? 3 : D == 64 ? 3 : 2;
-    static constexpr int kCtas = kTiles == 2 || (kBoth && D == 128) ? 1 : 2;   // (two: 128 registers; with options 28 to 40 bytes are spilled)
+    static constexpr int kCtas = kTiles == 2 ? 1 : 2;   // (two: 128 registers; with options 28 to 40 bytes are spilled)
     static constexpr int kKOff = kTiles * kQTile;
     static constexpr int kVOff = kKOff + kStagesK * kTileBytes;
     static constexpr int kCtlOff = kVOff + kStagesV * kTileBytes;
@@ -208,8 +208,9 @@ __device__ __forceinline__ void store_rows(E* out, int64_t at, int n_rows, const
 // 16384 keys: 969 us, tensor pipe busy on 72 % of the active cycles (57 % with K in one part).
 // With f16 q the results are f16 too, and roundings of V and of the weights would be as large as the results' own: both are in
 // two parts as well (kBoth), P's second one beside the first in TMEM, and O three products: with one part each results were off by
-// 1.7 times their rounding.  The same tokens take 1.5 ms; one row tile of heads above 64 columns has an SM to itself then (16 sequences
-// of up to 32768 keys, 20 heads of 80 on 4: 747 us with the expansion, for 531).
+// 1.7 times their rounding.  The same tokens take 1.5 ms.  With one row tile of heads above 64 columns K's parts share a place, so
+// that two CTAs still share an SM: 16 sequences of up to 32768 keys, 20 heads of 80 on 4, with the expansion 673 us (531 with one
+// part each; an SM to itself and three places 747, but one such sequence 126 for 154).
 template <typename T, bool kTwo>
 constexpr bool kBothParts = kTwo && std::is_same<T, __half>::value;
 
@@ -228,7 +229,8 @@ __global__ void __launch_bounds__(CfgOf<T, D, kTiles, kTwo>::kThreads, CfgOf<T, 
     constexpr bool kBf16V = std::is_same<V, __nv_bfloat16>::value;
     constexpr float kShift = kBf16V ? 0.f : 7.f;    // P is kept this much (log2) larger
     constexpr float kTop = kShift + 8.f;
-    constexpr bool kDouble = kDoubleS<D, kMods>;
+    constexpr bool kOneK = kTwo && C::kStagesK == 1;      // K's two entries come one after the other in one place
+    constexpr bool kDouble = kDoubleS<D, kMods> && !kOneK;
     constexpr int kPStep = kDouble || kBoth ? kHalf : kHalf / 2;      // TMEM columns from P's first half to its second
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -455,17 +457,27 @@ __global__ void __launch_bounds__(CfgOf<T, D, kTiles, kTwo>::kThreads, CfgOf<T, 
                 const uint32_t d = __shfl_sync(0xffffffffu, ts + half * kHalf, 0);
                 const bool last = !kDouble || half == 1;      // of the K tile
                 tc_fence_after();
-                if (elect_one()) {
+                auto product = [&](uint32_t k, uint32_t add) {
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks)
                         mma_f16_ss_lo(d, qa + (((ks >> 2) * C::kQBlock + (ks & 3) * 32) >> 4), k_hi,
-                                      ka + (((ks >> 2) * kColBlock + (ks & 3) * 32) >> 4), k_hi, id_qk, ks > 0 ? 1u : 0u);
+                                      k + (((ks >> 2) * kColBlock + (ks & 3) * 32) >> 4), k_hi, id_qk, ks > 0 ? 1u : add);
+                };
+                bool there = true;
+                if constexpr (kOneK) {
+                    if (elect_one()) {
+                        product(ka, 0u);
+                        mma_commit(&c.kempty[0]);
+                    }
+                    __syncwarp();
+                    there = warp_wait(&c.kfull[0], (uint32_t)kph ^ 1);
+                    tc_fence_after();
+                }
+                if (elect_one()) {
+                    if (!kOneK) product(ka, 0u);
                     if constexpr (kTwo) {
-                        if (last) mma_commit(&c.kempty[sk]);
-#pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks)
-                            mma_f16_ss_lo(d, qa + (((ks >> 2) * C::kQBlock + (ks & 3) * 32) >> 4), k_hi,
-                                          kr + (((ks >> 2) * kColBlock + (ks & 3) * 32) >> 4), k_hi, id_qk, 1u);
+                        if (!kOneK && last) mma_commit(&c.kempty[sk]);
+                        if (there) product(kr, 1u);
                     }
                     mma_commit(&c.sfull[i][half]);
                     if (last) mma_commit(&c.kempty[s2]);
@@ -477,12 +489,14 @@ __global__ void __launch_bounds__(CfgOf<T, D, kTiles, kTwo>::kThreads, CfgOf<T, 
                             sk = 0;
                             kph ^= 1;
                         }
+                return there;
             };
             // the K tile to use next is there
             auto wait_k = [&] {
                 bool there = warp_wait(&c.kfull[sk], (uint32_t)kph);
-                if (kTwo) there = there && (sk + 1 == C::kStagesK ? warp_wait(&c.kfull[0], (uint32_t)kph ^ 1)
-                                                                  : warp_wait(&c.kfull[sk + 1], (uint32_t)kph));
+                if (kTwo && !kOneK)
+                    there = there && (sk + 1 == C::kStagesK ? warp_wait(&c.kfull[0], (uint32_t)kph ^ 1)
+                                                            : warp_wait(&c.kfull[sk + 1], (uint32_t)kph));
                 return there;
             };
             // O += P V of half a tile, and the commits that follow it
@@ -512,10 +526,8 @@ __global__ void __launch_bounds__(CfgOf<T, D, kTiles, kTwo>::kThreads, CfgOf<T, 
                 __syncwarp();
             };
             ok = wait_k();
-            if (ok) {
-                qk(0);
-                if (kDouble) qk(1);
-            }
+            if (ok) ok = qk(0);
+            if (ok && kDouble) ok = qk(1);
             for (int j = 0; ok && j < n; ++j) {
                 const bool last = j + 1 == n;
                 ok = warp_wait(&c.vok[sv], (uint32_t)vph) &&
@@ -530,7 +542,7 @@ __global__ void __launch_bounds__(CfgOf<T, D, kTiles, kTwo>::kThreads, CfgOf<T, 
                     if (!last) {
                         ok = wait_k();
                         if (!ok) break;
-                        qk(0);
+                        ok = qk(0);
                     }
                 } else {
                     pv(0, j == 0, &c.pvdone[i], nullptr, nullptr);
@@ -539,7 +551,7 @@ __global__ void __launch_bounds__(CfgOf<T, D, kTiles, kTwo>::kThreads, CfgOf<T, 
                 ok = ok && warp_wait(&c.pready[i][1], (uint32_t)(j & 1));
                 if (!ok) break;
                 pv(1, false, &c.vempty[sv], last ? &c.odone[i] : nullptr, kBoth ? &c.vempty[second_v()] : nullptr);
-                if (!last) qk(kDouble ? 1 : 0);
+                if (!last) ok = qk(kDouble ? 1 : 0);
                 for (int x = 0; x < kEntriesV; ++x)
                     if (++sv == C::kStagesV) {
                         sv = 0;
