@@ -205,10 +205,10 @@ __device__ __forceinline__ void store_rows(E* out, int64_t at, int n_rows, const
 
 // kTwo: K is the sum of two tensors of T, for keys that T alone does not hold (values of 4-bit codes): the scores are two
 // products into the same accumulators.  V and the weights are f16 then, V at a power of two.  4096 tokens of 32 heads of 128 on
-// 16384 keys: 969 us, tensor pipe busy on 72 % of the active cycles (57 % with K in one part).
+// 16384 keys: 990 us, tensor pipe busy on 71 % of the active cycles (57 % with K in one part).
 // With f16 q the results are f16 too, and roundings of V and of the weights would be as large as the results' own: both are in
 // two parts as well (kBoth), P's second one beside the first in TMEM, and O three products: with one part each results were off by
-// 1.7 times their rounding.  The same tokens take 1.5 ms.  With one row tile of heads above 64 columns K's parts share a place, so
+// 1.7 times their rounding.  The same tokens take 1490 us, tensor pipe 80 %.  With one row tile of heads above 64 columns K's parts share a place, so
 // that two CTAs still share an SM: 16 sequences of up to 32768 keys, 20 heads of 80 on 4, with the expansion 673 us (531 with one
 // part each; an SM to itself and three places 747, but one such sequence 126 for 154).
 template <typename T, bool kTwo>

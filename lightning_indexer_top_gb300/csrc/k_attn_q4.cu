@@ -14,7 +14,7 @@
 //
 // 16 sequences of up to 32768 keys, 32 bf16 heads of 128 on 4, 64-row pages: 67 us for 231 MB, 3.4 TB/s.  Not memory bounds it
 // but the way from codes to operands: schedulers issue on half of the cycles, three warps to each, mostly waiting for their own
-// last result (tensor pipe 21 %, ALU 49 %).  No better: four CTAs to an SM at 128 registers, two to five blocks ahead, halves
+// last result (tensor pipe 20 %, ALU 49 %).  No better: four CTAs to an SM at 128 registers, two to five blocks ahead, halves
 // of a block one after the other (66 to 68), V expanded before the softmax (69), eight warps to a CTA (79), scales by plain
 // copies instead of TMA's (66 to 69).
 #include <algorithm>
@@ -121,7 +121,9 @@ __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t b
 __device__ __forceinline__ uint32_t h2(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
 __device__ __forceinline__ __half2 as_h2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
 
-// codes i (0 .. 3) of a word's two halves as a pair of f16: n - 8.  kRaw: the odd ones stay 1024 + 16 n = 16 (n - 8 + 72), and
+// codes i (0 .. 3) of a word's two halves as a pair of f16: n - 8.  A code under the exponent of 1024 is the f16 1024 + n, or
+// 1024 + 16 n, from which one addition or FMA takes the rest (Kim, Henry, Fahim and Awadalla, "Who Says Elephants Can't Run", 2022).
+// kRaw: the odd ones stay 1024 + 16 n = 16 (n - 8 + 72), and
 // the product's user takes 72 (and 16) off again: two instructions less, for K's sums of D terms.  (V's run over all keys: with
 // 72 too much in them their f32 rounding showed, an error of 0.4 % on averages over 30000 keys.)
 template <bool kRaw>

@@ -16,8 +16,8 @@
 //
 // The scan waits more than it works (seven instructions a logit): 16-bit logits stay packed so that more CTAs are at it,
 // sums run against the warp's maximum so that two barriers are enough.
-// 512 rows of 131072 bf16 logits, 16 kept of each eight: 65 us, two thirds of them the scan, in which schedulers issue on half of
-// the cycles; the merge waits for one load after another.
+// 512 rows of 131072 bf16 logits, 16 kept of each eight: 64 us (f32: 81).  By itself the scan takes 40, with issue slots used on 45 %
+// of the cycles, and the merge 27, with one CTA to a sequence, which waits at barriers and for one load after another.
 #include <float.h>
 
 #include "beam.cuh"
@@ -504,7 +504,9 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(BeamArgs a) {
 }
 
 // Logits to a thread: few while more would leave SMs without work, many where there is plenty (a CTA's barriers and its list
-// take as long whatever it holds)
+// take as long whatever it holds).  8, 32 and 64 of them: 4 f32 rows of 32000 9.3, 10.6 us; 16 of them 13.5, 23.7; 32 bf16 rows of
+// 32000 11.3, 15.1, 16.0; 64 bf16 rows of 131072 28.9, 16.2, 16.6; 512 of them 128, 66.6, 63.5 (f32: 131, 81.9).  Not the best
+// for few long rows: 8 bf16 rows of 131072 15.5, 11.0, 12.7.
 int logits_of(int64_t rows, int64_t vocab, int dtype) {
     auto ctas = [&](int n) { return rows * ((vocab + n * kThreads - 1) / (n * kThreads)); };
     return ctas(32) < 2 * 152 ? 8 : dtype != IDX_F32 && ctas(64) >= 8 * 152 ? 64 : 32;
