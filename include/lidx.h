@@ -732,9 +732,10 @@ idx_status idx_cache_read_q4(const void* k_cache, int64_t k_row_stride, const vo
  *     not 0, or q reaches 2^70, a piece of its keys goes key by key in f32.
  *   - more rows, and other heads of at most 128 columns, on K and V expanded in the workspace (to
  *     64 GB, counted by max_n_kv): K in two parts (16 bits of significand together in BF16, 22 in
- *     F16, nothing below F16's least number), V in f16 at a power of two of the sequence's and
- *     head's largest, the weights in f16 (F16 calls: both in two f16 parts).  With a number of K beyond dtype's range, or a key whose V
- *     is 2^-28 or less of that largest, the call goes to the CUDA cores after all.
+ *     F16), V and the weights in f16 (F16 calls: in two f16 parts), V, and K in F16 calls, at a power
+ *     of two of the sequence's and head's largest.  With a number of K beyond BF16's range, a key
+ *     whose V is 2^-28 or less of the largest, or in F16 calls one whose K is 2^-17 or less, the call
+ *     goes to the CUDA cores after all.
  * Everything else runs on the CUDA cores in f32.
  */
 idx_status dense_attn_q4(const void* q, idx_dtype dtype, int32_t n_q_heads, int32_t n_kv_heads, int32_t dk, int32_t dv,

@@ -28,13 +28,17 @@ struct DenseArgs {
     float* part_ml;           // [row * Hq + head][split][2]: maximum (natural-log units), sum
     const void* k_rest;       // or NULL.  Given (tensor cores): K is the sum of k and this, laid out alike, and V f16
     const int* v_top;         // ... at the power of two that v_exponent makes of this [B, Hkv]
-    const void* v_rest;       // ... with f16 q: what V lacks of its f32, in f16, laid out alike
+    const void* v_rest;       // ... with f16 q: what V lacks of its f32, in f16, laid out alike; K is at the power of two that
+                              // k_exponent makes of another [B, Hkv] behind v_top then
     const int* only_if;       // or NULL; given and 0 on the device: the launch has nothing to do (CUDA cores, 4 bits)
 };
 
 // The power of two at which f16 holds numbers of magnitudes up to top (a float's bits) as numbers below 2^15, so that those
 // 2^28 below the largest keep f16's eleven bits: -126 .. 113; and 2^n, n in [-126, 127]
 __device__ __forceinline__ int v_exponent(int top) { return max((top >> 23) - 127, -112) - 14; }
+
+// The same for K, whose power goes with the call's scale (so it is no smaller than 2^-60)
+__device__ __forceinline__ int k_exponent(int top) { return max(v_exponent(top), -60); }
 
 __device__ __forceinline__ float exp2_whole(int n) { return __int_as_float((n + 127) << 23); }
 
@@ -188,10 +192,11 @@ __device__ __forceinline__ void modify(float (&s)[N], const Score& sc, float d0,
     }
 }
 
-__device__ __forceinline__ Score make_score(const DenseArgs& a, float slope) {
+// scale: a.scale, times the power of two at which K is
+__device__ __forceinline__ Score make_score(const DenseArgs& a, float scale, float slope) {
     Score s;
-    s.c = a.scale * kLog2e;
-    s.inv_cap = a.mods.softcap > 0.f ? a.scale / a.mods.softcap : 0.f;
+    s.c = scale * kLog2e;
+    s.inv_cap = a.mods.softcap > 0.f ? scale / a.mods.softcap : 0.f;
     s.cap = a.mods.softcap * kLog2e;
     const float i2 = s.inv_cap * s.inv_cap, c9 = fabsf(s.c * i2 * i2 * i2 * i2 * (62.f / 2835.f));
     s.series = c9 >= 0x1p-126f && c9 <= 0x1p100f ? 0.3f / fabsf(s.inv_cap) : -1.f;

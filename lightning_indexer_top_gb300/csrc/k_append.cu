@@ -694,9 +694,12 @@ __global__ void __launch_bounds__(kThreads) read_q4_kernel(ExpandArgs p, Geom g,
         T* rest = kExpand ? static_cast<T*>(p.k_rest) + (dst - static_cast<T*>(a.k_out)) : nullptr;
         const float* pair = reinterpret_cast<const float*>(src + a.Hkv * (w / 2)) + 2 * h;
         const float scale = pair[0], low = pair[1];
-        if (kExpand && is_k && isfinite(scale) && isfinite(low) &&
-            isinf(to_f32(from_f32<T>(fmaxf(fabsf(low), fabsf(fmaf(15.f, scale, low)))))))
-            *p.lost = 1;      // (numbers, but not of type T)
+        const float k_unit = kExpand && is_k && p.k_top ? exp2_whole(-k_exponent(p.k_top[(r0 + i) / g.T * a.Hkv + h])) : 1.f;
+        if (kExpand && is_k && isfinite(scale) && isfinite(low)) {
+            // (numbers, but not of type T; or with a power of two below what two parts have 22 bits for)
+            const float most = fmaxf(fabsf(low), fabsf(fmaf(15.f, scale, low))) * k_unit;
+            if (isinf(to_f32(from_f32<T>(most))) || (p.k_top && most > 0.f && most < 0x1p-3f)) *p.lost = 1;
+        }
         uint32_t x[kCols / 8];
         if constexpr (kWide)
             *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(src + u * 16);
@@ -728,7 +731,8 @@ __global__ void __launch_bounds__(kThreads) read_q4_kernel(ExpandArgs p, Geom g,
             T y[E], z[E];
 #pragma unroll
             for (int j = 0; j < E; ++j) {
-                const float v = fmaf((float)((x[(c + j) / 8] >> (4 * ((c + j) % 8))) & 15u), scale, low);
+                float v = fmaf((float)((x[(c + j) / 8] >> (4 * ((c + j) % 8))) & 15u), scale, low);
+                if (kExpand) v *= k_unit;
                 y[j] = from_f32<T>(v);
                 if (kExpand) z[j] = from_f32<T>(v - to_f32(y[j]));
             }
@@ -744,9 +748,7 @@ cudaError_t run_read(const ExpandArgs& p, const Geom& g, cudaStream_t st) {
     const int64_t n = (int64_t)g.B * g.T;
     const uint64_t all = reinterpret_cast<uintptr_t>(a.k_cache) | reinterpret_cast<uintptr_t>(a.v_cache) | (uint64_t)a.kc_stride |
                          (a.v_cache ? (uint64_t)a.vc_stride : 0) | (uint64_t)(a.dk / 2) | (uint64_t)(a.dv / 2);
-    // (four results of each code are as many streams of stores, which want whole lines: 393,000 keys of 8 heads of 96 in f16
-    // calls, with the attention, 1686 us wide, 1412 narrow; with three in bf16 ones 1044 and 1093)
-    const bool wide = all % 16 == 0 && !p.v_rest;
+    const bool wide = all % 16 == 0;
     const int64_t per_row = (int64_t)a.Hkv * (a.dk + a.dv) / (wide ? 32 : 8);
     int per = 1;
     while (per < kThreads && per_row * per < 2 * kThreads && n / per > 2 * 152) per *= 2;

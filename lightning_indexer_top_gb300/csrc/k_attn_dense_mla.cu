@@ -400,7 +400,7 @@ __device__ __forceinline__ void softmax(Ctl& c, uint8_t* smem, uint32_t tmem, co
     const uint32_t pkts = mapa(smem + kVRing * kGroupBytes, 1);
     const float sl2 = kMods ? 1.f : p.a.scale * kLog2e;
     Score sc;
-    if (kMods) sc = make_score(p.a, p.a.mods.slopes ? p.a.mods.slopes[h] : 0.f);
+    if (kMods) sc = make_score(p.a, p.a.scale, p.a.mods.slopes ? p.a.mods.slopes[h] : 0.f);
     float m_used = 0.f, lsum = 0.f;
     bool has_m = false;
     bool ok = warp_wait(&c.bits, 0);

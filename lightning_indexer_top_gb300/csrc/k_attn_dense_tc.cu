@@ -137,7 +137,7 @@ __device__ __noinline__ void scalar_row(const DenseArgs& a, const Geom& g, int b
         const V* v_rest = a.v_rest ? static_cast<const V*>(a.v_rest) + row * a.v_stride + (int64_t)gkv * a.dv : nullptr;
         float x = 0.f;
         for (int c = 0; c < a.dk; ++c) x = fmaf(to_f32(q[c]), to_f32(k[c]) + (rest ? to_f32(rest[c]) : 0.f), x);
-        x *= a.scale;
+        x *= a.v_rest ? a.scale * exp2_whole(k_exponent(a.v_top[(int64_t)(g.B + b) * a.Hkv + gkv])) : a.scale;
         if (a.mods.softcap > 0.f) x = a.mods.softcap * tanhf(x / a.mods.softcap);
         if (a.mods.slopes) x -= a.mods.slopes[h] * fabsf((float)(iv.pos - j));
         x *= kLog2e;
@@ -205,12 +205,12 @@ __device__ __forceinline__ void store_rows(E* out, int64_t at, int n_rows, const
 
 // kTwo: K is the sum of two tensors of T, for keys that T alone does not hold (values of 4-bit codes): the scores are two
 // products into the same accumulators.  V and the weights are f16 then, V at a power of two.  4096 tokens of 32 heads of 128 on
-// 16384 keys: 990 us, tensor pipe busy on 71 % of the active cycles (57 % with K in one part).
+// 16384 keys: 965 us, tensor pipe busy on 74 % of the active cycles (57 % with K in one part).
 // With f16 q the results are f16 too, and roundings of V and of the weights would be as large as the results' own: both are in
 // two parts as well (kBoth), P's second one beside the first in TMEM, and O three products: with one part each results were off by
-// 1.7 times their rounding.  The same tokens take 1490 us, tensor pipe 80 %.  With one row tile of heads above 64 columns K's parts share a place, so
-// that two CTAs still share an SM: 16 sequences of up to 32768 keys, 20 heads of 80 on 4, with the expansion 673 us (531 with one
-// part each; an SM to itself and three places 747, but one such sequence 126 for 154).
+// 1.7 times their rounding.  The same tokens take 1518 us, tensor pipe 81 %.  With one row tile of heads above 64 columns K's parts share a place, so
+// that two CTAs still share an SM: 16 sequences of up to 32768 keys, 20 heads of 80 on 4, with the expansion 665 us (527 in bf16,
+// with one part each; an SM to itself and three places 747, but one such sequence 126 for 154).
 template <typename T, bool kTwo>
 constexpr bool kBothParts = kTwo && std::is_same<T, __half>::value;
 
@@ -605,7 +605,16 @@ __global__ void __launch_bounds__(CfgOf<T, D, kTiles, kTwo>::kThreads, CfgOf<T, 
     bool ok = n > 0;
     if (warp_rows) {
         const uint32_t ts = tmem + lane_off + rt * kKeys;
-        const Score sc = make_score(a, a.mods.slopes && has_row ? a.mods.slopes[h] : 0.f);
+        const Score sc = [&] {
+            const float slope = a.mods.slopes && has_row ? a.mods.slopes[h] : 0.f;
+            if constexpr (kBoth) {
+                // (from one lane, for all: a uniform register)
+                const float scale = a.scale * exp2_whole(k_exponent(a.v_top[(int64_t)(g.B + b) * a.Hkv + gkv]));
+                return make_score(a, __shfl_sync(0xffffffffu, kMods ? scale : fmaxf(scale, 0x1p-126f), 0), slope);      // (still above 0)
+            } else {
+                return make_score(a, a.scale, slope);
+            }
+        }();
         auto timed_out = [&] {
             *(volatile int*)&c.abort = 1;
             flag(g.status, IDX_ERR_TIMEOUT);

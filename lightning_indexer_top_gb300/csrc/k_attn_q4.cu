@@ -961,11 +961,14 @@ cudaError_t go(const DenseArgs& a, const Geom& g, void* ws, size_t ws_bytes, cud
 }
 
 // The positions that some row of a sequence sees, and nothing lost or found yet
-__global__ void __launch_bounds__(256) span_kernel(idx_attn_mods mods, Geom g, int2* span, int* lost, int* top, int Hkv) {
+__global__ void __launch_bounds__(256) span_kernel(idx_attn_mods mods, Geom g, int2* span, int* lost, int* top, int* k_top, int Hkv) {
     __shared__ int lo_s[8], hi_s[8];
     pdl_wait();
     const int b = blockIdx.x, warp = threadIdx.x >> 5;
-    for (int h = threadIdx.x; h < Hkv; h += 256) top[(int64_t)b * Hkv + h] = 0;
+    for (int h = threadIdx.x; h < Hkv; h += 256) {
+        top[(int64_t)b * Hkv + h] = 0;
+        if (k_top) k_top[(int64_t)b * Hkv + h] = 0;
+    }
     const int n_kv = seq_n_kv(g, b);
     int lo = INT32_MAX, hi = 0;
     for (int t = threadIdx.x; t < g.T; t += 256) {
@@ -991,11 +994,12 @@ __global__ void __launch_bounds__(256) span_kernel(idx_attn_mods mods, Geom g, i
     if (b == 0) *lost = 0;
 }
 
-// The largest magnitude of V in each (sequence, kv head)'s span, as a float's bits: what f16 is scaled by.  Values that are no
-// numbers say nothing; numbers past f32's go the CUDA cores' way.  The maximum does not depend on the order.
+// The largest magnitude of V, and of K where k_top is given, in each (sequence, kv head)'s span, as a float's bits: what f16 is
+// scaled by.  Values that are no numbers say nothing; numbers past f32's go the CUDA cores' way.  A maximum does not depend on the
+// order.
 constexpr int kTopKeys = 8;      // positions of a thread
 
-__global__ void __launch_bounds__(256) v_top_kernel(ExpandArgs p, Geom g, int* top, int chunks) {
+__global__ void __launch_bounds__(256) top_kernel(ExpandArgs p, Geom g, int* top, int* k_top, int chunks) {
     pdl_wait();
     const ReadArgs& a = p.r;
     const int b = blockIdx.x / chunks, heads = min(a.Hkv, 256), at_once = 256 / heads;
@@ -1003,34 +1007,44 @@ __global__ void __launch_bounds__(256) v_top_kernel(ExpandArgs p, Geom g, int* t
     const int64_t first = (int64_t)(blockIdx.x - b * chunks) * (at_once * kTopKeys) + threadIdx.x / heads;
     if (threadIdx.x >= heads * at_once) return;
     for (int h = threadIdx.x % heads; h < a.Hkv; h += heads) {
-        float most = 0.f;
+        float most = 0.f, most_k = 0.f;
+        auto take = [&](const void* cache, int64_t stride, int64_t row, int d, float& m) {
+            const uint8_t* pairs = static_cast<const uint8_t*>(cache) + row * stride + a.Hkv * (d / 2);
+            const float* pair = reinterpret_cast<const float*>(pairs) + 2 * h;
+            const float scale = pair[0], low = pair[1];
+            if (isfinite(scale) && isfinite(low)) m = fmaxf(m, fmaxf(fabsf(low), fabsf(fmaf(15.f, scale, low))));
+        };
 #pragma unroll
         for (int i = 0; i < kTopKeys; ++i) {
             const int64_t pos = first + i * at_once;
             if (pos < span.x || pos >= span.y) continue;
             const int64_t row = key_row(g, b, pos);
             if (row < 0 || row >= a.kv_rows) continue;
-            const uint8_t* pairs = static_cast<const uint8_t*>(a.v_cache) + row * a.vc_stride + a.Hkv * (a.dv / 2);
-            const float* pair = reinterpret_cast<const float*>(pairs) + 2 * h;
-            const float scale = pair[0], low = pair[1];
-            if (isfinite(scale) && isfinite(low)) most = fmaxf(most, fmaxf(fabsf(low), fabsf(fmaf(15.f, scale, low))));
+            take(a.v_cache, a.vc_stride, row, a.dv, most);
+            if (k_top) take(a.k_cache, a.kc_stride, row, a.dk, most_k);
         }
-        if (isinf(most)) *p.lost = 1;
-        int* to = top + (int64_t)b * a.Hkv + h;
-        if (__float_as_int(most) > *(volatile int*)to) atomicMax(to, __float_as_int(most));
+        if (isinf(most) || isinf(most_k)) *p.lost = 1;
+        auto put = [&](int* to, float m) {
+            if (__float_as_int(m) > *(volatile int*)to) atomicMax(to, __float_as_int(m));
+        };
+        put(top + (int64_t)b * a.Hkv + h, most);
+        if (k_top) put(k_top + (int64_t)b * a.Hkv + h, most_k);
     }
 }
 
 // where the expanded K (in two parts) and V (f16 calls: in two) lie in the workspace, behind the spans, the largest values and the mark of lost keys
 struct Expanded {
-    size_t top_at, k_at, rest_at, v_at, v_rest_at, bytes;
+    size_t top_at, k_top_at, k_at, rest_at, v_at, v_rest_at, bytes;
     Expanded(int dtype, int64_t n_seq, int64_t max_n_kv, int Hkv, int dk, int dv) {
         const size_t rows = (size_t)n_seq * max_n_kv * Hkv;
         top_at = n_seq * sizeof(int2) + sizeof(int);
-        k_at = (top_at + n_seq * Hkv * sizeof(int) + 15) / 16 * 16;
-        rest_at = k_at + rows * dk * 2;
-        v_at = rest_at + rows * dk * 2;
-        v_rest_at = v_at + rows * dv * 2;
+        k_top_at = top_at + n_seq * Hkv * sizeof(int);      // (right behind, see DenseArgs)
+        // (on whole lines: 16 bytes off them 4096 tokens on 12288 keys took 1070 us, 32 off 1025)
+        auto line = [](size_t n) { return (n + 127) / 128 * 128; };
+        k_at = line(k_top_at + n_seq * Hkv * sizeof(int));
+        rest_at = line(k_at + rows * dk * 2);
+        v_at = line(rest_at + rows * dk * 2);
+        v_rest_at = line(v_at + rows * dv * 2);
         bytes = v_rest_at + (dtype == IDX_F16 ? rows * dv * 2 : 0);
     }
 };
@@ -1069,11 +1083,12 @@ size_t q4_attn_workspace_bytes(int dtype, int64_t n_seq, int64_t n_q, int64_t ma
 // K and V of the span that some row sees, expanded, then dense_attn's tensor-core kernel on them: V rounded to f16 (and the
 // weights with it: bf16 for both leaves 4096 rows on 16384 keys with errors of 0.0029 of the result, 0.0017 is the result's
 // own rounding) at a power of two, K as a sum of two of dtype (16 or 22 bits), since the log of the weights' sum is f32.  Of
-// the 1004 to 1025 us of 4096 tokens of 32 heads on 16384 keys the second product of K takes some 240 (K in bf16 alone: 740),
+// the 985 to 1000 us of 4096 tokens of 32 heads on 16384 keys the second product of K takes some 240 (K in bf16 alone: 740),
 // spans, largest values and expansion of 16384 rows some 30.  (Scales applied to the products of exact codes, in the softmax: 1455 us; it is the
-// softmax that the kernel waits for.)  For f16 results the weights and V are in two parts too (1541 us).
-// What that kernel cannot know of or hold, keys without a row in the cache, numbers beyond dtype's range in K and keys whose V is
-// 2^-28 or less of the largest, sends everything through the CUDA cores again, which skip and flag the one and hold the others in
+// softmax that the kernel waits for.)  For f16 results the weights and V are in two parts too (1560 us).
+// f16 calls have K at a power of two too, which the call's scale takes back.
+// What that kernel cannot know of or hold, keys without a row in the cache, numbers of K beyond bf16's, keys whose V is 2^-28 or
+// less of the largest and, in f16 calls, whose K is 2^-17 or less, sends everything through the CUDA cores again, which skip and flag the one and hold the others in
 // f32.
 static cudaError_t run_expanded(DenseArgs a, int dtype, const Geom& g, uint8_t* ws, cudaStream_t st) {
     const Expanded e(dtype, g.B, g.max_n_kv, a.Hkv, a.dk, a.dv);
@@ -1111,15 +1126,19 @@ static cudaError_t run_expanded(DenseArgs a, int dtype, const Geom& g, uint8_t* 
     x.lost = lost;
     x.k_rest = ws + e.rest_at;
     d.k_rest = x.k_rest;
-    if (dtype == IDX_F16) d.v_rest = x.v_rest = ws + e.v_rest_at;
+    int* k_top = nullptr;
+    if (dtype == IDX_F16) {
+        d.v_rest = x.v_rest = ws + e.v_rest_at;
+        x.k_top = k_top = reinterpret_cast<int*>(ws + e.k_top_at);
+    }
     int* top = reinterpret_cast<int*>(ws + e.top_at);
     x.v_top = d.v_top = top;
     Geom all = g;
     all.T = g.max_n_kv;
     const int64_t chunk = 256 / std::min(a.Hkv, 256) * kTopKeys, chunks = (g.max_n_kv + chunk - 1) / chunk;
     if (chunks * g.B > INT32_MAX) return cudaErrorNotSupported;
-    cudaError_t err = launch_pdl(span_kernel, dim3((unsigned)g.B), dim3(256), 0, st, a.mods, g, span, lost, top, a.Hkv);
-    if (err == cudaSuccess) err = launch_pdl(v_top_kernel, dim3((unsigned)(chunks * g.B)), dim3(256), 0, st, x, g, top, (int)chunks);
+    cudaError_t err = launch_pdl(span_kernel, dim3((unsigned)g.B), dim3(256), 0, st, a.mods, g, span, lost, top, k_top, a.Hkv);
+    if (err == cudaSuccess) err = launch_pdl(top_kernel, dim3((unsigned)(chunks * g.B)), dim3(256), 0, st, x, g, top, k_top, (int)chunks);
     if (err == cudaSuccess) err = launch_expand_q4(x, dtype, all, st);
     if (err == cudaSuccess) err = launch_dense_tc(d, dtype, flat, st);
     if (err != cudaSuccess) return err;

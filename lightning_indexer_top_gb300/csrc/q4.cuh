@@ -36,7 +36,7 @@ cudaError_t launch_read_q4(const ReadArgs& a, int dtype, const Geom& g, cudaStre
 
 // The positions of each sequence's span (device, [lo, hi)) for the attention: the values of K in dtype, row b * g.T + position,
 // what they lack of their f32 in k_rest, and V in f16 (and v_rest).  A position whose cache row is out of range, with a number of K beyond
-// dtype's, or whose largest of V is no normal f16 sets *lost, in place of the device status.
+// dtype's, or with numbers that the powers of two leave too few bits sets *lost, in place of the device status.
 struct ExpandArgs {
     ReadArgs r;
     const int2* span;
@@ -44,6 +44,7 @@ struct ExpandArgs {
     void* k_rest;
     void* v_rest;          // or NULL.  What V lacks
     const int* v_top;      // [B, Hkv]: V becomes f16 times 2^-v_exponent of this
+    const int* k_top;      // or NULL.  Likewise K, by k_exponent
 };
 
 cudaError_t launch_expand_q4(const ExpandArgs& a, int dtype, const Geom& g, cudaStream_t st);

@@ -427,6 +427,23 @@ def test_keys_and_queries_of_every_size(dtype, T, d, mods):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,heads", [(1, (8, 2, 128)), (5, (8, 2, 64)), (70, (8, 2, 128)), (150, (4, 2, 64)), (3, (6, 2, 80)), (90, (6, 2, 96))])
+@pytest.mark.parametrize("mods", [{}, dict(cap=4.0), dict(slopes=True, window=60)])
+def test_f16_keys_of_every_size(T, heads, mods):
+    # head 0: all of one size, which the scale undoes; head 1: a key of another size, which the last rows alone see
+    for power in (-45, -20, -12, 12, 40):
+        c = Case4([300, 170], T, *heads, dtype=torch.float16, seed=20, page=16, **mods)
+        n = c.k.shape[0]
+        f = torch.full((n,), 2.0 ** power)
+        rescale(c, 0, 0, f)
+        f[c.rows[0][298]] *= 2.0 ** (power // 2)
+        rescale(c, 0, 1, f)
+        c.scale *= 2.0 ** -power
+        check_without_floor(c, *c.run())
+    assert L.idx_device_status(reset=True) == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T,heads", [(1, (8, 2, 64)), (1, (16, 2, 128)), (4, (24, 8, 64)), (20, (8, 1, 128)), (1, (20, 4, 80)), (1, (8, 8, 96)),
                                      (5, (4, 1, 32)), (70, (8, 2, 128)), (150, (4, 2, 64)), (90, (6, 2, 96)), (300, (2, 1, 128))])
 @pytest.mark.parametrize("n_kv", [(400, 130), (1, 2), (17, 33)])
