@@ -351,6 +351,29 @@ def test_q4_rows_without_a_number_stand_for_nan_and_leave_the_others(dtype, d, n
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("four", [False, True])
+def test_caches_beyond_32_bit_offsets(four):
+    # rows that lie more than 2^32 bytes behind the caches' first
+    c = Rows([300, 41], 60, 4, 8, 128, 128, torch.bfloat16, 16, [60, 41], 128, seed=9)
+    w = L.idx_q4_row_bytes(8, 128)
+    shape, size, dt = ((w,), w, torch.uint8) if four else ((8, 128), 2048, torch.bfloat16)
+    n = (2 ** 32 // size + 4096) // 16 * 16
+    big, small = ([torch.zeros(k, *shape, dtype=dt, device="cuda") for _ in range(2)] for k in (n, c.n_rows))
+    call = L.idx_cache_append_q4 if four else L.idx_cache_append
+    q, k, v = c.gpu()
+    a = call(k, v, *small, c.batch(), q=q, **c.rope())
+    far = c.batch(page_table=(c.table + (n - c.n_rows) // 16).cuda())
+    b = call(k, v, *big, far, q=q, **c.rope())
+    assert torch.equal(a, b)
+    for x, y in zip(big, small):
+        assert torch.equal(x[n - c.n_rows:], y) and not x[:4096].any()
+    if four:
+        x, y = (L.idx_cache_read_q4(*t, bb, 8, 128, 128) for t, bb in ((big, far), (small, c.batch())))
+        assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+    assert L.idx_device_status(reset=True) == 0
+
+
+@pytest.mark.gpu
 def test_many_rows_have_exact_codes():
     # half a million columns, some of which lie within f32's error of a border
     c = Rows([2048], 2048, 0, 2, 128, 128, torch.bfloat16, 0, None, 128, seed=5, base=1e6)

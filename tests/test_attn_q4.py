@@ -461,6 +461,28 @@ def test_f16_results_are_as_near_as_their_own_rounding(T, heads, n_kv, mods):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("page", [0, 16, 5])
+def test_caches_beyond_32_bit_offsets(dtype, page):
+    # rows that lie more than 2^32 bytes behind the caches' first
+    w = L.idx_q4_row_bytes(8, 128)
+    big = [torch.empty(2 ** 32 // w + 4096, w, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    for T in (1, 5, 70):
+        c = Case4([300, 170], T, 8, 8, 128, dtype=dtype, page=page, seed=21)
+        n = c.k.shape[0]
+        at = (big[0].shape[0] - n) // max(page, 1) * max(page, 1)
+        for x, y in zip(big, c.caches):
+            x[at:at + n] = y.cuda()
+        real = c.batch
+        if page:
+            c.table = c.table + at // page
+        else:
+            c.batch = lambda: dataclasses.replace(real(), kv_start=torch.tensor([at, at + c.N], dtype=torch.int32, device="cuda"))
+        c.check(*c.run(caches=big))
+    assert L.idx_device_status(reset=True) == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T,d", [(3, 80), (70, 128)])
 def test_a_workspace_that_does_not_fit_is_done_without(T, d):
     c = Case4([300, 41], T, 8, 2, d, dtype=torch.bfloat16, seed=18)
