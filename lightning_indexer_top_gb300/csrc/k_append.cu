@@ -721,8 +721,8 @@ __global__ void __launch_bounds__(kThreads) read_q4_kernel(ExpandArgs p, Geom g,
                     z[j] = from_f32<__half>(v - to_f32(y[j]));
                 }
                 *reinterpret_cast<uint4*>(dst + c) = *reinterpret_cast<const uint4*>(y);
-                if (p.v_rest)
-                    *reinterpret_cast<uint4*>(static_cast<T*>(p.v_rest) + (dst - static_cast<T*>(a.v_out)) + c) = *reinterpret_cast<const uint4*>(z);
+                T* v_rest = static_cast<T*>(p.v_rest);
+                if (v_rest) *reinterpret_cast<uint4*>(v_rest + (dst - static_cast<T*>(a.v_out)) + c) = *reinterpret_cast<const uint4*>(z);
             }
             continue;
         }

@@ -208,9 +208,9 @@ __device__ __forceinline__ void store_rows(E* out, int64_t at, int n_rows, const
 // 16384 keys: 965 us, tensor pipe busy on 74 % of the active cycles (57 % with K in one part).
 // With f16 q the results are f16 too, and roundings of V and of the weights would be as large as the results' own: both are in
 // two parts as well (kBoth), P's second one beside the first in TMEM, and O three products: with one part each results were off by
-// 1.7 times their rounding.  The same tokens take 1518 us, tensor pipe 81 %.  With one row tile of heads above 64 columns K's parts share a place, so
-// that two CTAs still share an SM: 16 sequences of up to 32768 keys, 20 heads of 80 on 4, with the expansion 665 us (527 in bf16,
-// with one part each; an SM to itself and three places 747, but one such sequence 126 for 154).
+// 1.7 times their rounding.  The same tokens take 1518 us, tensor pipe 81 %.  With one row tile of heads above 64 columns K's
+// parts share a place, so that two CTAs still share an SM: 16 sequences of up to 32768 keys, 20 heads of 80 on 4, with the
+// expansion 665 us (527 in bf16, with one part each; an SM to itself and three places 747, but one such sequence 126 for 154).
 template <typename T, bool kTwo>
 constexpr bool kBothParts = kTwo && std::is_same<T, __half>::value;
 

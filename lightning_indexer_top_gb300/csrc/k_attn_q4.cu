@@ -1032,7 +1032,8 @@ __global__ void __launch_bounds__(256) top_kernel(ExpandArgs p, Geom g, int* top
     }
 }
 
-// where the expanded K (in two parts) and V (f16 calls: in two) lie in the workspace, behind the spans, the largest values and the mark of lost keys
+// where the expanded K (in two parts) and V (f16 calls: in two) lie in the workspace, behind the spans, the largest values and
+// the mark of lost keys
 struct Expanded {
     size_t top_at, k_top_at, k_at, rest_at, v_at, v_rest_at, bytes;
     Expanded(int dtype, int64_t n_seq, int64_t max_n_kv, int Hkv, int dk, int dv) {
@@ -1088,8 +1089,8 @@ size_t q4_attn_workspace_bytes(int dtype, int64_t n_seq, int64_t n_q, int64_t ma
 // softmax that the kernel waits for.)  For f16 results the weights and V are in two parts too (1560 us).
 // f16 calls have K at a power of two too, which the call's scale takes back.
 // What that kernel cannot know of or hold, keys without a row in the cache, numbers of K beyond bf16's, keys whose V is 2^-28 or
-// less of the largest and, in f16 calls, whose K is 2^-17 or less, sends everything through the CUDA cores again, which skip and flag the one and hold the others in
-// f32.
+// less of the largest and, in f16 calls, whose K is 2^-17 or less, sends everything through the CUDA cores again, which skip and
+// flag the first and hold the others in f32.
 static cudaError_t run_expanded(DenseArgs a, int dtype, const Geom& g, uint8_t* ws, cudaStream_t st) {
     const Expanded e(dtype, g.B, g.max_n_kv, a.Hkv, a.dk, a.dv);
     int2* span = reinterpret_cast<int2*>(ws);
